@@ -35,7 +35,13 @@ SYMBOLS = (
     "hc_plan_tiles", "hc_fused_ctas", "hc_debug_wait_flag", "hc_device_error", "hc_status_string",
     "hc_host_pipeline_create", "hc_host_pipeline_chunk_tokens", "hc_host_pipeline_destroy", "hc_host_chunk_plan",
     "hc_host_post_then_pre",
+    "hc_rope_table_size", "hc_prepare_rope", "hc_qk_norm_rope", "hc_kv_cache_size", "hc_kv_write", "hc_kv_read",
+    "hc_kv_workspace_size", "hc_kv_attention",
 )
+
+# styles of hc_rope_t
+HC_ROPE_HALF = 0
+HC_ROPE_PAIRS = 1
 
 
 class HCError(RuntimeError):
@@ -52,6 +58,27 @@ class hc_shape_t(ctypes.Structure):
 class hc_params_t(ctypes.Structure):
     _fields_ = [("hc_fn_planes", ctypes.c_void_p), ("hc_scale", ctypes.c_void_p), ("hc_base", ctypes.c_void_p),
                 ("norm_w", ctypes.c_void_p)]
+
+
+class hc_rope_t(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("rot", ctypes.c_int), ("start", ctypes.c_int), ("axes", ctypes.c_int),
+                ("style", ctypes.c_int)]
+
+
+class hc_heads_t(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int), ("k_heads", ctypes.c_int), ("dim", ctypes.c_int),
+                ("gain_per_head", ctypes.c_int), ("norm_eps", ctypes.c_float)]
+
+
+class hc_kv_shape_t(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int), ("page_size", ctypes.c_int), ("heads", ctypes.c_int), ("dim", ctypes.c_int),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class hc_attention_t(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("seqs", ctypes.c_int), ("max_q_len", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("q_heads", ctypes.c_int), ("causal", ctypes.c_int),
+                ("window", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -90,6 +117,15 @@ def load(path: str = LIB_PATH):
     PI64 = ctypes.POINTER(I64)
     lib.hc_host_chunk_plan.argtypes = [I64, I64, I64, PI64, PI64, PI64]
     lib.hc_host_post_then_pre.argtypes = [P, P, P, P, P, P, hc_params_t, I64, hc_shape_t, P, P, P, P, P, P]
+    PSZ = ctypes.POINTER(ctypes.c_size_t)
+    lib.hc_rope_table_size.argtypes = [I, PSZ]
+    lib.hc_prepare_rope.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(I), I, I, P, P]
+    lib.hc_qk_norm_rope.argtypes = [P, I64, P, I64, P, P, P, hc_rope_t, I64, hc_heads_t, P, I64, P, I64, P]
+    lib.hc_kv_cache_size.argtypes = [hc_kv_shape_t, PSZ]
+    lib.hc_kv_write.argtypes = [P, I64, P, I64, P, I64, hc_kv_shape_t, P, P]
+    lib.hc_kv_read.argtypes = [P, P, I64, hc_kv_shape_t, P, I64, P, I64, P]
+    lib.hc_kv_workspace_size.argtypes = [PSZ]
+    lib.hc_kv_attention.argtypes = [P, I64, P, P, P, P, hc_attention_t, hc_kv_shape_t, P, I64, P, P, P]
     lib.hc_status_string.restype = ctypes.c_char_p
     for name in SYMBOLS:
         if name != "hc_status_string":
@@ -300,3 +336,90 @@ def hc_host_post_then_pre(p, delta, X, post, comb, pre_mix, nxt: hc_params_t, n:
     _check("hc_host_post_then_pre", load().hc_host_post_then_pre(
         handle, _ptr(delta), _ptr(X), _ptr(post), _ptr(comb), _ptr(pre_mix), nxt, n, s, _ptr(X_out), _ptr(y_normed),
         _ptr(pre_out), _ptr(post_out), _ptr(comb_out), _stream(stream)))
+
+
+# ---- the attention sublayer ---------------------------------------------------------------------
+
+
+def rope(table, rot: int, start: int = 0, axes: int = 1, style: int = HC_ROPE_HALF) -> hc_rope_t:
+    """The rotation of hc_qk_norm_rope (the table, filled by hc_prepare_rope, must outlive its use)."""
+    return hc_rope_t(_ptr(table), rot, start, axes, style)
+
+
+def heads(q_heads: int, k_heads: int, dim: int, norm_eps: float = 1e-6, gain_per_head: bool = False) -> hc_heads_t:
+    return hc_heads_t(q_heads, k_heads, dim, 1 if gain_per_head else 0, norm_eps)
+
+
+def kv_shape(pages: int, page_size: int, heads: int, dim: int, k_scale: float = 1.0,
+             v_scale: float = 1.0) -> hc_kv_shape_t:
+    """Shape of a 4-bit key/value cache on pages; the scales are powers of two."""
+    return hc_kv_shape_t(pages, page_size, heads, dim, k_scale, v_scale)
+
+
+def attention(n: int, seqs: int, max_q_len: int, max_pages: int, q_heads: int, scale: float, causal: bool = True,
+              window: int = 0) -> hc_attention_t:
+    return hc_attention_t(n, seqs, max_q_len, max_pages, q_heads, 1 if causal else 0, window, scale)
+
+
+def _size(fn: str, *args) -> int:
+    out = ctypes.c_size_t(0)
+    _check(fn, getattr(load(), fn)(*args, ctypes.byref(out)))
+    return out.value
+
+
+def hc_rope_table_size(rot: int) -> int:
+    return _size("hc_rope_table_size", rot)
+
+
+def hc_prepare_rope(inv_freq, axis, rot: int, axes: int, table, stream=None) -> None:
+    """Fill `table` from rot/2 frequencies (radians per position, any sequence of floats) and, for several
+    axes, the axis of each (a sequence of ints, or None for axis 0)."""
+    if inv_freq is not None:
+        if len(inv_freq) != rot // 2:
+            raise ValueError("inv_freq has %d entries for rot = %d" % (len(inv_freq), rot))
+        inv_freq = (ctypes.c_double * len(inv_freq))(*[float(f) for f in inv_freq])
+    if axis is not None:
+        if len(axis) != rot // 2:
+            raise ValueError("axis has %d entries for rot = %d" % (len(axis), rot))
+        axis = (ctypes.c_int * len(axis))(*[int(a) for a in axis])
+    _check("hc_prepare_rope", load().hc_prepare_rope(inv_freq, axis, rot, axes, _ptr(table), _stream(stream)))
+
+
+def hc_qk_norm_rope(q, q_stride: int, k, k_stride: int, q_w, k_w, positions, r: hc_rope_t, n: int, s: hc_heads_t, q_out,
+                    q_out_stride: int, k_out, k_out_stride: int, stream=None) -> None:
+    _check("hc_qk_norm_rope", load().hc_qk_norm_rope(
+        _ptr(q), q_stride, _ptr(k), k_stride, _ptr(q_w), _ptr(k_w), _ptr(positions), r, n, s, _ptr(q_out), q_out_stride,
+        _ptr(k_out), k_out_stride, _stream(stream)))
+
+
+def hc_kv_cache_size(s: hc_kv_shape_t) -> int:
+    return _size("hc_kv_cache_size", s)
+
+
+def hc_kv_write(k, k_stride: int, v, v_stride: int, slots, n: int, s: hc_kv_shape_t, cache, stream=None) -> None:
+    _check("hc_kv_write", load().hc_kv_write(_ptr(k), k_stride, _ptr(v), v_stride, _ptr(slots), n, s, _ptr(cache),
+                                             _stream(stream)))
+
+
+def hc_kv_read(cache, slots, n: int, s: hc_kv_shape_t, k_out, k_stride: int, v_out, v_stride: int, stream=None) -> None:
+    """k_out or v_out may be None."""
+    _check("hc_kv_read", load().hc_kv_read(_ptr(cache), _ptr(slots), n, s, _ptr(k_out), k_stride, _ptr(v_out), v_stride,
+                                           _stream(stream)))
+
+
+def hc_kv_workspace_size() -> int:
+    return _size("hc_kv_workspace_size")
+
+
+def new_kv_workspace(device=None):
+    """A zero-filled device workspace for hc_kv_attention (torch uint8 tensor)."""
+    import torch
+    return torch.zeros(hc_kv_workspace_size(), dtype=torch.uint8, device=device or "cuda")
+
+
+def hc_kv_attention(q, q_stride: int, q_start, kv_len, page_table, cache, a: hc_attention_t, s: hc_kv_shape_t, out,
+                    out_stride: int, lse, workspace, stream=None) -> None:
+    """lse may be None."""
+    _check("hc_kv_attention", load().hc_kv_attention(
+        _ptr(q), q_stride, _ptr(q_start), _ptr(kv_len), _ptr(page_table), _ptr(cache), a, s, _ptr(out), out_stride,
+        _ptr(lse), _ptr(workspace), _stream(stream)))

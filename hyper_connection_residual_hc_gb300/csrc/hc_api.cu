@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "../../include/hc.h"
+#include "hc_attn.h"
 #include "hc_internal.h"
 
 namespace hc {
@@ -580,9 +581,11 @@ int hc_debug_wait_flag(const unsigned long long* flags, int count, unsigned long
 int hc_device_error(unsigned int* word, int clear, hc_stream_t stream) {
     if (!word) return HC_ERR_NULL;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    unsigned int fused = 0, proj = 0;
-    if (read_device_error(&fused, clear, cs) != 0 || read_proj_error(&proj, clear, cs) != 0) return HC_ERR_CUDA;
-    *word = fused | proj;
+    unsigned int fused = 0, proj = 0, kv = 0, attention = 0;
+    if (read_device_error(&fused, clear, cs) != 0 || read_proj_error(&proj, clear, cs) != 0 ||
+        read_kv_error(&kv, clear, cs) != 0 || read_attention_error(&attention, clear, cs) != 0)
+        return HC_ERR_CUDA;
+    *word = fused | proj | kv | attention;
     return HC_OK;
 }
 

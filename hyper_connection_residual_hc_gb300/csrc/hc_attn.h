@@ -1,0 +1,100 @@
+// Declarations shared by the translation units of the attention sublayer's operators (hc_rope.cu,
+// hc_kv.cu, hc_attend.cu and their entry points in hc_attn_api.cu); not part of the C ABI. The
+// launchers take arguments that the entry points have checked and return 0 or -7 (CUDA failure).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace hc {
+
+// bits of the device error word set by these operators
+enum : unsigned int {
+    kErrPage = 1u << 20,   // a slot or a page outside the cache
+    kErrSeq = 1u << 21,    // a sequence's bounds outside the arrays
+    kErrCopy = 1u << 22,   // a bounded wait for a copy of cache blocks ran out
+    kErrTile = 1u << 23,   // a bounded wait between the warps of a tile ran out
+};
+
+// ---- norms and rotation (hc_rope.cu) -------------------------------------------------------------
+constexpr int kRopeMaxFreqs = 128;
+struct RopeEntry {
+    unsigned long long turns;  // turns per position, modulo 1, as a fraction of 2^64
+    int axis;
+    int pad;
+};
+static_assert(sizeof(RopeEntry) == 16, "one table entry per 16 bytes");
+struct RopeTable {
+    RopeEntry e[kRopeMaxFreqs];
+};
+struct RopeArgs {
+    const void* q;
+    const void* k;
+    long long q_stride, k_stride;  // elements
+    const float* q_w;
+    const float* k_w;
+    const long long* positions;
+    const RopeEntry* table;
+    int rot, start, axes, pairs;
+    long long n;
+    int q_heads, k_heads, dim, gain_per_head;
+    float eps;
+    void* q_out;
+    void* k_out;
+    long long q_out_stride, k_out_stride;
+};
+int launch_prepare_rope(const RopeTable& t, int freqs, void* table, cudaStream_t stream);
+int launch_norm_rope(const RopeArgs& a, cudaStream_t stream);
+
+// ---- the 4-bit cache (hc_kv.cu) ------------------------------------------------------------------
+struct KvShape {
+    int pages, page_shift, heads, dim;  // page_size = 1 << page_shift
+    float k_unit, v_unit;
+};
+// bytes of 16 tokens of one head
+__host__ __device__ constexpr int kv_block_bytes(int dim) { return 18 * dim; }
+inline size_t kv_cache_bytes(const KvShape& s) {
+    return (static_cast<size_t>(s.pages) << (s.page_shift - 4)) * static_cast<size_t>(s.heads) *
+           static_cast<size_t>(kv_block_bytes(s.dim));
+}
+struct KvArgs {
+    const void* k_in;   // bf16 (write)
+    const void* v_in;
+    void* k_out;        // bf16 (read; either may be null)
+    void* v_out;
+    long long k_stride, v_stride;
+    const long long* slots;
+    long long n;
+    KvShape s;
+    unsigned char* cache;
+};
+int launch_kv_write(const KvArgs& a, cudaStream_t stream);
+int launch_kv_read(const KvArgs& a, cudaStream_t stream);
+int read_kv_error(unsigned int* word, int clear, cudaStream_t stream);
+
+// ---- attention (hc_attend.cu) --------------------------------------------------------------------
+constexpr int kAttMaxCtas = 512;                // CTAs of a launch whose partial results the workspace holds
+constexpr int kAttPartFloats = 32 * (128 + 2);  // one partial result: rows x (dim + maximum + sum), any variant
+constexpr size_t kAttCounterBytes = kAttMaxCtas * 4;
+constexpr size_t kAttWorkspaceBytes = kAttCounterBytes + size_t(2) * kAttMaxCtas * kAttPartFloats * 4;
+struct AttArgs {
+    const void* q;
+    long long q_stride;
+    const int* q_start;
+    const int* kv_len;
+    const int* page_table;
+    const unsigned char* cache;
+    long long n;
+    int seqs, max_q_len, max_pages, q_heads, causal, window;
+    float scale;
+    KvShape s;
+    void* out;
+    long long out_stride;
+    float* lse;
+    void* workspace;
+};
+int launch_attention(const AttArgs& a, cudaStream_t stream);
+int read_attention_error(unsigned int* word, int clear, cudaStream_t stream);
+
+}  // namespace hc

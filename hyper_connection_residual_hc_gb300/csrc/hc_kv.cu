@@ -1,0 +1,430 @@
+// The 4-bit key/value cache: quantising tokens as they are written, and reading them back (format and
+// byte layout: include/hc.h).
+//
+// Each 16 columns of a token's head share the scale s = e4m3(amax / (6 unit)), and a code is
+// e2m1(x / (s unit)). Both are decided exactly: x has 8 significant bits, s 4 and a border between two
+// codes 3, so a quotient x / s either is a border exactly or is off it by 2^-9 relative and more. The
+// quotient is taken as x * (1/s) and one residual step (v + (x - v s) / s, the classical correction of
+// a quotient by its remainder), which is exact whenever the quotient has few bits: ties are seen as ties.
+//
+// The layout is the one that the attention's matrix instructions read, so the bytes of one token are
+// scattered in 1- and 2-byte pieces over its block of 16 tokens. A block takes 16 tokens of the call and
+// looks for a run among their slots: 16 consecutive tokens on the 16 slots of one cache block. A run
+// (prefill) goes block-wise: one warp takes the block of one head, each lane the same tokens and columns
+// that it has in the layout, so that it holds whole 16-column groups and whole words, and every store is
+// 16 bytes wide. Other tokens (decode, ragged ends) go token-wise: one warp per token and head, 8 columns
+// a lane. Both give the same bytes.
+//
+// Bound: HBM; (4 + 1.125) bytes a value pair each way.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "hc_attn.h"
+#include "hc_kv.cuh"
+
+namespace hc {
+namespace {
+
+__device__ unsigned int g_hc_kv_error = 0;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kGroup = 16;                 // tokens of the call per block
+constexpr int kWindow = 3 * kGroup - 2;    // slots looked at: 15 before the group, 15 after it
+
+// the largest magnitude's bits (the sign bit cleared, bf16 orders as its bits; NaN above infinity)
+__device__ __forceinline__ uint32_t amax_bits(const uint32_t* w, int words) {
+    uint32_t m = 0;
+    for (int i = 0; i < words; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    return max(m & 0xFFFFu, m >> 16);
+}
+
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax, float inv_unit) {
+    if (amax >= 0x7F80u) return 0x7Fu;  // NaN or infinity in the group
+    const float q = __fdiv_rn(__uint_as_float(amax << 16) * inv_unit, 6.0f);
+    uint16_t two;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(q));
+    return two & 0xFFu;
+}
+
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    const uint32_t h = e4m3x2_to_f16(byte);
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
+}
+
+// one bf16 pair (the even column in the low half) -> a byte of two codes
+__device__ __forceinline__ uint32_t code_byte(uint32_t pair, float inv_unit, float s, float rs) {
+    const float a = __uint_as_float(pair << 16) * inv_unit, b = __uint_as_float(pair & 0xFFFF0000u) * inv_unit;
+    float u = a * rs, v = b * rs;
+    // beyond 8 the code is the largest whatever the quotient's last bits (and an infinite one has no remainder)
+    if (fabsf(u) < 8.f) u = fmaf(fmaf(-u, s, a), rs, u);
+    if (fabsf(v) < 8.f) v = fmaf(fmaf(-v, s, b), rs, v);
+    uint32_t r;
+    asm("{\n\t.reg .b8 c;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\t"
+        "cvt.u32.u8 %0, c;\n\t}"
+        : "=r"(r)
+        : "f"(v), "f"(u));
+    return r;
+}
+
+__device__ __forceinline__ float recip_or_zero(float s) { return s > 0.f ? __frcp_rn(s) : 0.f; }
+
+// ---- one token's eight columns (token-wise) ------------------------------------------------------
+
+template <int D>
+__device__ __forceinline__ void write_token(const KvArgs& p, long long i, int h, unsigned char* block, int t, int lane) {
+    constexpr int kUnits = 2 * D / 8;  // keys, then values, eight columns each
+#pragma unroll
+    for (int u0 = 0; u0 < kUnits; u0 += 32) {
+        const int u = u0 + lane;
+        const bool active = u < kUnits;
+        const bool val = u >= D / 8;
+        const int col = 8 * (u % (D / 8));
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (active) {
+            const __nv_bfloat16* src = val ? static_cast<const __nv_bfloat16*>(p.v_in) + i * p.v_stride
+                                           : static_cast<const __nv_bfloat16*>(p.k_in) + i * p.k_stride;
+            x = __ldcs(reinterpret_cast<const uint4*>(src + static_cast<long long>(h) * D + col));
+        }
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t m = amax_bits(w, 4);
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        const float inv_unit = 1.0f / (val ? p.s.v_unit : p.s.k_unit);  // exact: a power of two
+        const uint32_t sb = scale_byte(m, inv_unit);
+        const float s = scale_value(sb), rs = recip_or_zero(s);
+        uint32_t b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = code_byte(w[e], inv_unit, s, rs);
+        if (!active) continue;
+        if (val) {
+            unsigned char* dst = block + KvPlace<D>::value_code(t, col);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[4 * e] = static_cast<unsigned char>(b[e]);
+            if (lane % 2 == 0) block[KvPlace<D>::value_scale(t, col)] = static_cast<unsigned char>(sb);
+        } else {
+            unsigned char* dst = block + KvPlace<D>::key_code(t, col);
+            *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(b[0] | b[1] << 8);
+            *reinterpret_cast<uint16_t*>(dst + 4) = static_cast<uint16_t>(b[2] | b[3] << 8);
+            if (lane % 2 == 0) block[KvPlace<D>::key_scale(t, col)] = static_cast<unsigned char>(sb);
+        }
+    }
+}
+
+// a pair of fp16 values times the unit, as a bf16 pair (exact)
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t v, float unit) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&v);
+    const float2 f = __half22float2(h);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(f.x * unit, f.y * unit);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t both(uint32_t scale_byte_) { return e4m3x2_to_f16(scale_byte_ | scale_byte_ << 8); }
+
+// block null: zeros
+template <int D>
+__device__ __forceinline__ void read_token(const KvArgs& p, long long i, int h, const unsigned char* block, int t,
+                                           int lane) {
+    constexpr int kUnits = 2 * D / 8;
+#pragma unroll
+    for (int u0 = 0; u0 < kUnits; u0 += 32) {
+        const int u = u0 + lane;
+        if (u >= kUnits) continue;
+        const bool val = u >= D / 8;
+        const int col = 8 * (u % (D / 8));
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(val ? p.v_out : p.k_out);
+        if (!dst) continue;
+        uint4 o = make_uint4(0, 0, 0, 0);
+        if (block) {
+            uint32_t w, s;
+            if (val) {
+                const unsigned char* src = block + KvPlace<D>::value_code(t, col);
+                w = src[0] | src[4] << 8 | src[8] << 16 | static_cast<uint32_t>(src[12]) << 24;
+                s = both(block[KvPlace<D>::value_scale(t, col)]);
+            } else {
+                const unsigned char* src = block + KvPlace<D>::key_code(t, col);
+                w = *reinterpret_cast<const uint16_t*>(src) | static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(src + 4)) << 16;
+                s = both(block[KvPlace<D>::key_scale(t, col)]);
+            }
+            uint32_t x[4];
+            e2m1_word_to_f16(w, x[0], x[1], x[2], x[3]);
+            const float unit = val ? p.s.v_unit : p.s.k_unit;
+            o = make_uint4(f16x2_to_bf16x2(mul_f16x2(x[0], s), unit), f16x2_to_bf16x2(mul_f16x2(x[1], s), unit),
+                           f16x2_to_bf16x2(mul_f16x2(x[2], s), unit), f16x2_to_bf16x2(mul_f16x2(x[3], s), unit));
+        }
+        const long long stride = val ? p.v_stride : p.k_stride;
+        __stcs(reinterpret_cast<uint4*>(dst + i * stride + static_cast<long long>(h) * D + col), o);
+    }
+}
+
+// ---- a whole block of 16 tokens (block-wise) ------------------------------------------------------
+// Lane (r, c) = (lane / 4, lane % 4). Keys: tokens r and r + 8, columns [c D/4, (c+1) D/4). Values: tokens
+// 2c, 2c+1, 2c+8, 2c+9, columns [r D/8, (r+1) D/8).
+
+template <int D>
+__device__ __forceinline__ void write_block(const KvArgs& p, long long i, int h, unsigned char* block, int lane) {
+    const int r = lane / 4, c = lane % 4;
+    {
+        constexpr int kN = D / 4;  // columns a lane
+        const float inv_unit = 1.0f / p.s.k_unit;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.k_in) + i * p.k_stride +
+                                   static_cast<long long>(h) * D + c * kN;
+        uint32_t codes[2][kN / 8];  // per token, 8 columns a word
+        uint32_t scales = 0, scales2 = 0;
+#pragma unroll
+        for (int hw = 0; hw < 2; ++hw) {
+            const uint4* row = reinterpret_cast<const uint4*>(src + (r + 8 * hw) * p.k_stride);
+            uint4 x[kN / 8];
+#pragma unroll
+            for (int e = 0; e < kN / 8; ++e) x[e] = __ldcs(row + e);
+#pragma unroll
+            for (int g = 0; g < kN / 16; ++g) {
+                const uint32_t w[8] = {x[2 * g].x, x[2 * g].y, x[2 * g].z, x[2 * g].w,
+                                       x[2 * g + 1].x, x[2 * g + 1].y, x[2 * g + 1].z, x[2 * g + 1].w};
+                const uint32_t sb = scale_byte(amax_bits(w, 8), inv_unit);
+                const float s = scale_value(sb), rs = recip_or_zero(s);
+                const int at = hw * (kN / 16) + g;  // place among the lane's scale bytes
+                if (at < 4) scales |= sb << (8 * at);
+                else scales2 |= sb << (8 * (at - 4));
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    codes[hw][2 * g + q] = code_byte(w[4 * q], inv_unit, s, rs) | code_byte(w[4 * q + 1], inv_unit, s, rs) << 8 |
+                                           code_byte(w[4 * q + 2], inv_unit, s, rs) << 16 |
+                                           code_byte(w[4 * q + 3], inv_unit, s, rs) << 24;
+            }
+        }
+#pragma unroll
+        for (int quad = 0; quad < D / 64; ++quad) {
+            // word s of the quad: four columns of token r (low half), the same of token r + 8
+            uint32_t o[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const uint32_t a = codes[0][2 * quad + s / 2], b = codes[1][2 * quad + s / 2];
+                o[s] = __byte_perm(a, b, s % 2 ? 0x7632 : 0x5410);
+            }
+            *reinterpret_cast<uint4*>(block + quad * 512 + lane * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        unsigned char* sc = block + KvPlace<D>::kKeyScales + lane * (D / 32);
+        if constexpr (D == 64) *reinterpret_cast<uint16_t*>(sc) = static_cast<uint16_t>(scales);
+        else if constexpr (D == 128) *reinterpret_cast<uint32_t*>(sc) = scales;
+        else *reinterpret_cast<uint2*>(sc) = make_uint2(scales, scales2);
+    }
+    {
+        constexpr int kN = D / 8;
+        const float inv_unit = 1.0f / p.s.v_unit;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.v_in) + i * p.v_stride +
+                                   static_cast<long long>(h) * D + r * kN;
+        uint32_t codes[4][kN / 8];
+        uint32_t scales[(kN + 15) / 16] = {};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = 2 * c + j % 2 + 8 * (j / 2);
+            const uint4* row = reinterpret_cast<const uint4*>(src + t * p.v_stride);
+            uint4 x[kN / 8];
+#pragma unroll
+            for (int e = 0; e < kN / 8; ++e) x[e] = __ldcs(row + e);
+            if constexpr (D == 64) {
+                const uint32_t w[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
+                uint32_t m = amax_bits(w, 4);
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));  // the 16 columns are shared by rows r and r ^ 1
+                const uint32_t sb = scale_byte(m, inv_unit);
+                const float s = scale_value(sb), rs = recip_or_zero(s);
+                scales[0] |= sb << (8 * j);
+                codes[j][0] = code_byte(w[0], inv_unit, s, rs) | code_byte(w[1], inv_unit, s, rs) << 8 |
+                              code_byte(w[2], inv_unit, s, rs) << 16 | code_byte(w[3], inv_unit, s, rs) << 24;
+            } else {
+#pragma unroll
+                for (int g = 0; g < kN / 16; ++g) {
+                    const uint32_t w[8] = {x[2 * g].x, x[2 * g].y, x[2 * g].z, x[2 * g].w,
+                                           x[2 * g + 1].x, x[2 * g + 1].y, x[2 * g + 1].z, x[2 * g + 1].w};
+                    const uint32_t sb = scale_byte(amax_bits(w, 8), inv_unit);
+                    const float s = scale_value(sb), rs = recip_or_zero(s);
+                    scales[g] |= sb << (8 * j);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        codes[j][2 * g + q] =
+                            code_byte(w[4 * q], inv_unit, s, rs) | code_byte(w[4 * q + 1], inv_unit, s, rs) << 8 |
+                            code_byte(w[4 * q + 2], inv_unit, s, rs) << 16 | code_byte(w[4 * q + 3], inv_unit, s, rs) << 24;
+                }
+            }
+        }
+#pragma unroll
+        for (int quad = 0; quad < D / 64; ++quad) {
+            // word m: byte j holds columns 2m, 2m + 1 of token j
+            uint32_t o[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const uint32_t lo = __byte_perm(codes[0][quad], codes[1][quad], m | (m + 4) << 4);
+                const uint32_t hi = __byte_perm(codes[2][quad], codes[3][quad], m | (m + 4) << 4);
+                o[m] = __byte_perm(lo, hi, 0x5410);
+            }
+            *reinterpret_cast<uint4*>(block + KvPlace<D>::kValueCodes + quad * 512 + lane * 16) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        unsigned char* sc = block + KvPlace<D>::kValueScales;
+        if constexpr (D == 64) {
+            if (r % 2 == 0) *reinterpret_cast<uint32_t*>(sc + (r / 2 * 4 + c) * 4) = scales[0];
+        } else {
+#pragma unroll
+            for (int g = 0; g < kN / 16; ++g)
+                *reinterpret_cast<uint32_t*>(sc + ((r * (kN / 16) + g) * 4 + c) * 4) = scales[g];
+        }
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void read_block(const KvArgs& p, long long i, int h, const unsigned char* block, int lane) {
+    const int r = lane / 4, c = lane % 4;
+    if (p.k_out) {
+        constexpr int kN = D / 4;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.k_out) + i * p.k_stride + static_cast<long long>(h) * D + c * kN;
+        const unsigned char* sc = block + KvPlace<D>::kKeyScales + lane * (D / 32);
+#pragma unroll
+        for (int quad = 0; quad < D / 64; ++quad) {
+            const uint4 v = __ldcs(reinterpret_cast<const uint4*>(block + quad * 512 + lane * 16));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t s0 = both(sc[quad]), s1 = both(sc[D / 64 + quad]);
+            uint32_t a[8], b[8];  // 16 columns of tokens r and r + 8
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                uint32_t x0, x1, x2, x3;
+                e2m1_word_to_f16(w[s], x0, x1, x2, x3);
+                a[2 * s] = f16x2_to_bf16x2(mul_f16x2(x0, s0), p.s.k_unit);
+                a[2 * s + 1] = f16x2_to_bf16x2(mul_f16x2(x1, s0), p.s.k_unit);
+                b[2 * s] = f16x2_to_bf16x2(mul_f16x2(x2, s1), p.s.k_unit);
+                b[2 * s + 1] = f16x2_to_bf16x2(mul_f16x2(x3, s1), p.s.k_unit);
+            }
+            uint4* ra = reinterpret_cast<uint4*>(dst + r * p.k_stride + quad * 16);
+            uint4* rb = reinterpret_cast<uint4*>(dst + (r + 8) * p.k_stride + quad * 16);
+            __stcs(ra, make_uint4(a[0], a[1], a[2], a[3]));
+            __stcs(ra + 1, make_uint4(a[4], a[5], a[6], a[7]));
+            __stcs(rb, make_uint4(b[0], b[1], b[2], b[3]));
+            __stcs(rb + 1, make_uint4(b[4], b[5], b[6], b[7]));
+        }
+    }
+    if (p.v_out) {
+        constexpr int kN = D / 8;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.v_out) + i * p.v_stride + static_cast<long long>(h) * D + r * kN;
+        const unsigned char* sc = block + KvPlace<D>::kValueScales;
+#pragma unroll
+        for (int quad = 0; quad < D / 64; ++quad) {
+            const uint4 v = __ldcs(reinterpret_cast<const uint4*>(block + KvPlace<D>::kValueCodes + quad * 512 + lane * 16));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t s4 = *reinterpret_cast<const uint32_t*>(sc + ((r * kN + quad * 8) / 16 * 4 + c) * 4);
+            uint32_t o[4][4];  // token j, 8 columns
+#pragma unroll
+            for (int m = 0; m < 4; ++m) e2m1_word_to_f16(w[m], o[0][m], o[1][m], o[2][m], o[3][m]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t s = both(s4 >> (8 * j) & 0xFFu);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) o[j][m] = f16x2_to_bf16x2(mul_f16x2(o[j][m], s), p.s.v_unit);
+                const int t = 2 * c + j % 2 + 8 * (j / 2);
+                __stcs(reinterpret_cast<uint4*>(dst + t * p.v_stride + quad * 8), make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]));
+            }
+        }
+    }
+}
+
+// gridDim.x: groups of 16 tokens; gridDim.y: parts of a group's work
+template <int D, bool kRead>
+__global__ void __launch_bounds__(kThreads) kv_move_kernel(const KvArgs p) {
+    __shared__ long long slot[kWindow];
+    __shared__ unsigned char run[kWindow];  // 1: 16 consecutive tokens on one cache block begin here
+    const int tid = static_cast<int>(threadIdx.x);
+    const int warp = tid / 32, lane = tid % 32;
+    const long long i0 = static_cast<long long>(blockIdx.x) * kGroup;
+    const long long cap = static_cast<long long>(p.s.pages) << p.s.page_shift;
+    if (tid < kWindow) {
+        const long long i = i0 - (kGroup - 1) + tid;
+        long long s = -1;
+        if (i >= 0 && i < p.n) {
+            s = p.slots[i];
+            if (s >= cap) {
+                if (blockIdx.y == 0 && i >= i0 && i < i0 + kGroup) atomicOr(&g_hc_kv_error, kErrPage);
+                s = -1;
+            }
+        }
+        slot[tid] = s < 0 ? -1 : s;
+    }
+    __syncthreads();
+    if (tid < kWindow) {
+        bool ok = tid + kGroup <= kWindow && slot[tid] >= 0 && slot[tid] % kGroup == 0;
+        for (int t = 1; t < kGroup && ok; ++t) ok = slot[tid + t] == slot[tid] + t;
+        run[tid] = ok ? 1 : 0;
+    }
+    __syncthreads();
+    const int heads = p.s.heads;
+    auto block_of = [&](long long s, int h) {
+        const long long page = s >> p.s.page_shift;
+        const int in_page = static_cast<int>(s & ((1LL << p.s.page_shift) - 1));
+        return p.cache + (((page * heads + h) << (p.s.page_shift - 4)) + in_page / kGroup) * kv_block_bytes(D);
+    };
+    const int worker = static_cast<int>(blockIdx.y) * kWarps + warp, workers = static_cast<int>(gridDim.y) * kWarps;
+    // the run that begins in this group, if any (two runs are 16 tokens apart at least)
+    for (int j = kGroup - 1; j < 2 * kGroup - 1; ++j) {
+        if (!run[j]) continue;
+        const long long i = i0 + j - (kGroup - 1);
+        for (int h = worker; h < heads; h += workers) {
+            if constexpr (kRead) read_block<D>(p, i, h, block_of(slot[j], h), lane);
+            else write_block<D>(p, i, h, block_of(slot[j], h), lane);
+        }
+    }
+    // the tokens of this group that no run has
+    for (int x = worker; x < kGroup * heads; x += workers) {
+        const int j = kGroup - 1 + x % kGroup, h = x / kGroup;
+        const long long i = i0 + x % kGroup, s = slot[j];
+        if (i >= p.n) continue;
+        if (s >= 0 && run[j - static_cast<int>(s % kGroup)]) continue;
+        if constexpr (kRead) {
+            read_token<D>(p, i, h, s < 0 ? nullptr : block_of(s, h), s < 0 ? 0 : static_cast<int>(s % kGroup), lane);
+        } else {
+            if (s >= 0) write_token<D>(p, i, h, block_of(s, h), static_cast<int>(s % kGroup), lane);
+        }
+    }
+}
+
+template <bool kRead>
+int launch_move(const KvArgs& a, cudaStream_t stream) {
+    if (a.n <= 0) return 0;
+    int dev = 0, sms = 152;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return -7;
+    const long long groups = (a.n + kGroup - 1) / kGroup;
+    // few groups: spread each over enough blocks to fill the GPU twice, down to one token and head a warp
+    long long parts = (2LL * sms + groups - 1) / groups;
+    const long long most = (static_cast<long long>(kGroup) * a.s.heads + kWarps - 1) / kWarps;
+    if (parts > most) parts = most;
+    if (parts < 1) parts = 1;
+    const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(parts));
+    switch (a.s.dim) {
+        case 64: kv_move_kernel<64, kRead><<<grid, kThreads, 0, stream>>>(a); break;
+        case 128: kv_move_kernel<128, kRead><<<grid, kThreads, 0, stream>>>(a); break;
+        default: kv_move_kernel<256, kRead><<<grid, kThreads, 0, stream>>>(a); break;
+    }
+    return cudaGetLastError() == cudaSuccess ? 0 : -7;
+}
+
+}  // namespace
+
+int launch_kv_write(const KvArgs& a, cudaStream_t stream) { return launch_move<false>(a, stream); }
+int launch_kv_read(const KvArgs& a, cudaStream_t stream) { return launch_move<true>(a, stream); }
+
+int read_kv_error(unsigned int* word, int clear, cudaStream_t stream) {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbolAsync(&v, g_hc_kv_error, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess) return -7;
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return -7;
+    if (clear && v != 0) {
+        const unsigned int z = 0;
+        if (cudaMemcpyToSymbolAsync(g_hc_kv_error, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess) return -7;
+        if (cudaStreamSynchronize(stream) != cudaSuccess) return -7;
+    }
+    *word = v;
+    return 0;
+}
+
+}  // namespace hc

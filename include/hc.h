@@ -54,7 +54,7 @@ typedef struct CUstream_st* hc_stream_t; /* identical to cudaStream_t */
 enum {
     HC_OK = 0,
     HC_ERR_NULL = -1,        /* a required pointer is NULL */
-    HC_ERR_SHAPE = -2,       /* n < 0, or hc < 1, or d not a positive multiple of 8 */
+    HC_ERR_SHAPE = -2,       /* n < 0, or hc < 1, or d not a positive multiple of 8, or what a call says of its shape */
     HC_ERR_UNSUPPORTED = -3, /* a valid configuration not implemented (hc > 8, d > 65536, no cooperative launch) */
     HC_ERR_ALIGN = -4,       /* a device pointer is not 16-byte aligned */
     HC_ERR_ALIAS = -5,       /* an output overlaps an input or another output (see each call) */
@@ -335,9 +335,173 @@ int hc_fused_ctas(int* ctas);
 int hc_debug_wait_flag(const unsigned long long* flags, int count, unsigned long long value, int64_t limit_ns,
                        hc_stream_t stream);
 
+/* ---- The attention sublayer ---------------------------------------------------------------------
+ * What stands between a sublayer's q/k/v projections and its output projection when it serves
+ * tokens: the norms and the position rotation of queries and keys, a key/value cache held in 4 bits
+ * on pages, and the attention over it. The input of the projections is the y_normed of the calls
+ * above; what the output projection makes of `out` is the Delta of the next hc_post_then_pre. No
+ * counterpart on the pages (they do not show the attention): these are this library's own operators
+ * for the same serving loop, under the conventions at the top of this file, except that
+ *   - q, k, v and the outputs may be strided: an array [n, heads, dim] whose token t starts `stride`
+ *     elements after token t - 1 (a slice of a fused projection's output, say). A stride is a
+ *     multiple of 8 elements and at least heads * dim (HC_ERR_SHAPE otherwise); heads and dim are
+ *     contiguous within a token. The 16-byte rule holds for q, k, v, out and the cache; positions,
+ *     slots, tables, lengths and lse need their own type's alignment only;
+ *   - indices that a call reads on the device (slots, page tables, lengths) cannot be checked on the
+ *     host. One that is out of range is not followed: the call leaves out what it points to, as each
+ *     call says, and sets a bit of the device error word (hc_device_error, bits 20-23). */
+
+enum {
+    HC_ROPE_HALF = 0, /* frequency j turns columns start + j and start + rot/2 + j */
+    HC_ROPE_PAIRS = 1 /* frequency j turns columns start + 2j and start + 2j + 1 */
+};
+
+/* The rotation of hc_qk_norm_rope: `rot` columns of each head from column `start` on, rot / 2
+ * frequencies of `table` (hc_prepare_rope). rot = 0: no rotation (table and positions unused). */
+typedef struct {
+    const void* table; /* [device] hc_rope_table_size bytes, filled by hc_prepare_rope for this rot and axes */
+    int rot;           /* a multiple of 16, 0..dim - start */
+    int start;         /* a multiple of 8 */
+    int axes;          /* rows of `positions`: 1..4 */
+    int style;         /* HC_ROPE_HALF or HC_ROPE_PAIRS */
+} hc_rope_t;
+
+/* Head layout and norm of hc_qk_norm_rope. */
+typedef struct {
+    int q_heads;       /* >= 1 */
+    int k_heads;       /* >= 0; 0: queries only (k, k_w, k_out unused) */
+    int dim;           /* width of a head: a multiple of 8, at most 256 */
+    int gain_per_head; /* 0: the gains are [dim], the same for every head; 1: q_w [q_heads, dim], k_w [k_heads, dim] */
+    float norm_eps;    /* >= 0, finite */
+} hc_heads_t;
+
+/* Size in bytes of the rotation table for `rot` rotated columns (16 per frequency; 0 for rot = 0).
+ * Returns HC_ERR_NULL, or HC_ERR_SHAPE (rot negative, above 256 or not a multiple of 16). Host-only. */
+int hc_rope_table_size(int rot, size_t* bytes);
+
+/* Fill a rotation table, once per set of frequencies. Both arrays are in HOST memory and are read
+ * before the call returns:
+ *   inv_freq fp64 [rot/2]  radians per position (scaled as the model scales them); finite
+ *   axis     int  [rot/2]  the row of `positions` that a frequency reads, 0..axes-1 (time, height and
+ *                          width of an image or video patch, say, in sections or interleaved);
+ *                          NULL: row 0 for all
+ * The table keeps each frequency in turns per position as a 64-bit fixed-point fraction, so that a
+ * rotation's angle modulo one turn is an exact integer product for every 64-bit position; its error
+ * is that of the frequency itself, 2^-52 relative and 2^-65 turns per position.
+ * HC_ERR_NULL, HC_ERR_SHAPE (rot as above or 0, axes outside 1..4), HC_ERR_ARG (an axis out of range, a
+ * frequency not finite), HC_ERR_ALIGN. */
+int hc_prepare_rope(const double* inv_freq, const int* axis, int rot, int axes, void* table, hc_stream_t stream);
+
+/* RMSNorm of every query and key head, then the position rotation, in one pass ("Final RMSNorm" page,
+ * RMSNorm excerpt, per head; the rotation as hc_rope_t says), for each token t and head h:
+ *   u = w * x / sqrt(mean(x^2) + norm_eps);  (a, b) a pair of u, phi = positions[axis, t] * inv_freq:
+ *   a' = a cos phi - b sin phi, b' = b cos phi + a sin phi     (fp32 math, rounded once to bf16)
+ *   q, k         [device] bf16 [n, q_heads, dim], [n, k_heads, dim], strided
+ *   q_w, k_w     [device] fp32 gains (gain_per_head); NULL: 1 (16-byte aligned)
+ *   positions    [device] int64 [axes, n]; any value, negative ones too
+ *   q_out, k_out [device] bf16, strided. q_out may be exactly q (with q's stride), k_out exactly k;
+ *                otherwise outputs must not overlap each other or an input (HC_ERR_ALIAS). Rows of one
+ *                stride that lie side by side (the q, k and v columns of one buffer) do not overlap. */
+int hc_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const float* q_w,
+                    const float* k_w, const int64_t* positions, hc_rope_t r, int64_t n, hc_heads_t s, void* q_out,
+                    int64_t q_out_stride, void* k_out, int64_t k_out_stride, hc_stream_t stream);
+
+/* A key/value cache in 4 bits on pages. */
+typedef struct {
+    int pages;     /* pages in the buffer, >= 1 */
+    int page_size; /* tokens per page: a power of two, 16..1024 */
+    int heads;     /* key/value heads, 1..1024 */
+    int dim;       /* width of a head: 64, 128 or 256 (HC_ERR_UNSUPPORTED otherwise) */
+    float k_scale; /* the values' unit, a power of two in 2^-40..2^40 (HC_ERR_ARG otherwise); 1 suits normed */
+    float v_scale; /* keys and values whose blocks have a largest magnitude between about 0.1 and 2688 */
+} hc_kv_shape_t;
+
+/* Size in bytes of a cache: pages * page_size * heads * dim * 9 / 8 (4.5 bits a value, keys and values).
+ *
+ * Format. 16 values next to each other along dim share a scale: s = e4m3(max|x| / (6 unit)), rounded to
+ * nearest even, at most 448; code = e2m1(x / (s unit)), rounded to nearest even, at most 6 (magnitudes 0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6 for codes 0-7, bit 3 the sign). A value is code * s * unit. A block that holds a
+ * NaN or an infinity gets the scale NaN: all its 16 values read as NaN.
+ *
+ * Layout, for callers who move pages or look into them: [pages, heads, page_size / 16] blocks of 16 tokens
+ * of one head, 18 * dim bytes each: 8*dim bytes of key codes, dim of key scales, 8*dim of value codes, dim
+ * of value scales, in the order in which the attention's matrix instructions take them. With t = 0..15 the
+ * token and i the column:
+ *   key code    byte  K/16*512 + t%8*64 + i/(dim/4)*16 + K/4%4*4 + t/8*2 + K/2%2,   K = i % (dim/4)
+ *   key scale   byte  t%8*dim/8 + i/(dim/4)*dim/32 + t/8*dim/64 + K/16
+ *   value code  byte  V/8*512 + i/(dim/8)*64 + t%8/2*16 + V/2%4*4 + t/8*2 + t%2,    V = i % (dim/8)
+ *   value scale byte  i/16*16 + t%8/2*4 + t/8*2 + t%2
+ * (all divisions of integers); even columns lie in the low four bits of a code byte, odd ones in the high.
+ * A token's bytes are its own: writing one touches no other. A page may be copied as it is.
+ * Returns HC_ERR_NULL, HC_ERR_SHAPE, HC_ERR_UNSUPPORTED or HC_ERR_ARG. Host-only, no CUDA call. */
+int hc_kv_cache_size(hc_kv_shape_t s, size_t* bytes);
+
+/* Quantise keys and values as they are written to the cache.
+ *   k, v  [device] bf16 [n, heads, dim], strided
+ *   slots [device] int64 [n]: page * page_size + place in the page of each token; negative: the token is
+ *         left out (padding). A slot past the cache is left out too and sets bit 20 of the error word.
+ *         The slots of one call must differ: of two tokens with one slot, each byte is one or the other's.
+ *   cache [device] hc_kv_cache_size bytes; only the written tokens' bytes change
+ * Each value is rounded once (an exact quotient decides ties), so the bytes do not depend on how tokens
+ * are grouped into calls. n at most 2^31 - 1. The cache must not overlap an input (HC_ERR_ALIAS). */
+int hc_kv_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int64_t* slots, int64_t n,
+                hc_kv_shape_t s, void* cache, hc_stream_t stream);
+
+/* Read tokens of the cache back as bf16 (exact while the products stay normal bf16 numbers: units of
+ * 2^-40..2^40 do).
+ *   slots        [device] int64 [n], in any order, the same one more than once if need be; a negative slot
+ *                reads as zeros, one past the cache as zeros with bit 20 of the error word
+ *   k_out, v_out [device] bf16 [n, heads, dim], strided; either may be NULL */
+int hc_kv_read(const void* cache, const int64_t* slots, int64_t n, hc_kv_shape_t s, void* k_out, int64_t k_stride,
+               void* v_out, int64_t v_stride, hc_stream_t stream);
+
+/* A call of hc_kv_attention. */
+typedef struct {
+    int64_t n;      /* rows of q and out: the queries of all sequences, at most 2^31 - 1 */
+    int seqs;       /* sequences, >= 0 */
+    int max_q_len;  /* queries of the longest sequence: sizes the tiles (longer ones are right, but slower) */
+    int max_pages;  /* columns of the page table */
+    int q_heads;    /* a multiple of the cache's heads, up to 128 times as many: head h reads kv head h * heads / q_heads */
+    int causal;     /* 1: a query sees the keys up to its own position; 0: all keys of its sequence */
+    int window;     /* > 0 (causal only): a query sees the last `window` of those keys; 0: all */
+    float scale;    /* of q . k, before the softmax; finite, >= 0 */
+} hc_attention_t;
+
+/* Size in bytes of the workspace of hc_kv_attention: room for the partial results of 512 CTAs and their
+ * counters. The caller allocates it once [device], 16-byte aligned, fills it with zeros before its first
+ * use and then keeps passing it unchanged: each call leaves the counters at zero. Calls that may run at the
+ * same time (two graphs replayed on two streams, say) must not share one. Host-only, no CUDA call. */
+int hc_kv_workspace_size(size_t* bytes);
+
+/* Softmax attention of ragged queries over the 4-bit cache: decode (one query a sequence), drafted tokens
+ * checked together, prefill in chunks. Sequence b has the queries q_start[b] .. q_start[b+1]-1 (they are its
+ * last positions: query i of q_len stands at kv_len - q_len + i; their own keys are in the cache already)
+ * and kv_len[b] keys, key p on page page_table[b, p / page_size]:
+ *   z_p = scale * q . K_p over the keys that the query sees; out = sum_p softmax(z)_p V_p; lse = log sum_p e^z_p
+ * A query that sees no key gets out = 0 and lse = -infinity.
+ *   q          [device] bf16 [n, q_heads, dim], strided
+ *   q_start    [device] int32 [seqs + 1], not decreasing, from 0 to at most n; rows of out and lse that no
+ *              sequence has are left as they were. Entries are clamped to 0..n (bit 21 of the error word).
+ *   kv_len     [device] int32 [seqs]; clamped to 0..max_pages * page_size (bit 21)
+ *   page_table [device] int32 [seqs, max_pages]; only the entries of pages with keys that some query of a tile
+ *              sees are read. The keys of a page that is out of range are left out (bit 20).
+ *   cache      [device] as hc_kv_write filled it
+ *   out        [device] bf16 [n, q_heads, dim], strided; lse [device] fp32 [n, q_heads] or NULL
+ *   workspace  [device] see hc_kv_workspace_size
+ * The products are taken on the tensor cores in fp16 with fp32 sums: the 4-bit keys and values are exact in
+ * fp16; a query row is scaled by a power of two first, so that its bf16 values are exact too (but for those
+ * below 2^-22 of the row's largest); a softmax weight is rounded to fp16's 11 bits. The result of a call does
+ * not change from run to run. Keys and values that a query does not see never reach its result, NaN ones
+ * included. Outputs and the workspace must not overlap each other or an input (HC_ERR_ALIAS). */
+int hc_kv_attention(const void* q, int64_t q_stride, const int* q_start, const int* kv_len, const int* page_table,
+                    const void* cache, hc_attention_t a, hc_kv_shape_t s, void* out, int64_t out_stride, float* lse,
+                    void* workspace, hc_stream_t stream);
+
 /* Read the device-side error word of the current device: nonzero when a kernel gave up a
  * bounded wait (it then returned early and its outputs are not valid); bits 0-15 are the fused
- * kernel's waits, bits 16-19 those of the generic path's projection. Synchronises `stream`.
+ * kernel's waits, bits 16-19 those of the generic path's projection, bits 22-23 those of
+ * hc_kv_attention. Bits 20 and 21 tell of an index out of range that a call left out (hc_kv_write,
+ * hc_kv_read, hc_kv_attention): its other results are valid. Synchronises `stream`.
  * If `clear` is nonzero the word is reset to 0, and, when it was nonzero, the library's own fixed
  * scratch of hc_post_then_pre_noalloc on this device is zeroed as well (on `stream`; no call using it
  * may still be running). Returns HC_OK, HC_ERR_NULL or HC_ERR_CUDA. */
