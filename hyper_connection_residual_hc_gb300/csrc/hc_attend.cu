@@ -1,18 +1,40 @@
 // Softmax attention of ragged queries over the 4-bit cache (formulas, masks and format: include/hc.h).
 //
-// One warp takes one query row of one head and walks its keys in cache blocks of 16 tokens with a running
-// maximum and sum. Lane (r, c) = (lane / 4, lane % 4) holds the tokens and columns of a block that the
-// layout gives it: keys r and r + 8, columns [c D/4, (c+1) D/4); values 2c, 2c+1, 2c+8, 2c+9, columns
-// [r D/8, (r+1) D/8).
+// The rows of a sequence and a kv head are its queries times the group of query heads that share the kv head
+// (row = query * group + head in the group): they read the same keys, so a tile takes R = 8 kNT of them at once
+// and the products go to mma.sync.m16n8k16 with the cache as the A operand (16 tokens, or 16 columns, by 16)
+// and the rows as the 8 columns of B: a tile of few rows wastes nothing, and A comes straight from registers.
+// The tensor memory path (tcgen05) would have to write every dequantised block to shared memory first, 8 times
+// the bytes that the cache has; this kernel's bound is the dequantisation and HBM, not the products.
+//
+// A cache block (16 tokens, one head) is laid out in A-fragment order: lane (r, c) = (lane / 4, lane % 4) finds
+// in its own 32-bit words the codes of keys r and r + 8, columns [c D/4, (c+1) D/4) (the contraction index of
+// the product may run in any order, so a lane takes whole 16-column groups and needs few scales), and of values
+// 2c, 2c+1, 2c+8, 2c+9, columns [r D/8, (r+1) D/8). A word becomes four fp16 pairs (cvt from e2m1x2), times its
+// scale (exact in fp16). S^T = K Q^T leaves lane (r, c) the scores of tokens r, r + 8 and rows 2c, 2c + 1; the
+// weights, rounded to fp16, are turned into the second product's B fragment by movmatrix.
+//
+// The softmax keeps a running maximum and sum per row. The maximum is raised only when a score exceeds it by
+// more than 2^8 (weights then stay below 2^8, far inside fp16), so that most steps need no exchange between lanes
+// and no rescaling of the sums. Sums, maxima and outputs are fp32; the weights are rounded to fp16's 11 bits: a
+// relative 2^-12 on average weights, well below the bf16 rounding of the result.
+//
+// Work. All the (sequence, kv head, tile of rows) segments of a call, each so many units of 32 tokens, are laid
+// end to end and cut into equal ranges, one a CTA, whatever the lengths. The 8 warps of a CTA take its units in
+// turn, each with a ring of cache blocks of its own, filled by bulk copies that the warp issues ahead; they join
+// at the end of a segment. A segment cut between CTAs leaves partial results in the workspace, and the CTA that
+// finishes last joins them in their order: the result does not depend on timing.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "hc_attn.h"
 #include "hc_kv.cuh"
+#include "hc_ptx.cuh"
 
 namespace hc {
 namespace {
@@ -20,146 +42,690 @@ namespace {
 __device__ unsigned int g_hc_attention_error = 0;
 
 constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;                 // how far (log2) a score may exceed the running maximum
+constexpr uint64_t kWaitNs = 1000000000ull;   // 1 s
+constexpr int kUnit = 32;                     // tokens a warp takes at a time: two cache blocks
+constexpr int kMinUnits = kWarps;             // a CTA's smallest share: one unit a warp
+constexpr int kMaxDevices = 64;
 
-__device__ __forceinline__ float2 f16x2_to_float2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+// ring depth (blocks a warp), CTAs per SM
+template <int D, int kNT>
+struct Plan {
+    static constexpr int kCtas = kNT == 1 && D <= 128 ? 2 : 1;
+    static constexpr int kStages = D == 64 ? 8 : D == 256 ? 4 : kCtas == 2 ? 5 : 8;
+    static constexpr int kRing = kWarps * kStages * kv_block_bytes(D);
+    static constexpr int kStateFloats = D / 16 * kNT * 4 * 32;  // a warp's outputs
+    static constexpr int kMl = 2 * 8 * kNT;                     // its maxima and sums
+    static constexpr int kMerge = kWarps / 2 * (kStateFloats + kMl) * 4;
+    static constexpr int kBars = kWarps * kStages * 8;
+    static constexpr int kSmem = kRing + kMerge + kBars;
+};
 
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps) attend_kernel(const AttArgs p) {
-    const int lane = static_cast<int>(threadIdx.x) % 32, warp = static_cast<int>(threadIdx.x) / 32;
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void wait_copy(uint32_t bar, uint32_t parity) {
+    if (mbar_test(bar, parity)) return;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        for (int i = 0; i < 32; ++i)
+            if (mbar_test(bar, parity)) return;
+        if (global_timer_ns() - t0 > kWaitNs) {
+            atomicOr(&g_hc_attention_error, kErrCopy);
+            return;
+        }
+    }
+}
+
+// ---- sequences and their work -----------------------------------------------------------------------
+
+struct Seq {
+    int qs, ql, kvl;  // first row of q, queries, keys
+};
+
+__device__ __forceinline__ Seq load_seq(const AttArgs& p, int b, bool tell) {
+    const int n = static_cast<int>(p.n);
+    const int q0 = p.q_start[b], q1 = p.q_start[b + 1], kv = p.kv_len[b];
+    const int most = p.max_pages << p.s.page_shift;
+    Seq s;
+    s.qs = min(max(q0, 0), n);
+    const int qe = min(max(q1, s.qs), n);
+    s.ql = qe - s.qs;
+    s.kvl = min(max(kv, 0), most);
+    if (tell && (s.qs != q0 || qe != q1 || s.kvl != kv)) atomicOr(&g_hc_attention_error, kErrSeq);
+    return s;
+}
+
+template <int R>
+struct Work {
+    int tiles, units;  // tiles of rows, units of each tile
+    __device__ __forceinline__ Work(const AttArgs& p, const Seq& s, int group) {
+        const long long rows = static_cast<long long>(s.ql) * group;
+        tiles = static_cast<int>((rows + R - 1) / R);
+        units = (s.kvl + kUnit - 1) / kUnit;
+        if (p.window > 0) {
+            // a tile's queries span so many positions at most; its first unit may begin up to 31 tokens early
+            const int span = min(s.ql, (R - 1) / group + 2);
+            const long long most = (static_cast<long long>(p.window) + span - 1 + 2 * (kUnit - 1)) / kUnit;
+            if (most < units) units = static_cast<int>(most);
+        }
+        if (units < 1) units = 1;  // a tile without keys still writes its zeros
+    }
+    __device__ __forceinline__ long long total(int heads) const { return static_cast<long long>(tiles) * heads * units; }
+};
+
+// A CTA's part of one segment.
+struct Segment {
+    int b, h, tile, u0, u1, units;
+    Seq s;
+    // positions: the tile's queries stand at first..last; some row sees [lo, hi), every row sees [all_lo, all_hi)
+    int lo, hi, all_lo, all_hi, base;
+    int first_block, end_block;
+};
+
+template <int D, int kNT>
+__global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_kernel(const AttArgs p) {
+    using P = Plan<D, kNT>;
+    constexpr int R = 8 * kNT;
+    constexpr int kKeySteps = D / 16;  // MMAs over a key's columns; also the 16-column tiles of the output
+    constexpr int kBlock = kv_block_bytes(D);
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long scan[kWarps + 1];
+    __shared__ long long found_at;
+    __shared__ int found_seq;
+    __shared__ int last_flag;
+    const int tid = static_cast<int>(threadIdx.x), warp = tid / 32, lane = tid % 32;
     const int r = lane / 4, c = lane % 4;
-    const long long item = static_cast<long long>(blockIdx.x) * kWarps + warp;
-    if (item >= p.n * p.q_heads) return;
-    const long long row = item / p.q_heads;
-    const int head = static_cast<int>(item % p.q_heads);
-    const int h = head / (p.q_heads / p.s.heads);
-    // the row's sequence: the last one that starts at or before it
-    int b = -1;
-    for (int i = 0; i < p.seqs; ++i)
-        if (p.q_start[i] <= row && row < p.q_start[i + 1]) b = i;
-    if (b < 0) return;
-    const long long qs = p.q_start[b], qe = p.q_start[b + 1];
-    if ((qs < 0 || qe > p.n) && lane == 0) atomicOr(&g_hc_attention_error, kErrSeq);
-    const long long most = static_cast<long long>(p.max_pages) << p.s.page_shift;
-    long long kvl = p.kv_len[b];
-    if (kvl < 0 || kvl > most) {
-        if (lane == 0) atomicOr(&g_hc_attention_error, kErrSeq);
-        kvl = kvl < 0 ? 0 : most;
-    }
-    const long long pos = kvl - qe + row;
-    const long long hi = p.causal ? (pos + 1 < kvl ? pos + 1 : kvl) : kvl;
-    const long long lo = p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
-    const float f = p.scale * kLog2e * p.s.k_unit;
+    const int heads = p.s.heads, group = p.q_heads / heads;
+    const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * P::kStages * kBlock);
+    float* merge = reinterpret_cast<float*>(smem + P::kRing);
+    const uint32_t bars = smem_u32(smem + P::kRing + P::kMerge) + static_cast<uint32_t>(warp * P::kStages * 8);
+    if (lane < P::kStages) mbar_init(bars + 8u * static_cast<uint32_t>(lane), 1);
+    fence_mbar_init();
 
-    float q[D / 4];
-    const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) + row * p.q_stride + static_cast<long long>(head) * D + c * (D / 4);
+    // ---- this CTA's range of the call's units ----------------------------------------------------------
+    long long mine = 0;
+    for (int b = tid; b < p.seqs; b += kThreads) mine += Work<R>(p, load_seq(p, b, blockIdx.x == 0), group).total(heads);
+    long long total = mine;
 #pragma unroll
-    for (int e = 0; e < D / 4; ++e) q[e] = __bfloat162float(qrow[e]) * f;
-    float m = -INFINITY, l = 0.f, acc[D / 8];
+    for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+    if (lane == 0) scan[warp] = total;
+    __syncthreads();
+    total = 0;
 #pragma unroll
-    for (int e = 0; e < D / 8; ++e) acc[e] = 0.f;
-
-    for (long long t0 = lo / 16 * 16; t0 < hi; t0 += 16) {
-        const int page = p.page_table[static_cast<long long>(b) * p.max_pages + (t0 >> p.s.page_shift)];
-        if (page < 0 || page >= p.s.pages) {
-            if (lane == 0) atomicOr(&g_hc_attention_error, kErrPage);
-            continue;
+    for (int w = 0; w < kWarps; ++w) total += scan[w];
+    const long long want = (total + kMinUnits - 1) / kMinUnits;
+    const long long ctas = want < gridDim.x ? want : static_cast<long long>(gridDim.x);
+    if (static_cast<long long>(blockIdx.x) >= ctas) return;
+    long long at = total * blockIdx.x / ctas;
+    const long long end = total * (blockIdx.x + 1) / ctas;
+    {
+        // the sequence that holds unit `at`: an inclusive scan over 256 sequences at a time
+        long long before = 0;
+        for (int b0 = 0; b0 < p.seqs; b0 += kThreads) {
+            const int b = b0 + tid;
+            const long long v = b < p.seqs ? Work<R>(p, load_seq(p, b, false), group).total(heads) : 0;
+            long long x = v;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                if (lane >= o) x += y;
+            }
+            __syncthreads();
+            if (lane == 31) scan[warp] = x;
+            __syncthreads();
+            long long chunk = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) x += scan[w];
+                chunk += scan[w];
+            }
+            x += before;
+            if (x > at && x - v <= at) {
+                found_seq = b;
+                found_at = at - (x - v);
+            }
+            before += chunk;
+            if (before > at) break;  // the same in every thread
         }
-        const long long in_page = t0 & ((1LL << p.s.page_shift) - 1);
-        const unsigned char* block = p.cache + (((static_cast<long long>(page) * p.s.heads + h) << (p.s.page_shift - 4)) + in_page / 16) * kv_block_bytes(D);
-        float z[2] = {0.f, 0.f};  // tokens r and r + 8
+        __syncthreads();
+    }
+
+    Segment g = {};
+    // the tile's bounds, from g.s, g.tile, g.u0 and g.u1
+    auto place = [&]() {
+        const int rows = g.s.ql * group;
+        const int row0 = g.tile * R, row1 = min(row0 + R, rows) - 1;
+        const int pos0 = g.s.kvl - g.s.ql;
+        const int first = pos0 + row0 / group, last = pos0 + row1 / group;
+        if (p.causal) {
+            g.hi = min(max(last + 1, 0), g.s.kvl);
+            g.all_hi = first + 1;
+            g.lo = p.window > 0 ? max(0, first + 1 - p.window) : 0;
+            g.all_lo = p.window > 0 ? max(0, last + 1 - p.window) : 0;
+        } else {
+            g.hi = g.all_hi = g.s.kvl;
+            g.lo = g.all_lo = 0;
+        }
+        g.base = g.lo / kUnit * kUnit;
+        g.first_block = g.base / 16 + 2 * g.u0;
+        g.end_block = min(g.base / 16 + 2 * g.u1, (g.hi + 15) / 16);
+    };
+    {
+        g.b = found_seq;
+        const long long in = found_at;
+        g.s = load_seq(p, g.b, false);
+        const Work<R> w(p, g.s, group);
+        g.units = w.units;
+        const long long k = in / w.units;
+        g.u0 = static_cast<int>(in - k * w.units);
+        g.h = static_cast<int>(k / w.tiles);
+        g.tile = static_cast<int>(k - static_cast<long long>(g.h) * w.tiles);
+        g.u1 = static_cast<int>(min(static_cast<long long>(w.units), g.u0 + (end - at)));
+        place();
+    }
+
+    // ---- the warp's stream of blocks ---------------------------------------------------------------------
+    // Step k of a segment takes unit warp + 8 k of the CTA's part: blocks i = 2k, 2k + 1 of the warp. Lane j looks up
+    // block 32 w + j of window w (its page and address) and issues its copy when its turn comes.
+    uint32_t uses = 0;       // blocks waited for since the kernel began; block i of a segment is use `uses` + i
+    const unsigned char* where = nullptr;
+    uint32_t there[2] = {};  // which blocks of the current (0) and the previous (1) window were copied
+    int window = 0;
+    auto steps_of = [&]() {
+        const int units_here = (g.end_block - g.first_block + 1) / 2;
+        return units_here > warp ? (units_here - warp + kWarps - 1) / kWarps : 0;
+    };
+    auto look_up = [&](int w) {
+        const int i = 32 * w + lane;
+        const int blk = g.first_block + 2 * (warp + kWarps * (i / 2)) + i % 2;
+        where = nullptr;
+        if (blk < g.end_block && blk * 16 + 16 > g.lo) {
+            const int tok = blk * 16;
+            const int page = p.page_table[static_cast<long long>(g.b) * p.max_pages + (tok >> p.s.page_shift)];
+            if (page >= 0 && page < p.s.pages)
+                where = p.cache + (((static_cast<long long>(page) * heads + g.h) << (p.s.page_shift - 4)) +
+                                   ((tok & ((1 << p.s.page_shift) - 1)) >> 4)) * kBlock;
+            else
+                atomicOr(&g_hc_attention_error, kErrPage);
+        }
+        there[1] = there[0];
+        there[0] = __ballot_sync(0xFFFFFFFFu, where != nullptr);
+        window = w;
+    };
+    auto issue = [&](int i) {  // block i of this segment
+        if (i / 32 != window) look_up(i / 32);
+        if (lane == i % 32) {
+            const uint32_t st = (uses + static_cast<uint32_t>(i)) % P::kStages;
+            if (where) {
+                mbar_arrive_expect_tx(bars + 8 * st, kBlock);
+                bulk_copy(ring + st * kBlock, where, kBlock, bars + 8 * st);
+            } else {
+                mbar_arrive(bars + 8 * st);
+            }
+        }
+    };
+    int issued = 0, blocks = 0;
+    auto open = [&]() {  // start the copies of a new segment
+        blocks = 2 * steps_of();
+        there[0] = there[1] = 0;
+        look_up(0);
+        issued = 0;
+        for (; issued < blocks && issued < P::kStages; ++issued) issue(issued);
+    };
+    __syncthreads();  // barriers ready
+    open();
+
+    while (true) {
+        // ---- the tile's queries ----------------------------------------------------------------------------
+        const int rows = g.s.ql * group, row0 = g.tile * R;
+        const int pos0 = g.s.kvl - g.s.ql;
+        uint32_t qf[kNT][kKeySteps][2];
+        float f[kNT][2];   // score factor (log2 units) of rows 2c, 2c + 1
+        int see[kNT][2];   // keys below this position are seen (causal)
 #pragma unroll
-        for (int quad = 0; quad < D / 64; ++quad) {
-            const uint4 v = *reinterpret_cast<const uint4*>(block + quad * 512 + lane * 16);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            const unsigned char* sc = block + KvPlace<D>::kKeyScales + lane * (D / 32);
-            const float s0 = f16x2_to_float2(e4m3x2_to_f16(sc[quad])).x, s1 = f16x2_to_float2(e4m3x2_to_f16(sc[D / 64 + quad])).x;
+        for (int t = 0; t < kNT; ++t) {
+            const int row = row0 + 8 * t + r;
+            const bool real = row < rows;
+            uint4 x[D / 32];
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+                                       static_cast<long long>(g.s.qs + (real ? row / group : 0)) * p.q_stride +
+                                       static_cast<long long>(g.h * group + (real ? row % group : 0)) * D + c * (D / 4);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                uint32_t x[4];
-                e2m1_word_to_f16(w[s], x[0], x[1], x[2], x[3]);
+            for (int e = 0; e < D / 32; ++e) x[e] = real ? __ldg(reinterpret_cast<const uint4*>(src) + e) : make_uint4(0, 0, 0, 0);
+            uint32_t m = 0;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float2 a = f16x2_to_float2(x[e]), d = f16x2_to_float2(x[2 + e]);
-                    const int i = quad * 16 + s * 4 + e * 2;
-                    z[0] = fmaf(q[i], a.x * s0, fmaf(q[i + 1], a.y * s0, z[0]));
-                    z[1] = fmaf(q[i], d.x * s1, fmaf(q[i + 1], d.y * s1, z[1]));
+            for (int e = 0; e < D / 32; ++e) {
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[e].x & 0x7FFF7FFFu, x[e].y & 0x7FFF7FFFu),
+                                         __vmaxu2(x[e].z & 0x7FFF7FFFu, x[e].w & 0x7FFF7FFFu)));
+            }
+            m = max(m & 0xFFFFu, m >> 16);
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            // scale the row by the power of two that brings its largest value to [2^7, 2^8): bf16's 8 bits are exact in
+            // fp16 down to 2^-14, and sums stay far below fp32's range. NaN and infinity stay what they are.
+            const uint32_t ex = m >= 0x7F80u ? 134u : max(m >> 7, 27u);
+            const float up = __uint_as_float((261u - ex) << 23), down = __uint_as_float((ex - 7u) << 23);
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) {
+                const uint32_t w[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    qf[t][2 * e + k / 2][k % 2] = pack_f16(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
+            }
+            const float fr = p.scale * kLog2e * p.s.k_unit * down;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                f[t][j] = __shfl_sync(0xFFFFFFFFu, fr, 4 * (2 * c + j));
+                const int col = row0 + 8 * t + 2 * c + j;
+                see[t][j] = p.causal ? (col < rows ? pos0 + col / group + 1 : 0x7FFFFFFF) : g.s.kvl;
+            }
+        }
+        float m[kNT][2], l[kNT][2], o[kKeySteps][kNT][4];
+#pragma unroll
+        for (int t = 0; t < kNT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                m[t][j] = -INFINITY;
+                l[t][j] = 0.f;
+            }
+#pragma unroll
+        for (int k = 0; k < kKeySteps; ++k)
+#pragma unroll
+            for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[k][t][e] = 0.f;
+
+        for (int i = 0; i < blocks; i += 2) {
+            float z[2][kNT][4];
+            const int blk0 = g.first_block + 2 * (warp + kWarps * (i / 2));
+            uint32_t slot[2];
+            bool have[2];
+            // ---- scores of two blocks --------------------------------------------------------------------------
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const uint32_t use = uses + static_cast<uint32_t>(i + n);
+                const uint32_t st = use % P::kStages;
+                have[n] = (there[(i + n) / 32 == window ? 0 : 1] >> ((i + n) % 32)) & 1;
+                wait_copy(bars + 8 * st, use / P::kStages & 1);
+                slot[n] = ring + st * kBlock;
+#pragma unroll
+                for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[n][t][e] = 0.f;
+                const uint32_t ks = slot[n] + KvPlace<D>::kKeyScales + static_cast<uint32_t>(lane * (D / 32));
+                uint32_t sw[2];
+                if constexpr (D == 64) {
+                    sw[0] = lds32(ks & ~3u) >> (8 * (ks & 2u)) & 0xFFFFu;
+                    sw[1] = 0;
+                } else {
+                    sw[0] = lds32(ks);
+                    sw[1] = D == 256 ? lds32(ks + 4) : 0;
+                }
+#pragma unroll
+                for (int quad = 0; quad < D / 64; ++quad) {
+                    const uint4 v = ld_smem_v4(slot[n] + static_cast<uint32_t>(quad * 512 + lane * 16));
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    // scale bytes: tokens r, then r + 8, D / 64 each
+                    const int i0 = quad, i1 = D / 64 + quad;
+                    const uint32_t h0 = e4m3x2_to_f16(sw[i0 / 4] >> (16 * (i0 % 4 / 2)) & 0xFFFFu);
+                    const uint32_t h1 = e4m3x2_to_f16(sw[i1 / 4] >> (16 * (i1 % 4 / 2)) & 0xFFFFu);
+                    const uint32_t s0 = __byte_perm(h0, 0, i0 % 2 ? 0x3232 : 0x1010), s1 = __byte_perm(h1, 0, i1 % 2 ? 0x3232 : 0x1010);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        uint32_t x0, x1, x2, x3;
+                        e2m1_word_to_f16(w[s], x0, x1, x2, x3);
+                        const uint32_t a0 = mul_f16x2(x0, s0), a2 = mul_f16x2(x1, s0), a1 = mul_f16x2(x2, s1), a3 = mul_f16x2(x3, s1);
+#pragma unroll
+                        for (int t = 0; t < kNT; ++t) mma_f16(z[n][t], a0, a1, a2, a3, qf[t][quad * 4 + s][0], qf[t][quad * 4 + s][1]);
+                    }
                 }
             }
-        }
+            // ---- masks, running maximum, weights ------------------------------------------------------------
+            const bool whole = have[0] && have[1] && blk0 * 16 >= g.all_lo && blk0 * 16 + kUnit <= g.all_hi;
+            bool raise = false;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            z[j] += __shfl_xor_sync(0xFFFFFFFFu, z[j], 1);
-            z[j] += __shfl_xor_sync(0xFFFFFFFFu, z[j], 2);
-            const long long t = t0 + r + 8 * j;
-            if (t < lo || t >= hi) z[j] = -INFINITY;
-        }
-        float top = fmaxf(z[0], z[1]);
+            for (int t = 0; t < kNT; ++t)
 #pragma unroll
-        for (int o = 4; o < 32; o *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const float m2 = fmaxf(m, top);
-        const float base = m2 == -INFINITY ? 0.f : m2;
-        const float w0 = exp2f(z[0] - base), w1 = exp2f(z[1] - base), fade = exp2f(m - base);
-        m = m2;
-        l = l * fade + (c == 0 ? w0 + w1 : 0.f);
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e) acc[e] *= fade;
-        float wt[4];  // weights of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+                    for (int e = 0; e < 4; ++e) {
+                        float v = z[n][t][e] * f[t][e % 2];
+                        if (!whole) {
+                            const int pos = (blk0 + n) * 16 + r + 8 * (e / 2);
+                            const int up_to = min(see[t][e % 2], g.s.kvl);
+                            if (!have[n] || pos >= up_to || (p.window > 0 && pos < see[t][e % 2] - p.window)) v = -INFINITY;
+                        }
+                        z[n][t][e] = v;
+                        raise |= v > m[t][e % 2] + kSlack;
+                    }
+            if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) wt[j] = __shfl_sync(0xFFFFFFFFu, j < 2 ? w0 : w1, 4 * (2 * c + j % 2));
+                for (int t = 0; t < kNT; ++t)
 #pragma unroll
-        for (int quad = 0; quad < D / 64; ++quad) {
-            const uint4 v = *reinterpret_cast<const uint4*>(block + KvPlace<D>::kValueCodes + quad * 512 + lane * 16);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            const uint32_t s4 = *reinterpret_cast<const uint32_t*>(block + KvPlace<D>::kValueScales + ((r * (D / 8) + quad * 8) / 16 * 4 + c) * 4);
-            float s[4];
+                    for (int j = 0; j < 2; ++j) {
+                        float top = fmaxf(fmaxf(z[0][t][j], z[0][t][2 + j]), fmaxf(z[1][t][j], z[1][t][2 + j]));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s[j] = f16x2_to_float2(e4m3x2_to_f16(s4 >> (8 * j) & 0xFFu)).x * wt[j];
-                const long long t = t0 + 2 * c + j % 2 + 8 * (j / 2);
-                if (t < lo || t >= hi) s[j] = 0.f;  // not seen: whatever the cache holds there
+                        for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+                        const float m2 = fmaxf(m[t][j], top);
+                        const float fade = m2 == -INFINITY ? 1.f : ex2(m[t][j] - m2);
+                        m[t][j] = m2;
+                        l[t][j] *= fade;
+#pragma unroll
+                        for (int k = 0; k < kKeySteps; ++k) {
+                            o[k][t][j] *= fade;
+                            o[k][t][2 + j] *= fade;
+                        }
+                    }
             }
+            uint32_t pb[2][kNT][2];
 #pragma unroll
-            for (int mm = 0; mm < 4; ++mm) {
-                uint32_t x[4];
-                e2m1_word_to_f16(w[mm], x[0], x[1], x[2], x[3]);
+            for (int t = 0; t < kNT; ++t) {
+                const float b0 = m[t][0] == -INFINITY ? 0.f : m[t][0], b1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 a = f16x2_to_float2(x[j]);
-                    acc[quad * 8 + 2 * mm] = fmaf(s[j], a.x, acc[quad * 8 + 2 * mm]);
-                    acc[quad * 8 + 2 * mm + 1] = fmaf(s[j], a.y, acc[quad * 8 + 2 * mm + 1]);
+                for (int n = 0; n < 2; ++n) {
+                    const float w0 = ex2(z[n][t][0] - b0), w1 = ex2(z[n][t][1] - b1);
+                    const float w2 = ex2(z[n][t][2] - b0), w3 = ex2(z[n][t][3] - b1);
+                    l[t][0] += w0 + w2;
+                    l[t][1] += w1 + w3;
+                    pb[n][t][0] = transpose_8x8(pack_f16(w0, w1));
+                    pb[n][t][1] = transpose_8x8(pack_f16(w2, w3));
                 }
             }
+            // ---- weighted values --------------------------------------------------------------------------------
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                uint32_t nan16[(D + 127) / 128] = {};  // per 16-column group of this lane: tokens of the block whose scale is NaN
+#pragma unroll
+                for (int quad = 0; quad < D / 64; ++quad) {
+                    uint32_t s4 = lds32(slot[n] + KvPlace<D>::kValueScales + static_cast<uint32_t>(((r * (D / 8) + quad * 8) / 16 * 4 + c) * 4));
+                    if (!whole) {
+                        // a token that some row does not see must not reach that row through 0 * NaN: its NaN scale becomes 0
+                        // here and is put into the rows that do see it below
+                        uint32_t bad = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if ((s4 >> (8 * j) & 0x7Fu) == 0x7Fu) {
+                                bad |= 1u << (2 * c + j % 2 + 8 * (j / 2));
+                                s4 &= ~(0xFFu << (8 * j));
+                            }
+                        bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 1);
+                        bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 2);
+                        nan16[quad * 64 / 128] |= have[n] ? bad : 0u;
+                    }
+                    const uint32_t sp0 = e4m3x2_to_f16(s4 & 0xFFFFu), sp1 = e4m3x2_to_f16(s4 >> 16);
+                    const uint4 v = ld_smem_v4(slot[n] + KvPlace<D>::kValueCodes + static_cast<uint32_t>(quad * 512 + lane * 16));
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int mm = 0; mm < 4; ++mm) {
+                        uint32_t x0, x1, x2, x3;
+                        e2m1_word_to_f16(w[mm], x0, x1, x2, x3);
+                        const uint32_t a0 = mul_f16x2(__byte_perm(x0, x1, 0x5410), sp0), a1 = mul_f16x2(__byte_perm(x0, x1, 0x7632), sp0);
+                        const uint32_t a2 = mul_f16x2(__byte_perm(x2, x3, 0x5410), sp1), a3 = mul_f16x2(__byte_perm(x2, x3, 0x7632), sp1);
+#pragma unroll
+                        for (int t = 0; t < kNT; ++t) mma_f16(o[quad * 4 + mm][t], a0, a1, a2, a3, pb[n][t][0], pb[n][t][1]);
+                    }
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int x = 0; x < (D + 127) / 128; ++x) {
+                        if (nan16[x] == 0) continue;
+#pragma unroll
+                        for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int lo = p.window > 0 ? see[t][j] - p.window : 0, hi = min(see[t][j], g.s.kvl);
+                                const int b0 = (blk0 + n) * 16;
+                                const int from = min(max(lo - b0, 0), 16), to = min(max(hi - b0, 0), 16);
+                                const uint32_t vis = to > from ? ((1u << to) - 1u) & ~((1u << from) - 1u) : 0u;
+                                if (nan16[x] & vis) {
+#pragma unroll
+                                    for (int k = 0; k < 8 && k + 8 * x < kKeySteps; ++k)
+                                        o[k + 8 * x][t][j] = o[k + 8 * x][t][2 + j] = __uint_as_float(0x7FC00000u);
+                                }
+                            }
+                    }
+                }
+                __syncwarp();
+                if (issued < blocks) issue(issued++);
+            }
+        }
+        uses += static_cast<uint32_t>(blocks);
+
+        // ---- the next part's copies start before this one is joined ---------------------------------------
+        const Segment done = g;
+        at += g.u1 - g.u0;
+        const bool more = at < end;
+        if (more) {
+            g.u0 = 0;
+            const Work<R> w(p, g.s, group);
+            if (++g.tile == w.tiles) {
+                g.tile = 0;
+                ++g.h;
+            }
+            if (g.h == heads) {
+                g.h = 0;
+                while (true) {  // `at` < `end` <= total: a sequence with work follows
+                    g.s = load_seq(p, ++g.b, false);
+                    if (g.s.ql > 0) break;
+                }
+            }
+            g.units = Work<R>(p, g.s, group).units;
+            g.u1 = static_cast<int>(min(static_cast<long long>(g.units), end - at));
+            place();
+            open();
+        }
+
+        // ---- join the warps: 4 + 4, 2 + 2, 1 + 1 ---------------------------------------------------------
+#pragma unroll
+        for (int t = 0; t < kNT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int x = 4; x < 32; x *= 2) l[t][j] += __shfl_xor_sync(0xFFFFFFFFu, l[t][j], x);
+        // another partial result: rows' maxima and sums, outputs; `get` loads one float
+        auto absorb = [&](const float* ml, const float* st, auto get) {
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) {
+                float mine_[2], theirs[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int col = 8 * t + 2 * c + j;
+                    const float m1 = get(ml + col), l1 = get(ml + 8 * kNT + col);
+                    const float m2 = fmaxf(m[t][j], m1);
+                    mine_[j] = m2 == -INFINITY ? 1.f : ex2(m[t][j] - m2);
+                    theirs[j] = m2 == -INFINITY ? 1.f : ex2(m1 - m2);
+                    m[t][j] = m2;
+                    l[t][j] = l[t][j] * mine_[j] + l1 * theirs[j];
+                }
+#pragma unroll
+                for (int k = 0; k < kKeySteps; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[k][t][e] = o[k][t][e] * mine_[e % 2] + get(st + ((k * kNT + t) * 4 + e) * 32 + lane) * theirs[e % 2];
+            }
+        };
+        auto leave = [&](float* ml, float* st) {
+            if (r == 0) {
+#pragma unroll
+                for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        ml[8 * t + 2 * c + j] = m[t][j];
+                        ml[8 * kNT + 8 * t + 2 * c + j] = l[t][j];
+                    }
+            }
+#pragma unroll
+            for (int k = 0; k < kKeySteps; ++k)
+#pragma unroll
+                for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) st[((k * kNT + t) * 4 + e) * 32 + lane] = o[k][t][e];
+        };
+        auto join_warps = [&]() {
+            for (int half = kWarps / 2; half >= 1; half /= 2) {
+                float* at_ = merge + (warp % half) * (P::kStateFloats + P::kMl);
+                if (warp >= half && warp < 2 * half) leave(at_, at_ + P::kMl);
+                __syncthreads();
+                if (warp < half) absorb(at_, at_ + P::kMl, [](const float* x) { return *x; });
+                __syncthreads();
+            }
+        };
+        auto write_out = [&]() {  // warp 0 has it all
+            if (warp != 0) return;
+            const int drows = done.s.ql * group, drow0 = done.tile * R;
+#pragma unroll
+            for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int row = drow0 + 8 * t + 2 * c + j;
+                    if (row >= drows) continue;
+                    const float lv = l[t][j];
+                    const float s = lv == 0.f ? 0.f : p.s.v_unit / lv;
+                    const long long token = done.s.qs + row / group;
+                    const int head = done.h * group + row % group;
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D + r * (D / 8);
+#pragma unroll
+                    for (int k = 0; k < kKeySteps; k += 4) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(o[k + e][t][j] * s, o[k + e][t][2 + j] * s);
+                            w[e] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                        *reinterpret_cast<uint4*>(dst + 2 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (p.lse && r == 0) p.lse[token * p.q_heads + head] = lv == 0.f ? -INFINITY : (m[t][j] + log2f(lv)) * kLn2;
+                }
+        };
+        join_warps();
+        if (done.u0 == 0 && done.u1 == done.units) {
+            write_out();
+        } else {
+            // a part of a segment: units [done.u0, done.u1) of it; the segment's first unit is `at` - done.u1 of the call
+            const long long seg0 = at - done.u1, seg1 = seg0 + done.units - 1;
+            auto cta_of = [&](long long x) { return static_cast<int>(((x + 1) * ctas - 1) / total); };
+            const int c0 = cta_of(seg0), c1 = cta_of(seg1);
+            unsigned int* counters = static_cast<unsigned int*>(p.workspace);
+            float* parts = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kAttCounterBytes);
+            // a CTA's second slot for the segment that begins in it, the first for one that began before
+            auto part_of = [&](int cta) { return parts + static_cast<long long>(2 * cta + (cta == c0 ? 1 : 0)) * kAttPartFloats; };
+            if (warp == 0) {
+                float* mine_ = part_of(static_cast<int>(blockIdx.x));
+                leave(mine_, mine_ + P::kMl);
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) {
+                    const unsigned int before = atomicAdd(&counters[c0], 1u);
+                    const bool last = before + 1 == static_cast<unsigned int>(c1 - c0 + 1);
+                    if (last) counters[c0] = 0;
+                    last_flag = last ? 1 : 0;
+                    __threadfence();
+                }
+            }
+            __syncthreads();
+            if (last_flag) {
+                // warp w takes parts w, w + 8, ... in their order, then the warps join as before
+#pragma unroll
+                for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        m[t][j] = -INFINITY;
+                        l[t][j] = 0.f;
+                    }
+#pragma unroll
+                for (int k = 0; k < kKeySteps; ++k)
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[k][t][e] = 0.f;
+                __threadfence();
+                for (int x = c0 + warp; x <= c1; x += kWarps) {
+                    const float* st = part_of(x);
+                    absorb(st, st + P::kMl, [](const float* x) { return __ldcg(x); });  // other SMs' writes: from L2
+                }
+                join_warps();
+                write_out();
+            }
+        }
+        if (!more) break;
+        __syncthreads();  // last_flag and the merge buffers are free again
+    }
+}
+
+template <int D, int kNT>
+int launch_rows(const AttArgs& a, cudaStream_t stream) {
+    using P = Plan<D, kNT>;
+    static_assert(8 * kNT * (D + 2) <= kAttPartFloats, "a partial result fits its place in the workspace");
+    static std::mutex mu;
+    static int ctas[kMaxDevices] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -7;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (ctas[dev] == 0) {
+            int sms = 0, per_sm = 0;
+            if (cudaFuncSetAttribute(attend_rows_kernel<D, kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem) != cudaSuccess ||
+                cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attend_rows_kernel<D, kNT>, kThreads, P::kSmem) != cudaSuccess ||
+                sms < 1 || per_sm < 1)
+                return -7;
+            ctas[dev] = sms * per_sm < kAttMaxCtas ? sms * per_sm : kAttMaxCtas;
         }
     }
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-    const float g = l == 0.f ? 0.f : p.s.v_unit / l;
-#pragma unroll
-    for (int e = 0; e < D / 8; ++e) {
-        acc[e] += __shfl_xor_sync(0xFFFFFFFFu, acc[e], 1);
-        acc[e] += __shfl_xor_sync(0xFFFFFFFFu, acc[e], 2);
-    }
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + row * p.out_stride + static_cast<long long>(head) * D + r * (D / 8);
-    if (c == 0) {
-#pragma unroll
-        for (int e = 0; e < D / 8; ++e) o[e] = __float2bfloat16_rn(acc[e] * g);
-    }
-    if (p.lse && lane == 0) p.lse[item] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    attend_rows_kernel<D, kNT><<<static_cast<unsigned>(ctas[dev]), kThreads, P::kSmem, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? 0 : -7;
 }
 
 }  // namespace
 
 int launch_attention(const AttArgs& a, cudaStream_t stream) {
-    const long long items = a.n * a.q_heads;
-    const unsigned grid = static_cast<unsigned>((items + kWarps - 1) / kWarps);
+    const long long rows = static_cast<long long>(a.max_q_len) * (a.q_heads / a.s.heads);
     switch (a.s.dim) {
-        case 64: attend_kernel<64><<<grid, 32 * kWarps, 0, stream>>>(a); break;
-        case 128: attend_kernel<128><<<grid, 32 * kWarps, 0, stream>>>(a); break;
-        default: attend_kernel<256><<<grid, 32 * kWarps, 0, stream>>>(a); break;
+        case 64:
+            if (rows <= 8) return launch_rows<64, 1>(a, stream);
+            if (rows <= 16) return launch_rows<64, 2>(a, stream);
+            return launch_rows<64, 4>(a, stream);
+        case 128:
+            if (rows <= 8) return launch_rows<128, 1>(a, stream);
+            if (rows <= 16) return launch_rows<128, 2>(a, stream);
+            if (rows <= 24) return launch_rows<128, 3>(a, stream);
+            return launch_rows<128, 4>(a, stream);
+        default:
+            if (rows <= 8) return launch_rows<256, 1>(a, stream);
+            return launch_rows<256, 2>(a, stream);
     }
-    return cudaGetLastError() == cudaSuccess ? 0 : -7;
 }
 
 int read_attention_error(unsigned int* word, int clear, cudaStream_t stream) {

@@ -240,6 +240,7 @@ int hc_kv_attention(const void* q, int64_t q_stride, const int* q_start, const i
     if (a.n < 0 || a.n > kMaxRows || a.seqs < 0 || a.max_q_len < 0 || a.max_pages < 1) return HC_ERR_SHAPE;
     if (static_cast<int64_t>(a.max_pages) * s.page_size > kMaxRows) return HC_ERR_SHAPE;  // positions are 32-bit
     if (a.q_heads < 1 || a.q_heads % s.heads != 0 || a.q_heads / s.heads > 128) return HC_ERR_SHAPE;
+    if (a.n * (a.q_heads / s.heads) > kMaxRows) return HC_ERR_SHAPE;  // rows are counted in 32 bits
     const int64_t w = static_cast<int64_t>(a.q_heads) * s.dim;
     if (!good_stride(q_stride, w) || !good_stride(out_stride, w)) return HC_ERR_SHAPE;
     if (!std::isfinite(a.scale) || a.scale < 0.f || a.window < 0 || (a.window > 0 && !a.causal)) return HC_ERR_ARG;

@@ -457,7 +457,7 @@ int hc_kv_read(const void* cache, const int64_t* slots, int64_t n, hc_kv_shape_t
 
 /* A call of hc_kv_attention. */
 typedef struct {
-    int64_t n;      /* rows of q and out: the queries of all sequences, at most 2^31 - 1 */
+    int64_t n;      /* rows of q and out: the queries of all sequences; n * q_heads / heads at most 2^31 - 1 */
     int seqs;       /* sequences, >= 0 */
     int max_q_len;  /* queries of the longest sequence: sizes the tiles (longer ones are right, but slower) */
     int max_pages;  /* columns of the page table */
