@@ -143,10 +143,18 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_torch = None
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        global _torch
+        if _torch is None:
+            import torch
+            _torch = torch
+        if _torch.cuda.is_initialized():  # the raw handle: a Stream object costs more than the rest of a call
+            return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+        return _torch.cuda.current_stream().cuda_stream if _torch.cuda.is_available() else None
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -17,6 +17,9 @@ enum : unsigned int {
     kErrTile = 1u << 23,   // a bounded wait between the warps of a tile ran out
 };
 
+// SMs of the current device, found once per device; 0 if that failed
+int attn_sm_count();
+
 // ---- norms and rotation (hc_rope.cu) -------------------------------------------------------------
 constexpr int kRopeMaxFreqs = 128;
 struct RopeEntry {

@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -70,6 +71,19 @@ int check_kv_shape(const hc_kv_shape_t& s, KvShape* out) {
 int status(int internal) { return internal == 0 ? HC_OK : HC_ERR_CUDA; }
 
 }  // namespace
+
+int attn_sm_count() {
+    static std::atomic<int> count[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = count[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 0;
+        count[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 }  // namespace hc
 
 using namespace hc;

@@ -8,12 +8,11 @@
 // a quotient by its remainder), which is exact whenever the quotient has few bits: ties are seen as ties.
 //
 // The layout is the one that the attention's matrix instructions read, so the bytes of one token are
-// scattered in 1- and 2-byte pieces over its block of 16 tokens. A block takes 16 tokens of the call and
-// looks for a run among their slots: 16 consecutive tokens on the 16 slots of one cache block. A run
-// (prefill) goes block-wise: one warp takes the block of one head, each lane the same tokens and columns
-// that it has in the layout, so that it holds whole 16-column groups and whole words, and every store is
-// 16 bytes wide. Other tokens (decode, ragged ends) go token-wise: one warp per token and head, 8 columns
-// a lane. Both give the same bytes.
+// scattered in 1- and 2-byte pieces over its block of 16 tokens. A warp takes 16 tokens of the call and one
+// head and looks for a run among their slots: 16 consecutive tokens on the 16 slots of one cache block. A run
+// (prefill) goes block-wise: each lane takes the tokens and columns that it has in the layout, so that it
+// holds whole 16-column groups and whole words, and every store is 16 bytes wide. Other tokens (decode,
+// ragged ends) go token-wise, 8 columns a lane. Both give the same bytes.
 //
 // Bound: HBM; (4 + 1.125) bytes a value pair each way.
 
@@ -330,60 +329,66 @@ __device__ __forceinline__ void read_block(const KvArgs& p, long long i, int h, 
     }
 }
 
-// gridDim.x: groups of 16 tokens; gridDim.y: parts of a group's work
+// One warp takes 16 tokens of the call and one head; gridDim.y parts share a group's tokens when there are few
+// groups. Warps are independent: each reads the slots of its group and of the 15 tokens on either side, lane j
+// those at j and j + 32 of this window (token i0 - 15 + j).
 template <int D, bool kRead>
 __global__ void __launch_bounds__(kThreads) kv_move_kernel(const KvArgs p) {
-    __shared__ long long slot[kWindow];
-    __shared__ unsigned char run[kWindow];  // 1: 16 consecutive tokens on one cache block begin here
-    const int tid = static_cast<int>(threadIdx.x);
-    const int warp = tid / 32, lane = tid % 32;
-    const long long i0 = static_cast<long long>(blockIdx.x) * kGroup;
+    const int lane = static_cast<int>(threadIdx.x) % 32;
+    const int heads = p.s.heads;
+    const long long item = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
+    const long long group = item / heads;
+    const int h = static_cast<int>(item - group * heads);
+    const long long i0 = group * kGroup;
+    if (i0 >= p.n) return;
     const long long cap = static_cast<long long>(p.s.pages) << p.s.page_shift;
-    if (tid < kWindow) {
-        const long long i = i0 - (kGroup - 1) + tid;
-        long long s = -1;
-        if (i >= 0 && i < p.n) {
-            s = p.slots[i];
-            if (s >= cap) {
-                if (blockIdx.y == 0 && i >= i0 && i < i0 + kGroup) atomicOr(&g_hc_kv_error, kErrPage);
-                s = -1;
+    long long s[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int j = lane + 32 * x;
+        const long long i = i0 - (kGroup - 1) + j;
+        s[x] = -1;
+        if (j < kWindow && i >= 0 && i < p.n) {
+            s[x] = __ldg(p.slots + i);
+            if (s[x] >= cap) {
+                if (h == 0 && blockIdx.y == 0 && j >= kGroup - 1 && j < 2 * kGroup - 1) atomicOr(&g_hc_kv_error, kErrPage);
+                s[x] = -1;
             }
         }
-        slot[tid] = s < 0 ? -1 : s;
     }
-    __syncthreads();
-    if (tid < kWindow) {
-        bool ok = tid + kGroup <= kWindow && slot[tid] >= 0 && slot[tid] % kGroup == 0;
-        for (int t = 1; t < kGroup && ok; ++t) ok = slot[tid + t] == slot[tid] + t;
-        run[tid] = ok ? 1 : 0;
-    }
-    __syncthreads();
-    const int heads = p.s.heads;
-    auto block_of = [&](long long s, int h) {
-        const long long page = s >> p.s.page_shift;
-        const int in_page = static_cast<int>(s & ((1LL << p.s.page_shift) - 1));
+    // bit j: token j + 1 of the window lies on the slot behind token j's
+    const long long after0 = __shfl_down_sync(0xFFFFFFFFu, s[0], 1), first1 = __shfl_sync(0xFFFFFFFFu, s[1], 0);
+    const long long after1 = __shfl_down_sync(0xFFFFFFFFu, s[1], 1);
+    const unsigned long long next =
+        __ballot_sync(0xFFFFFFFFu, s[0] >= 0 && (lane < 31 ? after0 : first1) == s[0] + 1) |
+        static_cast<unsigned long long>(__ballot_sync(0xFFFFFFFFu, lane < 31 && s[1] >= 0 && after1 == s[1] + 1)) << 32;
+    // bit j: a run of 16 tokens on one cache block begins at token j (they begin at 0..30: 15 tokens must follow)
+    const unsigned int run = __ballot_sync(0xFFFFFFFFu, lane < 2 * kGroup - 1 && s[0] >= 0 && s[0] % kGroup == 0 &&
+                                                             (next >> lane & 0x7FFFu) == 0x7FFFu);
+    auto block_of = [&](long long slot) {
+        const long long page = slot >> p.s.page_shift;
+        const int in_page = static_cast<int>(slot & ((1LL << p.s.page_shift) - 1));
         return p.cache + (((page * heads + h) << (p.s.page_shift - 4)) + in_page / kGroup) * kv_block_bytes(D);
     };
-    const int worker = static_cast<int>(blockIdx.y) * kWarps + warp, workers = static_cast<int>(gridDim.y) * kWarps;
-    // the run that begins in this group, if any (two runs are 16 tokens apart at least)
-    for (int j = kGroup - 1; j < 2 * kGroup - 1; ++j) {
-        if (!run[j]) continue;
-        const long long i = i0 + j - (kGroup - 1);
-        for (int h = worker; h < heads; h += workers) {
-            if constexpr (kRead) read_block<D>(p, i, h, block_of(slot[j], h), lane);
-            else write_block<D>(p, i, h, block_of(slot[j], h), lane);
-        }
+    // the run that begins in this group, if any (runs begin 16 tokens apart at least)
+    const unsigned int here = run >> (kGroup - 1);
+    if (here != 0 && blockIdx.y == 0) {
+        const int j = kGroup - 1 + __ffs(here) - 1;
+        const long long slot = __shfl_sync(0xFFFFFFFFu, s[0], j);  // j <= 30
+        if constexpr (kRead) read_block<D>(p, i0 + j - (kGroup - 1), h, block_of(slot), lane);
+        else write_block<D>(p, i0 + j - (kGroup - 1), h, block_of(slot), lane);
     }
     // the tokens of this group that no run has
-    for (int x = worker; x < kGroup * heads; x += workers) {
-        const int j = kGroup - 1 + x % kGroup, h = x / kGroup;
-        const long long i = i0 + x % kGroup, s = slot[j];
-        if (i >= p.n) continue;
-        if (s >= 0 && run[j - static_cast<int>(s % kGroup)]) continue;
+    for (int x = static_cast<int>(blockIdx.y); x < kGroup; x += static_cast<int>(gridDim.y)) {
+        const int j = kGroup - 1 + x;
+        if (i0 + x >= p.n) break;
+        const long long slot = __shfl_sync(0xFFFFFFFFu, s[0], j);
+        const int t = slot < 0 ? 0 : static_cast<int>(slot % kGroup);
+        if (slot >= 0 && (run >> (j - t) & 1u)) continue;
         if constexpr (kRead) {
-            read_token<D>(p, i, h, s < 0 ? nullptr : block_of(s, h), s < 0 ? 0 : static_cast<int>(s % kGroup), lane);
+            read_token<D>(p, i0 + x, h, slot < 0 ? nullptr : block_of(slot), t, lane);
         } else {
-            if (s >= 0) write_token<D>(p, i, h, block_of(s, h), static_cast<int>(s % kGroup), lane);
+            if (slot >= 0) write_token<D>(p, i0 + x, h, block_of(slot), t, lane);
         }
     }
 }
@@ -391,16 +396,15 @@ __global__ void __launch_bounds__(kThreads) kv_move_kernel(const KvArgs p) {
 template <bool kRead>
 int launch_move(const KvArgs& a, cudaStream_t stream) {
     if (a.n <= 0) return 0;
-    int dev = 0, sms = 152;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return -7;
-    const long long groups = (a.n + kGroup - 1) / kGroup;
-    // few groups: spread each over enough blocks to fill the GPU twice, down to one token and head a warp
-    long long parts = (2LL * sms + groups - 1) / groups;
-    const long long most = (static_cast<long long>(kGroup) * a.s.heads + kWarps - 1) / kWarps;
-    if (parts > most) parts = most;
-    if (parts < 1) parts = 1;
-    const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(parts));
+    const int sms = attn_sm_count();
+    if (sms == 0) return -7;
+    const long long items = (a.n + kGroup - 1) / kGroup * a.s.heads;
+    const long long blocks = (items + kWarps - 1) / kWarps;
+    if (blocks > 0x7FFFFFFFLL) return -7;
+    // few groups (decode, short prompts): spread the tokens of each, down to one token and head a warp
+    long long parts = (2LL * sms + blocks - 1) / blocks;
+    if (parts > kGroup) parts = kGroup;
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(parts));
     switch (a.s.dim) {
         case 64: kv_move_kernel<64, kRead><<<grid, kThreads, 0, stream>>>(a); break;
         case 128: kv_move_kernel<128, kRead><<<grid, kThreads, 0, stream>>>(a); break;

@@ -28,7 +28,7 @@ namespace hc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 4;  // rows per lane group whose loads are in flight together
+constexpr int kRows = 3;  // rows per lane group whose loads are in flight together
 
 __global__ void prepare_rope_kernel(const __grid_constant__ RopeTable t, int freqs, RopeEntry* out) {
     const int j = static_cast<int>(threadIdx.x);
@@ -43,7 +43,7 @@ __device__ __forceinline__ uint32_t pk(float a, float b) {
 }
 
 template <int kLanes>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs p) {
+__global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeArgs p) {
     __shared__ float2 cs[kRopeMaxFreqs];
     const int lane = static_cast<int>(threadIdx.x) % kLanes;
     const int group = static_cast<int>(threadIdx.x) / kLanes;
@@ -117,16 +117,13 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const RopeArgs p) {
     }
 
     for (int r0 = group; r0 < rows + group; r0 += kRows * kGroups) {  // the same trip count in every group
-        uint4 w4[kRows];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) w4[i] = v[i];
-        if (r0 + kRows * kGroups < rows + group) load(r0 + kRows * kGroups);
+        if (r0 != group) load(r0);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             const int r = r0 + i * kGroups;
             if (r0 - group + i * kGroups >= rows) break;  // no group has a row here
-            float u[8] = {lo16(w4[i].x), hi16(w4[i].x), lo16(w4[i].y), hi16(w4[i].y),
-                          lo16(w4[i].z), hi16(w4[i].z), lo16(w4[i].w), hi16(w4[i].w)};
+            float u[8] = {lo16(v[i].x), hi16(v[i].x), lo16(v[i].y), hi16(v[i].y),
+                          lo16(v[i].z), hi16(v[i].z), lo16(v[i].w), hi16(v[i].w)};
             float ss = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], ss);
