@@ -6,14 +6,16 @@
 //
 // The angle. A position times a frequency is taken modulo one turn in 64-bit fixed point: the table
 // holds round(f / 2 pi * 2^64) mod 2^64, the product with the position wraps modulo 2^64, and the
-// wrapped product, read as a signed integer, is the angle in (-1/2, 1/2] turns. Nothing is lost for
-// far positions, where an fp32 product would be off by radians; sincospif then takes an argument in
-// (-1, 1].
+// wrapped product's upper 32 bits, read as a signed integer, are the angle in [-1/2, 1/2) turns. Nothing is
+// lost for far positions, where an fp32 product would be off by radians; sincospif then takes an argument
+// in [-1, 1).
 //
-// Layout. One block takes one token: its first rot/2 threads make the (cos, sin) pairs once, for all
-// heads, while the rows' loads are in flight; then each row is 8 values a lane on a group of kLanes
-// lanes (dim / 8 rounded up to a power of two). The sum of squares is a shuffle tree over the group;
-// in the half style the partner columns sit rot/16 lanes away and come by shuffle too.
+// Layout. A block takes one token at a time: its first rot/2 threads make cosine and sine once, for all heads,
+// a token ahead, and leave them in shared memory multiplied with the gains, so that a row needs one product
+// and one FMA a value; each row is 8 values a lane on a group of kLanes lanes (dim / 8 rounded up to
+// a power of two). The sum of squares is a shuffle tree over the group; in the half style the partner
+// columns sit rot/16 lanes away and come by shuffle too. The grid is what is resident, and a register
+// is refilled with the next token's row as soon as it has been unpacked, so loads never pause.
 //
 // Bound: HBM (4 bytes a value). 40 + 8 heads of 128: see the table of measurements in the design notes.
 
@@ -28,7 +30,9 @@ namespace hc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 3;  // rows per lane group whose loads are in flight together
+constexpr int kRows = 3;         // rows per lane group whose loads are in flight together
+constexpr int kBlocksPerSm = 4;
+constexpr int kMaxDim = 256;
 
 __global__ void prepare_rope_kernel(const __grid_constant__ RopeTable t, int freqs, RopeEntry* out) {
     const int j = static_cast<int>(threadIdx.x);
@@ -42,127 +46,157 @@ __device__ __forceinline__ uint32_t pk(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// What a token's rows are multiplied with, per column: out = r (x direct + x_partner cross), the gains and the
+// rotation in one. [q or k][column]
+struct Turn {
+    float direct[2][kMaxDim];
+    float cross[2][kMaxDim];
+};
+
 template <int kLanes>
-__global__ void __launch_bounds__(kThreads, 4) norm_rope_kernel(const RopeArgs p) {
-    __shared__ float2 cs[kRopeMaxFreqs];
-    const int lane = static_cast<int>(threadIdx.x) % kLanes;
-    const int group = static_cast<int>(threadIdx.x) / kLanes;
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const RopeArgs p) {
+    __shared__ __align__(16) Turn turns[2];  // of this token and of the next
+    const int tid = static_cast<int>(threadIdx.x);
+    const int lane = tid % kLanes, group = tid / kLanes;
     constexpr int kGroups = kThreads / kLanes;
-    const long long t = blockIdx.x;
     const int rows = p.q_heads + p.k_heads;
+    const int chunks = (rows + kRows * kGroups - 1) / (kRows * kGroups);
     const int col = 8 * lane;
     const bool in = col < p.dim;
     const float inv_dim = 1.0f / static_cast<float>(p.dim);
+    const long long step = gridDim.x;
+    const float* gains[2] = {p.gain_per_head ? nullptr : p.q_w, p.gain_per_head ? nullptr : p.k_w};  // per-head ones apply to x
+    auto gain = [&](int kind, int i) { return gains[kind] ? __ldg(gains[kind] + i) : 1.f; };
 
-    const uint4* qrow = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride + col);
-    const uint4* krow = p.k_heads ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride + col)
-                                  : nullptr;
-    const int pitch = p.dim / 8;  // uint4 per row
-    uint4 v[kRows];
-    auto load = [&](int r0) {
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = r0 + i * kGroups;
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (in && r < rows)
-                v[i] = r < p.q_heads ? __ldcs(qrow + static_cast<long long>(r) * pitch)
-                                     : __ldcs(krow + static_cast<long long>(r - p.q_heads) * pitch);
-        }
+    auto load = [&](long long t, int r) {  // row r of token t; zeros where there is none
+        if (!in || r >= rows || t >= p.n) return make_uint4(0, 0, 0, 0);
+        const bool is_q = r < p.q_heads;
+        const __nv_bfloat16* x = is_q ? static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride
+                                      : static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride;
+        return __ldcs(reinterpret_cast<const uint4*>(x + ((is_q ? r : r - p.q_heads) * p.dim + col)));
     };
-    load(group);
 
-    if (static_cast<int>(threadIdx.x) < p.rot / 2) {
-        const int j = static_cast<int>(threadIdx.x);
-        const RopeEntry e = p.table[j];
+    long long t = blockIdx.x;
+    uint4 v[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) v[i] = load(t, group + i * kGroups);
+
+    for (int i = tid; i < p.dim; i += kThreads)  // the columns that are not turned keep these
+        for (int kind = 0; kind < 2; ++kind)
+            for (int buf = 0; buf < 2; ++buf) {
+                turns[buf].direct[kind][i] = gain(kind, i);
+                turns[buf].cross[kind][i] = 0.f;
+            }
+    // the thread's own frequency, if it makes one, and its two columns
+    const bool turns_one = tid < p.rot / 2;
+    const int ca = p.start + (p.pairs ? 2 * tid : tid), cb = ca + (p.pairs ? 1 : p.rot / 2);
+    RopeEntry entry = {};
+    float ga[2], gb[2];
+    if (turns_one) {
+        entry = p.table[tid];
         // an axis outside `axes` can only come from a table made for other axes
-        const int axis = e.axis < p.axes && e.axis >= 0 ? e.axis : 0;
-        const unsigned long long ph = static_cast<unsigned long long>(p.positions[axis * p.n + t]) * e.turns;
-        // signed 2^-64 turns to half turns
-        const float half_turns = static_cast<float>(static_cast<long long>(ph)) * 1.0842021724855044e-19f;  // 2^-63
+        if (entry.axis >= p.axes || entry.axis < 0) entry.axis = 0;
+        for (int kind = 0; kind < 2; ++kind) {
+            ga[kind] = gain(kind, ca);
+            gb[kind] = gain(kind, cb);
+        }
+    }
+    auto position = [&](long long tok) { return turns_one && tok < p.n ? __ldg(p.positions + entry.axis * p.n + tok) : 0; };
+    auto turn = [&](long long pos, Turn& to) {
+        const unsigned long long ph = static_cast<unsigned long long>(pos) * entry.turns;
+        // the upper 32 bits: the angle to 2^-32 turns, as a signed number of half turns
+        const float half_turns = static_cast<float>(static_cast<int>(ph >> 32)) * 4.6566128730773926e-10f;  // 2^-31
         float s, c;
         sincospif(half_turns, &s, &c);
-        cs[j] = make_float2(c, s);
-    }
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+            to.direct[kind][ca] = ga[kind] * c;
+            to.cross[kind][ca] = -gb[kind] * s;
+            to.direct[kind][cb] = gb[kind] * c;
+            to.cross[kind][cb] = ga[kind] * s;
+        }
+    };
     __syncthreads();
+    long long pos = position(t);
+    if (turns_one) turn(pos, turns[0]);
+    pos = position(t + step);
 
-    // this lane's eight columns: cos and signed sin of each, the lane of its partner columns (half style)
     const int x = col - p.start;
     const bool turned = in && x >= 0 && x < p.rot;
-    const int half = p.rot / 2;
-    const int away = p.rot / 16;  // lanes between partners
-    float c[8], s[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        c[e] = 1.f;
-        s[e] = 0.f;
-    }
-    int partner = lane;
-    if (turned) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            int j;
-            bool first;
-            if (p.pairs) {
-                j = (x + e) / 2;
-                first = (e & 1) == 0;
-            } else {
-                first = x < half;
-                j = first ? x + e : x - half + e;
-            }
-            const float2 f = cs[j];
-            c[e] = f.x;
-            s[e] = first ? -f.y : f.y;
-        }
-        partner = p.pairs ? lane : x < half ? lane + away : lane - away;
-    }
+    const int away = p.rot / 16;  // lanes between partners (half style)
+    const int partner = turned && !p.pairs ? (x < p.rot / 2 ? lane + away : lane - away) : lane;
 
-    for (int r0 = group; r0 < rows + group; r0 += kRows * kGroups) {  // the same trip count in every group
-        if (r0 != group) load(r0);
+    for (int buf = 0; t < p.n; t += step, buf ^= 1) {
+        __syncthreads();  // turns[buf] is there; turns[buf ^ 1] has been read
+        if (turns_one) {
+            turn(pos, turns[buf ^ 1]);
+            pos = position(t + 2 * step);
+        }
+        const Turn& now = turns[buf];
+        for (int k = 0; k < chunks; ++k) {
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = r0 + i * kGroups;
-            if (r0 - group + i * kGroups >= rows) break;  // no group has a row here
-            float u[8] = {lo16(v[i].x), hi16(v[i].x), lo16(v[i].y), hi16(v[i].y),
-                          lo16(v[i].z), hi16(v[i].z), lo16(v[i].w), hi16(v[i].w)};
-            float ss = 0.f;
+            for (int i = 0; i < kRows; ++i) {
+                const int r = (k * kRows + i) * kGroups + group;
+                float u[8] = {lo16(v[i].x), hi16(v[i].x), lo16(v[i].y), hi16(v[i].y),
+                              lo16(v[i].z), hi16(v[i].z), lo16(v[i].w), hi16(v[i].w)};
+                // the row that follows in this register: of the next chunk, or of the next token's first
+                v[i] = k + 1 < chunks ? load(t, r + kRows * kGroups) : load(t + step, group + i * kGroups);
+                if (r - group >= rows) continue;  // no group has a row here
+                float ss = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], ss);
+                for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], ss);
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o, 32);
-            const float rs = rsqrtf(fmaf(ss, inv_dim, p.eps));
-            const bool is_q = r < p.q_heads;
-            const float* w = is_q ? p.q_w : p.k_w;
-            if (in && r < rows && w) {
-                w += col + (p.gain_per_head ? static_cast<long long>(is_q ? r : r - p.q_heads) * p.dim : 0);
-                const float4 g0 = __ldg(reinterpret_cast<const float4*>(w));
-                const float4 g1 = __ldg(reinterpret_cast<const float4*>(w) + 1);
-                u[0] *= rs * g0.x; u[1] *= rs * g0.y; u[2] *= rs * g0.z; u[3] *= rs * g0.w;
-                u[4] *= rs * g1.x; u[5] *= rs * g1.y; u[6] *= rs * g1.z; u[7] *= rs * g1.w;
-            } else {
+                for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o, 32);
+                const float rs = rsqrtf(fmaf(ss, inv_dim, p.eps));
+                const bool is_q = r < p.q_heads;
+                const int at = (is_q ? r : r - p.q_heads) * p.dim + col;
+                if (p.gain_per_head) {
+                    const float* w = is_q ? p.q_w : p.k_w;
+                    if (in && r < rows && w) {
+                        const float4 g0 = __ldg(reinterpret_cast<const float4*>(w + at));
+                        const float4 g1 = __ldg(reinterpret_cast<const float4*>(w + at) + 1);
+                        u[0] *= g0.x; u[1] *= g0.y; u[2] *= g0.z; u[3] *= g0.w;
+                        u[4] *= g1.x; u[5] *= g1.y; u[6] *= g1.z; u[7] *= g1.w;
+                    }
+                }
+                // the partner columns; where nothing turns, zeros (cross is 0, but 0 * infinity is not)
+                float q[8];
+                if (p.pairs) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] *= rs;
-            }
-            float o[8];
-            if (p.pairs) {
+                    for (int e = 0; e < 8; ++e) q[e] = turned ? u[e ^ 1] : 0.f;
+                } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = fmaf(u[e ^ 1], s[e], u[e] * c[e]);
-            } else {
+                    for (int e = 0; e < 8; ++e) q[e] = __shfl_sync(0xFFFFFFFFu, u[e], partner, kLanes);
+                }
+                const int kind = is_q ? 0 : 1;
+                float o[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = fmaf(__shfl_sync(0xFFFFFFFFu, u[e], partner, kLanes), s[e], u[e] * c[e]);
-            }
-            if (!turned) {  // outside the rotated columns the value itself (a NaN partner must not reach it)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = u[e];
-            }
-            if (in && r < rows) {
-                __nv_bfloat16* dst = is_q ? static_cast<__nv_bfloat16*>(p.q_out) + t * p.q_out_stride + static_cast<long long>(r) * p.dim
-                                          : static_cast<__nv_bfloat16*>(p.k_out) + t * p.k_out_stride +
-                                                static_cast<long long>(r - p.q_heads) * p.dim;
-                *reinterpret_cast<uint4*>(dst + col) =
-                    make_uint4(pk(o[0], o[1]), pk(o[2], o[3]), pk(o[4], o[5]), pk(o[6], o[7]));
+                for (int e = 0; e < 8; e += 4) {
+                    const float4 d = *reinterpret_cast<const float4*>(&now.direct[kind][(col + e) % kMaxDim]);
+                    const float4 c = *reinterpret_cast<const float4*>(&now.cross[kind][(col + e) % kMaxDim]);
+                    o[e] = rs * fmaf(q[e], c.x, u[e] * d.x);
+                    o[e + 1] = rs * fmaf(q[e + 1], c.y, u[e + 1] * d.y);
+                    o[e + 2] = rs * fmaf(q[e + 2], c.z, u[e + 2] * d.z);
+                    o[e + 3] = rs * fmaf(q[e + 3], c.w, u[e + 3] * d.w);
+                }
+                if (in && r < rows) {
+                    __nv_bfloat16* dst = is_q ? static_cast<__nv_bfloat16*>(p.q_out) + t * p.q_out_stride
+                                              : static_cast<__nv_bfloat16*>(p.k_out) + t * p.k_out_stride;
+                    __stcs(reinterpret_cast<uint4*>(dst + at), make_uint4(pk(o[0], o[1]), pk(o[2], o[3]), pk(o[4], o[5]), pk(o[6], o[7])));
+                }
             }
         }
     }
+}
+
+template <int kLanes>
+int launch(const RopeArgs& a, cudaStream_t stream) {
+    const int sms = attn_sm_count();
+    if (sms == 0) return -7;
+    const long long resident = static_cast<long long>(kBlocksPerSm) * sms;
+    const unsigned grid = static_cast<unsigned>(a.n < resident ? a.n : resident);
+    norm_rope_kernel<kLanes><<<grid, kThreads, 0, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? 0 : -7;
 }
 
 }  // namespace
@@ -173,15 +207,13 @@ int launch_prepare_rope(const RopeTable& t, int freqs, void* table, cudaStream_t
 }
 
 int launch_norm_rope(const RopeArgs& a, cudaStream_t stream) {
-    const unsigned grid = static_cast<unsigned>(a.n);
     const int lanes = a.dim / 8;
-    if (lanes <= 1) norm_rope_kernel<1><<<grid, kThreads, 0, stream>>>(a);
-    else if (lanes <= 2) norm_rope_kernel<2><<<grid, kThreads, 0, stream>>>(a);
-    else if (lanes <= 4) norm_rope_kernel<4><<<grid, kThreads, 0, stream>>>(a);
-    else if (lanes <= 8) norm_rope_kernel<8><<<grid, kThreads, 0, stream>>>(a);
-    else if (lanes <= 16) norm_rope_kernel<16><<<grid, kThreads, 0, stream>>>(a);
-    else norm_rope_kernel<32><<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? 0 : -7;
+    if (lanes <= 1) return launch<1>(a, stream);
+    if (lanes <= 2) return launch<2>(a, stream);
+    if (lanes <= 4) return launch<4>(a, stream);
+    if (lanes <= 8) return launch<8>(a, stream);
+    if (lanes <= 16) return launch<16>(a, stream);
+    return launch<32>(a, stream);
 }
 
 }  // namespace hc
