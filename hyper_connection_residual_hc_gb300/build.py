@@ -11,8 +11,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libhc.so")
 SOURCES = ["hc_fused.cu", "hc_api.cu", "hc_final.cu", "hc_generic.cu", "hc_proj.cu", "hc_host.cu",
-           "hc_rope.cu", "hc_kv.cu", "hc_attend.cu", "hc_attn_api.cu"]
-HEADERS = ["hc_ptx.cuh", "hc_internal.h", "hc_attn.h", "hc_kv.cuh"]
+           "hc_rope.cu", "hc_kv.cu", "hc_attend.cu", "hc_attend_tiles.cu", "hc_attn_api.cu"]
+HEADERS = ["hc_ptx.cuh", "hc_internal.h", "hc_attn.h", "hc_attn_dev.cuh", "hc_kv.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]

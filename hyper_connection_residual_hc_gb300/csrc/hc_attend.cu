@@ -33,6 +33,7 @@
 #include <mutex>
 
 #include "hc_attn.h"
+#include "hc_attn_dev.cuh"
 #include "hc_kv.cuh"
 #include "hc_ptx.cuh"
 
@@ -43,13 +44,11 @@ __device__ unsigned int g_hc_attention_error = 0;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;                 // how far (log2) a score may exceed the running maximum
 constexpr uint64_t kWaitNs = 1000000000ull;   // 1 s
 constexpr int kUnit = 32;                     // tokens a warp takes at a time: two cache blocks
 constexpr int kMinUnits = kWarps;             // a CTA's smallest share: one unit a warp
 constexpr int kMaxDevices = 64;
+constexpr long long kTilesFromRows = 128;     // rows of the longest sequence from which hc_attend_tiles.cu takes a call
 
 // ring depth (blocks a warp), CTAs per SM
 template <int D, int kNT>
@@ -73,16 +72,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
@@ -110,27 +99,10 @@ __device__ __forceinline__ void wait_copy(uint32_t bar, uint32_t parity) {
 
 // ---- sequences and their work -----------------------------------------------------------------------
 
-struct Seq {
-    int qs, ql, kvl;  // first row of q, queries, keys
-};
-
-__device__ __forceinline__ Seq load_seq(const AttArgs& p, int b, bool tell) {
-    const int n = static_cast<int>(p.n);
-    const int q0 = p.q_start[b], q1 = p.q_start[b + 1], kv = p.kv_len[b];
-    const int most = p.max_pages << p.s.page_shift;
-    Seq s;
-    s.qs = min(max(q0, 0), n);
-    const int qe = min(max(q1, s.qs), n);
-    s.ql = qe - s.qs;
-    s.kvl = min(max(kv, 0), most);
-    if (tell && (s.qs != q0 || qe != q1 || s.kvl != kv)) atomicOr(&g_hc_attention_error, kErrSeq);
-    return s;
-}
-
 template <int R>
 struct Work {
     int tiles, units;  // tiles of rows, units of each tile
-    __device__ __forceinline__ Work(const AttArgs& p, const Seq& s, int group) {
+    __device__ __forceinline__ Work(const AttArgs& p, const SeqRows& s, int group) {
         const long long rows = static_cast<long long>(s.ql) * group;
         tiles = static_cast<int>((rows + R - 1) / R);
         units = (s.kvl + kUnit - 1) / kUnit;
@@ -148,10 +120,9 @@ struct Work {
 // A CTA's part of one segment.
 struct Segment {
     int b, h, tile, u0, u1, units;
-    Seq s;
-    // positions: the tile's queries stand at first..last; some row sees [lo, hi), every row sees [all_lo, all_hi)
-    int lo, hi, all_lo, all_hi, base;
-    int first_block, end_block;
+    SeqRows s;
+    int lo, hi, all_lo, all_hi;  // TileBounds
+    int first_block, end_block;  // this part's cache blocks
 };
 
 template <int D, int kNT>
@@ -176,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
 
     // ---- this CTA's range of the call's units ----------------------------------------------------------
     long long mine = 0;
-    for (int b = tid; b < p.seqs; b += kThreads) mine += Work<R>(p, load_seq(p, b, blockIdx.x == 0), group).total(heads);
+    for (int b = tid; b < p.seqs; b += kThreads) mine += Work<R>(p, load_seq(p, b, blockIdx.x == 0 ? &g_hc_attention_error : nullptr), group).total(heads);
     long long total = mine;
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
@@ -195,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
         long long before = 0;
         for (int b0 = 0; b0 < p.seqs; b0 += kThreads) {
             const int b = b0 + tid;
-            const long long v = b < p.seqs ? Work<R>(p, load_seq(p, b, false), group).total(heads) : 0;
+            const long long v = b < p.seqs ? Work<R>(p, load_seq(p, b, nullptr), group).total(heads) : 0;
             long long x = v;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
@@ -225,27 +196,19 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
     Segment g = {};
     // the tile's bounds, from g.s, g.tile, g.u0 and g.u1
     auto place = [&]() {
-        const int rows = g.s.ql * group;
-        const int row0 = g.tile * R, row1 = min(row0 + R, rows) - 1;
-        const int pos0 = g.s.kvl - g.s.ql;
-        const int first = pos0 + row0 / group, last = pos0 + row1 / group;
-        if (p.causal) {
-            g.hi = min(max(last + 1, 0), g.s.kvl);
-            g.all_hi = first + 1;
-            g.lo = p.window > 0 ? max(0, first + 1 - p.window) : 0;
-            g.all_lo = p.window > 0 ? max(0, last + 1 - p.window) : 0;
-        } else {
-            g.hi = g.all_hi = g.s.kvl;
-            g.lo = g.all_lo = 0;
-        }
-        g.base = g.lo / kUnit * kUnit;
-        g.first_block = g.base / 16 + 2 * g.u0;
-        g.end_block = min(g.base / 16 + 2 * g.u1, (g.hi + 15) / 16);
+        const TileBounds t = tile_bounds(p, g.s, group, g.tile * R, min(g.tile * R + R, g.s.ql * group) - 1);
+        g.lo = t.lo;
+        g.hi = t.hi;
+        g.all_lo = t.all_lo;
+        g.all_hi = t.all_hi;
+        const int base = g.lo / kUnit * kUnit;
+        g.first_block = base / 16 + 2 * g.u0;
+        g.end_block = min(base / 16 + 2 * g.u1, (g.hi + 15) / 16);
     };
     {
         g.b = found_seq;
         const long long in = found_at;
-        g.s = load_seq(p, g.b, false);
+        g.s = load_seq(p, g.b, nullptr);
         const Work<R> w(p, g.s, group);
         g.units = w.units;
         const long long k = in / w.units;
@@ -333,10 +296,8 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
             m = max(m & 0xFFFFu, m >> 16);
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            // scale the row by the power of two that brings its largest value to [2^7, 2^8): bf16's 8 bits are exact in
-            // fp16 down to 2^-14, and sums stay far below fp32's range. NaN and infinity stay what they are.
-            const uint32_t ex = m >= 0x7F80u ? 134u : max(m >> 7, 27u);
-            const float up = __uint_as_float((261u - ex) << 23), down = __uint_as_float((ex - 7u) << 23);
+            float up, down;
+            row_scale(m, up, down);
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) {
                 const uint32_t w[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
@@ -537,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
             if (g.h == heads) {
                 g.h = 0;
                 while (true) {  // `at` < `end` <= total: a sequence with work follows
-                    g.s = load_seq(p, ++g.b, false);
+                    g.s = load_seq(p, ++g.b, nullptr);
                     if (g.s.ql > 0) break;
                 }
             }
@@ -712,6 +673,7 @@ int launch_rows(const AttArgs& a, cudaStream_t stream) {
 
 int launch_attention(const AttArgs& a, cudaStream_t stream) {
     const long long rows = static_cast<long long>(a.max_q_len) * (a.q_heads / a.s.heads);
+    if (rows >= kTilesFromRows && a.s.dim <= 128) return launch_attention_tiles(a, stream);
     switch (a.s.dim) {
         case 64:
             if (rows <= 8) return launch_rows<64, 1>(a, stream);
@@ -729,7 +691,8 @@ int launch_attention(const AttArgs& a, cudaStream_t stream) {
 }
 
 int read_attention_error(unsigned int* word, int clear, cudaStream_t stream) {
-    unsigned int v = 0;
+    unsigned int v = 0, tiles = 0;
+    if (read_tiles_error(&tiles, clear, stream) != 0) return -7;
     if (cudaMemcpyFromSymbolAsync(&v, g_hc_attention_error, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess)
         return -7;
     if (cudaStreamSynchronize(stream) != cudaSuccess) return -7;
@@ -739,7 +702,7 @@ int read_attention_error(unsigned int* word, int clear, cudaStream_t stream) {
             return -7;
         if (cudaStreamSynchronize(stream) != cudaSuccess) return -7;
     }
-    *word = v;
+    *word = v | tiles;
     return 0;
 }
 

@@ -1,0 +1,654 @@
+// Attention over the 4-bit cache for many queries of a sequence (prefill, chunk by chunk), on the tensor cores'
+// tcgen05.mma with accumulators in tensor memory. Formulas, masks and format: include/hc.h; the kernel for few
+// queries (hc_attend.cu) shares the definitions of rows and masks.
+//
+// A CTA takes 256 rows of one (sequence, kv head): row = query * group + head in the group, two tiles of 128 (the
+// MMA's M). It walks the keys in tiles of 128 tokens:
+//   8 dequantising warps turn the tile's 8 cache blocks into fp16 (exact) in shared memory, once for both row
+//     tiles: keys and values as rows of 64 columns (128 bytes, 128-byte swizzle), one row a token. As the B operand of
+//     S = Q K^T that is K-major; as the B operand of O += P V the same layout reads as MN-major.
+//   1 warp issues the MMAs: S_a = Q_a K^T (128 x 128 x D) and O_a += P_a V (128 x D x 128), the two row tiles in turn,
+//     so that one tile's softmax runs under the other tile's products.
+//   2 x 4 softmax warps, one thread a row (a tensor-memory lane): scores to registers, the running maximum, weights to
+//     fp16 back into tensor memory over the scores, where the second MMA reads them as its A operand.
+// The maximum is raised only when a score exceeds it by more than 2^8 (as in hc_attend.cu), so the outputs in tensor
+// memory are rarely rescaled. S_a of the next tile is issued behind P_a V of this one: a thread that sees its scores
+// knows that its outputs are complete.
+//
+// Per key tile of 256 rows at D = 128 the tensor cores work 4 x 512 cycles, the exponentials take 2,048 cycles of
+// the SM's special function units, the shared memory about as long (operand reads 192 KB, dequantised writes
+// 64 KB at 128 bytes a cycle): three limits of the same size.
+//
+// Every wait is bounded: on expiry the kernel sets a bit of the device error word, stops waiting, lets its MMAs end
+// and frees its tensor memory.
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <mutex>
+
+#include "hc_attn.h"
+#include "hc_attn_dev.cuh"
+#include "hc_kv.cuh"
+#include "hc_ptx.cuh"
+
+namespace hc {
+namespace {
+
+__device__ unsigned int g_hc_tiles_error = 0;
+
+constexpr int kRowTile = 128;   // rows of an MMA
+constexpr int kRows = 2 * kRowTile;
+constexpr int kKeys = 128;      // keys of a tile
+constexpr int kSoftmaxWarps = 8, kDequantWarps = 8;
+constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kNotes = 8;       // key tiles whose notes (absent blocks, NaN values) are kept
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr int kMaxDevices = 64;
+
+template <int D>
+struct TilePlan {
+    static constexpr int kHalf = kKeys * 128;              // bytes of 128 rows of 64 columns
+    static constexpr int kTile = kHalf * (D / 64);         // one operand tile
+    static constexpr int kQ = 0;                           // two row tiles of Q
+    static constexpr int kK = kQ + 2 * kTile;              // two stages
+    static constexpr int kV = kK + 2 * kTile;
+    static constexpr int kNan = kV + 2 * kTile;            // [kNotes][kKeys] bits: 16-column groups whose scale is NaN
+    static constexpr int kBars = kNan + kNotes * kKeys * 2;
+    static constexpr int kSmem = kBars + 16 * 8 + 16 + 1024;  // + alignment
+    static constexpr int kO = 256;                         // tensor memory: S_0, S_1, O_0, O_1
+    static constexpr uint32_t kColumns = 512;
+};
+
+struct Wait {
+    volatile uint32_t* abort;
+    __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) const {
+        if (mbar_test(bar, parity)) return;
+        const uint64_t t0 = global_timer_ns();
+        while (true) {
+            for (int i = 0; i < 32; ++i)
+                if (mbar_test(bar, parity)) return;
+            if (*abort) return;
+            if (global_timer_ns() - t0 > kWaitNs) {
+                *abort = 1u;
+                atomicOr(&g_hc_tiles_error, kErrTile);
+                return;
+            }
+        }
+    }
+    // at exit: lets MMAs in flight end whatever was aborted
+    __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) const {
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_test(bar, parity)) {
+            if (global_timer_ns() - t0 > kWaitNs) {
+                atomicOr(&g_hc_tiles_error, kErrTile);
+                return;
+            }
+        }
+    }
+};
+
+// Shared-memory descriptor of an operand stored as rows of 128 bytes with the 128-byte swizzle, 8-row groups 1,024
+// bytes apart; `leading`: bytes between blocks of 64 columns (read by MN-major operands only). Fields as in
+// sdesc_kmajor_sw64; swizzle mode 2 = 128 bytes.
+__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t leading) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(leading >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+// kind::f16, fp16 operands, fp32 accumulator; bit 16: B is MN-major
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
+    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    umma_bf16(d, a, b, idesc, accumulate);  // the element types are the descriptor's
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const float (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+        "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+        "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// One lane's part of a cache block in registers.
+template <int D>
+struct BlockRegs {
+    uint4 k[D / 64], v[D / 64];
+    uint32_t ks[2];                    // D / 32 bytes
+    uint32_t vs[(D + 127) / 128];
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs p) {
+    using T = TilePlan<D>;
+    constexpr int kSteps = D / 16;       // MMAs of S
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ int scan[kThreads / 32 + 1];
+    __shared__ int found_seq, found_tile;
+    __shared__ uint32_t absent[kNotes], nan_any[kNotes];  // per key tile: blocks that are not there; some value's scale is NaN
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = static_cast<int>(threadIdx.x), warp = tid / 32, lane = tid % 32;
+    const int heads = p.s.heads, group = p.q_heads / heads;
+
+    // ---- which rows: blockIdx.x counts (kv head fastest) the tiles of all sequences ---------------------
+    const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(heads));
+    const int want = static_cast<int>(blockIdx.x / static_cast<unsigned>(heads));
+    if (tid == 0) found_seq = -1;
+    {
+        int before = 0;
+        for (int b0 = 0; b0 < p.seqs; b0 += kThreads) {
+            const int b = b0 + tid;
+            int v = 0;
+            if (b < p.seqs) {
+                const SeqRows s = load_seq(p, b, blockIdx.x == 0 ? &g_hc_tiles_error : nullptr);
+                v = static_cast<int>((static_cast<long long>(s.ql) * group + kRows - 1) / kRows);
+            }
+            int x = v;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                if (lane >= o) x += y;
+            }
+            __syncthreads();
+            if (lane == 31) scan[warp] = x;
+            __syncthreads();
+            int chunk = 0;
+            for (int w = 0; w < kThreads / 32; ++w) {
+                if (w < warp) x += scan[w];
+                chunk += scan[w];
+            }
+            x += before;
+            if (x > want && x - v <= want) {
+                found_seq = b;
+                found_tile = want - (x - v);
+            }
+            before += chunk;
+            if (before > want) break;  // the same in every thread
+        }
+        __syncthreads();
+    }
+    if (found_seq < 0) return;  // more CTAs than tiles
+    const int b = found_seq, tile = found_tile;
+    const SeqRows s = load_seq(p, b, nullptr);
+    const int rows = s.ql * group, row0 = tile * kRows;
+    const bool two = rows - row0 > kRowTile;  // the second row tile has rows
+    const TileBounds g = tile_bounds(p, s, group, row0, min(row0 + kRows, rows) - 1);
+    const int block0 = g.lo / 16, block_end = (g.hi + 15) / 16;
+    const int tiles = block_end > block0 ? (block_end - block0 + 7) / 8 : 0;
+
+    const uint32_t bars = sbase + T::kBars;
+    auto k_full = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+    auto k_empty = [&](int i) { return bars + 8u * static_cast<uint32_t>(2 + i); };
+    auto v_full = [&](int i) { return bars + 8u * static_cast<uint32_t>(4 + i); };
+    auto v_empty = [&](int i) { return bars + 8u * static_cast<uint32_t>(6 + i); };
+    auto s_full = [&](int a) { return bars + 8u * static_cast<uint32_t>(8 + a); };
+    auto p_full = [&](int a) { return bars + 8u * static_cast<uint32_t>(10 + a); };
+    const uint32_t o_full = bars + 8u * 12u;
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(smem + T::kBars + 16 * 8);
+    volatile uint32_t* abort_flag = tmem_ptr + 1;
+    const Wait wait{abort_flag};
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(k_full(i), kDequantWarps);
+            mbar_init(k_empty(i), 1);
+            mbar_init(v_full(i), kDequantWarps);
+            mbar_init(v_empty(i), 1);
+            mbar_init(s_full(i), 1);
+            mbar_init(p_full(i), 4);
+        }
+        mbar_init(o_full, 1);
+        for (int i = 0; i < kNotes; ++i) absent[i] = nan_any[i] = 0;
+        *abort_flag = 0u;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(tmem_ptr), T::kColumns);
+        tmem_relinquish();
+    }
+
+    // ---- queries: thread i < 256 takes row i ---------------------------------------------------------------
+    float f = 0.f;
+    int see = 0;
+    const bool softmax = warp < kSoftmaxWarps;
+    const int row = row0 + tid;
+    const bool real = softmax && row < rows;
+    if (softmax) {
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+                                   static_cast<long long>(s.qs + (real ? row / group : 0)) * p.q_stride +
+                                   static_cast<long long>(h * group + (real ? row % group : 0)) * D;
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) {
+            const uint4 x = real ? __ldg(reinterpret_cast<const uint4*>(src) + e) : make_uint4(0, 0, 0, 0);
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+        }
+        float up, down;
+        row_scale(max(m & 0xFFFFu, m >> 16), up, down);
+        f = p.scale * kLog2e * p.s.k_unit * down;
+        see = p.causal ? (real ? s.kvl - s.ql + row / group + 1 : 0) : s.kvl;
+        const int i = tid % kRowTile;
+        const uint32_t base = sbase + T::kQ + static_cast<uint32_t>(tid / kRowTile * T::kTile + i * 128);
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) {
+            const uint4 x = real ? __ldg(reinterpret_cast<const uint4*>(src) + e) : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = pack_f16(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
+            st_smem_v4(base + static_cast<uint32_t>(e / 8 * T::kHalf + ((e % 8 ^ i % 8) << 4)), make_uint4(o[0], o[1], o[2], o[3]));
+        }
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_ptr);
+
+    if (warp == kMmaWarp) {
+        // ===== MMAs =======================================================================================
+        constexpr uint32_t id_s = idesc_f16(kRowTile, kKeys, false), id_o = idesc_f16(kRowTile, D, true);
+        const int na = two ? 2 : 1;
+        auto scores = [&](int a, int j) {
+            const uint32_t q = sbase + T::kQ + static_cast<uint32_t>(a * T::kTile), k = sbase + T::kK + static_cast<uint32_t>(j % 2 * T::kTile);
+#pragma unroll
+            for (int st = 0; st < kSteps; ++st) {
+                const uint32_t off = static_cast<uint32_t>(st / 4 * T::kHalf + st % 4 * 32);
+                mma_ss(tmem + static_cast<uint32_t>(a * kKeys), sdesc_sw128(q + off, 16), sdesc_sw128(k + off, 16), id_s, st != 0 ? 1u : 0u);
+            }
+            umma_commit(s_full(a));
+        };
+        auto outputs = [&](int a, int j) {
+            const uint32_t v = sbase + T::kV + static_cast<uint32_t>(j % 2 * T::kTile);
+#pragma unroll
+            for (int st = 0; st < kKeys / 16; ++st)
+                mma_ts(tmem + static_cast<uint32_t>(T::kO + a * D), tmem + static_cast<uint32_t>(a * kKeys + st * 8),
+                       sdesc_sw128(v + static_cast<uint32_t>(st * 2048), T::kHalf), id_o, j != 0 || st != 0 ? 1u : 0u);
+        };
+        if (tiles > 0) {
+            wait(k_full(0), 0);
+            tc_fence_after();
+            if (lane == 0) {
+                for (int a = 0; a < na; ++a) scores(a, 0);
+                umma_commit(k_empty(0));
+            }
+            __syncwarp();
+        }
+        for (int j = 0; j < tiles; ++j) {
+            for (int a = 0; a < na; ++a) {
+                if (a == 0) wait(v_full(j % 2), j / 2 & 1);
+                wait(p_full(a), j & 1);
+                if (a == 0 && j + 1 < tiles) wait(k_full((j + 1) % 2), (j + 1) / 2 & 1);
+                tc_fence_after();
+                if (lane == 0) {
+                    outputs(a, j);
+                    if (a == na - 1) umma_commit(v_empty(j % 2));
+                    if (j + 1 < tiles) {
+                        scores(a, j + 1);
+                        if (a == na - 1) umma_commit(k_empty((j + 1) % 2));
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (lane == 0) {
+            umma_commit(o_full);
+            wait.drain(o_full, 0);
+        }
+        __syncwarp();
+    } else if (!softmax) {
+        // ===== dequantising: warp w takes block w of each key tile =========================================
+        const int w = warp - kSoftmaxWarps, r = lane / 4, c = lane % 4;
+        const int* table = p.page_table + static_cast<long long>(b) * p.max_pages;
+        auto page_of = [&](int j) {  // -1: nothing to load
+            const int blk = block0 + 8 * j + w;
+            return j < tiles && blk < block_end ? __ldg(table + (blk * 16 >> p.s.page_shift)) : -2;
+        };
+        bool there = false;
+        BlockRegs<D> x = {};
+        auto fetch = [&](int j, int page) {
+            there = false;
+            if (page == -2) return;
+            if (page < 0 || page >= p.s.pages) {
+                if (lane == 0) atomicOr(&g_hc_tiles_error, kErrPage);
+                return;
+            }
+            there = true;
+            const int tok = (block0 + 8 * j + w) * 16;
+            const unsigned char* src = p.cache + (((static_cast<long long>(page) * heads + h) << (p.s.page_shift - 4)) +
+                                                  ((tok & ((1 << p.s.page_shift) - 1)) >> 4)) * kv_block_bytes(D);
+#pragma unroll
+            for (int q = 0; q < D / 64; ++q) {
+                x.k[q] = *reinterpret_cast<const uint4*>(src + q * 512 + lane * 16);
+                x.v[q] = *reinterpret_cast<const uint4*>(src + KvPlace<D>::kValueCodes + q * 512 + lane * 16);
+            }
+            if constexpr (D == 64) x.ks[0] = *reinterpret_cast<const uint16_t*>(src + KvPlace<D>::kKeyScales + lane * 2);
+            else x.ks[0] = *reinterpret_cast<const uint32_t*>(src + KvPlace<D>::kKeyScales + lane * 4);
+            x.vs[0] = *reinterpret_cast<const uint32_t*>(src + KvPlace<D>::kValueScales + (r * (D / 8) / 16 * 4 + c) * 4);
+        };
+        int page = page_of(0);
+        fetch(0, page);
+        page = page_of(1);
+        for (int j = 0; j < tiles; ++j) {
+            const int st = j % 2, note = j % kNotes;
+            const uint32_t parity = static_cast<uint32_t>((j / 2 & 1) ^ 1);
+            const int tok0 = (block0 + 8 * j) * 16;
+            const bool whole = tok0 >= g.all_lo && tok0 + kKeys <= g.all_hi;
+            // keys: tokens r and r + 8, columns [c D/4, (c+1) D/4): 16-byte chunks of 8 columns
+            if (j >= 2) wait(k_empty(st), parity);
+            {
+                const uint32_t base = sbase + T::kK + static_cast<uint32_t>(st * T::kTile + (16 * w + r) * 128);
+                uint4 o[2][D / 32];  // [token][chunk]
+#pragma unroll
+                for (int q = 0; q < D / 64; ++q) {
+                    const uint32_t wd[4] = {x.k[q].x, x.k[q].y, x.k[q].z, x.k[q].w};
+                    const uint32_t h0 = e4m3x2_to_f16(x.ks[0] & 0xFFFFu), h1 = D == 64 ? h0 : e4m3x2_to_f16(x.ks[0] >> 16);
+                    const int i0 = D == 64 ? 0 : q, i1 = D == 64 ? 1 : q;
+                    const uint32_t s0 = __byte_perm(h0, 0, i0 ? 0x3232 : 0x1010), s1 = __byte_perm(h1, 0, i1 ? 0x3232 : 0x1010);
+                    uint32_t t0[8], t1[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t a0, a1, a2, a3;
+                        e2m1_word_to_f16(wd[e], a0, a1, a2, a3);
+                        t0[2 * e] = mul_f16x2(a0, s0);
+                        t0[2 * e + 1] = mul_f16x2(a1, s0);
+                        t1[2 * e] = mul_f16x2(a2, s1);
+                        t1[2 * e + 1] = mul_f16x2(a3, s1);
+                    }
+                    o[0][2 * q] = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+                    o[0][2 * q + 1] = make_uint4(t0[4], t0[5], t0[6], t0[7]);
+                    o[1][2 * q] = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                    o[1][2 * q + 1] = make_uint4(t1[4], t1[5], t1[6], t1[7]);
+                }
+                // the two 64-column halves lie in the same banks: lanes of the second take each pair of chunks the other way round
+                const bool swap = D > 64 && c >= 2;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) {
+                        uint4 v = swap ? o[t][e ^ 1] : o[t][e];
+                        if (!there) v = make_uint4(0, 0, 0, 0);
+                        const int chunk = c * (D / 32) + (swap ? e ^ 1 : e);
+                        st_smem_v4(base + static_cast<uint32_t>(t * 1024 + chunk / 8 * T::kHalf + ((chunk % 8 ^ r) << 4)), v);
+                    }
+            }
+            if (lane == 0) {
+                // tile j + 2's note, which no warp can write before this one arrives below, and whose last reader was
+                // tile j + 2 - kNotes: scores of tile j - 2 are done, so every softmax up to tile j - 3 is
+                if (w == 0) nan_any[(j + 2) % kNotes] = 0;
+                if (there) atomicAnd(&absent[note], ~(1u << w));
+                else atomicOr(&absent[note], 1u << w);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(k_full(st));
+            // values: tokens 2c, 2c+1, 2c+8, 2c+9, columns [r D/8, (r+1) D/8)
+            if (j >= 2) wait(v_empty(st), parity);
+            {
+                uint32_t s4 = x.vs[0];
+                if (!whole) {
+                    // a NaN scale must not reach rows that do not see the token: 0 here, noted for the rows that do
+                    uint16_t* notes = reinterpret_cast<uint16_t*>(smem + T::kNan) + note * kKeys + 16 * w;
+                    uint32_t bad = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (there && (s4 >> (8 * i) & 0x7Fu) == 0x7Fu) {
+                            bad |= 1u << i;
+                            s4 &= ~(0xFFu << (8 * i));
+                        }
+                    if (lane < 16) notes[lane] = 0;
+                    __syncwarp();
+                    const int kb = r * (D / 8) / 16;
+                    // lanes of one c hold the groups of the same tokens, in turn
+                    for (int y = 0; y < 8; ++y) {
+                        if (r == y && bad)
+                            for (int i = 0; i < 4; ++i)
+                                if (bad >> i & 1) notes[2 * c + i % 2 + 8 * (i / 2)] |= static_cast<uint16_t>(1u << kb);
+                        __syncwarp();
+                    }
+                    if (bad) atomicOr(&nan_any[note], 1u);
+                }
+                const uint32_t base = sbase + T::kV + static_cast<uint32_t>(st * T::kTile + 16 * w * 128);
+                uint32_t y[4][D / 16];  // [token][pairs of columns]
+#pragma unroll
+                for (int q = 0; q < D / 64; ++q) {
+                    const uint32_t wd[4] = {x.v[q].x, x.v[q].y, x.v[q].z, x.v[q].w};
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) e2m1_word_to_f16(wd[m], y[0][4 * q + m], y[1][4 * q + m], y[2][4 * q + m], y[3][4 * q + m]);
+                }
+                const uint32_t sp[2] = {e4m3x2_to_f16(s4 & 0xFFFFu), e4m3x2_to_f16(s4 >> 16)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t sc = __byte_perm(sp[i / 2], 0, i % 2 ? 0x3232 : 0x1010);
+                    const int t = 2 * c + i % 2 + 8 * (i / 2);
+#pragma unroll
+                    for (int m = 0; m < D / 16; ++m) y[i][m] = there ? mul_f16x2(y[i][m], sc) : 0u;
+                    // rows r and r ^ 1 would meet in the banks: odd ones store their chunks the other way round
+                    const bool swap = D > 64 && r % 2 != 0;
+#pragma unroll
+                    for (int q = 0; q < D / 64; ++q) {
+                        const int z = D > 64 ? q ^ 1 : q;
+                        const uint4 v = swap ? make_uint4(y[i][4 * z], y[i][4 * z + 1], y[i][4 * z + 2], y[i][4 * z + 3])
+                                             : make_uint4(y[i][4 * q], y[i][4 * q + 1], y[i][4 * q + 2], y[i][4 * q + 3]);
+                        const int chunk = r * (D / 64) + (swap ? z : q);
+                        st_smem_v4(base + static_cast<uint32_t>(t * 128 + chunk / 8 * T::kHalf + ((chunk % 8 ^ t % 8) << 4)), v);
+                    }
+                }
+            }
+            fetch(j + 1, page);
+            page = page_of(j + 2);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_full(st));
+        }
+    } else {
+        // ===== softmax ========================================================================================
+        const int a = warp / 4;
+        if (a == 0 || two) {
+            const uint32_t quad = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16);
+            const uint32_t ts = quad + static_cast<uint32_t>(a * kKeys), to = quad + static_cast<uint32_t>(T::kO + a * D);
+            float m = -INFINITY, l = 0.f;
+            uint32_t nan_groups = 0;
+            const int low = p.window > 0 ? see - p.window : 0, high = min(see, s.kvl);
+            for (int j = 0; j < tiles; ++j) {
+                wait(s_full(a), j & 1);
+                tc_fence_after();
+                const int tok0 = (block0 + 8 * j) * 16;
+                const uint32_t gone = *reinterpret_cast<volatile uint32_t*>(&absent[j % kNotes]);
+                const bool whole = tok0 >= g.all_lo && tok0 + kKeys <= g.all_hi && gone == 0;
+                // this row sees columns [from, upto) of the tile
+                const int from = low - tok0, upto = high - tok0;
+                float v[32];
+                float top = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < kKeys / 32; ++q) {
+                    tmem_ld32(ts + static_cast<uint32_t>(32 * q), v);
+                    if (whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int n = 32 * q + i;
+                            if (n >= from && n < upto && !(gone >> (n / 16) & 1)) top = fmaxf(top, v[i]);
+                        }
+                    }
+                }
+                top = top == -INFINITY ? top : top * f;
+                if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
+                    const float m2 = fmaxf(m, top);
+                    const float fade = m2 == -INFINITY ? 1.f : ex2(m - m2);
+                    m = m2;
+                    l *= fade;
+                    if (j > 0) {
+#pragma unroll
+                        for (int q = 0; q < D / 32; ++q) {
+                            tmem_ld32(to + static_cast<uint32_t>(32 * q), v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] *= fade;
+                            tmem_st32(to + static_cast<uint32_t>(32 * q), v);
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+                for (int q = 0; q < kKeys / 32; ++q) {
+                    tmem_ld32(ts + static_cast<uint32_t>(32 * q), v);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float z = fmaf(v[i], f, -base);
+                        if (!whole) {
+                            const int n = 32 * q + i;
+                            if (!(n >= from && n < upto) || (gone >> (n / 16) & 1)) z = -INFINITY;
+                        }
+                        v[i] = ex2(z);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        sum0 += v[2 * i];
+                        sum1 += v[2 * i + 1];
+                        w[i] = pack_f16(v[2 * i], v[2 * i + 1]);
+                    }
+                    tmem_st16(ts + static_cast<uint32_t>(16 * q), w);
+                }
+                l += sum0 + sum1;
+                if (!whole) {
+                    // the notes are complete with the tile's values, which may come after its scores
+                    wait(v_full(j % 2), j / 2 & 1);
+                    if (*reinterpret_cast<volatile uint32_t*>(&nan_any[j % kNotes])) {
+                        const uint16_t* notes = reinterpret_cast<const uint16_t*>(smem + T::kNan) + j % kNotes * kKeys;
+                        for (int n = max(from, 0); n < min(upto, kKeys); ++n) nan_groups |= notes[n];
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(a));
+            }
+            // ---- results -----------------------------------------------------------------------------------
+            if (tiles > 0) wait(o_full, 0);
+            tc_fence_after();
+            const float scale = l == 0.f ? 0.f : p.s.v_unit / l;
+            const long long token = s.qs + row / group;
+            const int head = h * group + row % group;
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D;
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+                float v[32];
+                if (tiles > 0) {
+                    tmem_ld32(to + static_cast<uint32_t>(32 * q), v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    v[i] = nan_groups >> (2 * q + i / 16) & 1 ? __uint_as_float(0x7FC00000u) : l == 0.f ? 0.f : v[i] * scale;
+                if (real) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 t = __floats2bfloat162_rn(v[i + 2 * e], v[i + 2 * e + 1]);
+                            w[e] = *reinterpret_cast<const uint32_t*>(&t);
+                        }
+                        *reinterpret_cast<uint4*>(dst + 32 * q + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            if (real && p.lse) p.lse[token * p.q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, T::kColumns);
+    }
+}
+
+template <int D>
+int launch_tiles(const AttArgs& a, cudaStream_t stream) {
+    using T = TilePlan<D>;
+    static std::mutex mu;
+    static bool done[kMaxDevices] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -7;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!done[dev]) {
+            if (cudaFuncSetAttribute(attend_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem) != cudaSuccess) return -7;
+            done[dev] = true;
+        }
+    }
+    const int group = a.q_heads / a.s.heads;
+    // at most this many tiles of rows: each sequence may end inside one
+    const long long most = a.n * group / kRows + (a.seqs < a.n ? a.seqs : a.n);
+    const long long grid = most * a.s.heads;
+    if (grid > 0x7FFFFFFFLL) return -7;
+    attend_tiles_kernel<D><<<static_cast<unsigned>(grid), kThreads, T::kSmem, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? 0 : -7;
+}
+
+}  // namespace
+
+int launch_attention_tiles(const AttArgs& a, cudaStream_t stream) {
+    return a.s.dim == 64 ? launch_tiles<64>(a, stream) : launch_tiles<128>(a, stream);
+}
+
+int read_tiles_error(unsigned int* word, int clear, cudaStream_t stream) {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbolAsync(&v, g_hc_tiles_error, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess) return -7;
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return -7;
+    if (clear && v != 0) {
+        const unsigned int z = 0;
+        if (cudaMemcpyToSymbolAsync(g_hc_tiles_error, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess) return -7;
+        if (cudaStreamSynchronize(stream) != cudaSuccess) return -7;
+    }
+    *word = v;
+    return 0;
+}
+
+}  // namespace hc

@@ -99,5 +99,8 @@ struct AttArgs {
 };
 int launch_attention(const AttArgs& a, cudaStream_t stream);
 int read_attention_error(unsigned int* word, int clear, cudaStream_t stream);
+// many queries a sequence (hc_attend_tiles.cu), dim 64 or 128
+int launch_attention_tiles(const AttArgs& a, cudaStream_t stream);
+int read_tiles_error(unsigned int* word, int clear, cudaStream_t stream);
 
 }  // namespace hc

@@ -1,0 +1,74 @@
+// Device code that the two attention kernels (hc_attend.cu, hc_attend_tiles.cu) share: sequences, masks and small
+// instructions.
+#pragma once
+
+#include <cstdint>
+#include <cuda_fp16.h>
+
+#include "hc_attn.h"
+
+namespace hc {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;  // how far (log2) a score may exceed the running maximum before it is raised
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The power of two that brings a query row whose largest magnitude has the bf16 bits m to [2^7, 2^8): bf16's 8 bits
+// are then exact in fp16 down to 2^-14, and sums stay far below fp32's range. NaN and infinity stay what they are.
+__device__ __forceinline__ void row_scale(uint32_t m, float& up, float& down) {
+    const uint32_t e = m >= 0x7F80u ? 134u : max(m >> 7, 27u);
+    up = __uint_as_float((261u - e) << 23);
+    down = __uint_as_float((e - 7u) << 23);
+}
+
+struct SeqRows {
+    int qs, ql, kvl;  // first row of q, queries, keys
+};
+
+// `tell`: the error word to note clamped bounds in, or null
+__device__ __forceinline__ SeqRows load_seq(const AttArgs& p, int b, unsigned int* tell) {
+    const int n = static_cast<int>(p.n);
+    const int q0 = p.q_start[b], q1 = p.q_start[b + 1], kv = p.kv_len[b];
+    const int most = p.max_pages << p.s.page_shift;
+    SeqRows s;
+    s.qs = min(max(q0, 0), n);
+    const int qe = min(max(q1, s.qs), n);
+    s.ql = qe - s.qs;
+    s.kvl = min(max(kv, 0), most);
+    if (tell && (s.qs != q0 || qe != q1 || s.kvl != kv)) atomicOr(tell, kErrSeq);
+    return s;
+}
+
+// Keys of the rows row0..row1 of a sequence (row = query * group + head of the group): some row sees [lo, hi), every
+// row sees [all_lo, all_hi).
+struct TileBounds {
+    int lo, hi, all_lo, all_hi;
+};
+__device__ __forceinline__ TileBounds tile_bounds(const AttArgs& p, const SeqRows& s, int group, int row0, int row1) {
+    TileBounds g;
+    if (p.causal) {
+        const int pos0 = s.kvl - s.ql;
+        const int first = pos0 + row0 / group, last = pos0 + row1 / group;
+        g.hi = min(max(last + 1, 0), s.kvl);
+        g.all_hi = first + 1;
+        g.lo = p.window > 0 ? max(0, first + 1 - p.window) : 0;
+        g.all_lo = p.window > 0 ? max(0, last + 1 - p.window) : 0;
+    } else {
+        g.hi = g.all_hi = s.kvl;
+        g.lo = g.all_lo = 0;
+    }
+    return g;
+}
+
+}  // namespace hc
