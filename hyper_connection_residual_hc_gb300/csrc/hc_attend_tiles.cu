@@ -4,7 +4,7 @@
 //
 // A CTA takes 256 rows of one (sequence, kv head): row = query * group + head in the group, two tiles of 128 (the
 // MMA's M). It walks the keys in tiles of 128 tokens:
-//   8 dequantising warps turn the tile's 8 cache blocks into fp16 (exact) in shared memory, once for both row
+//   4 dequantising warps turn the tile's 8 cache blocks into fp16 (exact) in shared memory, once for both row
 //     tiles: keys and values as rows of 64 columns (128 bytes, 128-byte swizzle), one row a token. As the B operand of
 //     S = Q K^T that is K-major; as the B operand of O += P V the same layout reads as MN-major.
 //   1 warp issues the MMAs: S_a = Q_a K^T (128 x 128 x D) and O_a += P_a V (128 x D x 128), the two row tiles in turn,
@@ -42,7 +42,8 @@ __device__ unsigned int g_hc_tiles_error = 0;
 constexpr int kRowTile = 128;   // rows of an MMA
 constexpr int kRows = 2 * kRowTile;
 constexpr int kKeys = 128;      // keys of a tile
-constexpr int kSoftmaxWarps = 8, kDequantWarps = 8;
+constexpr int kSoftmaxWarps = 8, kDequantWarps = 4;
+constexpr int kBlocksPerWarp = kKeys / 16 / kDequantWarps;  // cache blocks of a key tile that a dequantising warp takes
 constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kNotes = 8;       // key tiles whose notes (absent blocks, NaN values) are kept
@@ -140,7 +141,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const float (&v)[32]) {
         "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16};" ::"r"(addr),
@@ -149,12 +150,82 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]
         : "memory");
 }
 
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The weights 2^(score * f + shift) of one row of scores in tensor memory, as fp16 pairs, and their sum (in fp32, before
+// the rounding); returns the largest score seen. kMask: only columns [from, upto) without the blocks in `gone` are seen.
+template <bool kMask>
+__device__ __forceinline__ float weights(uint32_t ts, float f, float shift, int from, int upto, uint32_t gone, uint32_t (&w)[kKeys / 2],
+                                         float& sum) {
+    float top0 = -INFINITY, top1 = -INFINITY;
+    uint64_t s0 = pair(0.f, 0.f), s1 = s0;
+    const uint64_t ff = pair(f, f), sh = pair(shift, shift);
+#pragma unroll
+    for (int q = 0; q < kKeys / 32; ++q) {
+        float v[32];
+        tmem_ld32(ts + static_cast<uint32_t>(32 * q), v);
+        if constexpr (kMask) {
+            const int a = min(max(from - 32 * q, 0), 32), b = min(max(upto - 32 * q, 0), 32);
+            uint32_t seen = b > a ? (0xFFFFFFFFu >> (32 - (b - a))) << a : 0u;
+            if (gone >> (2 * q) & 1) seen &= 0xFFFF0000u;
+            if (gone >> (2 * q + 1) & 1) seen &= 0x0000FFFFu;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (!(seen >> i & 1)) v[i] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            top0 = fmaxf(top0, fmaxf(v[i], v[i + 1]));
+            top1 = fmaxf(top1, fmaxf(v[i + 2], v[i + 3]));
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            float a, b, c, d;
+            unpair(fma2(pair(v[i], v[i + 1]), ff, sh), a, b);
+            unpair(fma2(pair(v[i + 2], v[i + 3]), ff, sh), c, d);
+            if constexpr (kMask) {  // f may be 0
+                a = v[i] == -INFINITY ? -INFINITY : a;
+                b = v[i + 1] == -INFINITY ? -INFINITY : b;
+                c = v[i + 2] == -INFINITY ? -INFINITY : c;
+                d = v[i + 3] == -INFINITY ? -INFINITY : d;
+            }
+            a = ex2(a);
+            b = ex2(b);
+            c = ex2(c);
+            d = ex2(d);
+            s0 = add2(s0, pair(a, b));
+            s1 = add2(s1, pair(c, d));
+            w[16 * q + i / 2] = pack_f16(a, b);
+            w[16 * q + i / 2 + 1] = pack_f16(c, d);
+        }
+    }
+    float x, y;
+    unpair(add2(s0, s1), x, y);
+    sum = x + y;
+    return fmaxf(top0, top1);
+}
+
 // One lane's part of a cache block in registers.
 template <int D>
 struct BlockRegs {
     uint4 k[D / 64], v[D / 64];
-    uint32_t ks[2];                    // D / 32 bytes
-    uint32_t vs[(D + 127) / 128];
+    uint32_t ks, vs;  // D / 32 key scales, 4 value scales
 };
 
 template <int D>
@@ -165,7 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int scan[kThreads / 32 + 1];
     __shared__ int found_seq, found_tile;
-    __shared__ uint32_t absent[kNotes], nan_any[kNotes];  // per key tile: blocks that are not there; some value's scale is NaN
+    __shared__ uint32_t absent[kNotes][kDequantWarps];  // per key tile: bits of the blocks that are not there
+    __shared__ uint32_t nan_any[kNotes];                // per key tile: some value's scale is NaN
     const uint32_t sbase = smem_u32(smem);
     const int tid = static_cast<int>(threadIdx.x), warp = tid / 32, lane = tid % 32;
     const int heads = p.s.heads, group = p.q_heads / heads;
@@ -237,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             mbar_init(p_full(i), 4);
         }
         mbar_init(o_full, 1);
-        for (int i = 0; i < kNotes; ++i) absent[i] = nan_any[i] = 0;
+        for (int i = 0; i < kNotes; ++i) nan_any[i] = 0;
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -336,52 +408,77 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         }
         __syncwarp();
     } else if (!softmax) {
-        // ===== dequantising: warp w takes block w of each key tile =========================================
+        // ===== dequantising: warp w takes blocks 2w and 2w + 1 of each key tile ============================
         const int w = warp - kSoftmaxWarps, r = lane / 4, c = lane % 4;
         const int* table = p.page_table + static_cast<long long>(b) * p.max_pages;
-        auto page_of = [&](int j) {  // -1: nothing to load
-            const int blk = block0 + 8 * j + w;
-            return j < tiles && blk < block_end ? __ldg(table + (blk * 16 >> p.s.page_shift)) : -2;
-        };
-        bool there = false;
-        BlockRegs<D> x = {};
-        auto fetch = [&](int j, int page) {
-            there = false;
-            if (page == -2) return;
-            if (page < 0 || page >= p.s.pages) {
-                if (lane == 0) atomicOr(&g_hc_tiles_error, kErrPage);
-                return;
-            }
-            there = true;
-            const int tok = (block0 + 8 * j + w) * 16;
-            const unsigned char* src = p.cache + (((static_cast<long long>(page) * heads + h) << (p.s.page_shift - 4)) +
-                                                  ((tok & ((1 << p.s.page_shift) - 1)) >> 4)) * kv_block_bytes(D);
+        const unsigned char* src[kBlocksPerWarp];  // of the tile whose words are being loaded; null: nothing there
+        bool there[kBlocksPerWarp];
+        int page[kBlocksPerWarp];
+        BlockRegs<D> x[kBlocksPerWarp] = {};
+        auto find = [&](int j) {  // page entries of tile j; -2: behind the last block
 #pragma unroll
-            for (int q = 0; q < D / 64; ++q) {
-                x.k[q] = *reinterpret_cast<const uint4*>(src + q * 512 + lane * 16);
-                x.v[q] = *reinterpret_cast<const uint4*>(src + KvPlace<D>::kValueCodes + q * 512 + lane * 16);
+            for (int i = 0; i < kBlocksPerWarp; ++i) {
+                const int blk = block0 + 8 * j + kBlocksPerWarp * w + i;
+                page[i] = j < tiles && blk < block_end ? __ldg(table + (blk * 16 >> p.s.page_shift)) : -2;
             }
-            if constexpr (D == 64) x.ks[0] = *reinterpret_cast<const uint16_t*>(src + KvPlace<D>::kKeyScales + lane * 2);
-            else x.ks[0] = *reinterpret_cast<const uint32_t*>(src + KvPlace<D>::kKeyScales + lane * 4);
-            x.vs[0] = *reinterpret_cast<const uint32_t*>(src + KvPlace<D>::kValueScales + (r * (D / 8) / 16 * 4 + c) * 4);
         };
-        int page = page_of(0);
-        fetch(0, page);
-        page = page_of(1);
+        auto place = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < kBlocksPerWarp; ++i) {
+                src[i] = nullptr;
+                if (page[i] == -2) continue;
+                if (page[i] < 0 || page[i] >= p.s.pages) {
+                    if (lane == 0) atomicOr(&g_hc_tiles_error, kErrPage);
+                    continue;
+                }
+                const int tok = (block0 + 8 * j + kBlocksPerWarp * w + i) * 16;
+                src[i] = p.cache + (((static_cast<long long>(page[i]) * heads + h) << (p.s.page_shift - 4)) +
+                                    ((tok & ((1 << p.s.page_shift) - 1)) >> 4)) * kv_block_bytes(D);
+            }
+        };
+        auto fetch_keys = [&]() {
+#pragma unroll
+            for (int i = 0; i < kBlocksPerWarp; ++i) {
+                if (!src[i]) continue;
+#pragma unroll
+                for (int q = 0; q < D / 64; ++q) x[i].k[q] = *reinterpret_cast<const uint4*>(src[i] + q * 512 + lane * 16);
+                if constexpr (D == 64) x[i].ks = *reinterpret_cast<const uint16_t*>(src[i] + KvPlace<D>::kKeyScales + lane * 2);
+                else x[i].ks = *reinterpret_cast<const uint32_t*>(src[i] + KvPlace<D>::kKeyScales + lane * 4);
+            }
+        };
+        auto fetch_values = [&]() {
+#pragma unroll
+            for (int i = 0; i < kBlocksPerWarp; ++i) {
+                if (!src[i]) continue;
+#pragma unroll
+                for (int q = 0; q < D / 64; ++q)
+                    x[i].v[q] = *reinterpret_cast<const uint4*>(src[i] + KvPlace<D>::kValueCodes + q * 512 + lane * 16);
+                x[i].vs = *reinterpret_cast<const uint32_t*>(src[i] + KvPlace<D>::kValueScales + (r * (D / 8) / 16 * 4 + c) * 4);
+            }
+        };
+        find(0);
+        place(0);
+        fetch_keys();
+        fetch_values();
+        find(1);
         for (int j = 0; j < tiles; ++j) {
             const int st = j % 2, note = j % kNotes;
             const uint32_t parity = static_cast<uint32_t>((j / 2 & 1) ^ 1);
             const int tok0 = (block0 + 8 * j) * 16;
             const bool whole = tok0 >= g.all_lo && tok0 + kKeys <= g.all_hi;
+#pragma unroll
+            for (int i = 0; i < kBlocksPerWarp; ++i) there[i] = src[i] != nullptr;
+            place(j + 1);
             // keys: tokens r and r + 8, columns [c D/4, (c+1) D/4): 16-byte chunks of 8 columns
             if (j >= 2) wait(k_empty(st), parity);
-            {
-                const uint32_t base = sbase + T::kK + static_cast<uint32_t>(st * T::kTile + (16 * w + r) * 128);
+#pragma unroll
+            for (int i = 0; i < kBlocksPerWarp; ++i) {
+                const uint32_t base = sbase + T::kK + static_cast<uint32_t>(st * T::kTile + (16 * (kBlocksPerWarp * w + i) + r) * 128);
                 uint4 o[2][D / 32];  // [token][chunk]
 #pragma unroll
                 for (int q = 0; q < D / 64; ++q) {
-                    const uint32_t wd[4] = {x.k[q].x, x.k[q].y, x.k[q].z, x.k[q].w};
-                    const uint32_t h0 = e4m3x2_to_f16(x.ks[0] & 0xFFFFu), h1 = D == 64 ? h0 : e4m3x2_to_f16(x.ks[0] >> 16);
+                    const uint32_t wd[4] = {x[i].k[q].x, x[i].k[q].y, x[i].k[q].z, x[i].k[q].w};
+                    const uint32_t h0 = e4m3x2_to_f16(x[i].ks & 0xFFFFu), h1 = D == 64 ? h0 : e4m3x2_to_f16(x[i].ks >> 16);
                     const int i0 = D == 64 ? 0 : q, i1 = D == 64 ? 1 : q;
                     const uint32_t s0 = __byte_perm(h0, 0, i0 ? 0x3232 : 0x1010), s1 = __byte_perm(h1, 0, i1 ? 0x3232 : 0x1010);
                     uint32_t t0[8], t1[8];
@@ -406,76 +503,83 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
 #pragma unroll
                     for (int e = 0; e < D / 32; ++e) {
                         uint4 v = swap ? o[t][e ^ 1] : o[t][e];
-                        if (!there) v = make_uint4(0, 0, 0, 0);
+                        if (!there[i]) v = make_uint4(0, 0, 0, 0);
                         const int chunk = c * (D / 32) + (swap ? e ^ 1 : e);
                         st_smem_v4(base + static_cast<uint32_t>(t * 1024 + chunk / 8 * T::kHalf + ((chunk % 8 ^ r) << 4)), v);
                     }
             }
+            fetch_keys();  // tile j + 1's
             if (lane == 0) {
                 // tile j + 2's note, which no warp can write before this one arrives below, and whose last reader was
                 // tile j + 2 - kNotes: scores of tile j - 2 are done, so every softmax up to tile j - 3 is
                 if (w == 0) nan_any[(j + 2) % kNotes] = 0;
-                if (there) atomicAnd(&absent[note], ~(1u << w));
-                else atomicOr(&absent[note], 1u << w);
+                uint32_t off = 0;
+#pragma unroll
+                for (int i = 0; i < kBlocksPerWarp; ++i) off |= there[i] ? 0u : 1u << (kBlocksPerWarp * w + i);
+                absent[note][w] = off;
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(k_full(st));
             // values: tokens 2c, 2c+1, 2c+8, 2c+9, columns [r D/8, (r+1) D/8)
             if (j >= 2) wait(v_empty(st), parity);
-            {
-                uint32_t s4 = x.vs[0];
+#pragma unroll
+            for (int i = 0; i < kBlocksPerWarp; ++i) {
+                const int blk = kBlocksPerWarp * w + i;
+                uint32_t s4 = x[i].vs;
                 if (!whole) {
                     // a NaN scale must not reach rows that do not see the token: 0 here, noted for the rows that do
-                    uint16_t* notes = reinterpret_cast<uint16_t*>(smem + T::kNan) + note * kKeys + 16 * w;
+                    uint16_t* notes = reinterpret_cast<uint16_t*>(smem + T::kNan) + note * kKeys + 16 * blk;
                     uint32_t bad = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (there && (s4 >> (8 * i) & 0x7Fu) == 0x7Fu) {
-                            bad |= 1u << i;
-                            s4 &= ~(0xFFu << (8 * i));
+                    for (int e = 0; e < 4; ++e)
+                        if (there[i] && (s4 >> (8 * e) & 0x7Fu) == 0x7Fu) {
+                            bad |= 1u << e;
+                            s4 &= ~(0xFFu << (8 * e));
                         }
                     if (lane < 16) notes[lane] = 0;
                     __syncwarp();
-                    const int kb = r * (D / 8) / 16;
-                    // lanes of one c hold the groups of the same tokens, in turn
-                    for (int y = 0; y < 8; ++y) {
-                        if (r == y && bad)
-                            for (int i = 0; i < 4; ++i)
-                                if (bad >> i & 1) notes[2 * c + i % 2 + 8 * (i / 2)] |= static_cast<uint16_t>(1u << kb);
-                        __syncwarp();
+                    if (__any_sync(0xFFFFFFFFu, bad != 0)) {
+                        const int kb = r * (D / 8) / 16;
+                        // lanes of one c hold the groups of the same tokens, in turn
+                        for (int y = 0; y < 8; ++y) {
+                            if (r == y && bad)
+                                for (int e = 0; e < 4; ++e)
+                                    if (bad >> e & 1) notes[2 * c + e % 2 + 8 * (e / 2)] |= static_cast<uint16_t>(1u << kb);
+                            __syncwarp();
+                        }
+                        if (lane == 0) nan_any[note] = 1;
                     }
-                    if (bad) atomicOr(&nan_any[note], 1u);
                 }
-                const uint32_t base = sbase + T::kV + static_cast<uint32_t>(st * T::kTile + 16 * w * 128);
+                const uint32_t base = sbase + T::kV + static_cast<uint32_t>(st * T::kTile + 16 * blk * 128);
                 uint32_t y[4][D / 16];  // [token][pairs of columns]
 #pragma unroll
                 for (int q = 0; q < D / 64; ++q) {
-                    const uint32_t wd[4] = {x.v[q].x, x.v[q].y, x.v[q].z, x.v[q].w};
+                    const uint32_t wd[4] = {x[i].v[q].x, x[i].v[q].y, x[i].v[q].z, x[i].v[q].w};
 #pragma unroll
                     for (int m = 0; m < 4; ++m) e2m1_word_to_f16(wd[m], y[0][4 * q + m], y[1][4 * q + m], y[2][4 * q + m], y[3][4 * q + m]);
                 }
                 const uint32_t sp[2] = {e4m3x2_to_f16(s4 & 0xFFFFu), e4m3x2_to_f16(s4 >> 16)};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t sc = __byte_perm(sp[i / 2], 0, i % 2 ? 0x3232 : 0x1010);
-                    const int t = 2 * c + i % 2 + 8 * (i / 2);
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t sc = __byte_perm(sp[e / 2], 0, e % 2 ? 0x3232 : 0x1010);
+                    const int t = 2 * c + e % 2 + 8 * (e / 2);
 #pragma unroll
-                    for (int m = 0; m < D / 16; ++m) y[i][m] = there ? mul_f16x2(y[i][m], sc) : 0u;
+                    for (int m = 0; m < D / 16; ++m) y[e][m] = there[i] ? mul_f16x2(y[e][m], sc) : 0u;
                     // rows r and r ^ 1 would meet in the banks: odd ones store their chunks the other way round
                     const bool swap = D > 64 && r % 2 != 0;
 #pragma unroll
                     for (int q = 0; q < D / 64; ++q) {
                         const int z = D > 64 ? q ^ 1 : q;
-                        const uint4 v = swap ? make_uint4(y[i][4 * z], y[i][4 * z + 1], y[i][4 * z + 2], y[i][4 * z + 3])
-                                             : make_uint4(y[i][4 * q], y[i][4 * q + 1], y[i][4 * q + 2], y[i][4 * q + 3]);
+                        const uint4 v = swap ? make_uint4(y[e][4 * z], y[e][4 * z + 1], y[e][4 * z + 2], y[e][4 * z + 3])
+                                             : make_uint4(y[e][4 * q], y[e][4 * q + 1], y[e][4 * q + 2], y[e][4 * q + 3]);
                         const int chunk = r * (D / 64) + (swap ? z : q);
                         st_smem_v4(base + static_cast<uint32_t>(t * 128 + chunk / 8 * T::kHalf + ((chunk % 8 ^ t % 8) << 4)), v);
                     }
                 }
             }
-            fetch(j + 1, page);
-            page = page_of(j + 2);
+            fetch_values();  // tile j + 1's
+            find(j + 2);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(v_full(st));
@@ -493,33 +597,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                 wait(s_full(a), j & 1);
                 tc_fence_after();
                 const int tok0 = (block0 + 8 * j) * 16;
-                const uint32_t gone = *reinterpret_cast<volatile uint32_t*>(&absent[j % kNotes]);
+                uint32_t gone = 0;
+#pragma unroll
+                for (int w = 0; w < kDequantWarps; ++w) gone |= *reinterpret_cast<volatile uint32_t*>(&absent[j % kNotes][w]);
                 const bool whole = tok0 >= g.all_lo && tok0 + kKeys <= g.all_hi && gone == 0;
-                // this row sees columns [from, upto) of the tile
+                // this row sees columns [from, upto) of the tile, but for blocks that are not there
                 const int from = low - tok0, upto = high - tok0;
-                float v[32];
-                float top = -INFINITY;
-#pragma unroll
-                for (int q = 0; q < kKeys / 32; ++q) {
-                    tmem_ld32(ts + static_cast<uint32_t>(32 * q), v);
-                    if (whole) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int n = 32 * q + i;
-                            if (n >= from && n < upto && !(gone >> (n / 16) & 1)) top = fmaxf(top, v[i]);
-                        }
-                    }
-                }
-                top = top == -INFINITY ? top : top * f;
-                if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
+                uint32_t w[kKeys / 2];
+                float sum;
+                // Weights by the maximum so far; where a score is too far above it, the maximum is raised and they are taken again.
+                for (int turn = 0; turn < 2; ++turn) {
+                    const float base = m == -INFINITY ? 0.f : m;
+                    const float top = f * (whole ? weights<false>(ts, f, -base, 0, 0, 0u, w, sum) : weights<true>(ts, f, -base, from, upto, gone, w, sum));
+                    if (!__any_sync(0xFFFFFFFFu, top > m + kSlack)) break;
                     const float m2 = fmaxf(m, top);
                     const float fade = m2 == -INFINITY ? 1.f : ex2(m - m2);
                     m = m2;
                     l *= fade;
                     if (j > 0) {
+                        float v[32];
 #pragma unroll
                         for (int q = 0; q < D / 32; ++q) {
                             tmem_ld32(to + static_cast<uint32_t>(32 * q), v);
@@ -529,30 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                         }
                     }
                 }
-                const float base = m == -INFINITY ? 0.f : m;
-                float sum0 = 0.f, sum1 = 0.f;
+                l += sum;
 #pragma unroll
-                for (int q = 0; q < kKeys / 32; ++q) {
-                    tmem_ld32(ts + static_cast<uint32_t>(32 * q), v);
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float z = fmaf(v[i], f, -base);
-                        if (!whole) {
-                            const int n = 32 * q + i;
-                            if (!(n >= from && n < upto) || (gone >> (n / 16) & 1)) z = -INFINITY;
-                        }
-                        v[i] = ex2(z);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        sum0 += v[2 * i];
-                        sum1 += v[2 * i + 1];
-                        w[i] = pack_f16(v[2 * i], v[2 * i + 1]);
-                    }
-                    tmem_st16(ts + static_cast<uint32_t>(16 * q), w);
-                }
-                l += sum0 + sum1;
+                for (int q = 0; q < kKeys / 32; ++q) tmem_st16(ts + static_cast<uint32_t>(16 * q), w + 16 * q);
                 if (!whole) {
                     // the notes are complete with the tile's values, which may come after its scores
                     wait(v_full(j % 2), j / 2 & 1);
