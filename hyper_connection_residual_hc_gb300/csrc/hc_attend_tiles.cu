@@ -108,15 +108,37 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t leading
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    umma_bf16(d, a, b, idesc, accumulate);  // the element types are the descriptor's
+// The whole warp comes here with the same arguments (so that they stay in uniform registers); `lead` is 1 in one lane,
+// which issues.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t lead;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(lead));
+    return lead;
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(lead)
         : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
@@ -360,52 +382,50 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         // ===== MMAs =======================================================================================
         constexpr uint32_t id_s = idesc_f16(kRowTile, kKeys, false), id_o = idesc_f16(kRowTile, D, true);
         const int na = two ? 2 : 1;
+        const uint32_t lead = elect_lane();
+        // the descriptors of each operand's start; a step adds to the address field (16-byte units) only
+        const uint64_t qd = sdesc_sw128(sbase + T::kQ, 16), kd = sdesc_sw128(sbase + T::kK, 16), vd = sdesc_sw128(sbase + T::kV, T::kHalf);
         auto scores = [&](int a, int j) {
-            const uint32_t q = sbase + T::kQ + static_cast<uint32_t>(a * T::kTile), k = sbase + T::kK + static_cast<uint32_t>(j % 2 * T::kTile);
+            const uint64_t q = qd + static_cast<uint64_t>(a * (T::kTile / 16)), k = kd + static_cast<uint64_t>(j % 2 * (T::kTile / 16));
+            const uint32_t d = tmem + static_cast<uint32_t>(a * kKeys);
 #pragma unroll
             for (int st = 0; st < kSteps; ++st) {
-                const uint32_t off = static_cast<uint32_t>(st / 4 * T::kHalf + st % 4 * 32);
-                mma_ss(tmem + static_cast<uint32_t>(a * kKeys), sdesc_sw128(q + off, 16), sdesc_sw128(k + off, 16), id_s, st != 0 ? 1u : 0u);
+                const uint64_t off = static_cast<uint64_t>((st / 4 * T::kHalf + st % 4 * 32) / 16);
+                mma_ss(lead, d, q + off, k + off, id_s, st != 0 ? 1u : 0u);
             }
-            umma_commit(s_full(a));
+            commit(lead, s_full(a));
         };
         auto outputs = [&](int a, int j) {
-            const uint32_t v = sbase + T::kV + static_cast<uint32_t>(j % 2 * T::kTile);
+            const uint64_t v = vd + static_cast<uint64_t>(j % 2 * (T::kTile / 16));
+            const uint32_t d = tmem + static_cast<uint32_t>(T::kO + a * D), w = tmem + static_cast<uint32_t>(a * kKeys);
+            mma_ts(lead, d, w, v, id_o, j != 0 ? 1u : 0u);
 #pragma unroll
-            for (int st = 0; st < kKeys / 16; ++st)
-                mma_ts(tmem + static_cast<uint32_t>(T::kO + a * D), tmem + static_cast<uint32_t>(a * kKeys + st * 8),
-                       sdesc_sw128(v + static_cast<uint32_t>(st * 2048), T::kHalf), id_o, j != 0 || st != 0 ? 1u : 0u);
+            for (int st = 1; st < kKeys / 16; ++st)
+                mma_ts(lead, d, w + static_cast<uint32_t>(st * 8), v + static_cast<uint64_t>(st * 2048 / 16), id_o, 1u);
         };
         if (tiles > 0) {
             wait(k_full(0), 0);
             tc_fence_after();
-            if (lane == 0) {
-                for (int a = 0; a < na; ++a) scores(a, 0);
-                umma_commit(k_empty(0));
-            }
-            __syncwarp();
+            for (int a = 0; a < na; ++a) scores(a, 0);
+            commit(lead, k_empty(0));
         }
         for (int j = 0; j < tiles; ++j) {
             for (int a = 0; a < na; ++a) {
                 if (a == 0) wait(v_full(j % 2), j / 2 & 1);
                 wait(p_full(a), j & 1);
                 if (a == 0 && j + 1 < tiles) wait(k_full((j + 1) % 2), (j + 1) / 2 & 1);
-                tc_fence_after();
-                if (lane == 0) {
-                    outputs(a, j);
-                    if (a == na - 1) umma_commit(v_empty(j % 2));
-                    if (j + 1 < tiles) {
-                        scores(a, j + 1);
-                        if (a == na - 1) umma_commit(k_empty((j + 1) % 2));
-                    }
-                }
                 __syncwarp();
+                tc_fence_after();
+                outputs(a, j);
+                if (a == na - 1) commit(lead, v_empty(j % 2));
+                if (j + 1 < tiles) {
+                    scores(a, j + 1);
+                    if (a == na - 1) commit(lead, k_empty((j + 1) % 2));
+                }
             }
         }
-        if (lane == 0) {
-            umma_commit(o_full);
-            wait.drain(o_full, 0);
-        }
+        commit(lead, o_full);
+        if (lead) wait.drain(o_full, 0);
         __syncwarp();
     } else if (!softmax) {
         // ===== dequantising: warp w takes blocks 2w and 2w + 1 of each key tile ============================
@@ -439,7 +459,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         auto fetch_keys = [&]() {
 #pragma unroll
             for (int i = 0; i < kBlocksPerWarp; ++i) {
-                if (!src[i]) continue;
+                if (!src[i]) {  // zeros: codes of 0 with the scale 0
+#pragma unroll
+                    for (int q = 0; q < D / 64; ++q) x[i].k[q] = make_uint4(0, 0, 0, 0);
+                    x[i].ks = 0;
+                    continue;
+                }
 #pragma unroll
                 for (int q = 0; q < D / 64; ++q) x[i].k[q] = *reinterpret_cast<const uint4*>(src[i] + q * 512 + lane * 16);
                 if constexpr (D == 64) x[i].ks = *reinterpret_cast<const uint16_t*>(src[i] + KvPlace<D>::kKeyScales + lane * 2);
@@ -449,7 +474,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         auto fetch_values = [&]() {
 #pragma unroll
             for (int i = 0; i < kBlocksPerWarp; ++i) {
-                if (!src[i]) continue;
+                if (!src[i]) {
+#pragma unroll
+                    for (int q = 0; q < D / 64; ++q) x[i].v[q] = make_uint4(0, 0, 0, 0);
+                    x[i].vs = 0;
+                    continue;
+                }
 #pragma unroll
                 for (int q = 0; q < D / 64; ++q)
                     x[i].v[q] = *reinterpret_cast<const uint4*>(src[i] + KvPlace<D>::kValueCodes + q * 512 + lane * 16);
@@ -473,40 +503,29 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             if (j >= 2) wait(k_empty(st), parity);
 #pragma unroll
             for (int i = 0; i < kBlocksPerWarp; ++i) {
-                const uint32_t base = sbase + T::kK + static_cast<uint32_t>(st * T::kTile + (16 * (kBlocksPerWarp * w + i) + r) * 128);
-                uint4 o[2][D / 32];  // [token][chunk]
+                // 16-byte chunk e of the lane's columns goes to chunk (c D/32 + e) ^ r of its row. The two 64-column halves lie in
+                // the same banks: lanes of the second take each pair of chunks (two words of codes each) the other way round.
+                const bool swap = D > 64 && c >= 2;
+                const uint32_t base = sbase + T::kK + static_cast<uint32_t>(st * T::kTile + (16 * (kBlocksPerWarp * w + i) + r) * 128 +
+                                                                            c * (D / 32) / 8 * T::kHalf);
+                const uint32_t at = static_cast<uint32_t>((c * (D / 32) % 8 ^ r ^ (swap ? 1 : 0)) << 4);
+                const uint32_t h0 = e4m3x2_to_f16(x[i].ks & 0xFFFFu), h1 = D == 64 ? h0 : e4m3x2_to_f16(x[i].ks >> 16);
 #pragma unroll
                 for (int q = 0; q < D / 64; ++q) {
-                    const uint32_t wd[4] = {x[i].k[q].x, x[i].k[q].y, x[i].k[q].z, x[i].k[q].w};
-                    const uint32_t h0 = e4m3x2_to_f16(x[i].ks & 0xFFFFu), h1 = D == 64 ? h0 : e4m3x2_to_f16(x[i].ks >> 16);
+                    const uint4 k = x[i].k[q];
+                    const uint32_t wd[4] = {swap ? k.z : k.x, swap ? k.w : k.y, swap ? k.x : k.z, swap ? k.y : k.w};
                     const int i0 = D == 64 ? 0 : q, i1 = D == 64 ? 1 : q;
                     const uint32_t s0 = __byte_perm(h0, 0, i0 ? 0x3232 : 0x1010), s1 = __byte_perm(h1, 0, i1 ? 0x3232 : 0x1010);
-                    uint32_t t0[8], t1[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t a0, a1, a2, a3;
-                        e2m1_word_to_f16(wd[e], a0, a1, a2, a3);
-                        t0[2 * e] = mul_f16x2(a0, s0);
-                        t0[2 * e + 1] = mul_f16x2(a1, s0);
-                        t1[2 * e] = mul_f16x2(a2, s1);
-                        t1[2 * e + 1] = mul_f16x2(a3, s1);
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t t[8];
+                        e2m1_word_to_f16(wd[2 * e], t[0], t[1], t[4], t[5]);
+                        e2m1_word_to_f16(wd[2 * e + 1], t[2], t[3], t[6], t[7]);
+                        const uint32_t to = base + (at ^ static_cast<uint32_t>((2 * q + e) << 4));
+                        st_smem_v4(to, make_uint4(mul_f16x2(t[0], s0), mul_f16x2(t[1], s0), mul_f16x2(t[2], s0), mul_f16x2(t[3], s0)));
+                        st_smem_v4(to + 1024, make_uint4(mul_f16x2(t[4], s1), mul_f16x2(t[5], s1), mul_f16x2(t[6], s1), mul_f16x2(t[7], s1)));
                     }
-                    o[0][2 * q] = make_uint4(t0[0], t0[1], t0[2], t0[3]);
-                    o[0][2 * q + 1] = make_uint4(t0[4], t0[5], t0[6], t0[7]);
-                    o[1][2 * q] = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-                    o[1][2 * q + 1] = make_uint4(t1[4], t1[5], t1[6], t1[7]);
                 }
-                // the two 64-column halves lie in the same banks: lanes of the second take each pair of chunks the other way round
-                const bool swap = D > 64 && c >= 2;
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int e = 0; e < D / 32; ++e) {
-                        uint4 v = swap ? o[t][e ^ 1] : o[t][e];
-                        if (!there[i]) v = make_uint4(0, 0, 0, 0);
-                        const int chunk = c * (D / 32) + (swap ? e ^ 1 : e);
-                        st_smem_v4(base + static_cast<uint32_t>(t * 1024 + chunk / 8 * T::kHalf + ((chunk % 8 ^ r) << 4)), v);
-                    }
             }
             fetch_keys();  // tile j + 1's
             if (lane == 0) {
@@ -551,30 +570,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                         if (lane == 0) nan_any[note] = 1;
                     }
                 }
-                const uint32_t base = sbase + T::kV + static_cast<uint32_t>(st * T::kTile + 16 * blk * 128);
-                uint32_t y[4][D / 16];  // [token][pairs of columns]
+                // chunk q of the lane's columns goes to chunk (r D/64 + q) ^ (token % 8) of the token's row; odd r take their two
+                // chunks the other way round, or they would meet r ^ 1 in the banks
+                const bool swap = D > 64 && r % 2 != 0;
+                const uint32_t base = sbase + T::kV + static_cast<uint32_t>(st * T::kTile + 16 * blk * 128 + r * (D / 64) / 8 * T::kHalf);
+                const uint32_t at = static_cast<uint32_t>((r * (D / 64) % 8 ^ (swap ? 1 : 0)) << 4);
+                const uint32_t sp0 = e4m3x2_to_f16(s4 & 0xFFFFu), sp1 = e4m3x2_to_f16(s4 >> 16);
+                const uint32_t sc[4] = {__byte_perm(sp0, 0, 0x1010), __byte_perm(sp0, 0, 0x3232), __byte_perm(sp1, 0, 0x1010),
+                                        __byte_perm(sp1, 0, 0x3232)};
 #pragma unroll
                 for (int q = 0; q < D / 64; ++q) {
-                    const uint32_t wd[4] = {x[i].v[q].x, x[i].v[q].y, x[i].v[q].z, x[i].v[q].w};
+                    const uint4 k0 = x[i].v[q], k1 = x[i].v[D > 64 ? q ^ 1 : q];
+                    const uint32_t wd[4] = {swap ? k1.x : k0.x, swap ? k1.y : k0.y, swap ? k1.z : k0.z, swap ? k1.w : k0.w};
+                    uint32_t y[4][4];  // [token][pairs of columns]
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) e2m1_word_to_f16(wd[m], y[0][4 * q + m], y[1][4 * q + m], y[2][4 * q + m], y[3][4 * q + m]);
-                }
-                const uint32_t sp[2] = {e4m3x2_to_f16(s4 & 0xFFFFu), e4m3x2_to_f16(s4 >> 16)};
+                    for (int m = 0; m < 4; ++m) e2m1_word_to_f16(wd[m], y[0][m], y[1][m], y[2][m], y[3][m]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t sc = __byte_perm(sp[e / 2], 0, e % 2 ? 0x3232 : 0x1010);
-                    const int t = 2 * c + e % 2 + 8 * (e / 2);
-#pragma unroll
-                    for (int m = 0; m < D / 16; ++m) y[e][m] = there[i] ? mul_f16x2(y[e][m], sc) : 0u;
-                    // rows r and r ^ 1 would meet in the banks: odd ones store their chunks the other way round
-                    const bool swap = D > 64 && r % 2 != 0;
-#pragma unroll
-                    for (int q = 0; q < D / 64; ++q) {
-                        const int z = D > 64 ? q ^ 1 : q;
-                        const uint4 v = swap ? make_uint4(y[e][4 * z], y[e][4 * z + 1], y[e][4 * z + 2], y[e][4 * z + 3])
-                                             : make_uint4(y[e][4 * q], y[e][4 * q + 1], y[e][4 * q + 2], y[e][4 * q + 3]);
-                        const int chunk = r * (D / 64) + (swap ? z : q);
-                        st_smem_v4(base + static_cast<uint32_t>(t * 128 + chunk / 8 * T::kHalf + ((chunk % 8 ^ t % 8) << 4)), v);
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = 2 * c + e % 2 + 8 * (e / 2);
+                        st_smem_v4(base + static_cast<uint32_t>(t * 128) + (at ^ static_cast<uint32_t>((q ^ t % 8) << 4)),
+                                   make_uint4(mul_f16x2(y[e][0], sc[e]), mul_f16x2(y[e][1], sc[e]), mul_f16x2(y[e][2], sc[e]),
+                                              mul_f16x2(y[e][3], sc[e])));
                     }
                 }
             }
