@@ -50,12 +50,14 @@ constexpr int kMinUnits = kWarps;             // a CTA's smallest share: one uni
 constexpr int kMaxDevices = 64;
 constexpr long long kTilesFromRows = 128;     // rows of the longest sequence from which hc_attend_tiles.cu takes a call
 
-// ring depth (blocks a warp), CTAs per SM
+// Stages of a warp's ring (a power of two of them, one unit each), CTAs per SM.
 template <int D, int kNT>
 struct Plan {
     static constexpr int kCtas = kNT == 1 && D <= 128 ? 2 : 1;
-    static constexpr int kStages = D == 64 ? 8 : D == 256 ? 4 : kCtas == 2 ? 5 : 8;
-    static constexpr int kRing = kWarps * kStages * kv_block_bytes(D);
+    static constexpr int kLogStages = D == 256 || kCtas == 2 && D == 128 ? 1 : 2;
+    static constexpr int kStages = 1 << kLogStages;
+    static constexpr int kStage = kUnit / 16 * kv_block_bytes(D);
+    static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kStateFloats = D / 16 * kNT * 4 * 32;  // a warp's outputs
     static constexpr int kMl = 2 * 8 * kNT;                     // its maxima and sums
     static constexpr int kMerge = kWarps / 2 * (kStateFloats + kMl) * 4;
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
     const int tid = static_cast<int>(threadIdx.x), warp = tid / 32, lane = tid % 32;
     const int r = lane / 4, c = lane % 4;
     const int heads = p.s.heads, group = p.q_heads / heads;
-    const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * P::kStages * kBlock);
+    const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * P::kStages * P::kStage);
     float* merge = reinterpret_cast<float*>(smem + P::kRing);
     const uint32_t bars = smem_u32(smem + P::kRing + P::kMerge) + static_cast<uint32_t>(warp * P::kStages * 8);
     if (lane < P::kStages) mbar_init(bars + 8u * static_cast<uint32_t>(lane), 1);
@@ -219,20 +221,17 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
         place();
     }
 
-    // ---- the warp's stream of blocks ---------------------------------------------------------------------
-    // Step k of a segment takes unit warp + 8 k of the CTA's part: blocks i = 2k, 2k + 1 of the warp. Lane j looks up
-    // block 32 w + j of window w (its page and address) and issues its copy when its turn comes.
-    uint32_t uses = 0;       // blocks waited for since the kernel began; block i of a segment is use `uses` + i
+    // ---- the warp's stream of units ----------------------------------------------------------------------
+    // Step k of a segment takes unit warp + 8 k of the CTA's part: two cache blocks, one stage of the ring. The lanes look
+    // up the blocks of 16 steps at a time (page and address), lane j block j % 2 of step j / 2, and each issues its copy
+    // when its step's turn comes.
+    uint32_t uses = 0;                     // units before this segment's first: step k is use `uses` + k of the ring
+    uint32_t there = 0;                    // of the 16 steps looked up: bit j: block j is there
+    uint32_t staged = 0;                   // of the units in the ring: bits 2 st, 2 st + 1: the unit's blocks are there
     const unsigned char* where = nullptr;
-    uint32_t there[2] = {};  // which blocks of the current (0) and the previous (1) window were copied
-    int window = 0;
-    auto steps_of = [&]() {
-        const int units_here = (g.end_block - g.first_block + 1) / 2;
-        return units_here > warp ? (units_here - warp + kWarps - 1) / kWarps : 0;
-    };
-    auto look_up = [&](int w) {
-        const int i = 32 * w + lane;
-        const int blk = g.first_block + 2 * (warp + kWarps * (i / 2)) + i % 2;
+    int steps = 0, issued = 0;
+    auto look_up = [&](int k0) {
+        const int blk = g.first_block + 2 * (warp + kWarps * (k0 + lane / 2)) + lane % 2;
         where = nullptr;
         if (blk < g.end_block && blk * 16 + 16 > g.lo) {
             const int tok = blk * 16;
@@ -243,29 +242,23 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
             else
                 atomicOr(&g_hc_attention_error, kErrPage);
         }
-        there[1] = there[0];
-        there[0] = __ballot_sync(0xFFFFFFFFu, where != nullptr);
-        window = w;
+        there = __ballot_sync(0xFFFFFFFFu, where != nullptr);
     };
-    auto issue = [&](int i) {  // block i of this segment
-        if (i / 32 != window) look_up(i / 32);
-        if (lane == i % 32) {
-            const uint32_t st = (uses + static_cast<uint32_t>(i)) % P::kStages;
-            if (where) {
-                mbar_arrive_expect_tx(bars + 8 * st, kBlock);
-                bulk_copy(ring + st * kBlock, where, kBlock, bars + 8 * st);
-            } else {
-                mbar_arrive(bars + 8 * st);
-            }
+    auto issue = [&](int k) {  // in order of k
+        if (k % 16 == 0) look_up(k);
+        const uint32_t st = (uses + static_cast<uint32_t>(k)) % P::kStages;
+        const uint32_t here = there >> (2 * (k % 16)) & 3u;
+        staged = (staged & ~(3u << (2 * st))) | here << (2 * st);
+        if (lane / 2 == k % 16) {
+            const uint32_t bar = bars + 8 * st;
+            if (lane % 2 == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(here) * kBlock));
+            if (where) bulk_copy(ring + st * P::kStage + static_cast<uint32_t>(lane % 2 * kBlock), where, kBlock, bar);
         }
     };
-    int issued = 0, blocks = 0;
     auto open = [&]() {  // start the copies of a new segment
-        blocks = 2 * steps_of();
-        there[0] = there[1] = 0;
-        look_up(0);
-        issued = 0;
-        for (; issued < blocks && issued < P::kStages; ++issued) issue(issued);
+        const int units_here = (g.end_block - g.first_block + 1) / 2;
+        steps = units_here > warp ? (units_here - warp + kWarps - 1) / kWarps : 0;
+        for (issued = 0; issued < steps && issued < P::kStages; ++issued) issue(issued);
     };
     __syncthreads();  // barriers ready
     open();
@@ -328,96 +321,108 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[k][t][e] = 0.f;
 
-        for (int i = 0; i < blocks; i += 2) {
+        for (int k = 0; k < steps; ++k) {
+            const uint32_t use = uses + static_cast<uint32_t>(k), st = use % P::kStages;
+            const int blk0 = g.first_block + 2 * (warp + kWarps * k);
+            const uint32_t slot = ring + st * P::kStage;
+            const uint32_t have = staged >> (2 * st) & 3u;
+            wait_copy(bars + 8 * st, use >> P::kLogStages & 1);
+            // ---- scores of the unit's two blocks -----------------------------------------------------------------
             float z[2][kNT][4];
-            const int blk0 = g.first_block + 2 * (warp + kWarps * (i / 2));
-            uint32_t slot[2];
-            bool have[2];
-            // ---- scores of two blocks --------------------------------------------------------------------------
+            uint32_t ks[2][2];  // key scales: tokens r, then r + 8, D / 64 each
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                const uint32_t use = uses + static_cast<uint32_t>(i + n);
-                const uint32_t st = use % P::kStages;
-                have[n] = (there[(i + n) / 32 == window ? 0 : 1] >> ((i + n) % 32)) & 1;
-                wait_copy(bars + 8 * st, use / P::kStages & 1);
-                slot[n] = ring + st * kBlock;
 #pragma unroll
                 for (int t = 0; t < kNT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) z[n][t][e] = 0.f;
-                const uint32_t ks = slot[n] + KvPlace<D>::kKeyScales + static_cast<uint32_t>(lane * (D / 32));
-                uint32_t sw[2];
+                const uint32_t at_ = slot + static_cast<uint32_t>(n * kBlock + KvPlace<D>::kKeyScales + lane * (D / 32));
                 if constexpr (D == 64) {
-                    sw[0] = lds32(ks & ~3u) >> (8 * (ks & 2u)) & 0xFFFFu;
-                    sw[1] = 0;
+                    ks[n][0] = lds32(at_ & ~3u) >> (8 * (at_ & 2u)) & 0xFFFFu;
+                    ks[n][1] = 0;
                 } else {
-                    sw[0] = lds32(ks);
-                    sw[1] = D == 256 ? lds32(ks + 4) : 0;
+                    ks[n][0] = lds32(at_);
+                    ks[n][1] = D == 256 ? lds32(at_ + 4) : 0;
+                }
+            }
+#pragma unroll
+            for (int quad = 0; quad < D / 64; ++quad) {
+                uint32_t w[2][4], s0[2], s1[2];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const uint4 v = ld_smem_v4(slot + static_cast<uint32_t>(n * kBlock + quad * 512 + lane * 16));
+                    w[n][0] = v.x;
+                    w[n][1] = v.y;
+                    w[n][2] = v.z;
+                    w[n][3] = v.w;
+                    const int i0 = quad, i1 = D / 64 + quad;
+                    const uint32_t h0 = e4m3x2_to_f16(ks[n][i0 / 4] >> (16 * (i0 % 4 / 2)) & 0xFFFFu);
+                    const uint32_t h1 = e4m3x2_to_f16(ks[n][i1 / 4] >> (16 * (i1 % 4 / 2)) & 0xFFFFu);
+                    s0[n] = __byte_perm(h0, 0, i0 % 2 ? 0x3232 : 0x1010);
+                    s1[n] = __byte_perm(h1, 0, i1 % 2 ? 0x3232 : 0x1010);
                 }
 #pragma unroll
-                for (int quad = 0; quad < D / 64; ++quad) {
-                    const uint4 v = ld_smem_v4(slot[n] + static_cast<uint32_t>(quad * 512 + lane * 16));
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    // scale bytes: tokens r, then r + 8, D / 64 each
-                    const int i0 = quad, i1 = D / 64 + quad;
-                    const uint32_t h0 = e4m3x2_to_f16(sw[i0 / 4] >> (16 * (i0 % 4 / 2)) & 0xFFFFu);
-                    const uint32_t h1 = e4m3x2_to_f16(sw[i1 / 4] >> (16 * (i1 % 4 / 2)) & 0xFFFFu);
-                    const uint32_t s0 = __byte_perm(h0, 0, i0 % 2 ? 0x3232 : 0x1010), s1 = __byte_perm(h1, 0, i1 % 2 ? 0x3232 : 0x1010);
+                for (int s = 0; s < 4; ++s)
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
+                    for (int n = 0; n < 2; ++n) {
                         uint32_t x0, x1, x2, x3;
-                        e2m1_word_to_f16(w[s], x0, x1, x2, x3);
-                        const uint32_t a0 = mul_f16x2(x0, s0), a2 = mul_f16x2(x1, s0), a1 = mul_f16x2(x2, s1), a3 = mul_f16x2(x3, s1);
+                        e2m1_word_to_f16(w[n][s], x0, x1, x2, x3);
+                        const uint32_t a0 = mul_f16x2(x0, s0[n]), a2 = mul_f16x2(x1, s0[n]), a1 = mul_f16x2(x2, s1[n]), a3 = mul_f16x2(x3, s1[n]);
 #pragma unroll
                         for (int t = 0; t < kNT; ++t) mma_f16(z[n][t], a0, a1, a2, a3, qf[t][quad * 4 + s][0], qf[t][quad * 4 + s][1]);
                     }
-                }
             }
             // ---- masks, running maximum, weights ------------------------------------------------------------
-            const bool whole = have[0] && have[1] && blk0 * 16 >= g.all_lo && blk0 * 16 + kUnit <= g.all_hi;
+            const bool whole = have == 3u && blk0 * 16 >= g.all_lo && blk0 * 16 + kUnit <= g.all_hi;
+            if (!whole) {  // scores to their final scale here, so that a masked one stays -infinity whatever the factor
+#pragma unroll
+                for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int pos = (blk0 + n) * 16 + r + 8 * (e / 2);
+                            const bool seen = (have >> n & 1) && pos < min(see[t][e % 2], g.s.kvl) &&
+                                              (p.window == 0 || pos >= see[t][e % 2] - p.window);
+                            z[n][t][e] = seen ? z[n][t][e] * f[t][e % 2] : -INFINITY;
+                        }
+            }
+            float top[kNT][2];
             bool raise = false;
 #pragma unroll
             for (int t = 0; t < kNT; ++t)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v = z[n][t][e] * f[t][e % 2];
-                        if (!whole) {
-                            const int pos = (blk0 + n) * 16 + r + 8 * (e / 2);
-                            const int up_to = min(see[t][e % 2], g.s.kvl);
-                            if (!have[n] || pos >= up_to || (p.window > 0 && pos < see[t][e % 2] - p.window)) v = -INFINITY;
-                        }
-                        z[n][t][e] = v;
-                        raise |= v > m[t][e % 2] + kSlack;
-                    }
+                for (int j = 0; j < 2; ++j) {
+                    top[t][j] = fmaxf(fmaxf(z[0][t][j], z[0][t][2 + j]), fmaxf(z[1][t][j], z[1][t][2 + j])) * (whole ? f[t][j] : 1.f);
+                    raise |= top[t][j] > m[t][j] + kSlack;
+                }
             if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
                 for (int t = 0; t < kNT; ++t)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float top = fmaxf(fmaxf(z[0][t][j], z[0][t][2 + j]), fmaxf(z[1][t][j], z[1][t][2 + j]));
 #pragma unroll
-                        for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-                        const float m2 = fmaxf(m[t][j], top);
+                        for (int x = 4; x < 32; x *= 2) top[t][j] = fmaxf(top[t][j], __shfl_xor_sync(0xFFFFFFFFu, top[t][j], x));
+                        const float m2 = fmaxf(m[t][j], top[t][j]);
                         const float fade = m2 == -INFINITY ? 1.f : ex2(m[t][j] - m2);
                         m[t][j] = m2;
                         l[t][j] *= fade;
 #pragma unroll
-                        for (int k = 0; k < kKeySteps; ++k) {
-                            o[k][t][j] *= fade;
-                            o[k][t][2 + j] *= fade;
+                        for (int q = 0; q < kKeySteps; ++q) {
+                            o[q][t][j] *= fade;
+                            o[q][t][2 + j] *= fade;
                         }
                     }
             }
             uint32_t pb[2][kNT][2];
 #pragma unroll
             for (int t = 0; t < kNT; ++t) {
-                const float b0 = m[t][0] == -INFINITY ? 0.f : m[t][0], b1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+                const float b0 = m[t][0] == -INFINITY ? 0.f : -m[t][0], b1 = m[t][1] == -INFINITY ? 0.f : -m[t][1];
+                const float f0 = whole ? f[t][0] : 1.f, f1 = whole ? f[t][1] : 1.f;
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const float w0 = ex2(z[n][t][0] - b0), w1 = ex2(z[n][t][1] - b1);
-                    const float w2 = ex2(z[n][t][2] - b0), w3 = ex2(z[n][t][3] - b1);
+                    const float w0 = ex2(fmaf(z[n][t][0], f0, b0)), w1 = ex2(fmaf(z[n][t][1], f1, b1));
+                    const float w2 = ex2(fmaf(z[n][t][2], f0, b0)), w3 = ex2(fmaf(z[n][t][3], f1, b1));
                     l[t][0] += w0 + w2;
                     l[t][1] += w1 + w3;
                     pb[n][t][0] = transpose_8x8(pack_f16(w0, w1));
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
                 uint32_t nan16[(D + 127) / 128] = {};  // per 16-column group of this lane: tokens of the block whose scale is NaN
 #pragma unroll
                 for (int quad = 0; quad < D / 64; ++quad) {
-                    uint32_t s4 = lds32(slot[n] + KvPlace<D>::kValueScales + static_cast<uint32_t>(((r * (D / 8) + quad * 8) / 16 * 4 + c) * 4));
+                    uint32_t s4 = lds32(slot + static_cast<uint32_t>(n * kBlock + KvPlace<D>::kValueScales + ((r * (D / 8) + quad * 8) / 16 * 4 + c) * 4));
                     if (!whole) {
                         // a token that some row does not see must not reach that row through 0 * NaN: its NaN scale becomes 0
                         // here and is put into the rows that do see it below
@@ -443,10 +448,10 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
                             }
                         bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 1);
                         bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 2);
-                        nan16[quad * 64 / 128] |= have[n] ? bad : 0u;
+                        nan16[quad * 64 / 128] |= have >> n & 1 ? bad : 0u;
                     }
                     const uint32_t sp0 = e4m3x2_to_f16(s4 & 0xFFFFu), sp1 = e4m3x2_to_f16(s4 >> 16);
-                    const uint4 v = ld_smem_v4(slot[n] + KvPlace<D>::kValueCodes + static_cast<uint32_t>(quad * 512 + lane * 16));
+                    const uint4 v = ld_smem_v4(slot + static_cast<uint32_t>(n * kBlock + KvPlace<D>::kValueCodes + quad * 512 + lane * 16));
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int mm = 0; mm < 4; ++mm) {
@@ -478,11 +483,11 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
                             }
                     }
                 }
-                __syncwarp();
-                if (issued < blocks) issue(issued++);
             }
+            __syncwarp();
+            if (issued < steps) issue(issued++);  // into the stage that is free now
         }
-        uses += static_cast<uint32_t>(blocks);
+        uses += static_cast<uint32_t>(steps);
 
         // ---- the next part's copies start before this one is joined ---------------------------------------
         const Segment done = g;
