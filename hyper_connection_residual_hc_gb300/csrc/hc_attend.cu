@@ -66,8 +66,7 @@ struct Plan {
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -75,6 +74,19 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
+}
+// (a.low * s.low, b.low * t.high), where s.high and t.low are 0: two pairs of columns of two tokens become a pair of
+// tokens of one column, scaled. A permutation and a product would do as well, but permutations share their pipe with
+// the conversions, which is the fuller one (exact either way: one term of the sum is 0).
+__device__ __forceinline__ uint32_t weave(__half2 a, uint32_t s, __half2 b, uint32_t t) {
+    const __half2 r = __hfma2(a, *reinterpret_cast<const __half2*>(&s), __hmul2(b, *reinterpret_cast<const __half2*>(&t)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t weave_low(uint32_t a, uint32_t s, uint32_t b, uint32_t t) {
+    return weave(__low2half2(*reinterpret_cast<const __half2*>(&a)), s, __low2half2(*reinterpret_cast<const __half2*>(&b)), t);
+}
+__device__ __forceinline__ uint32_t weave_high(uint32_t a, uint32_t s, uint32_t b, uint32_t t) {
+    return weave(__high2half2(*reinterpret_cast<const __half2*>(&a)), s, __high2half2(*reinterpret_cast<const __half2*>(&b)), t);
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
@@ -434,8 +446,9 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
             for (int n = 0; n < 2; ++n) {
                 uint32_t nan16[(D + 127) / 128] = {};  // per 16-column group of this lane: tokens of the block whose scale is NaN
 #pragma unroll
-                for (int quad = 0; quad < D / 64; ++quad) {
-                    uint32_t s4 = lds32(slot + static_cast<uint32_t>(n * kBlock + KvPlace<D>::kValueScales + ((r * (D / 8) + quad * 8) / 16 * 4 + c) * 4));
+                for (int x = 0; x < (D + 127) / 128; ++x) {  // the lane's 16-column groups (D = 64: half a group)
+                    uint32_t s4 = lds32(slot + static_cast<uint32_t>(n * kBlock + KvPlace<D>::kValueScales +
+                                                                     ((D == 64 ? r / 2 : r * (D / 128) + x) * 4 + c) * 4));
                     if (!whole) {
                         // a token that some row does not see must not reach that row through 0 * NaN: its NaN scale becomes 0
                         // here and is put into the rows that do see it below
@@ -448,19 +461,23 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
                             }
                         bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 1);
                         bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, 2);
-                        nan16[quad * 64 / 128] |= have >> n & 1 ? bad : 0u;
+                        nan16[x] |= have >> n & 1 ? bad : 0u;
                     }
                     const uint32_t sp0 = e4m3x2_to_f16(s4 & 0xFFFFu), sp1 = e4m3x2_to_f16(s4 >> 16);
-                    const uint4 v = ld_smem_v4(slot + static_cast<uint32_t>(n * kBlock + KvPlace<D>::kValueCodes + quad * 512 + lane * 16));
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    const uint32_t e0 = sp0 & 0xFFFFu, o0 = sp0 & 0xFFFF0000u, e1 = sp1 & 0xFFFFu, o1 = sp1 & 0xFFFF0000u;
 #pragma unroll
-                    for (int mm = 0; mm < 4; ++mm) {
-                        uint32_t x0, x1, x2, x3;
-                        e2m1_word_to_f16(w[mm], x0, x1, x2, x3);
-                        const uint32_t a0 = mul_f16x2(__byte_perm(x0, x1, 0x5410), sp0), a1 = mul_f16x2(__byte_perm(x0, x1, 0x7632), sp0);
-                        const uint32_t a2 = mul_f16x2(__byte_perm(x2, x3, 0x5410), sp1), a3 = mul_f16x2(__byte_perm(x2, x3, 0x7632), sp1);
+                    for (int quad = x * 2; quad < (D == 64 ? 1 : x * 2 + 2); ++quad) {
+                        const uint4 v = ld_smem_v4(slot + static_cast<uint32_t>(n * kBlock + KvPlace<D>::kValueCodes + quad * 512 + lane * 16));
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int t = 0; t < kNT; ++t) mma_f16(o[quad * 4 + mm][t], a0, a1, a2, a3, pb[n][t][0], pb[n][t][1]);
+                        for (int mm = 0; mm < 4; ++mm) {
+                            uint32_t x0, x1, x2, x3;  // tokens 2c, 2c + 1, 2c + 8, 2c + 9; a pair of columns each
+                            e2m1_word_to_f16(w[mm], x0, x1, x2, x3);
+                            const uint32_t a0 = weave_low(x0, e0, x1, o0), a1 = weave_high(x0, e0, x1, o0);
+                            const uint32_t a2 = weave_low(x2, e1, x3, o1), a3 = weave_high(x2, e1, x3, o1);
+#pragma unroll
+                            for (int t = 0; t < kNT; ++t) mma_f16(o[quad * 4 + mm][t], a0, a1, a2, a3, pb[n][t][0], pb[n][t][1]);
+                        }
                     }
                 }
                 if (!whole) {
