@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRows = 3;         // rows per lane group whose loads are in flight together
-constexpr int kBlocksPerSm = 4;
+constexpr int kBlocksPerSm = 5;
 constexpr int kMaxDim = 256;
 
 __global__ void prepare_rope_kernel(const __grid_constant__ RopeTable t, int freqs, RopeEntry* out) {
@@ -41,26 +41,50 @@ __global__ void prepare_rope_kernel(const __grid_constant__ RopeTable t, int fre
 
 __device__ __forceinline__ float lo16(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi16(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+// pairs of fp32 in one instruction
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 split(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 __device__ __forceinline__ uint32_t pk(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // What a token's rows are multiplied with, per column: out = r (x direct + x_partner cross), the gains and the
-// rotation in one. [q or k][column]
+// rotation in one. [q or k][place of the column]: the first four of each lane's eight columns, then the other four, so that
+// 16-byte loads of neighbouring lanes lie side by side.
 struct Turn {
     float direct[2][kMaxDim];
     float cross[2][kMaxDim];
 };
+__device__ __forceinline__ int place(int col) { return col % 8 / 4 * (kMaxDim / 2) + col / 8 * 4 + col % 4; }
 
-template <int kLanes>
+// kOne: all rows of a token fit the block's registers at once
+template <int kLanes, bool kOne>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const RopeArgs p) {
     __shared__ __align__(16) Turn turns[2];  // of this token and of the next
     const int tid = static_cast<int>(threadIdx.x);
     const int lane = tid % kLanes, group = tid / kLanes;
     constexpr int kGroups = kThreads / kLanes;
     const int rows = p.q_heads + p.k_heads;
-    const int chunks = (rows + kRows * kGroups - 1) / (kRows * kGroups);
+    const int chunks = kOne ? 1 : (rows + kRows * kGroups - 1) / (kRows * kGroups);
     const int col = 8 * lane;
     const bool in = col < p.dim;
     const float inv_dim = 1.0f / static_cast<float>(p.dim);
@@ -84,12 +108,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
     for (int i = tid; i < p.dim; i += kThreads)  // the columns that are not turned keep these
         for (int kind = 0; kind < 2; ++kind)
             for (int buf = 0; buf < 2; ++buf) {
-                turns[buf].direct[kind][i] = gain(kind, i);
-                turns[buf].cross[kind][i] = 0.f;
+                turns[buf].direct[kind][place(i)] = gain(kind, i);
+                turns[buf].cross[kind][place(i)] = 0.f;
             }
     // the thread's own frequency, if it makes one, and its two columns
     const bool turns_one = tid < p.rot / 2;
     const int ca = p.start + (p.pairs ? 2 * tid : tid), cb = ca + (p.pairs ? 1 : p.rot / 2);
+    const int pa = place(ca), pb = place(cb);
     RopeEntry entry = {};
     float ga[2], gb[2];
     if (turns_one) {
@@ -110,10 +135,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
         sincospif(half_turns, &s, &c);
 #pragma unroll
         for (int kind = 0; kind < 2; ++kind) {
-            to.direct[kind][ca] = ga[kind] * c;
-            to.cross[kind][ca] = -gb[kind] * s;
-            to.direct[kind][cb] = gb[kind] * c;
-            to.cross[kind][cb] = ga[kind] * s;
+            to.direct[kind][pa] = ga[kind] * c;
+            to.cross[kind][pa] = -gb[kind] * s;
+            to.direct[kind][pb] = gb[kind] * c;
+            to.cross[kind][pb] = ga[kind] * s;
         }
     };
     __syncthreads();
@@ -137,14 +162,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
                 const int r = (k * kRows + i) * kGroups + group;
-                float u[8] = {lo16(v[i].x), hi16(v[i].x), lo16(v[i].y), hi16(v[i].y),
-                              lo16(v[i].z), hi16(v[i].z), lo16(v[i].w), hi16(v[i].w)};
+                const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                uint64_t u[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[e] = pair(lo16(w4[e]), hi16(w4[e]));
                 // the row that follows in this register: of the next chunk, or of the next token's first
                 v[i] = k + 1 < chunks ? load(t, r + kRows * kGroups) : load(t + step, group + i * kGroups);
                 if (r - group >= rows) continue;  // no group has a row here
-                float ss = 0.f;
+                uint64_t sq = mul2(u[0], u[0]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], ss);
+                for (int e = 1; e < 4; ++e) sq = fma2(u[e], u[e], sq);
+                const float2 sq2 = split(sq);
+                float ss = sq2.x + sq2.y;
 #pragma unroll
                 for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o, 32);
                 const float rs = rsqrtf(fmaf(ss, inv_dim, p.eps));
@@ -155,34 +184,31 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
                     if (in && r < rows && w) {
                         const float4 g0 = __ldg(reinterpret_cast<const float4*>(w + at));
                         const float4 g1 = __ldg(reinterpret_cast<const float4*>(w + at) + 1);
-                        u[0] *= g0.x; u[1] *= g0.y; u[2] *= g0.z; u[3] *= g0.w;
-                        u[4] *= g1.x; u[5] *= g1.y; u[6] *= g1.z; u[7] *= g1.w;
+                        u[0] = mul2(u[0], pair(g0.x, g0.y));
+                        u[1] = mul2(u[1], pair(g0.z, g0.w));
+                        u[2] = mul2(u[2], pair(g1.x, g1.y));
+                        u[3] = mul2(u[3], pair(g1.z, g1.w));
                     }
                 }
-                // the partner columns; where nothing turns, zeros (cross is 0, but 0 * infinity is not)
-                float q[8];
-                if (p.pairs) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) q[e] = turned ? u[e ^ 1] : 0.f;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) q[e] = __shfl_sync(0xFFFFFFFFu, u[e], partner, kLanes);
-                }
                 const int kind = is_q ? 0 : 1;
-                float o[8];
+                const uint64_t rr = pair(rs, rs);
+                uint32_t o[4];
 #pragma unroll
-                for (int e = 0; e < 8; e += 4) {
-                    const float4 d = *reinterpret_cast<const float4*>(&now.direct[kind][(col + e) % kMaxDim]);
-                    const float4 c = *reinterpret_cast<const float4*>(&now.cross[kind][(col + e) % kMaxDim]);
-                    o[e] = rs * fmaf(q[e], c.x, u[e] * d.x);
-                    o[e + 1] = rs * fmaf(q[e + 1], c.y, u[e + 1] * d.y);
-                    o[e + 2] = rs * fmaf(q[e + 2], c.z, u[e + 2] * d.z);
-                    o[e + 3] = rs * fmaf(q[e + 3], c.w, u[e + 3] * d.w);
+                for (int e = 0; e < 4; ++e) {
+                    // the partner columns; where nothing turns, zeros in the pairs style (cross is 0, but 0 * infinity is not)
+                    const float2 x2 = split(u[e]);
+                    const uint64_t q = p.pairs ? pair(turned ? x2.y : 0.f, turned ? x2.x : 0.f)
+                                               : pair(__shfl_sync(0xFFFFFFFFu, x2.x, partner, kLanes), __shfl_sync(0xFFFFFFFFu, x2.y, partner, kLanes));
+                    const int from = e / 2 * (kMaxDim / 2) + lane * 4 + e % 2 * 2;
+                    const uint64_t d = *reinterpret_cast<const uint64_t*>(&now.direct[kind][from]);
+                    const uint64_t c = *reinterpret_cast<const uint64_t*>(&now.cross[kind][from]);
+                    const float2 y = split(mul2(rr, fma2(q, c, mul2(u[e], d))));
+                    o[e] = pk(y.x, y.y);
                 }
                 if (in && r < rows) {
                     __nv_bfloat16* dst = is_q ? static_cast<__nv_bfloat16*>(p.q_out) + t * p.q_out_stride
                                               : static_cast<__nv_bfloat16*>(p.k_out) + t * p.k_out_stride;
-                    __stcs(reinterpret_cast<uint4*>(dst + at), make_uint4(pk(o[0], o[1]), pk(o[2], o[3]), pk(o[4], o[5]), pk(o[6], o[7])));
+                    __stcs(reinterpret_cast<uint4*>(dst + at), make_uint4(o[0], o[1], o[2], o[3]));
                 }
             }
         }
@@ -195,7 +221,8 @@ int launch(const RopeArgs& a, cudaStream_t stream) {
     if (sms == 0) return -7;
     const long long resident = static_cast<long long>(kBlocksPerSm) * sms;
     const unsigned grid = static_cast<unsigned>(a.n < resident ? a.n : resident);
-    norm_rope_kernel<kLanes><<<grid, kThreads, 0, stream>>>(a);
+    if (a.q_heads + a.k_heads <= kRows * (kThreads / kLanes)) norm_rope_kernel<kLanes, true><<<grid, kThreads, 0, stream>>>(a);
+    else norm_rope_kernel<kLanes, false><<<grid, kThreads, 0, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? 0 : -7;
 }
 
