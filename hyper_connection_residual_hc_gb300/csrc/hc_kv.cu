@@ -8,8 +8,8 @@
 // a quotient by its remainder), which is exact whenever the quotient has few bits: ties are seen as ties.
 //
 // The layout is the one that the attention's matrix instructions read, so the bytes of one token are
-// scattered in 1- and 2-byte pieces over its block of 16 tokens. A warp takes 16 tokens of the call and one
-// head and looks for a run among their slots: 16 consecutive tokens on the 16 slots of one cache block. A run
+// scattered in 1- and 2-byte pieces over its block of 16 tokens. A warp takes 16 tokens of the call and the keys or
+// the values of one head, and looks for a run among their slots: 16 consecutive tokens on the 16 slots of one cache block. A run
 // (prefill) goes block-wise: each lane takes the tokens and columns that it has in the layout, so that it
 // holds whole 16-column groups and whole words, and every store is 16 bytes wide. Other tokens (decode,
 // ragged ends) go token-wise, 8 columns a lane. Both give the same bytes.
@@ -73,44 +73,38 @@ __device__ __forceinline__ uint32_t code_byte(uint32_t pair, float inv_unit, flo
 
 __device__ __forceinline__ float recip_or_zero(float s) { return s > 0.f ? __frcp_rn(s) : 0.f; }
 
-// ---- one token's eight columns (token-wise) ------------------------------------------------------
+// ---- eight columns of one token a lane (token-wise) -----------------------------------------------
+// 32 / (D / 8) tokens side by side in a warp; all lanes come here (the scale is exchanged between two).
 
-template <int D>
-__device__ __forceinline__ void write_token(const KvArgs& p, long long i, int h, unsigned char* block, int t, int lane) {
-    constexpr int kUnits = 2 * D / 8;  // keys, then values, eight columns each
+template <int D, bool kKeys>
+__device__ __forceinline__ void write_token(const KvArgs& p, bool active, long long i, int h, unsigned char* block, int t, int lane) {
+    const int col = 8 * (lane % (D / 8));
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (active) {
+        const __nv_bfloat16* src = kKeys ? static_cast<const __nv_bfloat16*>(p.k_in) + i * p.k_stride
+                                         : static_cast<const __nv_bfloat16*>(p.v_in) + i * p.v_stride;
+        x = __ldcs(reinterpret_cast<const uint4*>(src + static_cast<long long>(h) * D + col));
+    }
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t m = amax_bits(w, 4);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    const float inv_unit = 1.0f / (kKeys ? p.s.k_unit : p.s.v_unit);  // exact: a power of two
+    const uint32_t sb = scale_byte(m, inv_unit);
+    const float s = scale_value(sb), rs = recip_or_zero(s);
+    uint32_t b[4];
 #pragma unroll
-    for (int u0 = 0; u0 < kUnits; u0 += 32) {
-        const int u = u0 + lane;
-        const bool active = u < kUnits;
-        const bool val = u >= D / 8;
-        const int col = 8 * (u % (D / 8));
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (active) {
-            const __nv_bfloat16* src = val ? static_cast<const __nv_bfloat16*>(p.v_in) + i * p.v_stride
-                                           : static_cast<const __nv_bfloat16*>(p.k_in) + i * p.k_stride;
-            x = __ldcs(reinterpret_cast<const uint4*>(src + static_cast<long long>(h) * D + col));
-        }
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t m = amax_bits(w, 4);
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        const float inv_unit = 1.0f / (val ? p.s.v_unit : p.s.k_unit);  // exact: a power of two
-        const uint32_t sb = scale_byte(m, inv_unit);
-        const float s = scale_value(sb), rs = recip_or_zero(s);
-        uint32_t b[4];
+    for (int e = 0; e < 4; ++e) b[e] = code_byte(w[e], inv_unit, s, rs);
+    if (!active) return;
+    if constexpr (kKeys) {
+        unsigned char* dst = block + KvPlace<D>::key_code(t, col);
+        *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(b[0] | b[1] << 8);
+        *reinterpret_cast<uint16_t*>(dst + 4) = static_cast<uint16_t>(b[2] | b[3] << 8);
+        if (lane % 2 == 0) block[KvPlace<D>::key_scale(t, col)] = static_cast<unsigned char>(sb);
+    } else {
+        unsigned char* dst = block + KvPlace<D>::value_code(t, col);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] = code_byte(w[e], inv_unit, s, rs);
-        if (!active) continue;
-        if (val) {
-            unsigned char* dst = block + KvPlace<D>::value_code(t, col);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dst[4 * e] = static_cast<unsigned char>(b[e]);
-            if (lane % 2 == 0) block[KvPlace<D>::value_scale(t, col)] = static_cast<unsigned char>(sb);
-        } else {
-            unsigned char* dst = block + KvPlace<D>::key_code(t, col);
-            *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(b[0] | b[1] << 8);
-            *reinterpret_cast<uint16_t*>(dst + 4) = static_cast<uint16_t>(b[2] | b[3] << 8);
-            if (lane % 2 == 0) block[KvPlace<D>::key_scale(t, col)] = static_cast<unsigned char>(sb);
-        }
+        for (int e = 0; e < 4; ++e) dst[4 * e] = static_cast<unsigned char>(b[e]);
+        if (lane % 2 == 0) block[KvPlace<D>::value_scale(t, col)] = static_cast<unsigned char>(sb);
     }
 }
 
@@ -125,211 +119,206 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t v, float unit) {
 __device__ __forceinline__ uint32_t both(uint32_t scale_byte_) { return e4m3x2_to_f16(scale_byte_ | scale_byte_ << 8); }
 
 // block null: zeros
-template <int D>
-__device__ __forceinline__ void read_token(const KvArgs& p, long long i, int h, const unsigned char* block, int t,
-                                           int lane) {
-    constexpr int kUnits = 2 * D / 8;
-#pragma unroll
-    for (int u0 = 0; u0 < kUnits; u0 += 32) {
-        const int u = u0 + lane;
-        if (u >= kUnits) continue;
-        const bool val = u >= D / 8;
-        const int col = 8 * (u % (D / 8));
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(val ? p.v_out : p.k_out);
-        if (!dst) continue;
-        uint4 o = make_uint4(0, 0, 0, 0);
-        if (block) {
-            uint32_t w, s;
-            if (val) {
-                const unsigned char* src = block + KvPlace<D>::value_code(t, col);
-                w = src[0] | src[4] << 8 | src[8] << 16 | static_cast<uint32_t>(src[12]) << 24;
-                s = both(block[KvPlace<D>::value_scale(t, col)]);
-            } else {
-                const unsigned char* src = block + KvPlace<D>::key_code(t, col);
-                w = *reinterpret_cast<const uint16_t*>(src) | static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(src + 4)) << 16;
-                s = both(block[KvPlace<D>::key_scale(t, col)]);
-            }
-            uint32_t x[4];
-            e2m1_word_to_f16(w, x[0], x[1], x[2], x[3]);
-            const float unit = val ? p.s.v_unit : p.s.k_unit;
-            o = make_uint4(f16x2_to_bf16x2(mul_f16x2(x[0], s), unit), f16x2_to_bf16x2(mul_f16x2(x[1], s), unit),
-                           f16x2_to_bf16x2(mul_f16x2(x[2], s), unit), f16x2_to_bf16x2(mul_f16x2(x[3], s), unit));
+template <int D, bool kKeys>
+__device__ __forceinline__ void read_token(const KvArgs& p, long long i, int h, const unsigned char* block, int t, int lane) {
+    const int col = 8 * (lane % (D / 8));
+    uint4 o = make_uint4(0, 0, 0, 0);
+    if (block) {
+        uint32_t w, s;
+        if constexpr (kKeys) {
+            const unsigned char* src = block + KvPlace<D>::key_code(t, col);
+            w = *reinterpret_cast<const uint16_t*>(src) | static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(src + 4)) << 16;
+            s = both(block[KvPlace<D>::key_scale(t, col)]);
+        } else {
+            const unsigned char* src = block + KvPlace<D>::value_code(t, col);
+            w = src[0] | src[4] << 8 | src[8] << 16 | static_cast<uint32_t>(src[12]) << 24;
+            s = both(block[KvPlace<D>::value_scale(t, col)]);
         }
-        const long long stride = val ? p.v_stride : p.k_stride;
-        __stcs(reinterpret_cast<uint4*>(dst + i * stride + static_cast<long long>(h) * D + col), o);
+        uint32_t x[4];
+        e2m1_word_to_f16(w, x[0], x[1], x[2], x[3]);
+        const float unit = kKeys ? p.s.k_unit : p.s.v_unit;
+        o = make_uint4(f16x2_to_bf16x2(mul_f16x2(x[0], s), unit), f16x2_to_bf16x2(mul_f16x2(x[1], s), unit),
+                       f16x2_to_bf16x2(mul_f16x2(x[2], s), unit), f16x2_to_bf16x2(mul_f16x2(x[3], s), unit));
     }
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(kKeys ? p.k_out : p.v_out) + i * (kKeys ? p.k_stride : p.v_stride);
+    __stcs(reinterpret_cast<uint4*>(dst + static_cast<long long>(h) * D + col), o);
 }
 
 // ---- a whole block of 16 tokens (block-wise) ------------------------------------------------------
 // Lane (r, c) = (lane / 4, lane % 4). Keys: tokens r and r + 8, columns [c D/4, (c+1) D/4). Values: tokens
 // 2c, 2c+1, 2c+8, 2c+9, columns [r D/8, (r+1) D/8).
 
+__device__ __forceinline__ uint32_t code_word(const uint32_t* w, float inv_unit, float s, float rs) {
+    return code_byte(w[0], inv_unit, s, rs) | code_byte(w[1], inv_unit, s, rs) << 8 | code_byte(w[2], inv_unit, s, rs) << 16 |
+           code_byte(w[3], inv_unit, s, rs) << 24;
+}
+
 template <int D>
-__device__ __forceinline__ void write_block(const KvArgs& p, long long i, int h, unsigned char* block, int lane) {
+__device__ __forceinline__ void write_key_block(const KvArgs& p, long long i, int h, unsigned char* block, int lane) {
+    constexpr int kN = D / 4;  // columns a lane
     const int r = lane / 4, c = lane % 4;
-    {
-        constexpr int kN = D / 4;  // columns a lane
-        const float inv_unit = 1.0f / p.s.k_unit;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.k_in) + i * p.k_stride +
-                                   static_cast<long long>(h) * D + c * kN;
-        uint32_t codes[2][kN / 8];  // per token, 8 columns a word
-        uint32_t scales = 0, scales2 = 0;
+    const float inv_unit = 1.0f / p.s.k_unit;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.k_in) + i * p.k_stride + static_cast<long long>(h) * D + c * kN;
+    uint4 x[2][kN / 8];
 #pragma unroll
-        for (int hw = 0; hw < 2; ++hw) {
-            const uint4* row = reinterpret_cast<const uint4*>(src + (r + 8 * hw) * p.k_stride);
-            uint4 x[kN / 8];
+    for (int hw = 0; hw < 2; ++hw)
 #pragma unroll
-            for (int e = 0; e < kN / 8; ++e) x[e] = __ldcs(row + e);
+        for (int e = 0; e < kN / 8; ++e) x[hw][e] = __ldcs(reinterpret_cast<const uint4*>(src + (r + 8 * hw) * p.k_stride) + e);
+    uint32_t codes[2][kN / 8];  // per token, 8 columns a word
+    uint32_t scales[2] = {};
 #pragma unroll
-            for (int g = 0; g < kN / 16; ++g) {
-                const uint32_t w[8] = {x[2 * g].x, x[2 * g].y, x[2 * g].z, x[2 * g].w,
-                                       x[2 * g + 1].x, x[2 * g + 1].y, x[2 * g + 1].z, x[2 * g + 1].w};
-                const uint32_t sb = scale_byte(amax_bits(w, 8), inv_unit);
-                const float s = scale_value(sb), rs = recip_or_zero(s);
-                const int at = hw * (kN / 16) + g;  // place among the lane's scale bytes
-                if (at < 4) scales |= sb << (8 * at);
-                else scales2 |= sb << (8 * (at - 4));
+    for (int hw = 0; hw < 2; ++hw)
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    codes[hw][2 * g + q] = code_byte(w[4 * q], inv_unit, s, rs) | code_byte(w[4 * q + 1], inv_unit, s, rs) << 8 |
-                                           code_byte(w[4 * q + 2], inv_unit, s, rs) << 16 |
-                                           code_byte(w[4 * q + 3], inv_unit, s, rs) << 24;
-            }
+        for (int g = 0; g < kN / 16; ++g) {
+            const uint32_t w[8] = {x[hw][2 * g].x, x[hw][2 * g].y, x[hw][2 * g].z, x[hw][2 * g].w,
+                                   x[hw][2 * g + 1].x, x[hw][2 * g + 1].y, x[hw][2 * g + 1].z, x[hw][2 * g + 1].w};
+            const uint32_t sb = scale_byte(amax_bits(w, 8), inv_unit);
+            const float s = scale_value(sb), rs = recip_or_zero(s);
+            const int at = hw * (kN / 16) + g;  // place among the lane's scale bytes
+            scales[at / 4] |= sb << (8 * (at % 4));
+            codes[hw][2 * g] = code_word(w, inv_unit, s, rs);
+            codes[hw][2 * g + 1] = code_word(w + 4, inv_unit, s, rs);
         }
 #pragma unroll
-        for (int quad = 0; quad < D / 64; ++quad) {
-            // word s of the quad: four columns of token r (low half), the same of token r + 8
-            uint32_t o[4];
+    for (int quad = 0; quad < D / 64; ++quad) {
+        // word s of the quad: four columns of token r (low half), the same of token r + 8
+        uint32_t o[4];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const uint32_t a = codes[0][2 * quad + s / 2], b = codes[1][2 * quad + s / 2];
-                o[s] = __byte_perm(a, b, s % 2 ? 0x7632 : 0x5410);
-            }
-            *reinterpret_cast<uint4*>(block + quad * 512 + lane * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        unsigned char* sc = block + KvPlace<D>::kKeyScales + lane * (D / 32);
-        if constexpr (D == 64) *reinterpret_cast<uint16_t*>(sc) = static_cast<uint16_t>(scales);
-        else if constexpr (D == 128) *reinterpret_cast<uint32_t*>(sc) = scales;
-        else *reinterpret_cast<uint2*>(sc) = make_uint2(scales, scales2);
+        for (int s = 0; s < 4; ++s)
+            o[s] = __byte_perm(codes[0][2 * quad + s / 2], codes[1][2 * quad + s / 2], s % 2 ? 0x7632 : 0x5410);
+        *reinterpret_cast<uint4*>(block + quad * 512 + lane * 16) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    {
-        constexpr int kN = D / 8;
-        const float inv_unit = 1.0f / p.s.v_unit;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.v_in) + i * p.v_stride +
-                                   static_cast<long long>(h) * D + r * kN;
-        uint32_t codes[4][kN / 8];
-        uint32_t scales[(kN + 15) / 16] = {};
+    unsigned char* sc = block + KvPlace<D>::kKeyScales + lane * (D / 32);
+    if constexpr (D == 64) *reinterpret_cast<uint16_t*>(sc) = static_cast<uint16_t>(scales[0]);
+    else if constexpr (D == 128) *reinterpret_cast<uint32_t*>(sc) = scales[0];
+    else *reinterpret_cast<uint2*>(sc) = make_uint2(scales[0], scales[1]);
+}
+
+template <int D>
+__device__ __forceinline__ void write_value_block(const KvArgs& p, long long i, int h, unsigned char* block, int lane) {
+    constexpr int kN = D / 8;
+    constexpr int kG = (kN + 15) / 16;  // groups a lane (D = 64: half a group)
+    const int r = lane / 4, c = lane % 4;
+    const float inv_unit = 1.0f / p.s.v_unit;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.v_in) + i * p.v_stride + static_cast<long long>(h) * D + r * kN;
+    uint4 x[4][kN / 8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < kN / 8; ++e)
+            x[j][e] = __ldcs(reinterpret_cast<const uint4*>(src + (2 * c + j % 2 + 8 * (j / 2)) * p.v_stride) + e);
+    uint32_t codes[4][kN / 8];
+    uint32_t scales[kG] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+            constexpr int kWords = kN < 16 ? 4 : 8;
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < kWords / 4; ++e) {
+                w[4 * e] = x[j][2 * g + e].x;
+                w[4 * e + 1] = x[j][2 * g + e].y;
+                w[4 * e + 2] = x[j][2 * g + e].z;
+                w[4 * e + 3] = x[j][2 * g + e].w;
+            }
+            uint32_t m = amax_bits(w, kWords);
+            if constexpr (D == 64) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));  // the group is shared by r and r ^ 1
+            const uint32_t sb = scale_byte(m, inv_unit);
+            const float s = scale_value(sb), rs = recip_or_zero(s);
+            scales[g] |= sb << (8 * j);
+#pragma unroll
+            for (int e = 0; e < kWords / 4; ++e) codes[j][2 * g + e] = code_word(w + 4 * e, inv_unit, s, rs);
+        }
+#pragma unroll
+    for (int quad = 0; quad < D / 64; ++quad) {
+        // word m: byte j holds columns 2m, 2m + 1 of token j
+        uint32_t o[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const uint32_t lo = __byte_perm(codes[0][quad], codes[1][quad], m | (m + 4) << 4);
+            const uint32_t hi = __byte_perm(codes[2][quad], codes[3][quad], m | (m + 4) << 4);
+            o[m] = __byte_perm(lo, hi, 0x5410);
+        }
+        *reinterpret_cast<uint4*>(block + KvPlace<D>::kValueCodes + quad * 512 + lane * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    unsigned char* sc = block + KvPlace<D>::kValueScales;
+    if constexpr (D == 64) {
+        if (r % 2 == 0) *reinterpret_cast<uint32_t*>(sc + (r / 2 * 4 + c) * 4) = scales[0];
+    } else {
+#pragma unroll
+        for (int g = 0; g < kG; ++g) *reinterpret_cast<uint32_t*>(sc + ((r * kG + g) * 4 + c) * 4) = scales[g];
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void read_key_block(const KvArgs& p, long long i, int h, const unsigned char* block, int lane) {
+    constexpr int kN = D / 4;
+    const int r = lane / 4, c = lane % 4;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.k_out) + i * p.k_stride + static_cast<long long>(h) * D + c * kN;
+    const unsigned char* sc = block + KvPlace<D>::kKeyScales + lane * (D / 32);
+    uint4 v[D / 64];
+    uint32_t s0[D / 64], s1[D / 64];
+#pragma unroll
+    for (int quad = 0; quad < D / 64; ++quad) {
+        v[quad] = __ldcs(reinterpret_cast<const uint4*>(block + quad * 512 + lane * 16));
+        s0[quad] = sc[quad];
+        s1[quad] = sc[D / 64 + quad];
+    }
+#pragma unroll
+    for (int quad = 0; quad < D / 64; ++quad) {
+        const uint32_t w[4] = {v[quad].x, v[quad].y, v[quad].z, v[quad].w};
+        const uint32_t f0 = both(s0[quad]), f1 = both(s1[quad]);
+        uint32_t a[8], b[8];  // 16 columns of tokens r and r + 8
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            uint32_t x0, x1, x2, x3;
+            e2m1_word_to_f16(w[s], x0, x1, x2, x3);
+            a[2 * s] = f16x2_to_bf16x2(mul_f16x2(x0, f0), p.s.k_unit);
+            a[2 * s + 1] = f16x2_to_bf16x2(mul_f16x2(x1, f0), p.s.k_unit);
+            b[2 * s] = f16x2_to_bf16x2(mul_f16x2(x2, f1), p.s.k_unit);
+            b[2 * s + 1] = f16x2_to_bf16x2(mul_f16x2(x3, f1), p.s.k_unit);
+        }
+        uint4* ra = reinterpret_cast<uint4*>(dst + r * p.k_stride + quad * 16);
+        uint4* rb = reinterpret_cast<uint4*>(dst + (r + 8) * p.k_stride + quad * 16);
+        __stcs(ra, make_uint4(a[0], a[1], a[2], a[3]));
+        __stcs(ra + 1, make_uint4(a[4], a[5], a[6], a[7]));
+        __stcs(rb, make_uint4(b[0], b[1], b[2], b[3]));
+        __stcs(rb + 1, make_uint4(b[4], b[5], b[6], b[7]));
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void read_value_block(const KvArgs& p, long long i, int h, const unsigned char* block, int lane) {
+    constexpr int kN = D / 8;
+    const int r = lane / 4, c = lane % 4;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.v_out) + i * p.v_stride + static_cast<long long>(h) * D + r * kN;
+    const unsigned char* sc = block + KvPlace<D>::kValueScales;
+    uint4 v[D / 64];
+    uint32_t s4[D / 64];
+#pragma unroll
+    for (int quad = 0; quad < D / 64; ++quad) {
+        v[quad] = __ldcs(reinterpret_cast<const uint4*>(block + KvPlace<D>::kValueCodes + quad * 512 + lane * 16));
+        s4[quad] = *reinterpret_cast<const uint32_t*>(sc + ((r * kN + quad * 8) / 16 * 4 + c) * 4);
+    }
+#pragma unroll
+    for (int quad = 0; quad < D / 64; ++quad) {
+        const uint32_t w[4] = {v[quad].x, v[quad].y, v[quad].z, v[quad].w};
+        uint32_t o[4][4];  // token j, 8 columns
+#pragma unroll
+        for (int m = 0; m < 4; ++m) e2m1_word_to_f16(w[m], o[0][m], o[1][m], o[2][m], o[3][m]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            const uint32_t s = both(s4[quad] >> (8 * j) & 0xFFu);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) o[j][m] = f16x2_to_bf16x2(mul_f16x2(o[j][m], s), p.s.v_unit);
             const int t = 2 * c + j % 2 + 8 * (j / 2);
-            const uint4* row = reinterpret_cast<const uint4*>(src + t * p.v_stride);
-            uint4 x[kN / 8];
-#pragma unroll
-            for (int e = 0; e < kN / 8; ++e) x[e] = __ldcs(row + e);
-            if constexpr (D == 64) {
-                const uint32_t w[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
-                uint32_t m = amax_bits(w, 4);
-                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));  // the 16 columns are shared by rows r and r ^ 1
-                const uint32_t sb = scale_byte(m, inv_unit);
-                const float s = scale_value(sb), rs = recip_or_zero(s);
-                scales[0] |= sb << (8 * j);
-                codes[j][0] = code_byte(w[0], inv_unit, s, rs) | code_byte(w[1], inv_unit, s, rs) << 8 |
-                              code_byte(w[2], inv_unit, s, rs) << 16 | code_byte(w[3], inv_unit, s, rs) << 24;
-            } else {
-#pragma unroll
-                for (int g = 0; g < kN / 16; ++g) {
-                    const uint32_t w[8] = {x[2 * g].x, x[2 * g].y, x[2 * g].z, x[2 * g].w,
-                                           x[2 * g + 1].x, x[2 * g + 1].y, x[2 * g + 1].z, x[2 * g + 1].w};
-                    const uint32_t sb = scale_byte(amax_bits(w, 8), inv_unit);
-                    const float s = scale_value(sb), rs = recip_or_zero(s);
-                    scales[g] |= sb << (8 * j);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        codes[j][2 * g + q] =
-                            code_byte(w[4 * q], inv_unit, s, rs) | code_byte(w[4 * q + 1], inv_unit, s, rs) << 8 |
-                            code_byte(w[4 * q + 2], inv_unit, s, rs) << 16 | code_byte(w[4 * q + 3], inv_unit, s, rs) << 24;
-                }
-            }
-        }
-#pragma unroll
-        for (int quad = 0; quad < D / 64; ++quad) {
-            // word m: byte j holds columns 2m, 2m + 1 of token j
-            uint32_t o[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const uint32_t lo = __byte_perm(codes[0][quad], codes[1][quad], m | (m + 4) << 4);
-                const uint32_t hi = __byte_perm(codes[2][quad], codes[3][quad], m | (m + 4) << 4);
-                o[m] = __byte_perm(lo, hi, 0x5410);
-            }
-            *reinterpret_cast<uint4*>(block + KvPlace<D>::kValueCodes + quad * 512 + lane * 16) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        unsigned char* sc = block + KvPlace<D>::kValueScales;
-        if constexpr (D == 64) {
-            if (r % 2 == 0) *reinterpret_cast<uint32_t*>(sc + (r / 2 * 4 + c) * 4) = scales[0];
-        } else {
-#pragma unroll
-            for (int g = 0; g < kN / 16; ++g)
-                *reinterpret_cast<uint32_t*>(sc + ((r * (kN / 16) + g) * 4 + c) * 4) = scales[g];
+            __stcs(reinterpret_cast<uint4*>(dst + t * p.v_stride + quad * 8), make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]));
         }
     }
 }
 
-template <int D>
-__device__ __forceinline__ void read_block(const KvArgs& p, long long i, int h, const unsigned char* block, int lane) {
-    const int r = lane / 4, c = lane % 4;
-    if (p.k_out) {
-        constexpr int kN = D / 4;
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.k_out) + i * p.k_stride + static_cast<long long>(h) * D + c * kN;
-        const unsigned char* sc = block + KvPlace<D>::kKeyScales + lane * (D / 32);
-#pragma unroll
-        for (int quad = 0; quad < D / 64; ++quad) {
-            const uint4 v = __ldcs(reinterpret_cast<const uint4*>(block + quad * 512 + lane * 16));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            const uint32_t s0 = both(sc[quad]), s1 = both(sc[D / 64 + quad]);
-            uint32_t a[8], b[8];  // 16 columns of tokens r and r + 8
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                uint32_t x0, x1, x2, x3;
-                e2m1_word_to_f16(w[s], x0, x1, x2, x3);
-                a[2 * s] = f16x2_to_bf16x2(mul_f16x2(x0, s0), p.s.k_unit);
-                a[2 * s + 1] = f16x2_to_bf16x2(mul_f16x2(x1, s0), p.s.k_unit);
-                b[2 * s] = f16x2_to_bf16x2(mul_f16x2(x2, s1), p.s.k_unit);
-                b[2 * s + 1] = f16x2_to_bf16x2(mul_f16x2(x3, s1), p.s.k_unit);
-            }
-            uint4* ra = reinterpret_cast<uint4*>(dst + r * p.k_stride + quad * 16);
-            uint4* rb = reinterpret_cast<uint4*>(dst + (r + 8) * p.k_stride + quad * 16);
-            __stcs(ra, make_uint4(a[0], a[1], a[2], a[3]));
-            __stcs(ra + 1, make_uint4(a[4], a[5], a[6], a[7]));
-            __stcs(rb, make_uint4(b[0], b[1], b[2], b[3]));
-            __stcs(rb + 1, make_uint4(b[4], b[5], b[6], b[7]));
-        }
-    }
-    if (p.v_out) {
-        constexpr int kN = D / 8;
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.v_out) + i * p.v_stride + static_cast<long long>(h) * D + r * kN;
-        const unsigned char* sc = block + KvPlace<D>::kValueScales;
-#pragma unroll
-        for (int quad = 0; quad < D / 64; ++quad) {
-            const uint4 v = __ldcs(reinterpret_cast<const uint4*>(block + KvPlace<D>::kValueCodes + quad * 512 + lane * 16));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            const uint32_t s4 = *reinterpret_cast<const uint32_t*>(sc + ((r * kN + quad * 8) / 16 * 4 + c) * 4);
-            uint32_t o[4][4];  // token j, 8 columns
-#pragma unroll
-            for (int m = 0; m < 4; ++m) e2m1_word_to_f16(w[m], o[0][m], o[1][m], o[2][m], o[3][m]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t s = both(s4 >> (8 * j) & 0xFFu);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) o[j][m] = f16x2_to_bf16x2(mul_f16x2(o[j][m], s), p.s.v_unit);
-                const int t = 2 * c + j % 2 + 8 * (j / 2);
-                __stcs(reinterpret_cast<uint4*>(dst + t * p.v_stride + quad * 8), make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]));
-            }
-        }
-    }
-}
-
-// One warp takes 16 tokens of the call and one head; gridDim.y parts share a group's tokens when there are few
+// One warp takes 16 tokens of the call and the keys or the values of one head; gridDim.y parts share a group's tokens when there are few
 // groups. Warps are independent: each reads the slots of its group and of the 15 tokens on either side, lane j
 // those at j and j + 32 of this window (token i0 - 15 + j).
 template <int D, bool kRead>
@@ -337,10 +326,12 @@ __global__ void __launch_bounds__(kThreads) kv_move_kernel(const KvArgs p) {
     const int lane = static_cast<int>(threadIdx.x) % 32;
     const int heads = p.s.heads;
     const long long item = static_cast<long long>(blockIdx.x) * kWarps + threadIdx.x / 32;
-    const long long group = item / heads;
-    const int h = static_cast<int>(item - group * heads);
+    const bool keys = (item & 1) == 0;
+    const long long group = item / 2 / heads;
+    const int h = static_cast<int>(item / 2 - group * heads);
     const long long i0 = group * kGroup;
     if (i0 >= p.n) return;
+    if (kRead && !(keys ? p.k_out : p.v_out)) return;
     const long long cap = static_cast<long long>(p.s.pages) << p.s.page_shift;
     long long s[2];
 #pragma unroll
@@ -375,20 +366,34 @@ __global__ void __launch_bounds__(kThreads) kv_move_kernel(const KvArgs p) {
     if (here != 0 && blockIdx.y == 0) {
         const int j = kGroup - 1 + __ffs(here) - 1;
         const long long slot = __shfl_sync(0xFFFFFFFFu, s[0], j);  // j <= 30
-        if constexpr (kRead) read_block<D>(p, i0 + j - (kGroup - 1), h, block_of(slot), lane);
-        else write_block<D>(p, i0 + j - (kGroup - 1), h, block_of(slot), lane);
+        const long long i = i0 + j - (kGroup - 1);
+        unsigned char* block = block_of(slot);
+        if constexpr (kRead) {
+            if (keys) read_key_block<D>(p, i, h, block, lane);
+            else read_value_block<D>(p, i, h, block, lane);
+        } else {
+            if (keys) write_key_block<D>(p, i, h, block, lane);
+            else write_value_block<D>(p, i, h, block, lane);
+        }
     }
-    // the tokens of this group that no run has
-    for (int x = static_cast<int>(blockIdx.y); x < kGroup; x += static_cast<int>(gridDim.y)) {
-        const int j = kGroup - 1 + x;
-        if (i0 + x >= p.n) break;
+    // the tokens of this group that no run has, kSide of them at a time
+    constexpr int kSide = 32 / (D / 8);
+    for (int x0 = static_cast<int>(blockIdx.y) * kSide; x0 < kGroup; x0 += static_cast<int>(gridDim.y) * kSide) {
+        const int x = x0 + lane / (D / 8), j = kGroup - 1 + x;
         const long long slot = __shfl_sync(0xFFFFFFFFu, s[0], j);
         const int t = slot < 0 ? 0 : static_cast<int>(slot % kGroup);
-        if (slot >= 0 && (run >> (j - t) & 1u)) continue;
+        const bool mine = i0 + x < p.n && !(slot >= 0 && (run >> (j - t) & 1u));
+        if (!__any_sync(0xFFFFFFFFu, mine)) continue;
         if constexpr (kRead) {
-            read_token<D>(p, i0 + x, h, slot < 0 ? nullptr : block_of(slot), t, lane);
+            if (!mine) continue;
+            const unsigned char* block = slot < 0 ? nullptr : block_of(slot);
+            if (keys) read_token<D, true>(p, i0 + x, h, block, t, lane);
+            else read_token<D, false>(p, i0 + x, h, block, t, lane);
         } else {
-            if (slot >= 0) write_token<D>(p, i0 + x, h, block_of(slot), t, lane);
+            const bool active = mine && slot >= 0;
+            unsigned char* block = active ? block_of(slot) : nullptr;
+            if (keys) write_token<D, true>(p, active, i0 + x, h, block, t, lane);
+            else write_token<D, false>(p, active, i0 + x, h, block, t, lane);
         }
     }
 }
@@ -398,12 +403,13 @@ int launch_move(const KvArgs& a, cudaStream_t stream) {
     if (a.n <= 0) return 0;
     const int sms = attn_sm_count();
     if (sms == 0) return -7;
-    const long long items = (a.n + kGroup - 1) / kGroup * a.s.heads;
+    const long long items = (a.n + kGroup - 1) / kGroup * a.s.heads * 2;
     const long long blocks = (items + kWarps - 1) / kWarps;
     if (blocks > 0x7FFFFFFFLL) return -7;
-    // few groups (decode, short prompts): spread the tokens of each, down to one token and head a warp
+    // few groups (decode, short prompts): spread the tokens of each, down to as many as a warp takes side by side
     long long parts = (2LL * sms + blocks - 1) / blocks;
-    if (parts > kGroup) parts = kGroup;
+    const long long most = kGroup * a.s.dim / 256;
+    if (parts > most) parts = most;
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(parts));
     switch (a.s.dim) {
         case 64: kv_move_kernel<64, kRead><<<grid, kThreads, 0, stream>>>(a); break;
