@@ -2,10 +2,14 @@
 // byte layout: include/hc.h).
 //
 // Each 16 columns of a token's head share the scale s = e4m3(amax / (6 unit)), and a code is
-// e2m1(x / (s unit)). Both are decided exactly: x has 8 significant bits, s 4 and a border between two
-// codes 3, so a quotient x / s either is a border exactly or is off it by 2^-9 relative and more. The
-// quotient is taken as x * (1/s) and one residual step (v + (x - v s) / s, the classical correction of
-// a quotient by its remainder), which is exact whenever the quotient has few bits: ties are seen as ties.
+// e2m1(x / (s unit)). Both are decided exactly.
+//   The code: borders b between two codes are 0.25, 0.75, 1.25, 1.75, 2.5, 3.5 and 5. x has 8 significant bits and
+//   b s at most 7, so |x - b s| is 0 or at least x / 256, and the quotient q = x / s is a border exactly or at least
+//   2^-10 away from one. x * (1/s) with the hardware's reciprocal (1 ulp) is off by less than 2^-19 for q up to 8; adding
+//   and taking away 1.5 * 2^11 rounds it to a multiple of 2^-12, which puts a border on itself and leaves the others on
+//   their side. (Above 8 all is the largest code.) The sign is put back from x, for the zeros.
+//   The scale: amax / 6 is taken as amax * (1/6) and one residual step (v + (a - 6 v) / 6, the classical correction of
+//   a quotient by its remainder), exact where the quotient has few bits, so that ties between two scales are seen as ties.
 //
 // The layout is the one that the attention's matrix instructions read, so the bytes of one token are
 // scattered in 1- and 2-byte pieces over its block of 16 tokens. A warp takes 16 tokens of the call and the keys or
@@ -24,6 +28,7 @@
 
 #include "hc_attn.h"
 #include "hc_kv.cuh"
+#include "hc_ptx.cuh"
 
 namespace hc {
 namespace {
@@ -44,7 +49,11 @@ __device__ __forceinline__ uint32_t amax_bits(const uint32_t* w, int words) {
 
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax, float inv_unit) {
     if (amax >= 0x7F80u) return 0x7Fu;  // NaN or infinity in the group
-    const float q = __fdiv_rn(__uint_as_float(amax << 16) * inv_unit, 6.0f);
+    const float a = __uint_as_float(amax << 16) * inv_unit;
+    constexpr float kSixth = 1.0f / 6.0f;
+    float q = a * kSixth;
+    q = fmaf(fmaf(-6.0f, q, a), kSixth, q);
+    if (!(a < 1e30f)) q = a;  // far above the largest scale; infinity has no remainder
     uint16_t two;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(q));
     return two & 0xFFu;
@@ -55,23 +64,31 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
 }
 
-// one bf16 pair (the even column in the low half) -> a byte of two codes
-__device__ __forceinline__ uint32_t code_byte(uint32_t pair, float inv_unit, float s, float rs) {
-    const float a = __uint_as_float(pair << 16) * inv_unit, b = __uint_as_float(pair & 0xFFFF0000u) * inv_unit;
-    float u = a * rs, v = b * rs;
-    // beyond 8 the code is the largest whatever the quotient's last bits (and an infinite one has no remainder)
-    if (fabsf(u) < 8.f) u = fmaf(fmaf(-u, s, a), rs, u);
-    if (fabsf(v) < 8.f) v = fmaf(fmaf(-v, s, b), rs, v);
+// 1 / (s unit), 0 for the scale 0
+__device__ __forceinline__ float recip_or_zero(float s, float inv_unit) { return s > 0.f ? rcp_approx(s) * inv_unit : 0.f; }
+
+// four bf16 pairs (the even column in the low half) -> four bytes of two codes
+__device__ __forceinline__ uint32_t code_word(const uint32_t* w, float rs) {
+    constexpr float kGrid = 0x1.8p11f;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float a = __uint_as_float(w[e] << 16), b = __uint_as_float(w[e] & 0xFFFF0000u);
+        const float u = fmaf(fabsf(a), rs, kGrid) - kGrid, t = fmaf(fabsf(b), rs, kGrid) - kGrid;
+        v[2 * e] = copysignf(u, a);
+        v[2 * e + 1] = copysignf(t, b);
+    }
     uint32_t r;
-    asm("{\n\t.reg .b8 c;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\t"
-        "cvt.u32.u8 %0, c;\n\t}"
+    asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c3, %8, %7;\n\t"
+        "mov.b32 %0, {c0, c1, c2, c3};\n\t}"
         : "=r"(r)
-        : "f"(v), "f"(u));
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return r;
 }
-
-__device__ __forceinline__ float recip_or_zero(float s) { return s > 0.f ? __frcp_rn(s) : 0.f; }
 
 // ---- eight columns of one token a lane (token-wise) -----------------------------------------------
 // 32 / (D / 8) tokens side by side in a warp; all lanes come here (the scale is exchanged between two).
@@ -90,20 +107,17 @@ __device__ __forceinline__ void write_token(const KvArgs& p, bool active, long l
     m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     const float inv_unit = 1.0f / (kKeys ? p.s.k_unit : p.s.v_unit);  // exact: a power of two
     const uint32_t sb = scale_byte(m, inv_unit);
-    const float s = scale_value(sb), rs = recip_or_zero(s);
-    uint32_t b[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) b[e] = code_byte(w[e], inv_unit, s, rs);
+    const uint32_t codes = code_word(w, recip_or_zero(scale_value(sb), inv_unit));
     if (!active) return;
     if constexpr (kKeys) {
         unsigned char* dst = block + KvPlace<D>::key_code(t, col);
-        *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(b[0] | b[1] << 8);
-        *reinterpret_cast<uint16_t*>(dst + 4) = static_cast<uint16_t>(b[2] | b[3] << 8);
+        *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(codes);
+        *reinterpret_cast<uint16_t*>(dst + 4) = static_cast<uint16_t>(codes >> 16);
         if (lane % 2 == 0) block[KvPlace<D>::key_scale(t, col)] = static_cast<unsigned char>(sb);
     } else {
         unsigned char* dst = block + KvPlace<D>::value_code(t, col);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dst[4 * e] = static_cast<unsigned char>(b[e]);
+        for (int e = 0; e < 4; ++e) dst[4 * e] = static_cast<unsigned char>(codes >> (8 * e));
         if (lane % 2 == 0) block[KvPlace<D>::value_scale(t, col)] = static_cast<unsigned char>(sb);
     }
 }
@@ -148,11 +162,6 @@ __device__ __forceinline__ void read_token(const KvArgs& p, long long i, int h, 
 // Lane (r, c) = (lane / 4, lane % 4). Keys: tokens r and r + 8, columns [c D/4, (c+1) D/4). Values: tokens
 // 2c, 2c+1, 2c+8, 2c+9, columns [r D/8, (r+1) D/8).
 
-__device__ __forceinline__ uint32_t code_word(const uint32_t* w, float inv_unit, float s, float rs) {
-    return code_byte(w[0], inv_unit, s, rs) | code_byte(w[1], inv_unit, s, rs) << 8 | code_byte(w[2], inv_unit, s, rs) << 16 |
-           code_byte(w[3], inv_unit, s, rs) << 24;
-}
-
 template <int D>
 __device__ __forceinline__ void write_key_block(const KvArgs& p, long long i, int h, unsigned char* block, int lane) {
     constexpr int kN = D / 4;  // columns a lane
@@ -173,11 +182,11 @@ __device__ __forceinline__ void write_key_block(const KvArgs& p, long long i, in
             const uint32_t w[8] = {x[hw][2 * g].x, x[hw][2 * g].y, x[hw][2 * g].z, x[hw][2 * g].w,
                                    x[hw][2 * g + 1].x, x[hw][2 * g + 1].y, x[hw][2 * g + 1].z, x[hw][2 * g + 1].w};
             const uint32_t sb = scale_byte(amax_bits(w, 8), inv_unit);
-            const float s = scale_value(sb), rs = recip_or_zero(s);
+            const float rs = recip_or_zero(scale_value(sb), inv_unit);
             const int at = hw * (kN / 16) + g;  // place among the lane's scale bytes
             scales[at / 4] |= sb << (8 * (at % 4));
-            codes[hw][2 * g] = code_word(w, inv_unit, s, rs);
-            codes[hw][2 * g + 1] = code_word(w + 4, inv_unit, s, rs);
+            codes[hw][2 * g] = code_word(w, rs);
+            codes[hw][2 * g + 1] = code_word(w + 4, rs);
         }
 #pragma unroll
     for (int quad = 0; quad < D / 64; ++quad) {
@@ -225,10 +234,10 @@ __device__ __forceinline__ void write_value_block(const KvArgs& p, long long i, 
             uint32_t m = amax_bits(w, kWords);
             if constexpr (D == 64) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));  // the group is shared by r and r ^ 1
             const uint32_t sb = scale_byte(m, inv_unit);
-            const float s = scale_value(sb), rs = recip_or_zero(s);
+            const float rs = recip_or_zero(scale_value(sb), inv_unit);
             scales[g] |= sb << (8 * j);
 #pragma unroll
-            for (int e = 0; e < kWords / 4; ++e) codes[j][2 * g + e] = code_word(w + 4 * e, inv_unit, s, rs);
+            for (int e = 0; e < kWords / 4; ++e) codes[j][2 * g + e] = code_word(w + 4 * e, rs);
         }
 #pragma unroll
     for (int quad = 0; quad < D / 64; ++quad) {
