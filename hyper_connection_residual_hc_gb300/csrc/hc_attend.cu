@@ -20,7 +20,7 @@
 // relative 2^-12 on average weights, well below the bf16 rounding of the result.
 //
 // Work. All the (sequence, kv head, tile of rows) segments of a call, each so many units of 32 tokens, are laid
-// end to end and cut into equal ranges, one a CTA, whatever the lengths. The 8 warps of a CTA take its units in
+// end to end and cut into equal ranges, one a CTA, whatever the lengths. The warps of a CTA take its units in
 // turn, each with a ring of cache blocks of its own, filled by bulk copies that the warp issues ahead; they join
 // at the end of a segment. A segment cut between CTAs leaves partial results in the workspace, and the CTA that
 // finishes last joins them in their order: the result does not depend on timing.
@@ -42,19 +42,23 @@ namespace {
 
 __device__ unsigned int g_hc_attention_error = 0;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr uint64_t kWaitNs = 1000000000ull;   // 1 s
 constexpr int kUnit = 32;                     // tokens a warp takes at a time: two cache blocks
-constexpr int kMinUnits = kWarps;             // a CTA's smallest share: one unit a warp
+constexpr int kWholeSteps = 4;                // segments of at most so many units a warp are not cut (see the kernel)
 constexpr int kMaxDevices = 64;
 constexpr long long kTilesFromRows = 128;     // rows of the longest sequence from which hc_attend_tiles.cu takes a call
 
-// Stages of a warp's ring (a power of two of them, one unit each), CTAs per SM.
+// Warps, CTAs per SM, stages of a warp's ring (a power of two of them, one unit each). 8 rows of up to 128 columns leave 128
+// registers a thread, 16 warps an SM, in CTAs of 8; more rows or columns take up to 255, 8 warps an SM, better as two
+// CTAs of 4 whose joins and waits overlap than as one of 8 (drafts of 5 queries, 20 rows a tile: 72 against 84 us; with
+// 8 rows it is the other way round, 255 against 221 us for 256 sequences: more parts to join).
 template <int D, int kNT>
 struct Plan {
-    static constexpr int kCtas = kNT == 1 && D <= 128 ? 2 : 1;
-    static constexpr int kLogStages = D == 256 || kCtas == 2 && D == 128 ? 1 : 2;
+    static constexpr bool kSmall = kNT == 1 && D <= 128;
+    static constexpr int kWarps = kSmall ? 8 : 4;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kCtas = 2;
+    static constexpr int kLogStages = D == 256 || (kSmall && D == 128) ? 1 : 2;
     static constexpr int kStages = 1 << kLogStages;
     static constexpr int kStage = kUnit / 16 * kv_block_bytes(D);
     static constexpr int kRing = kWarps * kStages * kStage;
@@ -140,8 +144,9 @@ struct Segment {
 };
 
 template <int D, int kNT>
-__global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_kernel(const AttArgs p) {
+__global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) attend_rows_kernel(const AttArgs p) {
     using P = Plan<D, kNT>;
+    constexpr int kWarps = P::kWarps, kThreads = P::kThreads;
     constexpr int R = 8 * kNT;
     constexpr int kKeySteps = D / 16;  // MMAs over a key's columns; also the 16-column tiles of the output
     constexpr int kBlock = kv_block_bytes(D);
@@ -160,52 +165,73 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
     fence_mbar_init();
 
     // ---- this CTA's range of the call's units ----------------------------------------------------------
-    long long mine = 0;
-    for (int b = tid; b < p.seqs; b += kThreads) mine += Work<R>(p, load_seq(p, b, blockIdx.x == 0 ? &g_hc_attention_error : nullptr), group).total(heads);
-    long long total = mine;
+    auto block_scan = [&](long long v, long long& sum) {  // inclusive, over the block's threads
+        long long x = v;
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    if (lane == 0) scan[warp] = total;
-    __syncthreads();
-    total = 0;
+        for (int o = 1; o < 32; o *= 2) {
+            const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = x;
+        __syncthreads();
+        sum = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += scan[w];
-    const long long want = (total + kMinUnits - 1) / kMinUnits;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) x += scan[w];
+            sum += scan[w];
+        }
+        return x;
+    };
+    // A sequence's segments, and its units where segments may be cut.
+    long long segments = 0, units = 0;
+    bool long_one = false;
+    for (int b = tid; b < p.seqs; b += kThreads) {
+        const Work<R> w(p, load_seq(p, b, blockIdx.x == 0 ? &g_hc_attention_error : nullptr), group);
+        segments += static_cast<long long>(w.tiles) * heads;
+        units += w.total(heads);
+        long_one |= w.tiles > 0 && w.units > kWholeSteps * kWarps;
+    }
+    long long total, all_segments;
+    const bool cut = __syncthreads_or(long_one);
+    long long x = block_scan(segments, all_segments);
+    // Short segments are left whole, one after the other: joining parts would cost more than the work. Not where that would
+    // leave some CTAs twice the others' share.
+    const bool whole_ones = !cut && (all_segments <= gridDim.x || all_segments >= 4LL * gridDim.x);
+    if (whole_ones) total = all_segments;
+    else x = block_scan(units, total);
+    const long long least = whole_ones ? 1 : kWarps;  // a CTA's smallest share: one unit a warp
+    const long long want = (total + least - 1) / least;
     const long long ctas = want < gridDim.x ? want : static_cast<long long>(gridDim.x);
     if (static_cast<long long>(blockIdx.x) >= ctas) return;
     long long at = total * blockIdx.x / ctas;
     const long long end = total * (blockIdx.x + 1) / ctas;
-    {
-        // the sequence that holds unit `at`: an inclusive scan over 256 sequences at a time
+    if (p.seqs <= kThreads) {
+        const long long v = whole_ones ? segments : units;
+        if (x > at && x - v <= at) {
+            found_seq = tid;
+            found_at = at - (x - v);
+        }
+    } else {
+        // the sequence that holds unit `at`, a scan of kThreads sequences at a time
         long long before = 0;
         for (int b0 = 0; b0 < p.seqs; b0 += kThreads) {
             const int b = b0 + tid;
-            const long long v = b < p.seqs ? Work<R>(p, load_seq(p, b, nullptr), group).total(heads) : 0;
-            long long x = v;
-#pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-                if (lane >= o) x += y;
+            long long v = 0, sum;
+            if (b < p.seqs) {
+                const Work<R> w(p, load_seq(p, b, nullptr), group);
+                v = whole_ones ? static_cast<long long>(w.tiles) * heads : w.total(heads);
             }
-            __syncthreads();
-            if (lane == 31) scan[warp] = x;
-            __syncthreads();
-            long long chunk = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) x += scan[w];
-                chunk += scan[w];
-            }
-            x += before;
-            if (x > at && x - v <= at) {
+            const long long y = block_scan(v, sum) + before;
+            if (y > at && y - v <= at) {
                 found_seq = b;
-                found_at = at - (x - v);
+                found_at = at - (y - v);
             }
-            before += chunk;
+            before += sum;
             if (before > at) break;  // the same in every thread
         }
-        __syncthreads();
     }
+    __syncthreads();
 
     Segment g = {};
     // the tile's bounds, from g.s, g.tile, g.u0 and g.u1
@@ -225,16 +251,16 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
         g.s = load_seq(p, g.b, nullptr);
         const Work<R> w(p, g.s, group);
         g.units = w.units;
-        const long long k = in / w.units;
-        g.u0 = static_cast<int>(in - k * w.units);
+        const long long k = whole_ones ? in : in / w.units;
+        g.u0 = whole_ones ? 0 : static_cast<int>(in - k * w.units);
         g.h = static_cast<int>(k / w.tiles);
         g.tile = static_cast<int>(k - static_cast<long long>(g.h) * w.tiles);
-        g.u1 = static_cast<int>(min(static_cast<long long>(w.units), g.u0 + (end - at)));
+        g.u1 = whole_ones ? w.units : static_cast<int>(min(static_cast<long long>(w.units), g.u0 + (end - at)));
         place();
     }
 
     // ---- the warp's stream of units ----------------------------------------------------------------------
-    // Step k of a segment takes unit warp + 8 k of the CTA's part: two cache blocks, one stage of the ring. The lanes look
+    // Step k of a segment takes unit warp + kWarps k of the CTA's part: two cache blocks, one stage of the ring. The lanes look
     // up the blocks of 16 steps at a time (page and address), lane j block j % 2 of step j / 2, and each issues its copy
     // when its step's turn comes.
     uint32_t uses = 0;                     // units before this segment's first: step k is use `uses` + k of the ring
@@ -508,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
 
         // ---- the next part's copies start before this one is joined ---------------------------------------
         const Segment done = g;
-        at += g.u1 - g.u0;
+        at += whole_ones ? 1 : g.u1 - g.u0;
         const bool more = at < end;
         if (more) {
             g.u0 = 0;
@@ -525,12 +551,12 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
                 }
             }
             g.units = Work<R>(p, g.s, group).units;
-            g.u1 = static_cast<int>(min(static_cast<long long>(g.units), end - at));
+            g.u1 = whole_ones ? g.units : static_cast<int>(min(static_cast<long long>(g.units), end - at));
             place();
             open();
         }
 
-        // ---- join the warps: 4 + 4, 2 + 2, 1 + 1 ---------------------------------------------------------
+        // ---- join the warps, in halves ---------------------------------------------------------
 #pragma unroll
         for (int t = 0; t < kNT; ++t)
 #pragma unroll
@@ -639,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, Plan<D, kNT>::kCtas) attend_rows_ker
             }
             __syncthreads();
             if (last_flag) {
-                // warp w takes parts w, w + 8, ... in their order, then the warps join as before
+                // warp w takes parts w, w + kWarps, ... in their order, then the warps join as before
 #pragma unroll
                 for (int t = 0; t < kNT; ++t)
 #pragma unroll
@@ -681,13 +707,13 @@ int launch_rows(const AttArgs& a, cudaStream_t stream) {
             int sms = 0, per_sm = 0;
             if (cudaFuncSetAttribute(attend_rows_kernel<D, kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem) != cudaSuccess ||
                 cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attend_rows_kernel<D, kNT>, kThreads, P::kSmem) != cudaSuccess ||
+                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attend_rows_kernel<D, kNT>, P::kThreads, P::kSmem) != cudaSuccess ||
                 sms < 1 || per_sm < 1)
                 return -7;
             ctas[dev] = sms * per_sm < kAttMaxCtas ? sms * per_sm : kAttMaxCtas;
         }
     }
-    attend_rows_kernel<D, kNT><<<static_cast<unsigned>(ctas[dev]), kThreads, P::kSmem, stream>>>(a);
+    attend_rows_kernel<D, kNT><<<static_cast<unsigned>(ctas[dev]), P::kThreads, P::kSmem, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? 0 : -7;
 }
 
