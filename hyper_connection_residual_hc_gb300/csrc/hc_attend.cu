@@ -48,25 +48,29 @@ constexpr int kWholeSteps = 4;                // segments of at most so many uni
 constexpr int kMaxDevices = 64;
 constexpr long long kTilesFromRows = 128;     // rows of the longest sequence from which hc_attend_tiles.cu takes a call
 
-// Warps, CTAs per SM, stages of a warp's ring (a power of two of them, one unit each). 8 rows of up to 128 columns leave 128
-// registers a thread, 16 warps an SM, in CTAs of 8; more rows or columns take up to 255, 8 warps an SM, better as two
-// CTAs of 4 whose joins and waits overlap than as one of 8 (drafts of 5 queries, 20 rows a tile: 72 against 84 us; with
-// 8 rows it is the other way round, 255 against 221 us for 256 sequences: more parts to join).
-template <int D, int kNT>
+// The shape of a CTA. A team of kSplit warps takes a unit at a time: alone (kSplit = 1), or two warps that share it, each
+// the scores of one of its two blocks and then half the output columns for both, the weights exchanged through
+// shared memory. Two halve the registers of the outputs, so that 16 warps an SM still fit with more rows or columns.
+template <int D, int kNT, int kSplit_>
 struct Plan {
-    static constexpr bool kSmall = kNT == 1 && D <= 128;
-    static constexpr int kWarps = kSmall ? 8 : 4;
+    static constexpr int kSplit = kSplit_;
+    static constexpr int kWarps = D == 256 ? 4 : 8;
+    static constexpr int kTeams = kWarps / kSplit;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kCtas = 2;
-    static constexpr int kLogStages = D == 256 || (kSmall && D == 128) ? 1 : 2;
+    static constexpr int kCtas = D == 256 ? (kSplit == 1 ? 2 : 3) : 2;
+    static constexpr int kLogStages = D == 64 ? 2 : 1;  // of a team's ring, one unit each
     static constexpr int kStages = 1 << kLogStages;
     static constexpr int kStage = kUnit / 16 * kv_block_bytes(D);
-    static constexpr int kRing = kWarps * kStages * kStage;
-    static constexpr int kStateFloats = D / 16 * kNT * 4 * 32;  // a warp's outputs
+    static constexpr int kRing = kTeams * kStages * kStage;
+    static constexpr int kTiles = D / 16 / kSplit;              // 16-column tiles of the output a warp
+    static constexpr int kStateFloats = kTiles * kNT * 4 * 32;  // a warp's outputs
     static constexpr int kMl = 2 * 8 * kNT;                     // its maxima and sums
     static constexpr int kMerge = kWarps / 2 * (kStateFloats + kMl) * 4;
-    static constexpr int kBars = kWarps * kStages * 8;
-    static constexpr int kSmem = kRing + kMerge + kBars;
+    static constexpr int kQ = kSplit == 1 ? 0 : kNT * (D / 16) * 32 * 8;            // the queries as B fragments
+    static constexpr int kWeights = kSplit == 1 ? 0 : kTeams * 2 * 2 * kNT * 2 * 128;  // [team][step parity][block][fragment]
+    static constexpr int kRows = kSplit == 1 ? 0 : (1 + 2 * kTeams) * 8 * kNT * 4;  // score factors; a team's exchange of maxima or sums
+    static constexpr int kBars = kTeams * kStages * 8;
+    static constexpr int kSmem = kRing + kMerge + kQ + kWeights + kRows + kBars;
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -96,6 +100,23 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
+}
+__device__ __forceinline__ void lds64(uint32_t a, uint32_t& x, uint32_t& y) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(a) : "memory");
+}
+// Barriers of a team's two warps (named barrier `id`).
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(static_cast<uint32_t>(x))
+        : "memory");
+    return r != 0;
 }
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
@@ -143,10 +164,11 @@ struct Segment {
     int first_block, end_block;  // this part's cache blocks
 };
 
-template <int D, int kNT>
-__global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) attend_rows_kernel(const AttArgs p) {
-    using P = Plan<D, kNT>;
-    constexpr int kWarps = P::kWarps, kThreads = P::kThreads;
+template <int D, int kNT, int kSplit>
+__global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, kSplit>::kCtas) attend_rows_kernel(const AttArgs p) {
+    using P = Plan<D, kNT, kSplit>;
+    constexpr int kWarps = P::kWarps, kThreads = P::kThreads, kTeams = P::kTeams, kTiles = P::kTiles;
+    constexpr int kOwn = 2 / kSplit;        // blocks of a unit whose scores a warp takes
     constexpr int R = 8 * kNT;
     constexpr int kKeySteps = D / 16;  // MMAs over a key's columns; also the 16-column tiles of the output
     constexpr int kBlock = kv_block_bytes(D);
@@ -158,11 +180,20 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
     const int tid = static_cast<int>(threadIdx.x), warp = tid / 32, lane = tid % 32;
     const int r = lane / 4, c = lane % 4;
     const int heads = p.s.heads, group = p.q_heads / heads;
-    const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * P::kStages * P::kStage);
+    const int team = warp / kSplit, part = warp % kSplit;
+    const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(team * P::kStages * P::kStage);
     float* merge = reinterpret_cast<float*>(smem + P::kRing);
-    const uint32_t bars = smem_u32(smem + P::kRing + P::kMerge) + static_cast<uint32_t>(warp * P::kStages * 8);
-    if (lane < P::kStages) mbar_init(bars + 8u * static_cast<uint32_t>(lane), 1);
+    const uint32_t queries = smem_u32(smem) + P::kRing + P::kMerge;
+    const uint32_t exchanged = queries + P::kQ + static_cast<uint32_t>(team * (P::kWeights / kTeams));
+    float* factors = reinterpret_cast<float*>(smem + P::kRing + P::kMerge + P::kQ + P::kWeights);
+    float* shared_rows = factors + R + team * 2 * R;  // [part][row]
+    const uint32_t bars = smem_u32(smem) + P::kSmem - P::kBars + static_cast<uint32_t>(team * P::kStages * 8);
+    if (part == 0 && lane < P::kStages) mbar_init(bars + 8u * static_cast<uint32_t>(lane), 1);
     fence_mbar_init();
+    auto team_sync = [&]() {
+        if constexpr (kSplit == 1) __syncwarp();
+        else pair_sync(1 + team);
+    };
 
     // ---- this CTA's range of the call's units ----------------------------------------------------------
     auto block_scan = [&](long long v, long long& sum) {  // inclusive, over the block's threads
@@ -190,7 +221,7 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
         const Work<R> w(p, load_seq(p, b, blockIdx.x == 0 ? &g_hc_attention_error : nullptr), group);
         segments += static_cast<long long>(w.tiles) * heads;
         units += w.total(heads);
-        long_one |= w.tiles > 0 && w.units > kWholeSteps * kWarps;
+        long_one |= w.tiles > 0 && w.units > kWholeSteps * kTeams;
     }
     long long total, all_segments;
     const bool cut = __syncthreads_or(long_one);
@@ -200,7 +231,7 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
     const bool whole_ones = !cut && (all_segments <= gridDim.x || all_segments >= 4LL * gridDim.x);
     if (whole_ones) total = all_segments;
     else x = block_scan(units, total);
-    const long long least = whole_ones ? 1 : kWarps;  // a CTA's smallest share: one unit a warp
+    const long long least = whole_ones ? 1 : kTeams;  // a CTA's smallest share: one unit a team
     const long long want = (total + least - 1) / least;
     const long long ctas = want < gridDim.x ? want : static_cast<long long>(gridDim.x);
     if (static_cast<long long>(blockIdx.x) >= ctas) return;
@@ -259,17 +290,17 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
         place();
     }
 
-    // ---- the warp's stream of units ----------------------------------------------------------------------
-    // Step k of a segment takes unit warp + kWarps k of the CTA's part: two cache blocks, one stage of the ring. The lanes look
+    // ---- the team's stream of units ----------------------------------------------------------------------
+    // Step k of a segment takes unit team + kTeams k of the CTA's part: two cache blocks, one stage of the ring. The lanes look
     // up the blocks of 16 steps at a time (page and address), lane j block j % 2 of step j / 2, and each issues its copy
-    // when its step's turn comes.
+    // when its step's turn comes (those of the team's first warp; the other warp keeps the same account).
     uint32_t uses = 0;                     // units before this segment's first: step k is use `uses` + k of the ring
     uint32_t there = 0;                    // of the 16 steps looked up: bit j: block j is there
     uint32_t staged = 0;                   // of the units in the ring: bits 2 st, 2 st + 1: the unit's blocks are there
     const unsigned char* where = nullptr;
     int steps = 0, issued = 0;
     auto look_up = [&](int k0) {
-        const int blk = g.first_block + 2 * (warp + kWarps * (k0 + lane / 2)) + lane % 2;
+        const int blk = g.first_block + 2 * (team + kTeams * (k0 + lane / 2)) + lane % 2;
         where = nullptr;
         if (blk < g.end_block && blk * 16 + 16 > g.lo) {
             const int tok = blk * 16;
@@ -287,7 +318,7 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
         const uint32_t st = (uses + static_cast<uint32_t>(k)) % P::kStages;
         const uint32_t here = there >> (2 * (k % 16)) & 3u;
         staged = (staged & ~(3u << (2 * st))) | here << (2 * st);
-        if (lane / 2 == k % 16) {
+        if (part == 0 && lane / 2 == k % 16) {
             const uint32_t bar = bars + 8 * st;
             if (lane % 2 == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(here) * kBlock));
             if (where) bulk_copy(ring + st * P::kStage + static_cast<uint32_t>(lane % 2 * kBlock), where, kBlock, bar);
@@ -295,7 +326,7 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
     };
     auto open = [&]() {  // start the copies of a new segment
         const int units_here = (g.end_block - g.first_block + 1) / 2;
-        steps = units_here > warp ? (units_here - warp + kWarps - 1) / kWarps : 0;
+        steps = units_here > team ? (units_here - team + kTeams - 1) / kTeams : 0;
         for (issued = 0; issued < steps && issued < P::kStages; ++issued) issue(issued);
     };
     __syncthreads();  // barriers ready
@@ -305,11 +336,12 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
         // ---- the tile's queries ----------------------------------------------------------------------------
         const int rows = g.s.ql * group, row0 = g.tile * R;
         const int pos0 = g.s.kvl - g.s.ql;
-        uint32_t qf[kNT][kKeySteps][2];
+        uint32_t qf[kSplit == 1 ? kNT : 1][kKeySteps][2];  // (kSplit = 2: in shared memory)
         float f[kNT][2];   // score factor (log2 units) of rows 2c, 2c + 1
         int see[kNT][2];   // keys below this position are seen (causal)
 #pragma unroll
         for (int t = 0; t < kNT; ++t) {
+            if (kSplit == 2 && t % kWarps != warp) continue;  // one warp makes a tile's fragments for all
             const int row = row0 + 8 * t + r;
             const bool real = row < rows;
             uint4 x[D / 32];
@@ -318,33 +350,52 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
                                        static_cast<long long>(g.h * group + (real ? row % group : 0)) * D + c * (D / 4);
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) x[e] = real ? __ldg(reinterpret_cast<const uint4*>(src) + e) : make_uint4(0, 0, 0, 0);
-            uint32_t m = 0;
+            uint32_t big = 0;
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) {
-                m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[e].x & 0x7FFF7FFFu, x[e].y & 0x7FFF7FFFu),
-                                         __vmaxu2(x[e].z & 0x7FFF7FFFu, x[e].w & 0x7FFF7FFFu)));
+                big = __vmaxu2(big, __vmaxu2(__vmaxu2(x[e].x & 0x7FFF7FFFu, x[e].y & 0x7FFF7FFFu),
+                                             __vmaxu2(x[e].z & 0x7FFF7FFFu, x[e].w & 0x7FFF7FFFu)));
             }
-            m = max(m & 0xFFFFu, m >> 16);
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            big = max(big & 0xFFFFu, big >> 16);
+            big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+            big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
             float up, down;
-            row_scale(m, up, down);
+            row_scale(big, up, down);
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) {
                 const uint32_t w[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+                uint32_t h[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    qf[t][2 * e + k / 2][k % 2] = pack_f16(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
+                for (int k = 0; k < 4; ++k) h[k] = pack_f16(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
+                if constexpr (kSplit == 1) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) qf[t][2 * e + k / 2][k % 2] = h[k];
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2)
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(queries + static_cast<uint32_t>(((t * kKeySteps + 2 * e + k / 2) * 32 + lane) * 8)),
+                                     "r"(h[k]), "r"(h[k + 1])
+                                     : "memory");
+                }
             }
             const float fr = p.scale * kLog2e * p.s.k_unit * down;
+            if constexpr (kSplit == 1) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) f[t][j] = __shfl_sync(0xFFFFFFFFu, fr, 4 * (2 * c + j));
+            } else {
+                if (c == 0) factors[8 * t + r] = fr;
+            }
+        }
+        if constexpr (kSplit == 2) __syncthreads();
+#pragma unroll
+        for (int t = 0; t < kNT; ++t)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                f[t][j] = __shfl_sync(0xFFFFFFFFu, fr, 4 * (2 * c + j));
+                if constexpr (kSplit == 2) f[t][j] = factors[8 * t + 2 * c + j];
                 const int col = row0 + 8 * t + 2 * c + j;
                 see[t][j] = p.causal ? (col < rows ? pos0 + col / group + 1 : 0x7FFFFFFF) : g.s.kvl;
             }
-        }
-        float m[kNT][2], l[kNT][2], o[kKeySteps][kNT][4];
+        float m[kNT][2], l[kNT][2], o[kTiles][kNT][4];
 #pragma unroll
         for (int t = 0; t < kNT; ++t)
 #pragma unroll
@@ -353,7 +404,7 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
                 l[t][j] = 0.f;
             }
 #pragma unroll
-        for (int k = 0; k < kKeySteps; ++k)
+        for (int k = 0; k < kTiles; ++k)
 #pragma unroll
             for (int t = 0; t < kNT; ++t)
 #pragma unroll
@@ -361,20 +412,21 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
 
         for (int k = 0; k < steps; ++k) {
             const uint32_t use = uses + static_cast<uint32_t>(k), st = use % P::kStages;
-            const int blk0 = g.first_block + 2 * (warp + kWarps * k);
+            const int blk0 = g.first_block + 2 * (team + kTeams * k);
             const uint32_t slot = ring + st * P::kStage;
             const uint32_t have = staged >> (2 * st) & 3u;
             wait_copy(bars + 8 * st, use >> P::kLogStages & 1);
-            // ---- scores of the unit's two blocks -----------------------------------------------------------------
-            float z[2][kNT][4];
-            uint32_t ks[2][2];  // key scales: tokens r, then r + 8, D / 64 each
+            // ---- scores of the unit's blocks (kSplit = 2: of block `part`) -------------------------------------
+            float z[kOwn][kNT][4];
+            uint32_t ks[kOwn][2];  // key scales: tokens r, then r + 8, D / 64 each
+            const uint32_t own = slot + static_cast<uint32_t>(kSplit == 1 ? 0 : part * kBlock);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < kOwn; ++n) {
 #pragma unroll
                 for (int t = 0; t < kNT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) z[n][t][e] = 0.f;
-                const uint32_t at_ = slot + static_cast<uint32_t>(n * kBlock + KvPlace<D>::kKeyScales + lane * (D / 32));
+                const uint32_t at_ = own + static_cast<uint32_t>(n * kBlock + KvPlace<D>::kKeyScales + lane * (D / 32));
                 if constexpr (D == 64) {
                     ks[n][0] = lds32(at_ & ~3u) >> (8 * (at_ & 2u)) & 0xFFFFu;
                     ks[n][1] = 0;
@@ -385,10 +437,10 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
             }
 #pragma unroll
             for (int quad = 0; quad < D / 64; ++quad) {
-                uint32_t w[2][4], s0[2], s1[2];
+                uint32_t w[kOwn][4], s0[kOwn], s1[kOwn];
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const uint4 v = ld_smem_v4(slot + static_cast<uint32_t>(n * kBlock + quad * 512 + lane * 16));
+                for (int n = 0; n < kOwn; ++n) {
+                    const uint4 v = ld_smem_v4(own + static_cast<uint32_t>(n * kBlock + quad * 512 + lane * 16));
                     w[n][0] = v.x;
                     w[n][1] = v.y;
                     w[n][2] = v.z;
@@ -402,12 +454,21 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
+                    for (int n = 0; n < kOwn; ++n) {
                         uint32_t x0, x1, x2, x3;
                         e2m1_word_to_f16(w[n][s], x0, x1, x2, x3);
                         const uint32_t a0 = mul_f16x2(x0, s0[n]), a2 = mul_f16x2(x1, s0[n]), a1 = mul_f16x2(x2, s1[n]), a3 = mul_f16x2(x3, s1[n]);
 #pragma unroll
-                        for (int t = 0; t < kNT; ++t) mma_f16(z[n][t], a0, a1, a2, a3, qf[t][quad * 4 + s][0], qf[t][quad * 4 + s][1]);
+                        for (int t = 0; t < kNT; ++t) {
+                            uint32_t b0, b1;
+                            if constexpr (kSplit == 1) {
+                                b0 = qf[t][quad * 4 + s][0];
+                                b1 = qf[t][quad * 4 + s][1];
+                            } else {
+                                lds64(queries + static_cast<uint32_t>(((t * kKeySteps + quad * 4 + s) * 32 + lane) * 8), b0, b1);
+                            }
+                            mma_f16(z[n][t], a0, a1, a2, a3, b0, b1);
+                        }
                     }
             }
             // ---- masks, running maximum, weights ------------------------------------------------------------
@@ -416,11 +477,12 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
 #pragma unroll
                 for (int t = 0; t < kNT; ++t)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < kOwn; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int pos = (blk0 + n) * 16 + r + 8 * (e / 2);
-                            const bool seen = (have >> n & 1) && pos < min(see[t][e % 2], g.s.kvl) &&
+                            const int in_unit = kSplit == 1 ? n : part;
+                            const int pos = (blk0 + in_unit) * 16 + r + 8 * (e / 2);
+                            const bool seen = (have >> in_unit & 1) && pos < min(see[t][e % 2], g.s.kvl) &&
                                               (p.window == 0 || pos >= see[t][e % 2] - p.window);
                             z[n][t][e] = seen ? z[n][t][e] * f[t][e % 2] : -INFINITY;
                         }
@@ -431,22 +493,45 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
             for (int t = 0; t < kNT; ++t)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    top[t][j] = fmaxf(fmaxf(z[0][t][j], z[0][t][2 + j]), fmaxf(z[1][t][j], z[1][t][2 + j])) * (whole ? f[t][j] : 1.f);
+                    float x = fmaxf(z[0][t][j], z[0][t][2 + j]);
+                    if constexpr (kSplit == 1) x = fmaxf(x, fmaxf(z[kOwn - 1][t][j], z[kOwn - 1][t][2 + j]));
+                    top[t][j] = x * (whole ? f[t][j] : 1.f);
                     raise |= top[t][j] > m[t][j] + kSlack;
                 }
-            if (__any_sync(0xFFFFFFFFu, raise)) {
+            if constexpr (kSplit == 1) {
+                raise = __any_sync(0xFFFFFFFFu, raise);
+            } else {
+                raise = pair_any(1 + team, raise);
+                if (k > 0 && issued < steps) issue(issued++);  // both warps are done with the last step's stage
+            }
+            if (raise) {
 #pragma unroll
                 for (int t = 0; t < kNT; ++t)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
 #pragma unroll
                         for (int x = 4; x < 32; x *= 2) top[t][j] = fmaxf(top[t][j], __shfl_xor_sync(0xFFFFFFFFu, top[t][j], x));
+                        if constexpr (kSplit == 2) {
+                            if (r == 0) shared_rows[part * R + 8 * t + 2 * c + j] = top[t][j];
+                        }
+                    }
+                if constexpr (kSplit == 2) {
+                    team_sync();
+#pragma unroll
+                    for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) top[t][j] = fmaxf(top[t][j], shared_rows[(part ^ 1) * R + 8 * t + 2 * c + j]);
+                }
+#pragma unroll
+                for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
                         const float m2 = fmaxf(m[t][j], top[t][j]);
                         const float fade = m2 == -INFINITY ? 1.f : ex2(m[t][j] - m2);
                         m[t][j] = m2;
                         l[t][j] *= fade;
 #pragma unroll
-                        for (int q = 0; q < kKeySteps; ++q) {
+                        for (int q = 0; q < kTiles; ++q) {
                             o[q][t][j] *= fade;
                             o[q][t][2 + j] *= fade;
                         }
@@ -458,7 +543,7 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
                 const float b0 = m[t][0] == -INFINITY ? 0.f : -m[t][0], b1 = m[t][1] == -INFINITY ? 0.f : -m[t][1];
                 const float f0 = whole ? f[t][0] : 1.f, f1 = whole ? f[t][1] : 1.f;
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < kOwn; ++n) {
                     const float w0 = ex2(fmaf(z[n][t][0], f0, b0)), w1 = ex2(fmaf(z[n][t][1], f1, b1));
                     const float w2 = ex2(fmaf(z[n][t][2], f0, b0)), w3 = ex2(fmaf(z[n][t][3], f1, b1));
                     l[t][0] += w0 + w2;
@@ -467,14 +552,35 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
                     pb[n][t][1] = transpose_8x8(pack_f16(w2, w3));
                 }
             }
-            // ---- weighted values --------------------------------------------------------------------------------
+            if constexpr (kSplit == 2) {
+                // this block's fragments to the other warp, its block's from there (two buffers in turn: the next step's
+                // writes pass no reads of this step's, which end before the other warp's next pair_any)
+                const uint32_t buf = exchanged + static_cast<uint32_t>(k % 2 * (2 * kNT * 2 * 128) + lane * 4);
+#pragma unroll
+                for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + static_cast<uint32_t>((part * kNT * 2 + t * 2 + i) * 128)), "r"(pb[0][t][i])
+                                     : "memory");
+                team_sync();
+#pragma unroll
+                for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t mine = pb[0][t][i], theirs = lds32(buf + static_cast<uint32_t>(((part ^ 1) * kNT * 2 + t * 2 + i) * 128));
+                        pb[0][t][i] = part == 0 ? mine : theirs;
+                        pb[1][t][i] = part == 0 ? theirs : mine;
+                    }
+            }
+            // ---- weighted values: the warp's output tiles, both blocks ------------------------------------------
+            constexpr int kGroups = (kTiles + 7) / 8, kPer = kTiles / kGroups;  // 16-column groups of a lane; tiles of each
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                uint32_t nan16[(D + 127) / 128] = {};  // per 16-column group of this lane: tokens of the block whose scale is NaN
+                uint32_t nan16[kGroups] = {};  // tokens of the block whose scale is NaN
 #pragma unroll
-                for (int x = 0; x < (D + 127) / 128; ++x) {  // the lane's 16-column groups (D = 64: half a group)
-                    uint32_t s4 = lds32(slot + static_cast<uint32_t>(n * kBlock + KvPlace<D>::kValueScales +
-                                                                     ((D == 64 ? r / 2 : r * (D / 128) + x) * 4 + c) * 4));
+                for (int x = 0; x < kGroups; ++x) {
+                    const int group16 = (r * (D / 8) + 2 * part * kTiles + 16 * x) / 16;
+                    uint32_t s4 = lds32(slot + static_cast<uint32_t>(n * kBlock + KvPlace<D>::kValueScales + (group16 * 4 + c) * 4));
                     if (!whole) {
                         // a token that some row does not see must not reach that row through 0 * NaN: its NaN scale becomes 0
                         // here and is put into the rows that do see it below
@@ -491,24 +597,35 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
                     }
                     const uint32_t sp0 = e4m3x2_to_f16(s4 & 0xFFFFu), sp1 = e4m3x2_to_f16(s4 >> 16);
                     const uint32_t e0 = sp0 & 0xFFFFu, o0 = sp0 & 0xFFFF0000u, e1 = sp1 & 0xFFFFu, o1 = sp1 & 0xFFFF0000u;
+                    constexpr int kWords = kPer < 4 ? kPer : 4;  // codes of so many tiles at a time
 #pragma unroll
-                    for (int quad = x * 2; quad < (D == 64 ? 1 : x * 2 + 2); ++quad) {
-                        const uint4 v = ld_smem_v4(slot + static_cast<uint32_t>(n * kBlock + KvPlace<D>::kValueCodes + quad * 512 + lane * 16));
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    for (int q = x * kPer; q < (x + 1) * kPer; q += kWords) {
+                        const int tile = part * kTiles + q;
+                        const uint32_t from = slot + static_cast<uint32_t>(n * kBlock + KvPlace<D>::kValueCodes + tile / 4 * 512 + lane * 16 + tile % 4 * 4);
+                        uint32_t w[4];
+                        if constexpr (kWords == 4) {
+                            const uint4 v = ld_smem_v4(from);
+                            w[0] = v.x;
+                            w[1] = v.y;
+                            w[2] = v.z;
+                            w[3] = v.w;
+                        } else {
+                            lds64(from, w[0], w[1]);
+                        }
 #pragma unroll
-                        for (int mm = 0; mm < 4; ++mm) {
+                        for (int mm = 0; mm < kWords; ++mm) {
                             uint32_t x0, x1, x2, x3;  // tokens 2c, 2c + 1, 2c + 8, 2c + 9; a pair of columns each
                             e2m1_word_to_f16(w[mm], x0, x1, x2, x3);
                             const uint32_t a0 = weave_low(x0, e0, x1, o0), a1 = weave_high(x0, e0, x1, o0);
                             const uint32_t a2 = weave_low(x2, e1, x3, o1), a3 = weave_high(x2, e1, x3, o1);
 #pragma unroll
-                            for (int t = 0; t < kNT; ++t) mma_f16(o[quad * 4 + mm][t], a0, a1, a2, a3, pb[n][t][0], pb[n][t][1]);
+                            for (int t = 0; t < kNT; ++t) mma_f16(o[q + mm][t], a0, a1, a2, a3, pb[n][t][0], pb[n][t][1]);
                         }
                     }
                 }
                 if (!whole) {
 #pragma unroll
-                    for (int x = 0; x < (D + 127) / 128; ++x) {
+                    for (int x = 0; x < kGroups; ++x) {
                         if (nan16[x] == 0) continue;
 #pragma unroll
                         for (int t = 0; t < kNT; ++t)
@@ -520,17 +637,19 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
                                 const uint32_t vis = to > from ? ((1u << to) - 1u) & ~((1u << from) - 1u) : 0u;
                                 if (nan16[x] & vis) {
 #pragma unroll
-                                    for (int k = 0; k < 8 && k + 8 * x < kKeySteps; ++k)
-                                        o[k + 8 * x][t][j] = o[k + 8 * x][t][2 + j] = __uint_as_float(0x7FC00000u);
+                                    for (int q = x * kPer; q < (x + 1) * kPer; ++q) o[q][t][j] = o[q][t][2 + j] = __uint_as_float(0x7FC00000u);
                                 }
                             }
                     }
                 }
             }
-            __syncwarp();
-            if (issued < steps) issue(issued++);  // into the stage that is free now
+            if constexpr (kSplit == 1) {
+                __syncwarp();
+                if (issued < steps) issue(issued++);  // into the stage that is free now
+            }
         }
         uses += static_cast<uint32_t>(steps);
+        if constexpr (kSplit == 2) team_sync();  // the ring is free
 
         // ---- the next part's copies start before this one is joined ---------------------------------------
         const Segment done = g;
@@ -556,13 +675,24 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
             open();
         }
 
-        // ---- join the warps, in halves ---------------------------------------------------------
+        // ---- join the teams, in halves -----------------------------------------------------------------------
 #pragma unroll
         for (int t = 0; t < kNT; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j) {
 #pragma unroll
                 for (int x = 4; x < 32; x *= 2) l[t][j] += __shfl_xor_sync(0xFFFFFFFFu, l[t][j], x);
+                if constexpr (kSplit == 2) {
+                    if (r == 0) shared_rows[part * R + 8 * t + 2 * c + j] = l[t][j];
+                }
+            }
+        if constexpr (kSplit == 2) {  // the two warps' sums (their maxima are the same)
+            team_sync();
+#pragma unroll
+            for (int t = 0; t < kNT; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) l[t][j] += shared_rows[(part ^ 1) * R + 8 * t + 2 * c + j];
+        }
         // another partial result: rows' maxima and sums, outputs; `get` loads one float
         auto absorb = [&](const float* ml, const float* st, auto get) {
 #pragma unroll
@@ -579,7 +709,7 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
                     l[t][j] = l[t][j] * mine_[j] + l1 * theirs[j];
                 }
 #pragma unroll
-                for (int k = 0; k < kKeySteps; ++k)
+                for (int k = 0; k < kTiles; ++k)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         o[k][t][e] = o[k][t][e] * mine_[e % 2] + get(st + ((k * kNT + t) * 4 + e) * 32 + lane) * theirs[e % 2];
@@ -596,23 +726,23 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
                     }
             }
 #pragma unroll
-            for (int k = 0; k < kKeySteps; ++k)
+            for (int k = 0; k < kTiles; ++k)
 #pragma unroll
                 for (int t = 0; t < kNT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) st[((k * kNT + t) * 4 + e) * 32 + lane] = o[k][t][e];
         };
-        auto join_warps = [&]() {
-            for (int half = kWarps / 2; half >= 1; half /= 2) {
-                float* at_ = merge + (warp % half) * (P::kStateFloats + P::kMl);
-                if (warp >= half && warp < 2 * half) leave(at_, at_ + P::kMl);
+        auto join_teams = [&]() {
+            for (int half = kTeams / 2; half >= 1; half /= 2) {
+                float* at_ = merge + (team % half * kSplit + part) * (P::kStateFloats + P::kMl);
+                if (team >= half && team < 2 * half) leave(at_, at_ + P::kMl);
                 __syncthreads();
-                if (warp < half) absorb(at_, at_ + P::kMl, [](const float* x) { return *x; });
+                if (team < half) absorb(at_, at_ + P::kMl, [](const float* x) { return *x; });
                 __syncthreads();
             }
         };
-        auto write_out = [&]() {  // warp 0 has it all
-            if (warp != 0) return;
+        auto write_out = [&]() {  // team 0 has it all
+            if (team != 0) return;
             const int drows = done.s.ql * group, drow0 = done.tile * R;
 #pragma unroll
             for (int t = 0; t < kNT; ++t)
@@ -624,21 +754,24 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
                     const float s = lv == 0.f ? 0.f : p.s.v_unit / lv;
                     const long long token = done.s.qs + row / group;
                     const int head = done.h * group + row % group;
-                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D + r * (D / 8);
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D + r * (D / 8) +
+                                         2 * part * kTiles;
+                    constexpr int kVec = kTiles < 4 ? kTiles : 4;
 #pragma unroll
-                    for (int k = 0; k < kKeySteps; k += 4) {
-                        uint32_t w[4];
+                    for (int k = 0; k < kTiles; k += kVec) {
+                        uint32_t w[kVec];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
+                        for (int e = 0; e < kVec; ++e) {
                             const __nv_bfloat162 v = __floats2bfloat162_rn(o[k + e][t][j] * s, o[k + e][t][2 + j] * s);
                             w[e] = *reinterpret_cast<const uint32_t*>(&v);
                         }
-                        *reinterpret_cast<uint4*>(dst + 2 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+                        if constexpr (kVec == 4) *reinterpret_cast<uint4*>(dst + 2 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+                        else *reinterpret_cast<uint2*>(dst + 2 * k) = make_uint2(w[0], w[1]);
                     }
-                    if (p.lse && r == 0) p.lse[token * p.q_heads + head] = lv == 0.f ? -INFINITY : (m[t][j] + log2f(lv)) * kLn2;
+                    if (p.lse && r == 0 && part == 0) p.lse[token * p.q_heads + head] = lv == 0.f ? -INFINITY : (m[t][j] + log2f(lv)) * kLn2;
                 }
         };
-        join_warps();
+        join_teams();
         if (done.u0 == 0 && done.u1 == done.units) {
             write_out();
         } else {
@@ -650,12 +783,12 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
             float* parts = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kAttCounterBytes);
             // a CTA's second slot for the segment that begins in it, the first for one that began before
             auto part_of = [&](int cta) { return parts + static_cast<long long>(2 * cta + (cta == c0 ? 1 : 0)) * kAttPartFloats; };
-            if (warp == 0) {
+            if (team == 0) {
                 float* mine_ = part_of(static_cast<int>(blockIdx.x));
-                leave(mine_, mine_ + P::kMl);
+                leave(mine_, mine_ + P::kMl + part * P::kStateFloats);  // both warps write the same maxima and sums
                 __threadfence();
-                __syncwarp();
-                if (lane == 0) {
+                team_sync();
+                if (warp == 0 && lane == 0) {
                     const unsigned int before = atomicAdd(&counters[c0], 1u);
                     const bool last = before + 1 == static_cast<unsigned int>(c1 - c0 + 1);
                     if (last) counters[c0] = 0;
@@ -665,7 +798,7 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
             }
             __syncthreads();
             if (last_flag) {
-                // warp w takes parts w, w + kWarps, ... in their order, then the warps join as before
+                // team w takes parts w, w + kTeams, ... in their order, then the teams join as before
 #pragma unroll
                 for (int t = 0; t < kNT; ++t)
 #pragma unroll
@@ -674,17 +807,17 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
                         l[t][j] = 0.f;
                     }
 #pragma unroll
-                for (int k = 0; k < kKeySteps; ++k)
+                for (int k = 0; k < kTiles; ++k)
 #pragma unroll
                     for (int t = 0; t < kNT; ++t)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[k][t][e] = 0.f;
                 __threadfence();
-                for (int x = c0 + warp; x <= c1; x += kWarps) {
+                for (int x = c0 + team; x <= c1; x += kTeams) {
                     const float* st = part_of(x);
-                    absorb(st, st + P::kMl, [](const float* x) { return __ldcg(x); });  // other SMs' writes: from L2
+                    absorb(st, st + P::kMl + part * P::kStateFloats, [](const float* x) { return __ldcg(x); });  // other SMs' writes: from L2
                 }
-                join_warps();
+                join_teams();
                 write_out();
             }
         }
@@ -693,9 +826,9 @@ __global__ void __launch_bounds__(Plan<D, kNT>::kThreads, Plan<D, kNT>::kCtas) a
     }
 }
 
-template <int D, int kNT>
+template <int D, int kNT, int kSplit>
 int launch_rows(const AttArgs& a, cudaStream_t stream) {
-    using P = Plan<D, kNT>;
+    using P = Plan<D, kNT, kSplit>;
     static_assert(8 * kNT * (D + 2) <= kAttPartFloats, "a partial result fits its place in the workspace");
     static std::mutex mu;
     static int ctas[kMaxDevices] = {};
@@ -705,15 +838,15 @@ int launch_rows(const AttArgs& a, cudaStream_t stream) {
         std::lock_guard<std::mutex> lk(mu);
         if (ctas[dev] == 0) {
             int sms = 0, per_sm = 0;
-            if (cudaFuncSetAttribute(attend_rows_kernel<D, kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem) != cudaSuccess ||
+            if (cudaFuncSetAttribute(attend_rows_kernel<D, kNT, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem) != cudaSuccess ||
                 cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attend_rows_kernel<D, kNT>, P::kThreads, P::kSmem) != cudaSuccess ||
+                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attend_rows_kernel<D, kNT, kSplit>, P::kThreads, P::kSmem) != cudaSuccess ||
                 sms < 1 || per_sm < 1)
                 return -7;
             ctas[dev] = sms * per_sm < kAttMaxCtas ? sms * per_sm : kAttMaxCtas;
         }
     }
-    attend_rows_kernel<D, kNT><<<static_cast<unsigned>(ctas[dev]), P::kThreads, P::kSmem, stream>>>(a);
+    attend_rows_kernel<D, kNT, kSplit><<<static_cast<unsigned>(ctas[dev]), P::kThreads, P::kSmem, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? 0 : -7;
 }
 
@@ -724,17 +857,17 @@ int launch_attention(const AttArgs& a, cudaStream_t stream) {
     if (rows >= kTilesFromRows && a.s.dim <= 128) return launch_attention_tiles(a, stream);
     switch (a.s.dim) {
         case 64:
-            if (rows <= 8) return launch_rows<64, 1>(a, stream);
-            if (rows <= 16) return launch_rows<64, 2>(a, stream);
-            return launch_rows<64, 4>(a, stream);
+            if (rows <= 8) return launch_rows<64, 1, 1>(a, stream);
+            if (rows <= 16) return launch_rows<64, 2, 2>(a, stream);
+            return launch_rows<64, 4, 2>(a, stream);
         case 128:
-            if (rows <= 8) return launch_rows<128, 1>(a, stream);
-            if (rows <= 16) return launch_rows<128, 2>(a, stream);
-            if (rows <= 24) return launch_rows<128, 3>(a, stream);
-            return launch_rows<128, 4>(a, stream);
+            if (rows <= 8) return launch_rows<128, 1, 1>(a, stream);
+            if (rows <= 16) return launch_rows<128, 2, 2>(a, stream);
+            if (rows <= 24) return launch_rows<128, 3, 2>(a, stream);
+            return launch_rows<128, 4, 2>(a, stream);
         default:
-            if (rows <= 8) return launch_rows<256, 1>(a, stream);
-            return launch_rows<256, 2>(a, stream);
+            if (rows <= 8) return launch_rows<256, 1, 2>(a, stream);
+            return launch_rows<256, 2, 2>(a, stream);
     }
 }
 
