@@ -141,17 +141,32 @@ __device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
         "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
+// 32 consecutive columns of this thread's lane; the values are there after tmem_ld_wait, which waits for all loads so far.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t addr, float (&v)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
           "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
           "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
           "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
         : "r"(addr)
         : "memory");
+}
+// The wait names the registers it waits for, so that no use of them moves above it.
+__device__ __forceinline__ void tmem_ld_wait(float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
+                   "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
+                   "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]),
+                   "+f"(v[28]), "+f"(v[29]), "+f"(v[30])
+                 :
+                 : "memory");
+    asm volatile("" : "+f"(v[31])::"memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
+    tmem_ld32_start(addr, v);
+    tmem_ld_wait(v);
 }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const float (&v)[32]) {
     asm volatile(
@@ -190,57 +205,75 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// The weights 2^(score * f + shift) of one row of scores in tensor memory, as fp16 pairs, and their sum (in fp32, before
-// the rounding); returns the largest score seen. kMask: only columns [from, upto) without the blocks in `gone` are seen.
+// Columns [from, upto) without the blocks in `gone`, as bits of columns 32 q .. 32 q + 31.
+__device__ __forceinline__ uint32_t seen_columns(int q, int from, int upto, uint32_t gone) {
+    const int a = min(max(from - 32 * q, 0), 32), b = min(max(upto - 32 * q, 0), 32);
+    uint32_t seen = b > a ? (0xFFFFFFFFu >> (32 - (b - a))) << a : 0u;
+    if (gone >> (2 * q) & 1) seen &= 0xFFFF0000u;
+    if (gone >> (2 * q + 1) & 1) seen &= 0x0000FFFFu;
+    return seen;
+}
+
+// The largest of a row's scores in tensor memory. kMask: of the columns in seen[].
 template <bool kMask>
-__device__ __forceinline__ float weights(uint32_t ts, float f, float shift, int from, int upto, uint32_t gone, uint32_t (&w)[kKeys / 2],
-                                         float& sum) {
+__device__ __forceinline__ float largest(uint32_t ts, const uint32_t* seen) {
     float top0 = -INFINITY, top1 = -INFINITY;
-    uint64_t s0 = pair(0.f, 0.f), s1 = s0;
-    const uint64_t ff = pair(f, f), sh = pair(shift, shift);
+    float v[2][32];
+    tmem_ld32_start(ts, v[0]);
 #pragma unroll
     for (int q = 0; q < kKeys / 32; ++q) {
-        float v[32];
-        tmem_ld32(ts + static_cast<uint32_t>(32 * q), v);
+        tmem_ld_wait(v[q % 2]);
+        if (q + 1 < kKeys / 32) tmem_ld32_start(ts + static_cast<uint32_t>(32 * (q + 1)), v[(q + 1) % 2]);
         if constexpr (kMask) {
-            const int a = min(max(from - 32 * q, 0), 32), b = min(max(upto - 32 * q, 0), 32);
-            uint32_t seen = b > a ? (0xFFFFFFFFu >> (32 - (b - a))) << a : 0u;
-            if (gone >> (2 * q) & 1) seen &= 0xFFFF0000u;
-            if (gone >> (2 * q + 1) & 1) seen &= 0x0000FFFFu;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                if (!(seen >> i & 1)) v[i] = -INFINITY;
+                if (!(seen[q] >> i & 1)) v[q % 2][i] = -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-            top0 = fmaxf(top0, fmaxf(v[i], v[i + 1]));
-            top1 = fmaxf(top1, fmaxf(v[i + 2], v[i + 3]));
+            top0 = fmaxf(top0, fmaxf(v[q % 2][i], v[q % 2][i + 1]));
+            top1 = fmaxf(top1, fmaxf(v[q % 2][i + 2], v[q % 2][i + 3]));
         }
+    }
+    return fmaxf(top0, top1);
+}
+
+// The weights 2^(score * f + shift) of half a row of scores in tensor memory, as fp16 pairs over the scores' first columns
+// (of which nothing is needed any more), and added to `sum` (in fp32, before the rounding).
+template <bool kMask>
+__device__ __forceinline__ void weights(uint32_t ts, int half, float f, float shift, const uint32_t* seen, uint64_t& sum) {
+    uint64_t s0 = pair(0.f, 0.f);
+    const uint64_t ff = pair(f, f), sh = pair(shift, shift);
+    float v[2][32];
+    tmem_ld32_start(ts + static_cast<uint32_t>(64 * half), v[0]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        tmem_ld_wait(v[q]);
+        if (q == 0) tmem_ld32_start(ts + static_cast<uint32_t>(64 * half + 32), v[1]);
+        uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
             float a, b, c, d;
-            unpair(fma2(pair(v[i], v[i + 1]), ff, sh), a, b);
-            unpair(fma2(pair(v[i + 2], v[i + 3]), ff, sh), c, d);
-            if constexpr (kMask) {  // f may be 0
-                a = v[i] == -INFINITY ? -INFINITY : a;
-                b = v[i + 1] == -INFINITY ? -INFINITY : b;
-                c = v[i + 2] == -INFINITY ? -INFINITY : c;
-                d = v[i + 3] == -INFINITY ? -INFINITY : d;
+            unpair(fma2(pair(v[q][i], v[q][i + 1]), ff, sh), a, b);
+            unpair(fma2(pair(v[q][i + 2], v[q][i + 3]), ff, sh), c, d);
+            if constexpr (kMask) {
+                a = seen[2 * half + q] >> i & 1 ? a : -INFINITY;
+                b = seen[2 * half + q] >> (i + 1) & 1 ? b : -INFINITY;
+                c = seen[2 * half + q] >> (i + 2) & 1 ? c : -INFINITY;
+                d = seen[2 * half + q] >> (i + 3) & 1 ? d : -INFINITY;
             }
             a = ex2(a);
             b = ex2(b);
             c = ex2(c);
             d = ex2(d);
-            s0 = add2(s0, pair(a, b));
-            s1 = add2(s1, pair(c, d));
-            w[16 * q + i / 2] = pack_f16(a, b);
-            w[16 * q + i / 2 + 1] = pack_f16(c, d);
+            sum = add2(sum, pair(a, b));
+            s0 = add2(s0, pair(c, d));
+            w[i / 2] = pack_f16(a, b);
+            w[i / 2 + 1] = pack_f16(c, d);
         }
+        tmem_st16(ts + static_cast<uint32_t>(32 * half + 16 * q), w);
     }
-    float x, y;
-    unpair(add2(s0, s1), x, y);
-    sum = x + y;
-    return fmaxf(top0, top1);
+    sum = add2(sum, s0);
 }
 
 // One lane's part of a cache block in registers.
@@ -316,8 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     auto v_full = [&](int i) { return bars + 8u * static_cast<uint32_t>(4 + i); };
     auto v_empty = [&](int i) { return bars + 8u * static_cast<uint32_t>(6 + i); };
     auto s_full = [&](int a) { return bars + 8u * static_cast<uint32_t>(8 + a); };
-    auto p_full = [&](int a) { return bars + 8u * static_cast<uint32_t>(10 + a); };
-    const uint32_t o_full = bars + 8u * 12u;
+    auto p_full = [&](int a, int half) { return bars + 8u * static_cast<uint32_t>(10 + 2 * a + half); };
+    const uint32_t o_full = bars + 8u * 14u;
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(smem + T::kBars + 16 * 8);
     volatile uint32_t* abort_flag = tmem_ptr + 1;
     const Wait wait{abort_flag};
@@ -328,7 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             mbar_init(v_full(i), kDequantWarps);
             mbar_init(v_empty(i), 1);
             mbar_init(s_full(i), 1);
-            mbar_init(p_full(i), 4);
+            mbar_init(p_full(i, 0), 4);
+            mbar_init(p_full(i, 1), 4);
         }
         mbar_init(o_full, 1);
         for (int i = 0; i < kNotes; ++i) nan_any[i] = 0;
@@ -395,12 +429,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             }
             commit(lead, s_full(a));
         };
-        auto outputs = [&](int a, int j) {
-            const uint64_t v = vd + static_cast<uint64_t>(j % 2 * (T::kTile / 16));
-            const uint32_t d = tmem + static_cast<uint32_t>(T::kO + a * D), w = tmem + static_cast<uint32_t>(a * kKeys);
-            mma_ts(lead, d, w, v, id_o, j != 0 ? 1u : 0u);
+        auto outputs = [&](int a, int j, int half) {
+            const uint64_t v = vd + static_cast<uint64_t>(j % 2 * (T::kTile / 16) + half * (64 * 128 / 16));
+            const uint32_t d = tmem + static_cast<uint32_t>(T::kO + a * D), w = tmem + static_cast<uint32_t>(a * kKeys + half * 32);
+            mma_ts(lead, d, w, v, id_o, j != 0 || half != 0 ? 1u : 0u);
 #pragma unroll
-            for (int st = 1; st < kKeys / 16; ++st)
+            for (int st = 1; st < kKeys / 32; ++st)
                 mma_ts(lead, d, w + static_cast<uint32_t>(st * 8), v + static_cast<uint64_t>(st * 2048 / 16), id_o, 1u);
         };
         if (tiles > 0) {
@@ -412,11 +446,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         for (int j = 0; j < tiles; ++j) {
             for (int a = 0; a < na; ++a) {
                 if (a == 0) wait(v_full(j % 2), j / 2 & 1);
-                wait(p_full(a), j & 1);
+                wait(p_full(a, 0), j & 1);
+                __syncwarp();
+                tc_fence_after();
+                outputs(a, j, 0);
+                wait(p_full(a, 1), j & 1);
                 if (a == 0 && j + 1 < tiles) wait(k_full((j + 1) % 2), (j + 1) / 2 & 1);
                 __syncwarp();
                 tc_fence_after();
-                outputs(a, j);
+                outputs(a, j, 1);
                 if (a == na - 1) commit(lead, v_empty(j % 2));
                 if (j + 1 < tiles) {
                     scores(a, j + 1);
@@ -433,26 +471,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         const int* table = p.page_table + static_cast<long long>(b) * p.max_pages;
         const unsigned char* src[kBlocksPerWarp];  // of the tile whose words are being loaded; null: nothing there
         bool there[kBlocksPerWarp];
-        int page[kBlocksPerWarp];
+        int pages[kBlocksPerWarp];  // lane i: the page entries of tile 32 k + i; -2: behind the last block
         BlockRegs<D> x[kBlocksPerWarp] = {};
-        auto find = [&](int j) {  // page entries of tile j; -2: behind the last block
+        auto place = [&](int j) {  // in order of j
+            if (j % 32 == 0) {
+                // 32 tiles' entries at once: a load a tile would wait, with its tile, for the codes that are on their way
 #pragma unroll
-            for (int i = 0; i < kBlocksPerWarp; ++i) {
-                const int blk = block0 + 8 * j + kBlocksPerWarp * w + i;
-                page[i] = j < tiles && blk < block_end ? __ldg(table + (blk * 16 >> p.s.page_shift)) : -2;
+                for (int i = 0; i < kBlocksPerWarp; ++i) {
+                    const int blk = block0 + 8 * (j + lane) + kBlocksPerWarp * w + i;
+                    pages[i] = j + lane < tiles && blk < block_end ? __ldg(table + (blk * 16 >> p.s.page_shift)) : -2;
+                }
             }
-        };
-        auto place = [&](int j) {
 #pragma unroll
             for (int i = 0; i < kBlocksPerWarp; ++i) {
                 src[i] = nullptr;
-                if (page[i] == -2) continue;
-                if (page[i] < 0 || page[i] >= p.s.pages) {
+                const int page = __shfl_sync(0xFFFFFFFFu, pages[i], j % 32);
+                if (page == -2) continue;
+                if (page < 0 || page >= p.s.pages) {
                     if (lane == 0) atomicOr(&g_hc_tiles_error, kErrPage);
                     continue;
                 }
                 const int tok = (block0 + 8 * j + kBlocksPerWarp * w + i) * 16;
-                src[i] = p.cache + (((static_cast<long long>(page[i]) * heads + h) << (p.s.page_shift - 4)) +
+                src[i] = p.cache + (((static_cast<long long>(page) * heads + h) << (p.s.page_shift - 4)) +
                                     ((tok & ((1 << p.s.page_shift) - 1)) >> 4)) * kv_block_bytes(D);
             }
         };
@@ -486,11 +526,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                 x[i].vs = *reinterpret_cast<const uint32_t*>(src[i] + KvPlace<D>::kValueScales + (r * (D / 8) / 16 * 4 + c) * 4);
             }
         };
-        find(0);
         place(0);
         fetch_keys();
         fetch_values();
-        find(1);
         for (int j = 0; j < tiles; ++j) {
             const int st = j % 2, note = j % kNotes;
             const uint32_t parity = static_cast<uint32_t>((j / 2 & 1) ^ 1);
@@ -595,7 +633,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                 }
             }
             fetch_values();  // tile j + 1's
-            find(j + 2);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(v_full(st));
@@ -619,13 +656,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                 const bool whole = tok0 >= g.all_lo && tok0 + kKeys <= g.all_hi && gone == 0;
                 // this row sees columns [from, upto) of the tile, but for blocks that are not there
                 const int from = low - tok0, upto = high - tok0;
-                uint32_t w[kKeys / 2];
-                float sum;
-                // Weights by the maximum so far; where a score is too far above it, the maximum is raised and they are taken again.
-                for (int turn = 0; turn < 2; ++turn) {
-                    const float base = m == -INFINITY ? 0.f : m;
-                    const float top = f * (whole ? weights<false>(ts, f, -base, 0, 0, 0u, w, sum) : weights<true>(ts, f, -base, from, upto, gone, w, sum));
-                    if (!__any_sync(0xFFFFFFFFu, top > m + kSlack)) break;
+                uint32_t seen[kKeys / 32] = {};
+                float top;
+                if (whole) {
+                    top = largest<false>(ts, seen);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kKeys / 32; ++q) seen[q] = seen_columns(q, from, upto, gone);
+                    top = largest<true>(ts, seen);
+                }
+                top = top == -INFINITY ? top : top * f;  // (f may be 0)
+                if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
                     const float m2 = fmaxf(m, top);
                     const float fade = m2 == -INFINITY ? 1.f : ex2(m - m2);
                     m = m2;
@@ -641,21 +682,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                         }
                     }
                 }
-                l += sum;
-#pragma unroll
-                for (int q = 0; q < kKeys / 32; ++q) tmem_st16(ts + static_cast<uint32_t>(16 * q), w + 16 * q);
                 if (!whole) {
-                    // the notes are complete with the tile's values, which may come after its scores
+                    // The notes are complete with the tile's values, which may come after its scores. (Before the weights are handed
+                    // over: after that the values' stage may be filled anew, and its barrier go on to another phase.)
                     wait(v_full(j % 2), j / 2 & 1);
                     if (*reinterpret_cast<volatile uint32_t*>(&nan_any[j % kNotes])) {
                         const uint16_t* notes = reinterpret_cast<const uint16_t*>(smem + T::kNan) + j % kNotes * kKeys;
                         for (int n = max(from, 0); n < min(upto, kKeys); ++n) nan_groups |= notes[n];
                     }
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(a));
+                const float shift = m == -INFINITY ? 0.f : -m;
+                uint64_t sum = pair(0.f, 0.f);
+                // half by half: the second product of the first 64 keys starts while the weights of the others are made
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (whole) weights<false>(ts, half, f, shift, seen, sum);
+                    else weights<true>(ts, half, f, shift, seen, sum);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full(a, half));
+                }
+                float x, y;
+                unpair(sum, x, y);
+                l += x + y;
             }
             // ---- results -----------------------------------------------------------------------------------
             if (tiles > 0) wait(o_full, 0);
