@@ -46,7 +46,10 @@ constexpr uint64_t kWaitNs = 1000000000ull;   // 1 s
 constexpr int kUnit = 32;                     // tokens a warp takes at a time: two cache blocks
 constexpr int kWholeSteps = 4;                // segments of at most so many units a warp are not cut (see the kernel)
 constexpr int kMaxDevices = 64;
-constexpr long long kTilesFromRows = 128;     // rows of the longest sequence from which hc_attend_tiles.cu takes a call
+// Rows of the longest sequence from which hc_attend_tiles.cu takes a call: more than this kernel's largest tile of rows
+// reads and dequantises the keys twice. 64 sequences of up to 4096 keys, 28 rows: 179 us here, 243 us there; 64 of up to
+// 1000 keys, 40 rows: 143 against 90 us; 32 of up to 4096 keys, 96 rows: 129 against 81 us.
+constexpr long long kTilesFromRows = 33;
 
 // The shape of a CTA. A team of kSplit warps takes a unit at a time: alone (kSplit = 1), or two warps that share it, each
 // the scores of one of its two blocks and then half the output columns for both, the weights exchanged through
@@ -854,7 +857,7 @@ int launch_rows(const AttArgs& a, cudaStream_t stream) {
 
 int launch_attention(const AttArgs& a, cudaStream_t stream) {
     const long long rows = static_cast<long long>(a.max_q_len) * (a.q_heads / a.s.heads);
-    if (rows >= kTilesFromRows && a.s.dim <= 128) return launch_attention_tiles(a, stream);
+    if (rows >= kTilesFromRows && attention_tiles_take(a)) return launch_attention_tiles(a, stream);
     switch (a.s.dim) {
         case 64:
             if (rows <= 8) return launch_rows<64, 1, 1>(a, stream);

@@ -62,6 +62,7 @@ struct TilePlan {
     static constexpr int kSmem = kBars + 16 * 8 + 16 + 1024;  // + alignment
     static constexpr int kO = 256;                         // tensor memory: S_0, S_1, O_0, O_1
     static constexpr uint32_t kColumns = 512;
+    static constexpr int kPartFloats = kRows * (D + 2);    // a slice's result in the workspace
 };
 
 struct Wait {
@@ -276,6 +277,19 @@ __device__ __forceinline__ void weights(uint32_t ts, int half, float f, float sh
     sum = add2(sum, s0);
 }
 
+__device__ __forceinline__ void store32(__nv_bfloat16* dst, const float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 t = __floats2bfloat162_rn(v[i + 2 * e], v[i + 2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&t);
+        }
+        *reinterpret_cast<uint4*>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 // One lane's part of a cache block in registers.
 template <int D>
 struct BlockRegs {
@@ -291,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ int scan[kThreads / 32 + 1];
     __shared__ int found_seq, found_tile;
+    __shared__ bool last_flag;
     __shared__ uint32_t absent[kNotes][kDequantWarps];  // per key tile: bits of the blocks that are not there
     __shared__ uint32_t nan_any[kNotes];                // per key tile: some value's scale is NaN
     const uint32_t sbase = smem_u32(smem);
@@ -307,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             const int b = b0 + tid;
             int v = 0;
             if (b < p.seqs) {
-                const SeqRows s = load_seq(p, b, blockIdx.x == 0 ? &g_hc_tiles_error : nullptr);
+                const SeqRows s = load_seq(p, b, blockIdx.x == 0 && blockIdx.y == 0 ? &g_hc_tiles_error : nullptr);
                 v = static_cast<int>((static_cast<long long>(s.ql) * group + kRows - 1) / kRows);
             }
             int x = v;
@@ -340,8 +355,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     const int rows = s.ql * group, row0 = tile * kRows;
     const bool two = rows - row0 > kRowTile;  // the second row tile has rows
     const TileBounds g = tile_bounds(p, s, group, row0, min(row0 + kRows, rows) - 1);
-    const int block0 = g.lo / 16, block_end = (g.hi + 15) / 16;
-    const int tiles = block_end > block0 ? (block_end - block0 + 7) / 8 : 0;
+    // this CTA's slice of the key tiles (blockIdx.y of gridDim.y): cache blocks from block0 on, `tiles` tiles of 8
+    int block0 = g.lo / 16;
+    const int block_end = (g.hi + 15) / 16;
+    int tiles = block_end > block0 ? (block_end - block0 + 7) / 8 : 0;
+    {
+        const int slices = static_cast<int>(gridDim.y), slice = static_cast<int>(blockIdx.y);
+        const int t0 = static_cast<int>(static_cast<long long>(tiles) * slice / slices);
+        tiles = static_cast<int>(static_cast<long long>(tiles) * (slice + 1) / slices) - t0;
+        block0 += 8 * t0;
+    }
 
     const uint32_t bars = sbase + T::kBars;
     auto k_full = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
@@ -375,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     }
 
     // ---- queries: thread i < 256 takes row i ---------------------------------------------------------------
+    float m = -INFINITY, l = 0.f;  // the row's running maximum (log2 units) and sum
     float f = 0.f;
     int see = 0;
     const bool softmax = warp < kSoftmaxWarps;
@@ -384,14 +408,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
                                    static_cast<long long>(s.qs + (real ? row / group : 0)) * p.q_stride +
                                    static_cast<long long>(h * group + (real ? row % group : 0)) * D;
-        uint32_t m = 0;
+        uint32_t big = 0;
 #pragma unroll
         for (int e = 0; e < D / 8; ++e) {
             const uint4 x = real ? __ldg(reinterpret_cast<const uint4*>(src) + e) : make_uint4(0, 0, 0, 0);
-            m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+            big = __vmaxu2(big, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
         }
         float up, down;
-        row_scale(max(m & 0xFFFFu, m >> 16), up, down);
+        row_scale(max(big & 0xFFFFu, big >> 16), up, down);
         f = p.scale * kLog2e * p.s.k_unit * down;
         see = p.causal ? (real ? s.kvl - s.ql + row / group + 1 : 0) : s.kvl;
         const int i = tid % kRowTile;
@@ -411,6 +435,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_ptr);
+    // where the row's results go
+    const long long token = s.qs + (real ? row / group : 0);
+    const int head = h * group + (real ? row % group : 0);
+    const long long at = token * p.q_heads + head;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D;
+    float* parts = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kAttCounterBytes);
+    float* mine = parts + (static_cast<size_t>(blockIdx.x) * gridDim.y + blockIdx.y) * T::kPartFloats;  // [column, maximum, sum][row]
 
     if (warp == kMmaWarp) {
         // ===== MMAs =======================================================================================
@@ -643,7 +674,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         if (a == 0 || two) {
             const uint32_t quad = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16);
             const uint32_t ts = quad + static_cast<uint32_t>(a * kKeys), to = quad + static_cast<uint32_t>(T::kO + a * D);
-            float m = -INFINITY, l = 0.f;
             uint32_t nan_groups = 0;
             const int low = p.window > 0 ? see - p.window : 0, high = min(see, s.kvl);
             for (int j = 0; j < tiles; ++j) {
@@ -710,10 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             // ---- results -----------------------------------------------------------------------------------
             if (tiles > 0) wait(o_full, 0);
             tc_fence_after();
-            const float scale = l == 0.f ? 0.f : p.s.v_unit / l;
-            const long long token = s.qs + row / group;
-            const int head = h * group + row % group;
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D;
+            const float scale = gridDim.y > 1 ? 1.f : l == 0.f ? 0.f : p.s.v_unit / l;
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
                 float v[32];
@@ -726,20 +753,60 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     v[i] = nan_groups >> (2 * q + i / 16) & 1 ? __uint_as_float(0x7FC00000u) : l == 0.f ? 0.f : v[i] * scale;
-                if (real) {
+                if (!real) continue;
+                if (gridDim.y == 1) {
+                    store32(dst + 32 * q, v);
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const __nv_bfloat162 t = __floats2bfloat162_rn(v[i + 2 * e], v[i + 2 * e + 1]);
-                            w[e] = *reinterpret_cast<const uint32_t*>(&t);
-                        }
-                        *reinterpret_cast<uint4*>(dst + 32 * q + i) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    for (int i = 0; i < 32; ++i) mine[(32 * q + i) * kRows + tid] = v[i];
                 }
             }
-            if (real && p.lse) p.lse[token * p.q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (real && gridDim.y == 1 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (real && gridDim.y > 1) {
+                mine[D * kRows + tid] = m;
+                mine[(D + 1) * kRows + tid] = l;
+            }
+        }
+    }
+    if (gridDim.y > 1) {
+        // The slices of a row tile are joined by the CTA that finishes last, in their order.
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            unsigned int* counter = static_cast<unsigned int*>(p.workspace) + blockIdx.x;
+            last_flag = atomicAdd(counter, 1u) + 1 == gridDim.y;
+            if (last_flag) *counter = 0;
+            __threadfence();
+        }
+        __syncthreads();
+        if (last_flag && real) {
+            const float* first = parts + static_cast<size_t>(blockIdx.x) * gridDim.y * T::kPartFloats + tid;
+            float top = -INFINITY;
+            for (unsigned int x = 0; x < gridDim.y; ++x) top = fmaxf(top, __ldcg(first + x * static_cast<size_t>(T::kPartFloats) + D * kRows));
+            const float base = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
+            for (unsigned int x = 0; x < gridDim.y; ++x) {
+                const float* part = first + x * static_cast<size_t>(T::kPartFloats);
+                const float lx = __ldcg(part + (D + 1) * kRows);
+                if (lx != 0.f) sum += lx * ex2(__ldcg(part + D * kRows) - base);
+            }
+            const float scale = sum == 0.f ? 0.f : p.s.v_unit / sum;
+            for (int q = 0; q < D / 32; ++q) {
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                for (unsigned int x = 0; x < gridDim.y; ++x) {
+                    const float* part = first + x * static_cast<size_t>(T::kPartFloats);
+                    if (__ldcg(part + (D + 1) * kRows) == 0.f) continue;  // a slice of which the row sees nothing
+                    const float w = ex2(__ldcg(part + D * kRows) - base);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = fmaf(w, __ldcg(part + (32 * q + i) * kRows), v[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= scale;
+                store32(dst + 32 * q, v);
+            }
+            if (p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
         }
     }
     tc_fence_before();
@@ -748,6 +815,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         tc_fence_after();
         tmem_dealloc(tmem, T::kColumns);
     }
+}
+
+// CTAs that a call's row tiles need at most: each sequence may end inside one.
+long long tiles_bound(const AttArgs& a) {
+    return (a.n * (a.q_heads / a.s.heads) / kRows + (a.seqs < a.n ? a.seqs : a.n)) * a.s.heads;
 }
 
 template <int D>
@@ -764,16 +836,23 @@ int launch_tiles(const AttArgs& a, cudaStream_t stream) {
             done[dev] = true;
         }
     }
-    const int group = a.q_heads / a.s.heads;
-    // at most this many tiles of rows: each sequence may end inside one
-    const long long most = a.n * group / kRows + (a.seqs < a.n ? a.seqs : a.n);
-    const long long grid = most * a.s.heads;
-    if (grid > 0x7FFFFFFFLL) return -7;
-    attend_tiles_kernel<D><<<static_cast<unsigned>(grid), kThreads, T::kSmem, stream>>>(a);
+    static_assert(static_cast<size_t>(T::kPartFloats) * kAttMaxSlices <= kAttPartFloatsTotal, "the slices' results fit the workspace");
+    const long long grid = tiles_bound(a);
+    // Few row tiles: the keys of each in slices, as many as fill the GPU, down to 4 key tiles a slice.
+    const int sms = attn_sm_count();
+    if (sms == 0) return -7;
+    const int room = sms < kAttMaxSlices ? sms : kAttMaxSlices;
+    long long slices = room / grid;
+    const long long most = (static_cast<long long>(a.max_pages) << a.s.page_shift) / (4 * kKeys);
+    if (slices > most) slices = most;
+    if (slices < 1) slices = 1;
+    attend_tiles_kernel<D><<<dim3(static_cast<unsigned>(grid), static_cast<unsigned>(slices)), kThreads, T::kSmem, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? 0 : -7;
 }
 
 }  // namespace
+
+bool attention_tiles_take(const AttArgs& a) { return a.s.dim <= 128 && tiles_bound(a) <= 0x7FFFFFFFLL; }
 
 int launch_attention_tiles(const AttArgs& a, cudaStream_t stream) {
     return a.s.dim == 64 ? launch_tiles<64>(a, stream) : launch_tiles<128>(a, stream);

@@ -77,10 +77,15 @@ int launch_kv_read(const KvArgs& a, cudaStream_t stream);
 int read_kv_error(unsigned int* word, int clear, cudaStream_t stream);
 
 // ---- attention (hc_attend.cu) --------------------------------------------------------------------
-constexpr int kAttMaxCtas = 512;                // CTAs of a launch whose partial results the workspace holds
-constexpr int kAttPartFloats = 32 * (128 + 2);  // one partial result: rows x (dim + maximum + sum), any variant
+// Workspace: counters, then the partial results of either kernel: 2 of each of up to 512 CTAs of hc_attend.cu, or the
+// slices of hc_attend_tiles.cu, 256 at most.
+constexpr int kAttMaxCtas = 512;
+constexpr int kAttPartFloats = 32 * (128 + 2);  // of hc_attend.cu, any variant: rows x (dim + maximum + sum)
+constexpr int kAttMaxSlices = 256;
+constexpr size_t kAttPartFloatsTotal = size_t(kAttMaxSlices) * 256 * (128 + 2);
+static_assert(size_t(2) * kAttMaxCtas * kAttPartFloats <= kAttPartFloatsTotal, "both fit");
 constexpr size_t kAttCounterBytes = kAttMaxCtas * 4;
-constexpr size_t kAttWorkspaceBytes = kAttCounterBytes + size_t(2) * kAttMaxCtas * kAttPartFloats * 4;
+constexpr size_t kAttWorkspaceBytes = kAttCounterBytes + kAttPartFloatsTotal * 4;
 struct AttArgs {
     const void* q;
     long long q_stride;
@@ -100,6 +105,7 @@ struct AttArgs {
 int launch_attention(const AttArgs& a, cudaStream_t stream);
 int read_attention_error(unsigned int* word, int clear, cudaStream_t stream);
 // many queries a sequence (hc_attend_tiles.cu), dim 64 or 128
+bool attention_tiles_take(const AttArgs& a);
 int launch_attention_tiles(const AttArgs& a, cudaStream_t stream);
 int read_tiles_error(unsigned int* word, int clear, cudaStream_t stream);
 

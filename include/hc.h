@@ -467,8 +467,8 @@ typedef struct {
     float scale;    /* of q . k, before the softmax; finite, >= 0 */
 } hc_attention_t;
 
-/* Size in bytes of the workspace of hc_kv_attention: room for the partial results of 512 CTAs and their
- * counters. The caller allocates it once [device], 16-byte aligned, fills it with zeros before its first
+/* Size in bytes of the workspace of hc_kv_attention (34,080,768: counters, and room for the partial results of
+ * sequences whose keys are spread over the GPU). The caller allocates it once [device], 16-byte aligned, fills it with zeros before its first
  * use and then keeps passing it unchanged: each call leaves the counters at zero. Calls that may run at the
  * same time (two graphs replayed on two streams, say) must not share one. Host-only, no CUDA call. */
 int hc_kv_workspace_size(size_t* bytes);

@@ -43,7 +43,7 @@ def test_sizes():
     assert hc.hc_kv_cache_size(hc.kv_shape(3, 64, 8, 128)) == 3 * 64 * 8 * 128 * 9 // 8
     # past 2^32 bytes
     assert hc.hc_kv_cache_size(hc.kv_shape(100000, 128, 8, 128)) == 100000 * 128 * 8 * 128 * 9 // 8
-    assert hc.hc_kv_workspace_size() == 512 * 4 + 2 * 512 * 32 * 130 * 4
+    assert hc.hc_kv_workspace_size() == 512 * 4 + 256 * 256 * 130 * 4 == 34080768
 
 
 @pytest.mark.parametrize("bad,status", [

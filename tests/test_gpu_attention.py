@@ -528,6 +528,25 @@ def test_attention_long_context():
     gu.device_error_clear()
 
 
+@pytest.mark.parametrize("window", [0, 700])
+@pytest.mark.parametrize("hq,hk,dim,size", [(5, 1, 128, 64), (8, 2, 64, 16)])
+def test_attention_chunk_behind_a_long_context(hq, hk, dim, size, window):
+    """A few row tiles over many keys: the keys of a tile in slices, joined in their order; one page is not there."""
+    p = Problem([(40, 3000), (33, 1201)], hq, hk, dim, size, seed=hq).to_device()
+    if window == 0:
+        p.table[0, 3] = -1
+        p.d["table"] = ints(p.table, torch.int32)
+    w = hc.new_kv_workspace()
+    out, lse = p.run(window=window, ws=w)
+    p.check(out, lse, window=window)
+    assert hc.hc_device_error(clear=True) == (1 << 20 if window == 0 else 0)
+    for _ in range(3):
+        again, lagain = p.run(window=window, ws=w)
+        assert torch.equal(out, again) and torch.equal(lse, lagain)
+    assert (w[:2048] == 0).all()
+    hc.hc_device_error(clear=True)
+
+
 @pytest.mark.parametrize("seqs", [300, 1000])
 def test_attention_many_sequences(seqs):
     rng = np.random.default_rng(seqs)
