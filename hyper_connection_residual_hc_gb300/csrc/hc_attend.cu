@@ -127,11 +127,10 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 __device__ __forceinline__ void wait_copy(uint32_t bar, uint32_t parity) {
-    if (mbar_test(bar, parity)) return;
+    if (mbar_sleep(bar, parity)) return;
     const uint64_t t0 = global_timer_ns();
     while (true) {
-        for (int i = 0; i < 32; ++i)
-            if (mbar_test(bar, parity)) return;
+        if (mbar_sleep(bar, parity)) return;
         if (global_timer_ns() - t0 > kWaitNs) {
             atomicOr(&g_hc_attention_error, kErrCopy);
             return;

@@ -68,11 +68,10 @@ struct TilePlan {
 struct Wait {
     volatile uint32_t* abort;
     __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) const {
-        if (mbar_test(bar, parity)) return;
+        if (mbar_sleep(bar, parity)) return;
         const uint64_t t0 = global_timer_ns();
         while (true) {
-            for (int i = 0; i < 32; ++i)
-                if (mbar_test(bar, parity)) return;
+            if (mbar_sleep(bar, parity)) return;
             if (*abort) return;
             if (global_timer_ns() - t0 > kWaitNs) {
                 *abort = 1u;

@@ -24,6 +24,20 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 
+// A probe of an mbarrier's phase that lets the warp sleep for up to a millisecond while the phase is not complete: a
+// warp that polls instead takes issue slots from those it waits for.
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+}
+
 // The power of two that brings a query row whose largest magnitude has the bf16 bits m to [2^7, 2^8): bf16's 8 bits
 // are then exact in fp16 down to 2^-14, and sums stay far below fp32's range. NaN and infinity stay what they are.
 __device__ __forceinline__ void row_scale(uint32_t m, float& up, float& down) {
