@@ -43,6 +43,7 @@ constexpr int kRowTile = 128;   // rows of an MMA
 constexpr int kRows = 2 * kRowTile;
 constexpr int kKeys = 128;      // keys of a tile
 constexpr int kSoftmaxWarps = 8, kDequantWarps = 4;
+static_assert(kDequantWarps == 4, "a word of notes");
 constexpr int kBlocksPerWarp = kKeys / 16 / kDequantWarps;  // cache blocks of a key tile that a dequantising warp takes
 constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     __shared__ int scan[kThreads / 32 + 1];
     __shared__ int found_seq, found_tile;
     __shared__ bool last_flag;
-    __shared__ uint32_t absent[kNotes][kDequantWarps];  // per key tile: bits of the blocks that are not there
+    __shared__ __align__(4) uint8_t absent[kNotes][kDequantWarps];  // per key tile and warp: bits of its blocks that are not there
     __shared__ uint32_t nan_any[kNotes];                // per key tile: some value's scale is NaN
     const uint32_t sbase = smem_u32(smem);
     const int tid = static_cast<int>(threadIdx.x), warp = tid / 32, lane = tid % 32;
@@ -467,21 +468,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             for (int st = 1; st < kKeys / 32; ++st)
                 mma_ts(lead, d, w + static_cast<uint32_t>(st * 8), v + static_cast<uint64_t>(st * 2048 / 16), id_o, 1u);
         };
+        // Keys and values are waited for right after the scores have been issued, ahead of their use: a wait takes a hundred
+        // cycles even where nothing is waited for, and between the weights' arrival and their product it would show.
         if (tiles > 0) {
             wait(k_full(0), 0);
             tc_fence_after();
             for (int a = 0; a < na; ++a) scores(a, 0);
             commit(lead, k_empty(0));
+            wait(v_full(0), 0);
+            if (tiles > 1) wait(k_full(1), 0);
         }
         for (int j = 0; j < tiles; ++j) {
             for (int a = 0; a < na; ++a) {
-                if (a == 0) wait(v_full(j % 2), j / 2 & 1);
                 wait(p_full(a, 0), j & 1);
                 __syncwarp();
                 tc_fence_after();
                 outputs(a, j, 0);
                 wait(p_full(a, 1), j & 1);
-                if (a == 0 && j + 1 < tiles) wait(k_full((j + 1) % 2), (j + 1) / 2 & 1);
                 __syncwarp();
                 tc_fence_after();
                 outputs(a, j, 1);
@@ -491,6 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                     if (a == na - 1) commit(lead, k_empty((j + 1) % 2));
                 }
             }
+            if (j + 1 < tiles) wait(v_full((j + 1) % 2), (j + 1) / 2 & 1);
+            if (j + 2 < tiles) wait(k_full(j % 2), (j + 2) / 2 & 1);
         }
         commit(lead, o_full);
         if (lead) wait.drain(o_full, 0);
@@ -602,8 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                 if (w == 0) nan_any[(j + 2) % kNotes] = 0;
                 uint32_t off = 0;
 #pragma unroll
-                for (int i = 0; i < kBlocksPerWarp; ++i) off |= there[i] ? 0u : 1u << (kBlocksPerWarp * w + i);
-                absent[note][w] = off;
+                for (int i = 0; i < kBlocksPerWarp; ++i) off |= there[i] ? 0u : 1u << i;
+                absent[note][w] = static_cast<uint8_t>(off);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -679,9 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                 wait(s_full(a), j & 1);
                 tc_fence_after();
                 const int tok0 = (block0 + 8 * j) * 16;
-                uint32_t gone = 0;
-#pragma unroll
-                for (int w = 0; w < kDequantWarps; ++w) gone |= *reinterpret_cast<volatile uint32_t*>(&absent[j % kNotes][w]);
+                uint32_t gone = *reinterpret_cast<volatile uint32_t*>(&absent[j % kNotes]);  // the four warps' bytes, two bits each
+                if (gone) gone = (gone & 3u) | (gone >> 6 & 12u) | (gone >> 12 & 48u) | (gone >> 18 & 192u);
                 const bool whole = tok0 >= g.all_lo && tok0 + kKeys <= g.all_hi && gone == 0;
                 // this row sees columns [from, upto) of the tile, but for blocks that are not there
                 const int from = low - tok0, upto = high - tok0;
