@@ -16,7 +16,9 @@ post_then_pre (the default step), pre_step, expand_pre_step (head of the stack),
 and final (tail of the stack, eps 1e-20), post (writing half alone), decode_chain (80 sublayers on 256
 tokens captured in one CUDA graph); or the step on the other single-step workloads: step_b1_t64 (one
 hc_post_then_pre on 64 tokens, each launch timed alone with L2 flushed before it: latency) and
-long_prefill_b1_t65536 (one hc_post_then_pre on 65,536 tokens).
+long_prefill_b1_t65536 (one hc_post_then_pre on 65,536 tokens); or attention_decode (the attention
+sublayer's decode step of 256 sequences: hc_qk_norm_rope, hc_kv_write, hc_kv_attention over contexts
+of 2,048 to 4,096 tokens, from the fused projection's output to the heads' output).
 """
 
 from __future__ import annotations
@@ -755,6 +757,148 @@ def run_decode_chain(args):
         dist.destroy_process_group()
 
 
+ATTENTION_METRIC = "attention sublayer tokens/s and achieved HBM GB/s vs peak, decode of 256 sequences"
+ATT = dict(seqs=256, q_heads=40, kv_heads=8, dim=128, page_size=64, longest=4096, shortest=2048, theta=10000.0)
+
+
+def attention_lengths():
+    """Keys of each sequence with its new token: spread evenly from the shortest to the longest, in no order."""
+    n = ATT["seqs"]
+    return [ATT["shortest"] + (i * 37 % n) * (ATT["longest"] - ATT["shortest"]) // (n - 1) for i in range(n)]
+
+
+def attention_step_bytes():
+    """What a decode step cannot do without: q, k and v in and the heads' output out (bf16; the rotated queries and keys
+    are written and read on the way, which a fused step would not), the keys' and values' 4.5 bits each, the new ones' too."""
+    n, hq, hk, d = ATT["seqs"], ATT["q_heads"], ATT["kv_heads"], ATT["dim"]
+    return 2 * n * (2 * hq + 2 * hk) * d + (sum(attention_lengths()) + n) * hk * d * 9 // 8
+
+
+def attention_config():
+    return dict(ATT, workload="decode_attention_b256", entry_point="hc_qk_norm_rope, hc_kv_write, hc_kv_attention",
+                tokens_per_gpu=ATT["seqs"], cache="4 bits a value, scales of 8 bits for 16",
+                l2="no flush: the keys and values of a step (%d MB) exceed the 129 MB L2" % (attention_step_bytes() // 10 ** 6))
+
+
+def run_attention_decode(args):
+    """The attention sublayer's decode step on 256 sequences. Timed by CUDA events around each step's three calls."""
+    import torch
+
+    import hyper_connection_residual_hc_gb300 as hc
+
+    rank, world, local = _dist()
+    torch.cuda.set_device(local)
+    dist = None
+    if world > 1:
+        import torch.distributed as dist
+        dist.init_process_group("nccl", device_id=torch.device("cuda", local))
+    n, hq, hk, d, size = (ATT[k] for k in ("seqs", "q_heads", "kv_heads", "dim", "page_size"))
+    lens = attention_lengths()
+    g = torch.Generator(device="cuda").manual_seed(1000 + rank)
+    per = -(-ATT["longest"] // size)
+    shape = hc.kv_shape(n * per, size, hk, d)
+    cache = torch.empty(hc.hc_kv_cache_size(shape), dtype=torch.uint8, device="cuda")
+    pages = torch.randperm(n * per, generator=g, device="cuda").int().reshape(n, per)
+    for i in range(per):  # the contexts, a page of every sequence at a time
+        kv = torch.randn((n * size, 2 * hk * d), generator=g, device="cuda", dtype=torch.bfloat16)
+        slots = (pages[:, i:i + 1].long() * size + torch.arange(size, device="cuda")).reshape(-1)
+        hc.hc_kv_write(kv, 2 * hk * d, kv[:, hk * d:], 2 * hk * d, slots, n * size, shape, cache)
+    freq = [ATT["theta"] ** (-2.0 * j / d) for j in range(d // 2)]
+    table = torch.empty(hc.hc_rope_table_size(d), dtype=torch.uint8, device="cuda")
+    hc.hc_prepare_rope(freq, None, d, 1, table)
+    qw = 1 + 0.1 * torch.randn(d, generator=g, device="cuda")
+    kw = 1 + 0.1 * torch.randn(d, generator=g, device="cuda")
+    host = {"qkv": torch.randn((n, (hq + 2 * hk) * d), dtype=torch.bfloat16).pin_memory()}
+    last = torch.tensor(lens) - 1
+    host["positions"] = last[None].contiguous().pin_memory()
+    host["slots"] = (torch.gather(pages.cpu().long(), 1, (last // size)[:, None])[:, 0] * size + last % size).pin_memory()
+    host["kv_len"] = torch.tensor(lens, dtype=torch.int32).pin_memory()
+    dev = {k: v.cuda() for k, v in host.items()}
+    q_start = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    roped = torch.empty((n, (hq + hk) * d), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty((n, hq * d), dtype=torch.bfloat16, device="cuda")
+    out_host = torch.empty(out.shape, dtype=out.dtype, pin_memory=True)
+    ws = hc.new_kv_workspace()
+    r, heads = hc.rope(table, d), hc.heads(hq, hk, d)
+    a = hc.attention(n, n, 1, per, hq, d ** -0.5)
+    stream = torch.cuda.current_stream()
+
+    def step():
+        qkv, st, w = dev["qkv"], (hq + 2 * hk) * d, (hq + hk) * d
+        hc.hc_qk_norm_rope(qkv, st, qkv[:, hq * d:], st, qw, kw, dev["positions"], r, n, heads, roped, w, roped[:, hq * d:], w, stream)
+        hc.hc_kv_write(roped[:, hq * d:], w, qkv[:, w:], st, dev["slots"], n, shape, cache, stream)
+        hc.hc_kv_attention(roped, w, q_start, dev["kv_len"], pages, cache, a, shape, out, hq * d, None, ws, stream)
+
+    def barrier():
+        torch.cuda.synchronize()
+        if dist is not None:
+            dist.barrier()
+        torch.cuda.synchronize()
+
+    warmup = max(3, args.warmup)
+    for _ in range(warmup):
+        step()
+    barrier()
+    werr = hc.hc_device_error(clear=True)
+    clocks = ClockSampler(local)
+    clocks.start()
+    ev = [(torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)) for _ in range(args.steps)]
+    t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    barrier()
+    t0.record(stream)
+    for b, e in ev:
+        b.record(stream)
+        step()
+        e.record(stream)
+    t1.record(stream)
+    barrier()
+    clk = clocks.stop()
+    per_step = sorted(b.elapsed_time(e) for b, e in ev)
+    el_ms = max_over_ranks(t0.elapsed_time(t1), dist, "cuda")
+    derr = hc.hc_device_error(clear=True)
+
+    e2e_steps = max(3, min(50, args.steps))
+
+    def e2e_step():
+        for k in dev:
+            dev[k].copy_(host[k], non_blocking=True)
+        step()
+        out_host.copy_(out, non_blocking=True)
+        stream.synchronize()
+
+    for _ in range(10):
+        e2e_step()
+    barrier()
+    w0 = time.perf_counter()
+    for _ in range(e2e_steps):
+        e2e_step()
+    barrier()
+    e2e_s = max_over_ranks(time.perf_counter() - w0, dist, "cuda")
+    if rank == 0:
+        peak, peak_kind = _peaks()
+        med = statistics.median(per_step)
+        achieved = attention_step_bytes() / (med / 1e3) / 1e9
+        line = {
+            "metric": ATTENTION_METRIC, "value": whole_job_rate(n * args.steps, world, el_ms / 1e3), "unit": "tokens/s",
+            "n_gpus": world, "steps": args.steps, "warmup": warmup, "ms_per_step": el_ms / args.steps,
+            "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16 in and out, 4-bit cache, f32 sums",
+            "data": "synthetic", "config": attention_config(),
+            "latency_us": {"median": 1e3 * med, "best": 1e3 * per_step[0]},
+            "roofline": {"bound": "HBM", "achieved": achieved, "peak": peak, "unit": "GB/s", "frac": achieved / peak,
+                         "peak_kind": peak_kind, "algorithmic_bytes": attention_step_bytes()},
+            "e2e": {"value": whole_job_rate(n * e2e_steps, world, e2e_s), "unit": "tokens/s",
+                    "h2d_bytes_per_step": sum(v.numel() * v.element_size() for v in host.values()),
+                    "d2h_bytes_per_step": out.numel() * 2},
+            "clocks": {"sm_mhz": clk["sm_mhz"], "sm_max_mhz": clk["sm_max_mhz"], "reasons": clk["reasons"],
+                       "samples": clk["samples"]},
+            "gpu_launches": 3 * args.steps, "device_error": werr | derr,
+        }
+        print(json.dumps(line), flush=True)
+    if dist is not None:
+        dist.barrier()
+        dist.destroy_process_group()
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -764,12 +908,18 @@ def main():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--e2e-chunk", type=int, default=0,
                     help="tokens per chunk of the host-buffer executor in the end-to-end run (0: the library's default)")
-    ap.add_argument("--op", default="post_then_pre", choices=sorted(OPS) + ["decode_chain"])
+    ap.add_argument("--op", default="post_then_pre", choices=sorted(OPS) + ["attention_decode", "decode_chain"])
     args = ap.parse_args()
-    if args.impl == "reference":
+    if args.impl == "reference" and args.op == "attention_decode":
+        if _dist()[0] == 0:
+            print(json.dumps({"impl": "reference", "unavailable": "the pages do not show the attention sublayer and the oracle has no "
+                                                                  "version of it"}), flush=True)
+    elif args.impl == "reference":
         run_reference(args)
     elif args.op == "decode_chain":
         run_decode_chain(args)
+    elif args.op == "attention_decode":
+        run_attention_decode(args)
     else:
         run_ours(args)
 

@@ -250,3 +250,15 @@ def test_symbols_are_bound():
     for name in ("hc_rope_table_size", "hc_prepare_rope", "hc_qk_norm_rope", "hc_kv_cache_size", "hc_kv_write", "hc_kv_read",
                  "hc_kv_workspace_size", "hc_kv_attention"):
         assert name in hc.SYMBOLS and getattr(lib, name).restype is ctypes.c_int
+
+
+def test_bench_counts_the_decode_step():
+    """bench.py's attention step: lengths that span its range, and the bytes that the step cannot do without."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    import bench
+    lens = bench.attention_lengths()
+    assert len(lens) == 256 and min(lens) == 2048 and max(lens) == 4096 and len(set(lens)) == 256
+    # q 5120, k and v 1024 each, out 5120 columns of bf16 a token; 1152 bytes of keys and values of 8 heads a cached token
+    assert bench.attention_step_bytes() == 256 * (2 * 5120 + 2 * 1024) * 2 + (sum(lens) + 256) * 2 * 576
