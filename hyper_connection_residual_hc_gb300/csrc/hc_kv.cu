@@ -40,11 +40,15 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kGroup = 16;                 // tokens of the call per block
 constexpr int kWindow = 3 * kGroup - 2;    // slots looked at: 15 before the group, 15 after it
 
-// the largest magnitude's bits (the sign bit cleared, bf16 orders as its bits; NaN above infinity)
+// the bits of the largest magnitude of bf16 pairs; a NaN's (above infinity's) if there is one
 __device__ __forceinline__ uint32_t amax_bits(const uint32_t* w, int words) {
     uint32_t m = 0;
-    for (int i = 0; i < words; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
-    return max(m & 0xFFFFu, m >> 16);
+    for (int i = 0; i < words; ++i) {
+        uint32_t x;
+        asm("abs.bf16x2 %0, %1;" : "=r"(x) : "r"(w[i]));
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(x));
+    }
+    return max(m & 0x7FFFu, m >> 16 & 0x7FFFu);
 }
 
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax, float inv_unit) {
