@@ -7,6 +7,13 @@
 // The tensor memory path (tcgen05) would have to write every dequantised block to shared memory first, 8 times
 // the bytes that the cache has; this kernel's bound is the dequantisation and HBM, not the products.
 //
+// Measured: 256 sequences of 2,050 to 4,096 keys, 40 query and 8 kv heads of 128 (912 MB): 215 us, 4.25 TB/s, 63% of the
+// measured copy rate; 3 sequences of up to 131,072 keys: 84 us, 66%; 8 of up to 509 keys: 8.9 us. With few rows what is
+// left is instructions: about 600 for a unit of 32 keys of a head (128 conversions from 4 bits, about as many products with
+// scales, 32 MMAs), issue slots 58% busy, no pipe above half; leaving out the keys' scale products would save 7 us,
+// two warps a unit (258 us) or blocks of 4 warps (255 us) lose. More rows cost more of everything: five queries of 4 heads each, 64 sequences, window of
+// 1,024 keys (81 MB): 68 us.
+//
 // A cache block (16 tokens, one head) is laid out in A-fragment order: lane (r, c) = (lane / 4, lane % 4) finds
 // in its own 32-bit words the codes of keys r and r + 8, columns [c D/4, (c+1) D/4) (the contraction index of
 // the product may run in any order, so a lane takes whole 16-column groups and needs few scales), and of values
@@ -216,6 +223,8 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
         }
         return x;
     };
+    // The tiles' kernel comes behind this one (launch_attention): its CTAs may move in as soon as SMs are free.
+    if (p.q_max != kAnyQueries) griddep_launch_dependents();
     // A sequence's segments, and its units where segments may be cut.
     long long segments = 0, units = 0;
     bool long_one = false;
@@ -395,7 +404,7 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
             for (int j = 0; j < 2; ++j) {
                 if constexpr (kSplit == 2) f[t][j] = factors[8 * t + 2 * c + j];
                 const int col = row0 + 8 * t + 2 * c + j;
-                see[t][j] = p.causal ? (col < rows ? pos0 + col / group + 1 : 0x7FFFFFFF) : g.s.kvl;
+                see[t][j] = p.causal ? (col < rows ? max(pos0 + col / group + 1, 0) : 0x7FFFFFFF) : g.s.kvl;
             }
         float m[kNT][2], l[kNT][2], o[kTiles][kNT][4];
 #pragma unroll
@@ -852,11 +861,8 @@ int launch_rows(const AttArgs& a, cudaStream_t stream) {
     return cudaGetLastError() == cudaSuccess ? 0 : -7;
 }
 
-}  // namespace
-
-int launch_attention(const AttArgs& a, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(a.max_q_len) * (a.q_heads / a.s.heads);
-    if (rows >= kTilesFromRows && attention_tiles_take(a)) return launch_attention_tiles(a, stream);
+// `rows`: of the sequences that the call's tiles are made for
+int launch_rows_for(long long rows, const AttArgs& a, cudaStream_t stream) {
     switch (a.s.dim) {
         case 64:
             if (rows <= 8) return launch_rows<64, 1, 1>(a, stream);
@@ -871,6 +877,30 @@ int launch_attention(const AttArgs& a, cudaStream_t stream) {
             if (rows <= 8) return launch_rows<256, 1, 2>(a, stream);
             return launch_rows<256, 2, 2>(a, stream);
     }
+}
+
+}  // namespace
+
+int launch_attention(const AttArgs& args, cudaStream_t stream) {
+    AttArgs a = args;
+    a.q_min = 0;
+    a.q_max = kAnyQueries;
+    const int group = a.q_heads / a.s.heads;
+    const long long rows = static_cast<long long>(a.max_q_len) * group;
+    if (rows < kTilesFromRows || !attention_tiles_take(a)) return launch_rows_for(rows, a, stream);
+    // Sequences of a single query, or so few that they fit the same tile of rows, among longer ones (chunks of a prefill in
+    // a batch that decodes) get a launch of their own. 255 single queries over 2,050 to 4,096 keys and one chunk of 2,305,
+    // 40 and 8 heads of 128: 510 us, 1,070 us where the tiles' kernel takes all; with a chunk of 513, 299 us. Where no
+    // sequence is short the launch costs 8 us, so n = seqs * max_q_len (none is) goes without.
+    const int few = group <= 32 ? (group + 7) / 8 * 8 / group : 0;
+    if (few > 0 && a.n != static_cast<long long>(a.seqs) * a.max_q_len) {
+        a.q_max = few;
+        const int st = launch_rows_for(static_cast<long long>(few) * group, a, stream);
+        if (st != 0) return st;
+        a.q_min = few + 1;
+        a.q_max = kAnyQueries;
+    }
+    return launch_attention_tiles(a, stream);
 }
 
 int read_attention_error(unsigned int* word, int clear, cudaStream_t stream) {

@@ -15,9 +15,15 @@
 // memory are rarely rescaled. S_a of the next tile is issued behind P_a V of this one: a thread that sees its scores
 // knows that its outputs are complete.
 //
-// Per key tile of 256 rows at D = 128 the tensor cores work 4 x 512 cycles, the exponentials take 2,048 cycles of
-// the SM's special function units, the shared memory about as long (operand reads 192 KB, dequantised writes
-// 64 KB at 128 bytes a cycle): three limits of the same size.
+// Few row tiles with many keys: the key tiles of each are cut into slices, one CTA each (gridDim.y), joined in their order by
+// the CTA that finishes last.
+//
+// Measured: 2 sequences of 2,048 queries behind 4,096 to 6,144 cached keys, 40 query and 8 kv heads of 128: 541 us, 952
+// TFLOP/s, 49% of the measured cuBLAS rate (the first form, with separate score and value steps by 17 warps of 96 registers,
+// took 1,806 us). Of the same call the MMAs alone take 302 us, dequantising alone 278 us, the softmax alone with its barriers 444 us, and its barriers
+// alone 283 us: the round trip scores -> weights -> scores is what bounds it, with two row tiles to overlap. Tried and
+// slower: 16 softmax warps with half a row each (604 us), an MMA warp that polls for whichever row tile is ready (704 us:
+// its polling takes issue slots), 8 dequantising warps (630 us).
 //
 // Every wait is bounded: on expiry the kernel sets a bit of the device error word, stops waiting, lets its MMAs end
 // and frees its tensor memory.
@@ -349,7 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         }
         __syncthreads();
     }
-    if (found_seq < 0) return;  // more CTAs than tiles
+    if (found_seq < 0) {  // more CTAs than tiles
+        griddep_wait();
+        return;
+    }
     const int b = found_seq, tile = found_tile;
     const SeqRows s = load_seq(p, b, nullptr);
     const int rows = s.ql * group, row0 = tile * kRows;
@@ -417,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         float up, down;
         row_scale(max(big & 0xFFFFu, big >> 16), up, down);
         f = p.scale * kLog2e * p.s.k_unit * down;
-        see = p.causal ? (real ? s.kvl - s.ql + row / group + 1 : 0) : s.kvl;
+        see = p.causal ? (real ? max(s.kvl - s.ql + row / group + 1, 0) : 0) : s.kvl;
         const int i = tid % kRowTile;
         const uint32_t base = sbase + T::kQ + static_cast<uint32_t>(tid / kRowTile * T::kTile + i * 128);
 #pragma unroll
@@ -743,6 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             // ---- results -----------------------------------------------------------------------------------
             if (tiles > 0) wait(o_full, 0);
             tc_fence_after();
+            if (gridDim.y > 1) griddep_wait();  // the kernel ahead may use the workspace
             const float scale = gridDim.y > 1 ? 1.f : l == 0.f ? 0.f : p.s.v_unit / l;
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
@@ -812,6 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             if (p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
         }
     }
+    griddep_wait();  // the call has ended when both kernels have
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
@@ -820,9 +831,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     }
 }
 
-// CTAs that a call's row tiles need at most: each sequence may end inside one.
+// CTAs that a call's row tiles need at most: each of its sequences may end inside one.
 long long tiles_bound(const AttArgs& a) {
-    return (a.n * (a.q_heads / a.s.heads) / kRows + (a.seqs < a.n ? a.seqs : a.n)) * a.s.heads;
+    const long long most = a.q_min > 1 ? a.n / a.q_min : a.n;
+    return (a.n * (a.q_heads / a.s.heads) / kRows + (a.seqs < most ? a.seqs : most)) * a.s.heads;
 }
 
 template <int D>
@@ -841,6 +853,7 @@ int launch_tiles(const AttArgs& a, cudaStream_t stream) {
     }
     static_assert(static_cast<size_t>(T::kPartFloats) * kAttMaxSlices <= kAttPartFloatsTotal, "the slices' results fit the workspace");
     const long long grid = tiles_bound(a);
+    if (grid == 0) return 0;  // no sequence can have q_min queries
     // Few row tiles: the keys of each in slices, as many as fill the GPU, down to 4 key tiles a slice.
     const int sms = attn_sm_count();
     if (sms == 0) return -7;
@@ -849,8 +862,19 @@ int launch_tiles(const AttArgs& a, cudaStream_t stream) {
     const long long most = (static_cast<long long>(a.max_pages) << a.s.page_shift) / (4 * kKeys);
     if (slices > most) slices = most;
     if (slices < 1) slices = 1;
-    attend_tiles_kernel<D><<<dim3(static_cast<unsigned>(grid), static_cast<unsigned>(slices)), kThreads, T::kSmem, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? 0 : -7;
+    // Behind a launch for the sequences of few queries this kernel may start before that one has ended: it reads
+    // nothing of it, and waits for it before it touches the workspace.
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>(slices));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = T::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = a.q_min > 0 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, attend_tiles_kernel<D>, a) == cudaSuccess ? 0 : -7;
 }
 
 }  // namespace

@@ -86,6 +86,7 @@ constexpr size_t kAttPartFloatsTotal = size_t(kAttMaxSlices) * 256 * (128 + 2);
 static_assert(size_t(2) * kAttMaxCtas * kAttPartFloats <= kAttPartFloatsTotal, "both fit");
 constexpr size_t kAttCounterBytes = kAttMaxCtas * 4;
 constexpr size_t kAttWorkspaceBytes = kAttCounterBytes + kAttPartFloatsTotal * 4;
+constexpr int kAnyQueries = 0x7FFFFFFF;
 struct AttArgs {
     const void* q;
     long long q_stride;
@@ -101,6 +102,7 @@ struct AttArgs {
     long long out_stride;
     float* lse;
     void* workspace;
+    int q_min, q_max;  // a kernel takes the sequences with so many queries and leaves the others to the other kernel
 };
 int launch_attention(const AttArgs& a, cudaStream_t stream);
 int read_attention_error(unsigned int* word, int clear, cudaStream_t stream);

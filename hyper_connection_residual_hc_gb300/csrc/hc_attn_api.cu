@@ -252,7 +252,8 @@ int hc_kv_attention(const void* q, int64_t q_stride, const int* q_start, const i
     const int st = check_kv_shape(s, &g.s);
     if (st != HC_OK) return st;
     if (a.n < 0 || a.n > kMaxRows || a.seqs < 0 || a.max_q_len < 0 || a.max_pages < 1) return HC_ERR_SHAPE;
-    if (static_cast<int64_t>(a.max_pages) * s.page_size > kMaxRows) return HC_ERR_SHAPE;  // positions are 32-bit
+    // positions are 32-bit, with room for what the kernels add to them; so are the sequences' numbers
+    if (static_cast<int64_t>(a.max_pages) * s.page_size > (1LL << 30) || a.seqs > 1 << 24) return HC_ERR_SHAPE;
     if (a.q_heads < 1 || a.q_heads % s.heads != 0 || a.q_heads / s.heads > 128) return HC_ERR_SHAPE;
     if (a.n * (a.q_heads / s.heads) > kMaxRows) return HC_ERR_SHAPE;  // rows are counted in 32 bits
     const int64_t w = static_cast<int64_t>(a.q_heads) * s.dim;

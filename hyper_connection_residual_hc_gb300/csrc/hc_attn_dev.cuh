@@ -47,7 +47,7 @@ __device__ __forceinline__ void row_scale(uint32_t m, float& up, float& down) {
 }
 
 struct SeqRows {
-    int qs, ql, kvl;  // first row of q, queries, keys
+    int qs, ql, kvl;  // first row of q, queries (0: another kernel takes the sequence), keys
 };
 
 // `tell`: the error word to note clamped bounds in, or null
@@ -61,6 +61,7 @@ __device__ __forceinline__ SeqRows load_seq(const AttArgs& p, int b, unsigned in
     s.ql = qe - s.qs;
     s.kvl = min(max(kv, 0), most);
     if (tell && (s.qs != q0 || qe != q1 || s.kvl != kv)) atomicOr(tell, kErrSeq);
+    if (s.ql < p.q_min || s.ql > p.q_max) s.ql = 0;
     return s;
 }
 
@@ -76,8 +77,9 @@ __device__ __forceinline__ TileBounds tile_bounds(const AttArgs& p, const SeqRow
         const int first = pos0 + row0 / group, last = pos0 + row1 / group;
         g.hi = min(max(last + 1, 0), s.kvl);
         g.all_hi = first + 1;
-        g.lo = p.window > 0 ? max(0, first + 1 - p.window) : 0;
-        g.all_lo = p.window > 0 ? max(0, last + 1 - p.window) : 0;
+        // (positions are negative where a sequence has more queries than keys; a window is as large as an int)
+        g.lo = p.window > 0 ? max(0, max(first + 1, 0) - p.window) : 0;
+        g.all_lo = p.window > 0 ? max(0, max(last + 1, 0) - p.window) : 0;
     } else {
         g.hi = g.all_hi = s.kvl;
         g.lo = g.all_lo = 0;

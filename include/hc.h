@@ -458,9 +458,9 @@ int hc_kv_read(const void* cache, const int64_t* slots, int64_t n, hc_kv_shape_t
 /* A call of hc_kv_attention. */
 typedef struct {
     int64_t n;      /* rows of q and out: the queries of all sequences; n * q_heads / heads at most 2^31 - 1 */
-    int seqs;       /* sequences, >= 0 */
+    int seqs;       /* sequences, 0..2^24 */
     int max_q_len;  /* queries of the longest sequence: sizes the tiles (longer ones are right, but slower) */
-    int max_pages;  /* columns of the page table */
+    int max_pages;  /* columns of the page table, >= 1; max_pages * page_size at most 2^30 */
     int q_heads;    /* a multiple of the cache's heads, up to 128 times as many: head h reads kv head h * heads / q_heads */
     int causal;     /* 1: a query sees the keys up to its own position; 0: all keys of its sequence */
     int window;     /* > 0 (causal only): a query sees the last `window` of those keys; 0: all */

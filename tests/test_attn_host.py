@@ -164,7 +164,7 @@ def test_attention_refusals():
     for i in (0, 2, 3, 4, 5, 8, 11):
         _expect(hc.HC_ERR_NULL, f, *_with(ok, **{"_%d" % i: None}))
     for k in (dict(n=-1), dict(n=1 << 31), dict(seqs=-1), dict(max_q_len=-1), dict(max_pages=0), dict(q_heads=0), dict(q_heads=41),
-              dict(q_heads=8 * 129), dict(max_pages=1 << 25)):
+              dict(q_heads=8 * 129), dict(max_pages=1 << 25), dict(max_pages=(1 << 24) + 1), dict(seqs=(1 << 24) + 1)):
         _expect(hc.HC_ERR_SHAPE, f, *_with(ok, _6=mk(**k), _1=1 << 18, _9=1 << 18))
     _expect(hc.HC_ERR_SHAPE, f, *_with(ok, _1=5112))
     _expect(hc.HC_ERR_SHAPE, f, *_with(ok, _9=5124))

@@ -376,6 +376,15 @@ def test_attention_window(lens, window, hq, hk, dim, size):
     gu.device_error_clear()
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5])
+@pytest.mark.parametrize("hq,hk,dim", [(5, 1, 128), (4, 2, 64), (2, 1, 256)])
+def test_attention_widest_window_with_fewer_keys_than_queries(hq, hk, dim, window):
+    for lens in ([(5, 3), (1, 20), (3, 0)], [(70, 40), (5, 3)]):
+        p = Problem(lens, hq, hk, dim, 32, seed=5).to_device()
+        out, lse = p.run(window=window)
+        p.check(out, lse)
+
+
 @pytest.mark.parametrize("hq,hk,dim", [(5, 1, 128), (4, 2, 64), (2, 1, 256)])
 def test_attention_without_causal_mask(hq, hk, dim):
     p = Problem([(4, 50), (20, 133), (3, 0), (150, 64)], hq, hk, dim, 32, seed=3).to_device()
@@ -405,6 +414,23 @@ def test_attention_right_for_any_longest_query_hint(hint):
     p = Problem([(9, 120), (1, 33), (200, 260)], 5, 1, 128, 32, seed=12).to_device()
     out, lse = p.run(max_q_len=hint)
     p.check(out, lse)
+
+
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("hq,hk,dim", [(1, 1, 64), (5, 1, 128), (16, 2, 64), (32, 1, 128), (34, 1, 128), (2, 1, 256)])
+def test_attention_chunks_among_single_tokens(hq, hk, dim, window):
+    """Sequences on either side of every border between few queries and many, in one batch; then a batch too small for
+    its own hint."""
+    p = Problem([(1, 70), (300, 400), (1, 0), (0, 5), (2, 33), (8, 50), (9, 60), (1, 513), (40, 40)], hq, hk, dim, 32, seed=hq).to_device()
+    out, lse = p.run(window=window)
+    p.check(out, lse, window=window)
+    again, lagain = p.run(window=window)
+    assert torch.equal(out, again) and torch.equal(lse, lagain)
+    gu.device_error_clear()
+    p = Problem([(1, 70), (0, 3), (2, 90)], hq, hk, dim, 32, seed=hq).to_device()
+    out, lse = p.run(window=window, max_q_len=500)
+    p.check(out, lse, window=window)
+    gu.device_error_clear()
 
 
 @pytest.mark.parametrize("scale", [1.0, 30.0])
