@@ -433,6 +433,28 @@ def test_attention_chunks_among_single_tokens(hq, hk, dim, window):
     gu.device_error_clear()
 
 
+@pytest.mark.parametrize("hq,hk,dim", [(5, 1, 128), (16, 2, 64)])
+def test_attention_chunk_among_single_tokens_replayed(hq, hk, dim):
+    """Both kernels of such a call cut their keys, and so use the workspace; calls follow each other in one graph."""
+    p = Problem([(1, 6000), (40, 5000), (1, 4100)], hq, hk, dim, 64, seed=21).to_device()
+    out, lse = p.run()
+    p.check(out, lse)
+    ws = hc.new_kv_workspace()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        results = [p.run(ws=ws, fill=float(i)) for i in range(3)]
+    for _ in range(3):
+        for o, l in results:
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for o, l in results:
+            assert torch.equal(o, out) and torch.equal(l, lse)
+    assert (ws[:2048] == 0).all()  # the counters
+    gu.device_error_clear()
+
+
 @pytest.mark.parametrize("scale", [1.0, 30.0])
 def test_attention_with_large_and_growing_scores(scale):
     """Scores of hundreds whose maximum comes late: a running maximum that rises at every step."""
