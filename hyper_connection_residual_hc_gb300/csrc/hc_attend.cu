@@ -51,7 +51,10 @@ __device__ unsigned int g_hc_attention_error = 0;
 
 constexpr uint64_t kWaitNs = 1000000000ull;   // 1 s
 constexpr int kUnit = 32;                     // tokens a warp takes at a time: two cache blocks
-constexpr int kWholeSteps = 4;                // segments of at most so many units a warp are not cut (see the kernel)
+// What it costs a CTA to have segments cut, in steps of its teams: left whole, they may take so many steps longer. 64 sequences
+// of 5 queries with a window of 1,024 keys, 18 steps whole, 14 cut: 57 us whole, 66 us cut; 8 of up to 509 keys: 9.1 and
+// 17.6 us; 128 of up to 1,000 keys: 51 and 57 us. At 13, 40 sequences with that window (18 and 8 steps): 56 and 44 us.
+constexpr int kJoinSteps = 9;
 constexpr int kMaxDevices = 64;
 // Rows of the longest sequence from which hc_attend_tiles.cu takes a call: more than this kernel's largest tile of rows
 // reads and dequantises the keys twice. 64 sequences of up to 4096 keys, 28 rows: 179 us here, 243 us there; 64 of up to
@@ -183,6 +186,7 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
     constexpr int kBlock = kv_block_bytes(D);
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long scan[kWarps + 1];
+    __shared__ int longest[kWarps];
     __shared__ long long found_at;
     __shared__ int found_seq;
     __shared__ int last_flag;
@@ -227,24 +231,26 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
     if (p.q_max != kAnyQueries) griddep_launch_dependents();
     // A sequence's segments, and its units where segments may be cut.
     long long segments = 0, units = 0;
-    bool long_one = false;
+    int most = 0;  // units of the longest segment
     for (int b = tid; b < p.seqs; b += kThreads) {
         const Work<R> w(p, load_seq(p, b, blockIdx.x == 0 ? &g_hc_attention_error : nullptr), group);
         segments += static_cast<long long>(w.tiles) * heads;
         units += w.total(heads);
-        long_one |= w.tiles > 0 && w.units > kWholeSteps * kTeams;
+        if (w.tiles > 0) most = max(most, w.units);
     }
-    long long total, all_segments;
-    const bool cut = __syncthreads_or(long_one);
-    long long x = block_scan(segments, all_segments);
-    // Short segments are left whole, one after the other: joining parts would cost more than the work. Not where that would
-    // leave some CTAs twice the others' share.
-    const bool whole_ones = !cut && (all_segments <= gridDim.x || all_segments >= 4LL * gridDim.x);
-    if (whole_ones) total = all_segments;
-    else x = block_scan(units, total);
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    if (lane == 0) longest[warp] = most;
+    long long all_units, all_segments;
+    const long long xs = block_scan(segments, all_segments), xu = block_scan(units, all_units);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) most = max(most, longest[w]);
+    // Segments are left whole, one after the other, where joining their parts would cost more than uneven shares.
+    const long long grid = gridDim.x;
+    const bool whole_ones = (all_segments + grid - 1) / grid * ((most + kTeams - 1) / kTeams) <= all_units / (grid * kTeams) + kJoinSteps;
+    const long long total = whole_ones ? all_segments : all_units, x = whole_ones ? xs : xu;
     const long long least = whole_ones ? 1 : kTeams;  // a CTA's smallest share: one unit a team
     const long long want = (total + least - 1) / least;
-    const long long ctas = want < gridDim.x ? want : static_cast<long long>(gridDim.x);
+    const long long ctas = want < grid ? want : grid;
     if (static_cast<long long>(blockIdx.x) >= ctas) return;
     long long at = total * blockIdx.x / ctas;
     const long long end = total * (blockIdx.x + 1) / ctas;
@@ -743,8 +749,8 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
 #pragma unroll
                     for (int e = 0; e < 4; ++e) st[((k * kNT + t) * 4 + e) * 32 + lane] = o[k][t][e];
         };
-        auto join_teams = [&]() {
-            for (int half = kTeams / 2; half >= 1; half /= 2) {
+        auto join_teams = [&](int teams) {  // the first `teams`; a power of two
+            for (int half = teams / 2; half >= 1; half /= 2) {
                 float* at_ = merge + (team % half * kSplit + part) * (P::kStateFloats + P::kMl);
                 if (team >= half && team < 2 * half) leave(at_, at_ + P::kMl);
                 __syncthreads();
@@ -782,7 +788,7 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
                     if (p.lse && r == 0 && part == 0) p.lse[token * p.q_heads + head] = lv == 0.f ? -INFINITY : (m[t][j] + log2f(lv)) * kLn2;
                 }
         };
-        join_teams();
+        join_teams(kTeams);
         if (done.u0 == 0 && done.u1 == done.units) {
             write_out();
         } else {
@@ -797,9 +803,9 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
             if (team == 0) {
                 float* mine_ = part_of(static_cast<int>(blockIdx.x));
                 leave(mine_, mine_ + P::kMl + part * P::kStateFloats);  // both warps write the same maxima and sums
-                __threadfence();
                 team_sync();
                 if (warp == 0 && lane == 0) {
+                    __threadfence();
                     const unsigned int before = atomicAdd(&counters[c0], 1u);
                     const bool last = before + 1 == static_cast<unsigned int>(c1 - c0 + 1);
                     if (last) counters[c0] = 0;
@@ -823,12 +829,13 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
                     for (int t = 0; t < kNT; ++t)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[k][t][e] = 0.f;
-                __threadfence();
                 for (int x = c0 + team; x <= c1; x += kTeams) {
                     const float* st = part_of(x);
                     absorb(st, st + P::kMl + part * P::kStateFloats, [](const float* x) { return __ldcg(x); });  // other SMs' writes: from L2
                 }
-                join_teams();
+                int teams = 1;
+                while (teams < kTeams && teams < c1 - c0 + 1) teams *= 2;
+                join_teams(teams);
                 write_out();
             }
         }
