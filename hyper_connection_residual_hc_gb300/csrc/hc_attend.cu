@@ -52,8 +52,8 @@ __device__ unsigned int g_hc_attention_error = 0;
 constexpr uint64_t kWaitNs = 1000000000ull;   // 1 s
 constexpr int kUnit = 32;                     // tokens a warp takes at a time: two cache blocks
 // What it costs a CTA to have segments cut, in steps of its teams: left whole, they may take so many steps longer. 64 sequences
-// of 5 queries with a window of 1,024 keys, 18 steps whole, 14 cut: 57 us whole, 66 us cut; 8 of up to 509 keys: 9.1 and
-// 17.6 us; 128 of up to 1,000 keys: 51 and 57 us. At 13, 40 sequences with that window (18 and 8 steps): 56 and 44 us.
+// of 5 queries with a window of 1,024 keys, 18 steps whole, 14 cut: 56 us whole, 63 us cut; 128 of up to 1,000 keys: 49 and
+// 53 us; 128 of up to 509: 34 and 42 us. At 11, 40 sequences with that window (18 and 8 steps): 55 us whole, 42 us cut.
 constexpr int kJoinSteps = 9;
 constexpr int kMaxDevices = 64;
 // Rows of the longest sequence from which hc_attend_tiles.cu takes a call: more than this kernel's largest tile of rows
@@ -76,12 +76,17 @@ struct Plan {
     static constexpr int kStage = kUnit / 16 * kv_block_bytes(D);
     static constexpr int kRing = kTeams * kStages * kStage;
     static constexpr int kTiles = D / 16 / kSplit;              // 16-column tiles of the output a warp
-    static constexpr int kStateFloats = kTiles * kNT * 4 * 32;  // a warp's outputs
-    static constexpr int kMl = 2 * 8 * kNT;                     // its maxima and sums
-    static constexpr int kMerge = kWarps / 2 * (kStateFloats + kMl) * 4;
+    // The outputs are joined in so many passes, so that shared memory holds two CTAs an SM or more, and the L1 cache gets a part
+    // of it: with kTiles * kNT = 12, 58.2 us in one pass, 55.7 us in two (5 queries of 4 heads, 64 sequences, window of 1,024
+    // keys); with 8, 209.7 us in one, 213.3 us in two (one query of 5 heads, 256 sequences of up to 4,096 keys).
+    static constexpr int kPasses = kTiles * kNT >= 12 ? 2 : 1;
+    static constexpr int kPassTiles = kTiles / kPasses;
+    static constexpr int kStateFloats = kPassTiles * kNT * 4 * 32;  // a warp's outputs of a pass
+    static constexpr int kMl = 2 * 8 * kNT;                         // its maxima and sums
+    static constexpr int kMerge = kWarps * (kStateFloats + kMl) * 4;
     static constexpr int kQ = kSplit == 1 ? 0 : kNT * (D / 16) * 32 * 8;            // the queries as B fragments
     static constexpr int kWeights = kSplit == 1 ? 0 : kTeams * 2 * 2 * kNT * 2 * 128;  // [team][step parity][block][fragment]
-    static constexpr int kRows = kSplit == 1 ? 0 : (1 + 2 * kTeams) * 8 * kNT * 4;  // score factors; a team's exchange of maxima or sums
+    static constexpr int kRows = kSplit == 1 ? 0 : (1 + 2 * kTeams) * 8 * kNT * 4;  // score factors; a team's exchange of maxima
     static constexpr int kBars = kTeams * kStages * 8;
     static constexpr int kSmem = kRing + kMerge + kQ + kWeights + kRows + kBars;
 };
@@ -692,48 +697,21 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
             open();
         }
 
-        // ---- join the teams, in halves -----------------------------------------------------------------------
+        // ---- join the warps' results --------------------------------------------------------------------------
+        // Each warp leaves its own in shared memory; then an item of four columns (two output tiles of the fragments' layout) of
+        // the rows 8 t + 2 c + j goes to one warp, which adds up what the teams have of it.
 #pragma unroll
         for (int t = 0; t < kNT; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int x = 4; x < 32; x *= 2) l[t][j] += __shfl_xor_sync(0xFFFFFFFFu, l[t][j], x);
-                if constexpr (kSplit == 2) {
-                    if (r == 0) shared_rows[part * R + 8 * t + 2 * c + j] = l[t][j];
-                }
-            }
-        if constexpr (kSplit == 2) {  // the two warps' sums (their maxima are the same)
-            team_sync();
-#pragma unroll
-            for (int t = 0; t < kNT; ++t)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) l[t][j] += shared_rows[(part ^ 1) * R + 8 * t + 2 * c + j];
-        }
-        // another partial result: rows' maxima and sums, outputs; `get` loads one float
-        auto absorb = [&](const float* ml, const float* st, auto get) {
-#pragma unroll
-            for (int t = 0; t < kNT; ++t) {
-                float mine_[2], theirs[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int col = 8 * t + 2 * c + j;
-                    const float m1 = get(ml + col), l1 = get(ml + 8 * kNT + col);
-                    const float m2 = fmaxf(m[t][j], m1);
-                    mine_[j] = m2 == -INFINITY ? 1.f : ex2(m[t][j] - m2);
-                    theirs[j] = m2 == -INFINITY ? 1.f : ex2(m1 - m2);
-                    m[t][j] = m2;
-                    l[t][j] = l[t][j] * mine_[j] + l1 * theirs[j];
-                }
-#pragma unroll
-                for (int k = 0; k < kTiles; ++k)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[k][t][e] = o[k][t][e] * mine_[e % 2] + get(st + ((k * kNT + t) * 4 + e) * 32 + lane) * theirs[e % 2];
-            }
-        };
-        auto leave = [&](float* ml, float* st) {
-            if (r == 0) {
+        constexpr int kPairs = kSplit * P::kPassTiles / 2, kItems = kPairs * 2 * kNT;
+        static_assert(P::kPassTiles % 2 == 0, "whole items");
+        constexpr int kWarpFloats = P::kStateFloats + P::kMl;
+        auto leave = [&](int pass) {
+            float* ml = merge + warp * kWarpFloats;
+            if (pass == 0 && r == 0) {
 #pragma unroll
                 for (int t = 0; t < kNT; ++t)
 #pragma unroll
@@ -743,100 +721,128 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
                     }
             }
 #pragma unroll
-            for (int k = 0; k < kTiles; ++k)
+            for (int k = 0; k < P::kPassTiles; ++k)
 #pragma unroll
                 for (int t = 0; t < kNT; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) st[((k * kNT + t) * 4 + e) * 32 + lane] = o[k][t][e];
+                    for (int e = 0; e < 4; ++e)
+                        ml[P::kMl + ((k * kNT + t) * 4 + e) * 32 + lane] = o[pass * P::kPassTiles + k][t][e];
         };
-        auto join_teams = [&](int teams) {  // the first `teams`; a power of two
-            for (int half = teams / 2; half >= 1; half /= 2) {
-                float* at_ = merge + (team % half * kSplit + part) * (P::kStateFloats + P::kMl);
-                if (team >= half && team < 2 * half) leave(at_, at_ + P::kMl);
-                __syncthreads();
-                if (team < half) absorb(at_, at_ + P::kMl, [](const float* x) { return *x; });
-                __syncthreads();
+        // one item's sum over the segment's keys to the outputs
+        const int drows = done.s.ql * group, drow0 = done.tile * R;
+        auto put = [&](int pass, int item, const float (&v)[4], float top, float sum) {
+            const int pr = item % kPairs, tj = item / kPairs;
+            const int row = drow0 + 8 * (tj / 2) + 2 * c + tj % 2;
+            if (row >= drows) return;
+            const float scale = sum == 0.f ? 0.f : p.s.v_unit / sum;
+            const long long token = done.s.qs + row / group;
+            const int head = done.h * group + row % group;
+            const int tile = 2 * pr / P::kPassTiles * kTiles + pass * P::kPassTiles + 2 * pr % P::kPassTiles;
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D + r * (D / 8) + 2 * tile;
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[0] * scale, v[1] * scale), y = __floats2bfloat162_rn(v[2] * scale, v[3] * scale);
+            *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+            if (p.lse && r == 0 && pr == 0 && pass == 0) p.lse[token * p.q_heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        };
+        const bool all = done.u0 == 0 && done.u1 == done.units;
+        // a part of a segment: units [done.u0, done.u1) of it; the segment's first unit is `at` - done.u1 of the call
+        const long long seg0 = at - done.u1, seg1 = seg0 + done.units - 1;
+        auto cta_of = [&](long long x) { return static_cast<int>(((x + 1) * ctas - 1) / total); };
+        const int c0 = all ? 0 : cta_of(seg0), c1 = all ? 0 : cta_of(seg1);
+        // in the workspace: rows' maxima and sums, then the items. A CTA's second slot is for the segment that begins in it, the
+        // first for one that began before.
+        auto part_of = [&](int cta) {
+            return reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kAttCounterBytes) +
+                   static_cast<long long>(2 * cta + (cta == c0 ? 1 : 0)) * kAttPartFloats;
+        };
+#pragma unroll
+        for (int pass = 0; pass < P::kPasses; ++pass) {
+            if (pass > 0) __syncthreads();
+            leave(pass);
+            __syncthreads();
+            // all of the warp's items at once, so that their loads overlap
+            constexpr int kMine = (kItems + kWarps - 1) / kWarps;
+            float top[kMine], sum[kMine], v[kMine][4];
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int item = min(warp + i * kWarps, kItems - 1), pr = item % kPairs, tj = item / kPairs, t = tj / 2, j = tj % 2;
+                const float* ml = merge + 8 * t + 2 * c + j;
+                const float* words = merge + 2 * pr / P::kPassTiles * kWarpFloats + P::kMl + ((2 * pr % P::kPassTiles * kNT + t) * 4 + j) * 32 + lane;
+                top[i] = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kTeams; ++w) top[i] = fmaxf(top[i], ml[w * kSplit * kWarpFloats]);
+                const float base = top[i] == -INFINITY ? 0.f : top[i];
+                sum[i] = v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kTeams; ++w) {
+                    const float* x = ml + w * kSplit * kWarpFloats;
+                    const float fade = ex2(x[0] - base);
+                    sum[i] = fmaf(fade, kSplit == 1 ? x[8 * kNT] : x[8 * kNT] + x[8 * kNT + kWarpFloats], sum[i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[i][e] = fmaf(fade, words[w * kSplit * kWarpFloats + (e / 2 * kNT * 4 + e % 2 * 2) * 32], v[i][e]);
+                }
             }
-        };
-        auto write_out = [&]() {  // team 0 has it all
-            if (team != 0) return;
-            const int drows = done.s.ql * group, drow0 = done.tile * R;
 #pragma unroll
-            for (int t = 0; t < kNT; ++t)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int row = drow0 + 8 * t + 2 * c + j;
-                    if (row >= drows) continue;
-                    const float lv = l[t][j];
-                    const float s = lv == 0.f ? 0.f : p.s.v_unit / lv;
-                    const long long token = done.s.qs + row / group;
-                    const int head = done.h * group + row % group;
-                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D + r * (D / 8) +
-                                         2 * part * kTiles;
-                    constexpr int kVec = kTiles < 4 ? kTiles : 4;
-#pragma unroll
-                    for (int k = 0; k < kTiles; k += kVec) {
-                        uint32_t w[kVec];
-#pragma unroll
-                        for (int e = 0; e < kVec; ++e) {
-                            const __nv_bfloat162 v = __floats2bfloat162_rn(o[k + e][t][j] * s, o[k + e][t][2 + j] * s);
-                            w[e] = *reinterpret_cast<const uint32_t*>(&v);
-                        }
-                        if constexpr (kVec == 4) *reinterpret_cast<uint4*>(dst + 2 * k) = make_uint4(w[0], w[1], w[2], w[3]);
-                        else *reinterpret_cast<uint2*>(dst + 2 * k) = make_uint2(w[0], w[1]);
+            for (int i = 0; i < kMine; ++i) {
+                const int item = warp + i * kWarps, tj = item / kPairs, col = 8 * (tj / 2) + 2 * c + tj % 2;
+                if (item >= kItems) break;
+                if (all) {
+                    put(pass, item, v[i], top[i], sum[i]);
+                } else {
+                    float* mine = part_of(static_cast<int>(blockIdx.x));
+                    if (pass == 0 && item % kPairs == 0 && r == 0) {
+                        mine[col] = top[i];
+                        mine[8 * kNT + col] = sum[i];
                     }
-                    if (p.lse && r == 0 && part == 0) p.lse[token * p.q_heads + head] = lv == 0.f ? -INFINITY : (m[t][j] + log2f(lv)) * kLn2;
+                    *reinterpret_cast<float4*>(mine + P::kMl + ((pass * kItems + item) * 32 + lane) * 4) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
                 }
-        };
-        join_teams(kTeams);
-        if (done.u0 == 0 && done.u1 == done.units) {
-            write_out();
-        } else {
-            // a part of a segment: units [done.u0, done.u1) of it; the segment's first unit is `at` - done.u1 of the call
-            const long long seg0 = at - done.u1, seg1 = seg0 + done.units - 1;
-            auto cta_of = [&](long long x) { return static_cast<int>(((x + 1) * ctas - 1) / total); };
-            const int c0 = cta_of(seg0), c1 = cta_of(seg1);
-            unsigned int* counters = static_cast<unsigned int*>(p.workspace);
-            float* parts = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kAttCounterBytes);
-            // a CTA's second slot for the segment that begins in it, the first for one that began before
-            auto part_of = [&](int cta) { return parts + static_cast<long long>(2 * cta + (cta == c0 ? 1 : 0)) * kAttPartFloats; };
-            if (team == 0) {
-                float* mine_ = part_of(static_cast<int>(blockIdx.x));
-                leave(mine_, mine_ + P::kMl + part * P::kStateFloats);  // both warps write the same maxima and sums
-                team_sync();
-                if (warp == 0 && lane == 0) {
-                    __threadfence();
-                    const unsigned int before = atomicAdd(&counters[c0], 1u);
-                    const bool last = before + 1 == static_cast<unsigned int>(c1 - c0 + 1);
-                    if (last) counters[c0] = 0;
-                    last_flag = last ? 1 : 0;
-                    __threadfence();
-                }
+            }
+        }
+        if (!all) {
+            __syncthreads();
+            if (tid == 0) {
+                unsigned int* counter = static_cast<unsigned int*>(p.workspace) + c0;
+                __threadfence();
+                const bool last = atomicAdd(counter, 1u) + 1 == static_cast<unsigned int>(c1 - c0 + 1);
+                if (last) *counter = 0;
+                last_flag = last ? 1 : 0;
+                __threadfence();
             }
             __syncthreads();
-            if (last_flag) {
-                // team w takes parts w, w + kTeams, ... in their order, then the teams join as before
+            if (last_flag) {  // the parts in their order (other SMs' writes: from L2)
+                constexpr int kMine = (P::kPasses * kItems + kWarps - 1) / kWarps;
+                float top[kMine], sum[kMine], v[kMine][4];
+                int col[kMine], x[kMine];
 #pragma unroll
-                for (int t = 0; t < kNT; ++t)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        m[t][j] = -INFINITY;
-                        l[t][j] = 0.f;
-                    }
-#pragma unroll
-                for (int k = 0; k < kTiles; ++k)
-#pragma unroll
-                    for (int t = 0; t < kNT; ++t)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[k][t][e] = 0.f;
-                for (int x = c0 + team; x <= c1; x += kTeams) {
-                    const float* st = part_of(x);
-                    absorb(st, st + P::kMl + part * P::kStateFloats, [](const float* x) { return __ldcg(x); });  // other SMs' writes: from L2
+                for (int i = 0; i < kMine; ++i) {
+                    x[i] = min(warp + i * kWarps, P::kPasses * kItems - 1);
+                    const int tj = x[i] % kItems / kPairs;
+                    col[i] = 8 * (tj / 2) + 2 * c + tj % 2;
+                    top[i] = -INFINITY;
+                    sum[i] = v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
                 }
-                int teams = 1;
-                while (teams < kTeams && teams < c1 - c0 + 1) teams *= 2;
-                join_teams(teams);
-                write_out();
+#pragma unroll 4
+                for (int w = c0; w <= c1; ++w) {
+                    const float* from = part_of(w);
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) top[i] = fmaxf(top[i], __ldcg(from + col[i]));
+                }
+#pragma unroll 2
+                for (int w = c0; w <= c1; ++w) {
+                    const float* from = part_of(w);
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) {
+                        const float fade = ex2(__ldcg(from + col[i]) - (top[i] == -INFINITY ? 0.f : top[i]));
+                        const float4 y = __ldcg(reinterpret_cast<const float4*>(from + P::kMl) + x[i] * 32 + lane);
+                        sum[i] = fmaf(fade, __ldcg(from + 8 * kNT + col[i]), sum[i]);
+                        v[i][0] = fmaf(fade, y.x, v[i][0]);
+                        v[i][1] = fmaf(fade, y.y, v[i][1]);
+                        v[i][2] = fmaf(fade, y.z, v[i][2]);
+                        v[i][3] = fmaf(fade, y.w, v[i][3]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kMine; ++i)
+                    if (warp + i * kWarps < P::kPasses * kItems) put(x[i] / kItems, x[i] % kItems, v[i], top[i], sum[i]);
             }
         }
         if (!more) break;
