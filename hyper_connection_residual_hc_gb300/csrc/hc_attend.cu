@@ -7,12 +7,12 @@
 // The tensor memory path (tcgen05) would have to write every dequantised block to shared memory first, 8 times
 // the bytes that the cache has; this kernel's bound is the dequantisation and HBM, not the products.
 //
-// Measured: 256 sequences of 2,050 to 4,096 keys, 40 query and 8 kv heads of 128 (912 MB): 215 us, 4.25 TB/s, 63% of the
-// measured copy rate; 3 sequences of up to 131,072 keys: 84 us, 66%; 8 of up to 509 keys: 8.9 us. With few rows what is
+// Measured: 256 sequences of 2,050 to 4,096 keys, 40 query and 8 kv heads of 128 (912 MB): 206 us, 4.4 TB/s, 65% of the
+// measured copy rate; 3 sequences of up to 131,072 keys: 84.5 us, 66%; 8 of up to 509 keys: 8.5 us. With few rows what is
 // left is instructions: about 600 for a unit of 32 keys of a head (128 conversions from 4 bits, about as many products with
-// scales, 32 MMAs), issue slots 58% busy, no pipe above half; leaving out the keys' scale products would save 7 us,
-// two warps a unit (258 us) or blocks of 4 warps (255 us) lose. More rows cost more of everything: five queries of 4 heads each, 64 sequences, window of
-// 1,024 keys (81 MB): 68 us.
+// scales, 32 MMAs), issue slots about 60% busy, no pipe above half. Leaving out the keys' scale products would save 7 us;
+// two warps a unit (258 us) or blocks of 4 warps (255 us) lose. More rows cost more of everything: five queries of 4
+// heads each, 64 sequences, window of 1,024 keys (81 MB): 55 us.
 //
 // A cache block (16 tokens, one head) is laid out in A-fragment order: lane (r, c) = (lane / 4, lane % 4) finds
 // in its own 32-bit words the codes of keys r and r + 8, columns [c D/4, (c+1) D/4) (the contraction index of
@@ -30,7 +30,8 @@
 // end to end and cut into equal ranges, one a CTA, whatever the lengths. The warps of a CTA take its units in
 // turn, each with a ring of cache blocks of its own, filled by bulk copies that the warp issues ahead; they join
 // at the end of a segment. A segment cut between CTAs leaves partial results in the workspace, and the CTA that
-// finishes last joins them in their order: the result does not depend on timing.
+// finishes last joins them in their order: the result does not depend on timing. Where a cut would cost more than it
+// evens out, segments stay whole (kJoinSteps).
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -86,7 +87,7 @@ struct Plan {
     static constexpr int kMerge = kWarps * (kStateFloats + kMl) * 4;
     static constexpr int kQ = kSplit == 1 ? 0 : kNT * (D / 16) * 32 * 8;            // the queries as B fragments
     static constexpr int kWeights = kSplit == 1 ? 0 : kTeams * 2 * 2 * kNT * 2 * 128;  // [team][step parity][block][fragment]
-    static constexpr int kRows = kSplit == 1 ? 0 : (1 + 2 * kTeams) * 8 * kNT * 4;  // score factors; a team's exchange of maxima
+    static constexpr int kRows = kSplit == 1 ? 0 : (2 + 2 * kTeams) * 8 * kNT * 4;  // score factors; ends of what rows see; a team's exchange of maxima
     static constexpr int kBars = kTeams * kStages * 8;
     static constexpr int kSmem = kRing + kMerge + kQ + kWeights + kRows + kBars;
 };
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
     const uint32_t queries = smem_u32(smem) + P::kRing + P::kMerge;
     const uint32_t exchanged = queries + P::kQ + static_cast<uint32_t>(team * (P::kWeights / kTeams));
     float* factors = reinterpret_cast<float*>(smem + P::kRing + P::kMerge + P::kQ + P::kWeights);
-    float* shared_rows = factors + R + team * 2 * R;  // [part][row]
+    float* shared_rows = factors + 2 * R + team * 2 * R;  // [part][row]
     const uint32_t bars = smem_u32(smem) + P::kSmem - P::kBars + static_cast<uint32_t>(team * P::kStages * 8);
     if (part == 0 && lane < P::kStages) mbar_init(bars + 8u * static_cast<uint32_t>(lane), 1);
     fence_mbar_init();
@@ -359,8 +360,13 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
         const int rows = g.s.ql * group, row0 = g.tile * R;
         const int pos0 = g.s.kvl - g.s.ql;
         uint32_t qf[kSplit == 1 ? kNT : 1][kKeySteps][2];  // (kSplit = 2: in shared memory)
-        float f[kNT][2];   // score factor (log2 units) of rows 2c, 2c + 1
-        int see[kNT][2];   // keys below this position are seen (causal)
+        float f[kNT][2];   // score factor (log2 units) of rows 2c, 2c + 1 (kSplit = 2: loaded when needed)
+        // keys below this position are seen (causal)
+        auto sees = [&](int row) { return p.causal ? (row < rows ? max(pos0 + row / group + 1, 0) : 0x7FFFFFFF) : g.s.kvl; };
+        auto see = [&](int t, int j) {
+            if constexpr (kSplit == 1) return sees(row0 + 8 * t + 2 * c + j);
+            else return static_cast<int>(lds32(smem_u32(factors) + static_cast<uint32_t>((R + 8 * t + 2 * c + j) * 4)));
+        };
 #pragma unroll
         for (int t = 0; t < kNT; ++t) {
             if (kSplit == 2 && t % kWarps != warp) continue;  // one warp makes a tile's fragments for all
@@ -406,17 +412,10 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
                 for (int j = 0; j < 2; ++j) f[t][j] = __shfl_sync(0xFFFFFFFFu, fr, 4 * (2 * c + j));
             } else {
                 if (c == 0) factors[8 * t + r] = fr;
+                if (c == 1) factors[R + 8 * t + r] = __int_as_float(sees(row));
             }
         }
         if constexpr (kSplit == 2) __syncthreads();
-#pragma unroll
-        for (int t = 0; t < kNT; ++t)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if constexpr (kSplit == 2) f[t][j] = factors[8 * t + 2 * c + j];
-                const int col = row0 + 8 * t + 2 * c + j;
-                see[t][j] = p.causal ? (col < rows ? max(pos0 + col / group + 1, 0) : 0x7FFFFFFF) : g.s.kvl;
-            }
         float m[kNT][2], l[kNT][2], o[kTiles][kNT][4];
 #pragma unroll
         for (int t = 0; t < kNT; ++t)
@@ -494,20 +493,31 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
                     }
             }
             // ---- masks, running maximum, weights ------------------------------------------------------------
+            if constexpr (kSplit == 2) {
+#pragma unroll
+                for (int t = 0; t < kNT; ++t) {
+                    uint32_t x, y;
+                    lds64(smem_u32(factors) + static_cast<uint32_t>((8 * t + 2 * c) * 4), x, y);
+                    f[t][0] = __uint_as_float(x);
+                    f[t][1] = __uint_as_float(y);
+                }
+            }
             const bool whole = have == 3u && blk0 * 16 >= g.all_lo && blk0 * 16 + kUnit <= g.all_hi;
             if (!whole) {  // scores to their final scale here, so that a masked one stays -infinity whatever the factor
 #pragma unroll
                 for (int t = 0; t < kNT; ++t)
 #pragma unroll
-                    for (int n = 0; n < kOwn; ++n)
+                    for (int j = 0; j < 2; ++j) {
+                        const int upto = see(t, j), hi = min(upto, g.s.kvl), lo = p.window > 0 ? upto - p.window : 0;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int in_unit = kSplit == 1 ? n : part;
-                            const int pos = (blk0 + in_unit) * 16 + r + 8 * (e / 2);
-                            const bool seen = (have >> in_unit & 1) && pos < min(see[t][e % 2], g.s.kvl) &&
-                                              (p.window == 0 || pos >= see[t][e % 2] - p.window);
-                            z[n][t][e] = seen ? z[n][t][e] * f[t][e % 2] : -INFINITY;
-                        }
+                        for (int n = 0; n < kOwn; ++n)
+#pragma unroll
+                            for (int e = j; e < 4; e += 2) {
+                                const int in_unit = kSplit == 1 ? n : part;
+                                const int pos = (blk0 + in_unit) * 16 + r + 8 * (e / 2);
+                                z[n][t][e] = (have >> in_unit & 1) && pos < hi && pos >= lo ? z[n][t][e] * f[t][j] : -INFINITY;
+                            }
+                    }
             }
             float top[kNT][2];
             bool raise = false;
@@ -653,7 +663,7 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
                         for (int t = 0; t < kNT; ++t)
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                const int lo = p.window > 0 ? see[t][j] - p.window : 0, hi = min(see[t][j], g.s.kvl);
+                                const int upto = see(t, j), lo = p.window > 0 ? upto - p.window : 0, hi = min(upto, g.s.kvl);
                                 const int b0 = (blk0 + n) * 16;
                                 const int from = min(max(lo - b0, 0), 16), to = min(max(hi - b0, 0), 16);
                                 const uint32_t vis = to > from ? ((1u << to) - 1u) & ~((1u << from) - 1u) : 0u;
