@@ -908,6 +908,7 @@ int launch_attention(const AttArgs& args, cudaStream_t stream) {
     AttArgs a = args;
     a.q_min = 0;
     a.q_max = kAnyQueries;
+    if (a.max_q_len > a.n) a.max_q_len = static_cast<int>(a.n);  // n is at most 2^31 - 1
     const int group = a.q_heads / a.s.heads;
     const long long rows = static_cast<long long>(a.max_q_len) * group;
     if (rows < kTilesFromRows || !attention_tiles_take(a)) return launch_rows_for(rows, a, stream);

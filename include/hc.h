@@ -459,7 +459,8 @@ int hc_kv_read(const void* cache, const int64_t* slots, int64_t n, hc_kv_shape_t
 typedef struct {
     int64_t n;      /* rows of q and out: the queries of all sequences; n * q_heads / heads at most 2^31 - 1 */
     int seqs;       /* sequences, 0..2^24 */
-    int max_q_len;  /* queries of the longest sequence: sizes the tiles (longer ones are right, but slower) */
+    int max_q_len;  /* queries of the longest sequence: chooses kernels and tiles (any value is right, others slower).
+                     * Single tokens and long chunks may share a call: each kind goes to a kernel of its own */
     int max_pages;  /* columns of the page table, >= 1; max_pages * page_size at most 2^30 */
     int q_heads;    /* a multiple of the cache's heads, up to 128 times as many: head h reads kv head h * heads / q_heads */
     int causal;     /* 1: a query sees the keys up to its own position; 0: all keys of its sequence */
@@ -467,10 +468,11 @@ typedef struct {
     float scale;    /* of q . k, before the softmax; finite, >= 0 */
 } hc_attention_t;
 
-/* Size in bytes of the workspace of hc_kv_attention (34,080,768: counters, and room for the partial results of
- * sequences whose keys are spread over the GPU). The caller allocates it once [device], 16-byte aligned, fills it with zeros before its first
- * use and then keeps passing it unchanged: each call leaves the counters at zero. Calls that may run at the
- * same time (two graphs replayed on two streams, say) must not share one. Host-only, no CUDA call. */
+/* Size in bytes of the workspace of hc_kv_attention (34,080,768: counters, and room for the partial results
+ * of sequences whose keys are spread over the GPU). The caller allocates it once [device], 16-byte aligned,
+ * fills it with zeros before its first use and then keeps passing it unchanged: each call leaves the counters
+ * at zero. Calls that may run at the same time (two graphs replayed on two streams, say) must not share one.
+ * Host-only, no CUDA call. */
 int hc_kv_workspace_size(size_t* bytes);
 
 /* Softmax attention of ragged queries over the 4-bit cache: decode (one query a sequence), drafted tokens
