@@ -15,8 +15,8 @@
 // memory are rarely rescaled. S_a of the next tile is issued behind P_a V of this one: a thread that sees its scores
 // knows that its outputs are complete.
 //
-// Few row tiles with many keys: the key tiles of each are cut into slices, one CTA each (gridDim.y), joined in their order by
-// the CTA that finishes last.
+// Row tiles that would leave SMs idle (few of them, or the last of many) have their key tiles cut into slices, one CTA
+// each, joined in their order by the CTA that finishes last.
 //
 // Measured: 2 sequences of 2,048 queries behind 4,096 to 6,144 cached keys, 40 query and 8 kv heads of 128: 541 us, 952
 // TFLOP/s, 49% of the measured cuBLAS rate (the first form, with separate score and value steps by 17 warps of 96 registers,
@@ -53,6 +53,8 @@ static_assert(kDequantWarps == 4, "a word of notes");
 constexpr int kBlocksPerWarp = kKeys / 16 / kDequantWarps;  // cache blocks of a key tile that a dequantising warp takes
 constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kLeastSlice = 4;  // key tiles of a slice at least
+constexpr int kOrderedWaves = 8;
 constexpr int kNotes = 8;       // key tiles whose notes (absent blocks, NaN values) are kept
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kMaxDevices = 64;
@@ -296,6 +298,146 @@ __device__ __forceinline__ void store32(__nv_bfloat16* dst, const float (&v)[32]
     }
 }
 
+// What a CTA works on: one slice of the keys of one row tile of a sequence and a kv head. seq is -1 for CTAs without work;
+// `rest` counts the sliced row tiles.
+struct Found {
+    int seq, tile, head, rest, slice, slices;
+};
+struct FindScratch {
+    int part[2][16], top[16];  // of the warps; two sums in turn
+    int seq, tile;
+};
+// By all threads. CTAs start in turn as SMs get free: the row tiles with the most key tiles come first, so that the last ones to
+// start are short (where an SM gets up to kOrderedWaves of them: among more it matters little). As many row tiles as
+// fill the SMs a whole number of times are taken whole; those left, if they fill half of the SMs at most, are cut into
+// slices that fill them.
+__device__ __forceinline__ Found find_tile(const AttArgs& p, int group, int cta, int sms, int tid, FindScratch& f) {
+    const int warp = tid / 32, lane = tid % 32;
+    struct Seq {
+        long long rows, behind;  // rows; those of (queries - keys) queries
+        int tiles, kvl;
+    };
+    auto load = [&](int b) {
+        Seq q = {};
+        if (b < p.seqs) {
+            const SeqRows s = load_seq(p, b, cta == 0 ? &g_hc_tiles_error : nullptr);
+            q.rows = static_cast<long long>(s.ql) * group;
+            q.tiles = static_cast<int>((q.rows + kRows - 1) / kRows);
+            q.kvl = s.kvl;
+            q.behind = static_cast<long long>(s.ql - s.kvl) * group;
+        }
+        return q;
+    };
+    // Up to 32 sequences: each warp does it all, one sequence a lane, without barriers.
+    const bool few = p.seqs <= 32;
+    const int me = few ? lane : tid, width = few ? 32 : kThreads;
+    const Seq own = load(me);
+    auto seq = [&](int b) { return b == me ? own : load(b); };
+    // how many of a sequence's row tiles (its last ones) have more than x key tiles, where there is no window
+    auto above = [&](const Seq& q, int x) {
+        if (x < 0) return q.tiles;
+        const long long keys = static_cast<long long>(kKeys) * x;  // a row must see more
+        if (!p.causal) return q.kvl > keys ? q.tiles : 0;
+        const long long r0 = q.behind + keys * group;  // the first row that does
+        return r0 <= 0 ? q.tiles : r0 >= q.rows ? 0 : q.tiles - static_cast<int>(r0 / kRows);
+    };
+    int turn = 0;
+    auto sum = [&](int v) {  // over the block; what a call leaves is read before the next but one writes there
+        v = __reduce_add_sync(0xFFFFFFFFu, v);
+        if (few) return v;
+        int* part = f.part[turn ^= 1];
+        if (lane == 0) part[warp] = v;
+        __syncthreads();
+        int all = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) all += part[w];
+        return all;
+    };
+    auto all_above = [&](int x) {
+        int n = 0;
+        for (int b = me; b < p.seqs; b += width) n += above(seq(b), x);
+        return sum(n);
+    };
+    if (tid == 0) f.seq = -1;
+    int top = 0;  // key tiles of the longest sequence
+    for (int b = me; b < p.seqs; b += width) {
+        const Seq q = seq(b);
+        if (q.tiles > 0) top = max(top, (q.kvl + kKeys - 1) / kKeys);
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (!few && lane == 0) f.top[warp] = top;
+    const int heads = p.s.heads;
+    const long long all = static_cast<long long>(all_above(-1)) * heads;
+    const int items = static_cast<int>(min(all, 0x7FFFFFFFLL)), whole = items / sms * sms, left = items - whole;
+    Found r = {-1, 0, 0, 0, 0, 1};
+    int item = cta;
+    if (cta >= whole && left > 0) {
+        r.slices = max(1, min(sms, kAttMaxSlices) / left);
+        r.rest = (cta - whole) / r.slices;
+        r.slice = (cta - whole) % r.slices;
+        item = whole + r.rest;
+    }
+    if (item >= items) return r;  // the same in every thread
+    const int want = item / heads;  // in the order
+    r.head = item - want * heads;
+    const bool ordered = items < kOrderedWaves * sms;
+    int lo = 0, exceed = 0;
+    if (ordered) {
+        // the least number of key tiles that no more than `want` row tiles exceed, and how many do
+        int hi = top;
+        if (!few) {
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) hi = max(hi, f.top[w]);
+        }
+        while (lo < hi) {
+            const int x = (lo + hi) / 2, n = all_above(x);
+            if (n <= want) {
+                hi = x;
+                exceed = n;
+            } else {
+                lo = x + 1;
+            }
+        }
+    }
+    int before = exceed;
+    for (int b0 = 0; b0 < p.seqs && before <= want; b0 += width) {
+        const Seq q = seq(b0 + me);
+        const int n0 = ordered ? above(q, lo) : 0, n = ordered ? above(q, lo - 1) - n0 : q.tiles;
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (few) {
+            x += before;
+            const int src = __ffs(static_cast<int>(__ballot_sync(0xFFFFFFFFu, x > want))) - 1;
+            if (src >= 0) {
+                r.seq = src;
+                r.tile = __shfl_sync(0xFFFFFFFFu, q.tiles - n0 - n + want - (x - n), src);
+            }
+            return r;
+        }
+        int* part = f.part[turn ^= 1];
+        if (lane == 31) part[warp] = x;
+        __syncthreads();
+        x += before;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) x += part[w];
+            before += part[w];
+        }
+        if (x > want && x - n <= want) {
+            f.seq = b0 + tid;
+            f.tile = q.tiles - n0 - n + want - (x - n);
+        }
+    }
+    __syncthreads();
+    r.seq = f.seq;
+    r.tile = f.tile;
+    return r;
+}
+
 // One lane's part of a cache block in registers.
 template <int D>
 struct BlockRegs {
@@ -304,76 +446,18 @@ struct BlockRegs {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs p) {
+__global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs p, int sms) {
     using T = TilePlan<D>;
     constexpr int kSteps = D / 16;       // MMAs of S
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ int scan[kThreads / 32 + 1];
-    __shared__ int found_seq, found_tile;
+    __shared__ FindScratch find_scratch;
     __shared__ bool last_flag;
     __shared__ __align__(4) uint8_t absent[kNotes][kDequantWarps];  // per key tile and warp: bits of its blocks that are not there
     __shared__ uint32_t nan_any[kNotes];                // per key tile: some value's scale is NaN
     const uint32_t sbase = smem_u32(smem);
     const int tid = static_cast<int>(threadIdx.x), warp = tid / 32, lane = tid % 32;
     const int heads = p.s.heads, group = p.q_heads / heads;
-
-    // ---- which rows: blockIdx.x counts (kv head fastest) the tiles of all sequences ---------------------
-    const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(heads));
-    const int want = static_cast<int>(blockIdx.x / static_cast<unsigned>(heads));
-    if (tid == 0) found_seq = -1;
-    {
-        int before = 0;
-        for (int b0 = 0; b0 < p.seqs; b0 += kThreads) {
-            const int b = b0 + tid;
-            int v = 0;
-            if (b < p.seqs) {
-                const SeqRows s = load_seq(p, b, blockIdx.x == 0 && blockIdx.y == 0 ? &g_hc_tiles_error : nullptr);
-                v = static_cast<int>((static_cast<long long>(s.ql) * group + kRows - 1) / kRows);
-            }
-            int x = v;
-#pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-                if (lane >= o) x += y;
-            }
-            __syncthreads();
-            if (lane == 31) scan[warp] = x;
-            __syncthreads();
-            int chunk = 0;
-            for (int w = 0; w < kThreads / 32; ++w) {
-                if (w < warp) x += scan[w];
-                chunk += scan[w];
-            }
-            x += before;
-            if (x > want && x - v <= want) {
-                found_seq = b;
-                found_tile = want - (x - v);
-            }
-            before += chunk;
-            if (before > want) break;  // the same in every thread
-        }
-        __syncthreads();
-    }
-    if (found_seq < 0) {  // more CTAs than tiles
-        griddep_wait();
-        return;
-    }
-    const int b = found_seq, tile = found_tile;
-    const SeqRows s = load_seq(p, b, nullptr);
-    const int rows = s.ql * group, row0 = tile * kRows;
-    const bool two = rows - row0 > kRowTile;  // the second row tile has rows
-    const TileBounds g = tile_bounds(p, s, group, row0, min(row0 + kRows, rows) - 1);
-    // this CTA's slice of the key tiles (blockIdx.y of gridDim.y): cache blocks from block0 on, `tiles` tiles of 8
-    int block0 = g.lo / 16;
-    const int block_end = (g.hi + 15) / 16;
-    int tiles = block_end > block0 ? (block_end - block0 + 7) / 8 : 0;
-    {
-        const int slices = static_cast<int>(gridDim.y), slice = static_cast<int>(blockIdx.y);
-        const int t0 = static_cast<int>(static_cast<long long>(tiles) * slice / slices);
-        tiles = static_cast<int>(static_cast<long long>(tiles) * (slice + 1) / slices) - t0;
-        block0 += 8 * t0;
-    }
 
     const uint32_t bars = sbase + T::kBars;
     auto k_full = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
@@ -382,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     auto v_empty = [&](int i) { return bars + 8u * static_cast<uint32_t>(6 + i); };
     auto s_full = [&](int a) { return bars + 8u * static_cast<uint32_t>(8 + a); };
     auto p_full = [&](int a, int half) { return bars + 8u * static_cast<uint32_t>(10 + 2 * a + half); };
-    const uint32_t o_full = bars + 8u * 14u;
+    const uint32_t o_full = bars + 8u * 14u, q_full = bars + 8u * 15u;
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(smem + T::kBars + 16 * 8);
     volatile uint32_t* abort_flag = tmem_ptr + 1;
     const Wait wait{abort_flag};
@@ -397,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             mbar_init(p_full(i, 1), 4);
         }
         mbar_init(o_full, 1);
+        mbar_init(q_full, kSoftmaxWarps);
         for (int i = 0; i < kNotes; ++i) nan_any[i] = 0;
         *abort_flag = 0u;
         fence_mbar_init();
@@ -406,51 +491,48 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         tmem_relinquish();
     }
 
-    // ---- queries: thread i < 256 takes row i ---------------------------------------------------------------
+    // ---- which rows and keys -------------------------------------------------------------------------------
+    const Found found = find_tile(p, group, static_cast<int>(blockIdx.x), sms, tid, find_scratch);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_ptr);
+    auto leave = [&]() {
+        griddep_wait();  // the call has ended when both kernels have
+        if (warp == kMmaWarp) tmem_dealloc(tmem, T::kColumns);
+    };
+    if (found.seq < 0) return leave();  // more CTAs than tiles and slices
+    const int b = found.seq, tile = found.tile, h = found.head, rest = found.rest;
+    const SeqRows s = load_seq(p, b, nullptr);
+    const int rows = s.ql * group, row0 = tile * kRows;
+    const bool two = rows - row0 > kRowTile;  // the second row tile has rows
+    const TileBounds g = tile_bounds(p, s, group, row0, min(row0 + kRows, rows) - 1);
+    // this CTA's slice of the key tiles: cache blocks from block0 on, `tiles` tiles of 8
+    int block0 = g.lo / 16;
+    const int block_end = (g.hi + 15) / 16;
+    int tiles = block_end > block0 ? (block_end - block0 + 7) / 8 : 0;
+    const int slices = min(found.slices, max(1, tiles / kLeastSlice)), slice = found.slice;
+    if (slice >= slices) return leave();
+    {
+        const int t0 = static_cast<int>(static_cast<long long>(tiles) * slice / slices);
+        tiles = static_cast<int>(static_cast<long long>(tiles) * (slice + 1) / slices) - t0;
+        block0 += 8 * t0;
+    }
+
     float m = -INFINITY, l = 0.f;  // the row's running maximum (log2 units) and sum
     float f = 0.f;
     int see = 0;
     const bool softmax = warp < kSoftmaxWarps;
     const int row = row0 + tid;
     const bool real = softmax && row < rows;
-    if (softmax) {
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
-                                   static_cast<long long>(s.qs + (real ? row / group : 0)) * p.q_stride +
-                                   static_cast<long long>(h * group + (real ? row % group : 0)) * D;
-        uint32_t big = 0;
-#pragma unroll
-        for (int e = 0; e < D / 8; ++e) {
-            const uint4 x = real ? __ldg(reinterpret_cast<const uint4*>(src) + e) : make_uint4(0, 0, 0, 0);
-            big = __vmaxu2(big, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
-        }
-        float up, down;
-        row_scale(max(big & 0xFFFFu, big >> 16), up, down);
-        f = p.scale * kLog2e * p.s.k_unit * down;
-        see = p.causal ? (real ? max(s.kvl - s.ql + row / group + 1, 0) : 0) : s.kvl;
-        const int i = tid % kRowTile;
-        const uint32_t base = sbase + T::kQ + static_cast<uint32_t>(tid / kRowTile * T::kTile + i * 128);
-#pragma unroll
-        for (int e = 0; e < D / 8; ++e) {
-            const uint4 x = real ? __ldg(reinterpret_cast<const uint4*>(src) + e) : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            uint32_t o[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[k] = pack_f16(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
-            st_smem_v4(base + static_cast<uint32_t>(e / 8 * T::kHalf + ((e % 8 ^ i % 8) << 4)), make_uint4(o[0], o[1], o[2], o[3]));
-        }
-        fence_proxy_async_smem();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_ptr);
     // where the row's results go
     const long long token = s.qs + (real ? row / group : 0);
     const int head = h * group + (real ? row % group : 0);
     const long long at = token * p.q_heads + head;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D;
     float* parts = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kAttCounterBytes);
-    float* mine = parts + (static_cast<size_t>(blockIdx.x) * gridDim.y + blockIdx.y) * T::kPartFloats;  // [column, maximum, sum][row]
+    float* first = parts + static_cast<size_t>(rest) * found.slices * T::kPartFloats;  // of this row tile's slices: [column, maximum, sum][row]
+    float* mine = first + static_cast<size_t>(slice) * T::kPartFloats;
 
     if (warp == kMmaWarp) {
         // ===== MMAs =======================================================================================
@@ -480,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         // Keys and values are waited for right after the scores have been issued, ahead of their use: a wait takes a hundred
         // cycles even where nothing is waited for, and between the weights' arrival and their product it would show.
         if (tiles > 0) {
+            wait(q_full, 0);
             wait(k_full(0), 0);
             tc_fence_after();
             for (int a = 0; a < na; ++a) scores(a, 0);
@@ -683,6 +766,44 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         }
     } else {
         // ===== softmax ========================================================================================
+        {
+            // the warp's 32 rows of queries, D / 8 lanes a row; thread i takes row i afterwards
+            constexpr int kLanes = D / 8, kSide = 32 / kLanes, kBatch = 8;
+            const int e = lane % kLanes;  // 16-byte chunk of the row
+            const uint32_t base = sbase + T::kQ + static_cast<uint32_t>(warp / 4 * T::kTile + e / 8 * T::kHalf);
+            for (int k0 = 0; k0 < kLanes; k0 += kBatch) {
+                uint4 x[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int qrow = row0 + 32 * warp + (k0 + k) * kSide + lane / kLanes;
+                    x[k] = make_uint4(0, 0, 0, 0);
+                    if (qrow < rows)
+                        x[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + static_cast<long long>(s.qs + qrow / group) * p.q_stride +
+                                                                    static_cast<long long>(h * group + qrow % group) * D) + e);
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    uint32_t big = __vmaxu2(__vmaxu2(x[k].x & 0x7FFF7FFFu, x[k].y & 0x7FFF7FFFu), __vmaxu2(x[k].z & 0x7FFF7FFFu, x[k].w & 0x7FFF7FFFu));
+                    big = max(big & 0xFFFFu, big >> 16);
+#pragma unroll
+                    for (int o = 1; o < kLanes; o *= 2) big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+                    float up, down;
+                    row_scale(big, up, down);
+                    const float fr = __shfl_sync(0xFFFFFFFFu, down, lane % kSide * kLanes);  // of row lane % kSide of these
+                    if (lane / kSide == k0 + k) f = p.scale * kLog2e * p.s.k_unit * fr;
+                    const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) o[y] = pack_f16(__uint_as_float(w[y] << 16) * up, __uint_as_float(w[y] & 0xFFFF0000u) * up);
+                    const int i = 32 * (warp % 4) + (k0 + k) * kSide + lane / kLanes;  // row of the row tile
+                    st_smem_v4(base + static_cast<uint32_t>(i * 128 + ((e % 8 ^ i % 8) << 4)), make_uint4(o[0], o[1], o[2], o[3]));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            see = p.causal ? (real ? max(s.kvl - s.ql + row / group + 1, 0) : 0) : s.kvl;
+        }
         const int a = warp / 4;
         if (a == 0 || two) {
             const uint32_t quad = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16);
@@ -752,8 +873,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             // ---- results -----------------------------------------------------------------------------------
             if (tiles > 0) wait(o_full, 0);
             tc_fence_after();
-            if (gridDim.y > 1) griddep_wait();  // the kernel ahead may use the workspace
-            const float scale = gridDim.y > 1 ? 1.f : l == 0.f ? 0.f : p.s.v_unit / l;
+            if (slices > 1) griddep_wait();  // the kernel ahead may use the workspace
+            const float scale = slices > 1 ? 1.f : l == 0.f ? 0.f : p.s.v_unit / l;
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
                 float v[32];
@@ -767,39 +888,39 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                 for (int i = 0; i < 32; ++i)
                     v[i] = nan_groups >> (2 * q + i / 16) & 1 ? __uint_as_float(0x7FC00000u) : l == 0.f ? 0.f : v[i] * scale;
                 if (!real) continue;
-                if (gridDim.y == 1) {
+                if (slices == 1) {
                     store32(dst + 32 * q, v);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) mine[(32 * q + i) * kRows + tid] = v[i];
                 }
             }
-            if (real && gridDim.y == 1 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-            if (real && gridDim.y > 1) {
+            if (real && slices == 1 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (real && slices > 1) {
                 mine[D * kRows + tid] = m;
                 mine[(D + 1) * kRows + tid] = l;
             }
         }
     }
-    if (gridDim.y > 1) {
+    if (slices > 1) {
         // The slices of a row tile are joined by the CTA that finishes last, in their order.
         __threadfence();
         __syncthreads();
         if (tid == 0) {
-            unsigned int* counter = static_cast<unsigned int*>(p.workspace) + blockIdx.x;
-            last_flag = atomicAdd(counter, 1u) + 1 == gridDim.y;
+            unsigned int* counter = static_cast<unsigned int*>(p.workspace) + rest;
+            last_flag = atomicAdd(counter, 1u) + 1 == static_cast<unsigned int>(slices);
             if (last_flag) *counter = 0;
             __threadfence();
         }
         __syncthreads();
         if (last_flag && real) {
-            const float* first = parts + static_cast<size_t>(blockIdx.x) * gridDim.y * T::kPartFloats + tid;
+            const float* from = first + tid;
             float top = -INFINITY;
-            for (unsigned int x = 0; x < gridDim.y; ++x) top = fmaxf(top, __ldcg(first + x * static_cast<size_t>(T::kPartFloats) + D * kRows));
+            for (int x = 0; x < slices; ++x) top = fmaxf(top, __ldcg(from + x * static_cast<size_t>(T::kPartFloats) + D * kRows));
             const float base = top == -INFINITY ? 0.f : top;
             float sum = 0.f;
-            for (unsigned int x = 0; x < gridDim.y; ++x) {
-                const float* part = first + x * static_cast<size_t>(T::kPartFloats);
+            for (int x = 0; x < slices; ++x) {
+                const float* part = from + x * static_cast<size_t>(T::kPartFloats);
                 const float lx = __ldcg(part + (D + 1) * kRows);
                 if (lx != 0.f) sum += lx * ex2(__ldcg(part + D * kRows) - base);
             }
@@ -808,8 +929,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                for (unsigned int x = 0; x < gridDim.y; ++x) {
-                    const float* part = first + x * static_cast<size_t>(T::kPartFloats);
+                for (int x = 0; x < slices; ++x) {
+                    const float* part = from + x * static_cast<size_t>(T::kPartFloats);
                     if (__ldcg(part + (D + 1) * kRows) == 0.f) continue;  // a slice of which the row sees nothing
                     const float w = ex2(__ldcg(part + D * kRows) - base);
 #pragma unroll
@@ -854,32 +975,26 @@ int launch_tiles(const AttArgs& a, cudaStream_t stream) {
     static_assert(static_cast<size_t>(T::kPartFloats) * kAttMaxSlices <= kAttPartFloatsTotal, "the slices' results fit the workspace");
     const long long grid = tiles_bound(a);
     if (grid == 0) return 0;  // no sequence can have q_min queries
-    // Few row tiles: the keys of each in slices, as many as fill the GPU, down to 4 key tiles a slice.
     const int sms = attn_sm_count();
     if (sms == 0) return -7;
-    const int room = sms < kAttMaxSlices ? sms : kAttMaxSlices;
-    long long slices = room / grid;
-    const long long most = (static_cast<long long>(a.max_pages) << a.s.page_shift) / (4 * kKeys);
-    if (slices > most) slices = most;
-    if (slices < 1) slices = 1;
     // Behind a launch for the sequences of few queries this kernel may start before that one has ended: it reads
     // nothing of it, and waits for it before it touches the workspace.
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), static_cast<unsigned>(slices));
+    cfg.gridDim = dim3(static_cast<unsigned>(grid + sms));  // slices take fewer than sms more
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = T::kSmem;
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = a.q_min > 0 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attend_tiles_kernel<D>, a) == cudaSuccess ? 0 : -7;
+    return cudaLaunchKernelEx(&cfg, attend_tiles_kernel<D>, a, sms) == cudaSuccess ? 0 : -7;
 }
 
 }  // namespace
 
-bool attention_tiles_take(const AttArgs& a) { return a.s.dim <= 128 && tiles_bound(a) <= 0x7FFFFFFFLL; }
+bool attention_tiles_take(const AttArgs& a) { return a.s.dim <= 128 && tiles_bound(a) <= 0x7FFF0000LL; }
 
 int launch_attention_tiles(const AttArgs& a, cudaStream_t stream) {
     return a.s.dim == 64 ? launch_tiles<64>(a, stream) : launch_tiles<128>(a, stream);
