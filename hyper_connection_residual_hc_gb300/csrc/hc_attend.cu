@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
     __shared__ int last_flag;
     const int tid = static_cast<int>(threadIdx.x), warp = tid / 32, lane = tid % 32;
     const int r = lane / 4, c = lane % 4;
-    const int heads = p.s.heads, group = p.q_heads / heads;
+    const int heads = p.s.heads, group = p.group.by;
     const int team = warp / kSplit, part = warp % kSplit;
     const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(team * P::kStages * P::kStage);
     float* merge = reinterpret_cast<float*>(smem + P::kRing);
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
     Segment g = {};
     // the tile's bounds, from g.s, g.tile, g.u0 and g.u1
     auto place = [&]() {
-        const TileBounds t = tile_bounds(p, g.s, group, g.tile * R, min(g.tile * R + R, g.s.ql * group) - 1);
+        const TileBounds t = tile_bounds(p, g.s, g.tile * R, min(g.tile * R + R, g.s.ql * group) - 1);
         g.lo = t.lo;
         g.hi = t.hi;
         g.all_lo = t.all_lo;
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
         uint32_t qf[kSplit == 1 ? kNT : 1][kKeySteps][2];  // (kSplit = 2: in shared memory)
         float f[kNT][2];   // score factor (log2 units) of rows 2c, 2c + 1 (kSplit = 2: loaded when needed)
         // keys below this position are seen (causal)
-        auto sees = [&](int row) { return p.causal ? (row < rows ? max(pos0 + row / group + 1, 0) : 0x7FFFFFFF) : g.s.kvl; };
+        auto sees = [&](int row) { return p.causal ? (row < rows ? max(pos0 + divide(row, p.group) + 1, 0) : 0x7FFFFFFF) : g.s.kvl; };
         auto see = [&](int t, int j) {
             if constexpr (kSplit == 1) return sees(row0 + 8 * t + 2 * c + j);
             else return static_cast<int>(lds32(smem_u32(factors) + static_cast<uint32_t>((R + 8 * t + 2 * c + j) * 4)));
@@ -372,10 +372,11 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
             if (kSplit == 2 && t % kWarps != warp) continue;  // one warp makes a tile's fragments for all
             const int row = row0 + 8 * t + r;
             const bool real = row < rows;
+            const int query = real ? divide(row, p.group) : 0;
             uint4 x[D / 32];
             const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
-                                       static_cast<long long>(g.s.qs + (real ? row / group : 0)) * p.q_stride +
-                                       static_cast<long long>(g.h * group + (real ? row % group : 0)) * D + c * (D / 4);
+                                       static_cast<long long>(g.s.qs + query) * p.q_stride +
+                                       static_cast<long long>(g.h * group + (real ? row - query * group : 0)) * D + c * (D / 4);
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) x[e] = real ? __ldg(reinterpret_cast<const uint4*>(src) + e) : make_uint4(0, 0, 0, 0);
             uint32_t big = 0;
@@ -745,8 +746,8 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
             const int row = drow0 + 8 * (tj / 2) + 2 * c + tj % 2;
             if (row >= drows) return;
             const float scale = sum == 0.f ? 0.f : p.s.v_unit / sum;
-            const long long token = done.s.qs + row / group;
-            const int head = done.h * group + row % group;
+            const int query = divide(row, p.group), head = done.h * group + row - query * group;
+            const long long token = done.s.qs + query;
             const int tile = 2 * pr / P::kPassTiles * kTiles + pass * P::kPassTiles + 2 * pr % P::kPassTiles;
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D + r * (D / 8) + 2 * tile;
             const __nv_bfloat162 x = __floats2bfloat162_rn(v[0] * scale, v[1] * scale), y = __floats2bfloat162_rn(v[2] * scale, v[3] * scale);
@@ -909,7 +910,7 @@ int launch_attention(const AttArgs& args, cudaStream_t stream) {
     a.q_min = 0;
     a.q_max = kAnyQueries;
     if (a.max_q_len > a.n) a.max_q_len = static_cast<int>(a.n);  // n is at most 2^31 - 1
-    const int group = a.q_heads / a.s.heads;
+    const int group = a.group.by;
     const long long rows = static_cast<long long>(a.max_q_len) * group;
     if (rows < kTilesFromRows || !attention_tiles_take(a)) return launch_rows_for(rows, a, stream);
     // Sequences of a single query, or so few that they fit the same tile of rows, among longer ones (chunks of a prefill in

@@ -311,18 +311,18 @@ struct FindScratch {
 // start are short (where an SM gets up to kOrderedWaves of them: among more it matters little). As many row tiles as
 // fill the SMs a whole number of times are taken whole; those left, if they fill half of the SMs at most, are cut into
 // slices that fill them.
-__device__ __forceinline__ Found find_tile(const AttArgs& p, int group, int cta, int sms, int tid, FindScratch& f) {
-    const int warp = tid / 32, lane = tid % 32;
+__device__ __forceinline__ Found find_tile(const AttArgs& p, int cta, const Divider& sms, const Divider& heads, int tid, FindScratch& f) {
+    const int warp = tid / 32, lane = tid % 32, group = p.group.by;
     struct Seq {
-        long long rows, behind;  // rows; those of (queries - keys) queries
-        int tiles, kvl;
+        long long behind;  // rows of (queries - keys) queries
+        int rows, tiles, kvl;
     };
     auto load = [&](int b) {
         Seq q = {};
         if (b < p.seqs) {
             const SeqRows s = load_seq(p, b, cta == 0 ? &g_hc_tiles_error : nullptr);
-            q.rows = static_cast<long long>(s.ql) * group;
-            q.tiles = static_cast<int>((q.rows + kRows - 1) / kRows);
+            q.rows = s.ql * group;
+            q.tiles = static_cast<int>((static_cast<unsigned int>(q.rows) + kRows - 1) / kRows);
             q.kvl = s.kvl;
             q.behind = static_cast<long long>(s.ql - s.kvl) * group;
         }
@@ -336,10 +336,10 @@ __device__ __forceinline__ Found find_tile(const AttArgs& p, int group, int cta,
     // how many of a sequence's row tiles (its last ones) have more than x key tiles, where there is no window
     auto above = [&](const Seq& q, int x) {
         if (x < 0) return q.tiles;
-        const long long keys = static_cast<long long>(kKeys) * x;  // a row must see more
+        const int keys = kKeys * x;  // a row must see more
         if (!p.causal) return q.kvl > keys ? q.tiles : 0;
-        const long long r0 = q.behind + keys * group;  // the first row that does
-        return r0 <= 0 ? q.tiles : r0 >= q.rows ? 0 : q.tiles - static_cast<int>(r0 / kRows);
+        const long long r0 = q.behind + static_cast<long long>(keys) * group;  // the first row that does
+        return r0 <= 0 ? q.tiles : r0 >= q.rows ? 0 : q.tiles - static_cast<int>(static_cast<unsigned int>(r0) / kRows);
     };
     int turn = 0;
     auto sum = [&](int v) {  // over the block; what a call leaves is read before the next but one writes there
@@ -366,21 +366,20 @@ __device__ __forceinline__ Found find_tile(const AttArgs& p, int group, int cta,
     }
     top = __reduce_max_sync(0xFFFFFFFFu, top);
     if (!few && lane == 0) f.top[warp] = top;
-    const int heads = p.s.heads;
-    const long long all = static_cast<long long>(all_above(-1)) * heads;
-    const int items = static_cast<int>(min(all, 0x7FFFFFFFLL)), whole = items / sms * sms, left = items - whole;
+    const long long all = static_cast<long long>(all_above(-1)) * heads.by;
+    const int items = static_cast<int>(min(all, 0x7FFFFFFFLL)), whole = divide(items, sms) * sms.by, left = items - whole;
     Found r = {-1, 0, 0, 0, 0, 1};
     int item = cta;
     if (cta >= whole && left > 0) {
-        r.slices = max(1, min(sms, kAttMaxSlices) / left);
+        r.slices = max(1, min(sms.by, kAttMaxSlices) / left);
         r.rest = (cta - whole) / r.slices;
-        r.slice = (cta - whole) % r.slices;
+        r.slice = cta - whole - r.rest * r.slices;
         item = whole + r.rest;
     }
     if (item >= items) return r;  // the same in every thread
-    const int want = item / heads;  // in the order
-    r.head = item - want * heads;
-    const bool ordered = items < kOrderedWaves * sms;
+    const int want = divide(item, heads);  // in the order
+    r.head = item - want * heads.by;
+    const bool ordered = items < kOrderedWaves * sms.by;
     int lo = 0, exceed = 0;
     if (ordered) {
         // the least number of key tiles that no more than `want` row tiles exceed, and how many do
@@ -446,9 +445,11 @@ struct BlockRegs {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs p, int sms) {
+__global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs p, const Divider sms, const Divider kv_heads) {
     using T = TilePlan<D>;
     constexpr int kSteps = D / 16;       // MMAs of S
+    constexpr int kLanes = D / 8, kSide = 32 / kLanes;  // lanes to a row in memory, 16 bytes each, and rows side by side
+    constexpr int kBatch = 8;                           // such loads of a warp in flight
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ FindScratch find_scratch;
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     __shared__ uint32_t nan_any[kNotes];                // per key tile: some value's scale is NaN
     const uint32_t sbase = smem_u32(smem);
     const int tid = static_cast<int>(threadIdx.x), warp = tid / 32, lane = tid % 32;
-    const int heads = p.s.heads, group = p.q_heads / heads;
+    const int group = p.group.by;
 
     const uint32_t bars = sbase + T::kBars;
     auto k_full = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     }
 
     // ---- which rows and keys -------------------------------------------------------------------------------
-    const Found found = find_tile(p, group, static_cast<int>(blockIdx.x), sms, tid, find_scratch);
+    const Found found = find_tile(p, static_cast<int>(blockIdx.x), sms, kv_heads, tid, find_scratch);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     const SeqRows s = load_seq(p, b, nullptr);
     const int rows = s.ql * group, row0 = tile * kRows;
     const bool two = rows - row0 > kRowTile;  // the second row tile has rows
-    const TileBounds g = tile_bounds(p, s, group, row0, min(row0 + kRows, rows) - 1);
+    const TileBounds g = tile_bounds(p, s, row0, min(row0 + kRows, rows) - 1);
     // this CTA's slice of the key tiles: cache blocks from block0 on, `tiles` tiles of 8
     int block0 = g.lo / 16;
     const int block_end = (g.hi + 15) / 16;
@@ -526,9 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     const int row = row0 + tid;
     const bool real = softmax && row < rows;
     // where the row's results go
-    const long long token = s.qs + (real ? row / group : 0);
-    const int head = h * group + (real ? row % group : 0);
-    const long long at = token * p.q_heads + head;
+    const int query = real ? divide(row, p.group) : 0, head = h * group + (real ? row - query * group : 0);
+    const long long token = s.qs + query, at = token * p.q_heads + head;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D;
     float* parts = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kAttCounterBytes);
     float* first = parts + static_cast<size_t>(rest) * found.slices * T::kPartFloats;  // of this row tile's slices: [column, maximum, sum][row]
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                     continue;
                 }
                 const int tok = (block0 + 8 * j + kBlocksPerWarp * w + i) * 16;
-                src[i] = p.cache + (((static_cast<long long>(page) * heads + h) << (p.s.page_shift - 4)) +
+                src[i] = p.cache + (((static_cast<long long>(page) * kv_heads.by + h) << (p.s.page_shift - 4)) +
                                     ((tok & ((1 << p.s.page_shift) - 1)) >> 4)) * kv_block_bytes(D);
             }
         };
@@ -767,19 +767,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     } else {
         // ===== softmax ========================================================================================
         {
-            // the warp's 32 rows of queries, D / 8 lanes a row; thread i takes row i afterwards
-            constexpr int kLanes = D / 8, kSide = 32 / kLanes, kBatch = 8;
+            // the warp's 32 rows of queries, kLanes lanes a row; thread i takes row i afterwards
             const int e = lane % kLanes;  // 16-byte chunk of the row
             const uint32_t base = sbase + T::kQ + static_cast<uint32_t>(warp / 4 * T::kTile + e / 8 * T::kHalf);
             for (int k0 = 0; k0 < kLanes; k0 += kBatch) {
                 uint4 x[kBatch];
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
-                    const int qrow = row0 + 32 * warp + (k0 + k) * kSide + lane / kLanes;
+                    const int y = row0 + 32 * warp + (k0 + k) * kSide + lane / kLanes, i = divide(y, p.group);
                     x[k] = make_uint4(0, 0, 0, 0);
-                    if (qrow < rows)
-                        x[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + static_cast<long long>(s.qs + qrow / group) * p.q_stride +
-                                                                    static_cast<long long>(h * group + qrow % group) * D) + e);
+                    if (y < rows)
+                        x[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + static_cast<long long>(s.qs + i) * p.q_stride +
+                                                                    static_cast<long long>(h * group + y - i * group) * D) + e);
                 }
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
@@ -802,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
-            see = p.causal ? (real ? max(s.kvl - s.ql + row / group + 1, 0) : 0) : s.kvl;
+            see = p.causal ? (real ? max(s.kvl - s.ql + query + 1, 0) : 0) : s.kvl;
         }
         const int a = warp / 4;
         if (a == 0 || two) {
@@ -887,12 +886,36 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     v[i] = nan_groups >> (2 * q + i / 16) & 1 ? __uint_as_float(0x7FC00000u) : l == 0.f ? 0.f : v[i] * scale;
-                if (!real) continue;
                 if (slices == 1) {
-                    store32(dst + 32 * q, v);
-                } else {
+                    // to where the row's queries were (all MMAs that read them are done), to be written by whole rows
+                    const int i = tid % kRowTile;
+                    const uint32_t to_row = sbase + T::kQ + static_cast<uint32_t>(a * T::kTile + q / 2 * T::kHalf + i * 128);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const __nv_bfloat162 t = __floats2bfloat162_rn(v[8 * y + 2 * z], v[8 * y + 2 * z + 1]);
+                            w[z] = *reinterpret_cast<const uint32_t*>(&t);
+                        }
+                        st_smem_v4(to_row + static_cast<uint32_t>((q % 2 * 4 + y ^ i % 8) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+                    }
+                } else if (real) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) mine[(32 * q + i) * kRows + tid] = v[i];
+                }
+            }
+            if (slices == 1) {
+                __syncwarp();
+                const int e = lane % kLanes;
+                const uint32_t from = sbase + T::kQ + static_cast<uint32_t>(a * T::kTile + e / 8 * T::kHalf);
+#pragma unroll
+                for (int k = 0; k < kLanes; ++k) {
+                    const int in = k * kSide + lane / kLanes, i = 32 * (warp % 4) + in, y = row0 + 32 * warp + in, j = divide(y, p.group);
+                    if (y >= rows) continue;
+                    const uint4 w = ld_smem_v4(from + static_cast<uint32_t>(i * 128 + ((e % 8 ^ i % 8) << 4)));
+                    reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(s.qs + j) * p.out_stride +
+                                             static_cast<long long>(h * group + y - j * group) * D)[e] = w;
                 }
             }
             if (real && slices == 1 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -989,7 +1012,7 @@ int launch_tiles(const AttArgs& a, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = a.q_min > 0 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, attend_tiles_kernel<D>, a, sms) == cudaSuccess ? 0 : -7;
+    return cudaLaunchKernelEx(&cfg, attend_tiles_kernel<D>, a, make_divider(sms), make_divider(a.s.heads)) == cudaSuccess ? 0 : -7;
 }
 
 }  // namespace

@@ -87,6 +87,18 @@ static_assert(size_t(2) * kAttMaxCtas * kAttPartFloats <= kAttPartFloatsTotal, "
 constexpr size_t kAttCounterBytes = kAttMaxCtas * 4;
 constexpr size_t kAttWorkspaceBytes = kAttCounterBytes + kAttPartFloatsTotal * 4;
 constexpr int kAnyQueries = 0x7FFFFFFF;
+// Division of 0..2^31 - 1 by a number that the host knows: n * ceil(2^(31 + s) / d) / 2^(31 + s) with 2^s >= d is off
+// by less than 1 / d, so its integer part is exact. One product and a shift, where a division takes a few tens of
+// instructions in a row.
+struct Divider {
+    int by;
+    unsigned int factor, shift;
+};
+inline Divider make_divider(int by) {
+    unsigned int s = 0;
+    while ((1ull << s) < static_cast<unsigned long long>(by)) ++s;
+    return {by, static_cast<unsigned int>(((1ull << (31 + s)) + static_cast<unsigned long long>(by) - 1) / static_cast<unsigned long long>(by)), 31 + s};
+}
 struct AttArgs {
     const void* q;
     long long q_stride;
@@ -102,6 +114,7 @@ struct AttArgs {
     long long out_stride;
     float* lse;
     void* workspace;
+    Divider group;     // query heads that share a kv head
     int q_min, q_max;  // a kernel takes the sequences with so many queries and leaves the others to the other kernel
 };
 int launch_attention(const AttArgs& a, cudaStream_t stream);

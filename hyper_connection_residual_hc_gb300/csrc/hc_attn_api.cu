@@ -293,6 +293,7 @@ int hc_kv_attention(const void* q, int64_t q_stride, const int* q_start, const i
     g.out_stride = out_stride;
     g.lse = lse;
     g.workspace = workspace;
+    g.group = make_divider(a.q_heads / s.heads);
     return status(launch_attention(g, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -46,6 +46,10 @@ __device__ __forceinline__ void row_scale(uint32_t m, float& up, float& down) {
     down = __uint_as_float((e - 7u) << 23);
 }
 
+__device__ __forceinline__ int divide(int n, const Divider& d) {
+    return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned int>(n)) * d.factor) >> d.shift);
+}
+
 struct SeqRows {
     int qs, ql, kvl;  // first row of q, queries (0: another kernel takes the sequence), keys
 };
@@ -70,11 +74,11 @@ __device__ __forceinline__ SeqRows load_seq(const AttArgs& p, int b, unsigned in
 struct TileBounds {
     int lo, hi, all_lo, all_hi;
 };
-__device__ __forceinline__ TileBounds tile_bounds(const AttArgs& p, const SeqRows& s, int group, int row0, int row1) {
+__device__ __forceinline__ TileBounds tile_bounds(const AttArgs& p, const SeqRows& s, int row0, int row1) {
     TileBounds g;
     if (p.causal) {
         const int pos0 = s.kvl - s.ql;
-        const int first = pos0 + row0 / group, last = pos0 + row1 / group;
+        const int first = pos0 + divide(row0, p.group), last = pos0 + divide(row1, p.group);
         g.hi = min(max(last + 1, 0), s.kvl);
         g.all_hi = first + 1;
         // (positions are negative where a sequence has more queries than keys; a window is as large as an int)
