@@ -53,8 +53,7 @@ static_assert(kDequantWarps == 4, "a word of notes");
 constexpr int kBlocksPerWarp = kKeys / 16 / kDequantWarps;  // cache blocks of a key tile that a dequantising warp takes
 constexpr int kMmaWarp = kSoftmaxWarps + kDequantWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
-constexpr int kLeastSlice = 4;  // key tiles of a slice at least
-constexpr int kOrderedWaves = 8;
+constexpr int kLeastSlice = 8;  // key tiles of a slice at least: joining costs as much as a few
 constexpr int kNotes = 8;       // key tiles whose notes (absent blocks, NaN values) are kept
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kMaxDevices = 64;
@@ -304,13 +303,14 @@ struct Found {
     int seq, tile, head, rest, slice, slices;
 };
 struct FindScratch {
-    int part[2][16], top[16];  // of the warps; two sums in turn
+    int part[2][16];  // of the warps, for one sum and the next
     int seq, tile;
 };
-// By all threads. CTAs start in turn as SMs get free: the row tiles with the most key tiles come first, so that the last ones to
-// start are short (where an SM gets up to kOrderedWaves of them: among more it matters little). As many row tiles as
-// fill the SMs a whole number of times are taken whole; those left, if they fill half of the SMs at most, are cut into
-// slices that fill them.
+// By all threads. CTAs start in turn as SMs get free, so the row tiles with the most key tiles come first, and the last ones to
+// start are short: 2 fresh prompts of 2,048 tokens, 143 us in this order, 152 us one sequence after the other. (With more
+// than 32 sequences the latter: the search would take barriers, and the order matters less: 64 of 10 queries, 111 and 104 us.)
+// As many row tiles as fill the SMs a whole number of times are taken whole; those left, if they fill half of the SMs at
+// most, are cut into slices that fill them: 1,024 queries behind 32,768 keys 1,024 us whole, 604 us cut.
 __device__ __forceinline__ Found find_tile(const AttArgs& p, int cta, const Divider& sms, const Divider& heads, int tid, FindScratch& f) {
     const int warp = tid / 32, lane = tid % 32, group = p.group.by;
     struct Seq {
@@ -330,44 +330,22 @@ __device__ __forceinline__ Found find_tile(const AttArgs& p, int cta, const Divi
     };
     // Up to 32 sequences: each warp does it all, one sequence a lane, without barriers.
     const bool few = p.seqs <= 32;
-    const int me = few ? lane : tid, width = few ? 32 : kThreads;
+    const int me = few ? lane : tid;
     const Seq own = load(me);
-    auto seq = [&](int b) { return b == me ? own : load(b); };
-    // how many of a sequence's row tiles (its last ones) have more than x key tiles, where there is no window
-    auto above = [&](const Seq& q, int x) {
-        if (x < 0) return q.tiles;
-        const int keys = kKeys * x;  // a row must see more
-        if (!p.causal) return q.kvl > keys ? q.tiles : 0;
-        const long long r0 = q.behind + static_cast<long long>(keys) * group;  // the first row that does
-        return r0 <= 0 ? q.tiles : r0 >= q.rows ? 0 : q.tiles - static_cast<int>(static_cast<unsigned int>(r0) / kRows);
-    };
-    int turn = 0;
-    auto sum = [&](int v) {  // over the block; what a call leaves is read before the next but one writes there
-        v = __reduce_add_sync(0xFFFFFFFFu, v);
-        if (few) return v;
-        int* part = f.part[turn ^= 1];
-        if (lane == 0) part[warp] = v;
+    int tiles = own.tiles;
+    if (!few)
+        for (int b = me + kThreads; b < p.seqs; b += kThreads) tiles += load(b).tiles;
+    tiles = __reduce_add_sync(0xFFFFFFFFu, tiles);
+    if (!few) {
+        if (tid == 0) f.seq = -1;
+        if (lane == 0) f.part[0][warp] = tiles;
         __syncthreads();
-        int all = 0;
+        tiles = 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) all += part[w];
-        return all;
-    };
-    auto all_above = [&](int x) {
-        int n = 0;
-        for (int b = me; b < p.seqs; b += width) n += above(seq(b), x);
-        return sum(n);
-    };
-    if (tid == 0) f.seq = -1;
-    int top = 0;  // key tiles of the longest sequence
-    for (int b = me; b < p.seqs; b += width) {
-        const Seq q = seq(b);
-        if (q.tiles > 0) top = max(top, (q.kvl + kKeys - 1) / kKeys);
+        for (int w = 0; w < kThreads / 32; ++w) tiles += f.part[0][w];
     }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if (!few && lane == 0) f.top[warp] = top;
-    const long long all = static_cast<long long>(all_above(-1)) * heads.by;
-    const int items = static_cast<int>(min(all, 0x7FFFFFFFLL)), whole = divide(items, sms) * sms.by, left = items - whole;
+    const int items = static_cast<int>(min(static_cast<long long>(tiles) * heads.by, 0x7FFFFFFFLL));
+    const int whole = divide(items, sms) * sms.by, left = items - whole;
     Found r = {-1, 0, 0, 0, 0, 1};
     int item = cta;
     if (cta >= whole && left > 0) {
@@ -379,17 +357,27 @@ __device__ __forceinline__ Found find_tile(const AttArgs& p, int cta, const Divi
     if (item >= items) return r;  // the same in every thread
     const int want = divide(item, heads);  // in the order
     r.head = item - want * heads.by;
-    const bool ordered = items < kOrderedWaves * sms.by;
-    int lo = 0, exceed = 0;
-    if (ordered) {
-        // the least number of key tiles that no more than `want` row tiles exceed, and how many do
-        int hi = top;
-        if (!few) {
+    auto scan = [&](int v) {  // inclusive, over the warp
 #pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w) hi = max(hi, f.top[w]);
+        for (int o = 1; o < 32; o *= 2) {
+            const int y = __shfl_up_sync(0xFFFFFFFFu, v, o);
+            if (lane >= o) v += y;
         }
+        return v;
+    };
+    if (few) {
+        // how many of the lane's row tiles (the last ones) have more than x key tiles, where there is no window
+        auto above = [&](int x) {
+            if (x < 0) return own.tiles;
+            const int keys = kKeys * x;  // a row must see more
+            if (!p.causal) return own.kvl > keys ? own.tiles : 0;
+            const long long r0 = own.behind + static_cast<long long>(keys) * group;  // the first row that does
+            return r0 <= 0 ? own.tiles : r0 >= own.rows ? 0 : own.tiles - static_cast<int>(static_cast<unsigned int>(r0) / kRows);
+        };
+        // the least number of key tiles that no more than `want` row tiles exceed, and how many do
+        int lo = 0, hi = __reduce_max_sync(0xFFFFFFFFu, own.tiles > 0 ? (own.kvl + kKeys - 1) / kKeys : 0), exceed = 0;
         while (lo < hi) {
-            const int x = (lo + hi) / 2, n = all_above(x);
+            const int x = (lo + hi) / 2, n = __reduce_add_sync(0xFFFFFFFFu, above(x));
             if (n <= want) {
                 hi = x;
                 exceed = n;
@@ -397,30 +385,21 @@ __device__ __forceinline__ Found find_tile(const AttArgs& p, int cta, const Divi
                 lo = x + 1;
             }
         }
+        const int n0 = above(lo), n = above(lo - 1) - n0, x = exceed + scan(n);
+        const int src = __ffs(static_cast<int>(__ballot_sync(0xFFFFFFFFu, x > want))) - 1;
+        if (src >= 0) {
+            r.seq = src;
+            r.tile = __shfl_sync(0xFFFFFFFFu, own.tiles - n0 - n + want - (x - n), src);
+        }
+        return r;
     }
-    int before = exceed;
-    for (int b0 = 0; b0 < p.seqs && before <= want; b0 += width) {
-        const Seq q = seq(b0 + me);
-        const int n0 = ordered ? above(q, lo) : 0, n = ordered ? above(q, lo - 1) - n0 : q.tiles;
-        int x = n;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (few) {
-            x += before;
-            const int src = __ffs(static_cast<int>(__ballot_sync(0xFFFFFFFFu, x > want))) - 1;
-            if (src >= 0) {
-                r.seq = src;
-                r.tile = __shfl_sync(0xFFFFFFFFu, q.tiles - n0 - n + want - (x - n), src);
-            }
-            return r;
-        }
-        int* part = f.part[turn ^= 1];
-        if (lane == 31) part[warp] = x;
+    int before = 0;
+    for (int b0 = 0; b0 < p.seqs && before <= want; b0 += kThreads) {
+        const int n = b0 == 0 ? own.tiles : load(b0 + tid).tiles;
+        int x = before + scan(n);
+        int* part = f.part[1 - b0 / kThreads % 2];
+        if (lane == 31) part[warp] = x - before;
         __syncthreads();
-        x += before;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) x += part[w];
@@ -428,7 +407,7 @@ __device__ __forceinline__ Found find_tile(const AttArgs& p, int cta, const Divi
         }
         if (x > want && x - n <= want) {
             f.seq = b0 + tid;
-            f.tile = q.tiles - n0 - n + want - (x - n);
+            f.tile = want - (x - n);
         }
     }
     __syncthreads();
@@ -449,7 +428,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     using T = TilePlan<D>;
     constexpr int kSteps = D / 16;       // MMAs of S
     constexpr int kLanes = D / 8, kSide = 32 / kLanes;  // lanes to a row in memory, 16 bytes each, and rows side by side
-    constexpr int kBatch = 8;                           // such loads of a warp in flight
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ FindScratch find_scratch;
@@ -770,33 +748,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             // the warp's 32 rows of queries, kLanes lanes a row; thread i takes row i afterwards
             const int e = lane % kLanes;  // 16-byte chunk of the row
             const uint32_t base = sbase + T::kQ + static_cast<uint32_t>(warp / 4 * T::kTile + e / 8 * T::kHalf);
-            for (int k0 = 0; k0 < kLanes; k0 += kBatch) {
-                uint4 x[kBatch];
+            uint4 x[kLanes];
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int y = row0 + 32 * warp + (k0 + k) * kSide + lane / kLanes, i = divide(y, p.group);
-                    x[k] = make_uint4(0, 0, 0, 0);
-                    if (y < rows)
-                        x[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + static_cast<long long>(s.qs + i) * p.q_stride +
-                                                                    static_cast<long long>(h * group + y - i * group) * D) + e);
-                }
+            for (int k = 0; k < kLanes; ++k) {
+                const int y = row0 + 32 * warp + k * kSide + lane / kLanes, i = divide(y, p.group);
+                x[k] = make_uint4(0, 0, 0, 0);
+                if (y < rows)
+                    x[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + static_cast<long long>(s.qs + i) * p.q_stride +
+                                                                static_cast<long long>(h * group + y - i * group) * D) + e);
+            }
 #pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    uint32_t big = __vmaxu2(__vmaxu2(x[k].x & 0x7FFF7FFFu, x[k].y & 0x7FFF7FFFu), __vmaxu2(x[k].z & 0x7FFF7FFFu, x[k].w & 0x7FFF7FFFu));
-                    big = max(big & 0xFFFFu, big >> 16);
+            for (int k = 0; k < kLanes; ++k) {
+                uint32_t big = __vmaxu2(__vmaxu2(x[k].x & 0x7FFF7FFFu, x[k].y & 0x7FFF7FFFu), __vmaxu2(x[k].z & 0x7FFF7FFFu, x[k].w & 0x7FFF7FFFu));
+                big = max(big & 0xFFFFu, big >> 16);
 #pragma unroll
-                    for (int o = 1; o < kLanes; o *= 2) big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
-                    float up, down;
-                    row_scale(big, up, down);
-                    const float fr = __shfl_sync(0xFFFFFFFFu, down, lane % kSide * kLanes);  // of row lane % kSide of these
-                    if (lane / kSide == k0 + k) f = p.scale * kLog2e * p.s.k_unit * fr;
-                    const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-                    uint32_t o[4];
+                for (int o = 1; o < kLanes; o *= 2) big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+                float up, down;
+                row_scale(big, up, down);
+                const float fr = __shfl_sync(0xFFFFFFFFu, down, lane % kSide * kLanes);  // of row lane % kSide of these
+                if (lane / kSide == k) f = p.scale * kLog2e * p.s.k_unit * fr;
+                const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                uint32_t o[4];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) o[y] = pack_f16(__uint_as_float(w[y] << 16) * up, __uint_as_float(w[y] & 0xFFFF0000u) * up);
-                    const int i = 32 * (warp % 4) + (k0 + k) * kSide + lane / kLanes;  // row of the row tile
-                    st_smem_v4(base + static_cast<uint32_t>(i * 128 + ((e % 8 ^ i % 8) << 4)), make_uint4(o[0], o[1], o[2], o[3]));
-                }
+                for (int y = 0; y < 4; ++y) o[y] = pack_f16(__uint_as_float(w[y] << 16) * up, __uint_as_float(w[y] & 0xFFFF0000u) * up);
+                const int i = 32 * (warp % 4) + k * kSide + lane / kLanes;  // row of the row tile
+                st_smem_v4(base + static_cast<uint32_t>(i * 128 + ((e % 8 ^ i % 8) << 4)), make_uint4(o[0], o[1], o[2], o[3]));
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -873,6 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             if (tiles > 0) wait(o_full, 0);
             tc_fence_after();
             if (slices > 1) griddep_wait();  // the kernel ahead may use the workspace
+            const bool nan_row = __any_sync(0xFFFFFFFFu, nan_groups != 0);
             const float scale = slices > 1 ? 1.f : l == 0.f ? 0.f : p.s.v_unit / l;
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
@@ -884,8 +861,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                     for (int i = 0; i < 32; ++i) v[i] = 0.f;
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    v[i] = nan_groups >> (2 * q + i / 16) & 1 ? __uint_as_float(0x7FC00000u) : l == 0.f ? 0.f : v[i] * scale;
+                for (int i = 0; i < 32; ++i) v[i] *= scale;  // a row that sees nothing has zeros here and the scale 0
+                if (nan_row) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (nan_groups >> (2 * q + i / 16) & 1) v[i] = __uint_as_float(0x7FC00000u);
+                }
                 if (slices == 1) {
                     // to where the row's queries were (all MMAs that read them are done), to be written by whole rows
                     const int i = tid % kRowTile;

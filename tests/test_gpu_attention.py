@@ -605,6 +605,16 @@ def test_attention_many_sequences(seqs):
     gu.device_error_clear()
 
 
+@pytest.mark.parametrize("seqs", [32, 33, 500, 900])
+def test_attention_many_sequences_of_many_queries(seqs):
+    rng = np.random.default_rng(seqs)
+    lens = [(int(q), int(kv)) for q, kv in zip(rng.choice([0, 1, 4, 5, 9, 20, 40], seqs), rng.integers(0, 40, seqs))]
+    p = Problem(lens, 8, 1, 64, 16, seed=seqs).to_device()
+    out, lse = p.run()
+    p.check(out, lse)
+    gu.device_error_clear()
+
+
 def test_attention_on_two_streams_at_once():
     """Two calls that overlap, each with a workspace of its own, on streams other than the tensors'."""
     ps = [Problem([(1, 3000), (1, 1000)], 5, 1, 128, 64, seed=21 + i).to_device() for i in range(2)]
