@@ -504,13 +504,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
     const bool softmax = warp < kSoftmaxWarps;
     const int row = row0 + tid;
     const bool real = softmax && row < rows;
-    // where the row's results go
-    const int query = real ? divide(row, p.group) : 0, head = h * group + (real ? row - query * group : 0);
-    const long long token = s.qs + query, at = token * p.q_heads + head;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D;
-    float* parts = reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kAttCounterBytes);
-    float* first = parts + static_cast<size_t>(rest) * found.slices * T::kPartFloats;  // of this row tile's slices: [column, maximum, sum][row]
-    float* mine = first + static_cast<size_t>(slice) * T::kPartFloats;
+    auto lse_at = [&]() {
+        const int query = divide(row, p.group);
+        return static_cast<long long>(s.qs + query) * p.q_heads + h * group + row - query * group;
+    };
+    // the slices' results in the workspace: of each [column, maximum, sum][row]
+    auto parts_of = [&](int sliced) {
+        return reinterpret_cast<float*>(static_cast<unsigned char*>(p.workspace) + kAttCounterBytes) +
+               static_cast<size_t>(sliced) * found.slices * T::kPartFloats;
+    };
 
     if (warp == kMmaWarp) {
         // ===== MMAs =======================================================================================
@@ -777,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
-            see = p.causal ? (real ? max(s.kvl - s.ql + query + 1, 0) : 0) : s.kvl;
+            see = p.causal ? (real ? max(s.kvl - s.ql + divide(row, p.group) + 1, 0) : 0) : s.kvl;
         }
         const int a = warp / 4;
         if (a == 0 || two) {
@@ -846,6 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                 l += x + y;
             }
             // ---- results -----------------------------------------------------------------------------------
+            float* mine = parts_of(rest) + static_cast<size_t>(slice) * T::kPartFloats;
             if (tiles > 0) wait(o_full, 0);
             tc_fence_after();
             if (slices > 1) griddep_wait();  // the kernel ahead may use the workspace
@@ -899,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                                              static_cast<long long>(h * group + y - j * group) * D)[e] = w;
                 }
             }
-            if (real && slices == 1 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (real && slices == 1 && p.lse) p.lse[lse_at()] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             if (real && slices > 1) {
                 mine[D * kRows + tid] = m;
                 mine[(D + 1) * kRows + tid] = l;
@@ -918,7 +921,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         }
         __syncthreads();
         if (last_flag && real) {
-            const float* from = first + tid;
+            const float* from = parts_of(rest) + tid;
+            const int query = divide(row, p.group);
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(s.qs + query) * p.out_stride +
+                                 static_cast<long long>(h * group + row - query * group) * D;
             float top = -INFINITY;
             for (int x = 0; x < slices; ++x) top = fmaxf(top, __ldcg(from + x * static_cast<size_t>(T::kPartFloats) + D * kRows));
             const float base = top == -INFINITY ? 0.f : top;
@@ -944,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                 for (int i = 0; i < 32; ++i) v[i] *= scale;
                 store32(dst + 32 * q, v);
             }
-            if (p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            if (p.lse) p.lse[lse_at()] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
         }
     }
     griddep_wait();  // the call has ended when both kernels have
