@@ -926,22 +926,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + static_cast<long long>(s.qs + query) * p.out_stride +
                                  static_cast<long long>(h * group + row - query * group) * D;
             float top = -INFINITY;
+#pragma unroll 4
             for (int x = 0; x < slices; ++x) top = fmaxf(top, __ldcg(from + x * static_cast<size_t>(T::kPartFloats) + D * kRows));
             const float base = top == -INFINITY ? 0.f : top;
             float sum = 0.f;
+#pragma unroll 4
             for (int x = 0; x < slices; ++x) {
                 const float* part = from + x * static_cast<size_t>(T::kPartFloats);
-                const float lx = __ldcg(part + (D + 1) * kRows);
-                if (lx != 0.f) sum += lx * ex2(__ldcg(part + D * kRows) - base);
+                sum = fmaf(__ldcg(part + (D + 1) * kRows), ex2(__ldcg(part + D * kRows) - base), sum);
             }
             const float scale = sum == 0.f ? 0.f : p.s.v_unit / sum;
             for (int q = 0; q < D / 32; ++q) {
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 2
                 for (int x = 0; x < slices; ++x) {
                     const float* part = from + x * static_cast<size_t>(T::kPartFloats);
-                    if (__ldcg(part + (D + 1) * kRows) == 0.f) continue;  // a slice of which the row sees nothing
                     const float w = ex2(__ldcg(part + D * kRows) - base);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = fmaf(w, __ldcg(part + (32 * q + i) * kRows), v[i]);
