@@ -7,12 +7,12 @@
 // The tensor memory path (tcgen05) would have to write every dequantised block to shared memory first, 8 times
 // the bytes that the cache has; this kernel's bound is the dequantisation and HBM, not the products.
 //
-// Measured: 256 sequences of 2,050 to 4,096 keys, 40 query and 8 kv heads of 128 (912 MB): 206 us, 4.4 TB/s, 65% of the
-// measured copy rate; 3 sequences of up to 131,072 keys: 84.5 us, 66%; 8 of up to 509 keys: 8.5 us. With few rows what is
+// Measured: 256 sequences of 2,050 to 4,096 keys, 40 query and 8 kv heads of 128 (912 MB): 202 us, 4.5 TB/s, 67% of the
+// measured copy rate; 3 sequences of up to 131,072 keys: 84 us, 67%; 8 of up to 509 keys: 8.2 us. With few rows what is
 // left is instructions: about 600 for a unit of 32 keys of a head (128 conversions from 4 bits, about as many products with
 // scales, 32 MMAs), issue slots about 60% busy, no pipe above half. Leaving out the keys' scale products would save 7 us;
 // two warps a unit (258 us) or blocks of 4 warps (255 us) lose. More rows cost more of everything: five queries of 4
-// heads each, 64 sequences, window of 1,024 keys (81 MB): 55 us.
+// heads each, 64 sequences, window of 1,024 keys (81 MB): 54 us.
 //
 // A cache block (16 tokens, one head) is laid out in A-fragment order: lane (r, c) = (lane / 4, lane % 4) finds
 // in its own 32-bit words the codes of keys r and r + 8, columns [c D/4, (c+1) D/4) (the contraction index of
@@ -58,8 +58,9 @@ constexpr int kUnit = 32;                     // tokens a warp takes at a time: 
 constexpr int kJoinSteps = 9;
 constexpr int kMaxDevices = 64;
 // Rows of the longest sequence from which hc_attend_tiles.cu takes a call: more than this kernel's largest tile of rows
-// reads and dequantises the keys twice. 64 sequences of up to 4096 keys, 28 rows: 179 us here, 243 us there; 64 of up to
-// 1000 keys, 40 rows: 143 against 90 us; 32 of up to 4096 keys, 96 rows: 129 against 81 us.
+// reads and dequantises the keys twice. 64 sequences of up to 4,096 keys, 28 rows: 143 us here, 195 us there; 64 of up to
+// 1,000 keys, 40 rows: 104 against 80 us; 32 of up to 4,096 keys, 96 rows: 107 against 62 us. (One sequence alone would be
+// better off here for longer: 40 rows over 32,768 keys, 54 against 80 us.)
 constexpr long long kTilesFromRows = 33;
 
 // The shape of a CTA. A team of kSplit warps takes a unit at a time: alone (kSplit = 1), or two warps that share it, each
@@ -915,8 +916,8 @@ int launch_attention(const AttArgs& args, cudaStream_t stream) {
     if (rows < kTilesFromRows || !attention_tiles_take(a)) return launch_rows_for(rows, a, stream);
     // Sequences of a single query, or so few that they fit the same tile of rows, among longer ones (chunks of a prefill in
     // a batch that decodes) get a launch of their own. 255 single queries over 2,050 to 4,096 keys and one chunk of 2,305,
-    // 40 and 8 heads of 128: 510 us, 1,070 us where the tiles' kernel takes all; with a chunk of 513, 299 us. Where no
-    // sequence is short the launch costs 8 us, so n = seqs * max_q_len (none is) goes without.
+    // 40 and 8 heads of 128: 434 us, 922 us where the tiles' kernel takes all; with a chunk of 513, 283 us. Where no
+    // sequence is short the launch costs 8 us or more, so n = seqs * max_q_len (none is) goes without.
     const int few = group <= 32 ? (group + 7) / 8 * 8 / group : 0;
     if (few > 0 && a.n != static_cast<long long>(a.seqs) * a.max_q_len) {
         a.q_max = few;

@@ -18,12 +18,15 @@
 // Row tiles that would leave SMs idle (few of them, or the last of many) have their key tiles cut into slices, one CTA
 // each, joined in their order by the CTA that finishes last.
 //
-// Measured: 2 sequences of 2,048 queries behind 4,096 to 6,144 cached keys, 40 query and 8 kv heads of 128: 541 us, 952
-// TFLOP/s, 49% of the measured cuBLAS rate (the first form, with separate score and value steps by 17 warps of 96 registers,
-// took 1,806 us). Of the same call the MMAs alone take 302 us, dequantising alone 278 us, the softmax alone with its barriers 444 us, and its barriers
-// alone 283 us: the round trip scores -> weights -> scores is what bounds it, with two row tiles to overlap. Tried and
-// slower: 16 softmax warps with half a row each (604 us), an MMA warp that polls for whichever row tile is ready (704 us:
-// its polling takes issue slots), 8 dequantising warps (630 us).
+// Measured: 2 sequences of 2,048 queries behind 4,096 to 6,144 cached keys, 40 query and 8 kv heads of 128: 418 us, 1,233
+// TFLOP/s, 63% of the measured cuBLAS rate (the first form, with separate score and value steps by 17 warps of 96 registers,
+// took 1,806 us). A key tile takes about 1.75 us; in an earlier form (541 us) the call's MMAs alone took 302 us,
+// dequantising alone 278, the softmax alone with its barriers 444 and its barriers alone 283: the round trip scores -> weights ->
+// scores is what bounds it, with two row tiles to overlap and no tensor memory left for a second set of scores. About 14 us a
+// CTA are its start and end; they were 27 before the queries were loaded and the outputs written by whole rows, beside
+// the first keys, and before divisions became products. Tried and slower: 16 softmax warps with half a row each
+// (604 us), an MMA warp that polls for whichever row tile is ready (704 us: its polling takes issue slots), 8
+// dequantising warps (630 us), an eighth of the exponentials by a polynomial instead of the special function unit (4% more).
 //
 // Every wait is bounded: on expiry the kernel sets a bit of the device error word, stops waiting, lets its MMAs end
 // and frees its tensor memory.
