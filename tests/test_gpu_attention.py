@@ -634,6 +634,28 @@ def test_attention_on_two_streams_at_once():
         p.check(o, l)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_of_many_queries_beside_other_calls(dim):
+    """A prefill on one stream, decode and another prefill on two others, each with a workspace of its own."""
+    ps = [Problem(lens, 8, 2, dim, 32, seed=31 + i).to_device()
+          for i, lens in enumerate([[(300, 700), (40, 1500)], [(1, 3000), (1, 1000)], [(1, 900), (200, 200), (64, 2500)]])]
+    alone = [p.run() for p in ps]
+    ws = [hc.new_kv_workspace() for _ in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for p, w, s in zip(ps, ws, streams):
+            with torch.cuda.stream(s):
+                got.append(p.run(ws=w))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert torch.equal(g[0], alone[i % 3][0]) and torch.equal(g[1], alone[i % 3][1])
+    for p, (o, l) in zip(ps, alone):
+        p.check(o, l)
+    gu.device_error_clear()
+
+
 def test_attention_replayed_as_the_context_grows():
     """One captured call, replayed with longer and shorter contexts, as a decode loop does; the workspace's counters are left
     at zero each time."""
