@@ -21,10 +21,11 @@
 // scale (exact in fp16). S^T = K Q^T leaves lane (r, c) the scores of tokens r, r + 8 and rows 2c, 2c + 1; the
 // weights, rounded to fp16, are turned into the second product's B fragment by movmatrix.
 //
-// The softmax keeps a running maximum and sum per row. The maximum is raised only when a score exceeds it by
-// more than 2^8 (weights then stay below 2^8, far inside fp16), so that most steps need no exchange between lanes
-// and no rescaling of the sums. Sums, maxima and outputs are fp32; the weights are rounded to fp16's 11 bits: a
-// relative 2^-12 on average weights, well below the bf16 rounding of the result.
+// The softmax keeps a running maximum (less a constant: kLift) and sum per row. The maximum is raised only when a score
+// exceeds it by more than 2^8 (weights then stay below 2^15, inside fp16), so that most steps need no exchange between
+// lanes and no rescaling of the sums. Sums, maxima and outputs are fp32; the weights are rounded to fp16: by 2^-11 of
+// themselves at most down to 2^-21 of the row's largest, by 2^-32 of the largest below, well below the bf16 rounding of
+// the result.
 //
 // Work. All the (sequence, kv head, tile of rows) segments of a call, each so many units of 32 tokens, are laid
 // end to end and cut into equal ranges, one a CTA, whatever the lengths. The warps of a CTA take its units in
@@ -560,7 +561,7 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
                 for (int t = 0; t < kNT; ++t)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float m2 = fmaxf(m[t][j], top[t][j]);
+                        const float m2 = fmaxf(m[t][j], top[t][j] - kLift);
                         const float fade = m2 == -INFINITY ? 1.f : ex2(m[t][j] - m2);
                         m[t][j] = m2;
                         l[t][j] *= fade;
@@ -753,7 +754,7 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + token * p.out_stride + static_cast<long long>(head) * D + r * (D / 8) + 2 * tile;
             const __nv_bfloat162 x = __floats2bfloat162_rn(v[0] * scale, v[1] * scale), y = __floats2bfloat162_rn(v[2] * scale, v[3] * scale);
             *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-            if (p.lse && r == 0 && pr == 0 && pass == 0) p.lse[token * p.q_heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            if (p.lse && r == 0 && pr == 0 && pass == 0) p.lse[token * p.q_heads + head] = log_sum_exp(top, sum);
         };
         const bool all = done.u0 == 0 && done.u1 == done.units;
         // a part of a segment: units [done.u0, done.u1) of it; the segment's first unit is `at` - done.u1 of the call

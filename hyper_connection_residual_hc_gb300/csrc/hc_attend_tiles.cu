@@ -11,9 +11,9 @@
 //     so that one tile's softmax runs under the other tile's products.
 //   2 x 4 softmax warps, one thread a row (a tensor-memory lane): scores to registers, the running maximum, weights to
 //     fp16 back into tensor memory over the scores, where the second MMA reads them as its A operand.
-// The maximum is raised only when a score exceeds it by more than 2^8 (as in hc_attend.cu), so the outputs in tensor
-// memory are rarely rescaled. S_a of the next tile is issued behind P_a V of this one: a thread that sees its scores
-// knows that its outputs are complete.
+// The maximum is raised only when a score exceeds it by more than 2^8 (as in hc_attend.cu, with weights as large as fp16
+// allows: kLift), so the outputs in tensor memory are rarely rescaled. S_a of the next tile is issued behind P_a V of this
+// one: a thread that sees its scores knows that its outputs are complete.
 //
 // Row tiles that would leave SMs idle (few of them, or the last of many) have their key tiles cut into slices, one CTA
 // each, joined in their order by the CTA that finishes last.
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
         block0 += 8 * t0;
     }
 
-    float m = -INFINITY, l = 0.f;  // the row's running maximum (log2 units) and sum
+    float m = -INFINITY, l = 0.f;  // the row's running maximum less kLift (log2 units) and sum
     float f = 0.f;
     int see = 0;
     const bool softmax = warp < kSoftmaxWarps;
@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                 }
                 top = top == -INFINITY ? top : top * f;  // (f may be 0)
                 if (__any_sync(0xFFFFFFFFu, top > m + kSlack)) {
-                    const float m2 = fmaxf(m, top);
+                    const float m2 = fmaxf(m, top - kLift);
                     const float fade = m2 == -INFINITY ? 1.f : ex2(m - m2);
                     m = m2;
                     l *= fade;
@@ -905,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                                              static_cast<long long>(h * group + y - j * group) * D)[e] = w;
                 }
             }
-            if (real && slices == 1 && p.lse) p.lse[lse_at()] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            if (real && slices == 1 && p.lse) p.lse[lse_at()] = log_sum_exp(m, l);
             if (real && slices > 1) {
                 mine[D * kRows + tid] = m;
                 mine[(D + 1) * kRows + tid] = l;
@@ -954,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttArgs
                 for (int i = 0; i < 32; ++i) v[i] *= scale;
                 store32(dst + 32 * q, v);
             }
-            if (p.lse) p.lse[lse_at()] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            if (p.lse) p.lse[lse_at()] = log_sum_exp(top, sum);
         }
     }
     griddep_wait();  // the call has ended when both kernels have

@@ -11,7 +11,17 @@ namespace hc {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;  // how far (log2) a score may exceed the running maximum before it is raised
+// A weight is 2^(score - m), where m is raised to kLift below a score that exceeds it by more than kSlack: the largest is
+// 2^7 or more and none is above 2^15, inside fp16's range (65,504), so that its normal numbers, 11 bits, reach down to 2^-21 of
+// the row's largest weight and its least steps to 2^-31. With m at the maximum itself, weights below 2^-25 of the largest
+// were 0 while the sums counted them: 2^17 keys 26 doublings behind one lost all that they add to the output.
+constexpr float kLift = 7.f;
+constexpr float kUnlift = 1.f / 128.f;
+constexpr float kSlack = 15.f;
+// log of the sum of e^z of a row with the sum l of such weights
+__device__ __forceinline__ float log_sum_exp(float m, float l) {
+    return l == 0.f ? -INFINITY : (m + kLift + log2f(l * kUnlift)) * kLn2;
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float r;

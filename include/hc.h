@@ -492,9 +492,10 @@ int hc_kv_workspace_size(size_t* bytes);
  *   workspace  [device] see hc_kv_workspace_size
  * The products are taken on the tensor cores in fp16 with fp32 sums: the 4-bit keys and values are exact in
  * fp16; a query row is scaled by a power of two first, so that its bf16 values are exact too (but for those
- * below 2^-22 of the row's largest); a softmax weight is rounded to fp16's 11 bits. The result of a call does
- * not change from run to run. Keys and values that a query does not see never reach its result, NaN ones
- * included. Outputs and the workspace must not overlap each other or an input (HC_ERR_ALIAS). */
+ * below 2^-22 of the row's largest); a softmax weight is rounded to fp16's 11 bits, or to multiples of 2^-31 of the
+ * row's largest weight where it is below 2^-21 of that. The result of a call does not change from run to run. Keys
+ * and values that a query does not see never reach its result, NaN ones included. Outputs and the workspace must not
+ * overlap each other or an input (HC_ERR_ALIAS). */
 int hc_kv_attention(const void* q, int64_t q_stride, const int* q_start, const int* kv_len, const int* page_table,
                     const void* cache, hc_attention_t a, hc_kv_shape_t s, void* out, int64_t out_stride, float* lse,
                     void* workspace, hc_stream_t stream);
