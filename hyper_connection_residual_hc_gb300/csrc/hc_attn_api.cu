@@ -105,11 +105,12 @@ int hc_prepare_rope(const double* inv_freq, const int* axis, int rot, int axes, 
     for (int j = 0; j < rot / 2; ++j) {
         const int a = axis ? axis[j] : 0;
         if (a < 0 || a >= axes || !std::isfinite(inv_freq[j])) return HC_ERR_ARG;
-        double turns = inv_freq[j] / 6.283185307179586476925286766559;
+        // The magnitude's fraction of a turn and its product with 2^64 are exact in fp64 and, below 1, far from 2^64; the
+        // sign is put back in integers, where 1 - a small fraction loses nothing.
+        double turns = std::fabs(inv_freq[j]) / 6.283185307179586476925286766559;
         turns -= std::floor(turns);
-        const double scaled = turns * 18446744073709551616.0;  // 2^64
-        // a fraction that rounds up to a whole turn is no turn at all
-        t.e[j].turns = scaled >= 18446744073709551616.0 ? 0ull : static_cast<unsigned long long>(scaled);
+        const unsigned long long fixed = static_cast<unsigned long long>(std::nearbyint(turns * 0x1p64));
+        t.e[j].turns = inv_freq[j] < 0.0 ? 0ull - fixed : fixed;
         t.e[j].axis = a;
     }
     return status(launch_prepare_rope(t, rot / 2, table, reinterpret_cast<cudaStream_t>(stream)));
