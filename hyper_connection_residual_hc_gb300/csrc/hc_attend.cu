@@ -258,8 +258,10 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
     const long long total = whole_ones ? all_segments : all_units, x = whole_ones ? xs : xu;
     const long long least = whole_ones ? 1 : kTeams;  // a CTA's smallest share: one unit a team
     const long long want = (total + least - 1) / least;
+    // More segments than the call's rows can have come from starts that decrease, and so claim rows again, only: nothing is
+    // done (the units of so many might not even be counted in 64 bits).
     const long long ctas = want < grid ? want : grid;
-    if (static_cast<long long>(blockIdx.x) >= ctas) return;
+    if (static_cast<long long>(blockIdx.x) >= ctas || all_segments > p.most_segments) return;
     long long at = total * blockIdx.x / ctas;
     const long long end = total * (blockIdx.x + 1) / ctas;
     if (p.seqs <= kThreads) {
@@ -864,8 +866,10 @@ __global__ void __launch_bounds__(Plan<D, kNT, kSplit>::kThreads, Plan<D, kNT, k
 }
 
 template <int D, int kNT, int kSplit>
-int launch_rows(const AttArgs& a, cudaStream_t stream) {
+int launch_rows(const AttArgs& args, cudaStream_t stream) {
     using P = Plan<D, kNT, kSplit>;
+    AttArgs a = args;
+    a.most_segments = (a.n * a.group.by / (8 * kNT) + (a.seqs < a.n ? a.seqs : a.n)) * a.s.heads;  // each sequence may end inside a tile
     static_assert(8 * kNT * (D + 2) <= kAttPartFloats, "a partial result fits its place in the workspace");
     static std::mutex mu;
     static int ctas[kMaxDevices] = {};

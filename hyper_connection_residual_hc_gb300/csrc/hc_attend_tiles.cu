@@ -347,7 +347,10 @@ __device__ __forceinline__ Found find_tile(const AttArgs& p, int cta, const Divi
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) tiles += f.part[0][w];
     }
-    const int items = static_cast<int>(min(static_cast<long long>(tiles) * heads.by, 0x7FFFFFFFLL));
+    // More than tiles_bound come from starts that decrease, and so claim rows again, only. The grid has no CTAs for them, and a
+    // row tile that got some of its slices would leave its counter in the workspace: nothing is done.
+    const long long all = static_cast<long long>(static_cast<unsigned int>(tiles)) * heads.by;
+    const int items = all > static_cast<long long>(gridDim.x) - sms.by ? 0 : static_cast<int>(all);
     const int whole = divide(items, sms) * sms.by, left = items - whole;
     Found r = {-1, 0, 0, 0, 0, 1};
     int item = cta;

@@ -115,6 +115,7 @@ struct AttArgs {
     float* lse;
     void* workspace;
     Divider group;     // query heads that share a kv head
+    long long most_segments;  // of the rows' kernel: (sequence, kv head, tile of rows)
     int q_min, q_max;  // a kernel takes the sequences with so many queries and leaves the others to the other kernel
 };
 int launch_attention(const AttArgs& a, cudaStream_t stream);

@@ -483,7 +483,9 @@ int hc_kv_workspace_size(size_t* bytes);
  * A query that sees no key gets out = 0 and lse = -infinity.
  *   q          [device] bf16 [n, q_heads, dim], strided
  *   q_start    [device] int32 [seqs + 1], not decreasing, from 0 to at most n; rows of out and lse that no
- *              sequence has are left as they were. Entries are clamped to 0..n (bit 21 of the error word).
+ *              sequence has are left as they were. Entries are clamped to 0..n (bit 21 of the error word). An entry below
+ *              the one before it leaves that sequence without queries (bit 21 too); rows that several sequences claim
+ *              then get the result of one of them, or the call leaves all rows as they were.
  *   kv_len     [device] int32 [seqs]; clamped to 0..max_pages * page_size (bit 21)
  *   page_table [device] int32 [seqs, max_pages]; only the entries of pages with keys that some query of a tile
  *              sees are read. The keys of a page that is out of range are left out (bit 20).
