@@ -143,17 +143,20 @@ def _ptr(x):
     return x.data_ptr()
 
 
-_torch = None
+_torch = _raw_stream = _current_device = None
 
 
 def _stream(s):
     if s is None:
-        global _torch
+        global _torch, _raw_stream, _current_device
         if _torch is None:
             import torch
             _torch = torch
-        if _torch.cuda.is_initialized():  # the raw handle: a Stream object costs more than the rest of a call
-            return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            _current_device = getattr(torch._C, "_cuda_getDevice", None)
+        # the raw handle, where torch offers it: a Stream object costs more than the rest of a call
+        if _raw_stream and _current_device and _torch.cuda.is_initialized():
+            return _raw_stream(_current_device())
         return _torch.cuda.current_stream().cuda_stream if _torch.cuda.is_available() else None
     if isinstance(s, int):
         return s
