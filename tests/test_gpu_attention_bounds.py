@@ -22,6 +22,46 @@ def _lib():
     gu.device_error_clear()
 
 
+@pytest.mark.parametrize("lens", [[(1, 160), (3, 96)], [(120, 160), (140, 320)]], ids=["few", "many"])
+@pytest.mark.parametrize("causal", [True, False])
+def test_clamped_bounds_give_the_results_of_the_clamped_call(lens, causal):
+    """Lengths past the table, rows past n, a start below 0: told of, and the results are those of the bounds as clamped."""
+    def problem():
+        return Problem(lens, 5, 1, 128, 32, seed=19).to_device()
+
+    def check(p, page=False):
+        out, lse = p.run(causal=causal)
+        word = hc.hc_device_error(clear=True)
+        assert word == (3 << 20 if page else 1 << 21)
+        p.check(out, lse, causal=causal)
+        m = int(p.q_start[-1])
+        assert (out[m:] == 7).all() and (lse[m:] == 7).all()
+
+    p = problem()  # keys past the table: as many as it has; the entry of its last page is -1
+    p.d["kv_len"] = ints([10 ** 9, lens[1][1]], torch.int32)
+    p.kv_len[0] = p.max_pages * 32
+    check(p, page=True)
+    p = problem()
+    p.d["kv_len"] = ints([lens[0][1], -(2 ** 31)], torch.int32)
+    p.kv_len[1] = 0
+    check(p)
+    p = problem()  # five rows more than there are
+    p.d["q_start"] = ints([0, lens[0][0], p.n + 5], torch.int32)
+    check(p)
+    p = problem()  # two rows of q are not the call's: the last sequence is shorter, its queries still the last of its keys
+    p.n -= 2
+    p.q_start[2] -= 2
+    check(p)
+    p = problem()
+    p.d["q_start"] = ints([-2, lens[0][0], p.n], torch.int32)
+    check(p)
+    p = problem()  # starts past n: no rows
+    p.d["q_start"] = ints([0, lens[0][0], 2 ** 31 - 1], torch.int32)
+    p.n = lens[0][0]
+    p.q_start[2] = lens[0][0]
+    check(p)
+
+
 @pytest.mark.parametrize("pairs,kv", [(50, 3200), (45, 6000)])
 def test_decreasing_starts_leave_the_workspace_as_it_was(pairs, kv):
     """Starts that go back claim the same rows again and again, more row tiles than the call can have: told of, and calls
