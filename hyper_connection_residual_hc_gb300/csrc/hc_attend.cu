@@ -38,6 +38,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 
@@ -50,6 +51,7 @@ namespace hc {
 namespace {
 
 __device__ unsigned int g_hc_attention_error = 0;
+std::atomic<bool> g_launched{false};  // whether the word above can be set at all (reading it costs a copy and a wait)
 
 constexpr uint64_t kWaitNs = 1000000000ull;   // 1 s
 constexpr int kUnit = 32;                     // tokens a warp takes at a time: two cache blocks
@@ -887,6 +889,7 @@ int launch_rows(const AttArgs& args, cudaStream_t stream) {
             ctas[dev] = sms * per_sm < kAttMaxCtas ? sms * per_sm : kAttMaxCtas;
         }
     }
+    g_launched.store(true, std::memory_order_relaxed);
     attend_rows_kernel<D, kNT, kSplit><<<static_cast<unsigned>(ctas[dev]), P::kThreads, P::kSmem, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? 0 : -7;
 }
@@ -937,6 +940,8 @@ int launch_attention(const AttArgs& args, cudaStream_t stream) {
 int read_attention_error(unsigned int* word, int clear, cudaStream_t stream) {
     unsigned int v = 0, tiles = 0;
     if (read_tiles_error(&tiles, clear, stream) != 0) return -7;
+    *word = tiles;
+    if (!g_launched.load(std::memory_order_relaxed)) return 0;
     if (cudaMemcpyFromSymbolAsync(&v, g_hc_attention_error, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess)
         return -7;
     if (cudaStreamSynchronize(stream) != cudaSuccess) return -7;

@@ -35,6 +35,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 
@@ -47,6 +48,7 @@ namespace hc {
 namespace {
 
 __device__ unsigned int g_hc_tiles_error = 0;
+std::atomic<bool> g_launched{false};  // whether the word above can be set at all (reading it costs a copy and a wait)
 
 constexpr int kRowTile = 128;   // rows of an MMA
 constexpr int kRows = 2 * kRowTile;
@@ -1006,6 +1008,7 @@ int launch_tiles(const AttArgs& a, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = a.q_min > 0 ? 1 : 0;
+    g_launched.store(true, std::memory_order_relaxed);
     return cudaLaunchKernelEx(&cfg, attend_tiles_kernel<D>, a, make_divider(sms), make_divider(a.s.heads)) == cudaSuccess ? 0 : -7;
 }
 
@@ -1019,6 +1022,8 @@ int launch_attention_tiles(const AttArgs& a, cudaStream_t stream) {
 
 int read_tiles_error(unsigned int* word, int clear, cudaStream_t stream) {
     unsigned int v = 0;
+    *word = 0;
+    if (!g_launched.load(std::memory_order_relaxed)) return 0;
     if (cudaMemcpyFromSymbolAsync(&v, g_hc_tiles_error, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess) return -7;
     if (cudaStreamSynchronize(stream) != cudaSuccess) return -7;
     if (clear && v != 0) {

@@ -28,6 +28,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "hc_attn.h"
@@ -38,6 +39,7 @@ namespace hc {
 namespace {
 
 __device__ unsigned int g_hc_kv_error = 0;
+std::atomic<bool> g_launched{false};  // whether the word above can be set at all (reading it costs a copy and a wait)
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -428,6 +430,7 @@ int launch_move(const KvArgs& a, cudaStream_t stream) {
     const long long most = kGroup * a.s.dim / 256;
     if (parts > most) parts = most;
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(parts));
+    g_launched.store(true, std::memory_order_relaxed);
     switch (a.s.dim) {
         case 64: kv_move_kernel<64, kRead><<<grid, kThreads, 0, stream>>>(a); break;
         case 128: kv_move_kernel<128, kRead><<<grid, kThreads, 0, stream>>>(a); break;
@@ -443,6 +446,8 @@ int launch_kv_read(const KvArgs& a, cudaStream_t stream) { return launch_move<tr
 
 int read_kv_error(unsigned int* word, int clear, cudaStream_t stream) {
     unsigned int v = 0;
+    *word = 0;
+    if (!g_launched.load(std::memory_order_relaxed)) return 0;
     if (cudaMemcpyFromSymbolAsync(&v, g_hc_kv_error, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess) return -7;
     if (cudaStreamSynchronize(stream) != cudaSuccess) return -7;
     if (clear && v != 0) {
