@@ -8,10 +8,13 @@
 // the bytes that the cache has; this kernel's bound is the dequantisation and HBM, not the products.
 //
 // Measured: 256 sequences of 2,050 to 4,096 keys, 40 query and 8 kv heads of 128 (912 MB): 202 us, 4.5 TB/s, 67% of the
-// measured copy rate; 3 sequences of up to 131,072 keys: 84 us, 67%; 8 of up to 509 keys: 8.2 us. With few rows what is
-// left is instructions: about 600 for a unit of 32 keys of a head (128 conversions from 4 bits, about as many products with
-// scales, 32 MMAs), issue slots about 60% busy, no pipe above half. Leaving out the keys' scale products would save 7 us;
-// two warps a unit (258 us) or blocks of 4 warps (255 us) lose. More rows cost more of everything: five queries of 4
+// measured copy rate; 3 sequences of up to 131,072 keys: 84 us, 67%; 8 of up to 509 keys: 8.1 us. With few rows nothing is
+// full: a unit of 32 keys of a head takes about 600 instructions (128 conversions from 4 bits, about as many products with
+// scales, 32 MMAs) in a chain of scores, maximum, weights and values whose fixed latencies 16 warps an SM cover in part:
+// issue slots about 60% busy, no pipe above half. In an earlier form that took 215 us, leaving out the keys' scale products
+// saved 7 us; two warps a unit took 258 us, blocks of 4 warps 255 us. Heads of 256 come here for prefills too, 16 rows a
+// tile, which dequantises the keys for each of them: 2 x 2,048 queries behind 4,096 to 6,144 keys, 40 and 8 heads, 4,850 us,
+// nine times their products at the measured cuBLAS rate. More rows cost more of everything: five queries of 4
 // heads each, 64 sequences, window of 1,024 keys (81 MB): 54 us.
 //
 // A cache block (16 tokens, one head) is laid out in A-fragment order: lane (r, c) = (lane / 4, lane % 4) finds

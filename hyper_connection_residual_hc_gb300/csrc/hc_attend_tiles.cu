@@ -24,9 +24,10 @@
 // dequantising alone 278, the softmax alone with its barriers 444 and its barriers alone 283: the round trip scores -> weights ->
 // scores is what bounds it, with two row tiles to overlap and no tensor memory left for a second set of scores. About 14 us a
 // CTA are its start and end; they were 27 before the queries were loaded and the outputs written by whole rows, beside
-// the first keys, and before divisions became products. Tried and slower: 16 softmax warps with half a row each
-// (604 us), an MMA warp that polls for whichever row tile is ready (704 us: its polling takes issue slots), 8
-// dequantising warps (630 us), an eighth of the exponentials by a polynomial instead of the special function unit (4% more).
+// the first keys, and before divisions became products. Tried and slower, against 560 to 577 us then: 16 softmax warps with
+// half a row each (604 us), an MMA warp that polls for whichever row tile is ready (704 us: its polling takes issue slots), 8
+// dequantising warps (630 us); against 428 us: an eighth of the exponentials by a polynomial instead of the special
+// function unit (444 us). Heads of 64, 64 query and 8 kv heads, the same lengths: 568 us, 725 TFLOP/s.
 //
 // Every wait is bounded: on expiry the kernel sets a bit of the device error word, stops waiting, lets its MMAs end
 // and frees its tensor memory.

@@ -344,8 +344,8 @@ int hc_debug_wait_flag(const unsigned long long* flags, int count, unsigned long
  * for the same serving loop, under the conventions at the top of this file, except that
  *   - q, k, v and the outputs may be strided: an array [n, heads, dim] whose token t starts `stride`
  *     elements after token t - 1 (a slice of a fused projection's output, say). A stride is a
- *     multiple of 8 elements and at least heads * dim (HC_ERR_SHAPE otherwise); heads and dim are
- *     contiguous within a token. The 16-byte rule holds for q, k, v, out and the cache; positions,
+ *     multiple of 8 elements, at least heads * dim and at most 2^40 (HC_ERR_SHAPE otherwise, as for more
+ *     than 2^31 - 1 tokens); heads and dim are contiguous within a token. The 16-byte rule holds for q, k, v, out and the cache; positions,
  *     slots, tables, lengths and lse need their own type's alignment only;
  *   - indices that a call reads on the device (slots, page tables, lengths) cannot be checked on the
  *     host. One that is out of range is not followed: the call leaves out what it points to, as each
@@ -368,8 +368,8 @@ typedef struct {
 
 /* Head layout and norm of hc_qk_norm_rope. */
 typedef struct {
-    int q_heads;       /* >= 1 */
-    int k_heads;       /* >= 0; 0: queries only (k, k_w, k_out unused) */
+    int q_heads;       /* 1..65536 */
+    int k_heads;       /* 0..65536; 0: queries only (k, k_w, k_out unused) */
     int dim;           /* width of a head: a multiple of 8, at most 256 */
     int gain_per_head; /* 0: the gains are [dim], the same for every head; 1: q_w [q_heads, dim], k_w [k_heads, dim] */
     float norm_eps;    /* >= 0, finite */
@@ -460,7 +460,9 @@ typedef struct {
     int64_t n;      /* rows of q and out: the queries of all sequences; n * q_heads / heads at most 2^31 - 1 */
     int seqs;       /* sequences, 0..2^24 */
     int max_q_len;  /* queries of the longest sequence: chooses kernels and tiles (any value is right, others slower).
-                     * Single tokens and long chunks may share a call: each kind goes to a kernel of its own */
+                     * Single tokens and long chunks may share a call. Each kind goes to a kernel of its own with
+                     * heads of 64 or 128 and up to 32 query heads a kv head; with more, all of them go to the kernel
+                     * for many rows, and heads of 256 to the one for few, 16 rows at a time */
     int max_pages;  /* columns of the page table, >= 1; max_pages * page_size at most 2^30 */
     int q_heads;    /* a multiple of the cache's heads, up to 128 times as many: head h reads kv head h * heads / q_heads */
     int causal;     /* 1: a query sees the keys up to its own position; 0: all keys of its sequence */
@@ -507,7 +509,7 @@ int hc_kv_attention(const void* q, int64_t q_stride, const int* q_start, const i
  * kernel's waits, bits 16-19 those of the generic path's projection, bits 22-23 those of
  * hc_kv_attention. Bits 20 and 21 tell of an index out of range that a call left out (hc_kv_write,
  * hc_kv_read, hc_kv_attention): its other results are valid. Synchronises `stream`.
- * If `clear` is nonzero the word is reset to 0, and, when it was nonzero, the library's own fixed
+ * If `clear` is nonzero the word is reset to 0, and, when one of bits 0-15 was set, the library's own fixed
  * scratch of hc_post_then_pre_noalloc on this device is zeroed as well (on `stream`; no call using it
  * may still be running). Returns HC_OK, HC_ERR_NULL or HC_ERR_CUDA. */
 int hc_device_error(unsigned int* word, int clear, hc_stream_t stream);
