@@ -21,8 +21,9 @@
 // Bound: HBM, (4 + 1.125) bytes for a column of a key and a value; at these rates the instructions that decide and
 // place the codes come close behind (the ALU pipe is 64% busy while writing). 16,384 tokens of 8 heads of 128, 86 MB:
 // written in 22.2 us (3.9 TB/s, 57% of the measured copy rate), read back in 21.8 us (4.0 TB/s), 41.8 us one after the
-// other (the read finds part of the cache in L2); 256 single tokens on as many pages in 3.8 and 3.1 us. Keys and values by separate warps balance the few waves of such a call (reading 28.9 to
-// 21.5 us); runs found by ballot in independent warps instead of by a loop in shared memory: 69 to 49 us for both.
+// other (the read finds part of the cache in L2); 256 single tokens on as many pages in 3.8 and 3.1 us. Keys and values by
+// separate warps balance the few waves of such a call (reading 28.9 to 21.5 us); runs found by ballot in independent warps
+// instead of by a loop in shared memory: 69 to 49 us for both.
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -345,8 +345,9 @@ int hc_debug_wait_flag(const unsigned long long* flags, int count, unsigned long
  *   - q, k, v and the outputs may be strided: an array [n, heads, dim] whose token t starts `stride`
  *     elements after token t - 1 (a slice of a fused projection's output, say). A stride is a
  *     multiple of 8 elements, at least heads * dim and at most 2^40 (HC_ERR_SHAPE otherwise, as for more
- *     than 2^31 - 1 tokens); heads and dim are contiguous within a token. The 16-byte rule holds for q, k, v, out and the cache; positions,
- *     slots, tables, lengths and lse need their own type's alignment only;
+ *     than 2^31 - 1 tokens); heads and dim are contiguous within a token. The 16-byte rule holds for
+ *     q, k, v, out and the cache; positions, slots, tables, lengths and lse need their own type's
+ *     alignment only;
  *   - indices that a call reads on the device (slots, page tables, lengths) cannot be checked on the
  *     host. One that is out of range is not followed: the call leaves out what it points to, as each
  *     call says, and sets a bit of the device error word (hc_device_error, bits 20-23). */
