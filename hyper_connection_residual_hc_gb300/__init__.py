@@ -37,11 +37,21 @@ SYMBOLS = (
     "hc_host_post_then_pre",
     "hc_rope_table_size", "hc_prepare_rope", "hc_qk_norm_rope", "hc_kv_cache_size", "hc_kv_write", "hc_kv_read",
     "hc_kv_workspace_size", "hc_kv_attention",
+    "hc_norm_quant8", "hc_mul8", "hc_gated_mul8", "hc_token_logprobs",
 )
 
 # styles of hc_rope_t
 HC_ROPE_HALF = 0
 HC_ROPE_PAIRS = 1
+
+# types of outputs and logits
+HC_BF16 = 0
+HC_F32 = 1
+HC_E4M3 = 2
+
+# activations of hc_gated_mul8
+HC_ACT_SILU = 0
+HC_ACT_GELU = 1
 
 
 class HCError(RuntimeError):
@@ -79,6 +89,23 @@ class hc_attention_t(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int64), ("seqs", ctypes.c_int), ("max_q_len", ctypes.c_int),
                 ("max_pages", ctypes.c_int), ("q_heads", ctypes.c_int), ("causal", ctypes.c_int),
                 ("window", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class hc_quant8_t(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("d", ctypes.c_int), ("norm", ctypes.c_int), ("norm_eps", ctypes.c_float)]
+
+
+class hc_mul8_t(ctypes.Structure):
+    _fields_ = [("features", ctypes.c_int), ("k", ctypes.c_int), ("out_type", ctypes.c_int)]
+
+
+class hc_gated8_t(ctypes.Structure):
+    _fields_ = [("features", ctypes.c_int), ("k", ctypes.c_int), ("act", ctypes.c_int), ("out_type", ctypes.c_int)]
+
+
+class hc_logprobs_t(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("vocab", ctypes.c_int), ("top", ctypes.c_int), ("type", ctypes.c_int),
+                ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -127,6 +154,10 @@ def load(path: str = LIB_PATH):
     lib.hc_kv_workspace_size.argtypes = [PSZ]
     lib.hc_kv_attention.argtypes = [P, I64, P, P, P, P, hc_attention_t, hc_kv_shape_t, P, I64, P, P, P]
     lib.hc_status_string.restype = ctypes.c_char_p
+    lib.hc_norm_quant8.argtypes = [P, I64, P, I64, P, hc_quant8_t, P, I64, P, I64, P, P]
+    lib.hc_mul8.argtypes = [P, I64, P, P, I64, P, I64, hc_mul8_t, P, I64, P]
+    lib.hc_gated_mul8.argtypes = [P, I64, P, P, P, P, P, I64, I64, hc_gated8_t, P, I64, P, P]
+    lib.hc_token_logprobs.argtypes = [P, I64, P, hc_logprobs_t, P, P, P, P, P]
     for name in SYMBOLS:
         if name != "hc_status_string":
             getattr(lib, name).restype = I
@@ -434,3 +465,52 @@ def hc_kv_attention(q, q_stride: int, q_start, kv_len, page_table, cache, a: hc_
     _check("hc_kv_attention", load().hc_kv_attention(
         _ptr(q), q_stride, _ptr(q_start), _ptr(kv_len), _ptr(page_table), _ptr(cache), a, s, _ptr(out), out_stride,
         _ptr(lse), _ptr(workspace), _stream(stream)))
+
+
+# ---- the feed-forward sublayer and the head in 8 bits -----------------------------------------------
+
+
+def quant8(n: int, d: int, norm: bool = True, norm_eps: float = 1e-6) -> hc_quant8_t:
+    return hc_quant8_t(n, d, 1 if norm else 0, norm_eps)
+
+
+def mul8(features: int, k: int, out_type: int = HC_BF16) -> hc_mul8_t:
+    return hc_mul8_t(features, k, out_type)
+
+
+def gated8(features: int, k: int, act: int = HC_ACT_SILU, out_type: int = HC_E4M3) -> hc_gated8_t:
+    return hc_gated8_t(features, k, act, out_type)
+
+
+def logprobs(n: int, vocab: int, top: int = 0, scale: float = 1.0, type: int = HC_F32) -> hc_logprobs_t:
+    return hc_logprobs_t(n, vocab, top, type, scale)
+
+
+def hc_norm_quant8(x, x_stride: int, residual, residual_stride: int, norm_w, q: hc_quant8_t, sum_out, sum_stride: int, codes,
+                   codes_stride: int, scales, stream=None) -> None:
+    """residual, norm_w and sum_out may be None (their strides are then unused)."""
+    _check("hc_norm_quant8", load().hc_norm_quant8(
+        _ptr(x), x_stride, _ptr(residual), residual_stride, _ptr(norm_w), q, _ptr(sum_out), sum_stride, _ptr(codes),
+        codes_stride, _ptr(scales), _stream(stream)))
+
+
+def hc_mul8(x, x_stride: int, x_scales, w, w_stride: int, w_scales, n: int, s: hc_mul8_t, out, out_stride: int,
+            stream=None) -> None:
+    _check("hc_mul8", load().hc_mul8(_ptr(x), x_stride, _ptr(x_scales), _ptr(w), w_stride, _ptr(w_scales), n, s, _ptr(out),
+                                     out_stride, _stream(stream)))
+
+
+def hc_gated_mul8(x, x_stride: int, x_scales, w_gate, gate_scales, w_up, up_scales, w_stride: int, n: int, s: hc_gated8_t,
+                  out, out_stride: int, out_scales, stream=None) -> None:
+    """out_scales is None with HC_BF16."""
+    _check("hc_gated_mul8", load().hc_gated_mul8(
+        _ptr(x), x_stride, _ptr(x_scales), _ptr(w_gate), _ptr(gate_scales), _ptr(w_up), _ptr(up_scales), w_stride, n, s,
+        _ptr(out), out_stride, _ptr(out_scales), _stream(stream)))
+
+
+def hc_token_logprobs(logits, stride: int, tokens, s: hc_logprobs_t, logprob, entropy, top_logprob, top_token,
+                      stream=None) -> None:
+    """tokens and logprob, entropy, and (without alternatives) top_logprob and top_token may be None."""
+    _check("hc_token_logprobs", load().hc_token_logprobs(
+        _ptr(logits), stride, _ptr(tokens), s, _ptr(logprob), _ptr(entropy), _ptr(top_logprob), _ptr(top_token),
+        _stream(stream)))

@@ -1,0 +1,17 @@
+// Host helpers that the launchers of the 8-bit products share.
+#pragma once
+
+#include <atomic>
+#include <cuda.h>
+
+namespace hc {
+
+constexpr int kMul8Devices = 64;
+
+// A tensor map of 8-bit rows (`cols` bytes, `stride` bytes apart) whose box is 128 columns by box_rows, 128-byte swizzle, zeros outside.
+bool mul8_map(CUtensorMap* m, const void* base, long long cols, long long rows, long long stride, int box_rows);
+
+// Lets a kernel use `bytes` of shared memory, once per device; `ready` has kMul8Devices entries.
+bool mul8_allow_smem(const void* kernel, int bytes, std::atomic<bool>* ready);
+
+}  // namespace hc

@@ -1,0 +1,155 @@
+// Residual addition, RMSNorm and quantisation of rows to 8 bits with a scale for each 128 columns, in one pass over the row.
+// Formulas and format: include/hc.h.
+//
+// A row stays in the registers of the threads that load it, 8 columns (16 bytes) at a time: 16 neighbouring lanes hold the 128
+// columns of a block, so that a block's largest magnitude takes four exchanges within half a warp. The norm needs one sum
+// over the whole row before that; without it the blocks are independent.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "hc_ffn.h"
+#include "hc_mul8_dev.cuh"
+
+namespace hc {
+namespace {
+
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(u[i] << 16);
+        f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// row_threads: threads that share a row (a multiple of 32); kVecs: 16-byte vectors of it that each holds, so that all of the row
+// is in registers.
+template <int kVecs, bool kResidual>
+__global__ void __launch_bounds__(kVecs < 4 ? 128 : 1024) quant8_kernel(const Quant8Args p, int row_threads) {
+    __shared__ float part[32];
+    const int t = threadIdx.x % row_threads, lane = threadIdx.x % 32;
+    const long long row = static_cast<long long>(blockIdx.x) * (blockDim.x / row_threads) + threadIdx.x / row_threads;
+    if (row >= p.n) return;  // (whole warps; a block of several rows has no barrier)
+    const int vecs = p.d / 8;
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + row * p.x_stride);
+    uint4 v[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const int c = t + i * row_threads;
+        v[i] = c < vecs ? x[c] : make_uint4(0, 0, 0, 0);
+    }
+    float f[8];
+    float ss = 0.f;
+    if constexpr (kResidual) {
+        const uint4* r = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + row * p.residual_stride);
+        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.sum_out) + row * p.sum_stride);
+        uint4 w[kVecs];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const int c = t + i * row_threads;
+            w[i] = c < vecs ? r[c] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            float g[8];
+            unpack(v[i], f);
+            unpack(w[i], g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] += g[j];
+            v[i] = pack(f);
+            const int c = t + i * row_threads;
+            if (p.sum_out && c < vecs) o[c] = v[i];
+        }
+    }
+    float inv = 1.f;
+    if (p.norm) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            unpack(v[i], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+        }
+#pragma unroll
+        for (int m = 16; m; m /= 2) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, m);
+        if (row_threads > 32) {
+            if (lane == 0) part[threadIdx.x / 32] = ss;
+            __syncthreads();
+            ss = lane < row_threads / 32 ? part[lane] : 0.f;
+#pragma unroll
+            for (int m = 16; m; m /= 2) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, m);
+        }
+        inv = rsqrtf(ss / static_cast<float>(p.d) + p.eps);
+    }
+    unsigned char* codes = p.codes + row * p.codes_stride;
+    float* scales = p.scales + row * blocks8(p.d);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+        const int c = t + i * row_threads;
+        unpack(v[i], f);
+        if (p.norm) {
+            float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = a;
+            if (p.w && c < vecs) {
+                a = reinterpret_cast<const float4*>(p.w)[2 * c];
+                b = reinterpret_cast<const float4*>(p.w)[2 * c + 1];
+            }
+            f[0] *= inv * a.x; f[1] *= inv * a.y; f[2] *= inv * a.z; f[3] *= inv * a.w;
+            f[4] *= inv * b.x; f[5] *= inv * b.y; f[6] *= inv * b.z; f[7] *= inv * b.w;
+        }
+        float top = fabsf(f[0]);
+#pragma unroll
+        for (int j = 1; j < 8; ++j) top = max_nan(top, fabsf(f[j]));
+#pragma unroll
+        for (int m = 8; m; m /= 2) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+        top = max_nan(top, kLeastTop8);
+        if (c < vecs) {
+            const float up = kTop8 / top;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] *= up;
+            *reinterpret_cast<uint2*>(codes + 8 * static_cast<long long>(c)) =
+                make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+            if (lane % 16 == 0) scales[c / 16] = top / kTop8;
+        }
+    }
+}
+
+template <int kVecs>
+void start(const Quant8Args& a, int row_threads, int rows, cudaStream_t stream) {
+    const unsigned blocks = static_cast<unsigned>((a.n + rows - 1) / rows), threads = static_cast<unsigned>(row_threads * rows);
+    if (a.residual)
+        quant8_kernel<kVecs, true><<<blocks, threads, 0, stream>>>(a, row_threads);
+    else
+        quant8_kernel<kVecs, false><<<blocks, threads, 0, stream>>>(a, row_threads);
+}
+
+}  // namespace
+
+int launch_norm_quant8(const Quant8Args& a, cudaStream_t stream) {
+    const int vecs = a.d / 8;
+    if (vecs <= 32) {
+        start<1>(a, 32, 4, stream);
+    } else if (vecs <= 64) {
+        start<2>(a, 32, 4, stream);
+    } else if (vecs <= 1024 * 4) {
+        const int threads = (vecs + 4 * 32 - 1) / (4 * 32) * 32;
+        start<4>(a, threads, 1, stream);
+    } else {
+        const int threads = (vecs + 8 * 32 - 1) / (8 * 32) * 32;
+        start<8>(a, threads, 1, stream);
+    }
+    return cudaGetLastError() == cudaSuccess ? 0 : -7;
+}
+
+}  // namespace hc

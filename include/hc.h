@@ -505,11 +505,117 @@ int hc_kv_attention(const void* q, int64_t q_stride, const int* q_start, const i
                     const void* cache, hc_attention_t a, hc_kv_shape_t s, void* out, int64_t out_stride, float* lse,
                     void* workspace, hc_stream_t stream);
 
+/* ---- The feed-forward sublayer and the head in 8 bits ----------------------------------------------
+ * What turns the y_normed of the calls above into the next Delta when a sublayer's weights are held in 8 bits, and the z of
+ * hc_final into what a model answers: rows quantised to 8 bits (hc_norm_quant8), the gate and up projections with their
+ * activation and product (hc_gated_mul8), a plain projection (hc_mul8: the way back to d, the attention's projections, the
+ * vocabulary's logits), and log probabilities of tokens with the most likely alternatives (hc_token_logprobs). No
+ * counterpart on the pages (their linear layers are not shown): this library's own operators for the same serving loop, under
+ * the conventions at the top of this file. Inference only: none has a backward pass.
+ *
+ * Format. Codes are e4m3 (1 sign, 4 exponent, 3 mantissa bits, no infinity, largest 448), one byte a value. Of a row of k values, each
+ * 128 next to each other share an fp32 scale: scales [n, ceil(k/128)], contiguous. Weights are [features, k] codes (a
+ * torch Linear's layout), and each 128 x 128 block shares a scale: [ceil(features/128), ceil(k/128)] fp32, contiguous. A
+ * value is code * scale; blocks at the end may be short. Any scales will do: their products are taken in fp32.
+ *
+ * Rows may be strided (the stride in elements): multiples of 8 for bf16 and fp32, of 16 for codes, at least the row's width and at
+ * most 2^38 (HC_ERR_SHAPE otherwise, as for more than 2^31 - 1 rows). The 16-byte rule holds for all rows and for norm_w; scales,
+ * tokens, log probabilities and alternatives need their own type's alignment only. Outputs must not overlap each other or an
+ * input unless a call says so (HC_ERR_ALIAS); rows of one stride that lie side by side do not overlap. What lies between
+ * the rows is neither read nor written. */
+
+enum {
+    HC_BF16 = 0, /* types of outputs and logits */
+    HC_F32 = 1,
+    HC_E4M3 = 2 /* codes and scales, as above */
+};
+enum {
+    HC_ACT_SILU = 0, /* g / (1 + e^-g) */
+    HC_ACT_GELU = 1  /* g / 2 * (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+};
+
+/* A call of hc_norm_quant8. */
+typedef struct {
+    int64_t n;      /* rows */
+    int d;          /* values of a row: a multiple of 16, 16..65536 */
+    int norm;       /* 0: no norm (norm_w and norm_eps unused) */
+    float norm_eps; /* >= 0, finite */
+} hc_quant8_t;
+
+/* Add the residual, take the RMSNorm and quantise, in one pass, for each row:
+ *   s = x, or bf16(x + residual), which sum_out gets
+ *   y = s, or norm_w * s / sqrt(mean(s^2) + norm_eps)           (fp32, not rounded before it is quantised)
+ *   top = max(largest |y| of 128 columns, 2^-64);  scale = top / 448;  code = e4m3(y * (448 / top)), to nearest even
+ *   x, residual [device] bf16 [n, d], strided; residual may be NULL
+ *   norm_w      [device] fp32 [d]; NULL: 1
+ *   sum_out     [device] bf16 [n, d], strided, or NULL; needs a residual; may be exactly x or exactly residual (with its stride)
+ *   codes       [device] e4m3 [n, d], strided;  scales [device] fp32 [n, ceil(d/128)]
+ * A block of 128 whose y holds a NaN or an infinity reads as NaN. With the norm a NaN in s reaches its whole row; an infinity makes
+ * its own block NaN and the row's other blocks 0. */
+int hc_norm_quant8(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, const float* norm_w, hc_quant8_t q,
+                   void* sum_out, int64_t sum_stride, void* codes, int64_t codes_stride, float* scales, hc_stream_t stream);
+
+/* Shape of hc_mul8. */
+typedef struct {
+    int features; /* rows of w, columns of out: 1..2^24 */
+    int k;        /* a multiple of 16, 16..2^20 */
+    int out_type; /* HC_BF16 or HC_F32 */
+} hc_mul8_t;
+
+/* out[t, f] = sum over blocks b of k  x_scales[t, b] * w_scales[f/128, b] * sum over i in b of  x[t, i] * w[f, i]
+ *   x   [device] codes [n, k], strided, with x_scales [n, ceil(k/128)]
+ *   w   [device] codes [features, k], strided, with w_scales [ceil(features/128), ceil(k/128)]
+ *   out [device] bf16 or fp32 [n, features], strided
+ * The products are taken on the tensor cores (exact, fp32 sums of 128 of them), the blocks' sums added up in fp32, one rounding
+ * for bf16. The result of a call does not change from run to run; that of a token may depend, in fp32's last bits, on
+ * how many tokens the call has. No workspace: calls may run at the same time on any streams. */
+int hc_mul8(const void* x, int64_t x_stride, const float* x_scales, const void* w, int64_t w_stride, const float* w_scales, int64_t n,
+            hc_mul8_t s, void* out, int64_t out_stride, hc_stream_t stream);
+
+/* Shape of hc_gated_mul8. */
+typedef struct {
+    int features; /* rows of w_gate and of w_up, columns of out: a multiple of 16, 16..2^24 */
+    int k;        /* a multiple of 16, 16..2^20 */
+    int act;      /* HC_ACT_SILU or HC_ACT_GELU */
+    int out_type; /* HC_BF16 or HC_E4M3 */
+} hc_gated8_t;
+
+/* out = act(x . w_gate) * (x . w_up), both products as hc_mul8 takes them, in one kernel: the projections stay in fp32 and the result
+ * is rounded once, to bf16, or to codes and scales as hc_norm_quant8 makes them (of 128 features each: the x of the hc_mul8
+ * that leads back). out_scales [device] fp32 [n, ceil(features/128)], unused with HC_BF16. w_gate and w_up have one stride
+ * (two halves of a joint matrix [2 features, k], or columns of one buffer). */
+int hc_gated_mul8(const void* x, int64_t x_stride, const float* x_scales, const void* w_gate, const float* gate_scales, const void* w_up,
+                  const float* up_scales, int64_t w_stride, int64_t n, hc_gated8_t s, void* out, int64_t out_stride, float* out_scales,
+                  hc_stream_t stream);
+
+/* A call of hc_token_logprobs. */
+typedef struct {
+    int64_t n;   /* rows of logits */
+    int vocab;   /* 1..2^30 */
+    int top;     /* alternatives: 0..32 and at most vocab (above 32: HC_ERR_UNSUPPORTED) */
+    int type;    /* of the logits: HC_BF16 or HC_F32 */
+    float scale; /* of the logits before the softmax (1 / temperature): finite, > 0 */
+} hc_logprobs_t;
+
+/* For each row, with z = scale * logits and lse = log sum over the vocabulary of e^z:
+ *   logprob[t] = z[tokens[t]] - lse;  entropy[t] = lse - sum of p z, p = e^(z - lse);  the `top` largest logits in order
+ *   logits      [device] bf16 or fp32 [n, vocab], strided
+ *   tokens      [device] int64 [n]; a negative token (padding) gets the log probability 0, one past the vocabulary too, with bit 24 of
+ *               the error word
+ *   logprob, entropy [device] fp32 [n]; either may be NULL (tokens too, without logprob)
+ *   top_logprob [device] fp32 [n, top], top_token [device] int32 [n, top]: of equal logits the lower token comes first, NaN last;
+ *               NULL with top = 0
+ * fp32 sums below the row's maximum. Minus infinity (a token ruled out) has probability 0, as has the type's lowest value beside
+ * ordinary logits; a row of minus infinities has the entropy 0 and every log probability minus infinity. A NaN or plus infinity
+ * makes its row's log probabilities and entropy NaN. */
+int hc_token_logprobs(const void* logits, int64_t stride, const int64_t* tokens, hc_logprobs_t s, float* logprob, float* entropy,
+                      float* top_logprob, int* top_token, hc_stream_t stream);
+
 /* Read the device-side error word of the current device: nonzero when a kernel gave up a
  * bounded wait (it then returned early and its outputs are not valid); bits 0-15 are the fused
  * kernel's waits, bits 16-19 those of the generic path's projection, bits 22-23 those of
- * hc_kv_attention. Bits 20 and 21 tell of an index out of range that a call left out (hc_kv_write,
- * hc_kv_read, hc_kv_attention): its other results are valid. Synchronises `stream`.
+ * hc_kv_attention, bit 25 those of hc_mul8 and hc_gated_mul8. Bits 20, 21 and 24 tell of an index out of range that a call left out
+ * (hc_kv_write, hc_kv_read, hc_kv_attention; hc_token_logprobs): its other results are valid. Synchronises `stream`.
  * If `clear` is nonzero the word is reset to 0, and, when one of bits 0-15 was set, the library's own fixed
  * scratch of hc_post_then_pre_noalloc on this device is zeroed as well (on `stream`; no call using it
  * may still be running). Returns HC_OK, HC_ERR_NULL or HC_ERR_CUDA. */
