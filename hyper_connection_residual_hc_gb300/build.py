@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libhc.so")
 SOURCES = ["hc_fused.cu", "hc_api.cu", "hc_final.cu", "hc_generic.cu", "hc_proj.cu", "hc_host.cu",
            "hc_rope.cu", "hc_kv.cu", "hc_attend.cu", "hc_attend_tiles.cu", "hc_attn_api.cu",
-           "hc_quant8.cu", "hc_mul8.cu", "hc_logprobs.cu", "hc_ffn_api.cu"]
+           "hc_quant8.cu", "hc_mul8.cu", "hc_mul8_tiles.cu", "hc_logprobs.cu", "hc_ffn_api.cu"]
 HEADERS = ["hc_ptx.cuh", "hc_internal.h", "hc_attn.h", "hc_attn_dev.cuh", "hc_kv.cuh", "hc_ffn.h", "hc_mul8_dev.cuh",
            "hc_mul8_host.h"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -58,6 +58,9 @@ struct Mul8Args {
 };
 int launch_mul8(const Mul8Args& a, cudaStream_t stream);
 int read_mul8_error(unsigned int* word, int clear, cudaStream_t stream);
+// many rows (hc_mul8_tiles.cu)
+int launch_mul8_tiles(const Mul8Args& a, cudaStream_t stream);
+int read_mul8_tiles_error(unsigned int* word, int clear, cudaStream_t stream);
 
 // ---- log probabilities (hc_logprobs.cu) ------------------------------------------------------------
 constexpr int kMostTop = 32;

@@ -376,6 +376,7 @@ bool mul8_allow_smem(const void* kernel, int bytes, std::atomic<bool>* ready) {
 int launch_mul8(const Mul8Args& a, cudaStream_t stream) {
     const int sms = attn_sm_count();
     if (sms < 1) return -7;
+    if (a.n > 256) return launch_mul8_tiles(a, stream);
     if (a.up) {
         if (a.n <= 16) return start<16, true, 2>(a, sms, stream);
         if (a.n <= 32) return start<32, true, 2>(a, sms, stream);
@@ -389,11 +390,13 @@ int launch_mul8(const Mul8Args& a, cudaStream_t stream) {
 }
 
 int read_mul8_error(unsigned int* word, int clear, cudaStream_t stream) {
-    *word = 0;
+    unsigned int v = 0;
+    if (read_mul8_tiles_error(word, clear, stream) != 0) return -7;
     if (!g_launched.load(std::memory_order_relaxed)) return 0;
-    if (cudaMemcpyFromSymbolAsync(word, g_hc_mul8_error, sizeof(*word), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess) return -7;
+    if (cudaMemcpyFromSymbolAsync(&v, g_hc_mul8_error, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess) return -7;
     if (cudaStreamSynchronize(stream) != cudaSuccess) return -7;
-    if (clear && *word != 0) {
+    *word |= v;
+    if (clear && v != 0) {
         const unsigned int z = 0;
         if (cudaMemcpyToSymbolAsync(g_hc_mul8_error, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess) return -7;
         if (cudaStreamSynchronize(stream) != cudaSuccess) return -7;

@@ -3,10 +3,14 @@
 
 #include <atomic>
 #include <cuda.h>
+#include <cudaTypedefs.h>
 
 namespace hc {
 
 constexpr int kMul8Devices = 64;
+
+// The driver's encoder of tensor maps; null if it has none.
+PFN_cuTensorMapEncodeTiled_v12000 mul8_encode();
 
 // A tensor map of 8-bit rows (`cols` bytes, `stride` bytes apart) whose box is 128 columns by box_rows, 128-byte swizzle, zeros outside.
 bool mul8_map(CUtensorMap* m, const void* base, long long cols, long long rows, long long stride, int box_rows);

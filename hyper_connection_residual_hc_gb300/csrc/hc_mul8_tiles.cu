@@ -1,0 +1,425 @@
+// Products of 8-bit rows with 8-bit weights for many rows (formulas and format: include/hc.h; few rows: hc_mul8.cu).
+//
+// A pair of CTAs (a cluster of 2) takes 256 tokens by 256 rows of weights with tcgen05.mma of cta_group::2: each CTA holds its 128
+// tokens and half of the weights in shared memory and the sums of its tokens, 128 lanes by 256 columns, in tensor memory. The 256
+// rows of weights are 256 features of a plain product, or 128 of the gate and 128 of the up projection.
+//
+// Scales are any fp32 numbers, one for each 128 values of k, so a block's sums (4 instructions of K = 32) leave tensor memory and
+// are added up in registers: acc += (token's scale * weights' scale) * sums. A token is a lane, so the factor is one number a
+// thread. Two sets of 256 columns take turns: the next block's MMAs run under this one's additions. An MMA block takes
+// 512 cycles at the full rate, the additions about 256 cycles of FMA issue and as many of tensor memory reads.
+//
+// Warps: 8 add up (4 for each half of the columns; a gated product's two halves are columns 0..63 and 64..127 of gate and up, so that a
+// thread has both), 1 issues TMA loads, 1 (of the first CTA) the MMAs. Registers move from the last 4 warps to the first 8.
+// Results leave through shared memory by TMA stores, 128 bytes of 32 rows at a time, which also cut off rows and columns
+// outside the output.
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "hc_attn.h"
+#include "hc_ffn.h"
+#include "hc_mul8_dev.cuh"
+#include "hc_mul8_host.h"
+
+namespace hc {
+namespace {
+
+__device__ unsigned int g_hc_mul8_tiles_error = 0;
+std::atomic<bool> g_launched{false};
+
+constexpr int kTokens = 256;                     // of a pair
+constexpr int kRowsW = 256;                      // rows of weights of a pair
+constexpr int kHalf = 128;
+constexpr int kStages = 6;
+constexpr int kOperand = kHalf * kBlock8;        // bytes: 128 rows of one operand
+constexpr int kStage = 2 * kOperand;
+constexpr int kAddWarps = 8, kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 384;
+constexpr int kOutWarp = 4096;                   // 32 rows of 128 bytes
+constexpr int kOut = kStages * kStage;
+constexpr int kTops = 2048;                      // of a warp's output, behind 32 rows of 64 bytes: [2][32] largest magnitudes
+constexpr int kBars = kOut + kAddWarps * kOutWarp;
+constexpr int kSmem = kBars + 256 + 1024;        // + alignment
+static_assert(kSmem <= 227 * 1024, "fits");
+constexpr int kBand = 8;                         // token tiles that go through the weights together
+
+struct Params {
+    Mul8Args a;
+    int k_blocks, token_tiles, feature_tiles, pairs;
+    int stored;  // features that TMA stores: whole 16 bytes of a row
+    long long tiles;
+};
+
+__device__ __forceinline__ void tmem_alloc2(uint32_t dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() { asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma8_pair(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs.
+__device__ __forceinline__ void commit8_pair(uint32_t lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "mov.b16 m, 3;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar),
+        "r"(lead)
+        : "memory");
+}
+// Into this CTA's shared memory, completing on a barrier of either CTA (`bar`: an address in the cluster's window).
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+// Without release: what the arrival stands for is tensor memory reads, which tcgen05.fence orders; a release at cluster scope would
+// wait for all of the thread's memory operations.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+struct Tile {
+    int tokens, features;  // tile numbers
+};
+// Bands of kBand token tiles; within a band the token tiles of one feature tile come first, so that what runs at the same time
+// shares both operands in L2.
+__device__ __forceinline__ Tile tile_at(const Params& p, long long i) {
+    const long long band = i / (static_cast<long long>(kBand) * p.feature_tiles);
+    const int first = static_cast<int>(band) * kBand, rows = min(kBand, p.token_tiles - first);
+    const int r = static_cast<int>(i - band * kBand * p.feature_tiles);
+    return {first + r % rows, r / rows};
+}
+
+template <bool kGated>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_up,
+                  const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ Params p) {
+    extern __shared__ unsigned char raw[];
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    unsigned char* at = raw + (base - smem_u32(raw));
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const uint32_t full = base + kBars, empty = full + 8 * kStages, acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, slot = acc_empty + 16;
+    volatile uint32_t* abort_word = reinterpret_cast<volatile uint32_t*>(at + (slot + 4 - base));
+    const Wait8 wait{abort_word, &g_hc_mul8_tiles_error};
+    const uint32_t rank = cluster_ctarank8();
+    const int pair = static_cast<int>(blockIdx.x) / 2;
+
+    if (warp == kMmaWarp) {
+        tmem_alloc2(slot, 512);
+        tmem_relinquish2();
+    }
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(acc_empty + 8 * i, 2 * kAddWarps);
+        }
+        *abort_word = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    cluster_sync8();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(at + (slot - base));
+
+    if (warp >= kAddWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == kLoadWarp && lane == 0) {  // ---- loads
+            const uint32_t first_full = mapa8(full, 0);
+            int i = 0;  // blocks so far
+            for (long long n = pair; n < p.tiles; n += p.pairs) {
+                const Tile t = tile_at(p, n);
+                const int token = t.tokens * kTokens + static_cast<int>(rank) * kHalf;
+                const int row = kGated ? t.features * kHalf : t.features * kRowsW + static_cast<int>(rank) * kHalf;
+                const CUtensorMap* w = kGated && rank ? &tm_up : &tm_w;
+                for (int b = 0; b < p.k_blocks; ++b, ++i) {
+                    const int s = i % kStages;
+                    if (i >= kStages) wait(empty + 8 * s, (i / kStages - 1) & 1);
+                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * kStage);
+                    const uint32_t st = base + s * kStage;
+                    tma_load_pair(st, &tm_x, first_full + 8 * s, b * kBlock8, token);
+                    tma_load_pair(st + kOperand, w, first_full + 8 * s, b * kBlock8, row);
+                }
+            }
+            // no copy of either CTA is in flight when the pair ends, whatever happened
+            if (rank == 0)
+                for (int j = max(i - kStages, 0); j < i; ++j) wait.drain(full + 8 * (j % kStages), (j / kStages) & 1);
+        } else if (warp == kMmaWarp && rank == 0) {  // ---- MMAs
+            const uint32_t lead = elect_one();
+            constexpr uint32_t idesc = idesc8(256, 256);
+            int i = 0;
+            for (long long n = pair; n < p.tiles; n += p.pairs) {
+                for (int b = 0; b < p.k_blocks; ++b, ++i) {
+                    const int s = i % kStages, u = i & 1;
+                    if (i >= 2) wait(acc_empty + 8 * u, (i / 2 - 1) & 1);
+                    wait(full + 8 * s, (i / kStages) & 1);
+                    tc_fence_after();
+                    const uint32_t st = base + s * kStage, d = tmem + u * 256;
+                    const uint64_t x = sdesc8(st), w = sdesc8(st + kOperand);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) mma8_pair(lead, d, x + 2 * q, w + 2 * q, idesc, q > 0);
+                    commit8_pair(lead, empty + 8 * s);
+                    commit8_pair(lead, acc_full + 8 * u);
+                }
+            }
+            if (i > 0) wait.drain(acc_full + 8 * ((i - 1) & 1), ((i - 1) / 2) & 1);
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int half = warp / 4, quarter = warp % 4;
+        const int in_cta = 32 * quarter + lane;  // token
+        const uint32_t mine = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
+        const uint32_t released = mapa8(acc_empty, 0);
+        const uint32_t out_smem = base + kOut + warp * kOutWarp;
+        // the scales of 4 blocks of k, fetched while the 4 before them are added up
+        float next_x[4], next_w[kGated ? 2 : 1][4];
+        auto fetch = [&](long long n, int b) {
+            if (n >= p.tiles) return;
+            const Tile t = tile_at(p, n);
+            const long long token = static_cast<long long>(t.tokens) * kTokens + rank * kHalf + in_cta;
+            const int fb = kGated ? t.features : 2 * t.features + half;
+            const bool has = token < p.a.n, hasw = fb < blocks8(p.a.features);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool in = b + j < p.k_blocks;
+                next_x[j] = in && has ? __ldg(p.a.x_scales + token * p.k_blocks + b + j) : 0.f;
+                const long long w = static_cast<long long>(fb) * p.k_blocks + b + j;
+                next_w[0][j] = in && hasw ? __ldg(p.a.w_scales + w) : 0.f;
+                if constexpr (kGated) next_w[1][j] = in && hasw ? __ldg(p.a.up_scales + w) : 0.f;
+            }
+        };
+        fetch(pair, 0);
+        int i = 0, turn = 0;
+        for (long long n = pair; n < p.tiles; n += p.pairs, ++turn) {
+            uint64_t acc[64];  // pairs of columns: 128 features, or 64 of the gate and 64 of up
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = 0;
+            for (int b0 = 0; b0 < p.k_blocks; b0 += 4) {
+                float f[2][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[0][j] = next_x[j] * next_w[0][j];
+                    f[1][j] = kGated ? next_x[j] * next_w[kGated ? 1 : 0][j] : f[0][j];
+                }
+                if (b0 + 4 < p.k_blocks)
+                    fetch(n, b0 + 4);
+                else
+                    fetch(n + p.pairs, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (b0 + j >= p.k_blocks) break;
+                    const int u = i & 1;
+                    wait(acc_full + 8 * u, (i / 2) & 1);
+                    ++i;
+                    tc_fence_after();
+                    const uint32_t from = mine + u * 256;
+                    float v[2][16];
+                    auto column = [&](int q) { return kGated ? (q / 4) * 128 + half * 64 + (q % 4) * 16 : half * 128 + q * 16; };
+                    tmem_start16(from + column(0), v[0]);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        tmem_wait16(v[q % 2]);
+                        if (q < 7) {
+                            tmem_start16(from + column(q + 1), v[(q + 1) % 2]);
+                        } else {
+                            tc_fence_before();
+                            if (lane == 0) arrive_cluster(released + 8 * u);
+                        }
+                        const uint64_t ff = pair8(f[q / 4][j], f[q / 4][j]);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) acc[8 * q + e] = fma8(pair8(v[q % 2][2 * e], v[q % 2][2 * e + 1]), ff, acc[8 * q + e]);
+                    }
+                }
+            }
+            const Tile t = tile_at(p, n);
+            const int token0 = t.tokens * kTokens + static_cast<int>(rank) * kHalf + 32 * quarter;  // of the warp
+            // Stages 128 bytes of each of the warp's 32 rows (a lane's words w, 16 bytes at a time, swizzled as the map says) and stores
+            // them at column x.
+            auto store = [&](const uint32_t* w, int bytes, int x) {
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
+                const int mask = bytes == 128 ? lane & 7 : (lane >> 1) & 3;
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (16 * c < bytes)
+                        st_smem_v4(out_smem + static_cast<uint32_t>(lane * bytes + ((c ^ mask) * 16)), make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && token0 < p.a.n) {
+                    if (x < p.stored) tma_store_2d(&tm_out, out_smem, x, token0);
+                    bulk_commit();
+                }
+                if constexpr (!kGated) {
+                    // A TMA store writes whole 16 bytes; the features past the last of those go one by one.
+                    const int size = p.a.out_type == kOutF32 ? 4 : 2, rest = p.a.features - p.stored, off = (p.stored - x) * size;
+                    if (rest > 0 && off >= 0 && off < 128 && token0 + lane < p.a.n) {
+                        const uint4 q = ld_smem_v4(out_smem + static_cast<uint32_t>(lane * 128 + ((off / 16) ^ mask) * 16));
+                        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+                        const long long o = (static_cast<long long>(token0) + lane) * p.a.out_stride + p.stored;
+#pragma unroll
+                        for (int e = 0; e < 7; ++e) {
+                            if (e >= rest) break;
+                            if (size == 4)
+                                static_cast<uint32_t*>(p.a.out)[o + e] = u[e % 4];
+                            else
+                                static_cast<uint16_t*>(p.a.out)[o + e] = static_cast<uint16_t>(u[e / 2] >> (e % 2 * 16));
+                        }
+                    }
+                }
+            };
+            if constexpr (kGated) {
+                float h[64];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    float g0, g1, u0, u1;
+                    unpair8(acc[e], g0, g1);
+                    unpair8(acc[32 + e], u0, u1);
+                    h[2 * e] = activate8(g0, p.a.act) * u0;
+                    h[2 * e + 1] = activate8(g1, p.a.act) * u1;
+                }
+                const int x = t.features * kHalf + 64 * half;
+                if (p.a.out_type == kOutE4m3) {
+                    float top = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) top = max_nan(top, fabsf(h[e]));  // (features past the last are 0)
+                    // the other 64 features' is with the warp of the other half
+                    float* tops = reinterpret_cast<float*>(at + kOut + kTops) + (turn & 1) * 32 + lane;
+                    tops[warp * (kOutWarp / 4)] = top;
+                    asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+                    top = max_nan(max_nan(top, tops[(warp ^ 4) * (kOutWarp / 4)]), kLeastTop8);
+                    const float up = kTop8 / top;
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = e4m3x4(h[4 * e] * up, h[4 * e + 1] * up, h[4 * e + 2] * up, h[4 * e + 3] * up);
+                    store(w, 64, x);
+                    const long long row = static_cast<long long>(token0) + lane;
+                    if (half == 0 && row < p.a.n) p.a.out_scales[row * p.feature_tiles + t.features] = top / kTop8;
+                } else {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) w[e] = bf16x2(h[2 * e], h[2 * e + 1]);
+                    store(w, 128, x);
+                }
+            } else {
+                const int x = t.features * kRowsW + kHalf * half;
+                if (p.a.out_type == kOutF32) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float a, b;
+                            unpair8(acc[16 * c + e], a, b);
+                            w[2 * e] = __float_as_uint(a);
+                            w[2 * e + 1] = __float_as_uint(b);
+                        }
+                        store(w, 128, x + 32 * c);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float a, b;
+                            unpair8(acc[32 * c + e], a, b);
+                            w[e] = bf16x2(a, b);
+                        }
+                        store(w, 128, x + 64 * c);
+                    }
+                }
+            }
+        }
+        if (lane == 0) bulk_wait<0>();
+        __syncwarp();
+    }
+    tc_fence_before();
+    cluster_sync8();  // nothing of this pair is in flight any more
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc2(tmem, 512);
+    }
+}
+
+bool out_map(CUtensorMap* m, const Mul8Args& a, int stored) {
+    const auto fn = mul8_encode();
+    if (!fn) return false;
+    const int size = a.out_type == kOutF32 ? 4 : a.out_type == kOutE4m3 ? 1 : 2;
+    const CUtensorMapDataType type = a.out_type == kOutF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : a.out_type == kOutE4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(stored > 0 ? stored : 8), static_cast<cuuint64_t>(a.n)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.out_stride) * static_cast<cuuint64_t>(size)};
+    const cuuint32_t box[2] = {a.out_type == kOutF32 ? 32u : 64u, 32}, ones[2] = {1, 1};
+    return fn(m, type, 2, a.out, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              a.out_type == kOutE4m3 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kGated>
+int start(const Mul8Args& a, int sms, cudaStream_t stream) {
+    static std::atomic<bool> ready[kMul8Devices];
+    if (!mul8_allow_smem(reinterpret_cast<const void*>(&mul8_tiles_kernel<kGated>), kSmem, ready)) return -7;
+    Params p;
+    p.a = a;
+    p.k_blocks = blocks8(a.k);
+    p.token_tiles = static_cast<int>((a.n + kTokens - 1) / kTokens);
+    p.feature_tiles = (a.features + (kGated ? kHalf : kRowsW) - 1) / (kGated ? kHalf : kRowsW);
+    p.tiles = static_cast<long long>(p.token_tiles) * p.feature_tiles;
+    p.pairs = static_cast<int>(p.tiles < sms / 2 ? p.tiles : sms / 2);
+    const int unit = a.out_type == kOutF32 ? 4 : a.out_type == kOutE4m3 ? 16 : 8;
+    p.stored = a.features / unit * unit;
+    CUtensorMap tm_x, tm_w, tm_up, tm_out;
+    if (!mul8_map(&tm_x, a.x, a.k, a.n, a.x_stride, kHalf) || !mul8_map(&tm_w, a.w, a.k, a.features, a.w_stride, kHalf) || !out_map(&tm_out, a, p.stored)) return -7;
+    tm_up = tm_w;
+    if (kGated && !mul8_map(&tm_up, a.up, a.k, a.features, a.w_stride, kHalf)) return -7;
+    g_launched.store(true, std::memory_order_relaxed);
+    mul8_tiles_kernel<kGated><<<static_cast<unsigned>(2 * p.pairs), kThreads, kSmem, stream>>>(tm_x, tm_w, tm_up, tm_out, p);
+    return cudaGetLastError() == cudaSuccess ? 0 : -7;
+}
+
+}  // namespace
+
+int launch_mul8_tiles(const Mul8Args& a, cudaStream_t stream) {
+    const int sms = attn_sm_count();
+    if (sms < 2) return -7;
+    return a.up ? start<true>(a, sms, stream) : start<false>(a, sms, stream);
+}
+
+int read_mul8_tiles_error(unsigned int* word, int clear, cudaStream_t stream) {
+    *word = 0;
+    if (!g_launched.load(std::memory_order_relaxed)) return 0;
+    if (cudaMemcpyFromSymbolAsync(word, g_hc_mul8_tiles_error, sizeof(*word), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess) return -7;
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return -7;
+    if (clear && *word != 0) {
+        const unsigned int z = 0;
+        if (cudaMemcpyToSymbolAsync(g_hc_mul8_tiles_error, &z, sizeof(z), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess) return -7;
+        if (cudaStreamSynchronize(stream) != cudaSuccess) return -7;
+    }
+    return 0;
+}
+
+}  // namespace hc
