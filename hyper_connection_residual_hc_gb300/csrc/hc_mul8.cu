@@ -195,14 +195,14 @@ mul8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 #pragma unroll
             for (int q = 0; q < kParts * P::kMats; ++q) {
                 const int m = q / kParts, c = q % kParts;
-                tmem_wait16(v[q % 2]);
+                tmem_wait();
                 if (q + 1 < kParts * P::kMats) tmem_start16(from + ((q + 1) / kParts) * kN + 16 * ((q + 1) % kParts), v[(q + 1) % 2]);
                 const float4* g = reinterpret_cast<const float4*>(f + m * kGroup * kN + 16 * c);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float4 s = g[j];
-                    acc[m][8 * c + 2 * j] = fma8(pair8(v[q % 2][4 * j], v[q % 2][4 * j + 1]), pair8(s.x, s.y), acc[m][8 * c + 2 * j]);
-                    acc[m][8 * c + 2 * j + 1] = fma8(pair8(v[q % 2][4 * j + 2], v[q % 2][4 * j + 3]), pair8(s.z, s.w), acc[m][8 * c + 2 * j + 1]);
+                    add_scaled(acc[m][8 * c + 2 * j], v[q % 2][4 * j], v[q % 2][4 * j + 1], pair8(s.x, s.y));
+                    add_scaled(acc[m][8 * c + 2 * j + 1], v[q % 2][4 * j + 2], v[q % 2][4 * j + 3], pair8(s.z, s.w));
                 }
             }
             tc_fence_before();

@@ -81,8 +81,9 @@ __device__ __forceinline__ void commit8(uint32_t lead, uint32_t bar) {
         : "memory");
 }
 
-// 16 consecutive columns of this thread's lane; the values are there after tmem_wait16 (which waits for all loads so far and
-// names the registers, so that no use of them moves above it).
+// 16 consecutive columns of this thread's lane; the values are there after tmem_wait, which waits for all loads so far. What uses
+// them has to be volatile (add_scaled), so that it stays behind the wait: naming the registers there instead made the compiler
+// move them about.
 __device__ __forceinline__ void tmem_start16(uint32_t addr, float (&v)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -92,13 +93,7 @@ __device__ __forceinline__ void tmem_start16(uint32_t addr, float (&v)[16]) {
         : "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_wait16(float (&v)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
-                   "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
-                 :
-                 : "memory");
-}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // Pairs of fp32 in one instruction.
 __device__ __forceinline__ uint64_t pair8(float a, float b) {
@@ -107,10 +102,14 @@ __device__ __forceinline__ uint64_t pair8(float a, float b) {
     return r;
 }
 __device__ __forceinline__ void unpair8(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma8(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
+// acc += {a, b} * scale, for values that came by tmem_start16
+__device__ __forceinline__ void add_scaled(uint64_t& acc, float a, float b, uint64_t scale) {
+    asm volatile(
+        "{\n\t.reg .b64 t;\n\t"
+        "mov.b64 t, {%1, %2};\n\t"
+        "fma.rn.f32x2 %0, t, %3, %0;\n\t}"
+        : "+l"(acc)
+        : "f"(a), "f"(b), "l"(scale));
 }
 
 __device__ __forceinline__ uint32_t cluster_ctarank8() {

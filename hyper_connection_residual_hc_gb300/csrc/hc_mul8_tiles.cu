@@ -196,64 +196,65 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         const uint32_t mine = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
         const uint32_t released = mapa8(acc_empty, 0);
         const uint32_t out_smem = base + kOut + warp * kOutWarp;
-        // the scales of 4 blocks of k, fetched while the 4 before them are added up
-        float next_x[4], next_w[kGated ? 2 : 1][4];
-        auto fetch = [&](long long n, int b) {
-            if (n >= p.tiles) return;
-            const Tile t = tile_at(p, n);
+        // The scales of a block are fetched two blocks ahead, into the next tile's first ones at a tile's end.
+        long long at_n = pair;
+        int at_b = 0;
+        const float *from_x = nullptr, *from_w = nullptr, *from_up = nullptr;
+        auto enter = [&]() {
+            const Tile t = tile_at(p, at_n);
             const long long token = static_cast<long long>(t.tokens) * kTokens + rank * kHalf + in_cta;
             const int fb = kGated ? t.features : 2 * t.features + half;
-            const bool has = token < p.a.n, hasw = fb < blocks8(p.a.features);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool in = b + j < p.k_blocks;
-                next_x[j] = in && has ? __ldg(p.a.x_scales + token * p.k_blocks + b + j) : 0.f;
-                const long long w = static_cast<long long>(fb) * p.k_blocks + b + j;
-                next_w[0][j] = in && hasw ? __ldg(p.a.w_scales + w) : 0.f;
-                if constexpr (kGated) next_w[1][j] = in && hasw ? __ldg(p.a.up_scales + w) : 0.f;
-            }
+            from_x = at_n < p.tiles && token < p.a.n ? p.a.x_scales + token * p.k_blocks : nullptr;
+            const bool has = at_n < p.tiles && fb < blocks8(p.a.features);
+            from_w = has ? p.a.w_scales + static_cast<long long>(fb) * p.k_blocks : nullptr;
+            if constexpr (kGated) from_up = has ? p.a.up_scales + static_cast<long long>(fb) * p.k_blocks : nullptr;
         };
-        fetch(pair, 0);
+        struct Scales {
+            float x, w, up;
+        };
+        auto fetch = [&]() {
+            Scales s;
+            s.x = from_x ? __ldg(from_x + at_b) : 0.f;
+            s.w = from_w ? __ldg(from_w + at_b) : 0.f;
+            s.up = kGated && from_up ? __ldg(from_up + at_b) : 0.f;
+            if (++at_b == p.k_blocks) {
+                at_b = 0;
+                at_n += p.pairs;
+                enter();
+            }
+            return s;
+        };
+        enter();
+        Scales first = fetch(), second = fetch();
         int i = 0, turn = 0;
         for (long long n = pair; n < p.tiles; n += p.pairs, ++turn) {
             uint64_t acc[64];  // pairs of columns: 128 features, or 64 of the gate and 64 of up
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0;
-            for (int b0 = 0; b0 < p.k_blocks; b0 += 4) {
-                float f[2][4];
+#pragma unroll 1
+            for (int b = 0; b < p.k_blocks; ++b, ++i) {
+                const float f0 = first.x * first.w, f1 = kGated ? first.x * first.up : f0;
+                const uint64_t f[2] = {pair8(f0, f0), pair8(f1, f1)};
+                first = second;
+                second = fetch();
+                const int u = i & 1;
+                wait(acc_full + 8 * u, (i / 2) & 1);
+                tc_fence_after();
+                const uint32_t from = mine + u * 256;
+                float v[2][16];
+                auto column = [&](int q) { return kGated ? (q / 4) * 128 + half * 64 + (q % 4) * 16 : half * 128 + q * 16; };
+                tmem_start16(from + column(0), v[0]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    f[0][j] = next_x[j] * next_w[0][j];
-                    f[1][j] = kGated ? next_x[j] * next_w[kGated ? 1 : 0][j] : f[0][j];
-                }
-                if (b0 + 4 < p.k_blocks)
-                    fetch(n, b0 + 4);
-                else
-                    fetch(n + p.pairs, 0);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (b0 + j >= p.k_blocks) break;
-                    const int u = i & 1;
-                    wait(acc_full + 8 * u, (i / 2) & 1);
-                    ++i;
-                    tc_fence_after();
-                    const uint32_t from = mine + u * 256;
-                    float v[2][16];
-                    auto column = [&](int q) { return kGated ? (q / 4) * 128 + half * 64 + (q % 4) * 16 : half * 128 + q * 16; };
-                    tmem_start16(from + column(0), v[0]);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        tmem_wait16(v[q % 2]);
-                        if (q < 7) {
-                            tmem_start16(from + column(q + 1), v[(q + 1) % 2]);
-                        } else {
-                            tc_fence_before();
-                            if (lane == 0) arrive_cluster(released + 8 * u);
-                        }
-                        const uint64_t ff = pair8(f[q / 4][j], f[q / 4][j]);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) acc[8 * q + e] = fma8(pair8(v[q % 2][2 * e], v[q % 2][2 * e + 1]), ff, acc[8 * q + e]);
+                for (int q = 0; q < 8; ++q) {
+                    tmem_wait();
+                    if (q < 7) {
+                        tmem_start16(from + column(q + 1), v[(q + 1) % 2]);
+                    } else {
+                        tc_fence_before();
+                        if (lane == 0) arrive_cluster(released + 8 * u);
                     }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) add_scaled(acc[8 * q + e], v[q % 2][2 * e], v[q % 2][2 * e + 1], f[q / 4]);
                 }
             }
             const Tile t = tile_at(p, n);
