@@ -94,6 +94,24 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// 64 consecutive columns of this thread's lane (see tmem_start16).
+__device__ __forceinline__ void tmem_start64(uint32_t addr, float (&v)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
+          "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]),
+          "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]),
+          "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
+          "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
+        : "r"(addr)
+        : "memory");
+}
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
     const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&t);
@@ -241,20 +259,17 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 wait(acc_full + 8 * u, (i / 2) & 1);
                 tc_fence_after();
                 const uint32_t from = mine + u * 256;
-                float v[2][16];
-                auto column = [&](int q) { return kGated ? (q / 4) * 128 + half * 64 + (q % 4) * 16 : half * 128 + q * 16; };
-                tmem_start16(from + column(0), v[0]);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                for (int q = 0; q < 2; ++q) {
+                    float v[64];
+                    tmem_start64(from + (kGated ? q * 128 + half * 64 : half * 128 + q * 64), v);
                     tmem_wait();
-                    if (q < 7) {
-                        tmem_start16(from + column(q + 1), v[(q + 1) % 2]);
-                    } else {
+                    if (q == 1) {
                         tc_fence_before();
                         if (lane == 0) arrive_cluster(released + 8 * u);
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) add_scaled(acc[8 * q + e], v[q % 2][2 * e], v[q % 2][2 * e + 1], f[q / 4]);
+                    for (int e = 0; e < 32; ++e) add_scaled(acc[32 * q + e], v[2 * e], v[2 * e + 1], f[q]);
                 }
             }
             const Tile t = tile_at(p, n);
