@@ -17,10 +17,14 @@ struct Wait8 {
     unsigned int* error;
     static constexpr uint64_t kNs = 1000000000ull;
     __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) const {
-        if (mbar_sleep(bar, parity)) return;
+        if (mbar_test(bar, parity)) return;
+        slow(bar, parity);
+    }
+    __device__ __forceinline__ void slow(uint32_t bar, uint32_t parity) const {
         const uint64_t t0 = global_timer_ns();
         while (true) {
-            if (mbar_sleep(bar, parity)) return;
+            for (int i = 0; i < 64; ++i)
+                if (mbar_test(bar, parity)) return;
             if (*abort) return;
             if (global_timer_ns() - t0 > kNs) {
                 *abort = 1u;
@@ -148,12 +152,14 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return r;
 }
 
-// The gate's activation. Both forms are x times a logistic function, in which e^-x overflows to infinity for a large
-// negative x and the quotient is -0, as it should be; GELU is its form with tanh, (1 + tanh y) / 2 = 1 / (1 + e^-2y).
+// The gate's activation. Both forms are x times a logistic function, 1 / (1 + e^-y), in which e^-y overflows to infinity for a
+// large negative y and the quotient is 0, as it should be; GELU is its form with tanh, (1 + tanh z) / 2 = 1 / (1 + e^-2z). By the
+// special function unit's 2^t and 1/t, each within 2^-22 or so of the exact value: a full exponential and a division took
+// as long as 4 blocks of k a tile.
 __device__ __forceinline__ float activate8(float x, int act) {
-    float y = x;
-    if (act == kActGelu) y = 1.5957691216057308f * fmaf(0.044715f * x * x, x, x);
-    return x / (1.f + expf(-y));
+    float y = -kLog2e * x;
+    if (act == kActGelu) y *= 1.5957691216057308f * fmaf(0.044715f * x, x, 1.f);
+    return x * rcp_approx(1.f + ex2(y));
 }
 
 }  // namespace hc

@@ -35,15 +35,17 @@ std::atomic<bool> g_launched{false};
 constexpr int kTokens = 256;                     // of a pair
 constexpr int kRowsW = 256;                      // rows of weights of a pair
 constexpr int kHalf = 128;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kOperand = kHalf * kBlock8;        // bytes: 128 rows of one operand
 constexpr int kStage = 2 * kOperand;
-constexpr int kAddWarps = 8, kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kAddWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kScaleWarps = 2;  // in this order
 constexpr int kThreads = 384;
 constexpr int kOutWarp = 4096;                   // 32 rows of 128 bytes
 constexpr int kOut = kStages * kStage;
 constexpr int kTops = 2048;                      // of a warp's output, behind 32 rows of 64 bytes: [2][32] largest magnitudes
-constexpr int kBars = kOut + kAddWarps * kOutWarp;
+constexpr int kBatch = 8;                        // blocks of k whose scales are handed over together
+constexpr int kScales = kOut + kAddWarps * kOutWarp;  // [2][kBatch][2][128] factors
+constexpr int kBars = kScales + 2 * kBatch * 2 * kHalf * 4;
 constexpr int kSmem = kBars + 256 + 1024;        // + alignment
 static_assert(kSmem <= 227 * 1024, "fits");
 constexpr int kBand = 8;                         // token tiles that go through the weights together
@@ -89,10 +91,24 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
+// One lane's arrival without a branch around it, in this CTA.
+__device__ __forceinline__ void arrive_if(uint32_t bar, bool lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"(static_cast<uint32_t>(lead))
+        : "memory");
+}
 // Without release: what the arrival stands for is tensor memory reads, which tcgen05.fence orders; a release at cluster scope would
 // wait for all of the thread's memory operations.
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void arrive_cluster(uint32_t bar, bool lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"(static_cast<uint32_t>(lead))
+        : "memory");
 }
 // 64 consecutive columns of this thread's lane (see tmem_start16).
 __device__ __forceinline__ void tmem_start64(uint32_t addr, float (&v)[64]) {
@@ -137,7 +153,7 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     unsigned char* at = raw + (base - smem_u32(raw));
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const uint32_t full = base + kBars, empty = full + 8 * kStages, acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, slot = acc_empty + 16;
+    const uint32_t full = base + kBars, empty = full + 8 * kStages, acc_full = empty + 8 * kStages, acc_empty = acc_full + 32, sc_full = acc_empty + 32, sc_empty = sc_full + 16, slot = sc_empty + 16;
     volatile uint32_t* abort_word = reinterpret_cast<volatile uint32_t*>(at + (slot + 4 - base));
     const Wait8 wait{abort_word, &g_hc_mul8_tiles_error};
     const uint32_t rank = cluster_ctarank8();
@@ -152,9 +168,13 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(acc_full + 8 * i, 1);
-            mbar_init(acc_empty + 8 * i, 2 * kAddWarps);
+            mbar_init(acc_empty + 8 * i, kAddWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sc_full + 8 * i, kScaleWarps);
+            mbar_init(sc_empty + 8 * i, kAddWarps);
         }
         *abort_word = 0;
         fence_mbar_init();
@@ -165,14 +185,14 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(at + (slot - base));
 
     if (warp >= kAddWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kLoadWarp && lane == 0) {  // ---- loads
             const uint32_t first_full = mapa8(full, 0);
             int i = 0;  // blocks so far
             for (long long n = pair; n < p.tiles; n += p.pairs) {
                 const Tile t = tile_at(p, n);
                 const int token = t.tokens * kTokens + static_cast<int>(rank) * kHalf;
-                const int row = kGated ? t.features * kHalf : t.features * kRowsW + static_cast<int>(rank) * kHalf;
+                const int row = kGated ? t.features * kHalf : t.features * kRowsW + static_cast<int>(rank) * 64, step = kGated ? 64 : kHalf;
                 const CUtensorMap* w = kGated && rank ? &tm_up : &tm_w;
                 for (int b = 0; b < p.k_blocks; ++b, ++i) {
                     const int s = i % kStages;
@@ -181,6 +201,7 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     const uint32_t st = base + s * kStage;
                     tma_load_pair(st, &tm_x, first_full + 8 * s, b * kBlock8, token);
                     tma_load_pair(st + kOperand, w, first_full + 8 * s, b * kBlock8, row);
+                    tma_load_pair(st + kOperand + kOperand / 2, w, first_full + 8 * s, b * kBlock8, row + step);
                 }
             }
             // no copy of either CTA is in flight when the pair ends, whatever happened
@@ -188,89 +209,106 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 for (int j = max(i - kStages, 0); j < i; ++j) wait.drain(full + 8 * (j % kStages), (j / kStages) & 1);
         } else if (warp == kMmaWarp && rank == 0) {  // ---- MMAs
             const uint32_t lead = elect_one();
-            constexpr uint32_t idesc = idesc8(256, 256);
+            constexpr uint32_t idesc = idesc8(256, 128);
             int i = 0;
             for (long long n = pair; n < p.tiles; n += p.pairs) {
                 for (int b = 0; b < p.k_blocks; ++b, ++i) {
                     const int s = i % kStages, u = i & 1;
-                    if (i >= 2) wait(acc_empty + 8 * u, (i / 2 - 1) & 1);
                     wait(full + 8 * s, (i / kStages) & 1);
-                    tc_fence_after();
-                    const uint32_t st = base + s * kStage, d = tmem + u * 256;
-                    const uint64_t x = sdesc8(st), w = sdesc8(st + kOperand);
+                    const uint32_t st = base + s * kStage;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) mma8_pair(lead, d, x + 2 * q, w + 2 * q, idesc, q > 0);
+                    for (int h = 0; h < 2; ++h) {
+                        if (i >= 2) wait(acc_empty + 16 * u + 8 * h, (i / 2 - 1) & 1);
+                        tc_fence_after();
+                        const uint32_t d = tmem + u * 256 + h * 128;
+                        const uint64_t x = sdesc8(st), w = sdesc8(st + kOperand + h * (kOperand / 2));
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) mma8_pair(lead, d, x + 2 * q, w + 2 * q, idesc, q > 0);
+                        commit8_pair(lead, acc_full + 16 * u + 8 * h);
+                    }
                     commit8_pair(lead, empty + 8 * s);
-                    commit8_pair(lead, acc_full + 8 * u);
                 }
             }
-            if (i > 0) wait.drain(acc_full + 8 * ((i - 1) & 1), ((i - 1) / 2) & 1);
+            if (i > 0) wait.drain(acc_full + 16 * ((i - 1) & 1) + 8, ((i - 1) / 2) & 1);
+        } else if (warp > kMmaWarp) {  // ---- scales
+            // The factors of the CTA's 128 tokens, 2 to a lane, with the weights of either half of the columns (gate and up). Tokens and
+            // features outside the matrices take the last ones inside (their sums are not stored).
+            int batch = 0;
+            for (long long n = pair; n < p.tiles; n += p.pairs) {
+                const Tile t = tile_at(p, n);
+                const int in_cta = 64 * (warp - kMmaWarp - 1) + lane;
+                const long long token = static_cast<long long>(t.tokens) * kTokens + rank * kHalf + in_cta;
+                const float* x0 = p.a.x_scales + min(token, p.a.n - 1) * p.k_blocks;
+                const float* x1 = p.a.x_scales + min(token + 32, p.a.n - 1) * p.k_blocks;
+                const int most = blocks8(p.a.features) - 1;
+                const float* w0 = p.a.w_scales + static_cast<long long>(min(kGated ? t.features : 2 * t.features, most)) * p.k_blocks;
+                const float* w1 = kGated ? p.a.up_scales + static_cast<long long>(t.features) * p.k_blocks
+                                         : p.a.w_scales + static_cast<long long>(min(2 * t.features + 1, most)) * p.k_blocks;
+                for (int b = 0; b < p.k_blocks; b += kBatch, ++batch) {
+                    if (batch >= 2) wait(sc_empty + 8 * (batch & 1), (batch / 2 - 1) & 1);
+                    float* o = reinterpret_cast<float*>(at + kScales) + (batch & 1) * kBatch * 2 * kHalf + in_cta;
+#pragma unroll
+                    for (int j0 = 0; j0 < kBatch; j0 += 4) {
+                        float x[2][4], w[2][4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int from = min(b + j0 + j, p.k_blocks - 1);
+                            x[0][j] = __ldg(x0 + from);
+                            x[1][j] = __ldg(x1 + from);
+                            w[0][j] = __ldg(w0 + from);
+                            w[1][j] = __ldg(w1 + from);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) o[((j0 + j) * 2 + r / 2) * kHalf + r % 2 * 32] = x[r % 2][j] * w[r / 2][j];
+                    }
+                    __syncwarp();
+                    arrive_if(sc_full + 8 * (batch & 1), lane == 0);
+                }
+            }
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int half = warp / 4, quarter = warp % 4;
         const int in_cta = 32 * quarter + lane;  // token
         const uint32_t mine = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
         const uint32_t released = mapa8(acc_empty, 0);
         const uint32_t out_smem = base + kOut + warp * kOutWarp;
-        // The scales of a block are fetched two blocks ahead, into the next tile's first ones at a tile's end.
-        long long at_n = pair;
-        int at_b = 0;
-        const float *from_x = nullptr, *from_w = nullptr, *from_up = nullptr;
-        auto enter = [&]() {
-            const Tile t = tile_at(p, at_n);
-            const long long token = static_cast<long long>(t.tokens) * kTokens + rank * kHalf + in_cta;
-            const int fb = kGated ? t.features : 2 * t.features + half;
-            from_x = at_n < p.tiles && token < p.a.n ? p.a.x_scales + token * p.k_blocks : nullptr;
-            const bool has = at_n < p.tiles && fb < blocks8(p.a.features);
-            from_w = has ? p.a.w_scales + static_cast<long long>(fb) * p.k_blocks : nullptr;
-            if constexpr (kGated) from_up = has ? p.a.up_scales + static_cast<long long>(fb) * p.k_blocks : nullptr;
-        };
-        struct Scales {
-            float x, w, up;
-        };
-        auto fetch = [&]() {
-            Scales s;
-            s.x = from_x ? __ldg(from_x + at_b) : 0.f;
-            s.w = from_w ? __ldg(from_w + at_b) : 0.f;
-            s.up = kGated && from_up ? __ldg(from_up + at_b) : 0.f;
-            if (++at_b == p.k_blocks) {
-                at_b = 0;
-                at_n += p.pairs;
-                enter();
-            }
-            return s;
-        };
-        enter();
-        Scales first = fetch(), second = fetch();
-        int i = 0, turn = 0;
+        const float* factors = reinterpret_cast<const float*>(at + kScales) + (kGated ? 0 : half * kHalf) + in_cta;
+        int i = 0, batch = 0, turn = 0;
         for (long long n = pair; n < p.tiles; n += p.pairs, ++turn) {
             uint64_t acc[64];  // pairs of columns: 128 features, or 64 of the gate and 64 of up
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0;
 #pragma unroll 1
             for (int b = 0; b < p.k_blocks; ++b, ++i) {
-                const float f0 = first.x * first.w, f1 = kGated ? first.x * first.up : f0;
-                const uint64_t f[2] = {pair8(f0, f0), pair8(f1, f1)};
-                first = second;
-                second = fetch();
+                const int j = b % kBatch;
+                if (j == 0) wait(sc_full + 8 * (batch & 1), (batch / 2) & 1);
+                const float* g = factors + ((batch & 1) * kBatch + j) * 2 * kHalf;
+                const float factor[2] = {g[0], kGated ? g[kHalf] : g[0]};
+                const bool done = j == kBatch - 1 || b + 1 == p.k_blocks;  // with these factors
                 const int u = i & 1;
-                wait(acc_full + 8 * u, (i / 2) & 1);
+                wait(acc_full + 16 * u + 8 * half, (i / 2) & 1);
                 tc_fence_after();
-                const uint32_t from = mine + u * 256;
+                const uint32_t from = mine + u * 256 + half * 128;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     float v[64];
-                    tmem_start64(from + (kGated ? q * 128 + half * 64 : half * 128 + q * 64), v);
+                    tmem_start64(from + q * 64, v);
                     tmem_wait();
                     if (q == 1) {
                         tc_fence_before();
-                        if (lane == 0) arrive_cluster(released + 8 * u);
+                        arrive_cluster(released + 16 * u + 8 * half, lane == 0);
                     }
+                    const uint64_t f = pair8(factor[q], factor[q]);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) add_scaled(acc[32 * q + e], v[2 * e], v[2 * e + 1], f[q]);
+                    for (int e = 0; e < 32; ++e) add_scaled(acc[32 * q + e], v[2 * e], v[2 * e + 1], f);
                 }
+                __syncwarp();
+                arrive_if(sc_empty + 8 * (batch & 1), lane == 0 && done);
+                batch += done;
             }
             const Tile t = tile_at(p, n);
             const int token0 = t.tokens * kTokens + static_cast<int>(rank) * kHalf + 32 * quarter;  // of the warp
@@ -409,9 +447,9 @@ int start(const Mul8Args& a, int sms, cudaStream_t stream) {
     const int unit = a.out_type == kOutF32 ? 4 : a.out_type == kOutE4m3 ? 16 : 8;
     p.stored = a.features / unit * unit;
     CUtensorMap tm_x, tm_w, tm_up, tm_out;
-    if (!mul8_map(&tm_x, a.x, a.k, a.n, a.x_stride, kHalf) || !mul8_map(&tm_w, a.w, a.k, a.features, a.w_stride, kHalf) || !out_map(&tm_out, a, p.stored)) return -7;
+    if (!mul8_map(&tm_x, a.x, a.k, a.n, a.x_stride, kHalf) || !mul8_map(&tm_w, a.w, a.k, a.features, a.w_stride, kHalf / 2) || !out_map(&tm_out, a, p.stored)) return -7;
     tm_up = tm_w;
-    if (kGated && !mul8_map(&tm_up, a.up, a.k, a.features, a.w_stride, kHalf)) return -7;
+    if (kGated && !mul8_map(&tm_up, a.up, a.k, a.features, a.w_stride, kHalf / 2)) return -7;
     g_launched.store(true, std::memory_order_relaxed);
     mul8_tiles_kernel<kGated><<<static_cast<unsigned>(2 * p.pairs), kThreads, kSmem, stream>>>(tm_x, tm_w, tm_up, tm_out, p);
     return cudaGetLastError() == cudaSuccess ? 0 : -7;
