@@ -283,32 +283,33 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0;
 #pragma unroll 1
-            for (int b = 0; b < p.k_blocks; ++b, ++i) {
-                const int j = b % kBatch;
-                if (j == 0) wait(sc_full + 8 * (batch & 1), (batch / 2) & 1);
-                const float* g = factors + ((batch & 1) * kBatch + j) * 2 * kHalf;
-                const float factor[2] = {g[0], kGated ? g[kHalf] : g[0]};
-                const bool done = j == kBatch - 1 || b + 1 == p.k_blocks;  // with these factors
-                const int u = i & 1;
-                wait(acc_full + 16 * u + 8 * half, (i / 2) & 1);
-                tc_fence_after();
-                const uint32_t from = mine + u * 256 + half * 128;
+            for (int b = 0; b < p.k_blocks; b += kBatch, ++batch) {
+                wait(sc_full + 8 * (batch & 1), (batch / 2) & 1);
+                const float* g = factors + (batch & 1) * kBatch * 2 * kHalf;
+                const int until = i + min(kBatch, p.k_blocks - b);
+#pragma unroll 1
+                for (; i < until; ++i, g += 2 * kHalf) {
+                    const float factor[2] = {g[0], kGated ? g[kHalf] : g[0]};
+                    const int u = i & 1;
+                    wait(acc_full + 16 * u + 8 * half, (i / 2) & 1);
+                    tc_fence_after();
+                    const uint32_t from = mine + u * 256 + half * 128;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float v[64];
-                    tmem_start64(from + q * 64, v);
-                    tmem_wait();
-                    if (q == 1) {
-                        tc_fence_before();
-                        arrive_cluster(released + 16 * u + 8 * half, lane == 0);
+                    for (int q = 0; q < 2; ++q) {
+                        float v[64];
+                        tmem_start64(from + q * 64, v);
+                        tmem_wait();
+                        if (q == 1) {
+                            tc_fence_before();
+                            arrive_cluster(released + 16 * u + 8 * half, lane == 0);
+                        }
+                        const uint64_t f = pair8(factor[q], factor[q]);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) add_scaled(acc[32 * q + e], v[2 * e], v[2 * e + 1], f);
                     }
-                    const uint64_t f = pair8(factor[q], factor[q]);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) add_scaled(acc[32 * q + e], v[2 * e], v[2 * e + 1], f);
                 }
                 __syncwarp();
-                arrive_if(sc_empty + 8 * (batch & 1), lane == 0 && done);
-                batch += done;
+                arrive_if(sc_empty + 8 * (batch & 1), lane == 0);
             }
             const Tile t = tile_at(p, n);
             const int token0 = t.tokens * kTokens + static_cast<int>(rank) * kHalf + 32 * quarter;  // of the warp
