@@ -293,32 +293,39 @@ mul8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     }
 }
 
-// CTAs of a cluster: the blocks of k cut so that the busiest SM has the least to do. A CTA's start and end cost about as much as
-// kStart blocks.
-int cluster_ctas(long long units, int k_blocks, int sms) {
-    constexpr long long kStart = 2;
-    int best = 1;
-    long long least = 1LL << 62;
-    for (int c = 1; c <= kMostCluster && c <= k_blocks; ++c) {
-        const long long each = (units * c + sms - 1) / sms, cost = each * ((k_blocks + c - 1) / c + kStart);
-        if (cost < least) {
-            least = cost;
-            best = c;
-        }
-    }
-    return best;
+// CTAs of a cluster: as many as let all clusters run at once, at least 2 blocks of k for each. One more and some clusters wait for others to
+// end, which costs more than fewer readers do: 20,480 x 5,120 weights (40 tiles) and one token 19.7 us in clusters of 4, 19.4 of 5,
+// 25.2 of 7 (all 8 parts of the GPU hold 4 clusters of 7, some 5); gate and up of 5,120 x 20,480 (160 tiles) 35.8 us in clusters of
+// 1, 42.3 of 2. `fit`: clusters of each size that run at once.
+int cluster_ctas(long long units, int k_blocks, const std::atomic<int>* fit) {
+    int c = 1;
+    for (int more = 2; more <= kMostCluster && 2 * more <= k_blocks; ++more)
+        if (units <= fit[more].load(std::memory_order_relaxed)) c = more;
+    return c;
 }
 
 template <int kN, bool kGated, int kPerSm>
-int start(const Mul8Args& a, int sms, cudaStream_t stream) {
+int start(const Mul8Args& a, cudaStream_t stream) {
     using P = Plan<kN, kGated, kPerSm>;
     static std::atomic<bool> ready[kMul8Devices];
-    if (!mul8_allow_smem(reinterpret_cast<const void*>(&mul8_rows_kernel<kN, kGated, kPerSm>), P::kSmem, ready)) return -7;
+    static std::atomic<int> fit[kMul8Devices][kMostCluster + 1];
+    const auto kernel = &mul8_rows_kernel<kN, kGated, kPerSm>;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMul8Devices) return -7;
+    if (!ready[dev].load(std::memory_order_acquire)) {  // once per device
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem) != cudaSuccess) return -7;
+        for (int c = 2; c <= kMostCluster; ++c) {
+            const int n = mul8_clusters(reinterpret_cast<const void*>(kernel), c, P::kThreads, P::kSmem);
+            if (n < 0) return -7;
+            fit[dev][c].store(n, std::memory_order_relaxed);
+        }
+        ready[dev].store(true, std::memory_order_release);
+    }
     Params p;
     p.a = a;
     p.k_blocks = blocks8(a.k);
     const long long token_tiles = (a.n + kN - 1) / kN, units = token_tiles * blocks8(a.features);
-    p.ctas = cluster_ctas(units, p.k_blocks, sms);
+    p.ctas = cluster_ctas(units, p.k_blocks, fit[dev]);
     if (units * p.ctas > 0x7FFFFFFFLL) return -7;
     p.token_tiles = static_cast<int>(token_tiles);
     CUtensorMap tm_x, tm_w, tm_up;
@@ -337,7 +344,7 @@ int start(const Mul8Args& a, int sms, cudaStream_t stream) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     g_launched.store(true, std::memory_order_relaxed);
-    return cudaLaunchKernelEx(&cfg, mul8_rows_kernel<kN, kGated, kPerSm>, tm_x, tm_w, tm_up, p) == cudaSuccess ? 0 : -7;
+    return cudaLaunchKernelEx(&cfg, kernel, tm_x, tm_w, tm_up, p) == cudaSuccess ? 0 : -7;
 }
 
 }  // namespace
@@ -364,6 +371,21 @@ bool mul8_map(CUtensorMap* m, const void* base, long long cols, long long rows, 
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+int mul8_clusters(const void* kernel, int ctas, int threads, int smem) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : -1;
+}
+
 bool mul8_allow_smem(const void* kernel, int bytes, std::atomic<bool>* ready) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMul8Devices) return false;
@@ -374,19 +396,17 @@ bool mul8_allow_smem(const void* kernel, int bytes, std::atomic<bool>* ready) {
 }
 
 int launch_mul8(const Mul8Args& a, cudaStream_t stream) {
-    const int sms = attn_sm_count();
-    if (sms < 1) return -7;
     if (a.n > 256) return launch_mul8_tiles(a, stream);
     if (a.up) {
-        if (a.n <= 16) return start<16, true, 2>(a, sms, stream);
-        if (a.n <= 32) return start<32, true, 2>(a, sms, stream);
-        if (a.n <= 64) return start<64, true, 1>(a, sms, stream);
-        return start<128, true, 1>(a, sms, stream);
+        if (a.n <= 16) return start<16, true, 2>(a, stream);
+        if (a.n <= 32) return start<32, true, 2>(a, stream);
+        if (a.n <= 64) return start<64, true, 1>(a, stream);
+        return start<128, true, 1>(a, stream);
     }
-    if (a.n <= 16) return start<16, false, 2>(a, sms, stream);
-    if (a.n <= 32) return start<32, false, 2>(a, sms, stream);
-    if (a.n <= 64) return start<64, false, 2>(a, sms, stream);
-    return start<128, false, 1>(a, sms, stream);
+    if (a.n <= 16) return start<16, false, 2>(a, stream);
+    if (a.n <= 32) return start<32, false, 2>(a, stream);
+    if (a.n <= 64) return start<64, false, 2>(a, stream);
+    return start<128, false, 1>(a, stream);
 }
 
 int read_mul8_error(unsigned int* word, int clear, cudaStream_t stream) {

@@ -15,6 +15,9 @@ PFN_cuTensorMapEncodeTiled_v12000 mul8_encode();
 // A tensor map of 8-bit rows (`cols` bytes, `stride` bytes apart) whose box is 128 columns by box_rows, 128-byte swizzle, zeros outside.
 bool mul8_map(CUtensorMap* m, const void* base, long long cols, long long rows, long long stride, int box_rows);
 
+// Clusters of `ctas` CTAs of a kernel that run at once on the current device; -1 if that cannot be told.
+int mul8_clusters(const void* kernel, int ctas, int threads, int smem);
+
 // Lets a kernel use `bytes` of shared memory, once per device; `ready` has kMul8Devices entries.
 bool mul8_allow_smem(const void* kernel, int bytes, std::atomic<bool>* ready);
 
