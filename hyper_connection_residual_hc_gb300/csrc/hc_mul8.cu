@@ -45,6 +45,7 @@ struct Plan {
     static constexpr int kSets = kN > 64 ? 2 : 1;             // sets of 4 warps that share the tokens
     static constexpr int kCols = kN / kSets;                  // of a thread
     static constexpr int kAddWarps = 4 * kSets;
+    static constexpr int kAhead = kMats * kCols < 128 ? 1 : 0;  // loads of 16 columns ahead of their use, where registers allow it
     static constexpr int kThreads = 32 * (kAddWarps + 2);
     static constexpr int kW = kTile * kBlock8;                // bytes
     static constexpr int kX = kN * kBlock8;
@@ -190,19 +191,25 @@ mul8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
             const uint32_t from = tmem + (static_cast<uint32_t>(32 * (warp % 4)) << 16) + u * P::kBuffer + set * P::kCols;
             const float* f = scales + ((group & 1) * P::kMats * kGroup + i % kGroup) * kN + set * P::kCols;
             constexpr int kParts = P::kCols / 16;
-            float v[2][16];
-            tmem_start16(from, v[0]);
+            float v[P::kAhead + 1][16];
+            if constexpr (P::kAhead) tmem_start16(from, v[0]);
 #pragma unroll
             for (int q = 0; q < kParts * P::kMats; ++q) {
                 const int m = q / kParts, c = q % kParts;
-                tmem_wait();
-                if (q + 1 < kParts * P::kMats) tmem_start16(from + ((q + 1) / kParts) * kN + 16 * ((q + 1) % kParts), v[(q + 1) % 2]);
+                if constexpr (P::kAhead) {
+                    tmem_wait();
+                    if (q + 1 < kParts * P::kMats) tmem_start16(from + ((q + 1) / kParts) * kN + 16 * ((q + 1) % kParts), v[(q + 1) % 2]);
+                } else {
+                    tmem_start16(from + m * kN + 16 * c, v[0]);
+                    tmem_wait();
+                }
+                const float(&w)[16] = v[P::kAhead ? q % 2 : 0];
                 const float4* g = reinterpret_cast<const float4*>(f + m * kGroup * kN + 16 * c);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float4 s = g[j];
-                    add_scaled(acc[m][8 * c + 2 * j], v[q % 2][4 * j], v[q % 2][4 * j + 1], pair8(s.x, s.y));
-                    add_scaled(acc[m][8 * c + 2 * j + 1], v[q % 2][4 * j + 2], v[q % 2][4 * j + 3], pair8(s.z, s.w));
+                    add_scaled(acc[m][8 * c + 2 * j], w[4 * j], w[4 * j + 1], pair8(s.x, s.y));
+                    add_scaled(acc[m][8 * c + 2 * j + 1], w[4 * j + 2], w[4 * j + 3], pair8(s.z, s.w));
                 }
             }
             tc_fence_before();
@@ -304,48 +311,91 @@ int cluster_ctas(long long units, int k_blocks, const std::atomic<int>* fit) {
     return c;
 }
 
+// How a call would run with tiles of kN tokens, and about how long it would take, in ns: the weights' bytes or the busiest SM's blocks (kBlockNs each),
+// a start and an end, and the join of a cluster's parts. Measured (us, model in brackets): 128 tokens by 20,480 x 5,120 27.4 (27), by
+// 5,120 x 5,120 11.2 (11); gated, 64 tokens by 5,120 x 20,480 50.8 (48), 128 tokens by 1,024 x 512 10.8 (10).
+struct RowsPlan {
+    long long token_tiles, units;
+    int ctas;
+    long long ns;
+};
+template <int kN, bool kGated>
+constexpr int kBlockNs = kGated ? (kN == 128 ? 1000 : kN == 64 ? 550 : 250) : (kN == 128 ? 400 : 200);
+
 template <int kN, bool kGated, int kPerSm>
-int start(const Mul8Args& a, cudaStream_t stream) {
+struct Rows {
     using P = Plan<kN, kGated, kPerSm>;
-    static std::atomic<bool> ready[kMul8Devices];
-    static std::atomic<int> fit[kMul8Devices][kMostCluster + 1];
-    const auto kernel = &mul8_rows_kernel<kN, kGated, kPerSm>;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMul8Devices) return -7;
-    if (!ready[dev].load(std::memory_order_acquire)) {  // once per device
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem) != cudaSuccess) return -7;
-        for (int c = 2; c <= kMostCluster; ++c) {
-            const int n = mul8_clusters(reinterpret_cast<const void*>(kernel), c, P::kThreads, P::kSmem);
-            if (n < 0) return -7;
-            fit[dev][c].store(n, std::memory_order_relaxed);
+
+    // Clusters of each size that run at once, found once per device; null if that failed.
+    static const std::atomic<int>* fit() {
+        static std::atomic<bool> ready[kMul8Devices];
+        static std::atomic<int> fits[kMul8Devices][kMostCluster + 1];
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMul8Devices) return nullptr;
+        if (!ready[dev].load(std::memory_order_acquire)) {
+            const auto kernel = &mul8_rows_kernel<kN, kGated, kPerSm>;
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem) != cudaSuccess) return nullptr;
+            for (int c = 2; c <= kMostCluster; ++c) {
+                const int n = mul8_clusters(reinterpret_cast<const void*>(kernel), c, P::kThreads, P::kSmem);
+                if (n < 0) return nullptr;
+                fits[dev][c].store(n, std::memory_order_relaxed);
+            }
+            ready[dev].store(true, std::memory_order_release);
         }
-        ready[dev].store(true, std::memory_order_release);
+        return fits[dev];
     }
-    Params p;
-    p.a = a;
-    p.k_blocks = blocks8(a.k);
-    const long long token_tiles = (a.n + kN - 1) / kN, units = token_tiles * blocks8(a.features);
-    p.ctas = cluster_ctas(units, p.k_blocks, fit[dev]);
-    if (units * p.ctas > 0x7FFFFFFFLL) return -7;
-    p.token_tiles = static_cast<int>(token_tiles);
-    CUtensorMap tm_x, tm_w, tm_up;
-    if (!mul8_map(&tm_x, a.x, a.k, a.n, a.x_stride, kN) || !mul8_map(&tm_w, a.w, a.k, a.features, a.w_stride, kTile)) return -7;
-    tm_up = tm_w;
-    if (kGated && !mul8_map(&tm_up, a.up, a.k, a.features, a.w_stride, kTile)) return -7;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(units * p.ctas));
-    cfg.blockDim = dim3(P::kThreads);
-    cfg.dynamicSmemBytes = P::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(p.ctas);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    g_launched.store(true, std::memory_order_relaxed);
-    return cudaLaunchKernelEx(&cfg, kernel, tm_x, tm_w, tm_up, p) == cudaSuccess ? 0 : -7;
-}
+
+    static bool plan(const Mul8Args& a, int sms, RowsPlan* r) {
+        const std::atomic<int>* f = fit();
+        if (!f) return false;
+        const int k_blocks = blocks8(a.k);
+        r->token_tiles = (a.n + kN - 1) / kN;
+        r->units = r->token_tiles * blocks8(a.features);
+        r->ctas = cluster_ctas(r->units, k_blocks, f);
+        const long long bytes_ns = static_cast<long long>(P::kMats) * a.features * a.k / 6200;
+        const long long block_ns = (r->units * r->ctas + sms - 1) / sms * ((k_blocks + r->ctas - 1) / r->ctas) * kBlockNs<kN, kGated>;
+        r->ns = 4000 + (bytes_ns > block_ns ? bytes_ns : block_ns) + (r->ctas > 1 ? 15 * kN * P::kMats : 0);
+        return true;
+    }
+
+    static int run(const Mul8Args& a, const RowsPlan& r, cudaStream_t stream) {
+        if (r.units * r.ctas > 0x7FFFFFFFLL) return -7;
+        Params p;
+        p.a = a;
+        p.k_blocks = blocks8(a.k);
+        p.token_tiles = static_cast<int>(r.token_tiles);
+        p.ctas = r.ctas;
+        CUtensorMap tm_x, tm_w, tm_up;
+        if (!mul8_map(&tm_x, a.x, a.k, a.n, a.x_stride, kN) || !mul8_map(&tm_w, a.w, a.k, a.features, a.w_stride, kTile)) return -7;
+        tm_up = tm_w;
+        if (kGated && !mul8_map(&tm_up, a.up, a.k, a.features, a.w_stride, kTile)) return -7;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(r.units * r.ctas));
+        cfg.blockDim = dim3(P::kThreads);
+        cfg.dynamicSmemBytes = P::kSmem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = static_cast<unsigned>(r.ctas);
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        g_launched.store(true, std::memory_order_relaxed);
+        return cudaLaunchKernelEx(&cfg, &mul8_rows_kernel<kN, kGated, kPerSm>, tm_x, tm_w, tm_up, p) == cudaSuccess ? 0 : -7;
+    }
+
+    // The shorter of this and the pairs' kernel.
+    static int choose(const Mul8Args& a, int sms, cudaStream_t stream) {
+        RowsPlan r;
+        if (!plan(a, sms, &r)) return -7;
+        if (a.n > 32) {
+            const long long tiles = mul8_tiles_ns(a);
+            if (tiles < 0) return -7;
+            if (tiles < r.ns) return launch_mul8_tiles(a, stream);
+        }
+        return run(a, r, stream);
+    }
+};
 
 }  // namespace
 
@@ -386,27 +436,19 @@ int mul8_clusters(const void* kernel, int ctas, int threads, int smem) {
     return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : -1;
 }
 
-bool mul8_allow_smem(const void* kernel, int bytes, std::atomic<bool>* ready) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMul8Devices) return false;
-    if (ready[dev].load(std::memory_order_acquire)) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-    ready[dev].store(true, std::memory_order_release);
-    return true;
-}
-
 int launch_mul8(const Mul8Args& a, cudaStream_t stream) {
-    if (a.n > 256) return launch_mul8_tiles(a, stream);
+    const int sms = attn_sm_count();
+    if (sms < 1) return -7;
     if (a.up) {
-        if (a.n <= 16) return start<16, true, 2>(a, stream);
-        if (a.n <= 32) return start<32, true, 2>(a, stream);
-        if (a.n <= 64) return start<64, true, 1>(a, stream);
-        return start<128, true, 1>(a, stream);
+        if (a.n <= 16) return Rows<16, true, 2>::choose(a, sms, stream);
+        if (a.n <= 32) return Rows<32, true, 2>::choose(a, sms, stream);
+        if (a.n <= 64) return Rows<64, true, 2>::choose(a, sms, stream);
+        return Rows<128, true, 1>::choose(a, sms, stream);
     }
-    if (a.n <= 16) return start<16, false, 2>(a, stream);
-    if (a.n <= 32) return start<32, false, 2>(a, stream);
-    if (a.n <= 64) return start<64, false, 2>(a, stream);
-    return start<128, false, 1>(a, stream);
+    if (a.n <= 16) return Rows<16, false, 2>::choose(a, sms, stream);
+    if (a.n <= 32) return Rows<32, false, 2>::choose(a, sms, stream);
+    if (a.n <= 64) return Rows<64, false, 2>::choose(a, sms, stream);
+    return Rows<128, false, 1>::choose(a, sms, stream);
 }
 
 int read_mul8_error(unsigned int* word, int clear, cudaStream_t stream) {

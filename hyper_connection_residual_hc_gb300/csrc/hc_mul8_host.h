@@ -1,7 +1,6 @@
 // Host helpers that the launchers of the 8-bit products share.
 #pragma once
 
-#include <atomic>
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -17,8 +16,5 @@ bool mul8_map(CUtensorMap* m, const void* base, long long cols, long long rows, 
 
 // Clusters of `ctas` CTAs of a kernel that run at once on the current device; -1 if that cannot be told.
 int mul8_clusters(const void* kernel, int ctas, int threads, int smem);
-
-// Lets a kernel use `bytes` of shared memory, once per device; `ready` has kMul8Devices entries.
-bool mul8_allow_smem(const void* kernel, int bytes, std::atomic<bool>* ready);
 
 }  // namespace hc

@@ -20,8 +20,8 @@
 
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
 
-#include "hc_attn.h"
 #include "hc_ffn.h"
 #include "hc_mul8_dev.cuh"
 #include "hc_mul8_host.h"
@@ -52,9 +52,10 @@ constexpr int kBand = 8;                         // token tiles that go through 
 
 struct Params {
     Mul8Args a;
-    int k_blocks, token_tiles, feature_tiles, pairs;
+    int k_blocks, token_tiles, feature_tiles;
+    int pairs;   // of the grid, which take tiles in turn; with kSplit the pairs of a cluster, which share one tile's blocks of k
     int stored;  // features that TMA stores: whole 16 bytes of a row
-    long long tiles;
+    long long first, until;  // tiles
 };
 
 __device__ __forceinline__ void tmem_alloc2(uint32_t dst, uint32_t ncols) {
@@ -73,14 +74,13 @@ __device__ __forceinline__ void mma8_pair(uint32_t lead, uint32_t d, uint64_t a,
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
         : "memory");
 }
-// Arrives on the barrier at this offset in both CTAs.
-__device__ __forceinline__ void commit8_pair(uint32_t lead, uint32_t bar) {
+// Arrives on the barrier at this offset in both CTAs of the pair (`both`: their bits).
+__device__ __forceinline__ void commit8_pair(uint32_t lead, uint32_t bar, uint16_t both) {
     asm volatile(
-        "{\n\t.reg .pred q;\n\t.reg .b16 m;\n\t"
+        "{\n\t.reg .pred q;\n\t"
         "setp.ne.b32 q, %1, 0;\n\t"
-        "mov.b16 m, 3;\n\t"
-        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar),
-        "r"(lead)
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(bar),
+        "r"(lead), "h"(both)
         : "memory");
 }
 // Into this CTA's shared memory, completing on a barrier of either CTA (`bar`: an address in the cluster's window).
@@ -145,8 +145,134 @@ __device__ __forceinline__ Tile tile_at(const Params& p, long long i) {
     return {first + r % rows, r / rows};
 }
 
+__device__ __forceinline__ float ld_cluster_f1(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// With kSplit, by the adding warps of all pairs of the cluster: their sums of a tile are added up in the order of the pairs. Each
+// thread puts its columns into shared memory, over the ring (the last block's MMAs are done, so all copies are), 4 at a time:
+// [column / 4][token][4]. Then
+// the columns are dealt out 16 at a time: a pair takes every p.pairs-th of each half (of a gated product 16 features with their 16
+// columns of up), reads them from all pairs and writes the result.
 template <bool kGated>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__device__ __forceinline__ void join_parts(const Params& p, const Tile& t, const uint64_t (&acc)[64], uint32_t base, unsigned char* at, int half, int in_cta,
+                                           int rank, int pair) {
+    float4* part = reinterpret_cast<float4*>(at) + half * kHalf * kHalf / 4 + in_cta;
+    static_assert(2 * kHalf * kHalf * 4 + 2 * kHalf * 4 <= kStages * kStage, "the sums and the largest magnitudes take the ring's place");
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        float4 v;
+        unpair8(acc[2 * j], v.x, v.y);
+        unpair8(acc[2 * j + 1], v.z, v.w);
+        part[j * kHalf] = v;
+    }
+    cluster_sync8();
+    const long long row = static_cast<long long>(t.tokens) * kTokens + rank * kHalf + in_cta;
+    const bool has = row < p.a.n;
+    // the sums of columns c .. c + 15 of this half
+    auto columns = [&](int c, float (&s)[16]) {
+        const uint32_t mine = base + static_cast<uint32_t>(((half * kHalf + c) / 4 * kHalf + in_cta) * 16);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = 0.f;
+        for (int r = 0; r < p.pairs; ++r) {
+            const uint32_t from = mapa8(mine, static_cast<uint32_t>(2 * r + rank));
+            float4 v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = ld_cluster_f4(from + static_cast<uint32_t>(e * kHalf * 16));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[4 * e] += v[e].x;
+                s[4 * e + 1] += v[e].y;
+                s[4 * e + 2] += v[e].z;
+                s[4 * e + 3] += v[e].w;
+            }
+        }
+    };
+    if constexpr (kGated) {
+        float h[4][16];
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c % p.pairs != pair) continue;
+            float g[16], u[16];
+            columns(16 * c, g);
+            columns(64 + 16 * c, u);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                h[c][e] = activate8(g[e], p.a.act) * u[e];
+                top = max_nan(top, fabsf(h[c][e]));  // (features past the last are 0)
+            }
+        }
+        const bool codes = p.a.out_type == kOutE4m3;
+        float up = 1.f;
+        if (codes) {  // the token's largest of all 128 features
+            const uint32_t tops = 2 * kHalf * kHalf * 4;
+            *reinterpret_cast<float*>(at + tops + (half * kHalf + in_cta) * 4) = top;
+            cluster_sync8();
+            top = kLeastTop8;
+            for (int r = 0; r < p.pairs; ++r)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) top = max_nan(top, ld_cluster_f1(mapa8(base + tops + static_cast<uint32_t>((g * kHalf + in_cta) * 4), static_cast<uint32_t>(2 * r + rank))));
+            up = kTop8 / top;
+            if (pair == 0 && half == 0 && has) p.a.out_scales[row * p.feature_tiles + t.features] = top / kTop8;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int f = t.features * kHalf + 64 * half + 16 * c;
+            if (c % p.pairs != pair || f >= p.a.features || !has) continue;
+            if (codes) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = e4m3x4(h[c][4 * e] * up, h[c][4 * e + 1] * up, h[c][4 * e + 2] * up, h[c][4 * e + 3] * up);
+                *reinterpret_cast<uint4*>(static_cast<unsigned char*>(p.a.out) + row * p.a.out_stride + f) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = bf16x2(h[c][2 * e], h[c][2 * e + 1]);
+                uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + row * p.a.out_stride + f);
+                o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        }
+    } else {
+        for (int c = pair; c < 8; c += p.pairs) {
+            const int f = t.features * kRowsW + kHalf * half + 16 * c, left = p.a.features - f;
+            if (left <= 0) break;
+            float s[16];
+            columns(16 * c, s);
+            if (!has) continue;
+            const long long o = row * p.a.out_stride + f;
+            if (p.a.out_type == kOutF32) {
+                float* to = static_cast<float*>(p.a.out) + o;
+                if (left >= 16) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) reinterpret_cast<float4*>(to)[e] = make_float4(s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (e < left) to[e] = s[e];
+                }
+            } else {
+                __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.a.out) + o;
+                if (left >= 16) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        reinterpret_cast<uint4*>(to)[e] = make_uint4(bf16x2(s[8 * e], s[8 * e + 1]), bf16x2(s[8 * e + 2], s[8 * e + 3]),
+                                                                     bf16x2(s[8 * e + 4], s[8 * e + 5]), bf16x2(s[8 * e + 6], s[8 * e + 7]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (e < left) to[e] = __float2bfloat16_rn(s[e]);
+                }
+            }
+        }
+    }
+}
+
+template <bool kGated, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1)
 mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_up,
                   const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ Params p) {
     extern __shared__ unsigned char raw[];
@@ -156,8 +282,11 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     const uint32_t full = base + kBars, empty = full + 8 * kStages, acc_full = empty + 8 * kStages, acc_empty = acc_full + 32, sc_full = acc_empty + 32, sc_empty = sc_full + 16, slot = sc_empty + 16;
     volatile uint32_t* abort_word = reinterpret_cast<volatile uint32_t*>(at + (slot + 4 - base));
     const Wait8 wait{abort_word, &g_hc_mul8_tiles_error};
-    const uint32_t rank = cluster_ctarank8();
-    const int pair = static_cast<int>(blockIdx.x) / 2;
+    const uint32_t in_cluster = cluster_ctarank8(), rank = in_cluster & 1, leader = in_cluster & ~1u;
+    const int pair = kSplit ? static_cast<int>(in_cluster) / 2 : 0;  // of those that share a tile
+    // tiles n0, n0 + step, ...; blocks k0 .. k1 - 1 of each
+    const long long n0 = p.first + (kSplit ? blockIdx.x / (2 * p.pairs) : blockIdx.x / 2), step = kSplit ? p.until : p.pairs;
+    const int k0 = kSplit ? p.k_blocks * pair / p.pairs : 0, k1 = kSplit ? p.k_blocks * (pair + 1) / p.pairs : p.k_blocks;
 
     if (warp == kMmaWarp) {
         tmem_alloc2(slot, 512);
@@ -187,21 +316,21 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     if (warp >= kAddWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kLoadWarp && lane == 0) {  // ---- loads
-            const uint32_t first_full = mapa8(full, 0);
+            const uint32_t first_full = mapa8(full, leader);
             int i = 0;  // blocks so far
-            for (long long n = pair; n < p.tiles; n += p.pairs) {
+            for (long long n = n0; n < p.until; n += step) {
                 const Tile t = tile_at(p, n);
                 const int token = t.tokens * kTokens + static_cast<int>(rank) * kHalf;
-                const int row = kGated ? t.features * kHalf : t.features * kRowsW + static_cast<int>(rank) * 64, step = kGated ? 64 : kHalf;
+                const int row = kGated ? t.features * kHalf : t.features * kRowsW + static_cast<int>(rank) * 64, next = kGated ? 64 : kHalf;
                 const CUtensorMap* w = kGated && rank ? &tm_up : &tm_w;
-                for (int b = 0; b < p.k_blocks; ++b, ++i) {
+                for (int b = k0; b < k1; ++b, ++i) {
                     const int s = i % kStages;
                     if (i >= kStages) wait(empty + 8 * s, (i / kStages - 1) & 1);
                     if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, 2 * kStage);
                     const uint32_t st = base + s * kStage;
                     tma_load_pair(st, &tm_x, first_full + 8 * s, b * kBlock8, token);
                     tma_load_pair(st + kOperand, w, first_full + 8 * s, b * kBlock8, row);
-                    tma_load_pair(st + kOperand + kOperand / 2, w, first_full + 8 * s, b * kBlock8, row + step);
+                    tma_load_pair(st + kOperand + kOperand / 2, w, first_full + 8 * s, b * kBlock8, row + next);
                 }
             }
             // no copy of either CTA is in flight when the pair ends, whatever happened
@@ -209,10 +338,11 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 for (int j = max(i - kStages, 0); j < i; ++j) wait.drain(full + 8 * (j % kStages), (j / kStages) & 1);
         } else if (warp == kMmaWarp && rank == 0) {  // ---- MMAs
             const uint32_t lead = elect_one();
+            const uint16_t both = static_cast<uint16_t>(3u << leader);
             constexpr uint32_t idesc = idesc8(256, 128);
             int i = 0;
-            for (long long n = pair; n < p.tiles; n += p.pairs) {
-                for (int b = 0; b < p.k_blocks; ++b, ++i) {
+            for (long long n = n0; n < p.until; n += step) {
+                for (int b = k0; b < k1; ++b, ++i) {
                     const int s = i % kStages, u = i & 1;
                     wait(full + 8 * s, (i / kStages) & 1);
                     const uint32_t st = base + s * kStage;
@@ -224,9 +354,9 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                         const uint64_t x = sdesc8(st), w = sdesc8(st + kOperand + h * (kOperand / 2));
 #pragma unroll
                         for (int q = 0; q < 4; ++q) mma8_pair(lead, d, x + 2 * q, w + 2 * q, idesc, q > 0);
-                        commit8_pair(lead, acc_full + 16 * u + 8 * h);
+                        commit8_pair(lead, acc_full + 16 * u + 8 * h, both);
                     }
-                    commit8_pair(lead, empty + 8 * s);
+                    commit8_pair(lead, empty + 8 * s, both);
                 }
             }
             if (i > 0) wait.drain(acc_full + 16 * ((i - 1) & 1) + 8, ((i - 1) / 2) & 1);
@@ -234,7 +364,7 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             // The factors of the CTA's 128 tokens, 2 to a lane, with the weights of either half of the columns (gate and up). Tokens and
             // features outside the matrices take the last ones inside (their sums are not stored).
             int batch = 0;
-            for (long long n = pair; n < p.tiles; n += p.pairs) {
+            for (long long n = n0; n < p.until; n += step) {
                 const Tile t = tile_at(p, n);
                 const int in_cta = 64 * (warp - kMmaWarp - 1) + lane;
                 const long long token = static_cast<long long>(t.tokens) * kTokens + rank * kHalf + in_cta;
@@ -244,7 +374,7 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 const float* w0 = p.a.w_scales + static_cast<long long>(min(kGated ? t.features : 2 * t.features, most)) * p.k_blocks;
                 const float* w1 = kGated ? p.a.up_scales + static_cast<long long>(t.features) * p.k_blocks
                                          : p.a.w_scales + static_cast<long long>(min(2 * t.features + 1, most)) * p.k_blocks;
-                for (int b = 0; b < p.k_blocks; b += kBatch, ++batch) {
+                for (int b = k0; b < k1; b += kBatch, ++batch) {
                     if (batch >= 2) wait(sc_empty + 8 * (batch & 1), (batch / 2 - 1) & 1);
                     float* o = reinterpret_cast<float*>(at + kScales) + (batch & 1) * kBatch * 2 * kHalf + in_cta;
 #pragma unroll
@@ -252,7 +382,7 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                         float x[2][4], w[2][4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int from = min(b + j0 + j, p.k_blocks - 1);
+                            const int from = min(b + j0 + j, k1 - 1);
                             x[0][j] = __ldg(x0 + from);
                             x[1][j] = __ldg(x1 + from);
                             w[0][j] = __ldg(w0 + from);
@@ -274,19 +404,19 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         const int half = warp / 4, quarter = warp % 4;
         const int in_cta = 32 * quarter + lane;  // token
         const uint32_t mine = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-        const uint32_t released = mapa8(acc_empty, 0);
+        const uint32_t released = mapa8(acc_empty, leader);
         const uint32_t out_smem = base + kOut + warp * kOutWarp;
         const float* factors = reinterpret_cast<const float*>(at + kScales) + (kGated ? 0 : half * kHalf) + in_cta;
         int i = 0, batch = 0, turn = 0;
-        for (long long n = pair; n < p.tiles; n += p.pairs, ++turn) {
+        for (long long n = n0; n < p.until; n += step, ++turn) {
             uint64_t acc[64];  // pairs of columns: 128 features, or 64 of the gate and 64 of up
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = 0;
 #pragma unroll 1
-            for (int b = 0; b < p.k_blocks; b += kBatch, ++batch) {
+            for (int b = k0; b < k1; b += kBatch, ++batch) {
                 wait(sc_full + 8 * (batch & 1), (batch / 2) & 1);
                 const float* g = factors + (batch & 1) * kBatch * 2 * kHalf;
-                const int until = i + min(kBatch, p.k_blocks - b);
+                const int until = i + min(kBatch, k1 - b);
 #pragma unroll 1
                 for (; i < until; ++i, g += 2 * kHalf) {
                     const float factor[2] = {g[0], kGated ? g[kHalf] : g[0]};
@@ -313,6 +443,10 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             }
             const Tile t = tile_at(p, n);
             const int token0 = t.tokens * kTokens + static_cast<int>(rank) * kHalf + 32 * quarter;  // of the warp
+            if constexpr (kSplit) {
+                join_parts<kGated>(p, t, acc, base, at, half, in_cta, static_cast<int>(rank), pair);
+                break;
+            }
             // Stages 128 bytes of each of the warp's 32 rows (a lane's words w, 16 bytes at a time, swizzled as the map says) and stores
             // them at column x.
             auto store = [&](const uint32_t* w, int bytes, int x) {
@@ -410,8 +544,14 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 }
             }
         }
-        if (lane == 0) bulk_wait<0>();
-        __syncwarp();
+        if constexpr (!kSplit) {
+            if (lane == 0) bulk_wait<0>();
+            __syncwarp();
+        }
+    }
+    if (kSplit && warp >= kAddWarps) {  // (the other warps' barriers are in join_parts)
+        cluster_sync8();
+        if (kGated && p.a.out_type == kOutE4m3) cluster_sync8();
     }
     tc_fence_before();
     cluster_sync8();  // nothing of this pair is in flight any more
@@ -434,34 +574,143 @@ bool out_map(CUtensorMap* m, const Mul8Args& a, int stored) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// How the tiles go to pairs: as many as fill all pairs a whole number of times are taken whole, and so are the others unless sharing
+// each of them between the pairs of a cluster is shorter (they are few then: the clusters run at once). In blocks of k: a tile's
+// start and end cost about as much as kEnds, joining kJoin more, another launch kLaunch. `fit`: clusters of 1 to 4 pairs that run at once.
+constexpr int kMostPairs = 4;
+constexpr int kEnds = 6, kJoin = 11, kLaunch = 16;
+struct Schedule {
+    long long whole;  // tiles
+    int split;        // pairs that share each of the others; 1: none are left
+};
+Schedule schedule(long long tiles, int k_blocks, const std::atomic<int>* fit) {
+    const int pairs = fit[1].load(std::memory_order_relaxed);
+    const long long whole = tiles / pairs * pairs, rest = tiles - whole;
+    Schedule best = {tiles, 1};
+    int least = k_blocks + kEnds;  // of another turn
+    for (int s = 2; s <= kMostPairs && 2 * s <= k_blocks && rest > 0; ++s) {
+        const int cost = (k_blocks + s - 1) / s + kEnds + kJoin + (whole > 0 ? kLaunch : 0);
+        if (rest <= fit[s].load(std::memory_order_relaxed) && cost < least) {
+            least = cost;
+            best = {whole, s};
+        }
+    }
+    return best;
+}
+
+struct Maps {
+    CUtensorMap x, w, up, out;
+};
+
+template <bool kGated, bool kSplit>
+cudaError_t start(const Maps& m, const Params& p, unsigned ctas, int cluster, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, &mul8_tiles_kernel<kGated, kSplit>, m.x, m.w, m.up, m.out, p);
+}
+
+// Clusters of 1 to kMostPairs pairs that run at once, found once per device; null if that failed.
 template <bool kGated>
-int start(const Mul8Args& a, int sms, cudaStream_t stream) {
+const std::atomic<int>* fits() {
     static std::atomic<bool> ready[kMul8Devices];
-    if (!mul8_allow_smem(reinterpret_cast<const void*>(&mul8_tiles_kernel<kGated>), kSmem, ready)) return -7;
+    static std::atomic<int> fit[kMul8Devices][kMostPairs + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMul8Devices) return nullptr;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        const void* const whole = reinterpret_cast<const void*>(&mul8_tiles_kernel<kGated, false>);
+        const void* const shared = reinterpret_cast<const void*>(&mul8_tiles_kernel<kGated, true>);
+        for (const void* k : {whole, shared})
+            if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return nullptr;
+        for (int c = 1; c <= kMostPairs; ++c) {
+            const int n = mul8_clusters(c == 1 ? whole : shared, 2 * c, kThreads, kSmem);
+            if (n < (c == 1 ? 1 : 0)) return nullptr;
+            fit[dev][c].store(n, std::memory_order_relaxed);
+        }
+        ready[dev].store(true, std::memory_order_release);
+    }
+    return fit[dev];
+}
+
+struct Shape {
+    int token_tiles, feature_tiles;
+    long long tiles;
+};
+Shape shape_of(const Mul8Args& a) {
+    Shape s;
+    const int wide = a.up ? kHalf : kRowsW;
+    s.token_tiles = static_cast<int>((a.n + kTokens - 1) / kTokens);
+    s.feature_tiles = (a.features + wide - 1) / wide;
+    s.tiles = static_cast<long long>(s.token_tiles) * s.feature_tiles;
+    return s;
+}
+
+template <bool kGated>
+int start(const Mul8Args& a, cudaStream_t stream) {
+    const std::atomic<int>* fit = fits<kGated>();
+    if (!fit) return -7;
     Params p;
     p.a = a;
     p.k_blocks = blocks8(a.k);
-    p.token_tiles = static_cast<int>((a.n + kTokens - 1) / kTokens);
-    p.feature_tiles = (a.features + (kGated ? kHalf : kRowsW) - 1) / (kGated ? kHalf : kRowsW);
-    p.tiles = static_cast<long long>(p.token_tiles) * p.feature_tiles;
-    p.pairs = static_cast<int>(p.tiles < sms / 2 ? p.tiles : sms / 2);
+    const Shape shape = shape_of(a);
+    p.token_tiles = shape.token_tiles;
+    p.feature_tiles = shape.feature_tiles;
     const int unit = a.out_type == kOutF32 ? 4 : a.out_type == kOutE4m3 ? 16 : 8;
     p.stored = a.features / unit * unit;
-    CUtensorMap tm_x, tm_w, tm_up, tm_out;
-    if (!mul8_map(&tm_x, a.x, a.k, a.n, a.x_stride, kHalf) || !mul8_map(&tm_w, a.w, a.k, a.features, a.w_stride, kHalf / 2) || !out_map(&tm_out, a, p.stored)) return -7;
-    tm_up = tm_w;
-    if (kGated && !mul8_map(&tm_up, a.up, a.k, a.features, a.w_stride, kHalf / 2)) return -7;
+    Maps m;
+    if (!mul8_map(&m.x, a.x, a.k, a.n, a.x_stride, kHalf) || !mul8_map(&m.w, a.w, a.k, a.features, a.w_stride, kHalf / 2) || !out_map(&m.out, a, p.stored))
+        return -7;
+    m.up = m.w;
+    if (kGated && !mul8_map(&m.up, a.up, a.k, a.features, a.w_stride, kHalf / 2)) return -7;
+    const long long tiles = shape.tiles;
+    const Schedule plan = schedule(tiles, p.k_blocks, fit);
     g_launched.store(true, std::memory_order_relaxed);
-    mul8_tiles_kernel<kGated><<<static_cast<unsigned>(2 * p.pairs), kThreads, kSmem, stream>>>(tm_x, tm_w, tm_up, tm_out, p);
-    return cudaGetLastError() == cudaSuccess ? 0 : -7;
+    if (plan.whole > 0) {
+        p.first = 0;
+        p.until = plan.whole;
+        const long long pairs = fit[1].load(std::memory_order_relaxed);
+        p.pairs = static_cast<int>(plan.whole < pairs ? plan.whole : pairs);
+        if (start<kGated, false>(m, p, static_cast<unsigned>(2 * p.pairs), 2, stream) != cudaSuccess) return -7;
+    }
+    if (plan.whole < tiles) {
+        p.first = plan.whole;
+        p.until = tiles;
+        p.pairs = plan.split;
+        if (start<kGated, true>(m, p, static_cast<unsigned>((tiles - plan.whole) * 2 * plan.split), 2 * plan.split, stream) != cudaSuccess) return -7;
+    }
+    return 0;
 }
 
 }  // namespace
 
+// In blocks of kBlockNs; with one token tile what runs at once reads weights of its own, and the more of it the longer a block takes.
+// Measured (us, model in brackets): 256 tokens by 20,480 x 5,120 30.8 (29), by 5,120 x 5,120 14.8 (14), 4,096 tokens by 20,480 x 5,120
+// 285 (273); gated, 256 tokens by 5,120 x 20,480 54 (62), 128 tokens by 1,024 x 512 8.1 (8).
+long long mul8_tiles_ns(const Mul8Args& a) {
+    constexpr long long kBlockNs = 300, kStartNs = 5500;
+    const std::atomic<int>* fit = a.up ? fits<true>() : fits<false>();
+    if (!fit) return -1;
+    const Shape shape = shape_of(a);
+    const int k_blocks = blocks8(a.k);
+    const Schedule plan = schedule(shape.tiles, k_blocks, fit);
+    const long long pairs = fit[1].load(std::memory_order_relaxed), at_once = plan.split > 1 && plan.whole == 0 ? shape.tiles * plan.split : shape.tiles < pairs ? shape.tiles : pairs;
+    const long long block = kBlockNs + (shape.token_tiles == 1 ? 2 * at_once : 0) * 9 / 10;
+    const long long turns = (plan.whole + pairs - 1) / pairs;
+    long long ns = kStartNs + turns * k_blocks * block + (turns > 1 ? turns - 1 : 0) * kEnds * kBlockNs;
+    if (plan.whole < shape.tiles) ns += (k_blocks + plan.split - 1) / plan.split * block + kJoin * kBlockNs + (plan.whole > 0 ? kLaunch * kBlockNs : 0);
+    return ns;
+}
+
 int launch_mul8_tiles(const Mul8Args& a, cudaStream_t stream) {
-    const int sms = attn_sm_count();
-    if (sms < 2) return -7;
-    return a.up ? start<true>(a, sms, stream) : start<false>(a, sms, stream);
+    return a.up ? start<true>(a, stream) : start<false>(a, stream);
 }
 
 int read_mul8_tiles_error(unsigned int* word, int clear, cudaStream_t stream) {

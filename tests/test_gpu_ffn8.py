@@ -143,7 +143,7 @@ def make_codes(rng, rows, cols, scales_shape, size=1.0, stride=None):
 
 
 SHAPES = [(1, 128, 128), (1, 16, 1), (2, 144, 130), (3, 1280, 257), (16, 2048, 384), (17, 400, 7), (31, 5120, 200), (33, 1152, 640), (64, 256, 1000), (65, 640, 129),
-          (100, 272, 260), (128, 1024, 512), (129, 512, 300), (200, 2064, 272), (257, 384, 1027), (300, 1040, 513), (515, 896, 768)]
+          (100, 272, 260), (128, 1024, 512), (129, 512, 300), (200, 2064, 272), (257, 384, 1027), (300, 1040, 513), (515, 896, 768), (400, 2448, 130), (270, 4112, 1544), (2100, 4112, 2600)]
 
 
 @pytest.mark.parametrize("wide", [False, True])
