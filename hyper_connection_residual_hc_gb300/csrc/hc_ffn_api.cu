@@ -172,7 +172,7 @@ int hc_token_logprobs(const void* logits, int64_t stride, const int64_t* tokens,
     if (s.n < 0 || s.n > kMaxRows || s.vocab < 1 || s.vocab > (1 << 30) || s.top < 0 || s.top > s.vocab) return HC_ERR_SHAPE;
     if (s.top > kMostTop) return HC_ERR_UNSUPPORTED;
     if (!good_stride(stride, s.vocab, 8)) return HC_ERR_SHAPE;
-    if (!std::isfinite(s.scale) || !(s.scale > 0.f) || (s.type != HC_BF16 && s.type != HC_F32)) return HC_ERR_ARG;
+    if (!(s.scale >= 0x1p-64f && s.scale <= 0x1p64f) || (s.type != HC_BF16 && s.type != HC_F32)) return HC_ERR_ARG;
     if (!aligned(logits, 16) || !aligned(tokens, 8) || !aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(top_logprob, 4) || !aligned(top_token, 4))
         return HC_ERR_ALIGN;
     const Rows z(logits, s.n, stride, s.vocab, s.type == HC_F32 ? 4 : 2), tk = flat(logprob ? tokens : nullptr, s.n, 8);

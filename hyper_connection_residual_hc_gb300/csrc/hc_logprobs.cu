@@ -1,18 +1,20 @@
 // Log probabilities of given tokens, the entropy and the most likely alternatives of rows of logits, in one pass over them.
 // Formulas and edge cases: include/hc.h.
 //
-// A row is cut into equal segments for a cluster of 1, 2, 4 or 8 CTAs. A CTA takes its segment in chunks of 256 threads x 8
-// vectors of 16 bytes, held in registers. Each thread keeps, for z = scale * logit in units of log 2 below its own running
-// maximum m: S = sum 2^t and W = sum t 2^t, t = (x - m) * scale * log2(e); joined over threads, warps and the cluster
-// (shared memory of the other CTAs), log sum e^z = m * scale + ln S and the entropy is ln S - ln 2 * W / S.
+// A row is cut into equal segments for a cluster of 1, 2, 4 or 8 CTAs. A CTA takes its segment in chunks of 256 threads x 4
+// vectors of 16 bytes, held in registers, the next chunk's loads in flight. Each thread keeps, for z = scale * logit in units of
+// log 2 below its own running maximum m: S = sum 2^t and W = sum t 2^t, t = (x - m) * scale * log2(e); joined over threads, warps and
+// the cluster (shared memory of the other CTAs), log sum e^z = m * scale + ln S and the entropy is ln S - ln 2 * W / S. Logits
+// far below m are raised to where 2^t is still 0, so that minus infinity does not make t 2^t a NaN; a NaN stays one.
 //
-// The alternatives ride along as a sorted list of 64-bit keys: the logit's bits as a number that rises with it, then the index
-// backwards, so that keys differ and of two equal logits the lower index is the greater key. A chunk is looked at again (in
-// registers) only if some thread's largest logit exceeds the last key of a full list. For the first chunk, the q-th
-// largest of each warp's 32 thread maxima, q * warps >= top, bounds the list's last key from below. What passes goes to a buffer
-// in any order and is ranked there by counting, so the result does not depend on it. Should more pass than the buffer holds
-// (many equal logits), the top-th largest of the threads' own first keys takes the bound's place: exactly `top` threads then have
-// candidates, whose 64 values each fit.
+// The alternatives ride along as 64-bit keys: the logit's bits as a number that rises with it, then the index backwards, so that
+// keys differ and of two equal logits the lower index is the greater key. Each warp collects candidates of its own, without
+// barriers. A bound keeps them few: with q * warps >= top, the q-th largest of a warp's 32 lanes' running maxima is posted
+// in shared memory, and the least of what the warps have posted is no larger than the CTA's top-th logit, however old a posted number
+// is. A lane looks at its values one by one only where a vector's largest reaches the bound. A warp whose buffer is full ranks it by
+// counting and keeps the first `top`, of which the last is a bound of its own (rising or equal logits get there). At the
+// end the candidates that reach the last bound are ranked together, and the lists of a cluster's CTAs once more; the
+// result does not depend on the order in which candidates came.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -32,11 +34,11 @@ __device__ unsigned int g_hc_logprob_error = 0;
 std::atomic<bool> g_launched{false};
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kVecs = 8;                                // vectors of a thread in a chunk
-constexpr int kMostEach = kVecs * 8;                    // values of a thread in a chunk (bf16)
-constexpr int kCandidates = kMostTop * kMostEach;       // see above: `top` threads' values always fit
+constexpr int kVecs = 4;                                // vectors of a thread in a chunk
+constexpr int kBuffer = 96;                             // candidates of a warp
+static_assert(kBuffer % 32 == 0 && kBuffer >= 2 * kMostTop + 32 - 1, "room for one of each lane behind a ranked list");
 constexpr int kChunk = kThreads * kVecs;
-constexpr float kFar = -256.f;                          // 2^t is 0 in fp32 from -150 on; keeps t 2^t from being -inf * 0
+constexpr float kFar = -256.f;                          // 2^t is 0 in fp32 from -150 on
 
 struct Sums {
     float m, s, w;  // s == 0: nothing yet, m means nothing
@@ -51,14 +53,6 @@ __device__ __forceinline__ void lower_to(Sums& a, float m, float c) {
         a.s *= f;
     }
     a.m = m;
-}
-__device__ __forceinline__ Sums join(Sums a, Sums b, float c) {
-    if (b.s == 0.f) return a;
-    if (a.s == 0.f) return b;
-    const float m = fmaxf(a.m, b.m);
-    lower_to(a, m, c);
-    lower_to(b, m, c);
-    return {m, a.s + b.s, a.w + b.w};
 }
 
 // A number that rises with x; NaN below everything, never 0
@@ -98,48 +92,56 @@ __device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t addr) {
 }
 
 struct Shared {
-    unsigned long long candidates[kCandidates + kMostTop];
-    unsigned long long list[2][kMostTop];
-    unsigned long long keys[kThreads];
-    unsigned long long bound;
-    uint32_t of_warp[kWarps];
-    int count;
+    uint4 chunk[kVecs][kThreads];  // values that their threads look at one by one
+    __align__(16) unsigned long long buffer[kWarps][kBuffer];
+    __align__(16) unsigned long long candidates[kWarps * kBuffer + 2];
+    unsigned long long list[kMostTop];
+    unsigned long long last[kMostTop];  // the list of a cluster's CTA, 0 where there is none
+    float total[3];                     // its sums
     float warp_sums[kWarps][3];
-    float total[3];
-    int list_n;  // of the list that counts, for the cluster's first CTA
-    int list_at;
+    uint32_t posted[kWarps];
+    int count;
 };
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float low_half(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float high_half(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
 template <bool kWide>
 struct Chunk {
     static constexpr int kEach = kWide ? 4 : 8;
     uint4 v[kVecs];
-    __device__ __forceinline__ float at(int i) const {  // (i known at compile time)
-        const uint4& q = v[i / kEach];
-        const int e = i % kEach;
+    __device__ __forceinline__ uint32_t word(int j, int i) const { return i == 0 ? v[j].x : i == 1 ? v[j].y : i == 2 ? v[j].z : v[j].w; }
+    __device__ __forceinline__ float at(int j, int e) const {  // value e of vector j (both known at compile time)
+        if constexpr (kWide) return __uint_as_float(word(j, e));
+        return e % 2 ? high_half(word(j, e / 2)) : low_half(word(j, e / 2));
+    }
+    __device__ __forceinline__ float largest(int j) const {  // of the numbers of a vector
         if constexpr (kWide) {
-            return __uint_as_float(e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w);
+            return fmaxf(fmaxf(at(j, 0), at(j, 1)), fmaxf(at(j, 2), at(j, 3)));
         } else {
-            const uint32_t u = e / 2 == 0 ? q.x : e / 2 == 1 ? q.y : e / 2 == 2 ? q.z : q.w;
-            return __uint_as_float(e % 2 ? u & 0xFFFF0000u : u << 16);
+            auto h = [](const uint32_t& u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+            const __nv_bfloat162 m = __hmax2(__hmax2(h(v[j].x), h(v[j].y)), __hmax2(h(v[j].z), h(v[j].w)));
+            return fmaxf(__low2float(m), __high2float(m));
         }
     }
-    __device__ __forceinline__ float largest() const {  // of the numbers among them
-        if constexpr (kWide) {
-            float m = -INFINITY;
+    static constexpr uint32_t kNone = kWide ? 0xFF800000u : 0xFF80FF80u;  // minus infinity
+    // Vectors first, first + kThreads, ... below `until` of a row; minus infinity in the place of others.
+    __device__ __forceinline__ void load(const char* row, int first, int until) {
 #pragma unroll
-            for (int i = 0; i < kVecs * kEach; ++i) m = fmaxf(m, at(i));
-            return m;
-        } else {
-            __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&v[0].x);
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].x));
-                m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].y));
-                m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].z));
-                m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&v[i].w));
-            }
-            return fmaxf(__low2float(m), __high2float(m));
+        for (int j = 0; j < kVecs; ++j) {
+            const int i = first + j * kThreads;
+            v[j] = make_uint4(kNone, kNone, kNone, kNone);
+            if (i < until) v[j] = __ldcs(reinterpret_cast<const uint4*>(row) + i);
         }
     }
 };
@@ -151,191 +153,271 @@ __device__ __forceinline__ float logit(const LogprobArgs& p, long long row, int 
     return __bfloat162float(static_cast<const __nv_bfloat16*>(p.logits)[at]);
 }
 
-// Ranks the `total` candidates by counting and puts the first `top` in order into list.
-__device__ __forceinline__ void rank_candidates(const unsigned long long* candidates, int total, int top, unsigned long long* list) {
+// How many of `total` keys are above `mine`; keys[total] is 0 if total is odd.
+__device__ __forceinline__ int keys_above(const unsigned long long* keys, int total, unsigned long long mine) {
+    const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(keys);
+    int above = 0;
+#pragma unroll 8
+    for (int j = 0; j < (total + 1) / 2; ++j) {
+        const ulonglong2 k = pairs[j];
+        above += (k.x > mine) + (k.y > mine);
+    }
+    return above;
+}
+
+// The first `top` of the CTA's candidates, in order, as `list`. Zeros are none.
+__device__ __forceinline__ void rank_candidates(unsigned long long* candidates, int total, int top, unsigned long long* list) {
+    if (total % 2 && threadIdx.x == 0) candidates[total] = 0;
+    __syncthreads();
     for (int i = threadIdx.x; i < total; i += kThreads) {
         const unsigned long long mine = candidates[i];
-        int above = 0;
-        for (int j = 0; j < total; ++j) above += candidates[j] > mine;
+        if (mine == 0) continue;
+        const int above = keys_above(candidates, total, mine);
         if (above < top) list[above] = mine;
     }
 }
 
+// The same of a warp's own buffer, in place; returns how many there are then.
+__device__ __forceinline__ int rank_buffer(unsigned long long* buffer, int count, int top) {
+    const int lane = threadIdx.x % 32;
+    if (count % 2 && lane == 0) buffer[count] = 0;
+    __syncwarp();
+    unsigned long long mine[kBuffer / 32];
+    int above[kBuffer / 32];
+#pragma unroll
+    for (int i = 0; i < kBuffer / 32; ++i) {
+        mine[i] = lane + 32 * i < count ? buffer[lane + 32 * i] : 0;
+        above[i] = mine[i] ? keys_above(buffer, count, mine[i]) : top;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kBuffer / 32; ++i)
+        if (above[i] < top) buffer[above[i]] = mine[i];
+    __syncwarp();
+    return min(count, top);
+}
+
+// Four CTAs an SM: their loads and barriers cover each other.
 template <bool kWide>
-__global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobArgs p, int ctas) {
+__global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs p, int ctas) {
     using C = Chunk<kWide>;
-    constexpr int kEach = C::kEach, kValues = kVecs * kEach;
+    constexpr int kEach = C::kEach;
     __shared__ __align__(16) Shared sh;
     const int t = threadIdx.x, warp = t / 32, lane = t % 32;
     const int rank = ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
     const long long row = blockIdx.x / static_cast<unsigned>(ctas);
     const char* base = static_cast<const char*>(p.logits) + row * p.stride * (kWide ? 4 : 2);
-    const int vecs = (p.vocab + kEach - 1) / kEach, whole = p.vocab / kEach;
-    const int each = (vecs + ctas - 1) / ctas;
-    const int v0 = min(rank * each, vecs), v1 = min(v0 + each, vecs);
+    const int whole = p.vocab / kEach;  // vectors; the values behind them are a chunk of their own, of the last CTA's first thread
+    const int each = (whole + ctas - 1) / ctas;
+    const int v0 = min(rank * each, whole), v1 = min(v0 + each, whole);
+    const int chunks = (v1 - v0 + kChunk - 1) / kChunk, all_chunks = chunks + (rank == ctas - 1 && whole * kEach < p.vocab ? 1 : 0);
     const float c = p.scale * kLog2e;
     Sums sum = {0.f, 0.f, 0.f};
-    unsigned long long bound = 0;  // the list's last key once it is full
-    int list_n = 0, cur = 0;
+    const float range = kFar / c;
+    float far = range;  // logits below sum.m + range count as that: 2^t is 0
+    uint32_t far2 = 0;  // the same as a pair of bf16
+    auto refer_to = [&](float m) {
+        lower_to(sum, m, c);
+        far = m + range;  // or the next number below m, where the sum is m itself; that is far enough then
+        if constexpr (kWide) {
+            if (far >= m) far = falling(rising(m) - 1u);
+        } else {
+            uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rd(far));
+            if (!(low_half(h) < m)) h = __float_as_uint(falling(rising(m) - 0x10000u)) >> 16;
+            far2 = h | h << 16;
+        }
+    };
+    refer_to(0.f);
+    // candidates
+    const int full = min(v1 - v0, kThreads) / 32;           // warps whose every thread has a vector at least
+    const int q = full > 0 ? (p.top + full - 1) / full : 0;
+    float lane_best = -INFINITY;                            // of all chunks so far
+    uint32_t posted = 0;
+    unsigned long long own = 0;                             // keys up to this one are not among the first `top`
+    int count = 0;                                          // in the warp's buffer
+    volatile uint32_t* all_posted = sh.posted;
+    auto bound = [&]() { return full > 0 ? __reduce_min_sync(0xFFFFFFFFu, all_posted[lane % full]) : 0u; };
+    if (t == 0) sh.count = 0;
 
-    for (int b = v0; b < v1; b += kChunk) {
-        C x;
+    C x, next;
+    auto load = [&](C& to, int i) {
+        to.load(base, v0 + i * kChunk + t, i < chunks ? v1 : 0);
+        if (i == chunks && t == 0) {
+            to.v[0] = make_uint4(C::kNone, C::kNone, C::kNone, C::kNone);
+#pragma unroll 1
+            for (int e = p.vocab - 1; e >= whole * kEach; --e) {  // (shifted in from below)
+                const uint32_t u = kWide ? reinterpret_cast<const uint32_t*>(base)[e] : reinterpret_cast<const uint16_t*>(base)[e];
+                uint4& v = to.v[0];
+                if constexpr (kWide)
+                    v = make_uint4(u, v.x, v.y, v.z);
+                else
+                    v = make_uint4(v.x << 16 | u, v.y << 16 | v.x >> 16, v.z << 16 | v.y >> 16, v.w << 16 | v.z >> 16);
+            }
+        }
+    };
+    load(x, 0);
+#pragma unroll 1
+    for (int i = 0; i < all_chunks; ++i) {
+        if (i + 1 < all_chunks) load(next, i + 1);
+        float best[kVecs];
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) best[j] = x.largest(j);
+        const float most = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
+        static_assert(kVecs == 4, "above");
+        if (most > (sum.s != 0.f ? sum.m : -INFINITY)) refer_to(most);
+        // (one number an instruction: what pairs of fp32 save goes into moving them together)
+        float s[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) {
-            const int i = b + j * kThreads + t;
-            constexpr uint32_t kNone = kWide ? 0xFF800000u : 0xFF80FF80u;  // minus infinity
-            x.v[j] = make_uint4(kNone, kNone, kNone, kNone);
-            if (i < v1) {
-                if (i < whole) {
-                    x.v[j] = __ldcs(reinterpret_cast<const uint4*>(base) + i);
-                } else {  // the row's last values
-                    uint32_t* u = &x.v[j].x;
 #pragma unroll
-                    for (int e = 0; e < kEach; ++e) {
-                        if (i * kEach + e >= p.vocab) break;
-                        if constexpr (kWide) {
-                            u[e] = reinterpret_cast<const uint32_t*>(base)[i * kEach + e];
-                        } else {
-                            const uint32_t h = reinterpret_cast<const uint16_t*>(base)[i * kEach + e];
-                            u[e / 2] = e % 2 ? (u[e / 2] & 0xFFFFu) | h << 16 : (u[e / 2] & 0xFFFF0000u) | h;
+            for (int e = 0; e < kEach; e += 2) {
+                float d[2];
+                if constexpr (kWide) {
+                    d[0] = max_nan(x.at(j, e), far);
+                    d[1] = max_nan(x.at(j, e + 1), far);
+                } else {
+                    const uint32_t u = max_nan2(x.word(j, e / 2), far2);
+                    d[0] = low_half(u);
+                    d[1] = high_half(u);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    d[i] = (d[i] - sum.m) * c;
+                    const float f = ex2(d[i]);
+                    s[i] += f;
+                    w[i] = fmaf(f, d[i], w[i]);
+                }
+            }
+        }
+        {
+            sum.s += s[0] + s[1];
+            sum.w += w[0] + w[1];
+            // Below the lowest number there is only minus infinity, for which t 2^t is a NaN: all else has had t = 0.
+            if (sum.w != sum.w && sum.s == sum.s) sum.w = 0.f;
+        }
+        if (p.top > 0) {
+            const int b = i < chunks ? v0 + i * kChunk : whole, until = i < chunks ? v1 : whole + 1;
+            lane_best = fmaxf(lane_best, most);
+            if (warp < full) {
+                const uint32_t r = lane_best > -INFINITY ? rising(lane_best) : 1u;  // (what is not there is minus infinity too)
+                if (__any_sync(0xFFFFFFFFu, r > posted)) {
+                    uint32_t left = r, w = 0;
+                    for (int k = 0; k < q; ++k) {
+                        w = __reduce_max_sync(0xFFFFFFFFu, left);
+                        const uint32_t who = __ballot_sync(0xFFFFFFFFu, left == w);
+                        if (lane == __ffs(static_cast<int>(who)) - 1) left = 0;
+                    }
+                    posted = w;
+                    if (lane == 0) all_posted[warp] = w;
+                }
+            }
+            if (i == 0) __syncthreads();
+            const uint32_t least = max(bound(), static_cast<uint32_t>(own >> 32));
+            const bool all = least <= 1;  // NaN is wanted
+            const float from = all ? 0.f : falling(least);
+            if (__any_sync(0xFFFFFFFFu, all || most >= from)) {
+                uint32_t mask = 0;
+                static_assert(kVecs * kEach <= 32, "a bit for each value");
+                if (all || most >= from) {
+#pragma unroll
+                    for (int j = 0; j < kVecs; ++j) {
+                        sh.chunk[j][t] = x.v[j];
+                        if (all || best[j] >= from) {
+#pragma unroll
+                            for (int e = 0; e < kEach; ++e) mask |= (all || x.at(j, e) >= from ? 1u : 0u) << (j * kEach + e);
                         }
                     }
                 }
-            }
-        }
-        const float most = x.largest();
-        {
-            const float m = reference(fmaxf(sum.s != 0.f ? sum.m : -INFINITY, most));
-            lower_to(sum, m, c);
-            float s = 0.f, w = 0.f;
-#pragma unroll
-            for (int i = 0; i < kValues; ++i) {
-                const float d = (x.at(i) - m) * c;
-                const float e = ex2(d);
-                s += e;
-                w = fmaf(e, fmaxf(d, kFar), w);
-            }
-            sum.s += s;
-            sum.w += w;
-        }
-        if (p.top == 0) continue;
-        const uint32_t mine = rising(most);
-        // (the barrier also keeps the buffers of the last chunk until all have read them)
-        if (!__syncthreads_or(mine > static_cast<uint32_t>(bound >> 32))) continue;
-        uint32_t least = static_cast<uint32_t>(bound >> 32) + 1;  // equal logits further on rank behind
-        const int full = min(v1 - b, kThreads) / 32;             // warps whose every thread has a vector at least
-        if (t == 0) sh.count = 0;
-        if (bound == 0) {
-            if (full > 0) {
-                const int q = (p.top + full - 1) / full;
-                uint32_t left = most > -INFINITY ? mine : 1u, w = 0;  // (padding counts as minus infinity, and is none)
-                for (int i = 0; i < q; ++i) {
-                    w = __reduce_max_sync(0xFFFFFFFFu, left);
-                    const uint32_t who = __ballot_sync(0xFFFFFFFFu, left == w);
-                    if (lane == __ffs(static_cast<int>(who)) - 1) left = 0;
-                }
-                if (lane == 0) sh.of_warp[warp] = w;
-            }
-            __syncthreads();
-            least = full > 0 ? sh.of_warp[0] : 0;
-            for (int i = 1; i < full; ++i) least = min(least, sh.of_warp[i]);
-            if (list_n > 0) least = 0;  // (a list that a short first chunk left unfilled)
-        } else {
-            __syncthreads();
-        }
-        const int first = b + t;
-        auto index = [&](int i) { return (first + i / kEach * kThreads) * kEach + i % kEach; };
-        if (mine >= least) {
-#pragma unroll
-            for (int i = 0; i < kValues; ++i) {
-                const uint32_t r = rising(x.at(i));
-                if (r >= least && first + i / kEach * kThreads < v1 && index(i) < p.vocab) {
-                    const int at = atomicAdd(&sh.count, 1);
-                    if (at < kCandidates) sh.candidates[at] = make_key(r, index(i));
-                }
-            }
-        }
-        __syncthreads();
-        int count = sh.count;
-        if (count > kCandidates) {
-            unsigned long long key = 0;  // this thread's greatest
-            if (mine >= least) {
-#pragma unroll
-                for (int i = 0; i < kValues; ++i)
-                    if (first + i / kEach * kThreads < v1 && index(i) < p.vocab) key = max(key, make_key(rising(x.at(i)), index(i)));
-            }
-            sh.keys[t] = key;
-            __syncthreads();
-            if (t == 0) sh.count = 0;
-            int above = 0;
-            for (int i = 0; i < kThreads; ++i) above += sh.keys[i] > key;
-            if (key != 0 && above == p.top - 1) sh.bound = key;
-            __syncthreads();
-            const unsigned long long from = sh.bound;
-            if (key >= from) {
-#pragma unroll
-                for (int i = 0; i < kValues; ++i) {
-                    const unsigned long long k = make_key(rising(x.at(i)), index(i));
-                    if (k >= from && first + i / kEach * kThreads < v1 && index(i) < p.vocab) {
-                        const int at = atomicAdd(&sh.count, 1);
-                        if (at < kCandidates) sh.candidates[at] = k;
+                while (__any_sync(0xFFFFFFFFu, mask != 0)) {  // one of each lane
+                    unsigned long long key = 0;
+                    if (mask) {
+                        const int bit = __ffs(static_cast<int>(mask)) - 1, j = bit / kEach, e = bit % kEach, vec = b + t + j * kThreads, index = vec * kEach + e;
+                        mask &= mask - 1;
+                        const float v = kWide ? reinterpret_cast<const float*>(&sh.chunk[j][t])[e]
+                                              : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(&sh.chunk[j][t])[e]) << 16);
+                        if (vec < until && index < p.vocab) key = make_key(rising(v), index);
+                        if (key <= own) key = 0;
                     }
+                    uint32_t who = __ballot_sync(0xFFFFFFFFu, key != 0);
+                    if (count + __popc(who) > kBuffer) {
+                        count = rank_buffer(sh.buffer[warp], count, p.top);
+                        own = sh.buffer[warp][p.top - 1];  // (the buffer held more than kMostTop)
+                        if (key <= own) key = 0;
+                        who = __ballot_sync(0xFFFFFFFFu, key != 0);
+                    }
+                    if (key != 0) sh.buffer[warp][count + __popc(who & ((1u << lane) - 1u))] = key;
+                    count += __popc(who);
+                    __syncwarp();
                 }
             }
-            __syncthreads();
-            count = min(sh.count, kCandidates);
         }
-        if (t < list_n) sh.candidates[count + t] = sh.list[cur][t];
+        x = next;
+    }
+    __syncthreads();
+    if (p.top > 0) {
+        const uint32_t least = bound();
+        for (int i = lane; i < kBuffer; i += 32) {
+            const unsigned long long key = i < count ? sh.buffer[warp][i] : 0;
+            const bool in = key != 0 && static_cast<uint32_t>(key >> 32) >= least;
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&sh.count, __popc(who));
+            at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(who & ((1u << lane) - 1u));
+            if (in) sh.candidates[at] = key;
+        }
         __syncthreads();
-        cur ^= 1;
-        rank_candidates(sh.candidates, count + list_n, p.top, sh.list[cur]);
-        list_n = min(count + list_n, p.top);
+        rank_candidates(sh.candidates, sh.count, p.top, sh.list);
         __syncthreads();
-        bound = list_n == p.top ? sh.list[cur][p.top - 1] : 0;
     }
 
-    // the CTA's sums
+    // The CTA's sums: all lanes refer to the largest maximum, then sums add up.
+    auto gather = [&](int lanes) {
+        float m = sum.s != 0.f ? sum.m : -INFINITY;
 #pragma unroll
-    for (int o = 16; o; o /= 2) {
-        const Sums other = {__shfl_xor_sync(0xFFFFFFFFu, sum.m, o), __shfl_xor_sync(0xFFFFFFFFu, sum.s, o), __shfl_xor_sync(0xFFFFFFFFu, sum.w, o)};
-        sum = lane & o ? join(other, sum, c) : join(sum, other, c);
-    }
+        for (int o = 16; o; o /= 2)
+            if (o < lanes) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        lower_to(sum, reference(m), c);
+#pragma unroll
+        for (int o = 16; o; o /= 2) {
+            if (o < lanes) {
+                sum.s += __shfl_xor_sync(0xFFFFFFFFu, sum.s, o);
+                sum.w += __shfl_xor_sync(0xFFFFFFFFu, sum.w, o);
+            }
+        }
+    };
+    gather(32);
     if (lane == 0) {
         sh.warp_sums[warp][0] = sum.m;
         sh.warp_sums[warp][1] = sum.s;
         sh.warp_sums[warp][2] = sum.w;
     }
     __syncthreads();
-    sum = {sh.warp_sums[0][0], sh.warp_sums[0][1], sh.warp_sums[0][2]};
-    for (int i = 1; i < kWarps; ++i) sum = join(sum, {sh.warp_sums[i][0], sh.warp_sums[i][1], sh.warp_sums[i][2]}, c);
+    sum = {sh.warp_sums[lane % kWarps][0], sh.warp_sums[lane % kWarps][1], sh.warp_sums[lane % kWarps][2]};
+    gather(kWarps);
 
     if (ctas > 1) {
         if (t == 0) {
             sh.total[0] = sum.m;
             sh.total[1] = sum.s;
             sh.total[2] = sum.w;
-            sh.list_n = list_n;
-            sh.list_at = cur;
         }
+        if (t < p.top) sh.last[t] = t < sh.count ? sh.list[t] : 0;
         cluster_sync();
         if (rank == 0) {
-            int total = 0;
-            for (int r = 1; r < ctas; ++r) {
-                const uint32_t from = in_cta(smem_u32(&sh), static_cast<uint32_t>(r));
-                const uint32_t tot = from + static_cast<uint32_t>(offsetof(Shared, total));
-                sum = join(sum, {__uint_as_float(ld_cluster_u32(tot)), __uint_as_float(ld_cluster_u32(tot + 4)), __uint_as_float(ld_cluster_u32(tot + 8))}, c);
+            const uint32_t own_smem = smem_u32(&sh);
+            sum = {0.f, 0.f, 0.f};
+            if (lane % 8 < ctas) {
+                const uint32_t from = in_cta(own_smem + static_cast<uint32_t>(offsetof(Shared, total)), static_cast<uint32_t>(lane % 8));
+                sum.m = __uint_as_float(ld_cluster_u32(from));
+                sum.s = __uint_as_float(ld_cluster_u32(from + 4));
+                sum.w = __uint_as_float(ld_cluster_u32(from + 8));
             }
+            gather(8);
             if (p.top > 0) {
-                for (int r = 0; r < ctas; ++r) {
-                    const uint32_t from = in_cta(smem_u32(&sh), static_cast<uint32_t>(r));
-                    const int have = static_cast<int>(ld_cluster_u32(from + static_cast<uint32_t>(offsetof(Shared, list_n))));
-                    const int at = static_cast<int>(ld_cluster_u32(from + static_cast<uint32_t>(offsetof(Shared, list_at))));
-                    if (t < have) sh.candidates[total + t] = ld_cluster_u64(from + static_cast<uint32_t>(offsetof(Shared, list)) + static_cast<uint32_t>((at * kMostTop + t) * 8));
-                    total += have;
-                }
-                __syncthreads();
-                rank_candidates(sh.candidates, total, p.top, sh.list[cur ^ 1]);
-                cur ^= 1;
+                static_assert(kThreads == 8 * kMostTop, "a thread for each key");
+                if (t < ctas * p.top)
+                    sh.candidates[t] = ld_cluster_u64(in_cta(own_smem + static_cast<uint32_t>(offsetof(Shared, last) + t % p.top * 8), static_cast<uint32_t>(t / p.top)));
+                rank_candidates(sh.candidates, ctas * p.top, p.top, sh.list);
                 __syncthreads();
             }
         }
@@ -362,7 +444,7 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobArgs p, 
         }
     }
     if (t < p.top) {
-        const unsigned long long key = sh.list[cur][t];
+        const unsigned long long key = sh.list[t];
         p.top_logprob[row * p.top + t] = log_probability(falling(static_cast<uint32_t>(key >> 32)));
         p.top_token[row * p.top + t] = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key));
     }

@@ -594,7 +594,7 @@ typedef struct {
     int vocab;   /* 1..2^30 */
     int top;     /* alternatives: 0..32 and at most vocab (above 32: HC_ERR_UNSUPPORTED) */
     int type;    /* of the logits: HC_BF16 or HC_F32 */
-    float scale; /* of the logits before the softmax (1 / temperature): finite, > 0 */
+    float scale; /* of the logits before the softmax (1 / temperature): 2^-64..2^64 */
 } hc_logprobs_t;
 
 /* For each row, with z = scale * logits and lse = log sum over the vocabulary of e^z:

@@ -134,7 +134,7 @@ def test_logprob_refusals():
     _expect(hc.HC_ERR_UNSUPPORTED, f, *_with(ok, _3=s(top=33)))
     for stride in (96, 108, 1 << 39):
         _expect(hc.HC_ERR_SHAPE, f, *_with(ok, _1=stride))
-    for bad in (dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(type=hc.HC_E4M3), dict(type=-1)):
+    for bad in (dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=2.0 ** -65), dict(scale=2.0 ** 65), dict(type=hc.HC_E4M3), dict(type=-1)):
         _expect(hc.HC_ERR_ARG, f, *_with(ok, _3=s(**bad)))
     _expect(hc.HC_ERR_ALIGN, f, *_with(ok, _0=A[0] + 8))
     _expect(hc.HC_ERR_ALIGN, f, *_with(ok, _2=A[1] + 4))

@@ -256,7 +256,7 @@ def test_logprobs(n, vocab, top, scale, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("kind", ["equal", "zeros of both signs", "two values", "rising", "falling", "banned", "all banned", "lowest", "all lowest", "one left", "far"])
+@pytest.mark.parametrize("kind", ["equal", "zeros of both signs", "two values", "rising", "falling", "banned", "all banned", "lowest", "all lowest", "lowest and banned", "one left", "far", "far below", "far up"])
 @pytest.mark.parametrize("n,vocab", [(3, 5000), (2, 70001), (400, 17000)])
 def test_logprobs_hard_rows(n, vocab, kind, dtype):
     rng = np.random.default_rng(vocab)
@@ -285,10 +285,22 @@ def test_logprobs_hard_rows(n, vocab, kind, dtype):
         z[:, ::2] = low
     elif kind == "all lowest":
         z[:] = low
+    elif kind == "lowest and banned":
+        z[:] = float("-inf")
+        z[:, ::3] = low
+        z[0, vocab // 2:] = low
+        z[1, -1] = 0.9 * low
+    elif kind in ("far below", "far up"):
+        z = z + (1e10 if kind == "far up" else -1e10)
+        z[:, 1::7] = float("-inf")
+        z[0, 5] = z[0].max() * (1.5 if kind == "far up" else 0.5)
     pad = -vocab % 8
     z = torch.nn.functional.pad(z, (0, pad))[:, :vocab]
     check_logprobs(z, rng.integers(0, vocab, n), 1.0, 32)
     check_logprobs(z, rng.integers(0, vocab, n), 1.0, 3)
+    if kind not in ("lowest", "all lowest", "lowest and banned"):  # (nothing overflows)
+        for scale in (2.0 ** -64, 2.0 ** 20):
+            check_logprobs(z, rng.integers(0, vocab, n), scale, 1)
     no_error()
 
 
