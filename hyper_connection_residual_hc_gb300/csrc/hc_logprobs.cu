@@ -9,9 +9,10 @@
 //
 // The alternatives ride along as 64-bit keys: the logit's bits as a number that rises with it, then the index backwards, so that
 // keys differ and of two equal logits the lower index is the greater key. Each warp collects candidates of its own, without
-// barriers. A bound keeps them few: with q * warps >= top, the q-th largest of a warp's 32 lanes' running maxima is posted
-// in shared memory, and the least of what the warps have posted is no larger than the CTA's top-th logit, however old a posted number
-// is. A lane looks at its values one by one only where a vector's largest reaches the bound. A warp whose buffer is full ranks it by
+// barriers. A bound keeps them few: each warp posts the 4 largest of its 32 lanes' running maxima in shared memory, and the top-th
+// largest of the 32 posted numbers (or less, below) is no larger than the CTA's top-th logit, however old a posted number is (a segment that does
+// not fill the warps has the bound that so many candidates need not be kept out). A lane looks at its values one by one only
+// where a vector's largest reaches the bound. A warp whose buffer is full ranks it by
 // counting and keeps the first `top`, of which the last is a bound of its own (rising or equal logits get there). At the
 // end the candidates that reach the last bound are ranked together, and the lists of a cluster's CTAs once more; the
 // result does not depend on the order in which candidates came.
@@ -35,6 +36,8 @@ std::atomic<bool> g_launched{false};
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVecs = 4;                                // vectors of a thread in a chunk
+constexpr int kPosted = 4;                              // numbers that a warp posts
+static_assert(kWarps * kPosted == 32 && kMostTop <= 32, "a lane for each");
 constexpr int kBuffer = 96;                             // candidates of a warp
 static_assert(kBuffer % 32 == 0 && kBuffer >= 2 * kMostTop + 32 - 1, "room for one of each lane behind a ranked list");
 constexpr int kChunk = kThreads * kVecs;
@@ -99,7 +102,7 @@ struct Shared {
     unsigned long long last[kMostTop];  // the list of a cluster's CTA, 0 where there is none
     float total[3];                     // its sums
     float warp_sums[kWarps][3];
-    uint32_t posted[kWarps];
+    uint32_t posted[kWarps * kPosted];
     int count;
 };
 
@@ -135,15 +138,7 @@ struct Chunk {
         }
     }
     static constexpr uint32_t kNone = kWide ? 0xFF800000u : 0xFF80FF80u;  // minus infinity
-    // Vectors first, first + kThreads, ... below `until` of a row; minus infinity in the place of others.
-    __device__ __forceinline__ void load(const char* row, int first, int until) {
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            const int i = first + j * kThreads;
-            v[j] = make_uint4(kNone, kNone, kNone, kNone);
-            if (i < until) v[j] = __ldcs(reinterpret_cast<const uint4*>(row) + i);
-        }
-    }
+    __device__ __forceinline__ void clear(int j) { v[j] = make_uint4(kNone, kNone, kNone, kNone); }
 };
 
 template <bool kWide>
@@ -229,93 +224,90 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
     };
     refer_to(0.f);
     // candidates
-    const int full = min(v1 - v0, kThreads) / 32;           // warps whose every thread has a vector at least
-    const int q = full > 0 ? (p.top + full - 1) / full : 0;
+    const bool bounded = v1 - v0 >= kThreads;               // every lane has a vector at least
     float lane_best = -INFINITY;                            // of all chunks so far
-    uint32_t posted = 0;
+    uint32_t posted = 0;                                    // the least that this warp has posted
+    uint32_t least = 0;                                     // logits below are not wanted
     unsigned long long own = 0;                             // keys up to this one are not among the first `top`
     int count = 0;                                          // in the warp's buffer
     volatile uint32_t* all_posted = sh.posted;
-    auto bound = [&]() { return full > 0 ? __reduce_min_sync(0xFFFFFFFFu, all_posted[lane % full]) : 0u; };
-    if (t == 0) sh.count = 0;
-
-    C x, next;
-    auto load = [&](C& to, int i) {
-        to.load(base, v0 + i * kChunk + t, i < chunks ? v1 : 0);
-        if (i == chunks && t == 0) {
-            to.v[0] = make_uint4(C::kNone, C::kNone, C::kNone, C::kNone);
-#pragma unroll 1
-            for (int e = p.vocab - 1; e >= whole * kEach; --e) {  // (shifted in from below)
-                const uint32_t u = kWide ? reinterpret_cast<const uint32_t*>(base)[e] : reinterpret_cast<const uint16_t*>(base)[e];
-                uint4& v = to.v[0];
-                if constexpr (kWide)
-                    v = make_uint4(u, v.x, v.y, v.z);
-                else
-                    v = make_uint4(v.x << 16 | u, v.y << 16 | v.x >> 16, v.z << 16 | v.y >> 16, v.w << 16 | v.z >> 16);
-            }
+    // Posts the largest of the lanes' maxima, the greatest first: old and new numbers together are then still different logits'.
+    auto post = [&](uint32_t mine) {
+#pragma unroll
+        for (int k = 0; k < kPosted; ++k) {
+            posted = __reduce_max_sync(0xFFFFFFFFu, mine);
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine == posted);
+            if (lane == __ffs(static_cast<int>(who)) - 1) mine = 0;
+            if (lane == 0) all_posted[warp * kPosted + k] = posted;
         }
     };
-    load(x, 0);
+    // For few alternatives the top-th largest of what is posted, taken at one moment, else the least of the warps' q-th numbers, q *
+    // warps >= top, which is less, but there at once (20 alternatives, 256 rows: 31 us, 33 with the top-th largest; 1: 26 and 21).
+    auto bound = [&]() {
+        if (!bounded) return 0u;
+        if (p.top > 8) return __reduce_min_sync(0xFFFFFFFFu, all_posted[lane % kWarps * kPosted + (p.top - 1) / kWarps]);
+        uint32_t mine = all_posted[lane], w = 0;
+        for (int k = 0; k < p.top; ++k) {
+            w = __reduce_max_sync(0xFFFFFFFFu, mine);
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine == w);
+            if (lane == __ffs(static_cast<int>(who)) - 1) mine = 0;
+        }
+        return w;
+    };
+    if (t == 0) sh.count = 0;
+
+    // Vector j of chunk i; minus infinity in the place of what is not there.
+    C x;
+    auto load = [&](int i, int j) {
+        const int vec = v0 + i * kChunk + j * kThreads + t;
+        const uint4* from = reinterpret_cast<const uint4*>(base) + vec;
+        if (v0 + (i + 1) * kChunk <= v1) {
+            x.v[j] = __ldcs(from);
+        } else {
+            x.clear(j);
+            if (i < chunks && vec < v1) x.v[j] = __ldcs(from);
+        }
+    };
+    auto load_last = [&]() {  // the values behind the whole vectors
+        x.clear(0);
+        if (t != 0) return;
+#pragma unroll 1
+        for (int e = p.vocab - 1; e >= whole * kEach; --e) {  // (shifted in from below)
+            const uint32_t u = kWide ? reinterpret_cast<const uint32_t*>(base)[e] : reinterpret_cast<const uint16_t*>(base)[e];
+            uint4& v = x.v[0];
+            if constexpr (kWide)
+                v = make_uint4(u, v.x, v.y, v.z);
+            else
+                v = make_uint4(v.x << 16 | u, v.y << 16 | v.x >> 16, v.z << 16 | v.y >> 16, v.w << 16 | v.z >> 16);
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) load(0, j);
+    if (chunks == 0) load_last();
 #pragma unroll 1
     for (int i = 0; i < all_chunks; ++i) {
-        if (i + 1 < all_chunks) load(next, i + 1);
         float best[kVecs];
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) best[j] = x.largest(j);
         const float most = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
         static_assert(kVecs == 4, "above");
         if (most > (sum.s != 0.f ? sum.m : -INFINITY)) refer_to(most);
-        // (one number an instruction: what pairs of fp32 save goes into moving them together)
-        float s[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-#pragma unroll
-            for (int e = 0; e < kEach; e += 2) {
-                float d[2];
-                if constexpr (kWide) {
-                    d[0] = max_nan(x.at(j, e), far);
-                    d[1] = max_nan(x.at(j, e + 1), far);
-                } else {
-                    const uint32_t u = max_nan2(x.word(j, e / 2), far2);
-                    d[0] = low_half(u);
-                    d[1] = high_half(u);
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    d[i] = (d[i] - sum.m) * c;
-                    const float f = ex2(d[i]);
-                    s[i] += f;
-                    w[i] = fmaf(f, d[i], w[i]);
-                }
-            }
-        }
-        {
-            sum.s += s[0] + s[1];
-            sum.w += w[0] + w[1];
-            // Below the lowest number there is only minus infinity, for which t 2^t is a NaN: all else has had t = 0.
-            if (sum.w != sum.w && sum.s == sum.s) sum.w = 0.f;
-        }
         if (p.top > 0) {
             const int b = i < chunks ? v0 + i * kChunk : whole, until = i < chunks ? v1 : whole + 1;
             lane_best = fmaxf(lane_best, most);
-            if (warp < full) {
+            bool all = least <= 1;  // NaN is wanted
+            float from = all ? 0.f : falling(least);
+            bool some = __any_sync(0xFFFFFFFFu, all || most >= from);
+            if (some && bounded) {
                 const uint32_t r = lane_best > -INFINITY ? rising(lane_best) : 1u;  // (what is not there is minus infinity too)
-                if (__any_sync(0xFFFFFFFFu, r > posted)) {
-                    uint32_t left = r, w = 0;
-                    for (int k = 0; k < q; ++k) {
-                        w = __reduce_max_sync(0xFFFFFFFFu, left);
-                        const uint32_t who = __ballot_sync(0xFFFFFFFFu, left == w);
-                        if (lane == __ffs(static_cast<int>(who)) - 1) left = 0;
-                    }
-                    posted = w;
-                    if (lane == 0) all_posted[warp] = w;
-                }
+                if (__any_sync(0xFFFFFFFFu, r > posted)) post(r);
+                if (i == 0) __syncthreads();
+                least = max(bound(), static_cast<uint32_t>(own >> 32));
+                all = least <= 1;
+                from = all ? 0.f : falling(least);
+                some = __any_sync(0xFFFFFFFFu, all || most >= from);
             }
-            if (i == 0) __syncthreads();
-            const uint32_t least = max(bound(), static_cast<uint32_t>(own >> 32));
-            const bool all = least <= 1;  // NaN is wanted
-            const float from = all ? 0.f : falling(least);
-            if (__any_sync(0xFFFFFFFFu, all || most >= from)) {
+            if (some) {
                 uint32_t mask = 0;
                 static_assert(kVecs * kEach <= 32, "a bit for each value");
                 if (all || most >= from) {
@@ -351,11 +343,60 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
                 }
             }
         }
-        x = next;
+        // t = x c - m c by one FMA with m c rounded; what that rounding is off by goes back into the sums. Each vector's registers
+        // take the next chunk's as soon as its sums are made. (One number an instruction: what pairs of fp32 save goes into
+        // moving them together.)
+        const float mc = sum.m * c;
+        float s[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
+        if (fabsf(mc) < 1e6f) {
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+#pragma unroll
+                for (int e = 0; e < kEach; e += 2) {
+                    float d[2];
+                    if constexpr (kWide) {
+                        d[0] = max_nan(x.at(j, e), far);
+                        d[1] = max_nan(x.at(j, e + 1), far);
+                    } else {
+                        const uint32_t u = max_nan2(x.word(j, e / 2), far2);
+                        d[0] = low_half(u);
+                        d[1] = high_half(u);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        d[k] = fmaf(d[k], c, -mc);
+                        const float f = ex2(d[k]);
+                        s[k] += f;
+                        w[k] = fmaf(f, d[k], w[k]);
+                    }
+                }
+                load(i + 1, j);
+            }
+            const float off = -fmaf(sum.m, c, -mc), f = ex2(off);
+            s[0] = (s[0] + s[1]) * f;
+            w[0] = fmaf(s[0], off, (w[0] + w[1]) * f);
+        } else {  // so far out that the rounding would be whole doublings
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) sh.chunk[j][t] = x.v[j];
+#pragma unroll 1
+            for (int k = 0; k < kVecs * kEach; ++k) {
+                const uint4* v = &sh.chunk[k / kEach][t];
+                const float u = kWide ? reinterpret_cast<const float*>(v)[k % kEach]
+                                      : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(v)[k % kEach]) << 16);
+                const float d = (u - sum.m) * c, f = ex2(d);
+                s[0] += f;
+                if (f != 0.f) w[0] = fmaf(f, d, w[0]);  // (below the lowest number there is minus infinity)
+            }
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) load(i + 1, j);
+        }
+        sum.s += s[0];
+        sum.w += w[0];
+        if (i + 1 == chunks) load_last();
     }
     __syncthreads();
     if (p.top > 0) {
-        const uint32_t least = bound();
+        least = bound();
         for (int i = lane; i < kBuffer; i += 32) {
             const unsigned long long key = i < count ? sh.buffer[warp][i] : 0;
             const bool in = key != 0 && static_cast<uint32_t>(key >> 32) >= least;
