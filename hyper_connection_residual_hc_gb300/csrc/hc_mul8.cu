@@ -311,9 +311,10 @@ int cluster_ctas(long long units, int k_blocks, const std::atomic<int>* fit) {
     return c;
 }
 
-// How a call would run with tiles of kN tokens, and about how long it would take, in ns: the weights' bytes or the busiest SM's blocks (kBlockNs each),
-// a start and an end, and the join of a cluster's parts. Measured (us, model in brackets): 128 tokens by 20,480 x 5,120 27.4 (27), by
-// 5,120 x 5,120 11.2 (11); gated, 64 tokens by 5,120 x 20,480 50.8 (48), 128 tokens by 1,024 x 512 10.8 (10).
+// How a call would run with tiles of kN tokens, and about how long it would take, in ns: the weights' bytes, or the busiest SM's tiles
+// with their blocks (kBlockNs each) and their ends (kEndNs: out of registers, joined, written), a launch, and the join of a cluster's
+// parts. Measured (us, model in brackets): 128 tokens by 20,480 x 5,120 27.4 (28), by 5,120 x 5,120 11.2 (12), 715 tokens by 320 x
+// 19,728 39 (32); gated, 64 tokens by 5,120 x 20,480 50.8 (52), 344 tokens by 176 x 6,720 24.6 (22).
 struct RowsPlan {
     long long token_tiles, units;
     int ctas;
@@ -321,6 +322,8 @@ struct RowsPlan {
 };
 template <int kN, bool kGated>
 constexpr int kBlockNs = kGated ? (kN == 128 ? 1000 : kN == 64 ? 550 : 250) : (kN == 128 ? 400 : 200);
+template <int kN, bool kGated>
+constexpr int kEndNs = kGated ? (kN == 128 ? 7500 : kN == 64 ? 3000 : 1500) : (kN == 128 ? 3000 : 1500);
 
 template <int kN, bool kGated, int kPerSm>
 struct Rows {
@@ -352,9 +355,10 @@ struct Rows {
         r->token_tiles = (a.n + kN - 1) / kN;
         r->units = r->token_tiles * blocks8(a.features);
         r->ctas = cluster_ctas(r->units, k_blocks, f);
-        const long long bytes_ns = static_cast<long long>(P::kMats) * a.features * a.k / 6200;
-        const long long block_ns = (r->units * r->ctas + sms - 1) / sms * ((k_blocks + r->ctas - 1) / r->ctas) * kBlockNs<kN, kGated>;
-        r->ns = 4000 + (bytes_ns > block_ns ? bytes_ns : block_ns) + (r->ctas > 1 ? 15 * kN * P::kMats : 0);
+        const long long turns = (r->units * r->ctas + sms - 1) / sms, end = kEndNs<kN, kGated>;
+        const long long bytes_ns = static_cast<long long>(P::kMats) * a.features * a.k / 6200 + end;
+        const long long tiles_ns = turns * ((k_blocks + r->ctas - 1) / r->ctas * kBlockNs<kN, kGated> + end);
+        r->ns = 2500 + (bytes_ns > tiles_ns ? bytes_ns : tiles_ns) + (r->ctas > 1 ? 7 * kN * P::kMats : 0);
         return true;
     }
 

@@ -11,7 +11,7 @@
 //
 // Warps: 8 add up (4 for each half of the columns; a gated product's two halves are columns 0..63 and 64..127 of gate and up, so that a
 // thread has both), 1 issues TMA loads, 1 (of the first CTA) the MMAs. Registers move from the last 4 warps to the first 8.
-// Results leave through shared memory by TMA stores, 128 bytes of 32 rows at a time, which also cut off rows and columns
+// Results leave through shared memory by TMA stores, 64 bytes of 32 rows at a time, which also cut off rows and columns
 // outside the output.
 
 #include <cuda.h>
@@ -40,14 +40,15 @@ constexpr int kOperand = kHalf * kBlock8;        // bytes: 128 rows of one opera
 constexpr int kStage = 2 * kOperand;
 constexpr int kAddWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kScaleWarps = 2;  // in this order
 constexpr int kThreads = 384;
-constexpr int kOutWarp = 4096;                   // 32 rows of 128 bytes
+constexpr int kOutWarp = 4096;                   // two buffers of 32 rows of 64 bytes
 constexpr int kOut = kStages * kStage;
-constexpr int kTops = 2048;                      // of a warp's output, behind 32 rows of 64 bytes: [2][32] largest magnitudes
 constexpr int kBatch = 8;                        // blocks of k whose scales are handed over together
 constexpr int kScales = kOut + kAddWarps * kOutWarp;  // [2][kBatch][2][128] factors
-constexpr int kBars = kScales + 2 * kBatch * 2 * kHalf * 4;
+constexpr int kTops = kScales + 2 * kBatch * 2 * kHalf * 4;  // [2][kAddWarps][32] largest magnitudes
+constexpr int kBars = kTops + 2 * kAddWarps * 32 * 4;
 constexpr int kSmem = kBars + 256 + 1024;        // + alignment
 static_assert(kSmem <= 227 * 1024, "fits");
+constexpr int kMostPairs = 4;                    // that share a tile
 constexpr int kBand = 8;                         // token tiles that go through the weights together
 
 struct Params {
@@ -176,17 +177,28 @@ __device__ __forceinline__ void join_parts(const Params& p, const Tile& t, const
         const uint32_t mine = base + static_cast<uint32_t>(((half * kHalf + c) / 4 * kHalf + in_cta) * 16);
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[e] = 0.f;
-        for (int r = 0; r < p.pairs; ++r) {
-            const uint32_t from = mapa8(mine, static_cast<uint32_t>(2 * r + rank));
-            float4 v[4];
+        float4 v[kMostPairs][4];  // all loads at once: one by one they took as long as 10 blocks
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = ld_cluster_f4(from + static_cast<uint32_t>(e * kHalf * 16));
+        for (int r = 0; r < kMostPairs; ++r) {
+            if (r >= p.pairs) break;
+            const uint32_t from = mapa8(mine, static_cast<uint32_t>(2 * r + rank));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                s[4 * e] += v[e].x;
-                s[4 * e + 1] += v[e].y;
-                s[4 * e + 2] += v[e].z;
-                s[4 * e + 3] += v[e].w;
+                if (r == pair)
+                    v[r][e] = *reinterpret_cast<const float4*>(at + (mine - base) + e * kHalf * 16);
+                else
+                    v[r][e] = ld_cluster_f4(from + static_cast<uint32_t>(e * kHalf * 16));
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kMostPairs; ++r) {
+            if (r >= p.pairs) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[4 * e] += v[r][e].x;
+                s[4 * e + 1] += v[r][e].y;
+                s[4 * e + 2] += v[r][e].z;
+                s[4 * e + 3] += v[r][e].w;
             }
         }
     };
@@ -288,6 +300,10 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     const long long n0 = p.first + (kSplit ? blockIdx.x / (2 * p.pairs) : blockIdx.x / 2), step = kSplit ? p.until : p.pairs;
     const int k0 = kSplit ? p.k_blocks * pair / p.pairs : 0, k1 = kSplit ? p.k_blocks * (pair + 1) / p.pairs : p.k_blocks;
 
+    if (warp == kLoadWarp && lane == 0) {
+        tma_prefetch_desc(&tm_x);
+        tma_prefetch_desc(kGated && rank ? &tm_up : &tm_w);
+    }
     if (warp == kMmaWarp) {
         tmem_alloc2(slot, 512);
         tmem_relinquish2();
@@ -377,22 +393,19 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 for (int b = k0; b < k1; b += kBatch, ++batch) {
                     if (batch >= 2) wait(sc_empty + 8 * (batch & 1), (batch / 2 - 1) & 1);
                     float* o = reinterpret_cast<float*>(at + kScales) + (batch & 1) * kBatch * 2 * kHalf + in_cta;
+                    float x[2][kBatch], w[2][kBatch];  // (all loads at once: the first ones are waited for)
 #pragma unroll
-                    for (int j0 = 0; j0 < kBatch; j0 += 4) {
-                        float x[2][4], w[2][4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int from = min(b + j0 + j, k1 - 1);
-                            x[0][j] = __ldg(x0 + from);
-                            x[1][j] = __ldg(x1 + from);
-                            w[0][j] = __ldg(w0 + from);
-                            w[1][j] = __ldg(w1 + from);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) o[((j0 + j) * 2 + r / 2) * kHalf + r % 2 * 32] = x[r % 2][j] * w[r / 2][j];
+                    for (int j = 0; j < kBatch; ++j) {
+                        const int from = min(b + j, k1 - 1);
+                        x[0][j] = __ldg(x0 + from);
+                        x[1][j] = __ldg(x1 + from);
+                        w[0][j] = __ldg(w0 + from);
+                        w[1][j] = __ldg(w1 + from);
                     }
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) o[(j * 2 + r / 2) * kHalf + r % 2 * 32] = x[r % 2][j] * w[r / 2][j];
                     __syncwarp();
                     arrive_if(sc_full + 8 * (batch & 1), lane == 0);
                 }
@@ -407,7 +420,7 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         const uint32_t released = mapa8(acc_empty, leader);
         const uint32_t out_smem = base + kOut + warp * kOutWarp;
         const float* factors = reinterpret_cast<const float*>(at + kScales) + (kGated ? 0 : half * kHalf) + in_cta;
-        int i = 0, batch = 0, turn = 0;
+        int i = 0, batch = 0, turn = 0, stores = 0;
         for (long long n = n0; n < p.until; n += step, ++turn) {
             uint64_t acc[64];  // pairs of columns: 128 features, or 64 of the gate and 64 of up
 #pragma unroll
@@ -447,27 +460,26 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                 join_parts<kGated>(p, t, acc, base, at, half, in_cta, static_cast<int>(rank), pair);
                 break;
             }
-            // Stages 128 bytes of each of the warp's 32 rows (a lane's words w, 16 bytes at a time, swizzled as the map says) and stores
-            // them at column x.
-            auto store = [&](const uint32_t* w, int bytes, int x) {
-                if (lane == 0) bulk_wait_read<0>();
+            // Stages 64 bytes of each of the warp's 32 rows (a lane's words w, 16 bytes at a time, swizzled as the map says) and stores them
+            // at column x, in one of two buffers by turns: the store before this one is read out meanwhile.
+            auto store = [&](const uint32_t (&w)[16], int x) {
+                const uint32_t to = out_smem + (stores++ & 1) * (kOutWarp / 2) + static_cast<uint32_t>(lane * 64);
+                const int mask = (lane >> 1) & 3;
+                if (lane == 0) bulk_wait_read<1>();
                 __syncwarp();
-                const int mask = bytes == 128 ? lane & 7 : (lane >> 1) & 3;
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    if (16 * c < bytes)
-                        st_smem_v4(out_smem + static_cast<uint32_t>(lane * bytes + ((c ^ mask) * 16)), make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]));
+                for (int c = 0; c < 4; ++c) st_smem_v4(to + (c ^ mask) * 16, make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]));
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0 && token0 < p.a.n) {
-                    if (x < p.stored) tma_store_2d(&tm_out, out_smem, x, token0);
+                if (lane == 0) {
+                    if (token0 < p.a.n && x < p.stored) tma_store_2d(&tm_out, to, x, token0);
                     bulk_commit();
                 }
                 if constexpr (!kGated) {
                     // A TMA store writes whole 16 bytes; the features past the last of those go one by one.
                     const int size = p.a.out_type == kOutF32 ? 4 : 2, rest = p.a.features - p.stored, off = (p.stored - x) * size;
-                    if (rest > 0 && off >= 0 && off < 128 && token0 + lane < p.a.n) {
-                        const uint4 q = ld_smem_v4(out_smem + static_cast<uint32_t>(lane * 128 + ((off / 16) ^ mask) * 16));
+                    if (rest > 0 && off >= 0 && off < 64 && token0 + lane < p.a.n) {
+                        const uint4 q = ld_smem_v4(to + ((off / 16) ^ mask) * 16);
                         const uint32_t u[4] = {q.x, q.y, q.z, q.w};
                         const long long o = (static_cast<long long>(token0) + lane) * p.a.out_stride + p.stored;
 #pragma unroll
@@ -497,49 +509,52 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
 #pragma unroll
                     for (int e = 0; e < 64; ++e) top = max_nan(top, fabsf(h[e]));  // (features past the last are 0)
                     // the other 64 features' is with the warp of the other half
-                    float* tops = reinterpret_cast<float*>(at + kOut + kTops) + (turn & 1) * 32 + lane;
-                    tops[warp * (kOutWarp / 4)] = top;
+                    float* tops = reinterpret_cast<float*>(at + kTops) + (turn & 1) * 32 * kAddWarps + lane;
+                    tops[warp * 32] = top;
                     asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-                    top = max_nan(max_nan(top, tops[(warp ^ 4) * (kOutWarp / 4)]), kLeastTop8);
+                    top = max_nan(max_nan(top, tops[(warp ^ 4) * 32]), kLeastTop8);
                     const float up = kTop8 / top;
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) w[e] = e4m3x4(h[4 * e] * up, h[4 * e + 1] * up, h[4 * e + 2] * up, h[4 * e + 3] * up);
-                    store(w, 64, x);
+                    store(w, x);
                     const long long row = static_cast<long long>(token0) + lane;
                     if (half == 0 && row < p.a.n) p.a.out_scales[row * p.feature_tiles + t.features] = top / kTop8;
                 } else {
-                    uint32_t w[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) w[e] = bf16x2(h[2 * e], h[2 * e + 1]);
-                    store(w, 128, x);
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = bf16x2(h[32 * c + 2 * e], h[32 * c + 2 * e + 1]);
+                        store(w, x + 32 * c);
+                    }
                 }
             } else {
                 const int x = t.features * kRowsW + kHalf * half;
                 if (p.a.out_type == kOutF32) {
 #pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float a, b;
+                            unpair8(acc[8 * c + e], a, b);
+                            w[2 * e] = __float_as_uint(a);
+                            w[2 * e + 1] = __float_as_uint(b);
+                        }
+                        store(w, x + 16 * c);
+                    }
+                } else {
+#pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t w[32];
+                        uint32_t w[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float a, b;
                             unpair8(acc[16 * c + e], a, b);
-                            w[2 * e] = __float_as_uint(a);
-                            w[2 * e + 1] = __float_as_uint(b);
-                        }
-                        store(w, 128, x + 32 * c);
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t w[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float a, b;
-                            unpair8(acc[32 * c + e], a, b);
                             w[e] = bf16x2(a, b);
                         }
-                        store(w, 128, x + 64 * c);
+                        store(w, x + 32 * c);
                     }
                 }
             }
@@ -568,17 +583,15 @@ bool out_map(CUtensorMap* m, const Mul8Args& a, int stored) {
     const CUtensorMapDataType type = a.out_type == kOutF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : a.out_type == kOutE4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(stored > 0 ? stored : 8), static_cast<cuuint64_t>(a.n)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.out_stride) * static_cast<cuuint64_t>(size)};
-    const cuuint32_t box[2] = {a.out_type == kOutF32 ? 32u : 64u, 32}, ones[2] = {1, 1};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / size), 32}, ones[2] = {1, 1};
     return fn(m, type, 2, a.out, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              a.out_type == kOutE4m3 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // How the tiles go to pairs: as many as fill all pairs a whole number of times are taken whole, and so are the others unless sharing
 // each of them between the pairs of a cluster is shorter (they are few then: the clusters run at once). In blocks of k: a tile's
 // start and end cost about as much as kEnds, joining kJoin more, another launch kLaunch. `fit`: clusters of 1 to 4 pairs that run at once.
-constexpr int kMostPairs = 4;
-constexpr int kEnds = 6, kJoin = 11, kLaunch = 16;
+constexpr int kEnds = 6, kJoin = 11, kLaunch = 20;
 struct Schedule {
     long long whole;  // tiles
     int split;        // pairs that share each of the others; 1: none are left
@@ -692,8 +705,8 @@ int start(const Mul8Args& a, cudaStream_t stream) {
 }  // namespace
 
 // In blocks of kBlockNs; with one token tile what runs at once reads weights of its own, and the more of it the longer a block takes.
-// Measured (us, model in brackets): 256 tokens by 20,480 x 5,120 30.8 (29), by 5,120 x 5,120 14.8 (14), 4,096 tokens by 20,480 x 5,120
-// 285 (273); gated, 256 tokens by 5,120 x 20,480 54 (62), 128 tokens by 1,024 x 512 8.1 (8).
+// Measured (us, model in brackets): 256 tokens by 20,480 x 5,120 30.8 (29), by 5,120 x 5,120 14.8 (14), 715 tokens by 320 x 19,728 14.4
+// (15), 4,096 tokens by 20,480 x 5,120 280 (263); gated, 256 tokens by 5,120 x 20,480 55 (62), 128 tokens by 1,024 x 512 8.1 (8).
 long long mul8_tiles_ns(const Mul8Args& a) {
     constexpr long long kBlockNs = 300, kStartNs = 5500;
     const std::atomic<int>* fit = a.up ? fits<true>() : fits<false>();
@@ -702,7 +715,7 @@ long long mul8_tiles_ns(const Mul8Args& a) {
     const int k_blocks = blocks8(a.k);
     const Schedule plan = schedule(shape.tiles, k_blocks, fit);
     const long long pairs = fit[1].load(std::memory_order_relaxed), at_once = plan.split > 1 && plan.whole == 0 ? shape.tiles * plan.split : shape.tiles < pairs ? shape.tiles : pairs;
-    const long long block = kBlockNs + (shape.token_tiles == 1 ? 2 * at_once : 0) * 9 / 10;
+    const long long block = kBlockNs + (shape.token_tiles == 1 ? at_once * 6 / 5 : 0);
     const long long turns = (plan.whole + pairs - 1) / pairs;
     long long ns = kStartNs + turns * k_blocks * block + (turns > 1 ? turns - 1 : 0) * kEnds * kBlockNs;
     if (plan.whole < shape.tiles) ns += (k_blocks + plan.split - 1) / plan.split * block + kJoin * kBlockNs + (plan.whole > 0 ? kLaunch * kBlockNs : 0);
