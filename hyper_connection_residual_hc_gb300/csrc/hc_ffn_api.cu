@@ -14,7 +14,7 @@ namespace hc {
 namespace {
 
 constexpr int64_t kMaxRows = 0x7FFFFFFFLL;
-constexpr int64_t kMaxStride = 1LL << 38;
+constexpr int64_t kMaxStride = 1LL << 37;  // (a tensor map's strides are below 2^40 bytes)
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 

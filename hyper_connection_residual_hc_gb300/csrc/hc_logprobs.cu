@@ -102,7 +102,7 @@ struct Shared {
     unsigned long long last[kMostTop];  // the list of a cluster's CTA, 0 where there is none
     float total[3];                     // its sums
     float warp_sums[kWarps][3];
-    uint32_t posted[kWarps * kPosted];
+    __align__(16) uint32_t posted[kWarps * kPosted];
     int count;
 };
 
@@ -230,16 +230,21 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
     uint32_t least = 0;                                     // logits below are not wanted
     unsigned long long own = 0;                             // keys up to this one are not among the first `top`
     int count = 0;                                          // in the warp's buffer
-    volatile uint32_t* all_posted = sh.posted;
-    // Posts the largest of the lanes' maxima, the greatest first: old and new numbers together are then still different logits'.
+    const volatile uint32_t* all_posted = sh.posted;
+    // Posts the largest of the lanes' maxima, in order and by one store, as they are read by one load.
     auto post = [&](uint32_t mine) {
+        uint32_t w[kPosted];
 #pragma unroll
         for (int k = 0; k < kPosted; ++k) {
-            posted = __reduce_max_sync(0xFFFFFFFFu, mine);
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine == posted);
+            w[k] = __reduce_max_sync(0xFFFFFFFFu, mine);
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine == w[k]);
             if (lane == __ffs(static_cast<int>(who)) - 1) mine = 0;
-            if (lane == 0) all_posted[warp * kPosted + k] = posted;
         }
+        posted = w[kPosted - 1];
+        static_assert(kPosted == 4, "one store");
+        if (lane == 0)
+            asm volatile("st.volatile.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(&sh.posted[warp * kPosted])), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
     };
     // For few alternatives the top-th largest of what is posted, taken at one moment, else the least of the warps' q-th numbers, q *
     // warps >= top, which is less, but there at once (20 alternatives, 256 rows: 31 us, 33 with the top-th largest; 1: 26 and 21).

@@ -519,7 +519,7 @@ int hc_kv_attention(const void* q, int64_t q_stride, const int* q_start, const i
  * value is code * scale; blocks at the end may be short. Any scales will do: their products are taken in fp32.
  *
  * Rows may be strided (the stride in elements): multiples of 8 for bf16 and fp32, of 16 for codes, at least the row's width and at
- * most 2^38 (HC_ERR_SHAPE otherwise, as for more than 2^31 - 1 rows). The 16-byte rule holds for all rows and for norm_w; scales,
+ * most 2^37 (HC_ERR_SHAPE otherwise, as for more than 2^31 - 1 rows). The 16-byte rule holds for all rows and for norm_w; scales,
  * tokens, log probabilities and alternatives need their own type's alignment only. Outputs must not overlap each other or an
  * input unless a call says so (HC_ERR_ALIAS); rows of one stride that lie side by side do not overlap. What lies between
  * the rows is neither read nor written. */

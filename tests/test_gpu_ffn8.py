@@ -215,6 +215,31 @@ def test_product_repeats_bit_for_bit(n, k, features):
     assert all(torch.equal(o[:, :features], outs[0][:, :features]) for o in outs)
 
 
+@pytest.mark.parametrize("n", [2, 50, 300])
+def test_products_of_scales_out_of_range(n):
+    """NaN, infinite, zero and very small scales do to a product what they do to the values they stand for."""
+    rng = np.random.default_rng(n)
+    k, features = 400, 272
+    x, xv, xs, xsv = make_codes(rng, n, k, (n, 4))
+    w, wv, ws, wsv = make_codes(rng, features, k, (3, 4), 0.05)
+    xsv[0, 1], xsv[1, 3] = np.nan, 2.0 ** -100
+    wsv[2, 0], wsv[1, 2] = np.inf, 0.0
+    xs, ws = dev(xsv), dev(wsv)
+    out = torch.empty((n, features), device="cuda")
+    hc.hc_mul8(x, k, xs, w, k, ws, n, hc.mul8(features, k, hc.HC_F32), out, features)
+    h, hs = torch.empty((n, features), dtype=E4M3, device="cuda"), torch.empty((n, 3), device="cuda")
+    hc.hc_gated_mul8(x, k, xs, w, ws, w, ws, k, n, hc.gated8(features, k), h, features, hs)
+    no_error()
+    got = f64(out)
+    assert np.isnan(got[0]).all() and (~np.isfinite(got[1:, 256:])).all()
+    fine = np.nan_to_num(wsv, posinf=0.0)
+    ref, e = fr.product(xv[1:], xsv[1:], wv, fine)
+    assert_within(got[1:, :256], ref[:, :256], e[:, :256])
+    hv = f64(h) * fr.spread(f64(hs), features)
+    assert np.isnan(hv[0]).all() and np.isnan(hv[1:, 256:]).all()
+    check_codes(f64(h)[1:, :256], f64(hs)[1:, :2], *[v[:, :256] for v in fr.gated(xv[1:], xsv[1:], wv, fine, wv, fine, "silu")])
+
+
 # ---- log probabilities ----------------------------------------------------------------------------------
 
 def check_logprobs(z, tokens, scale, top, x64=None, stride=None):
@@ -467,6 +492,43 @@ def test_two_graphs_and_an_eager_call_at_once():
     for (ffn, y, delta, _), w in zip(runs, want):
         assert torch.equal(delta, w)
         ffn.check(y, delta)
+
+
+FIRST_CALLS = """
+import sys
+import torch
+import hyper_connection_residual_hc_gb300 as hc
+
+torch.zeros(1, device="cuda")
+hc.load()
+n, k, f = int(sys.argv[1]), 1152, 272
+e = lambda *s, t=torch.float32: torch.ones(s, device="cuda").to(t)
+x, w, u, xs, ws = e(n, k, t=torch.float8_e4m3fn), e(f, k, t=torch.float8_e4m3fn), e(f, k, t=torch.float8_e4m3fn), e(n, 9), e(3, 9) / k
+y, h, hs, out = e(n, k, t=torch.bfloat16), e(n, f, t=torch.float8_e4m3fn), e(n, 3), e(n, f)
+tokens, lp = torch.zeros(n, dtype=torch.int64, device="cuda"), e(n)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):  # the process's first calls
+    hc.hc_norm_quant8(y, k, None, 0, None, hc.quant8(n, k), None, 0, x, k, xs)
+    hc.hc_mul8(x, k, xs, w, k, ws, n, hc.mul8(f, k, hc.HC_F32), out, f)
+    hc.hc_gated_mul8(x, k, xs, w, ws, u, ws, k, n, hc.gated8(f, k), h, f, hs)
+    hc.hc_token_logprobs(out, f, tokens, hc.logprobs(n, f), lp, None, None, None)
+g.replay()
+torch.cuda.synchronize()
+assert hc.hc_device_error(clear=True) == 0
+assert torch.allclose(out, torch.ones_like(out), rtol=1e-5) and torch.allclose(h.float() * hs[0, 0], torch.full((n, f), 0.7310586, device="cuda"), rtol=1e-4)
+assert torch.allclose(lp, torch.full_like(lp, -5.605802), rtol=1e-5)
+"""
+
+
+@pytest.mark.parametrize("n", [1, 40, 100, 400])
+def test_first_calls_of_a_process_captured(n):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS, str(n)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
 
 
 def test_rows_past_32_bits():
