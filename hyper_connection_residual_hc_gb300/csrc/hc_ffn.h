@@ -23,6 +23,27 @@ __host__ __device__ constexpr int blocks8(int n) { return (n + kBlock8 - 1) / kB
 constexpr float kTop8 = 448.f;
 constexpr float kLeastTop8 = 0x1p-64f;
 
+// The kernels may start under the end of the kernel ahead on their stream (they wait for it before they touch memory): 256 tokens by
+// 20,480 x 5,120 30.4 -> 28.8 us in a graph, 32.9 -> 30.1 called one by one. Such a launch takes the host 1 us longer, which counts
+// where the host is what one waits for (64 rows of 5,120 quantised: 11.7 us a call, 12.5 so launched), so that short kernels are
+// launched plainly; `in_graphs`: unless they go into a graph. That is for the products, whose CTAs have much to set up (one token by
+// 5,120 x 5,120 6.5 -> 5.8 us); many small CTAs that only wait are slower (1,027 rows of 2,000 quantised 4.3 -> 5.5 us). `ns`: about how
+// long the kernel takes.
+inline int programmatic_launch(long long ns, bool in_graphs, cudaStream_t stream, cudaLaunchAttribute* a) {
+    if (ns < 12000) {
+        if (!in_graphs) return 0;
+        cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(stream, &s) != cudaSuccess) {
+            cudaGetLastError();  // (another stream's capture forbids the question, and the launch will tell)
+            return 0;
+        }
+        if (s != cudaStreamCaptureStatusActive) return 0;
+    }
+    a->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a->val.programmaticStreamSerializationAllowed = 1;
+    return 1;
+}
+
 // ---- norm and quantisation (hc_quant8.cu) ----------------------------------------------------------
 struct Quant8Args {
     const void* x;         // bf16

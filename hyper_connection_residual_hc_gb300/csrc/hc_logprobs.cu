@@ -198,6 +198,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
     using C = Chunk<kWide>;
     constexpr int kEach = C::kEach;
     __shared__ __align__(16) Shared sh;
+    griddep_launch_dependents();
+    griddep_wait();
     const int t = threadIdx.x, warp = t / 32, lane = t % 32;
     const int rank = ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
     const long long row = blockIdx.x / static_cast<unsigned>(ctas);
@@ -502,12 +504,17 @@ cudaError_t start(const LogprobArgs& a, int ctas, cudaStream_t stream) {
     cfg.gridDim = dim3(static_cast<unsigned>(a.n * ctas));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(ctas);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    cudaLaunchAttribute attrs[2];
+    unsigned more = 0;
+    if (ctas > 1) {
+        attrs[0].id = cudaLaunchAttributeClusterDimension;
+        attrs[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+        attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+        more = 1;
+    }
+    more += static_cast<unsigned>(programmatic_launch(a.n * a.vocab / 600, false, stream, attrs + more));  // (0.5 to 1.5 values a ps)
+    cfg.attrs = attrs;
+    cfg.numAttrs = more;
     return cudaLaunchKernelEx(&cfg, logprob_kernel<kWide>, a, ctas);
 }
 

@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(Plan<kN, kGated, kPerSm>::kThreads, kPerSm)
 mul8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_up,
                  const __grid_constant__ Params p) {
     using P = Plan<kN, kGated, kPerSm>;
+    let_next_start();
     extern __shared__ unsigned char raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -110,6 +111,7 @@ mul8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(at + (slot - base));
+    griddep_wait();  // what the kernels ahead write and read
 
     if (warp == P::kAddWarps) {  // ---- loads
         if (lane == 0) {
@@ -378,12 +380,12 @@ struct Rows {
         cfg.blockDim = dim3(P::kThreads);
         cfg.dynamicSmemBytes = P::kSmem;
         cfg.stream = stream;
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = static_cast<unsigned>(r.ctas);
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
+        cudaLaunchAttribute attrs[2];
+        attrs[0].id = cudaLaunchAttributeClusterDimension;
+        attrs[0].val.clusterDim.x = static_cast<unsigned>(r.ctas);
+        attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+        cfg.attrs = attrs;
+        cfg.numAttrs = 1 + static_cast<unsigned>(programmatic_launch(r.ns, true, stream, attrs + 1));
         g_launched.store(true, std::memory_order_relaxed);
         return cudaLaunchKernelEx(&cfg, &mul8_rows_kernel<kN, kGated, kPerSm>, tm_x, tm_w, tm_up, p) == cudaSuccess ? 0 : -7;
     }

@@ -287,6 +287,7 @@ template <bool kGated, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_up,
                   const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ Params p) {
+    let_next_start();
     extern __shared__ unsigned char raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     unsigned char* at = raw + (base - smem_u32(raw));
@@ -328,6 +329,7 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     cluster_sync8();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(at + (slot - base));
+    griddep_wait();  // what the kernels ahead write and read
 
     if (warp >= kAddWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -622,18 +624,18 @@ struct Maps {
 };
 
 template <bool kGated, bool kSplit>
-cudaError_t start(const Maps& m, const Params& p, unsigned ctas, int cluster, cudaStream_t stream) {
+cudaError_t start(const Maps& m, const Params& p, unsigned ctas, int cluster, long long ns, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeClusterDimension;
+    attrs[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 1 + static_cast<unsigned>(programmatic_launch(ns, true, stream, attrs + 1));
     return cudaLaunchKernelEx(&cfg, &mul8_tiles_kernel<kGated, kSplit>, m.x, m.w, m.up, m.out, p);
 }
 
@@ -691,19 +693,20 @@ int start(const Mul8Args& a, cudaStream_t stream) {
     if (kGated && !mul8_map(&m.up, a.up, a.k, a.features, a.w_stride, kHalf / 2)) return -7;
     const long long tiles = shape.tiles;
     const Schedule plan = schedule(tiles, p.k_blocks, fit);
+    const long long ns = mul8_tiles_ns(a);
     g_launched.store(true, std::memory_order_relaxed);
     if (plan.whole > 0) {
         p.first = 0;
         p.until = plan.whole;
         const long long pairs = fit[1].load(std::memory_order_relaxed);
         p.pairs = static_cast<int>(plan.whole < pairs ? plan.whole : pairs);
-        if (start<kGated, false>(m, p, static_cast<unsigned>(2 * p.pairs), 2, stream) != cudaSuccess) return -7;
+        if (start<kGated, false>(m, p, static_cast<unsigned>(2 * p.pairs), 2, ns, stream) != cudaSuccess) return -7;
     }
     if (plan.whole < tiles) {
         p.first = plan.whole;
         p.until = tiles;
         p.pairs = plan.split;
-        if (start<kGated, true>(m, p, static_cast<unsigned>((tiles - plan.whole) * 2 * plan.split), 2 * plan.split, stream) != cudaSuccess) return -7;
+        if (start<kGated, true>(m, p, static_cast<unsigned>((tiles - plan.whole) * 2 * plan.split), 2 * plan.split, ns, stream) != cudaSuccess) return -7;
     }
     return 0;
 }

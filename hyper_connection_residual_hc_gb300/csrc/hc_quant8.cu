@@ -40,6 +40,8 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
 template <int kVecs, bool kResidual>
 __global__ void __launch_bounds__(kVecs < 4 ? 128 : 1024) quant8_kernel(const Quant8Args p, int row_threads) {
     __shared__ float part[32];
+    let_next_start();
+    griddep_wait();
     const int t = threadIdx.x % row_threads, lane = threadIdx.x % 32;
     const long long row = static_cast<long long>(blockIdx.x) * (blockDim.x / row_threads) + threadIdx.x / row_threads;
     if (row >= p.n) return;  // (whole warps; a block of several rows has no barrier)
@@ -126,30 +128,31 @@ __global__ void __launch_bounds__(kVecs < 4 ? 128 : 1024) quant8_kernel(const Qu
 }
 
 template <int kVecs>
-void start(const Quant8Args& a, int row_threads, int rows, cudaStream_t stream) {
-    const unsigned blocks = static_cast<unsigned>((a.n + rows - 1) / rows), threads = static_cast<unsigned>(row_threads * rows);
-    if (a.residual)
-        quant8_kernel<kVecs, true><<<blocks, threads, 0, stream>>>(a, row_threads);
-    else
-        quant8_kernel<kVecs, false><<<blocks, threads, 0, stream>>>(a, row_threads);
+cudaError_t start(const Quant8Args& a, int row_threads, int rows, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((a.n + rows - 1) / rows));
+    cfg.blockDim = dim3(static_cast<unsigned>(row_threads * rows));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    cfg.attrs = &attr;
+    cfg.numAttrs = static_cast<unsigned>(programmatic_launch(a.n * a.d * (a.residual ? 7 : 3) / 6500, false, stream, &attr));
+    return cudaLaunchKernelEx(&cfg, a.residual ? quant8_kernel<kVecs, true> : quant8_kernel<kVecs, false>, a, row_threads);
 }
 
 }  // namespace
 
 int launch_norm_quant8(const Quant8Args& a, cudaStream_t stream) {
     const int vecs = a.d / 8;
-    if (vecs <= 32) {
-        start<1>(a, 32, 4, stream);
-    } else if (vecs <= 64) {
-        start<2>(a, 32, 4, stream);
-    } else if (vecs <= 1024 * 4) {
-        const int threads = (vecs + 4 * 32 - 1) / (4 * 32) * 32;
-        start<4>(a, threads, 1, stream);
-    } else {
-        const int threads = (vecs + 8 * 32 - 1) / (8 * 32) * 32;
-        start<8>(a, threads, 1, stream);
-    }
-    return cudaGetLastError() == cudaSuccess ? 0 : -7;
+    cudaError_t e;
+    if (vecs <= 32)
+        e = start<1>(a, 32, 4, stream);
+    else if (vecs <= 64)
+        e = start<2>(a, 32, 4, stream);
+    else if (vecs <= 1024 * 4)
+        e = start<4>(a, (vecs + 4 * 32 - 1) / (4 * 32) * 32, 1, stream);
+    else
+        e = start<8>(a, (vecs + 8 * 32 - 1) / (8 * 32) * 32, 1, stream);
+    return e == cudaSuccess ? 0 : -7;
 }
 
 }  // namespace hc
