@@ -57,6 +57,7 @@ struct Params {
     int pairs;   // of the grid, which take tiles in turn; with kSplit the pairs of a cluster, which share one tile's blocks of k
     int stored;  // features that TMA stores: whole 16 bytes of a row
     long long first, until;  // tiles
+    int beside;  // the second launch of a call
 };
 
 __device__ __forceinline__ void tmem_alloc2(uint32_t dst, uint32_t ncols) {
@@ -287,7 +288,6 @@ template <bool kGated, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_up,
                   const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ Params p) {
-    let_next_start();
     extern __shared__ unsigned char raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     unsigned char* at = raw + (base - smem_u32(raw));
@@ -329,7 +329,10 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     cluster_sync8();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(at + (slot - base));
-    griddep_wait();  // what the kernels ahead write and read
+    // What the kernels ahead write and read. The tiles that a call's second launch takes are not the first one's: it starts beside that
+    // (which has let it start behind its own wait) and waits for its end at its own.
+    if (!p.beside) griddep_wait();
+    griddep_launch_dependents();
 
     if (warp >= kAddWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -582,6 +585,7 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         tc_fence_after();
         tmem_dealloc2(tmem, 512);
     }
+    if (p.beside) griddep_wait();
 }
 
 bool out_map(CUtensorMap* m, const Mul8Args& a, int stored) {
@@ -698,6 +702,7 @@ int start(const Mul8Args& a, cudaStream_t stream) {
     if (plan.whole > 0) {
         p.first = 0;
         p.until = plan.whole;
+        p.beside = 0;
         const long long pairs = fit[1].load(std::memory_order_relaxed);
         p.pairs = static_cast<int>(plan.whole < pairs ? plan.whole : pairs);
         if (start<kGated, false>(m, p, static_cast<unsigned>(2 * p.pairs), 2, ns, stream) != cudaSuccess) return -7;
@@ -705,6 +710,7 @@ int start(const Mul8Args& a, cudaStream_t stream) {
     if (plan.whole < tiles) {
         p.first = plan.whole;
         p.until = tiles;
+        p.beside = plan.whole > 0 ? 1 : 0;
         p.pairs = plan.split;
         if (start<kGated, true>(m, p, static_cast<unsigned>((tiles - plan.whole) * 2 * plan.split), 2 * plan.split, ns, stream) != cudaSuccess) return -7;
     }
