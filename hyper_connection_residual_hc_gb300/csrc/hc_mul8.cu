@@ -13,6 +13,11 @@
 // does not depend on timing.
 //
 // Warps: one issues TMA loads (a ring of k blocks: 128 x 128 bytes of weights, the tokens' block), one the MMAs, 4 or 8 add up.
+//
+// Measured: one token by 20,480 x 5,120 20 us (16 of it reading, at 6.6 TB/s; the rest is launch, set-up and the join), by 5,120 x 5,120 5.8
+// in a graph, 33 tokens by 5,120 x 100,003 87 us (89% of the copy rate); gated, one token by 5,120 x 20,480 35 us. With more than 128
+// tokens, or gated more than 64, hc_mul8_tiles.cu is faster nearly always: its adding warps have one factor a thread, these have one
+// a column, from shared memory. launch_mul8 compares the two kernels' estimated times.
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -303,9 +308,10 @@ mul8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 }
 
 // CTAs of a cluster: as many as let all clusters run at once, at least 2 blocks of k for each. One more and some clusters wait for others to
-// end, which costs more than fewer readers do: 20,480 x 5,120 weights (40 tiles) and one token 19.7 us in clusters of 4, 19.4 of 5,
-// 25.2 of 7 (all 8 parts of the GPU hold 4 clusters of 7, some 5); gate and up of 5,120 x 20,480 (160 tiles) 35.8 us in clusters of
-// 1, 42.3 of 2. `fit`: clusters of each size that run at once.
+// end, which costs more than fewer readers do: 20,480 x 5,120 weights (40 tiles) and one token 20.2 us in clusters of 3, 19.7 of 4, 19.4 of
+// 5, 25.2 of 7; gate and up of 5,120 x 20,480 (160 tiles) 35.8 us in clusters of 1, 42.3 of 2. `fit`: clusters of each size that run
+// at once, as the runtime tells; it counts one CTA an SM for a kernel with tensor memory, though two of the smaller ones share
+// one, so that it leaves something over.
 int cluster_ctas(long long units, int k_blocks, const std::atomic<int>* fit) {
     int c = 1;
     for (int more = 2; more <= kMostCluster && 2 * more <= k_blocks; ++more)
