@@ -11,10 +11,6 @@
 
 namespace hc {
 
-// First thing in every kernel of these operators, which are launched as programmatic dependents: the kernel behind may start as SMs get
-// free, and set itself up under the end of this one.
-__device__ __forceinline__ void let_next_start() { griddep_launch_dependents(); }
-
 // A bounded wait: on expiry it notes so in the error word and in the CTA's `abort`, after which no wait of the CTA lasts.
 struct Wait8 {
     volatile uint32_t* abort;

@@ -163,9 +163,8 @@ __device__ __forceinline__ float ld_cluster_f1(uint32_t addr) {
 
 // With kSplit, by the adding warps of all pairs of the cluster: their sums of a tile are added up in the order of the pairs. Each
 // thread puts its columns into shared memory, over the ring (the last block's MMAs are done, so all copies are), 4 at a time:
-// [column / 4][token][4]. Then
-// the columns are dealt out 16 at a time: a pair takes every p.pairs-th of each half (of a gated product 16 features with their 16
-// columns of up), reads them from all pairs and writes the result.
+// [column / 4][token][4]. Then the columns are dealt out 16 at a time: a pair takes every p.pairs-th of each half (of a gated
+// product 16 features with their 16 columns of up), reads them from all pairs and writes the result.
 template <bool kGated>
 __device__ __forceinline__ void join_parts(const Params& p, const Tile& t, const uint64_t (&acc)[64], uint32_t base, unsigned char* at, int half, int in_cta,
                                            int rank, int pair) {

@@ -44,7 +44,7 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
 template <int kVecs, bool kResidual>
 __global__ void __launch_bounds__(kVecs < 4 ? 128 : 1024) quant8_kernel(const Quant8Args p, int row_threads) {
     __shared__ float part[32];
-    let_next_start();
+    griddep_launch_dependents();
     griddep_wait();
     const int t = threadIdx.x % row_threads, lane = threadIdx.x % 32;
     const long long row = static_cast<long long>(blockIdx.x) * (blockDim.x / row_threads) + threadIdx.x / row_threads;

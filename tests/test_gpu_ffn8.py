@@ -143,7 +143,7 @@ def make_codes(rng, rows, cols, scales_shape, size=1.0, stride=None):
 
 
 SHAPES = [(1, 128, 128), (1, 16, 1), (2, 144, 130), (3, 1280, 257), (16, 2048, 384), (17, 400, 7), (31, 5120, 200), (33, 1152, 640), (64, 256, 1000), (65, 640, 129),
-          (100, 272, 260), (128, 1024, 512), (129, 512, 300), (200, 2064, 272), (257, 384, 1027), (300, 1040, 513), (515, 896, 768), (400, 2448, 130), (270, 4112, 1544), (2100, 4112, 2600)]
+          (100, 272, 260), (128, 1024, 512), (129, 512, 300), (200, 2064, 272), (257, 384, 1027), (300, 1040, 513), (515, 896, 768), (400, 2448, 130), (270, 4112, 1544), (2100, 8208, 2600)]
 
 
 @pytest.mark.parametrize("wide", [False, True])
@@ -492,6 +492,51 @@ def test_two_graphs_and_an_eager_call_at_once():
     for (ffn, y, delta, _), w in zip(runs, want):
         assert torch.equal(delta, w)
         ffn.check(y, delta)
+
+
+@pytest.mark.parametrize("n,d,f", [(3, 640, 1296), (70, 512, 1040), (300, 1152, 2064), (2100, 2608, 8208)])
+def test_chain_of_dependent_calls(n, d, f):
+    """Calls that start under each other's end wait for each other's results: a chain without a pause, and replayed from a graph, gives
+    the bytes of the chain with a synchronisation behind every call. (The last shape takes two launches for the way back.)"""
+    rng = np.random.default_rng(n)
+    layers = [Ffn(rng, n, d, f) for _ in range(2)]
+    y0 = dev(rng.standard_normal((n, d)), torch.bfloat16)
+    bufs = [torch.empty((n, d), dtype=torch.bfloat16, device="cuda") for _ in range(7)]
+    gain = dev(1 + 0.1 * rng.standard_normal(d))
+
+    def chain(sync):
+        y = y0
+        for i, b in enumerate(bufs):
+            ffn = layers[i % 2]
+            hc.hc_norm_quant8(y, d, y0, d, gain, hc.quant8(n, d), None, 0, ffn.c, d, ffn.s)
+            sync()
+            hc.hc_gated_mul8(ffn.c, d, ffn.s, ffn.gate[0], ffn.gate[2], ffn.up[0], ffn.up[2], d, n, hc.gated8(f, d), ffn.hc_, f, ffn.hs)
+            sync()
+            hc.hc_mul8(ffn.hc_, f, ffn.hs, ffn.down[0], f, ffn.down[2], n, hc.mul8(d, f), b, d)
+            sync()
+            y = b
+
+    chain(torch.cuda.synchronize)
+    want = [b.clone() for b in bufs]
+    for _ in range(3):
+        for b in bufs:
+            b.fill_(float("nan"))
+        chain(lambda: None)
+        no_error()
+        assert all(torch.equal(b, w) for b, w in zip(bufs, want))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        chain(lambda: None)
+    for _ in range(3):
+        for b in bufs:
+            b.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        g.replay()
+        no_error()
+        assert all(torch.equal(b, w) for b, w in zip(bufs, want))
 
 
 FIRST_CALLS = """
