@@ -597,3 +597,58 @@ def test_rows_past_32_bits():
     no_error()
     ref, e = fr.product(xv, xsv, wv, wsv)
     assert_within(f64(out), ref, e)
+
+
+@pytest.mark.parametrize("n", [20, 300])
+def test_wide_strides_of_products(n):
+    """Rows of weights and of outputs that start past 2^32 bytes, by either kernel."""
+    rng = np.random.default_rng(n)
+    k, features, pitch = 272, 272, 1 << 24
+    x, xv, xs, xsv = make_codes(rng, n, k, (n, 3))
+    raw = torch.zeros((features - 1) * pitch + 1024, dtype=torch.uint8, device="cuda")
+    w = raw.as_strided((features, k), (pitch, 1))
+    cw, wv, ws, wsv = make_codes(rng, features, k, (3, 3), 0.1)
+    w.copy_(cw.view(torch.uint8))
+    buf = torch.zeros((n - 1) * pitch + 1024, device="cuda")
+    out = buf.as_strided((n, features), (pitch, 1))
+    hc.hc_mul8(x, k, xs, w, pitch, ws, n, hc.mul8(features, k, hc.HC_F32), out, pitch)
+    no_error()
+    ref, e = fr.product(xv, xsv, wv, wsv)
+    assert_within(f64(out), ref, e)
+    h = buf.view(torch.uint8).as_strided((n, features), (4 * pitch, 1))
+    hs = torch.empty((n, 3), device="cuda")
+    hc.hc_gated_mul8(x, k, xs, w, ws, w, ws, pitch, n, hc.gated8(features, k), h, 4 * pitch, hs)
+    no_error()
+    ref, e = fr.gated(xv, xsv, wv, wsv, wv, wsv, "silu")
+    check_codes(f64(h.contiguous().view(E4M3)), f64(hs), ref, e)
+
+
+def test_norm_quant_rows_past_32_bits():
+    rng = np.random.default_rng(2)
+    n, d, pitch = 3, 1040, 1 << 31
+    buf = torch.zeros(2 * pitch + 4096, dtype=torch.bfloat16, device="cuda")
+    x, r = buf.as_strided((n, d), (pitch, 1)), buf.as_strided((n, d), (pitch, 1), 2048)
+    x.copy_(dev(rng.standard_normal((n, d)), torch.bfloat16))
+    r.copy_(dev(rng.standard_normal((n, d)), torch.bfloat16))
+    want = (x.float() + r.float()).to(torch.bfloat16)
+    codes, scales = torch.empty((n, d), dtype=E4M3, device="cuda"), torch.empty((n, 9), device="cuda")
+    hc.hc_norm_quant8(x, pitch, r, pitch, None, hc.quant8(n, d), r, pitch, codes, d, scales)
+    no_error()
+    assert torch.equal(r, want)
+    y = fr.norm(f64(want), None, 1e-6)
+    check_codes(f64(codes), f64(scales), y, (d / 2 + 16) * fr.U * np.abs(y))
+
+
+@pytest.mark.parametrize("n", [2, 40, 260])
+def test_longest_k(n):
+    rng = np.random.default_rng(n)
+    k, features = 1 << 20, 16
+    x, xv, xs, xsv = make_codes(rng, n, k, (n, k // 128))
+    w, wv, ws, wsv = make_codes(rng, features, k, (1, k // 128), 0.01)
+    out = torch.empty((n, features), device="cuda")
+    hc.hc_mul8(x, k, xs, w, k, ws, n, hc.mul8(features, k, hc.HC_F32), out, features)
+    no_error()
+    # (8,192 blocks are added up one after the other by as few as one thread)
+    a, b = dev(xv * fr.spread(xsv, k), torch.float64), dev(wv * fr.spread(wsv, k, features), torch.float64)
+    ref, mag = f64(a @ b.T), f64(a.abs() @ b.abs().T)
+    assert_within(f64(out), ref, (2 * fr.BLOCK + k // 128 + 16) * fr.U * mag)
