@@ -37,6 +37,7 @@ namespace {
 
 __device__ unsigned int g_hc_logprob_error = 0;
 std::atomic<bool> g_launched{false};
+constexpr int kDevices = 64;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kVecs = 4;                                // vectors of a thread in a chunk
@@ -45,6 +46,7 @@ static_assert(kWarps * kPosted == 32 && kMostTop <= 32, "a lane for each");
 constexpr int kBuffer = 96;                             // candidates of a warp
 static_assert(kBuffer % 32 == 0 && kBuffer >= 2 * kMostTop + 32 - 1, "room for one of each lane behind a ranked list");
 constexpr int kChunk = kThreads * kVecs;
+constexpr int kSlots = 3;                               // chunks in shared memory: one in work, two on their way
 constexpr float kFar = -256.f;                          // 2^t is 0 in fp32 from -150 on
 
 struct Sums {
@@ -99,9 +101,11 @@ __device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t addr) {
 }
 
 struct Shared {
-    uint4 chunk[kVecs][kThreads];  // values that their threads look at one by one
+    union {
+        uint4 ring[kSlots][kVecs][kThreads];  // a thread's vectors are its own
+        unsigned long long candidates[kWarps * kBuffer + 2];  // once the last chunk is done with
+    };
     __align__(16) unsigned long long buffer[kWarps][kBuffer];
-    __align__(16) unsigned long long candidates[kWarps * kBuffer + 2];
     unsigned long long list[kMostTop];
     unsigned long long last[kMostTop];  // the list of a cluster's CTA, 0 where there is none
     float total[3];                     // its sums
@@ -109,6 +113,19 @@ struct Shared {
     __align__(16) uint32_t posted[kWarps * kPosted];
     int count;
 };
+
+// 16 bytes of global memory to shared memory, behind the thread's back.
+__device__ __forceinline__ void copy_ahead(uint4* to, const uint4* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits for all but the last n groups of copies.
+template <int n>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+
+static_assert(4 * (sizeof(Shared) + 1024) <= 228 * 1024, "four CTAs an SM");
 
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
@@ -142,7 +159,6 @@ struct Chunk {
         }
     }
     static constexpr uint32_t kNone = kWide ? 0xFF800000u : 0xFF80FF80u;  // minus infinity
-    __device__ __forceinline__ void clear(int j) { v[j] = make_uint4(kNone, kNone, kNone, kNone); }
 };
 
 template <bool kWide>
@@ -201,7 +217,8 @@ template <bool kWide>
 __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs p, int ctas) {
     using C = Chunk<kWide>;
     constexpr int kEach = C::kEach;
-    __shared__ __align__(16) Shared sh;
+    extern __shared__ __align__(16) unsigned char smem[];
+    Shared& sh = *reinterpret_cast<Shared*>(smem);
     griddep_launch_dependents();
     griddep_wait();
     const int t = threadIdx.x, warp = t / 32, lane = t % 32;
@@ -267,36 +284,47 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
     };
     if (t == 0) sh.count = 0;
 
-    // Vector j of chunk i; minus infinity in the place of what is not there.
+    // Chunk i on its way to a slot; minus infinity in the place of what is not there.
+    const uint4* ahead = reinterpret_cast<const uint4*>(base) + v0 + t;
     C x;
-    auto load = [&](int i, int j) {
-        const int vec = v0 + i * kChunk + j * kThreads + t;
-        const uint4* from = reinterpret_cast<const uint4*>(base) + vec;
+    auto load = [&](int i, int slot) {
+        uint4* const to = &sh.ring[slot][0][t];
         if (v0 + (i + 1) * kChunk <= v1) {
-            x.v[j] = __ldcs(from);
-        } else {
-            x.clear(j);
-            if (i < chunks && vec < v1) x.v[j] = __ldcs(from);
-        }
-    };
-    auto load_last = [&]() {  // the values behind the whole vectors
-        x.clear(0);
-        if (t != 0) return;
-#pragma unroll 1
-        for (int e = p.vocab - 1; e >= whole * kEach; --e) {  // (shifted in from below)
-            const uint32_t u = kWide ? reinterpret_cast<const uint32_t*>(base)[e] : reinterpret_cast<const uint16_t*>(base)[e];
-            uint4& v = x.v[0];
-            if constexpr (kWide)
-                v = make_uint4(u, v.x, v.y, v.z);
-            else
-                v = make_uint4(v.x << 16 | u, v.y << 16 | v.x >> 16, v.z << 16 | v.y >> 16, v.w << 16 | v.z >> 16);
-        }
-    };
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) load(0, j);
-    if (chunks == 0) load_last();
+            for (int j = 0; j < kVecs; ++j) copy_ahead(to + j * kThreads, ahead + j * kThreads);
+        } else if (i < all_chunks) {
+            const uint4 nothing = make_uint4(C::kNone, C::kNone, C::kNone, C::kNone);
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) {
+                if (i < chunks && v0 + i * kChunk + j * kThreads + t < v1)
+                    copy_ahead(to + j * kThreads, ahead + j * kThreads);
+                else
+                    to[j * kThreads] = nothing;
+            }
+            if (i == chunks && t == 0) {  // the values behind the whole vectors
 #pragma unroll 1
-    for (int i = 0; i < all_chunks; ++i) {
+                for (int e = whole * kEach; e < p.vocab; ++e) {
+                    if constexpr (kWide)
+                        reinterpret_cast<uint32_t*>(to)[e - whole * kEach] = reinterpret_cast<const uint32_t*>(base)[e];
+                    else
+                        reinterpret_cast<uint16_t*>(to)[e - whole * kEach] = reinterpret_cast<const uint16_t*>(base)[e];
+                }
+            }
+        }
+        ahead += kChunk;
+        copies_end();
+    };
+    static_assert(kSlots == 3, "two chunks ahead");
+    load(0, 0);
+    load(1, 1);
+    int slot = 0;
+#pragma unroll 1
+    for (int i = 0; i < all_chunks; ++i, slot = slot == kSlots - 1 ? 0 : slot + 1) {
+        wait_copies<kSlots - 2>();
+        const uint4* const here = &sh.ring[slot][0][t];
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) x.v[j] = here[j * kThreads];
+        load(i + kSlots - 1, slot == 0 ? kSlots - 1 : slot - 1);
         float best[kVecs];
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) best[j] = x.largest(j);
@@ -324,7 +352,6 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
                 if (all || most >= from) {
 #pragma unroll
                     for (int j = 0; j < kVecs; ++j) {
-                        sh.chunk[j][t] = x.v[j];
                         if (all || best[j] >= from) {
 #pragma unroll
                             for (int e = 0; e < kEach; ++e) mask |= (all || x.at(j, e) >= from ? 1u : 0u) << (j * kEach + e);
@@ -336,8 +363,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
                     if (mask) {
                         const int bit = __ffs(static_cast<int>(mask)) - 1, j = bit / kEach, e = bit % kEach, vec = b + t + j * kThreads, index = vec * kEach + e;
                         mask &= mask - 1;
-                        const float v = kWide ? reinterpret_cast<const float*>(&sh.chunk[j][t])[e]
-                                              : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(&sh.chunk[j][t])[e]) << 16);
+                        const float v = kWide ? reinterpret_cast<const float*>(here + j * kThreads)[e]
+                                              : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(here + j * kThreads)[e]) << 16);
                         if (vec < until && index < p.vocab) key = make_key(rising(v), index);
                         if (key <= own) key = 0;
                     }
@@ -381,29 +408,23 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
                         w[k] = fmaf(f, d[k], w[k]);
                     }
                 }
-                load(i + 1, j);
             }
             const float off = -fmaf(sum.m, c, -mc), f = ex2(off);
             s[0] = (s[0] + s[1]) * f;
             w[0] = fmaf(s[0], off, (w[0] + w[1]) * f);
         } else {  // so far out that the rounding would be whole doublings
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) sh.chunk[j][t] = x.v[j];
 #pragma unroll 1
             for (int k = 0; k < kVecs * kEach; ++k) {
-                const uint4* v = &sh.chunk[k / kEach][t];
+                const uint4* v = here + k / kEach * kThreads;
                 const float u = kWide ? reinterpret_cast<const float*>(v)[k % kEach]
                                       : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(v)[k % kEach]) << 16);
                 const float d = (u - sum.m) * c, f = ex2(d);
                 s[0] += f;
                 if (f != 0.f) w[0] = fmaf(f, d, w[0]);  // (below the lowest number there is minus infinity)
             }
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) load(i + 1, j);
         }
         sum.s += s[0];
         sum.w += w[0];
-        if (i + 1 == chunks) load_last();
     }
     __syncthreads();
     if (p.top > 0) {
@@ -504,9 +525,18 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
 
 template <bool kWide>
 cudaError_t start(const LogprobArgs& a, int ctas, cudaStream_t stream) {
+    static std::atomic<bool> ready[kDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(logprob_kernel<kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.n * ctas));
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = stream;
     cudaLaunchAttribute attrs[2];
     unsigned more = 0;
