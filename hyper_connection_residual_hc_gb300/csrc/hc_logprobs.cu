@@ -100,6 +100,10 @@ __device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ unsigned long long pair(float a, float b) { unsigned long long r; asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b)); return r; }
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) { unsigned long long r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c)); return r; }
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) { unsigned long long r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
+
 struct Shared {
     union {
         uint4 ring[kSlots][kVecs][kThreads];  // a thread's vectors are its own
@@ -112,6 +116,8 @@ struct Shared {
     float warp_sums[kWarps][3];
     __align__(16) uint32_t posted[kWarps * kPosted];
     int count;
+    uint32_t given;  // the given token's logit, or the word that holds it
+    __align__(8) long long token;
 };
 
 // 16 bytes of global memory to shared memory, behind the thread's back.
@@ -168,22 +174,21 @@ __device__ __forceinline__ float logit(const LogprobArgs& p, long long row, int 
     return __bfloat162float(static_cast<const __nv_bfloat16*>(p.logits)[at]);
 }
 
-// How many of `total` keys are above `mine`; keys[total] is 0 if total is odd.
+// How many of `total` keys are above `mine`
 __device__ __forceinline__ int keys_above(const unsigned long long* keys, int total, unsigned long long mine) {
     const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(keys);
     int above = 0;
 #pragma unroll 8
-    for (int j = 0; j < (total + 1) / 2; ++j) {
+    for (int j = 0; j < total / 2; ++j) {
         const ulonglong2 k = pairs[j];
         above += (k.x > mine) + (k.y > mine);
     }
+    if (total % 2) above += keys[total - 1] > mine;
     return above;
 }
 
 // The first `top` of the CTA's candidates, in order, as `list`. Zeros are none.
 __device__ __forceinline__ void rank_candidates(unsigned long long* candidates, int total, int top, unsigned long long* list) {
-    if (total % 2 && threadIdx.x == 0) candidates[total] = 0;
-    __syncthreads();
     for (int i = threadIdx.x; i < total; i += kThreads) {
         const unsigned long long mine = candidates[i];
         if (mine == 0) continue;
@@ -195,8 +200,6 @@ __device__ __forceinline__ void rank_candidates(unsigned long long* candidates, 
 // The same of a warp's own buffer, in place; returns how many there are then.
 __device__ __forceinline__ int rank_buffer(unsigned long long* buffer, int count, int top) {
     const int lane = threadIdx.x % 32;
-    if (count % 2 && lane == 0) buffer[count] = 0;
-    __syncwarp();
     unsigned long long mine[kBuffer / 32];
     int above[kBuffer / 32];
 #pragma unroll
@@ -315,6 +318,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
         copies_end();
     };
     static_assert(kSlots == 3, "two chunks ahead");
+    // The given token and its logit come on the way, as at the end they would be waited for one after the other.
+    const bool gives = t == 0 && rank == 0 && p.logprob;
+    if (gives) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(&sh.token)), "l"(p.tokens + row) : "memory");
     load(0, 0);
     load(1, 1);
     int slot = 0;
@@ -324,6 +330,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
         const uint4* const here = &sh.ring[slot][0][t];
 #pragma unroll
         for (int j = 0; j < kVecs; ++j) x.v[j] = here[j * kThreads];
+        if (i == 0 && gives && sh.token >= 0 && (kWide ? sh.token : sh.token | 1) < p.vocab)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&sh.given)), "l"(base + (kWide ? sh.token * 4 : sh.token / 2 * 4)) : "memory");
         load(i + kSlots - 1, slot == 0 ? kSlots - 1 : slot - 1);
         float best[kVecs];
 #pragma unroll
@@ -334,39 +342,38 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
         if (p.top > 0) {
             const int b = i < chunks ? v0 + i * kChunk : whole, until = i < chunks ? v1 : whole + 1;
             lane_best = fmaxf(lane_best, most);
-            bool all = least <= 1;  // NaN is wanted
-            float from = all ? 0.f : falling(least);
-            bool some = __any_sync(0xFFFFFFFFu, all || most >= from);
+            float from = least <= 1 ? -INFINITY : falling(least);  // what is not below is looked at, NaN too
+            bool some = __any_sync(0xFFFFFFFFu, !(most < from));
             if (some && bounded) {
                 const uint32_t r = lane_best > -INFINITY ? rising(lane_best) : 1u;  // (what is not there is minus infinity too)
                 if (__any_sync(0xFFFFFFFFu, r > posted)) post(r);
                 if (i == 0) __syncthreads();
                 least = max(bound(), static_cast<uint32_t>(own >> 32));
-                all = least <= 1;
-                from = all ? 0.f : falling(least);
-                some = __any_sync(0xFFFFFFFFu, all || most >= from);
+                from = least <= 1 ? -INFINITY : falling(least);
+                some = __any_sync(0xFFFFFFFFu, !(most < from));
             }
             if (some) {
-                uint32_t mask = 0;
-                static_assert(kVecs * kEach <= 32, "a bit for each value");
-                if (all || most >= from) {
+                uint32_t vectors = 0, mask = 0;
+                int j = 0;
 #pragma unroll
-                    for (int j = 0; j < kVecs; ++j) {
-                        if (all || best[j] >= from) {
+                for (int k = 0; k < kVecs; ++k) vectors |= (best[k] < from ? 0u : 1u) << k;
+                while (__any_sync(0xFFFFFFFFu, (vectors | mask) != 0)) {  // one value of each lane
+                    if (mask == 0 && vectors != 0) {
+                        j = __ffs(static_cast<int>(vectors)) - 1;
+                        vectors &= vectors - 1;
+                        C one;
+                        one.v[0] = here[j * kThreads];
 #pragma unroll
-                            for (int e = 0; e < kEach; ++e) mask |= (all || x.at(j, e) >= from ? 1u : 0u) << (j * kEach + e);
-                        }
+                        for (int e = 0; e < kEach; ++e) mask |= (one.at(0, e) < from ? 0u : 1u) << e;
                     }
-                }
-                while (__any_sync(0xFFFFFFFFu, mask != 0)) {  // one of each lane
                     unsigned long long key = 0;
                     if (mask) {
-                        const int bit = __ffs(static_cast<int>(mask)) - 1, j = bit / kEach, e = bit % kEach, vec = b + t + j * kThreads, index = vec * kEach + e;
+                        const int e = __ffs(static_cast<int>(mask)) - 1, vec = b + t + j * kThreads, index = vec * kEach + e;
                         mask &= mask - 1;
                         const float v = kWide ? reinterpret_cast<const float*>(here + j * kThreads)[e]
                                               : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(here + j * kThreads)[e]) << 16);
                         if (vec < until && index < p.vocab) key = make_key(rising(v), index);
-                        if (key <= own) key = 0;
+                        if (key <= own || static_cast<uint32_t>(key >> 32) < least) key = 0;
                     }
                     uint32_t who = __ballot_sync(0xFFFFFFFFu, key != 0);
                     if (count + __popc(who) > kBuffer) {
@@ -386,6 +393,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
         // moving them together.)
         const float mc = sum.m * c;
         float s[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
+        unsigned long long s2 = 0, w2 = 0;
+        const unsigned long long c2 = pair(c, c), mc2 = pair(-mc, -mc);
         if (fabsf(mc) < 1e6f) {
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
@@ -401,14 +410,18 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
                         d[1] = high_half(u);
                     }
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        d[k] = fmaf(d[k], c, -mc);
-                        const float f = ex2(d[k]);
-                        s[k] += f;
-                        w[k] = fmaf(f, d[k], w[k]);
+                    for (int k = 0; k < 1; ++k) {
+                        const unsigned long long dd = fma2(pair(d[0], d[1]), c2, mc2);
+                        float d0, d1;
+                        asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(dd));
+                        const unsigned long long f = pair(ex2(d0), ex2(d1));
+                        s2 = add2(s2, f);
+                        w2 = fma2(f, dd, w2);
                     }
                 }
             }
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(s[0]), "=f"(s[1]) : "l"(s2));
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(w[0]), "=f"(w[1]) : "l"(w2));
             const float off = -fmaf(sum.m, c, -mc), f = ex2(off);
             s[0] = (s[0] + s[1]) * f;
             w[0] = fmaf(s[0], off, (w[0] + w[1]) * f);
@@ -426,10 +439,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
         sum.s += s[0];
         sum.w += w[0];
     }
-    __syncthreads();
+    wait_copies<0>();
     if (p.top > 0) {
+        __syncthreads();
         least = bound();
-        for (int i = lane; i < kBuffer; i += 32) {
+        for (int i = lane; i - lane < count; i += 32) {
             const unsigned long long key = i < count ? sh.buffer[warp][i] : 0;
             const bool in = key != 0 && static_cast<uint32_t>(key >> 32) >= least;
             const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
@@ -440,7 +454,6 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
         }
         __syncthreads();
         rank_candidates(sh.candidates, sh.count, p.top, sh.list);
-        __syncthreads();
     }
 
     // The CTA's sums: all lanes refer to the largest maximum, then sums add up.
@@ -490,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
                 static_assert(kThreads == 8 * kMostTop, "a thread for each key");
                 if (t < ctas * p.top)
                     sh.candidates[t] = ld_cluster_u64(in_cta(own_smem + static_cast<uint32_t>(offsetof(Shared, last) + t % p.top * 8), static_cast<uint32_t>(t / p.top)));
+                __syncthreads();
                 rank_candidates(sh.candidates, ctas * p.top, p.top, sh.list);
                 __syncthreads();
             }
@@ -503,9 +517,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
     auto log_probability = [&](float x) { return none ? -INFINITY : (x - sum.m) * p.scale - log_s; };
     if (t == 0) {
         if (p.logprob) {
-            const long long token = p.tokens[row];
+            const long long token = sh.token;
             float lp = 0.f;
-            if (token >= 0 && token < p.vocab)
+            if (token >= 0 && (kWide ? token : token | 1) < p.vocab)
+                lp = log_probability(kWide ? __uint_as_float(sh.given) : token % 2 ? high_half(sh.given) : low_half(sh.given));
+            else if (token >= 0 && token < p.vocab)  // (the last of an odd number)
                 lp = log_probability(logit<kWide>(p, row, static_cast<int>(token)));
             else if (token >= 0)
                 atomicOr(&g_hc_logprob_error, kErrToken);
