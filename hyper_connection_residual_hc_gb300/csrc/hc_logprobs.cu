@@ -45,9 +45,12 @@ constexpr int kPosted = 4;                              // numbers that a warp p
 static_assert(kWarps * kPosted == 32 && kMostTop <= 32, "a lane for each");
 constexpr int kBuffer = 96;                             // candidates of a warp
 static_assert(kBuffer % 32 == 0 && kBuffer >= 2 * kMostTop + 32 - 1, "room for one of each lane behind a ranked list");
+constexpr int kGroups = 12;                             // of chunks, whose largest logits are kept
 constexpr int kChunk = kThreads * kVecs;
 constexpr int kSlots = 3;                               // chunks in shared memory: one in work, two on their way
 constexpr float kFar = -256.f;                          // 2^t is 0 in fp32 from -150 on
+
+static_assert(kGroups * 32 * sizeof(uint16_t) == kBuffer * sizeof(unsigned long long), "a warp's own part of the same memory");
 
 struct Sums {
     float m, s, w;  // s == 0: nothing yet, m means nothing
@@ -109,7 +112,10 @@ struct Shared {
         uint4 ring[kSlots][kVecs][kThreads];  // a thread's vectors are its own
         unsigned long long candidates[kWarps * kBuffer + 2];  // once the last chunk is done with
     };
-    __align__(16) unsigned long long buffer[kWarps][kBuffer];
+    union {
+        uint16_t most[kWarps][kGroups][32];  // the largest of a lane's logits in a group of chunks, or the next bf16 above
+        __align__(16) unsigned long long buffer[kWarps][kBuffer];  // a warp's candidates, once it has been through its `most`
+    };
     unsigned long long list[kMostTop];
     unsigned long long last[kMostTop];  // the list of a cluster's CTA, 0 where there is none
     float total[3];                     // its sums
@@ -142,6 +148,9 @@ __device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+__device__ __forceinline__ uint32_t not_below2(uint32_t a, uint32_t b) {  // all ones in the halves where a is not below b
+    return __hgeu2_mask(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
 }
 __device__ __forceinline__ float low_half(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float high_half(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
@@ -250,41 +259,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
     };
     refer_to(0.f);
     // candidates
-    const bool bounded = v1 - v0 >= kThreads;               // every lane has a vector at least
     float lane_best = -INFINITY;                            // of all chunks so far
-    uint32_t posted = 0;                                    // the least that this warp has posted
-    uint32_t least = 0;                                     // logits below are not wanted
-    unsigned long long own = 0;                             // keys up to this one are not among the first `top`
-    int count = 0;                                          // in the warp's buffer
-    const volatile uint32_t* all_posted = sh.posted;
-    // Posts the largest of the lanes' maxima, in order and by one store, as they are read by one load.
-    auto post = [&](uint32_t mine) {
-        uint32_t w[kPosted];
-#pragma unroll
-        for (int k = 0; k < kPosted; ++k) {
-            w[k] = __reduce_max_sync(0xFFFFFFFFu, mine);
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine == w[k]);
-            if (lane == __ffs(static_cast<int>(who)) - 1) mine = 0;
-        }
-        posted = w[kPosted - 1];
-        static_assert(kPosted == 4, "one store");
-        if (lane == 0)
-            asm volatile("st.volatile.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(&sh.posted[warp * kPosted])), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                         : "memory");
-    };
-    // For few alternatives the top-th largest of what is posted, taken at one moment, else the least of the warps' q-th numbers, q *
-    // warps >= top, which is less, but there at once (20 alternatives, 256 rows: 31 us, 33 with the top-th largest; 1: 26 and 21).
-    auto bound = [&]() {
-        if (!bounded) return 0u;
-        if (p.top > 8) return __reduce_min_sync(0xFFFFFFFFu, all_posted[lane % kWarps * kPosted + (p.top - 1) / kWarps]);
-        uint32_t mine = all_posted[lane], w = 0;
-        for (int k = 0; k < p.top; ++k) {
-            w = __reduce_max_sync(0xFFFFFFFFu, mine);
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine == w);
-            if (lane == __ffs(static_cast<int>(who)) - 1) mine = 0;
-        }
-        return w;
-    };
+    float group_best = -INFINITY;                           // of the group's chunks so far
+    const int group = (chunks + kGroups - 1) / kGroups;     // chunks
+    int in_group = 0;
+    uint16_t* to_most = &sh.most[warp][0][lane];
     if (t == 0) sh.count = 0;
 
     // Chunk i on its way to a slot; minus infinity in the place of what is not there.
@@ -339,53 +318,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
         const float most = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
         static_assert(kVecs == 4, "above");
         if (most > (sum.s != 0.f ? sum.m : -INFINITY)) refer_to(most);
-        if (p.top > 0) {
-            const int b = i < chunks ? v0 + i * kChunk : whole, until = i < chunks ? v1 : whole + 1;
+        if (p.top > 0 && i < chunks) {
             lane_best = fmaxf(lane_best, most);
-            float from = least <= 1 ? -INFINITY : falling(least);  // what is not below is looked at, NaN too
-            bool some = __any_sync(0xFFFFFFFFu, !(most < from));
-            if (some && bounded) {
-                const uint32_t r = lane_best > -INFINITY ? rising(lane_best) : 1u;  // (what is not there is minus infinity too)
-                if (__any_sync(0xFFFFFFFFu, r > posted)) post(r);
-                if (i == 0) __syncthreads();
-                least = max(bound(), static_cast<uint32_t>(own >> 32));
-                from = least <= 1 ? -INFINITY : falling(least);
-                some = __any_sync(0xFFFFFFFFu, !(most < from));
-            }
-            if (some) {
-                uint32_t vectors = 0, mask = 0;
-                int j = 0;
-#pragma unroll
-                for (int k = 0; k < kVecs; ++k) vectors |= (best[k] < from ? 0u : 1u) << k;
-                while (__any_sync(0xFFFFFFFFu, (vectors | mask) != 0)) {  // one value of each lane
-                    if (mask == 0 && vectors != 0) {
-                        j = __ffs(static_cast<int>(vectors)) - 1;
-                        vectors &= vectors - 1;
-                        C one;
-                        one.v[0] = here[j * kThreads];
-#pragma unroll
-                        for (int e = 0; e < kEach; ++e) mask |= (one.at(0, e) < from ? 0u : 1u) << e;
-                    }
-                    unsigned long long key = 0;
-                    if (mask) {
-                        const int e = __ffs(static_cast<int>(mask)) - 1, vec = b + t + j * kThreads, index = vec * kEach + e;
-                        mask &= mask - 1;
-                        const float v = kWide ? reinterpret_cast<const float*>(here + j * kThreads)[e]
-                                              : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(here + j * kThreads)[e]) << 16);
-                        if (vec < until && index < p.vocab) key = make_key(rising(v), index);
-                        if (key <= own || static_cast<uint32_t>(key >> 32) < least) key = 0;
-                    }
-                    uint32_t who = __ballot_sync(0xFFFFFFFFu, key != 0);
-                    if (count + __popc(who) > kBuffer) {
-                        count = rank_buffer(sh.buffer[warp], count, p.top);
-                        own = sh.buffer[warp][p.top - 1];  // (the buffer held more than kMostTop)
-                        if (key <= own) key = 0;
-                        who = __ballot_sync(0xFFFFFFFFu, key != 0);
-                    }
-                    if (key != 0) sh.buffer[warp][count + __popc(who & ((1u << lane) - 1u))] = key;
-                    count += __popc(who);
-                    __syncwarp();
-                }
+            group_best = fmaxf(group_best, most);
+            if (++in_group == group || i + 1 == chunks) {
+                *to_most = kWide ? __bfloat16_as_ushort(__float2bfloat16_ru(group_best)) : static_cast<uint16_t>(__float_as_uint(group_best) >> 16);
+                to_most += 32;
+                in_group = 0;
+                group_best = -INFINITY;
             }
         }
         // t = x c - m c by one FMA with m c rounded; what that rounding is off by goes back into the sums. Each vector's registers
@@ -441,17 +381,107 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
     }
     wait_copies<0>();
     if (p.top > 0) {
-        __syncthreads();
-        least = bound();
-        for (int i = lane; i - lane < count; i += 32) {
-            const unsigned long long key = i < count ? sh.buffer[warp][i] : 0;
-            const bool in = key != 0 && static_cast<uint32_t>(key >> 32) >= least;
-            const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
-            int at = 0;
-            if (lane == 0) at = atomicAdd(&sh.count, __popc(who));
-            at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(who & ((1u << lane) - 1u));
-            if (in) sh.candidates[at] = key;
+        // the warp's largest numbers for the others
+        {
+            uint32_t mine = lane_best > -INFINITY ? rising(lane_best) : 1u, w = 0;  // (what is not there is minus infinity too)
+#pragma unroll
+            for (int k = 0; k < kPosted; ++k) {
+                w = __reduce_max_sync(0xFFFFFFFFu, mine);
+                const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine == w);
+                if (lane == __ffs(static_cast<int>(who)) - 1) mine = 0;
+                if (lane == 0) sh.posted[warp * kPosted + k] = w;
+            }
         }
+        __syncthreads();
+        uint32_t least = 0;  // logits below are not wanted: the top-th largest of what is posted
+        {
+            const uint32_t mine = sh.posted[lane];
+            int above = 0;
+#pragma unroll
+            for (int k = 0; k < kWarps * kPosted; k += 4) {
+                const uint4 u = *reinterpret_cast<const uint4*>(&sh.posted[k]);
+                above += (u.x > mine) + (u.y > mine) + (u.z > mine) + (u.w > mine);
+            }
+            least = __reduce_min_sync(0xFFFFFFFFu, above < p.top ? mine : 0xFFFFFFFFu);
+        }
+        const float from = least <= 1 ? -INFINITY : falling(least);  // what is not below is looked at, NaN too
+        uint32_t groups = 0;
+        for (int g = 0; g * group < chunks; ++g) groups |= (__uint_as_float(static_cast<uint32_t>(sh.most[warp][g][lane]) << 16) < from ? 0u : 1u) << g;
+        __syncwarp();
+        unsigned long long own = 0;  // keys up to this one are not among the first `top`
+        int count = 0;               // in the warp's buffer
+        // A value of each lane (0 bits: none) becomes a candidate.
+        auto collect = [&](unsigned long long key) {
+            if (key <= own || static_cast<uint32_t>(key >> 32) < least) key = 0;
+            uint32_t who = __ballot_sync(0xFFFFFFFFu, key != 0);
+            if (count + __popc(who) > kBuffer) {
+                count = rank_buffer(sh.buffer[warp], count, p.top);
+                own = sh.buffer[warp][p.top - 1];  // (the buffer held more than kMostTop)
+                if (key <= own) key = 0;
+                who = __ballot_sync(0xFFFFFFFFu, key != 0);
+            }
+            if (key != 0) sh.buffer[warp][count + __popc(who & ((1u << lane) - 1u))] = key;
+            count += __popc(who);
+            __syncwarp();
+        };
+        int i = 0, until = 0;  // chunks to look at
+        while (true) {
+            if (i == until && groups != 0) {
+                const int g = __ffs(static_cast<int>(groups)) - 1;
+                groups &= groups - 1;
+                i = g * group;
+                until = min(i + group, chunks);
+            }
+            if (!__any_sync(0xFFFFFFFFu, i < until)) break;
+            uint32_t mask = 0;  // a bit for each value
+            const int vec = v0 + i * kChunk + t;
+            if (i < until) {
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    if (i >= all_chunks - kSlots)
+                        x.v[j] = sh.ring[i % kSlots][j][t];
+                    else
+                        x.v[j] = reinterpret_cast<const uint4*>(base)[vec + j * kThreads];  // (all of such a chunk is there)
+                }
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    uint32_t bits = 0;
+                    if constexpr (kWide) {
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e) bits |= (x.at(j, e) < from ? 0u : 1u) << e;
+                    } else {  // the even values' bits first
+                        const uint32_t f = __float_as_uint(from), pair_from = __byte_perm(f, f, 0x3232);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) bits |= not_below2(x.word(j, k), pair_from) & 0x00010001u << k;
+                        bits = (bits | bits >> 12) & 0xFFu;
+                    }
+                    if (vec + j * kThreads < v1) mask |= bits << (j * kEach);
+                }
+                ++i;
+            }
+            while (__any_sync(0xFFFFFFFFu, mask != 0)) {  // one value of each lane
+                unsigned long long key = 0;
+                if (mask) {
+                    const int bit = __ffs(static_cast<int>(mask)) - 1, j = bit / kEach;
+                    mask &= mask - 1;
+                    uint4 v = j & 2 ? (j & 1 ? x.v[3] : x.v[2]) : (j & 1 ? x.v[1] : x.v[0]);
+                    const int k = bit % 4;
+                    const uint32_t u = k & 2 ? (k & 1 ? v.w : v.z) : (k & 1 ? v.y : v.x);
+                    const int e = kWide ? k : 2 * k + bit / 4 % 2;
+                    key = make_key(rising(kWide ? __uint_as_float(u) : e % 2 ? high_half(u) : low_half(u)), (vec + j * kThreads) * kEach + e);
+                }
+                collect(key);
+            }
+        }
+        if (rank == ctas - 1 && warp == 0 && whole * kEach < p.vocab) {  // the values behind the whole vectors
+            const int index = whole * kEach + lane;
+            collect(index < p.vocab ? make_key(rising(logit<kWide>(p, row, index)), index) : 0);
+        }
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&sh.count, count);
+        at = __shfl_sync(0xFFFFFFFFu, at, 0);
+        __syncthreads();  // the ring is done with
+        for (int k = lane; k < count; k += 32) sh.candidates[at + k] = sh.buffer[warp][k];
         __syncthreads();
         rank_candidates(sh.candidates, sh.count, p.top, sh.list);
     }
