@@ -2,24 +2,24 @@
 // Formulas and edge cases: include/hc.h.
 //
 // A row is cut into equal segments for a cluster of 1, 2, 4 or 8 CTAs. A CTA takes its segment in chunks of 256 threads x 4
-// vectors of 16 bytes, held in registers, the next chunk's loads in flight. Each thread keeps, for z = scale * logit in units of
+// vectors of 16 bytes; two chunks are on their way into shared memory while one is worked on (in registers, one ahead, fp32 rows of
+// 100,003 took 16% longer). Each thread keeps, for z = scale * logit in units of
 // log 2 below its own running maximum m: S = sum 2^t and W = sum t 2^t, t = (x - m) * scale * log2(e); joined over threads, warps and
 // the cluster (shared memory of the other CTAs), log sum e^z = m * scale + ln S and the entropy is ln S - ln 2 * W / S. Logits
 // far below m are raised to where 2^t is still 0, so that minus infinity does not make t 2^t a NaN; a NaN stays one.
 //
-// The alternatives ride along as 64-bit keys: the logit's bits as a number that rises with it, then the index backwards, so that
-// keys differ and of two equal logits the lower index is the greater key. Each warp collects candidates of its own, without
-// barriers. A bound keeps them few: each warp posts the 4 largest of its 32 lanes' running maxima in shared memory, and the top-th
-// largest of the 32 posted numbers (or less, below) is no larger than the CTA's top-th logit, however old a posted number is (a segment that does
-// not fill the warps has the bound that so many candidates need not be kept out). A lane looks at its values one by one only
-// where a vector's largest reaches the bound. A warp whose buffer is full ranks it by
-// counting and keeps the first `top`, of which the last is a bound of its own (rising or equal logits get there). At the
-// end the candidates that reach the last bound are ranked together, and the lists of a cluster's CTAs once more; the
-// result does not depend on the order in which candidates came.
+// The alternatives are 64-bit keys: the logit's bits as a number that rises with it, then the index backwards, so that
+// keys differ and of two equal logits the lower index is the greater key. They are looked for once the segment has gone by. On the way a lane
+// keeps only the largest logit of each of up to 12 groups of chunks. Then each warp posts the 4 largest of its 32 lanes' maxima; the
+// top-th largest of the 32 posted numbers is no larger than the CTA's top-th logit, and 1.1 top logits (of normal ones) reach it. Lanes with such a logit in a group
+// take the group's vectors once more, from shared memory or L2 (1% of a segment; collecting candidates on the way, against a bound that rises, took 27 us
+// instead of 20 for 256 rows of 131,072 with 20: it doubles the instructions). A warp whose buffer is full ranks it by
+// counting and keeps the first `top`, of which the last is a bound of its own (many equal logits get there). The warps' candidates
+// are ranked together, and the lists of a cluster's CTAs once more; the result does not depend on the order in which candidates came.
 
-// Measured: 256 rows of 131,072 (bf16) with 20 alternatives 31 us, 17 without alternatives (3,900 GB/s: 8 instructions a value, 62% of
-// the issue slots; the alternatives' steps wait for one another), 21 with one; 4,097 rows of 100,003 (fp32) with 5 277 us, 5,900 GB/s, 87% of
-// the copy rate; 8 rows of 131,072 with 20 10 us.
+// Measured: 256 rows of 131,072 (bf16) with 20 alternatives 20 us, 15 without alternatives (4,500 GB/s: 9 instructions a value, 60% of
+// the issue slots, and 512 CTAs are 3 on some SMs and 4 on others), 18 with one; 4,097 rows of 100,003 (fp32) with 5 243 us, 6,740 GB/s, at
+// the copy rate; 8 rows of 131,072 with 20 8 us.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -283,14 +283,16 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
                 else
                     to[j * kThreads] = nothing;
             }
-            if (i == chunks && t == 0) {  // the values behind the whole vectors
+            if (i == chunks && t == 0) {  // the values behind the whole vectors, shifted in from below
+                uint4 v = nothing;
 #pragma unroll 1
-                for (int e = whole * kEach; e < p.vocab; ++e) {
+                for (int e = p.vocab - 1; e >= whole * kEach; --e) {
                     if constexpr (kWide)
-                        reinterpret_cast<uint32_t*>(to)[e - whole * kEach] = reinterpret_cast<const uint32_t*>(base)[e];
+                        v = make_uint4(reinterpret_cast<const uint32_t*>(base)[e], v.x, v.y, v.z);
                     else
-                        reinterpret_cast<uint16_t*>(to)[e - whole * kEach] = reinterpret_cast<const uint16_t*>(base)[e];
+                        v = make_uint4(v.x << 16 | reinterpret_cast<const uint16_t*>(base)[e], v.y << 16 | v.x >> 16, v.z << 16 | v.y >> 16, v.w << 16 | v.z >> 16);
                 }
+                to[0] = v;
             }
         }
         ahead += kChunk;
@@ -436,6 +438,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
             uint32_t mask = 0;  // a bit for each value
             const int vec = v0 + i * kChunk + t;
             if (i < until) {
+                // Behind the bound's own index only greater logits are wanted: rows of many equal ones, masked ones above all, would
+                // go through the ranking for nothing (256 rows of 131,072 with 16 of them not minus infinity: 167 us without this).
+                float wanted = from;
+                if (own != 0) {
+                    uint32_t u = static_cast<uint32_t>(own >> 32);
+                    if (static_cast<uint32_t>(vec) * kEach > 0xFFFFFFFFu - static_cast<uint32_t>(own)) u += kWide ? 1u : 0x10000u;
+                    if (u > 1 && u <= 0xFF800000u) wanted = falling(u);  // (up to infinity)
+                }
 #pragma unroll
                 for (int j = 0; j < kVecs; ++j) {
                     if (i >= all_chunks - kSlots)
@@ -448,11 +458,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
                     uint32_t bits = 0;
                     if constexpr (kWide) {
 #pragma unroll
-                        for (int e = 0; e < kEach; ++e) bits |= (x.at(j, e) < from ? 0u : 1u) << e;
+                        for (int e = 0; e < kEach; ++e) bits |= (x.at(j, e) < wanted ? 0u : 1u) << e;
                     } else {  // the even values' bits first
-                        const uint32_t f = __float_as_uint(from), pair_from = __byte_perm(f, f, 0x3232);
+                        const uint32_t f = __float_as_uint(wanted), pair_wanted = __byte_perm(f, f, 0x3232);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) bits |= not_below2(x.word(j, k), pair_from) & 0x00010001u << k;
+                        for (int k = 0; k < 4; ++k) bits |= not_below2(x.word(j, k), pair_wanted) & 0x00010001u << k;
                         bits = (bits | bits >> 12) & 0xFFu;
                     }
                     if (vec + j * kThreads < v1) mask |= bits << (j * kEach);

@@ -329,6 +329,28 @@ def test_logprobs_hard_rows(n, vocab, kind, dtype):
     no_error()
 
 
+# Rows whose segments are many chunks, so that several share the maxima that say where alternatives are.
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kind", ["normal", "few values", "few left", "equal", "equal but late"])
+@pytest.mark.parametrize("n,vocab", [(2, 1500007), (309, 110003)])
+def test_logprobs_long_rows(n, vocab, kind, dtype):
+    rng = np.random.default_rng(vocab)
+    x = (3 * rng.standard_normal((n, vocab), dtype=np.float32))
+    if kind == "few values":
+        x = np.round(x)
+    elif kind == "few left":
+        x[:, np.arange(vocab) % 8192 != 5] = -np.inf
+    elif kind == "equal":
+        x[:] = -2.0
+    elif kind == "equal but late":
+        x[:] = -2.0
+        x[:, -40:] = -1.0
+        x[0, -3:] = -3.0
+    z = torch.nn.functional.pad(dev(x, dtype), (0, -vocab % 8))[:, :vocab]
+    check_logprobs(z, rng.integers(0, vocab, n), 1.0, 20)
+    no_error()
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("vocab", [40, 5000, 70001])
 def test_logprobs_nan_and_infinity(vocab, dtype):
