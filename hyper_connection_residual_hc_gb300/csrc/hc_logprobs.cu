@@ -164,12 +164,20 @@ struct Chunk {
         if constexpr (kWide) return __uint_as_float(word(j, e));
         return e % 2 ? high_half(word(j, e / 2)) : low_half(word(j, e / 2));
     }
-    __device__ __forceinline__ float largest(int j) const {  // of the numbers of a vector
+    __device__ __forceinline__ float largest() const {  // of the numbers
         if constexpr (kWide) {
-            return fmaxf(fmaxf(at(j, 0), at(j, 1)), fmaxf(at(j, 2), at(j, 3)));
+            float m = at(0, 0);
+#pragma unroll
+            for (int k = 1; k < kVecs * 4; ++k) m = fmaxf(m, at(k / 4, k % 4));
+            return m;
         } else {
             auto h = [](const uint32_t& u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
-            const __nv_bfloat162 m = __hmax2(__hmax2(h(v[j].x), h(v[j].y)), __hmax2(h(v[j].z), h(v[j].w)));
+            __nv_bfloat162 m = h(v[0].x);
+#pragma unroll
+            for (int k = 1; k < kVecs * 4; ++k) {
+                const uint32_t u = word(k / 4, k % 4);
+                m = __hmax2(m, h(u));
+            }
             return fmaxf(__low2float(m), __high2float(m));
         }
     }
@@ -314,11 +322,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
         if (i == 0 && gives && sh.token >= 0 && (kWide ? sh.token : sh.token | 1) < p.vocab)
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&sh.given)), "l"(base + (kWide ? sh.token * 4 : sh.token / 2 * 4)) : "memory");
         load(i + kSlots - 1, slot == 0 ? kSlots - 1 : slot - 1);
-        float best[kVecs];
-#pragma unroll
-        for (int j = 0; j < kVecs; ++j) best[j] = x.largest(j);
-        const float most = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
-        static_assert(kVecs == 4, "above");
+        const float most = x.largest();
         if (most > (sum.s != 0.f ? sum.m : -INFINITY)) refer_to(most);
         if (p.top > 0 && i < chunks) {
             lane_best = fmaxf(lane_best, most);
