@@ -1,25 +1,26 @@
 // Log probabilities of given tokens, the entropy and the most likely alternatives of rows of logits, in one pass over them.
 // Formulas and edge cases: include/hc.h.
 //
-// A row is cut into equal segments for a cluster of 1, 2, 4 or 8 CTAs. A CTA takes its segment in chunks of 256 threads x 4
-// vectors of 16 bytes; two chunks are on their way into shared memory while one is worked on (in registers, one ahead, fp32 rows of
-// 100,003 took 16% longer). Each thread keeps, for z = scale * logit in units of
-// log 2 below its own running maximum m: S = sum 2^t and W = sum t 2^t, t = (x - m) * scale * log2(e); joined over threads, warps and
-// the cluster (shared memory of the other CTAs), log sum e^z = m * scale + ln S and the entropy is ln S - ln 2 * W / S. Logits
-// far below m are raised to where 2^t is still 0, so that minus infinity does not make t 2^t a NaN; a NaN stays one.
+// A row is cut into equal segments for a cluster of 1, 2, 4 or 8 CTAs. A CTA takes its segment in chunks of 256 threads x 4 vectors of
+// 16 bytes; two chunks are on their way into shared memory while one is worked on (with one on its way, into registers, fp32 rows of
+// 100,003 took 16% longer). Each thread keeps, for z = scale * logit in units of log 2 below its own running maximum m: S = sum 2^t
+// and W = sum t 2^t, t = (x - m) * scale * log2(e); joined over threads, warps and the cluster (shared memory of the other CTAs),
+// log sum e^z = m * scale + ln S and the entropy is ln S - ln 2 * W / S. Logits far below m are raised to where 2^t is still 0, so
+// that minus infinity does not make t 2^t a NaN; a NaN stays one.
 //
-// The alternatives are 64-bit keys: the logit's bits as a number that rises with it, then the index backwards, so that
-// keys differ and of two equal logits the lower index is the greater key. They are looked for once the segment has gone by. On the way a lane
-// keeps only the largest logit of each of up to 12 groups of chunks. Then each warp posts the 4 largest of its 32 lanes' maxima; the
-// top-th largest of the 32 posted numbers is no larger than the CTA's top-th logit, and 1.1 top logits (of normal ones) reach it. Lanes with such a logit in a group
-// take the group's vectors once more, from shared memory or L2 (1% of a segment; collecting candidates on the way, against a bound that rises, took 27 us
-// instead of 20 for 256 rows of 131,072 with 20: it doubles the instructions). A warp whose buffer is full ranks it by
-// counting and keeps the first `top`, of which the last is a bound of its own (many equal logits get there). The warps' candidates
-// are ranked together, and the lists of a cluster's CTAs once more; the result does not depend on the order in which candidates came.
+// The alternatives are 64-bit keys: the logit's bits as a number that rises with it, then the index backwards, so that keys differ
+// and of two equal logits the lower index is the greater key. They are looked for once the segment has gone by. On the way a lane keeps
+// only the largest logit of each of up to 12 groups of chunks. Then each warp posts the 4 largest of its 32 lanes' maxima; the top-th
+// largest of the 32 posted numbers is no larger than the CTA's top-th logit, and of normal logits 1.1 top reach it. Lanes with such a
+// logit in a group take the group's vectors once more, from shared memory or L2: 1% of a segment. (Collecting candidates on the way,
+// against a bound that rises, took 27 us instead of 20 for 256 rows of 131,072 with 20: it doubles the instructions.) A warp whose
+// buffer is full ranks it by counting and keeps the first `top`, of which the last is a bound of its own (many equal logits get there).
+// The warps' candidates are ranked together, and the lists of a cluster's CTAs once more; the result does not depend on the order in
+// which candidates came.
 
-// Measured: 256 rows of 131,072 (bf16) with 20 alternatives 20 us, 15 without alternatives (4,500 GB/s: 9 instructions a value, 60% of
-// the issue slots, and 512 CTAs are 3 on some SMs and 4 on others), 18 with one; 4,097 rows of 100,003 (fp32) with 5 243 us, 6,740 GB/s, at
-// the copy rate; 8 rows of 131,072 with 20 8 us.
+// Measured: 256 rows of 131,072 (bf16) with 20 alternatives 20 us, 14.4 without alternatives (4,650 GB/s: 9 instructions a value, 60% of
+// the issue slots, and 512 CTAs are 3 on some SMs and 4 on others), 18 with one; 4,097 rows of 100,003 (fp32) with 5 239 to 243 us,
+// 6,800 GB/s, the copy rate; 8 rows of 131,072 with 20 8 us.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -619,7 +620,10 @@ int launch_logprobs(const LogprobArgs& a, cudaStream_t stream) {
     if (sms < 1) return -7;
     const int vecs = (a.vocab + (a.wide ? 3 : 7)) / (a.wide ? 4 : 8);
     int ctas = 1;
-    while (ctas < 8 && a.n * ctas < 2LL * sms && vecs >= 2 * ctas * kThreads) ctas *= 2;
+    // CTAs a row: until there are 2 an SM, or a segment would be less than 2 chunks, as a cluster's join takes 1.5 us or more. 256 rows of
+    // 131,072 (bf16, 20 alternatives): 1 CTA a row 27 us, 2 20, 4 26. 160 rows of 16,384: 1 5.6, 2 7.3. 64 rows of 8,192 (fp32): 1
+    // 5.1, 4 8.9. One row of 32,768 (bf16) is the other way round: 2 6.2, 4 5.7.
+    while (ctas < 8 && a.n * ctas < 2LL * sms && vecs >= 4 * ctas * kChunk) ctas *= 2;
     g_launched.store(true, std::memory_order_relaxed);
     return (a.wide ? start<true>(a, ctas, stream) : start<false>(a, ctas, stream)) == cudaSuccess ? 0 : -7;
 }
