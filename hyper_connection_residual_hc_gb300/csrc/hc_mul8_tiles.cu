@@ -162,7 +162,7 @@ __device__ __forceinline__ float ld_cluster_f1(uint32_t addr) {
 }
 
 // With kSplit, by the adding warps of all pairs of the cluster: their sums of a tile are added up in the order of the pairs. Each
-// thread puts its columns into shared memory, over the ring (the last block's MMAs are done, so all copies are), 4 at a time:
+// thread puts its columns into shared memory, over the ring (the last block's MMAs of both halves are done, so all copies are), 4 at a time:
 // [column / 4][token][4]. Then the columns are dealt out 16 at a time: a pair takes every p.pairs-th of each half (of a gated
 // product 16 features with their 16 columns of up), reads them from all pairs and writes the result.
 template <bool kGated>
@@ -469,6 +469,8 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
             const Tile t = tile_at(p, n);
             const int token0 = t.tokens * kTokens + static_cast<int>(rank) * kHalf + 32 * quarter;  // of the warp
             if constexpr (kSplit) {
+                // The ring is free when the other half's last MMAs have read it too.
+                wait(acc_full + 16 * ((i - 1) & 1) + 8 * (1 - half), ((i - 1) / 2) & 1);
                 join_parts<kGated>(p, t, acc, base, at, half, in_cta, static_cast<int>(rank), pair);
                 break;
             }
