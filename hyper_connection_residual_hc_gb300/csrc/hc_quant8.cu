@@ -12,6 +12,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 
 #include "hc_ffn.h"
@@ -39,11 +40,32 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+// The sum or the largest of a row's threads, the same in all of them; `part` is one call's own.
+template <bool kMax>
+__device__ __forceinline__ float over_row(float v, int row_threads, float* part) {
+    auto over_warp = [](float u) {
+#pragma unroll
+        for (int m = 16; m; m /= 2) {
+            const float o = __shfl_xor_sync(0xFFFFFFFFu, u, m);
+            u = kMax ? fmaxf(u, o) : u + o;
+        }
+        return u;
+    };
+    v = over_warp(v);
+    if (row_threads > 32) {
+        const int lane = threadIdx.x % 32;
+        if (lane == 0) part[threadIdx.x / 32] = v;
+        __syncthreads();
+        v = over_warp(lane < row_threads / 32 ? part[lane] : 0.f);
+    }
+    return v;
+}
+
 // row_threads: threads that share a row (a multiple of 32); kVecs: 16-byte vectors of it that each holds, so that all of the row
 // is in registers.
 template <int kVecs, bool kResidual>
 __global__ void __launch_bounds__(kVecs < 4 ? 128 : 1024) quant8_kernel(const Quant8Args p, int row_threads) {
-    __shared__ float part[32];
+    __shared__ float part[3][32];
     griddep_launch_dependents();
     griddep_wait();
     const int t = threadIdx.x % row_threads, lane = threadIdx.x % 32;
@@ -58,7 +80,6 @@ __global__ void __launch_bounds__(kVecs < 4 ? 128 : 1024) quant8_kernel(const Qu
         v[i] = c < vecs ? x[c] : make_uint4(0, 0, 0, 0);
     }
     float f[8];
-    float ss = 0.f;
     if constexpr (kResidual) {
         const uint4* r = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + row * p.residual_stride);
         uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.sum_out) + row * p.sum_stride);
@@ -82,22 +103,46 @@ __global__ void __launch_bounds__(kVecs < 4 ? 128 : 1024) quant8_kernel(const Qu
     }
     float inv = 1.f;
     if (p.norm) {
+        auto squares = [&]() {
+            float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            unpack(v[i], f);
+            for (int i = 0; i < kVecs; ++i) {
+                unpack(v[i], f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+                for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+            }
+            return sum;
+        };
+        float mean = over_row<false>(squares(), row_threads, part[0]) / static_cast<float>(p.d) + p.eps;
+        // bf16 has fp32's range, squares twice that. Where their mean overflowed, or (with an eps that allows it) came near the subnormal
+        // numbers, the row is taken times a power of two that brings the larger of its largest value and sqrt(eps) to 1 .. 4; the result
+        // does not change with it. What falls below bf16's least number by that is 2^-126 of the largest. All threads of a row agree.
+        if (mean > FLT_MAX || mean < 0x1p-100f) {
+            uint32_t pairs = 0;
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                pairs = __vmaxu2(__vmaxu2(pairs, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu)), __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+            float most = fmaxf(fmaxf(__uint_as_float(pairs << 16), __uint_as_float(pairs & 0xFFFF0000u)), sqrtf(p.eps));
+            most = over_row<true>(most, row_threads, part[1]);
+            if (most > 0.f && most <= FLT_MAX) {  // (an infinity stays one)
+                const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23), 1), 253);
+                const float by = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+                const __nv_bfloat162 by2 = __float2bfloat162_rn(by);
+                auto times = [&](uint32_t& u) {
+                    const __nv_bfloat162 t = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u), by2);
+                    u = *reinterpret_cast<const uint32_t*>(&t);
+                };
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) {
+                    times(v[i].x);
+                    times(v[i].y);
+                    times(v[i].z);
+                    times(v[i].w);
+                }
+                mean = over_row<false>(squares(), row_threads, part[2]) / static_cast<float>(p.d) + p.eps * by * by;
+            }
         }
-#pragma unroll
-        for (int m = 16; m; m /= 2) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, m);
-        if (row_threads > 32) {
-            if (lane == 0) part[threadIdx.x / 32] = ss;
-            __syncthreads();
-            ss = lane < row_threads / 32 ? part[lane] : 0.f;
-#pragma unroll
-            for (int m = 16; m; m /= 2) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, m);
-        }
-        inv = rsqrtf(ss / static_cast<float>(p.d) + p.eps);
+        inv = rsqrtf(mean);
     }
     unsigned char* codes = p.codes + row * p.codes_stride;
     float* scales = p.scales + row * blocks8(p.d);

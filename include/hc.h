@@ -551,7 +551,8 @@ typedef struct {
  *   sum_out     [device] bf16 [n, d], strided, or NULL; needs a residual; may be exactly x or exactly residual (with its stride)
  *   codes       [device] e4m3 [n, d], strided;  scales [device] fp32 [n, ceil(d/128)]
  * A block of 128 whose y holds a NaN or an infinity reads as NaN. With the norm a NaN in s reaches its whole row; an infinity makes
- * its own block NaN and the row's other blocks 0. */
+ * its own block NaN and the row's other blocks 0. Finite rows are normed over all of bf16's range, squares beyond fp32's too; a row of
+ * zeros reads as NaN with norm_eps = 0 (0 / 0) and as zeros otherwise. */
 int hc_norm_quant8(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, const float* norm_w, hc_quant8_t q,
                    void* sum_out, int64_t sum_stride, void* codes, int64_t codes_stride, float* scales, hc_stream_t stream);
 

@@ -130,6 +130,57 @@ def test_quant_edges():
     assert (c[5] == -448).all()
 
 
+# The mean of squares in fp32: rounding a square or a scaled value that is subnormal costs at most 2^-126 of the row's largest. What the norm
+# adds to that is as in test_norm_quant.
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("n,d", [(3, 256), (2, 512), (5, 1040), (3, 5120), (2, 32784)])
+@pytest.mark.parametrize("kind,eps", [("largest", 1e-6), ("large", 1e-6), ("large", 0.0), ("one large", 1e-6), ("small", 0.0), ("small", 1e-40), ("small", 2.0 ** -99),
+                                      ("small", 2.0 ** -101), ("smallest", 0.0), ("smallest", 1e-6), ("ordinary", 3e38), ("ordinary", 0.0), ("largest", 3e38)])
+def test_norm_quant_ends_of_the_range(n, d, kind, eps, residual):
+    """Finite rows are normed whether or not their squares fit into fp32."""
+    rng = np.random.default_rng(d + n)
+    x = rng.standard_normal((n, d))
+    if kind == "largest":
+        x = np.where(x > 0, 1.0, -1.0) * 2.0 ** 127 * (1 + rng.integers(0, 128, (n, d)) / 128)
+    elif kind == "large":
+        x *= 2.0 ** 70
+    elif kind == "one large":
+        x[:, d // 3] = 2.0 ** 110
+    elif kind == "small":
+        x *= 2.0 ** -100
+    elif kind == "smallest":
+        x = rng.integers(-3, 4, (n, d)) * 2.0 ** -133
+    x = dev(x, torch.bfloat16)
+    assert torch.isfinite(x).all()
+    r = torch.zeros_like(x) if residual else None
+    w = dev(1 + 0.2 * rng.standard_normal(d))
+    codes, scales = gu.guarded((n, d), E4M3), gu.guarded((n, fr.blocks(d)), torch.float32)
+    out = gu.guarded((n, d)) if residual else None
+    q = hc.quant8(n, d, norm_eps=eps)
+    hc.hc_norm_quant8(x, d, r, d, w, q, out, d, codes, d, scales)
+    no_error()
+    if residual:
+        assert torch.equal(out, x)
+    y = fr.norm(f64(x), f64(w), float(q.norm_eps))
+    check_codes(f64(codes), f64(scales), y, (d / 2 + 16) * fr.U * np.abs(y) + 2.0 ** -110)
+
+
+def test_norm_quant_zeros_and_infinities_beside_large_rows():
+    x = torch.zeros((4, 512), dtype=torch.bfloat16, device="cuda")
+    x[1] = 2.0 ** 100
+    x[2, 300], x[2, 5] = float("inf"), 2.0 ** 100
+    x[3, 7], x[3, 200] = float("nan"), 2.0 ** 100
+    codes, scales = torch.empty((4, 512), dtype=E4M3, device="cuda"), torch.empty((4, 4), device="cuda")
+    for eps in (1e-6, 0.0):
+        hc.hc_norm_quant8(x, 512, None, 0, None, hc.quant8(4, 512, norm_eps=eps), None, 0, codes, 512, scales)
+        no_error()
+        c, s = f64(codes), f64(scales)
+        assert np.isnan(c[0]).all() if eps == 0 else (c[0] == 0).all()
+        assert (c[1] == 448).all() and np.allclose(s[1], 1 / 448, rtol=600 * fr.U)
+        assert np.isnan(c[2, 256:384]).all() and (np.delete(c[2], np.s_[256:384]) == 0).all()
+        assert np.isnan(c[3]).all()
+
+
 # ---- products -----------------------------------------------------------------------------------------
 
 def make_codes(rng, rows, cols, scales_shape, size=1.0, stride=None):
