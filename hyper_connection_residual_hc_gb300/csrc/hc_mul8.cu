@@ -130,8 +130,11 @@ mul8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 if constexpr (kGated) tma_load_2d(st + P::kW, &tm_up, full + 8 * s, b * kBlock8, ft * kTile, once);
                 tma_load_2d(st + P::kMats * P::kW, &tm_x, full + 8 * s, b * kBlock8, static_cast<int>(t0), again);
             }
-            // no copy is in flight when the CTA ends, whatever happened
-            for (int i = max(b1 - b0 - P::kStages, 0); i < b1 - b0; ++i) wait.drain(full + 8 * (i % P::kStages), (i / P::kStages) & 1);
+            // no copy and no commit's arrival is in flight when the CTA ends, whatever happened
+            for (int i = max(b1 - b0 - P::kStages, 0); i < b1 - b0; ++i) {
+                wait.drain(full + 8 * (i % P::kStages), (i / P::kStages) & 1);
+                wait.drain(empty + 8 * (i % P::kStages), (i / P::kStages) & 1);
+            }
         }
         __syncwarp();
     } else if (warp == P::kAddWarps + 1) {  // ---- MMAs

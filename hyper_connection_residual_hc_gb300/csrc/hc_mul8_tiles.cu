@@ -361,9 +361,13 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
                     tma_load_pair(st + kOperand + kOperand / 2, w, first_full + 8 * s, b * kBlock8, row + next);
                 }
             }
-            // no copy of either CTA is in flight when the pair ends, whatever happened
+            // No copy of either CTA is in flight when the pair ends, whatever happened, and no arrival of a commit, which come to both CTAs by
+            // themselves: nothing else waits for the last ones on `empty`.
             if (rank == 0)
                 for (int j = max(i - kStages, 0); j < i; ++j) wait.drain(full + 8 * (j % kStages), (j / kStages) & 1);
+            for (int j = max(i - kStages, 0); j < i; ++j) wait.drain(empty + 8 * (j % kStages), (j / kStages) & 1);
+            for (int j = max(i - 2, 0); j < i; ++j)
+                for (int h = 0; h < 2; ++h) wait.drain(acc_full + 16 * (j & 1) + 8 * h, (j / 2) & 1);
         } else if (warp == kMmaWarp && rank == 0) {  // ---- MMAs
             const uint32_t lead = elect_one();
             const uint16_t both = static_cast<uint16_t>(3u << leader);

@@ -612,6 +612,38 @@ def test_chain_of_dependent_calls(n, d, f):
         assert all(torch.equal(b, w) for b, w in zip(bufs, want))
 
 
+@pytest.mark.parametrize("n,k,features", [(3, 16, 300), (40, 144, 640), (300, 16, 1027), (300, 272, 2600), (2100, 144, 2600)])
+def test_short_products_one_after_the_other(n, k, features):
+    """Kernels of one to three blocks of k, whose last arrivals come close to their end, in a row on the same SMs."""
+    rng = np.random.default_rng(k)
+    x, xv, xs, xsv = make_codes(rng, n, k, (n, fr.blocks(k)))
+    w, wv, ws, wsv = make_codes(rng, features, k, (fr.blocks(features), fr.blocks(k)), 0.05)
+    pitch = (features + 7) // 8 * 8
+    outs = [torch.full((n, pitch), float("nan"), device="cuda") for _ in range(20)]
+
+    def run():
+        for o in outs:
+            hc.hc_mul8(x, k, xs, w, k, ws, n, hc.mul8(features, k, hc.HC_F32), o, pitch)
+
+    def check():
+        no_error()
+        ref, e = fr.product(xv, xsv, wv, wsv)
+        assert_within(f64(outs[0])[:, :features], ref, e)
+        assert all(torch.equal(o[:, :features], outs[0][:, :features]) for o in outs)
+
+    run()
+    check()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        run()
+    for o in outs:
+        o.fill_(float("nan"))
+    g.replay()
+    g.replay()
+    check()
+
+
 FIRST_CALLS = """
 import sys
 import torch
