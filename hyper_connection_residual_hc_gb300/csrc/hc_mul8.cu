@@ -79,7 +79,6 @@ __global__ void __launch_bounds__(Plan<kN, kGated, kPerSm>::kThreads, kPerSm)
 mul8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_up,
                  const __grid_constant__ Params p) {
     using P = Plan<kN, kGated, kPerSm>;
-    griddep_launch_dependents();  // (the kernel behind sets itself up as SMs get free)
     extern __shared__ unsigned char raw[];
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -99,6 +98,9 @@ mul8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     if (warp == P::kAddWarps + 1) {
         tmem_alloc(slot, P::kColumns);
         tmem_relinquish();
+        // The kernel behind sets itself up as SMs get free. It may hold tensor memory while it waits for this grid's end, so that it must
+        // not come before this CTA has its own.
+        griddep_launch_dependents();
     }
     if (tid == 0) {
         for (int i = 0; i < P::kStages; ++i) {

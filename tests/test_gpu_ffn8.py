@@ -644,6 +644,39 @@ def test_short_products_one_after_the_other(n, k, features):
     check()
 
 
+def test_products_of_different_sizes_in_a_row():
+    """Kernels that hold from 32 to all 512 columns of an SM's tensor memory, each set up under the end of the one ahead, in a graph."""
+    rng = np.random.default_rng(8)
+    k, f = 1152, 1040
+    g, _, gs, _ = make_codes(rng, f, k, (fr.blocks(f), 9), 4.0 / np.sqrt(k))
+    u, _, us, _ = make_codes(rng, f, k, (fr.blocks(f), 9), 4.0 / np.sqrt(k))
+    calls = []
+    for n in (64, 1, 128, 30, 300, 5, 64, 600, 64, 100):
+        x, _, xs, _ = make_codes(rng, n, k, (n, 9))
+        calls.append((n, x, xs, torch.empty((n, f), device="cuda"), torch.empty((n, f), dtype=torch.bfloat16, device="cuda")))
+
+    def run(sync):
+        for n, x, xs, y, h in calls:
+            hc.hc_gated_mul8(x, k, xs, g, gs, u, us, k, n, hc.gated8(f, k, out_type=hc.HC_BF16), h, f, None)
+            sync()
+            hc.hc_mul8(x, k, xs, g, k, gs, n, hc.mul8(f, k, hc.HC_F32), y, f)
+            sync()
+
+    run(torch.cuda.synchronize)
+    want = [(y.clone(), h.clone()) for _, _, _, y, h in calls]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        run(lambda: None)
+    for _ in range(5):
+        for _, _, _, y, h in calls:
+            y.fill_(float("nan"))
+            h.fill_(float("nan"))
+        graph.replay()
+        graph.replay()
+        no_error()
+        assert all(torch.equal(y, a) and torch.equal(h, b) for (_, _, _, y, h), (a, b) in zip(calls, want))
+
+
 FIRST_CALLS = """
 import sys
 import torch
