@@ -132,11 +132,8 @@ mul8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
                 if constexpr (kGated) tma_load_2d(st + P::kW, &tm_up, full + 8 * s, b * kBlock8, ft * kTile, once);
                 tma_load_2d(st + P::kMats * P::kW, &tm_x, full + 8 * s, b * kBlock8, static_cast<int>(t0), again);
             }
-            // no copy and no commit's arrival is in flight when the CTA ends, whatever happened
-            for (int i = max(b1 - b0 - P::kStages, 0); i < b1 - b0; ++i) {
-                wait.drain(full + 8 * (i % P::kStages), (i / P::kStages) & 1);
-                wait.drain(empty + 8 * (i % P::kStages), (i / P::kStages) & 1);
-            }
+            // no copy is in flight when the CTA ends, whatever happened
+            for (int i = max(b1 - b0 - P::kStages, 0); i < b1 - b0; ++i) wait.drain(full + 8 * (i % P::kStages), (i / P::kStages) & 1);
         }
         __syncwarp();
     } else if (warp == P::kAddWarps + 1) {  // ---- MMAs
@@ -155,7 +152,7 @@ mul8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
 #pragma unroll
                 for (int q = 0; q < 4; ++q) mma8(lead, d + m * kN, w + 2 * q, x + 2 * q, idesc, q > 0);
             }
-            commit8(lead, empty + 8 * s);
+            if (i + P::kStages < b1 - b0) commit8(lead, empty + 8 * s);  // (an arrival that nothing waited for could come when the CTA has ended)
             commit8(lead, acc_full + 8 * u);
         }
         if (b1 > b0) wait.drain(acc_full + 8 * ((b1 - b0 - 1) & 1), ((b1 - b0 - 1) / 2) & 1);
