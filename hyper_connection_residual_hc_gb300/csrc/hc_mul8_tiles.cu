@@ -65,7 +65,6 @@ struct Params {
     int pairs;   // of the grid, which take tiles in turn; with kSplit the pairs of a cluster, which share one tile's blocks of k
     int stored;  // features that TMA stores: whole 16 bytes of a row
     long long first, until;  // tiles
-    int beside;  // the second launch of a call
 };
 
 __device__ __forceinline__ void tmem_alloc2(uint32_t dst, uint32_t ncols) {
@@ -336,9 +335,9 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
     cluster_sync8();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(at + (slot - base));
-    // What the kernels ahead write and read. The tiles that a call's second launch takes are not the first one's: it starts beside that
-    // (which has let it start behind its own wait) and waits for its end at its own.
-    if (!p.beside) griddep_wait();
+    // What the kernels ahead write and read. (A call's second launch could take its tiles beside the first's last ones, 1 to 3% sooner, but
+    // that what the kernels before the first wrote is visible to it is only promised behind a wait of its own.)
+    griddep_wait();
     griddep_launch_dependents();
 
     if (warp >= kAddWarps) {
@@ -598,7 +597,6 @@ mul8_tiles_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constan
         tc_fence_after();
         tmem_dealloc2(tmem, 512);
     }
-    if (p.beside) griddep_wait();
 }
 
 bool out_map(CUtensorMap* m, const Mul8Args& a, int stored) {
@@ -715,7 +713,6 @@ int start(const Mul8Args& a, cudaStream_t stream) {
     if (plan.whole > 0) {
         p.first = 0;
         p.until = plan.whole;
-        p.beside = 0;
         const long long pairs = fit[1].load(std::memory_order_relaxed);
         p.pairs = static_cast<int>(plan.whole < pairs ? plan.whole : pairs);
         if (start<kGated, false>(m, p, static_cast<unsigned>(2 * p.pairs), 2, ns, stream) != cudaSuccess) return -7;
@@ -723,7 +720,6 @@ int start(const Mul8Args& a, cudaStream_t stream) {
     if (plan.whole < tiles) {
         p.first = plan.whole;
         p.until = tiles;
-        p.beside = plan.whole > 0 ? 1 : 0;
         p.pairs = plan.split;
         if (start<kGated, true>(m, p, static_cast<unsigned>((tiles - plan.whole) * 2 * plan.split), 2 * plan.split, ns, stream) != cudaSuccess) return -7;
     }

@@ -677,6 +677,58 @@ def test_products_of_different_sizes_in_a_row():
         assert all(torch.equal(y, a) and torch.equal(h, b) for (_, _, _, y, h), (a, b) in zip(calls, want))
 
 
+# 9 x 20 gated tiles are two turns of 76 pairs and 28 tiles, which two pairs share each in a launch of their own; the last block of k is short.
+TWO_LAUNCHES = (2100, 10256, 2480)
+
+
+@pytest.mark.parametrize("kind,short", [("silu", True), ("gelu", False)])
+def test_gated_in_two_launches(kind, short):
+    n, k, features = TWO_LAUNCHES
+    test_gated(n, k, features, short, kind)
+
+
+def test_chain_of_calls_of_two_launches():
+    """Rows quantised into the same buffers again and again, each time read by products of two launches; plain and replayed, as with a
+    synchronisation behind every call."""
+    n, k, f = TWO_LAUNCHES
+    rng = np.random.default_rng(5)
+    g, _, gs, _ = make_codes(rng, f, k, (fr.blocks(f), fr.blocks(k)), 4.0 / np.sqrt(k))
+    u, _, us, _ = make_codes(rng, f, k, (fr.blocks(f), fr.blocks(k)), 4.0 / np.sqrt(k))
+    ys = [dev(rng.standard_normal((n, k)) * (i + 1), torch.bfloat16) for i in range(4)]
+    c, s = torch.empty((n, k), dtype=E4M3, device="cuda"), torch.empty((n, fr.blocks(k)), device="cuda")
+    hs = [torch.empty((n, f), dtype=torch.bfloat16, device="cuda") for _ in ys]
+    zs = [torch.empty((n, f), device="cuda") for _ in ys]
+
+    def chain(sync):
+        for y, h, z in zip(ys, hs, zs):
+            hc.hc_norm_quant8(y, k, None, 0, None, hc.quant8(n, k, norm=False), None, 0, c, k, s)
+            sync()
+            hc.hc_gated_mul8(c, k, s, g, gs, u, us, k, n, hc.gated8(f, k, out_type=hc.HC_BF16), h, f, None)
+            sync()
+            hc.hc_mul8(c, k, s, g, k, gs, n, hc.mul8(f, k, hc.HC_F32), z, f)
+            sync()
+
+    chain(torch.cuda.synchronize)
+    want = [t.clone() for t in hs + zs]
+
+    def check():
+        no_error()
+        assert all(torch.equal(t, w) for t, w in zip(hs + zs, want))
+        for t in hs + zs:
+            t.fill_(float("nan"))
+
+    for _ in range(3):
+        chain(lambda: None)
+        check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        chain(lambda: None)
+    for _ in range(3):
+        graph.replay()
+        graph.replay()
+        check()
+
+
 FIRST_CALLS = """
 import sys
 import torch
