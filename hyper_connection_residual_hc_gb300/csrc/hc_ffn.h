@@ -81,7 +81,7 @@ int launch_mul8(const Mul8Args& a, cudaStream_t stream);
 int read_mul8_error(unsigned int* word, int clear, cudaStream_t stream);
 // many rows (hc_mul8_tiles.cu)
 int launch_mul8_tiles(const Mul8Args& a, cudaStream_t stream);
-long long mul8_tiles_ns(const Mul8Args& a);  // about how long it would take; negative if that cannot be told
+long long mul8_tiles_ns(const Mul8Args& a);  // about how long it would take; negative if it cannot run
 int read_mul8_tiles_error(unsigned int* word, int clear, cudaStream_t stream);
 
 // ---- log probabilities (hc_logprobs.cu) ------------------------------------------------------------

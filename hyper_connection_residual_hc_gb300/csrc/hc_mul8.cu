@@ -403,9 +403,9 @@ struct Rows {
         RowsPlan r;
         if (!plan(a, sms, &r)) return -7;
         if (a.n > 32) {
-            const long long tiles = mul8_tiles_ns(a);
-            if (tiles < 0) return -7;
-            if (tiles < r.ns) return launch_mul8_tiles(a, stream);
+            const long long pairs = mul8_tiles_ns(a);
+            if (mul8_by_pairs(pairs, r.ns)) return launch_mul8_tiles(a, stream);
+            if (pairs < 0) cudaGetLastError();  // (what refused the plan is not this call's error)
         }
         return run(a, r, stream);
     }

@@ -8,6 +8,10 @@ namespace hc {
 
 constexpr int kMul8Devices = 64;
 
+// Whether a call goes to the pairs' kernel, by both kernels' estimated times. A negative one: that kernel cannot run here (the pairs'
+// needs two SMs next to each other, with nearly all of their shared memory), and the other takes the call.
+constexpr bool mul8_by_pairs(long long pairs_ns, long long rows_ns) { return pairs_ns >= 0 && pairs_ns < rows_ns; }
+
 // The driver's encoder of tensor maps; null if it has none.
 PFN_cuTensorMapEncodeTiled_v12000 mul8_encode();
 

@@ -1,6 +1,9 @@
 """The 8-bit operators of the feed-forward sublayer and the head where no GPU is needed: argument checks (fake device addresses that are
 never dereferenced: each call returns from its checks, or is a no-op) and the 64-bit reference itself against hand-worked values."""
 
+import os
+import subprocess
+
 import numpy as np
 import pytest
 
@@ -143,6 +146,19 @@ def test_logprob_refusals():
         for j in (0, 2, 4, 5, 6, 7):
             if i != j:
                 _expect(hc.HC_ERR_ALIAS, f, *_with(ok, **{"_%d" % i: ok[j]}))
+
+
+def test_products_go_to_the_kernel_that_can_run(tmp_path):
+    """The choice between the two kernels of the products: the shorter one, and the one for few rows where the other cannot be planned."""
+    csrc = os.path.join(os.path.dirname(hc.__file__), "csrc")
+    src = tmp_path / "choice.cu"
+    src.write_text("""
+#include "hc_mul8_host.h"
+static_assert(hc::mul8_by_pairs(10, 11) && hc::mul8_by_pairs(0, 1), "the shorter one");
+static_assert(!hc::mul8_by_pairs(11, 11) && !hc::mul8_by_pairs(12, 11), "the shorter one");
+static_assert(!hc::mul8_by_pairs(-1, 11), "no plan: the other kernel");
+""")
+    subprocess.run([hcbuild.NVCC, "-std=c++17", "-I", csrc, "-c", str(src), "-o", str(tmp_path / "choice.o")], check=True)
 
 
 # ---- the reference ----------------------------------------------------------------------------------------
