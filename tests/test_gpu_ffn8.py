@@ -677,6 +677,83 @@ def test_products_of_different_sizes_in_a_row():
         assert all(torch.equal(y, a) and torch.equal(h, b) for (_, _, _, y, h), (a, b) in zip(calls, want))
 
 
+def unpaused(chain, reset, outs):
+    """A chain of calls without a pause, and replayed, gives the bytes of the chain with a synchronisation behind every call."""
+    reset()
+    chain(torch.cuda.synchronize)
+    no_error()
+    want = [t.clone().view(torch.uint8) for t in outs]
+    graph = torch.cuda.CUDAGraph()
+    reset()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        chain(lambda: None)
+    for run in [lambda: chain(lambda: None)] * 3 + [graph.replay] * 3:
+        reset()
+        run()
+        no_error()
+        assert all(torch.equal(t.view(torch.uint8), w) for t, w in zip(outs, want))
+
+
+def test_chain_of_long_norms():
+    """Quantisations long enough (an estimated 12 us) to start under the end of the product that writes their rows, and products behind
+    them; the residual in place."""
+    n, d = 4800, 2608
+    rng = np.random.default_rng(6)
+    w, _, ws, _ = make_codes(rng, d, d, (fr.blocks(d), fr.blocks(d)), 4.0 / np.sqrt(d))
+    c0, _, s0, _ = make_codes(rng, n, d, (n, fr.blocks(d)))
+    r0, gain = dev(rng.standard_normal((n, d)), torch.bfloat16), dev(1 + 0.1 * rng.standard_normal(d))
+    c, s, r, y = c0.clone(), s0.clone(), r0.clone(), torch.empty_like(r0)
+
+    def reset():
+        for a, b in ((c, c0), (s, s0), (r, r0)):
+            a.copy_(b)
+        y.fill_(float("nan"))
+
+    def chain(sync):
+        for _ in range(6):
+            hc.hc_mul8(c, d, s, w, d, ws, n, hc.mul8(d, d), y, d)
+            sync()
+            hc.hc_norm_quant8(y, d, r, d, gain, hc.quant8(n, d), r, d, c, d, s)
+            sync()
+
+    unpaused(chain, reset, [c, s, r, y])
+    total = f64(r)
+    check_codes(f64(c), f64(s), fr.norm(total, f64(gain), 1e-6), (d / 2 + 16) * fr.U * np.abs(fr.norm(total, f64(gain), 1e-6)))
+
+
+@pytest.mark.parametrize("n,vocab", [(33, 250003), (300, 40000)])
+def test_chain_of_long_heads(n, vocab):
+    """Log probabilities long enough (an estimated 12 us) to start under the end of the product that writes their logits, which the next
+    product writes again."""
+    k, top, pitch = 272, 5, (vocab + 7) // 8 * 8
+    rng = np.random.default_rng(9)
+    w, _, ws, _ = make_codes(rng, vocab, k, (fr.blocks(vocab), fr.blocks(k)), 4.0 / np.sqrt(k))
+    rows = [make_codes(rng, n, k, (n, fr.blocks(k))) for _ in range(5)]
+    logits = torch.empty((n, pitch), device="cuda")
+    tokens = dev(rng.integers(0, vocab, n), torch.int64)
+    outs = [(torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty((n, top), device="cuda"), torch.empty((n, top), dtype=torch.int32, device="cuda"))
+            for _ in rows]
+    flat = [t for o in outs for t in o]
+
+    def reset():
+        logits.fill_(float("nan"))
+        for t in flat:
+            t.fill_(-7)
+
+    def chain(sync):
+        for (x, _, xs, _), o in zip(rows, outs):
+            hc.hc_mul8(x, k, xs, w, k, ws, n, hc.mul8(vocab, k, hc.HC_F32), logits, pitch)
+            sync()
+            hc.hc_token_logprobs(logits, pitch, tokens, hc.logprobs(n, vocab, top), *o)
+            sync()
+
+    unpaused(chain, reset, flat)
+    ref = fr.logprobs(f64(logits)[:, :vocab], tokens.cpu().numpy(), 1.0, top)
+    assert_within(f64(outs[-1][0]), ref[0], ref[4] + 8 * fr.U * np.abs(ref[0]))
+    assert np.array_equal(outs[-1][3].cpu().numpy(), ref[3])
+
+
 # 9 x 20 gated tiles are two turns of 76 pairs and 28 tiles, which two pairs share each in a launch of their own; the last block of k is short.
 TWO_LAUNCHES = (2100, 10256, 2480)
 
