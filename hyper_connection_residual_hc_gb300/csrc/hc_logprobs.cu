@@ -18,9 +18,10 @@
 // The warps' candidates are ranked together, and the lists of a cluster's CTAs once more; the result does not depend on the order in
 // which candidates came.
 
-// Measured: 256 rows of 131,072 (bf16) with 20 alternatives 20 us, 14.4 without alternatives (4,650 GB/s: 9 instructions a value, 60% of
-// the issue slots, and 512 CTAs are 3 on some SMs and 4 on others), 18 with one; 4,097 rows of 100,003 (fp32) with 5 239 to 243 us,
-// 6,800 GB/s, the copy rate; 8 rows of 131,072 with 20 8 us.
+// Measured: 256 rows of 131,072 (bf16) with 20 alternatives 20 us, 14.4 without alternatives (4,650 GB/s: 9 instructions a value, 56% of
+// the issue slots with 20, and 512 CTAs are 3 on some SMs and 4 on others), 18 with one; 4,097 rows of 100,003 (fp32) with 5 239 to 243 us,
+// 6,700 to 6,800 GB/s, the copy rate; 8 rows of 131,072 with 20 8 us. A row takes a whole chunk (8,192 bf16 or 4,096 fp32 values) at
+// least, however short: 4,000 rows of 500 (bf16) 28 us, of 2,000 19, of 8,192 20; with 5 alternatives 43, 35 and 36.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -105,6 +106,7 @@ __device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t addr) {
 }
 
 __device__ __forceinline__ unsigned long long pair(float a, float b) { unsigned long long r; asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b)); return r; }
+__device__ __forceinline__ void unpair(unsigned long long v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
 __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) { unsigned long long r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c)); return r; }
 __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) { unsigned long long r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b)); return r; }
 
@@ -335,56 +337,53 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
                 group_best = -INFINITY;
             }
         }
-        // t = x c - m c by one FMA with m c rounded; what that rounding is off by goes back into the sums. Each vector's registers
-        // take the next chunk's as soon as its sums are made. (One number an instruction: what pairs of fp32 save goes into
-        // moving them together.)
+        // t = x c - m c by one FMA with m c rounded; what that rounding is off by goes back into the sums. Two values an instruction,
+        // but for the unpacking and 2^t.
         const float mc = sum.m * c;
-        float s[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
-        unsigned long long s2 = 0, w2 = 0;
-        const unsigned long long c2 = pair(c, c), mc2 = pair(-mc, -mc);
+        float s, w;
         if (fabsf(mc) < 1e6f) {
+            unsigned long long s2 = 0, w2 = 0;
+            const unsigned long long c2 = pair(c, c), mc2 = pair(-mc, -mc);
 #pragma unroll
             for (int j = 0; j < kVecs; ++j) {
 #pragma unroll
                 for (int e = 0; e < kEach; e += 2) {
-                    float d[2];
+                    float d0, d1;
                     if constexpr (kWide) {
-                        d[0] = max_nan(x.at(j, e), far);
-                        d[1] = max_nan(x.at(j, e + 1), far);
+                        d0 = max_nan(x.at(j, e), far);
+                        d1 = max_nan(x.at(j, e + 1), far);
                     } else {
                         const uint32_t u = max_nan2(x.word(j, e / 2), far2);
-                        d[0] = low_half(u);
-                        d[1] = high_half(u);
+                        d0 = low_half(u);
+                        d1 = high_half(u);
                     }
-#pragma unroll
-                    for (int k = 0; k < 1; ++k) {
-                        const unsigned long long dd = fma2(pair(d[0], d[1]), c2, mc2);
-                        float d0, d1;
-                        asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(dd));
-                        const unsigned long long f = pair(ex2(d0), ex2(d1));
-                        s2 = add2(s2, f);
-                        w2 = fma2(f, dd, w2);
-                    }
+                    const unsigned long long d = fma2(pair(d0, d1), c2, mc2);
+                    unpair(d, d0, d1);
+                    const unsigned long long f = pair(ex2(d0), ex2(d1));
+                    s2 = add2(s2, f);
+                    w2 = fma2(f, d, w2);
                 }
             }
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(s[0]), "=f"(s[1]) : "l"(s2));
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(w[0]), "=f"(w[1]) : "l"(w2));
+            float s0, s1, w0, w1;
+            unpair(s2, s0, s1);
+            unpair(w2, w0, w1);
             const float off = -fmaf(sum.m, c, -mc), f = ex2(off);
-            s[0] = (s[0] + s[1]) * f;
-            w[0] = fmaf(s[0], off, (w[0] + w[1]) * f);
+            s = (s0 + s1) * f;
+            w = fmaf(s, off, (w0 + w1) * f);
         } else {  // so far out that the rounding would be whole doublings
+            s = w = 0.f;
 #pragma unroll 1
             for (int k = 0; k < kVecs * kEach; ++k) {
                 const uint4* v = here + k / kEach * kThreads;
                 const float u = kWide ? reinterpret_cast<const float*>(v)[k % kEach]
                                       : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(v)[k % kEach]) << 16);
                 const float d = (u - sum.m) * c, f = ex2(d);
-                s[0] += f;
-                if (f != 0.f) w[0] = fmaf(f, d, w[0]);  // (below the lowest number there is minus infinity)
+                s += f;
+                if (f != 0.f) w = fmaf(f, d, w);  // (below the lowest number there is minus infinity)
             }
         }
-        sum.s += s[0];
-        sum.w += w[0];
+        sum.s += s;
+        sum.w += w;
     }
     wait_copies<0>();
     if (p.top > 0) {
