@@ -154,8 +154,9 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 
 // The gate's activation. Both forms are x times a logistic function, 1 / (1 + e^-y), in which e^-y overflows to infinity for a
 // large negative y and the quotient is 0, as it should be; GELU is its form with tanh, (1 + tanh z) / 2 = 1 / (1 + e^-2z). By the
-// special function unit's 2^t and 1/t, each within 2^-22 or so of the exact value: a full exponential and a division took
-// as long as 4 blocks of k a tile.
+// special function unit's 2^t and 1/t, each within 2^-22 or so of the exact value for its argument; that of 2^t is rounded before, which
+// adds |y| 2^-24 to the relative error, and where 1/t falls below fp32's normal numbers it is 0 (SILU below about -87, GELU
+// below -10, where the results are below 2^-119). A full exponential and a division took as long as 4 blocks of k a tile.
 __device__ __forceinline__ float activate8(float x, int act) {
     float y = -kLog2e * x;
     if (act == kActGelu) y *= 1.5957691216057308f * fmaf(0.044715f * x, x, 1.f);

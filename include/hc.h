@@ -583,7 +583,7 @@ typedef struct {
 
 /* out = act(x . w_gate) * (x . w_up), both products as hc_mul8 takes them, in one kernel: the projections stay in fp32 and the result
  * is rounded once, to bf16, or to codes and scales as hc_norm_quant8 makes them (of 128 features each: the x of the hc_mul8
- * that leads back). out_scales [device] fp32 [n, ceil(features/128)], unused with HC_BF16. w_gate and w_up have one stride
+ * that leads back). An activation below 2^-119 in size may count as 0. out_scales [device] fp32 [n, ceil(features/128)], unused with HC_BF16. w_gate and w_up have one stride
  * (two halves of a joint matrix [2 features, k], or columns of one buffer). */
 int hc_gated_mul8(const void* x, int64_t x_stride, const float* x_scales, const void* w_gate, const float* gate_scales, const void* w_up,
                   const float* up_scales, int64_t w_stride, int64_t n, hc_gated8_t s, void* out, int64_t out_stride, float* out_scales,

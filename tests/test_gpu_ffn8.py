@@ -235,6 +235,32 @@ def test_gated(n, k, features, short, kind):
     assert (buf[:, features:].float() == 5).all()
 
 
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("n", [2, 300])
+def test_gates_far_out(n, kind):
+    """Gates from where the activation passes them on to where nothing is left of them. A token's gate is its code times a power of two; up is 1."""
+    values = np.concatenate([np.arange(-126, 127) / 1.0, np.arange(-126, 127) / 8.0, [-448.0, 448.0, -0.5, 0.0, 2.0 ** -9]])
+    features, k = (len(values) + 15) // 16 * 16, 16
+    wv = np.zeros((features, k))
+    wv[:len(values), 0] = values
+    w, u = dev(wv).to(E4M3), torch.zeros((features, k), dtype=E4M3, device="cuda")
+    u[:, 1] = 1.0
+    x = torch.zeros((n, k), dtype=E4M3, device="cuda")
+    x[:, :2] = 1.0
+    ones = torch.ones((n, 1), device="cuda")
+    ws = torch.ones((fr.blocks(features), 1), device="cuda")
+    out = torch.empty((n, features), dtype=torch.bfloat16, device="cuda")
+    hc.hc_gated_mul8(x, k, ones, w, ws, u, ws, k, n, hc.gated8(features, k, hc.HC_ACT_SILU if kind == "silu" else hc.HC_ACT_GELU, hc.HC_BF16), out, features, None)
+    no_error()
+    g = f64(w)[:, 0]
+    y = -g if kind == "silu" else -2 * np.sqrt(2 / np.pi) * (g + 0.044715 * g ** 3)
+    with np.errstate(over="ignore"):
+        ref = g / (1 + np.exp(y))
+    # the exponent's argument takes up to 6 roundings (2^-24 each, of |y|), 2^t, 1/t, their sum and the products 16
+    e = (6 * np.minimum(np.abs(y), 100) + 16) * fr.U * np.abs(ref) + 2.0 ** -119
+    assert_within(f64(out), np.broadcast_to(ref, out.shape), e + fr.BF16 * (np.abs(ref) + e))
+
+
 @pytest.mark.parametrize("n", [1, 40, 130, 400])
 def test_product_nan_stays_in_its_row_and_column(n):
     rng = np.random.default_rng(n)
