@@ -780,6 +780,61 @@ def test_chain_of_long_heads(n, vocab):
     assert np.array_equal(outs[-1][3].cpu().numpy(), ref[3])
 
 
+@pytest.mark.parametrize("n", [3, 300])
+def test_products_behind_copies_and_other_streams(n):
+    """A captured product whose inputs come from a copy, from another stream's kernels, and from both; and whose output another stream reads."""
+    rng = np.random.default_rng(n)
+    k, f = 2064, 528
+    w, _, ws, _ = make_codes(rng, f, k, (fr.blocks(f), fr.blocks(k)), 4.0 / np.sqrt(k))
+    x0, _, s0, _ = make_codes(rng, n, k, (n, fr.blocks(k)))
+    y = dev(rng.standard_normal((n, k)), torch.bfloat16)
+    x, s, c, cs = torch.empty_like(x0), torch.empty_like(s0), torch.empty_like(x0), torch.empty_like(s0)
+    outs = [torch.empty((n, f), device="cuda") for _ in range(3)]
+    side = torch.cuda.Stream()
+
+    def mul(a, b, o):
+        hc.hc_mul8(a, k, b, w, k, ws, n, hc.mul8(f, k, hc.HC_F32), o, f)
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        x.copy_(x0)
+        s.copy_(s0)
+        mul(x, s, outs[0])
+        with torch.cuda.stream(side):
+            hc.hc_norm_quant8(y, k, None, 0, None, hc.quant8(n, k), None, 0, c, k, cs)
+            mul(c, cs, outs[1])
+        main.wait_stream(side)
+        outs[1].add_(outs[0])
+        mul(c, cs, outs[2])
+        outs[2].add_(outs[1])
+
+    def clear():
+        for t in outs + [s, cs]:
+            t.fill_(float("nan"))
+        x.view(torch.uint8).zero_()
+        c.view(torch.uint8).zero_()
+
+    clear()
+    step()
+    no_error()
+    want = [o.clone() for o in outs]
+    first, second = torch.empty_like(outs[0]), torch.empty_like(outs[0])
+    mul(x0, s0, first)
+    mul(c, cs, second)
+    no_error()
+    assert torch.equal(want[0], first) and torch.equal(want[1], first + second) and torch.equal(want[2], second + (first + second))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        step()
+    for _ in range(3):
+        clear()
+        g.replay()
+        g.replay()
+        no_error()
+        assert all(torch.equal(o, v) for o, v in zip(outs, want))
+
+
 # 9 x 20 gated tiles are two turns of 76 pairs and 28 tiles, which two pairs share each in a launch of their own; the last block of k is short.
 TWO_LAUNCHES = (2100, 10256, 2480)
 
